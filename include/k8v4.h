@@ -102,6 +102,16 @@ typedef struct {
   int32_t format;     /* k8v4_format */
 } k8v4_cache;
 
+/* A position rotation's table and pairing (plain data, no ownership). */
+typedef struct {
+  const float* table;  /* device, fp32 [n_pos][rot_dim], 16-byte aligned: row t holds the
+                          rot_dim / 2 cosines of position t's angles, then their sines */
+  int64_t n_pos;       /* rows of the table, >= 1 */
+  int32_t rot_dim;     /* elements of a head that rotate: a multiple of 16, 16..256; the
+                          elements past them pass through */
+  int32_t interleaved; /* 0: pairs (i, i + rot_dim / 2); nonzero: pairs (2i, 2i + 1) */
+} k8v4_rope;
+
 /* Bytes per cell (all H heads) of a format: 816 for K8V4, 1,056 for INT8 and
  * 576 for Q4 at H = 2 (the three sizes the k8v4 PR compares in "What").
  * Returns 0 for an unknown format or H outside 1..8. */
@@ -131,6 +141,78 @@ int k8v4_device_check(void);
 int kv_append_k8v4(const k8v4_cache* cache, const int32_t* page_table, int64_t max_pages, int32_t n_seqs,
                    const int64_t* pos, int32_t n_tok, const void* k, const void* v, int32_t dtype,
                    void* stream);
+
+/* ---------------------------------------------------------------- around the attention
+ * The steps of a layer next to the cache: queries and keys normed and rotated
+ * by their positions before they are used, and, after a verify call, the
+ * drafted tokens accepted or replaced.  (The pages give the cache and its
+ * attention only; these follow the published definitions stated here.)
+ *
+ * Rotation: a pair (x1, x2) at position t becomes
+ *   (x1 c - x2 s, x2 c + x1 s),  c and s the pair's entries of table row t;
+ * each result is the exact value rounded to fp32, then to the row's type (the
+ * errors of the products and of their sum are carried).  Norm, where a weight w
+ * is given: x -> x / sqrt(mean(x^2) + eps) * w over the head's 256 elements, in
+ * fp32, ahead of the rotation (|x| < 2^60 there).  Inputs are finite. */
+
+/* Norm (optional) and rotation of every query and key head, one pass.
+ *   q, k:     [n_seqs][n_tok] tokens of n_q_heads (n_k_heads) heads x 256 of
+ *             `dtype`; token i starts at q + i * q_stride elements, its heads
+ *             contiguous, so both may be slices of a packed projection.
+ *             Strides >= heads * 256, multiples of 16 bytes; pointers 16-byte
+ *             aligned.  n_k_heads may be 0 (k, k_out unused), or n_q_heads.
+ *   q_weight, k_weight: fp32 [256], 16-byte aligned, or NULL for no norm;
+ *             eps >= 0 is read only with a weight.
+ *   pos:      int64 [n_seqs]: token t of sequence b is at position pos[b] + t.
+ *   q_out, k_out: contiguous [n_seqs][n_tok][heads][256] of `dtype`; each may
+ *             be its own input when that is contiguous (in place), and must
+ *             not overlap it otherwise.
+ * Device-side: a token whose position has no table row is recorded
+ * (K8V4_ERANGE) and its output rows are left as they were. */
+int qk_norm_rope_k8v4(const void* q, int64_t q_stride, int32_t n_q_heads, const void* k, int64_t k_stride,
+                      int32_t n_k_heads, int32_t dtype, const float* q_weight, const float* k_weight, float eps,
+                      const int64_t* pos, int32_t n_seqs, int32_t n_tok, const k8v4_rope* rope, void* q_out,
+                      void* k_out, void* stream);
+
+/* kv_append_k8v4 with K normed (when k_weight is not NULL) and rotated on the
+ * way: the bytes written are those of qk_norm_rope_k8v4 on K followed by
+ * kv_append_k8v4, without the rotated keys going through memory.  The
+ * rotation's position is the cell: token t of sequence b is cell pos[b] + t.
+ *   k, v:  tokens of H heads x 256 with a stride between tokens, as in
+ *          qk_norm_rope_k8v4.
+ * Other arguments as kv_append_k8v4.  Every format.  Device-side: a cell with
+ * no table row is skipped like one with no page (K8V4_ERANGE). */
+int kv_append_k8v4_rope(const k8v4_cache* cache, const int32_t* page_table, int64_t max_pages, int32_t n_seqs,
+                        const int64_t* pos, int32_t n_tok, const void* k, int64_t k_stride, const void* v,
+                        int64_t v_stride, int32_t dtype, const float* k_weight, float eps, const k8v4_rope* rope,
+                        void* stream);
+
+/* Accept or replace drafted tokens from the target's probabilities and given
+ * random numbers.  Draft i of a sequence, token x_i, is accepted while
+ *   u_accept[i] * q_i(x_i) < p_i(x_i)
+ * (exactly, no rounding of the product).  At the first draft a that is not, the next
+ * token is drawn from max(p_a - q_a, 0) (the difference rounded to fp32), after
+ * the last accepted draft from the target row behind it: the smallest j whose
+ * running sum of the weights passes u_sample times their whole sum, the sums
+ * carried to about 46 bits.  Where p_a equals q_a everywhere, p_a itself is
+ * drawn from.
+ *   target_probs: [n_seqs][max_drafts + 1][vocab] of `dtype`, >= 0 and finite,
+ *                 row i the target's distribution after i drafts (need not sum to 1).
+ *   draft_probs:  [n_seqs][max_drafts][vocab] of `dtype`, or NULL for drafts
+ *                 that were certain (q_i = 1 at x_i, 0 elsewhere).
+ *   draft_tokens: int32 [n_seqs][max_drafts]; n_drafts: int32 [n_seqs], each in
+ *                 [0, max_drafts], or NULL (max_drafts each).
+ *   u_accept:     fp32 [n_seqs][max_drafts], u_sample: fp32 [n_seqs], in [0, 1).
+ *   tokens:       int32 [n_seqs][max_drafts + 1]: the accepted drafts, the drawn
+ *                 token, then -1; n_accepted: int32 [n_seqs], accepted drafts.
+ *   0 <= max_drafts <= 32 (with 0, draft_tokens, draft_probs and u_accept are not
+ *   read), 1 <= vocab <= 2^24.
+ * Device-side: a draft outside [0, vocab) is not accepted, a draft count out of
+ * range is clipped, a row without positive finite weight gives token -1; each is
+ * recorded (K8V4_ERANGE). */
+int spec_accept_k8v4(const void* target_probs, const void* draft_probs, int32_t dtype, const int32_t* draft_tokens,
+                     const int32_t* n_drafts, const float* u_accept, const float* u_sample, int32_t n_seqs,
+                     int32_t max_drafts, int32_t vocab, int32_t* tokens, int32_t* n_accepted, void* stream);
 
 /* Workspace bytes attn_k8v4_decode / attn_k8v4_verify need for a launch with
  * these host-side bounds (the split-K partial results). */

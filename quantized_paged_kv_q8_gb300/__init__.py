@@ -35,6 +35,11 @@ class k8v4_cache(ctypes.Structure):
                 ("n_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("format", ctypes.c_int32)]
 
 
+class k8v4_rope(ctypes.Structure):
+    _fields_ = [("table", ctypes.c_void_p), ("n_pos", ctypes.c_int64), ("rot_dim", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32)]
+
+
 _lib = None
 
 
@@ -51,7 +56,7 @@ def lib():
             raise RuntimeError(f"libk8v4.so is not built ({LIB_PATH}); call quantized_paged_kv_q8_gb300.build()")
         L = ctypes.CDLL(LIB_PATH)
         P, I32, I64, F, SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float, ctypes.c_size_t
-        C = ctypes.POINTER(k8v4_cache)
+        C, R = ctypes.POINTER(k8v4_cache), ctypes.POINTER(k8v4_rope)
         sigs = {
             "k8v4_bytes_per_cell": ([I32, I32], SZ),
             "k8v4_status_string": ([ctypes.c_int], ctypes.c_char_p),
@@ -72,6 +77,9 @@ def lib():
             "attn_k8v4_partial_workspace_bytes": ([C, I32, I32, I32], SZ),
             "attn_k8v4_decode_partial": ([C, P, I32, P, I64, P, I32, I32, I32, I32, F, P, P, SZ, P], ctypes.c_int),
             "attn_k8v4_combine_partials": ([P, I32, I32, I32, P, P], ctypes.c_int),
+            "qk_norm_rope_k8v4": ([P, I64, I32, P, I64, I32, I32, P, P, F, P, I32, I32, R, P, P, P], ctypes.c_int),
+            "kv_append_k8v4_rope": ([C, P, I64, I32, P, I32, P, I64, P, I64, I32, P, F, R, P], ctypes.c_int),
+            "spec_accept_k8v4": ([P, P, I32, P, P, P, P, I32, I32, I32, P, P, P], ctypes.c_int),
             "k8v4_set_wait_limit_ns": ([ctypes.c_uint32], None),
             "k8v4_set_withheld_copy": ([ctypes.c_int32], None),
         }
@@ -90,6 +98,7 @@ EXPORTED = ("k8v4_bytes_per_cell", "k8v4_status_string", "k8v4_device_check", "k
             "kv_dequant_k8v4", "k8v4_last_device_status",
             "kv_append_k8v4_mirrored", "kv_stream_workspace_bytes", "kv_stream_resolve", "kv_stream_copy",
             "attn_k8v4_partial_workspace_bytes", "attn_k8v4_decode_partial", "attn_k8v4_combine_partials",
+            "qk_norm_rope_k8v4", "kv_append_k8v4_rope", "spec_accept_k8v4",
             "k8v4_set_wait_limit_ns", "k8v4_set_withheld_copy")
 
 
@@ -166,6 +175,106 @@ def kv_append_k8v4(cache: PagedCache, page_table: torch.Tensor, pos: torch.Tenso
     rc = lib().kv_append_k8v4(cache.ref(), _ptr(page_table), page_table.shape[-1], n_seqs, _ptr(pos), n_tok,
                               _ptr(k), _ptr(v), _dtype(k), _stream(stream))
     _check(rc, "kv_append_k8v4")
+
+
+# ---------------------------------------------------------------- around the attention
+def _need(ok: bool, what: str) -> None:
+    if not ok:
+        raise ValueError(what)
+
+
+def _token_stride(x: torch.Tensor, heads: int, what: str) -> int:
+    """Elements between the tokens of x [n_seqs, n_tok, heads, 256]; heads are
+    contiguous, tokens evenly spaced over the sequences (a slice of a packed
+    projection qualifies)."""
+    _need(x.dim() == 4 and x.shape[2] == heads and x.shape[3] == HEAD_DIM, f"{what}: [n_seqs, n_tok, heads, 256] expected")
+    n_seqs, n_tok = x.shape[0], x.shape[1]
+    _need(heads == 0 or (x.stride(3) == 1 and (heads == 1 or x.stride(2) == HEAD_DIM)), f"{what}: heads must be contiguous")
+    step = x.stride(1) if n_tok > 1 else x.stride(0) if n_seqs > 1 else heads * HEAD_DIM
+    _need(n_seqs <= 1 or n_tok == 0 or x.stride(0) == n_tok * step, f"{what}: tokens must be evenly spaced")
+    return step
+
+
+def _rope(table: torch.Tensor, interleaved: bool) -> k8v4_rope:
+    _need(table.dtype == torch.float32 and table.dim() == 2 and table.is_contiguous(),
+          "rope_table: contiguous float32 [n_pos, rot_dim] expected")
+    return k8v4_rope(_ptr(table), table.shape[0], table.shape[1], 1 if interleaved else 0)
+
+
+def _weight(w: torch.Tensor | None, what: str):
+    _need(w is None or (w.dtype == torch.float32 and w.shape == (HEAD_DIM,) and w.is_contiguous()),
+          f"{what}: contiguous float32 [256] expected")
+    return _ptr(w)
+
+
+def _same_device(*tensors) -> None:
+    _need(len({t.device for t in tensors if t is not None}) == 1, "tensors on different devices")
+
+
+def qk_norm_rope_k8v4(q: torch.Tensor, k: torch.Tensor | None, pos: torch.Tensor, rope_table: torch.Tensor,
+                      q_out: torch.Tensor, k_out: torch.Tensor | None, q_weight: torch.Tensor | None = None,
+                      k_weight: torch.Tensor | None = None, eps: float = 1e-6, interleaved: bool = False,
+                      stream=None) -> None:
+    """Per-head RMS norm (with a weight) and position rotation of q [n_seqs, n_tok, HQ, 256]
+    and k [n_seqs, n_tok, H, 256] (or None) into contiguous q_out, k_out.  pos int64 [n_seqs];
+    rope_table float32 [n_pos, rot_dim]: cosines, then sines, of each position."""
+    n_seqs, n_tok, n_q = q.shape[0], q.shape[1], q.shape[2]
+    n_k = 0 if k is None else k.shape[2]
+    q_stride = _token_stride(q, n_q, "q")
+    k_stride = 0 if k is None else _token_stride(k, n_k, "k")
+    _need(q_out.shape == q.shape and q_out.dtype == q.dtype and q_out.is_contiguous(), "q_out: contiguous, like q")
+    if k is not None:
+        _need(k.dtype == q.dtype and k.shape[:2] == q.shape[:2], "k: same dtype and tokens as q")
+        _need(k_out is not None and k_out.shape == k.shape and k_out.dtype == k.dtype and k_out.is_contiguous(),
+              "k_out: contiguous, like k")
+    _need(pos.dtype == torch.int64 and pos.numel() == n_seqs and pos.is_contiguous(), "pos: int64 [n_seqs]")
+    _same_device(q, k, pos, rope_table, q_out, None if k is None else k_out, q_weight, k_weight)
+    r = _rope(rope_table, interleaved)
+    rc = lib().qk_norm_rope_k8v4(_ptr(q), q_stride, n_q, _ptr(k), k_stride, n_k, _dtype(q), _weight(q_weight, "q_weight"),
+                                 _weight(k_weight, "k_weight"), eps, _ptr(pos), n_seqs, n_tok, ctypes.byref(r),
+                                 _ptr(q_out), None if k is None else _ptr(k_out), _stream(stream))
+    _check(rc, "qk_norm_rope_k8v4")
+
+
+def kv_append_k8v4_rope(cache: PagedCache, page_table: torch.Tensor, pos: torch.Tensor, k: torch.Tensor,
+                        v: torch.Tensor, rope_table: torch.Tensor, k_weight: torch.Tensor | None = None,
+                        eps: float = 1e-6, interleaved: bool = False, stream=None) -> None:
+    """kv_append_k8v4 with k normed (with a weight) and rotated to its cell's position on the
+    way.  k, v: [n_seqs, n_tok, H, 256], possibly slices of a packed projection."""
+    n_seqs, n_tok, h = k.shape[0], k.shape[1], cache.n_kv_heads
+    _need(k.shape == v.shape and k.dtype == v.dtype, "k and v: same shape and dtype")
+    _need(page_table.dtype == torch.int32 and page_table.dim() == 2 and page_table.shape[0] == n_seqs
+          and page_table.is_contiguous(), "page_table: contiguous int32 [n_seqs, max_pages]")
+    _need(pos.dtype == torch.int64 and pos.numel() == n_seqs and pos.is_contiguous(), "pos: int64 [n_seqs]")
+    _same_device(cache.pages, page_table, pos, k, v, rope_table, k_weight)
+    r = _rope(rope_table, interleaved)
+    rc = lib().kv_append_k8v4_rope(cache.ref(), _ptr(page_table), page_table.shape[-1], n_seqs, _ptr(pos), n_tok,
+                                   _ptr(k), _token_stride(k, h, "k"), _ptr(v), _token_stride(v, h, "v"), _dtype(k),
+                                   _weight(k_weight, "k_weight"), eps, ctypes.byref(r), _stream(stream))
+    _check(rc, "kv_append_k8v4_rope")
+
+
+def spec_accept_k8v4(target_probs: torch.Tensor, draft_probs: torch.Tensor | None, draft_tokens: torch.Tensor,
+                     u_accept: torch.Tensor, u_sample: torch.Tensor, tokens: torch.Tensor, n_accepted: torch.Tensor,
+                     n_drafts: torch.Tensor | None = None, stream=None) -> None:
+    """Accept or replace drafted tokens.  target_probs [n_seqs, n + 1, vocab], draft_probs
+    [n_seqs, n, vocab] or None (certain drafts), draft_tokens int32 [n_seqs, n], u_accept
+    float32 [n_seqs, n], u_sample float32 [n_seqs] -> tokens int32 [n_seqs, n + 1] (accepted
+    drafts, the drawn token, then -1), n_accepted int32 [n_seqs]."""
+    _need(target_probs.dim() == 3 and target_probs.is_contiguous(), "target_probs: contiguous [n_seqs, n + 1, vocab]")
+    b, n, vocab = target_probs.shape[0], target_probs.shape[1] - 1, target_probs.shape[2]
+    _need(draft_probs is None or (draft_probs.shape == (b, n, vocab) and draft_probs.dtype == target_probs.dtype
+                                  and draft_probs.is_contiguous()), "draft_probs: contiguous [n_seqs, n, vocab], like target_probs")
+    for t, shape, dtype, what in ((draft_tokens, (b, n), torch.int32, "draft_tokens"), (u_accept, (b, n), torch.float32, "u_accept"),
+                                  (u_sample, (b,), torch.float32, "u_sample"), (tokens, (b, n + 1), torch.int32, "tokens"),
+                                  (n_accepted, (b,), torch.int32, "n_accepted"), (n_drafts, (b,), torch.int32, "n_drafts")):
+        _need(t is None and what == "n_drafts" or (tuple(t.shape) == shape and t.dtype == dtype and t.is_contiguous()),
+              f"{what}: contiguous {dtype} {shape} expected")
+    _same_device(target_probs, draft_probs, draft_tokens, u_accept, u_sample, tokens, n_accepted, n_drafts)
+    rc = lib().spec_accept_k8v4(_ptr(target_probs), _ptr(draft_probs), _dtype(target_probs), _ptr(draft_tokens),
+                                _ptr(n_drafts), _ptr(u_accept), _ptr(u_sample), b, n, vocab, _ptr(tokens),
+                                _ptr(n_accepted), _stream(stream))
+    _check(rc, "spec_accept_k8v4")
 
 
 def attn_k8v4_workspace_bytes(cache: PagedCache, n_seqs: int, n_q: int, max_seq_len: int) -> int:

@@ -162,6 +162,94 @@ int kv_append_k8v4(const k8v4_cache* cache, const int32_t* page_table, int64_t m
   return launch_append(L, C, page_table, max_pages, n_seqs, pos, n_tok, k, v, dtype);
 }
 
+// the table of a rotation: sizes and alignment
+static int check_rope(const k8v4_rope* r) {
+  if (!r || !r->table) return K8V4_EINVAL;
+  if (r->rot_dim < 16 || r->rot_dim > kD || r->rot_dim % 16) return K8V4_EINVAL;
+  if (r->n_pos < 1 || r->n_pos > (int64_t(1) << 40)) return K8V4_EINVAL;
+  return aligned(r->table, 16) ? K8V4_OK : K8V4_EALIGN;
+}
+// rows of `heads` heads a token with a stride between tokens (elements)
+static int check_rows(const void* x, int64_t stride, int32_t heads, int32_t dtype) {
+  if (!x || stride < static_cast<int64_t>(heads) * kD || stride > (int64_t(1) << 31)) return K8V4_EINVAL;
+  if (stride % (dtype == K8V4_BF16 ? 8 : 4) || !aligned(x, 16)) return K8V4_EALIGN;
+  return K8V4_OK;
+}
+static int check_weight(const float* w, float eps) {
+  if (!w) return K8V4_OK;
+  if (!(eps >= 0.0f) || eps > 1e30f) return K8V4_EINVAL;
+  return aligned(w, 16) ? K8V4_OK : K8V4_EALIGN;
+}
+
+int qk_norm_rope_k8v4(const void* q, int64_t q_stride, int32_t n_q_heads, const void* k, int64_t k_stride,
+                      int32_t n_k_heads, int32_t dtype, const float* q_weight, const float* k_weight, float eps,
+                      const int64_t* pos, int32_t n_seqs, int32_t n_tok, const k8v4_rope* rope, void* q_out,
+                      void* k_out, void* stream) {
+  int rc = check_rope(rope);
+  if (rc) return rc;
+  if (n_seqs < 0 || n_tok < 0 || (dtype != K8V4_F32 && dtype != K8V4_BF16)) return K8V4_EINVAL;
+  if (n_q_heads < 0 || n_k_heads < 0 || n_q_heads > 1024 || n_k_heads > 1024 || n_q_heads + n_k_heads == 0)
+    return K8V4_EINVAL;
+  if (n_seqs == 0 || n_tok == 0) return K8V4_OK;
+  if (n_q_heads && (rc = check_rows(q, q_stride, n_q_heads, dtype))) return rc;
+  if (n_k_heads && (rc = check_rows(k, k_stride, n_k_heads, dtype))) return rc;
+  if (!pos || (n_q_heads && !q_out) || (n_k_heads && !k_out)) return K8V4_EINVAL;
+  // in place only where the input is laid out as the output
+  if ((n_q_heads && q_out == q && q_stride != int64_t(n_q_heads) * kD) ||
+      (n_k_heads && k_out == k && k_stride != int64_t(n_k_heads) * kD))
+    return K8V4_EINVAL;
+  if (!aligned(pos, 8) || (n_q_heads && !aligned(q_out, 16)) || (n_k_heads && !aligned(k_out, 16))) return K8V4_EALIGN;
+  if ((rc = check_weight(n_q_heads ? q_weight : nullptr, eps)) || (rc = check_weight(n_k_heads ? k_weight : nullptr, eps)))
+    return rc;
+  if (static_cast<int64_t>(n_seqs) * n_tok >= (int64_t(1) << 31)) return K8V4_EINVAL;
+  Launch L;
+  if ((rc = make_launch(stream, &L))) return rc;
+  return launch_norm_rope(L, q, q_stride, n_q_heads, k, k_stride, n_k_heads, dtype, q_weight, k_weight, eps, pos,
+                          n_seqs, n_tok, *rope, q_out, k_out);
+}
+
+int kv_append_k8v4_rope(const k8v4_cache* cache, const int32_t* page_table, int64_t max_pages, int32_t n_seqs,
+                        const int64_t* pos, int32_t n_tok, const void* k, int64_t k_stride, const void* v,
+                        int64_t v_stride, int32_t dtype, const float* k_weight, float eps, const k8v4_rope* rope,
+                        void* stream) {
+  CacheView C;
+  int rc = view_of(cache, &C);
+  if (rc) return rc;
+  if ((rc = check_table(C, page_table, max_pages)) || (rc = check_rope(rope))) return rc;
+  if (n_seqs < 0 || n_tok < 0 || (dtype != K8V4_F32 && dtype != K8V4_BF16)) return K8V4_EINVAL;
+  if (n_seqs == 0 || n_tok == 0) return K8V4_OK;
+  if (!pos) return K8V4_EINVAL;
+  if ((rc = check_rows(k, k_stride, C.H, dtype)) || (rc = check_rows(v, v_stride, C.H, dtype))) return rc;
+  if (!aligned(pos, 8)) return K8V4_EALIGN;
+  if ((rc = check_weight(k_weight, eps))) return rc;
+  if (static_cast<int64_t>(n_seqs) * n_tok * C.H >= (int64_t(1) << 31)) return K8V4_EINVAL;
+  Launch L;
+  if ((rc = make_launch(stream, &L))) return rc;
+  return launch_append_rope(L, C, page_table, max_pages, n_seqs, pos, n_tok, k, k_stride, v, v_stride, dtype, k_weight,
+                            eps, *rope);
+}
+
+int spec_accept_k8v4(const void* target_probs, const void* draft_probs, int32_t dtype, const int32_t* draft_tokens,
+                     const int32_t* n_drafts, const float* u_accept, const float* u_sample, int32_t n_seqs,
+                     int32_t max_drafts, int32_t vocab, int32_t* tokens, int32_t* n_accepted, void* stream) {
+  if (dtype != K8V4_F32 && dtype != K8V4_BF16) return K8V4_EINVAL;
+  if (n_seqs < 0 || n_seqs > (1 << 24) || max_drafts < 0 || max_drafts > 32 || vocab < 1 || vocab > (1 << 24))
+    return K8V4_EINVAL;
+  if (n_seqs == 0) return K8V4_OK;
+  if (!target_probs || !u_sample || !tokens || !n_accepted) return K8V4_EINVAL;
+  if (max_drafts > 0 && (!draft_tokens || !u_accept)) return K8V4_EINVAL;
+  const uintptr_t e = dtype == K8V4_BF16 ? 2 : 4;
+  if (!aligned(target_probs, e) || (draft_probs && !aligned(draft_probs, e)) || !aligned(draft_tokens, 4) ||
+      !aligned(n_drafts, 4) || !aligned(u_accept, 4) || !aligned(u_sample, 4) || !aligned(tokens, 4) ||
+      !aligned(n_accepted, 4))
+    return K8V4_EALIGN;
+  Launch L;
+  int rc = make_launch(stream, &L);
+  if (rc) return rc;
+  return launch_accept(L, target_probs, max_drafts ? draft_probs : nullptr, dtype, draft_tokens, n_drafts, u_accept,
+                       u_sample, n_seqs, max_drafts, vocab, tokens, n_accepted);
+}
+
 size_t attn_k8v4_workspace_bytes(const k8v4_cache* cache, int32_t n_seqs, int32_t n_q_per_seq, int32_t max_seq_len) {
   CacheView C;
   if (view_of(cache, &C) != K8V4_OK) return 0;

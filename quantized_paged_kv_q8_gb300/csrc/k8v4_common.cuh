@@ -169,6 +169,18 @@ int launch_combine_partial(const Launch& L, const float* ws, int splits, int n_s
 // gathered partials [n_parts][n_seqs][rows][260] -> out [n_seqs][rows][256]
 int launch_combine_parts(const Launch& L, const float* parts, int n_parts, int n_seqs, int n_rows_per_seq,
                          float* out);
+// queries and keys: per-head RMS norm (weights may be null) and position rotation
+int launch_norm_rope(const Launch& L, const void* q, int64_t q_stride, int n_q, const void* k, int64_t k_stride,
+                     int n_k, int dtype, const float* q_weight, const float* k_weight, float eps, const int64_t* pos,
+                     int n_seqs, int n_tok, const k8v4_rope& rope, void* q_out, void* k_out);
+// the append with K normed (k_weight not null) and rotated on the way
+int launch_append_rope(const Launch& L, const CacheView& C, const int32_t* pt, int64_t max_pages, int n_seqs,
+                       const int64_t* pos, int n_tok, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                       int dtype, const float* k_weight, float eps, const k8v4_rope& rope);
+// acceptance of drafted tokens
+int launch_accept(const Launch& L, const void* p, const void* q, int dtype, const int32_t* drafts,
+                  const int32_t* n_drafts, const float* u_accept, const float* u_sample, int n_seqs, int max_drafts,
+                  int vocab, int32_t* tokens, int32_t* n_accepted);
 int launch_prefill(const Launch& L, const CacheView& C, const void* q, const int32_t* pt, int64_t max_pages,
                    int seq_len, int n_q_tok, const int32_t* steps, float sm_scale, float* out);
 

@@ -1,0 +1,111 @@
+"""CPU checks of the calls around the attention: bad arguments are refused on the
+host, before any device call, and the binding checks its tensors."""
+import ctypes
+
+import pytest
+import torch
+
+import quantized_paged_kv_q8_gb300 as k8
+
+FAKE = ctypes.c_void_p(0x20000)
+ODD = ctypes.c_void_p(0x20004)
+
+
+@pytest.fixture(scope="module")
+def L():
+    k8.build()
+    return k8.lib()
+
+
+def _desc(**kw):
+    d = dict(pages=0x10000, n_pages=4, page_size=16, n_kv_heads=2, head_dim=256, format=k8.FORMAT_K8V4)
+    d.update(kw)
+    return ctypes.byref(k8.k8v4_cache(ctypes.c_void_p(d["pages"]), d["n_pages"], d["page_size"], d["n_kv_heads"],
+                                      d["head_dim"], d["format"]))
+
+
+def _rope(table=0x40000, n_pos=64, rot=64, inter=0):
+    return ctypes.byref(k8.k8v4_rope(ctypes.c_void_p(table), n_pos, rot, inter))
+
+
+BAD_ROPES = [(None, k8.EINVAL), (_rope(table=0), k8.EINVAL), (_rope(n_pos=0), k8.EINVAL), (_rope(rot=0), k8.EINVAL),
+             (_rope(rot=24), k8.EINVAL), (_rope(rot=272), k8.EINVAL), (_rope(table=0x40008), k8.EALIGN)]
+
+
+def _norm_rope(L, q=FAKE, qs=4096, hq=16, k=FAKE, ks=512, hk=2, dtype=k8.BF16, qw=None, kw=None, eps=1e-6, pos=FAKE,
+               n=1, t=1, rope=None, qo=ctypes.c_void_p(0x90000), ko=ctypes.c_void_p(0xa0000)):
+    return L.qk_norm_rope_k8v4(q, qs, hq, k, ks, hk, dtype, qw, kw, eps, pos, n, t, rope or _rope(), qo, ko, None)
+
+
+@pytest.mark.parametrize("bad,code", [
+    (dict(dtype=5), k8.EINVAL), (dict(hq=-1), k8.EINVAL), (dict(hq=0, hk=0), k8.EINVAL), (dict(hq=2000), k8.EINVAL),
+    (dict(qs=4095), k8.EINVAL), (dict(qs=4100), k8.EALIGN), (dict(ks=511), k8.EINVAL), (dict(q=None), k8.EINVAL),
+    (dict(q=ODD), k8.EALIGN), (dict(k=None), k8.EINVAL), (dict(pos=None), k8.EINVAL), (dict(pos=ODD), k8.EALIGN),
+    (dict(qo=None), k8.EINVAL), (dict(ko=None), k8.EINVAL), (dict(qo=ODD), k8.EALIGN), (dict(qw=ODD), k8.EALIGN),
+    (dict(kw=FAKE, eps=-1.0), k8.EINVAL), (dict(kw=FAKE, eps=float("nan")), k8.EINVAL), (dict(n=-1), k8.EINVAL),
+    (dict(t=-1), k8.EINVAL), (dict(n=1 << 20, t=1 << 20), k8.EINVAL), (dict(qs=8192, qo=FAKE), k8.EINVAL)])
+def test_norm_rope_refuses(L, bad, code):
+    assert _norm_rope(L, **bad) == code
+
+
+@pytest.mark.parametrize("rope,code", BAD_ROPES)
+def test_bad_tables_refused(L, rope, code):
+    assert L.qk_norm_rope_k8v4(FAKE, 4096, 16, FAKE, 512, 2, k8.BF16, None, None, 0.0, FAKE, 1, 1, rope, FAKE, FAKE, None) == code
+    assert L.kv_append_k8v4_rope(_desc(), FAKE, 4, 1, FAKE, 1, FAKE, 512, FAKE, 512, k8.BF16, None, 0.0, rope, None) == code
+
+
+def test_nothing_to_do(L):
+    assert _norm_rope(L, n=0) == k8.OK and _norm_rope(L, t=0) == k8.OK
+    assert L.kv_append_k8v4_rope(_desc(), FAKE, 4, 1, FAKE, 0, FAKE, 512, FAKE, 512, k8.BF16, None, 0.0, _rope(), None) == k8.OK
+    assert L.spec_accept_k8v4(None, None, k8.F32, None, None, None, None, 0, 4, 100, None, None, None) == k8.OK
+
+
+@pytest.mark.parametrize("bad,code", [
+    (dict(k=None), k8.EINVAL), (dict(v=None), k8.EINVAL), (dict(k=ODD), k8.EALIGN), (dict(ks=511), k8.EINVAL),
+    (dict(vs=516), k8.EALIGN), (dict(pos=None), k8.EINVAL), (dict(pos=ODD), k8.EALIGN), (dict(dtype=2), k8.EINVAL),
+    (dict(n=-1), k8.EINVAL), (dict(pt=None), k8.EINVAL), (dict(mp=0), k8.EINVAL), (dict(w=ODD), k8.EALIGN),
+    (dict(w=FAKE, eps=-1.0), k8.EINVAL), (dict(n=1 << 15, t=1 << 15), k8.EINVAL)])
+def test_append_rope_refuses(L, bad, code):
+    a = dict(pt=FAKE, mp=4, n=1, pos=FAKE, t=1, k=FAKE, ks=512, v=FAKE, vs=512, dtype=k8.BF16, w=None, eps=1e-6)
+    a.update(bad)
+    assert L.kv_append_k8v4_rope(_desc(), a["pt"], a["mp"], a["n"], a["pos"], a["t"], a["k"], a["ks"], a["v"], a["vs"],
+                                 a["dtype"], a["w"], a["eps"], _rope(), None) == code
+    assert L.kv_append_k8v4_rope(_desc(head_dim=128), FAKE, 4, 1, FAKE, 1, FAKE, 512, FAKE, 512, k8.BF16, None, 0.0,
+                                 _rope(), None) == k8.EINVAL
+
+
+@pytest.mark.parametrize("bad,code", [
+    (dict(p=None), k8.EINVAL), (dict(dtype=9), k8.EINVAL), (dict(drafts=None), k8.EINVAL), (dict(u=None), k8.EINVAL),
+    (dict(us=None), k8.EINVAL), (dict(out=None), k8.EINVAL), (dict(acc=None), k8.EINVAL), (dict(n=33), k8.EINVAL),
+    (dict(n=-1), k8.EINVAL), (dict(vocab=0), k8.EINVAL), (dict(vocab=(1 << 24) + 1), k8.EINVAL), (dict(b=-1), k8.EINVAL),
+    (dict(p=ctypes.c_void_p(0x20002)), k8.EALIGN), (dict(out=ctypes.c_void_p(0x20002)), k8.EALIGN)])
+def test_accept_refuses(L, bad, code):
+    a = dict(p=FAKE, q=FAKE, dtype=k8.F32, drafts=FAKE, nd=None, u=FAKE, us=FAKE, b=1, n=4, vocab=100, out=FAKE, acc=FAKE)
+    a.update(bad)
+    assert L.spec_accept_k8v4(a["p"], a["q"], a["dtype"], a["drafts"], a["nd"], a["u"], a["us"], a["b"], a["n"],
+                              a["vocab"], a["out"], a["acc"], None) == code
+
+
+def test_binding_checks_its_tensors(L):
+    """Shapes, types and spacing are checked before the library is called (CPU tensors suffice)."""
+    q = torch.zeros(2, 3, 16, 256, dtype=torch.bfloat16)
+    pos = torch.zeros(2, dtype=torch.int64)
+    tab = torch.zeros(8, 64)
+    with pytest.raises(ValueError):
+        k8.qk_norm_rope_k8v4(q[:, :, :, :128], None, pos, tab, q, None)
+    with pytest.raises(ValueError):
+        k8.qk_norm_rope_k8v4(q.transpose(0, 1), None, torch.zeros(3, dtype=torch.int64), tab, q.transpose(0, 1).contiguous(), None)
+    with pytest.raises(ValueError):
+        k8.qk_norm_rope_k8v4(q, None, pos, tab, q[:, :2], None)
+    with pytest.raises(ValueError):
+        k8.qk_norm_rope_k8v4(q, None, pos.int(), tab, torch.empty_like(q), None)
+    with pytest.raises(ValueError):
+        k8.qk_norm_rope_k8v4(q, None, pos, tab.double(), torch.empty_like(q), None)
+    with pytest.raises(ValueError):
+        k8.spec_accept_k8v4(torch.zeros(2, 3, 50), torch.zeros(2, 2, 49), torch.zeros(2, 2, dtype=torch.int32),
+                            torch.zeros(2, 2), torch.zeros(2), torch.zeros(2, 3, dtype=torch.int32), torch.zeros(2, dtype=torch.int32))
+    # tokens of several sequences in one packed buffer are evenly spaced, a sequence-strided slice is not
+    packed = torch.zeros(2, 3, 20, 256)
+    assert k8._token_stride(packed[:, :, 16:18], 2, "k") == 20 * 256
+    with pytest.raises(ValueError):
+        k8._token_stride(packed[:, :2, 16:18], 2, "k")
