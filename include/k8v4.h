@@ -259,6 +259,29 @@ int attn_k8v4_decode_step(const k8v4_cache* cache, const void* q, int32_t q_dtyp
                           const int32_t* seq_lens, int32_t n_seqs, int32_t max_seq_len, float sm_scale,
                           float* out, void* workspace, size_t workspace_bytes, void* stream);
 
+/* Workspace bytes attn_k8v4_decode_shared needs; 0 for a format other than K8V4
+ * or a bad size. */
+size_t attn_k8v4_shared_workspace_bytes(const k8v4_cache* cache, int32_t n_seqs, int32_t shared_len,
+                                        int32_t max_seq_len);
+
+/* Decode attention of a batch whose sequences share their first cells (one
+ * system prompt, one document, several samples of one context): the result of
+ * attn_k8v4_decode, with the shared cells read once for the batch.
+ *   shared_len: host-side number of leading cells that are the same for every
+ *             sequence, >= 0 (it may exceed max_seq_len).  Every sequence's page-table
+ *             row names these cells (same pages, or pages with the same
+ *             bytes); which rows the shared cells are read through is the library's
+ *             choice.
+ *   seq_lens: may be shorter than shared_len (such a row sees its own first
+ *             seq_lens[b] cells), or 0 (zero output).
+ *   workspace: >= attn_k8v4_shared_workspace_bytes(cache, n_seqs, shared_len,
+ *             max_seq_len) bytes, 256-byte aligned.
+ * Other arguments as attn_k8v4_decode.  K8V4 format, bf16 q. */
+int attn_k8v4_decode_shared(const k8v4_cache* cache, const void* q, int32_t q_dtype, const int32_t* page_table,
+                            int64_t max_pages, const int32_t* seq_lens, int32_t n_seqs, int32_t max_seq_len,
+                            int32_t shared_len, float sm_scale, float* out, void* workspace, size_t workspace_bytes,
+                            void* stream);
+
 /* Decode attention that allocates nothing and takes no workspace.  The pages
  * have no counterpart to this call; it exists for callers that cannot allocate
  * device memory: a host with no device allocator of its own (a plain C program

@@ -77,6 +77,8 @@ def lib():
             "attn_k8v4_partial_workspace_bytes": ([C, I32, I32, I32], SZ),
             "attn_k8v4_decode_partial": ([C, P, I32, P, I64, P, I32, I32, I32, I32, F, P, P, SZ, P], ctypes.c_int),
             "attn_k8v4_combine_partials": ([P, I32, I32, I32, P, P], ctypes.c_int),
+            "attn_k8v4_shared_workspace_bytes": ([C, I32, I32, I32], SZ),
+            "attn_k8v4_decode_shared": ([C, P, I32, P, I64, P, I32, I32, I32, F, P, P, SZ, P], ctypes.c_int),
             "qk_norm_rope_k8v4": ([P, I64, I32, P, I64, I32, I32, P, P, F, P, I32, I32, R, P, P, P], ctypes.c_int),
             "kv_append_k8v4_rope": ([C, P, I64, I32, P, I32, P, I64, P, I64, I32, P, F, R, P], ctypes.c_int),
             "spec_accept_k8v4": ([P, P, I32, P, P, P, P, I32, I32, I32, P, P, P], ctypes.c_int),
@@ -98,6 +100,7 @@ EXPORTED = ("k8v4_bytes_per_cell", "k8v4_status_string", "k8v4_device_check", "k
             "kv_dequant_k8v4", "k8v4_last_device_status",
             "kv_append_k8v4_mirrored", "kv_stream_workspace_bytes", "kv_stream_resolve", "kv_stream_copy",
             "attn_k8v4_partial_workspace_bytes", "attn_k8v4_decode_partial", "attn_k8v4_combine_partials",
+            "attn_k8v4_shared_workspace_bytes", "attn_k8v4_decode_shared",
             "qk_norm_rope_k8v4", "kv_append_k8v4_rope", "spec_accept_k8v4",
             "k8v4_set_wait_limit_ns", "k8v4_set_withheld_copy")
 
@@ -234,6 +237,36 @@ def qk_norm_rope_k8v4(q: torch.Tensor, k: torch.Tensor | None, pos: torch.Tensor
                                  _weight(k_weight, "k_weight"), eps, _ptr(pos), n_seqs, n_tok, ctypes.byref(r),
                                  _ptr(q_out), None if k is None else _ptr(k_out), _stream(stream))
     _check(rc, "qk_norm_rope_k8v4")
+
+
+def attn_k8v4_shared_workspace_bytes(cache: PagedCache, n_seqs: int, shared_len: int, max_seq_len: int) -> int:
+    return int(lib().attn_k8v4_shared_workspace_bytes(cache.ref(), n_seqs, shared_len, max_seq_len))
+
+
+def shared_workspace(cache: PagedCache, n_seqs: int, shared_len: int, max_seq_len: int, device="cuda") -> torch.Tensor:
+    n = attn_k8v4_shared_workspace_bytes(cache, n_seqs, shared_len, max_seq_len)
+    return torch.empty(max(n, 256), dtype=torch.uint8, device=device)
+
+
+def attn_k8v4_decode_shared(cache: PagedCache, q: torch.Tensor, page_table: torch.Tensor, seq_lens: torch.Tensor,
+                            max_seq_len: int, shared_len: int, out: torch.Tensor, ws: torch.Tensor,
+                            sm_scale: float = 1.0 / 16.0, stream=None) -> torch.Tensor:
+    """attn_k8v4_decode for a batch whose first shared_len cells are the same in every
+    sequence, read once for all of them.  q: bf16 [n_seqs, 8H, 256]; page_table int32
+    [n_seqs, max_pages]; seq_lens int32 [n_seqs]; out float32 like q."""
+    n_seqs = q.shape[0]
+    _need(tuple(q.shape[1:]) == (GQA * cache.n_kv_heads, HEAD_DIM) and q.is_contiguous(), "q: contiguous [n_seqs, 8H, 256]")
+    _need(page_table.dtype == torch.int32 and page_table.dim() == 2 and page_table.shape[0] == n_seqs
+          and page_table.is_contiguous(), "page_table: contiguous int32 [n_seqs, max_pages]")
+    _need(seq_lens.dtype == torch.int32 and seq_lens.numel() == n_seqs and seq_lens.is_contiguous(), "seq_lens: int32 [n_seqs]")
+    _need(out.shape == q.shape and out.dtype == torch.float32 and out.is_contiguous(), "out: contiguous float32, like q")
+    _need(ws.dtype == torch.uint8 and ws.is_contiguous(), "ws: uint8")
+    _same_device(cache.pages, q, page_table, seq_lens, out, ws)
+    rc = lib().attn_k8v4_decode_shared(cache.ref(), _ptr(q), _dtype(q), _ptr(page_table), page_table.shape[1],
+                                       _ptr(seq_lens), n_seqs, max_seq_len, shared_len, sm_scale, _ptr(out), _ptr(ws),
+                                       ws.numel(), _stream(stream))
+    _check(rc, "attn_k8v4_decode_shared")
+    return out
 
 
 def kv_append_k8v4_rope(cache: PagedCache, page_table: torch.Tensor, pos: torch.Tensor, k: torch.Tensor,

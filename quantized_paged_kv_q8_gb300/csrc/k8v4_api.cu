@@ -309,6 +309,67 @@ int attn_k8v4_verify(const k8v4_cache* cache, const void* q, int32_t q_dtype, co
                        workspace, workspace_bytes, stream);
 }
 
+// the splits of a shared-prefix decode: the prefix's, and those of the sequences'
+// own cells behind it
+static SharedPlan shared_plans(const CacheView& C, int n_seqs, int shared_len, int max_seq_len, int sms, AttendPlan* own) {
+  const SharedPlan pre = plan_shared(C, n_seqs, shared_len, max_seq_len, sms);
+  *own = AttendPlan{};
+  if (pre.cells == 0) *own = plan_attend(C, n_seqs, 1, max_seq_len, sms);
+  else if (max_seq_len > pre.cells) *own = plan_decode(C, n_seqs, max_seq_len - pre.cells, sms);
+  return pre;
+}
+static size_t shared_ws_bytes(const CacheView& C, const SharedPlan& pre, const AttendPlan& own, int n_seqs) {
+  if (pre.cells == 0) return own.ws_bytes;
+  return static_cast<size_t>(n_seqs) * (pre.splits + own.splits) * C.H * kGqa * 260 * sizeof(float);
+}
+
+size_t attn_k8v4_shared_workspace_bytes(const k8v4_cache* cache, int32_t n_seqs, int32_t shared_len,
+                                        int32_t max_seq_len) {
+  CacheView C;
+  if (view_of(cache, &C) != K8V4_OK || !shared_prefix_supported(C)) return 0;
+  if (n_seqs < 0 || n_seqs > 65535 || shared_len < 0 || max_seq_len < 0) return 0;
+  DeviceState* s = nullptr;
+  const int sms = device_state(&s) == K8V4_OK ? s->num_sms : 152;
+  AttendPlan own;
+  const SharedPlan pre = shared_plans(C, n_seqs, shared_len, max_seq_len, sms, &own);
+  return shared_ws_bytes(C, pre, own, n_seqs);
+}
+
+int attn_k8v4_decode_shared(const k8v4_cache* cache, const void* q, int32_t q_dtype, const int32_t* page_table,
+                            int64_t max_pages, const int32_t* seq_lens, int32_t n_seqs, int32_t max_seq_len,
+                            int32_t shared_len, float sm_scale, float* out, void* workspace, size_t workspace_bytes,
+                            void* stream) {
+  CacheView C;
+  int rc = view_of(cache, &C);
+  if (rc) return rc;
+  if (!shared_prefix_supported(C) || q_dtype != K8V4_BF16) return K8V4_EINVAL;
+  if ((rc = check_table(C, page_table, max_pages))) return rc;
+  if (n_seqs < 0 || n_seqs > 65535 || shared_len < 0) return K8V4_EINVAL;
+  if (max_seq_len < 0 || static_cast<int64_t>(max_seq_len) > max_pages * C.P) return K8V4_EINVAL;
+  if (!(sm_scale > 0.0f) || sm_scale > 1e30f) return K8V4_EINVAL;
+  if (n_seqs == 0) return K8V4_OK;
+  if (!q || !seq_lens || !out || !workspace) return K8V4_EINVAL;
+  if (!aligned(q, 16) || !aligned(out, 16) || !aligned(workspace, 256) || !aligned(seq_lens, 4)) return K8V4_EALIGN;
+  Launch L;
+  if ((rc = make_launch(stream, &L))) return rc;
+  AttendPlan own;
+  const SharedPlan pre = shared_plans(C, n_seqs, shared_len, max_seq_len, L.num_sms, &own);
+  if (workspace_bytes < shared_ws_bytes(C, pre, own, n_seqs)) return K8V4_ENOSPACE;
+  if (pre.cells == 0)
+    return launch_attend(L, C, own, q, q_dtype, page_table, max_pages, seq_lens, n_seqs, max_seq_len, sm_scale, out,
+                         workspace);
+  float* ws = static_cast<float*>(workspace);
+  const int splits = pre.splits + own.splits;
+  rc = launch_shared_prefix(L, C, pre, q, page_table, max_pages, seq_lens, n_seqs, max_seq_len, sm_scale, ws, splits);
+  if (rc) return rc;
+  if (own.splits > 0) {
+    rc = launch_decode_splits(L, C, own, q, q_dtype, page_table, max_pages, seq_lens, n_seqs, max_seq_len, pre.cells,
+                              sm_scale, ws, splits, pre.splits, wait_limit_ns());
+    if (rc) return rc;
+  }
+  return launch_combine(L, ws, splits, n_seqs, 1, C.H, out);
+}
+
 size_t attn_k8v4_partial_workspace_bytes(const k8v4_cache* cache, int32_t n_seqs, int32_t cell_begin,
                                          int32_t cell_end) {
   CacheView C;

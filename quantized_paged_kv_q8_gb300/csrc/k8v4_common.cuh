@@ -169,6 +169,22 @@ int launch_combine_partial(const Launch& L, const float* ws, int splits, int n_s
 // gathered partials [n_parts][n_seqs][rows][260] -> out [n_seqs][rows][256]
 int launch_combine_parts(const Launch& L, const float* parts, int n_parts, int n_seqs, int n_rows_per_seq,
                          float* out);
+// decode with a shared prefix (k8v4_shared.cu): the first `cells` cells through the
+// pair kernel, which writes partial rows [n_seqs][ws_splits][8 H][260], the first
+// plan.splits of each sequence
+struct SharedPlan {
+  int cells = 0, splits = 0, tiles_per_split = 0;
+};
+bool shared_prefix_supported(const CacheView& C);
+SharedPlan plan_shared(const CacheView& C, int n_seqs, int shared_len, int max_seq_len, int num_sms);
+int launch_shared_prefix(const Launch& L, const CacheView& C, const SharedPlan& plan, const void* q, const int32_t* pt,
+                         int64_t max_pages, const int32_t* lens, int n_seqs, int max_seq_len, float sm_scale, float* ws,
+                         int ws_splits);
+// the cells from cell_begin on of every sequence as split partials (no merge):
+// splits first_split .. of [n_seqs][ws_splits][8 H][260]
+int launch_decode_splits(const Launch& L, const CacheView& C, const AttendPlan& plan, const void* q, int q_dtype,
+                         const int32_t* pt, int64_t max_pages, const int32_t* steps, int n_seqs, int max_seq_len,
+                         int cell_begin, float sm_scale, float* ws, int ws_splits, int first_split, uint32_t wait_ns);
 // queries and keys: per-head RMS norm (weights may be null) and position rotation
 int launch_norm_rope(const Launch& L, const void* q, int64_t q_stride, int n_q, const void* k, int64_t k_stride,
                      int n_k, int dtype, const float* q_weight, const float* k_weight, float eps, const int64_t* pos,

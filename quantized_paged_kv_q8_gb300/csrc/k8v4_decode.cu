@@ -105,6 +105,7 @@ struct DecodeParams {
   int64_t max_pages;
   const int32_t* steps;
   int max_seq_len, cells_per_split, splits;
+  int ws_splits;              // partial rows per sequence in ws (the splits, or more where others write theirs beside them)
   int cell_base, cell_limit;  // the cell range the splits cover: [cell_base, cell_limit)
   float sm_scale_log2;
   float* ws;
@@ -352,7 +353,7 @@ __global__ void __launch_bounds__(32 * (QF32 ? kMaxWorkersF32 : kMaxWorkers), 1)
   // rows empty (m = -inf: the combine skips them) and leaves
   if (n_tiles == 0) {
     if (threadIdx.x < kGqa) {
-      float* dst = p.ws + ((static_cast<int64_t>(b) * p.splits + split) * HQ + g * kGqa + threadIdx.x) * kPStride;
+      float* dst = p.ws + ((static_cast<int64_t>(b) * p.ws_splits + split) * HQ + g * kGqa + threadIdx.x) * kPStride;
       dst[256] = -INFINITY;
       dst[257] = 0.0f;
     }
@@ -804,7 +805,7 @@ __global__ void __launch_bounds__(32 * (QF32 ? kMaxWorkersF32 : kMaxWorkers), 1)
     } else {
       scale = 1.0f / 16384.0f;          // 2^-14 of p'
     }
-    float* dst = p.ws + ((static_cast<int64_t>(b) * p.splits + split) * HQ + g * kGqa + h) * kPStride;
+    float* dst = p.ws + ((static_cast<int64_t>(b) * p.ws_splits + split) * HQ + g * kGqa + h) * kPStride;
     reinterpret_cast<float4*>(dst)[lane] = make_float4(v[0] * scale, v[1] * scale, v[2] * scale, v[3] * scale);
     reinterpret_cast<float4*>(dst)[32 + lane] = make_float4(v[4] * scale, v[5] * scale, v[6] * scale, v[7] * scale);
     if (lane == 0) {
@@ -1416,8 +1417,11 @@ bool maps_of(const CacheView& C, CUtensorMap* k, CUtensorMap* v, int box_rows = 
   return true;
 }
 
+// what follows the split kernel: the final rows, one merged partial row each, or nothing
+enum class Join { kFinal, kPartial, kNone };
+
 template <int FMT, bool QF32>
-int launch_impl(const Launch& L, DecodeParams p, int n_seqs, float* out, bool partial) {
+int launch_impl(const Launch& L, DecodeParams p, int n_seqs, float* out, Join join) {
   p.L = layout_of(FMT, p.C.H, QF32 ? kMaxWorkersF32 : kMaxWorkers);
   CUtensorMap mk, mv;
   if (!maps_of(p.C, &mk, &mv)) return K8V4_ECUDA;
@@ -1438,8 +1442,9 @@ int launch_impl(const Launch& L, DecodeParams p, int n_seqs, float* out, bool pa
   cfg.numAttrs = 1;
   if (cudaLaunchKernelEx(&cfg, kern, mk, mv, p) != cudaSuccess) return K8V4_ECUDA;
   if (cudaGetLastError() != cudaSuccess) return K8V4_ECUDA;
-  return partial ? launch_combine_partial(L, p.ws, p.splits, n_seqs, p.C.H, out)
-                 : launch_combine(L, p.ws, p.splits, n_seqs, 1, p.C.H, out);
+  if (join == Join::kNone) return K8V4_OK;
+  return join == Join::kPartial ? launch_combine_partial(L, p.ws, p.splits, n_seqs, p.C.H, out)
+                                : launch_combine(L, p.ws, p.splits, n_seqs, 1, p.C.H, out);
 }
 
 }  // namespace
@@ -1494,6 +1499,7 @@ DecodeParams params_of(const Launch& L, const CacheView& C, const AttendPlan& pl
   p.max_seq_len = max_seq_len;
   p.cells_per_split = plan.cells_per_split;
   p.splits = plan.splits;
+  p.ws_splits = plan.splits;
   p.cell_base = 0;
   p.cell_limit = max_seq_len;
   p.sm_scale_log2 = sm_scale * 1.4426950408889634f;
@@ -1507,12 +1513,12 @@ DecodeParams params_of(const Launch& L, const CacheView& C, const AttendPlan& pl
   p.page_div = FastDiv(static_cast<uint32_t>(C.P));
   return p;
 }
-int dispatch(const Launch& L, const DecodeParams& p, int fmt, bool f32, int n_seqs, float* out, bool partial) {
+int dispatch(const Launch& L, const DecodeParams& p, int fmt, bool f32, int n_seqs, float* out, Join join) {
   if (fmt == K8V4_FORMAT_K8V4)
-    return f32 ? launch_impl<K8V4_FORMAT_K8V4, true>(L, p, n_seqs, out, partial)
-               : launch_impl<K8V4_FORMAT_K8V4, false>(L, p, n_seqs, out, partial);
-  return f32 ? launch_impl<K8V4_FORMAT_INT8, true>(L, p, n_seqs, out, partial)
-             : launch_impl<K8V4_FORMAT_INT8, false>(L, p, n_seqs, out, partial);
+    return f32 ? launch_impl<K8V4_FORMAT_K8V4, true>(L, p, n_seqs, out, join)
+               : launch_impl<K8V4_FORMAT_K8V4, false>(L, p, n_seqs, out, join);
+  return f32 ? launch_impl<K8V4_FORMAT_INT8, true>(L, p, n_seqs, out, join)
+             : launch_impl<K8V4_FORMAT_INT8, false>(L, p, n_seqs, out, join);
 }
 
 template <int NQ>
@@ -1548,7 +1554,7 @@ int launch_decode(const Launch& L, const CacheView& C, const AttendPlan& plan, c
   p.k_new = k_new;
   p.v_new = v_new;
   p.kv_bf16 = kv_dtype == K8V4_BF16 ? 1 : 0;
-  return dispatch(L, p, C.fmt, q_dtype == K8V4_F32, n_seqs, out, false);
+  return dispatch(L, p, C.fmt, q_dtype == K8V4_F32, n_seqs, out, Join::kFinal);
 }
 
 int launch_decode_partial(const Launch& L, const CacheView& C, const AttendPlan& plan, const void* q, int q_dtype,
@@ -1559,7 +1565,19 @@ int launch_decode_partial(const Launch& L, const CacheView& C, const AttendPlan&
   DecodeParams p = params_of(L, C, plan, q, pt, max_pages, steps, max_seq_len, sm_scale, ws, wait_ns);
   p.cell_base = cell_begin;
   p.cell_limit = cell_end;
-  return dispatch(L, p, C.fmt, q_dtype == K8V4_F32, n_seqs, partial, true);
+  return dispatch(L, p, C.fmt, q_dtype == K8V4_F32, n_seqs, partial, Join::kPartial);
+}
+
+int launch_decode_splits(const Launch& L, const CacheView& C, const AttendPlan& plan, const void* q, int q_dtype,
+                         const int32_t* pt, int64_t max_pages, const int32_t* steps, int n_seqs, int max_seq_len,
+                         int cell_begin, float sm_scale, float* ws, int ws_splits, int first_split, uint32_t wait_ns) {
+  if (n_seqs == 0) return K8V4_OK;
+  float* first = ws + static_cast<int64_t>(first_split) * C.H * kGqa * kPStride;
+  DecodeParams p = params_of(L, C, plan, q, pt, max_pages, steps, max_seq_len, sm_scale, first, wait_ns);
+  p.cell_base = cell_begin;
+  p.cell_limit = max_seq_len;
+  p.ws_splits = ws_splits;
+  return dispatch(L, p, C.fmt, q_dtype == K8V4_F32, n_seqs, nullptr, Join::kNone);
 }
 
 

@@ -109,3 +109,28 @@ def test_binding_checks_its_tensors(L):
     assert k8._token_stride(packed[:, :, 16:18], 2, "k") == 20 * 256
     with pytest.raises(ValueError):
         k8._token_stride(packed[:, :2, 16:18], 2, "k")
+
+
+@pytest.mark.parametrize("bad,code", [
+    (dict(q=None), k8.EINVAL), (dict(q=ODD), k8.EALIGN), (dict(dtype=k8.F32), k8.EINVAL), (dict(pt=None), k8.EINVAL),
+    (dict(mp=0), k8.EINVAL), (dict(lens=None), k8.EINVAL), (dict(n=-1), k8.EINVAL), (dict(n=65536), k8.EINVAL),
+    (dict(max_len=65), k8.EINVAL), (dict(shared=-1), k8.EINVAL), (dict(scale=0.0), k8.EINVAL),
+    (dict(scale=float("nan")), k8.EINVAL), (dict(out=None), k8.EINVAL), (dict(out=ODD), k8.EALIGN),
+    (dict(ws=None), k8.EINVAL), (dict(ws=ODD), k8.EALIGN)])
+def test_decode_shared_refuses(L, bad, code):
+    a = dict(q=FAKE, dtype=k8.BF16, pt=FAKE, mp=4, lens=FAKE, n=4, max_len=64, shared=64, scale=0.0625, out=FAKE, ws=FAKE)
+    a.update(bad)
+    call = lambda d: L.attn_k8v4_decode_shared(d, a["q"], a["dtype"], a["pt"], a["mp"], a["lens"], a["n"], a["max_len"],
+                                               a["shared"], a["scale"], a["out"], a["ws"], 1 << 24, None)
+    assert call(_desc()) == code
+    for fmt in (k8.FORMAT_INT8, k8.FORMAT_Q4):
+        assert call(_desc(format=fmt)) == k8.EINVAL
+
+
+def test_decode_shared_workspace(L):
+    d = _desc(n_pages=1 << 20, page_size=64)
+    size = L.attn_k8v4_shared_workspace_bytes
+    assert size(d, 32, 32768, 34101) > size(d, 16, 32768, 34101) > 0
+    assert size(d, 32, 0, 1000) == L.attn_k8v4_workspace_bytes(d, 32, 1, 1000)
+    assert size(_desc(format=k8.FORMAT_Q4), 32, 64, 64) == 0 and size(d, -1, 64, 64) == 0 and size(d, 4, -1, 64) == 0
+    assert L.attn_k8v4_decode_shared(d, None, k8.BF16, FAKE, 4, None, 0, 64, 64, 0.0625, None, None, 0, None) == k8.OK

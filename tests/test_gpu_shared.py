@@ -1,0 +1,202 @@
+"""attn_k8v4_decode_shared against the oracle (64-bit attention over its own
+cache) and, at sizes the oracle is slow for, against attn_k8v4_decode: prefixes that
+end inside a tile or a page, sequences that end inside the prefix or see nothing,
+group sizes around the 16 and 32 sequences of a CTA and a pair, page sizes, head
+counts, bad pages, the bounded waits, and graphs."""
+import numpy as np
+import pytest
+import torch
+
+import oracle
+import quantized_paged_kv_q8_gb300 as k8
+import synth
+from gpu_util import TOL, dev_tensor, rel_err
+
+pytestmark = pytest.mark.gpu
+
+
+def build(seed, n_seqs, shared, own, P, H=2, with_oracle=True):
+    """A cache whose sequences share their first `shared` cells (the page the prefix ends in is each
+    sequence's own copy), `own` cells behind it each: (gpu cache, oracle cache, page table)."""
+    n_sh, full = -(-shared // P), shared // P
+    total = shared + own
+    n_pages = n_sh + n_seqs * (-(-total // P) - full) + 2
+    ids = np.random.default_rng(seed).permutation(n_pages).astype(np.int32)
+    pt = np.empty((n_seqs, -(-total // P)), np.int32)
+    pt[:, :full] = ids[:full]
+    pt[:, full:] = ids[n_sh:n_sh + n_seqs * (pt.shape[1] - full)].reshape(n_seqs, -1)
+    gpu = k8.PagedCache(n_pages, P, H)
+    gpu.pages.random_(0, 256)                       # pages nobody fills hold anything
+    gpu.pages.bitwise_and_(0x7b)                    # but no NaN scale
+    ref = oracle.Cache(n_pages, P, H) if with_oracle else None
+    kv = [synth.kv_values(seed, t, 0, shared, H, 3, "bf16") for t in (synth.T_K, synth.T_V)]
+    pos = torch.zeros(1, dtype=torch.int64, device="cuda")
+    for b in range(n_seqs if shared % P else 1):    # every copy of the shared cells
+        kd, vd = (dev_tensor(t, (1, shared, H, 256)) for t in kv)
+        row = pt[b:b + 1]
+        k8.kv_append_k8v4(gpu, torch.from_numpy(row.copy()).cuda(), pos, kd, vd)
+        if ref is not None:
+            ref.append(row, np.array([0]), kv[0].f32.reshape(1, shared, H, 256), kv[1].f32.reshape(1, shared, H, 256))
+    if own:
+        for b in range(n_seqs):
+            mine = [synth.kv_values(seed + 1 + b, t, 1, own, H, 3, "bf16") for t in (synth.T_K, synth.T_V)]
+            kd, vd = (dev_tensor(t, (1, own, H, 256)) for t in mine)
+            row = pt[b:b + 1]
+            k8.kv_append_k8v4(gpu, torch.from_numpy(row.copy()).cuda(), pos + shared, kd, vd)
+            if ref is not None:
+                ref.append(row, np.array([shared]), mine[0].f32.reshape(1, own, H, 256), mine[1].f32.reshape(1, own, H, 256))
+    return gpu, ref, pt
+
+
+def run(gpu, q, pt, lens, max_len, shared):
+    lens_d = torch.from_numpy(np.asarray(lens, np.int32)).cuda()
+    out = torch.full(q.shape, float("nan"), device="cuda")
+    ws = k8.shared_workspace(gpu, q.shape[0], shared, max_len)
+    ws.fill_(0xFF)                                  # NaN partials where nothing is written
+    k8.attn_k8v4_decode_shared(gpu, q, pt, lens_d, max_len, shared, out, ws)
+    return out
+
+
+@pytest.mark.parametrize("n_seqs,shared,own,P,H", [
+    (2, 64, 0, 64, 2), (3, 128, 5, 16, 1), (5, 1000, 40, 16, 2), (8, 333, 70, 48, 2), (16, 640, 17, 64, 2),
+    (17, 2064, 33, 128, 2), (32, 1531, 100, 64, 2), (33, 777, 1, 16, 3), (70, 700, 30, 64, 2), (4, 64, 200, 32, 2),
+    (6, 79, 3, 64, 2), (9, 15, 100, 16, 2)])
+def test_shared_decode_against_oracle(n_seqs, shared, own, P, H):
+    seed = synth.config_seed(3) + 31 * n_seqs + shared
+    gpu, ref, pt = build(seed, n_seqs, shared, own, P, H)
+    rng = np.random.default_rng(seed)
+    lens = shared + rng.integers(0, own + 1, n_seqs)
+    lens[0] = shared + own
+    if n_seqs > 3:                                  # inside the prefix (also its first tile), nothing, just behind it
+        lens[1], lens[2], lens[3] = rng.integers(1, shared), 0, min(shared + own, shared + 1)
+        lens[-1] = min(3, shared)
+    q = synth.q_values(seed, 7, n_seqs, H, "bf16")
+    got = run(gpu, dev_tensor(q, (n_seqs, 8 * H, 256)), torch.from_numpy(pt).cuda(), lens, shared + own, shared)
+    assert k8.k8v4_last_device_status() == 0
+    rs, rh, rv = oracle.decode_rows(n_seqs, 8 * H, lens)
+    want = ref.attention(pt, rs, rh, rv, q.f32.reshape(-1, 256))
+    assert rel_err(got.cpu().numpy().reshape(-1, 256), want) <= TOL
+
+
+@pytest.mark.parametrize("n_seqs,shared,own", [(32, 32768, 300), (48, 20011, 64), (128, 16384, 16)])
+def test_shared_decode_against_decode_long(n_seqs, shared, own):
+    """Both calls are within TOL of the exact result, so within 2 TOL of each other."""
+    seed = synth.config_seed(3) + n_seqs
+    gpu, _, pt = build(seed, n_seqs, shared, own, 64, with_oracle=False)
+    rng = np.random.default_rng(seed)
+    lens = (shared + rng.integers(0, own + 1, n_seqs)).astype(np.int32)
+    lens[3], lens[5] = 0, shared // 3
+    q = dev_tensor(synth.q_values(seed, 7, n_seqs, 2, "bf16"), (n_seqs, 16, 256))
+    ptd = torch.from_numpy(pt).cuda()
+    got = run(gpu, q, ptd, lens, shared + own, shared)
+    want = torch.empty_like(got)
+    ws = k8.workspace(gpu, n_seqs, 1, shared + own)
+    k8.attn_k8v4_decode(gpu, q, ptd, torch.from_numpy(lens).cuda(), shared + own, want, ws)
+    assert k8.k8v4_last_device_status() == 0
+    assert rel_err(got.cpu().numpy(), want.cpu().numpy()) <= 2 * TOL
+
+
+def test_shared_decode_moving_maxima_and_extreme_queries():
+    """Scores that grow along the prefix by far more than 2^8 (every few tiles a row's reference maximum
+    moves), next to zero queries and queries of 1e30 and 1e-30."""
+    n_seqs, shared, P, H = 40, 2048, 64, 2
+    seed = synth.config_seed(3) + 5
+    rng = np.random.default_rng(seed)
+    k = rng.standard_normal((1, shared, H, 256)).astype(np.float32)
+    k *= (np.linspace(0, 6, shared)[None, :, None, None] * rng.choice([0.2, 1.0], shared)[None, :, None, None]).astype(np.float32)
+    v = rng.standard_normal((1, shared, H, 256)).astype(np.float32)
+    q = rng.standard_normal((n_seqs, 16, 256)).astype(np.float32)
+    q[3] = 0
+    q[5] *= 1e-30
+    q[7, 2] *= 40
+    kt, vt, qt = (torch.from_numpy(x).bfloat16() for x in (k, v, q))
+    pt = np.random.default_rng(1).permutation(shared // P).astype(np.int32)[None]
+    gpu, ref = k8.PagedCache(shared // P, P, H), oracle.Cache(shared // P, P, H)
+    k8.kv_append_k8v4(gpu, torch.from_numpy(pt).cuda(), torch.zeros(1, dtype=torch.int64, device="cuda"), kt.cuda(), vt.cuda())
+    ref.append(pt, np.array([0]), kt.float().numpy(), vt.float().numpy())
+    ptn = np.repeat(pt, n_seqs, 0)
+    lens = np.full(n_seqs, shared)
+    lens[9] = 130
+    got = run(gpu, qt.cuda(), torch.from_numpy(ptn).cuda(), lens, shared, shared)
+    assert k8.k8v4_last_device_status() == 0
+    rs, rh, rv = oracle.decode_rows(n_seqs, 16, lens)
+    want = ref.attention(ptn, rs, rh, rv, qt.float().numpy().reshape(-1, 256))
+    assert rel_err(got.cpu().numpy().reshape(-1, 256), want) <= TOL
+
+
+def test_shared_decode_bad_pages_and_lengths():
+    """A page id out of range inside the prefix: its cells are skipped and recorded; a length past max_seq_len is
+    clipped, one below 0 counts as 0."""
+    n_seqs, shared, P = 20, 640, 16
+    seed = synth.config_seed(3) + 6
+    gpu, ref, pt = build(seed, n_seqs, shared, 0, P)
+    q = synth.q_values(seed, 7, n_seqs, 2, "bf16")
+    qd = dev_tensor(q, (n_seqs, 16, 256))
+    bad = pt.copy()
+    bad[:, 2] = gpu.n_pages + 3
+    bad[:, 21] = -1
+    lens = np.full(n_seqs, shared)
+    got = run(gpu, qd, torch.from_numpy(bad).cuda(), lens, shared, shared)
+    assert k8.k8v4_last_device_status() == k8.ERANGE
+    # the same attention with those cells cut out: a table without the two pages
+    keep = np.delete(pt, [2, 21], 1)
+    rs, rh, rv = oracle.decode_rows(n_seqs, 16, np.full(n_seqs, shared - 2 * P))
+    want = ref.attention(keep, rs, rh, rv, q.f32.reshape(-1, 256))
+    assert rel_err(got.cpu().numpy().reshape(-1, 256), want) <= TOL
+    lens[4], lens[6] = shared + 9, -3
+    got = run(gpu, qd, torch.from_numpy(pt).cuda(), lens, shared, shared)
+    assert k8.k8v4_last_device_status() == k8.ERANGE
+    rs, rh, rv = oracle.decode_rows(n_seqs, 16, np.clip(lens, 0, shared))
+    want = ref.attention(pt, rs, rh, rv, q.f32.reshape(-1, 256))
+    assert rel_err(got.cpu().numpy().reshape(-1, 256), want) <= TOL
+    assert k8.k8v4_last_device_status() == 0
+
+
+def test_shared_decode_wait_timeout_then_recovery():
+    """With the wait bound below 1 us the pair kernel's waits give up at their first poll: it records K8V4_ECUDA,
+    waits for its own products, frees its tensor memory and returns; a normal call afterwards is right."""
+    n_seqs, shared = 33, 4096
+    seed = synth.config_seed(3) + 8
+    gpu, ref, pt = build(seed, n_seqs, shared, 0, 64)
+    q = synth.q_values(seed, 7, n_seqs, 2, "bf16")
+    qd, ptd = dev_tensor(q, (n_seqs, 16, 256)), torch.from_numpy(pt).cuda()
+    lens = np.full(n_seqs, shared)
+    assert k8.k8v4_last_device_status() == 0
+    try:
+        k8.k8v4_set_wait_limit_ns(1)
+        run(gpu, qd, ptd, lens, shared, shared)
+        assert k8.k8v4_last_device_status() == k8.ECUDA
+    finally:
+        k8.k8v4_set_wait_limit_ns(0)
+    got = run(gpu, qd, ptd, lens, shared, shared)
+    assert k8.k8v4_last_device_status() == 0
+    rs, rh, rv = oracle.decode_rows(n_seqs, 16, lens)
+    want = ref.attention(pt, rs, rh, rv, q.f32.reshape(-1, 256))
+    assert rel_err(got.cpu().numpy().reshape(-1, 256), want) <= TOL
+
+
+def test_shared_decode_captured_and_repeatable():
+    """Captured and replayed with new queries and lengths in place; equal bits each time and on another stream."""
+    n_seqs, shared, own = 24, 3000, 200
+    seed = synth.config_seed(3) + 9
+    gpu, _, pt = build(seed, n_seqs, shared, own, 64, with_oracle=False)
+    q = dev_tensor(synth.q_values(seed, 7, n_seqs, 2, "bf16"), (n_seqs, 16, 256))
+    ptd = torch.from_numpy(pt).cuda()
+    lens = torch.full((n_seqs,), shared + own, dtype=torch.int32, device="cuda")
+    out = torch.empty(q.shape, device="cuda")
+    ws = k8.shared_workspace(gpu, n_seqs, shared, shared + own)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        k8.attn_k8v4_decode_shared(gpu, q, ptd, lens, shared + own, shared, out, ws)
+    side = torch.cuda.Stream()
+    for step in range(3):
+        lens.sub_(37)
+        q.neg_()
+        graph.replay()
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            want = torch.empty_like(out)
+            k8.attn_k8v4_decode_shared(gpu, q, ptd, lens, shared + own, shared, want, torch.empty_like(ws))
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+    assert k8.k8v4_last_device_status() == 0
