@@ -44,6 +44,7 @@
 #include <mutex>
 
 #include "k8v4_quant.cuh"
+#include "k8v4_tma.cuh"
 
 namespace k8v4 {
 namespace {
@@ -227,23 +228,6 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, uint32_
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-__device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes) {
-  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* tm, int c0, int c1, int c2, int c3,
-                                            uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
-      "[%6];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(tm)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar)
-      : "memory");
-}
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-               "l"(src), "r"(bytes), "r"(bar)
-               : "memory");
-}
-
 // four int8 codes -> two fp16x2 (exact): 0x64XX is 1024 + XX in fp16
 __device__ __forceinline__ void codes_to_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
   const uint32_t u = w ^ 0x80808080u;            // c + 128
@@ -1448,6 +1432,8 @@ int launch_impl(const Launch& L, DecodeParams p, int n_seqs, float* out, Join jo
 }
 
 }  // namespace
+
+bool tensor_maps_of(const CacheView& C, CUtensorMap* k, CUtensorMap* v) { return maps_of(C, k, v); }
 
 bool decode_ws_supported(const CacheView& C) {
   return (C.fmt == K8V4_FORMAT_K8V4 || C.fmt == K8V4_FORMAT_INT8) && C.n_pages < (int64_t(1) << 31) &&

@@ -21,17 +21,18 @@
 //  - warps have roles, handing over through mbarriers, so the tensor pipe, the
 //    softmax and the conversion of neighbouring tiles overlap:
 //      warps 0-7    rows: two threads per row (32 cells, and 128 of O's dims, each)
-//      warps 8-11   conversion: global memory -> registers -> operand tiles
+//      warps 8-11   conversion: raw tile -> registers -> operand tiles
 //      warp 12      (leader CTA) issues every product of the pair
-//    The row warps hold O in fp32 registers (208 a thread, from the others' share);
+//      warp 13      copies the raw tiles (TMA)
+//    The row warps hold O in fp32 registers (216 a thread, from the others' share);
 //  - the reference maximum of a row moves only when a tile exceeds it by 2^8, and
 //    then its O tile is rescaled in tensor memory, so the two CTAs need not agree;
 //    every kChain tiles O is folded into the registers, in both CTAs at the same
 //    tile, because the tensor core's accumulation is not rounded to nearest (2.9e-5
 //    after 2,048 cells without the fold).
 //
-// Tensor memory (512 columns): S buffers [0,128), [128,256) (S0 | S1 each; the
-// P terms overlay S0), O [256,512).  QK(i+2) overwrites P(i): its S1 half, which
+// Tensor memory (512 columns): S buffers [0,128), [128,256) (S0 | S1 each; a
+// thread's P terms overlay its own columns of S0), O [256,512).  QK(i+2) overwrites P(i): its S1 half, which
 // P does not touch, is issued behind PV(i) at once, its S0 half when PV(i) is done.
 //
 // Every mbarrier wait is bounded: on timeout the warp raises the CTA's failure
@@ -39,8 +40,10 @@
 // kernel records an error, waits for its own products (bounded), frees its tensor
 // memory and returns.
 #include <algorithm>
+#include <mutex>
 
 #include "k8v4_tc.cuh"
+#include "k8v4_tma.cuh"
 
 namespace k8v4 {
 namespace {
@@ -51,12 +54,12 @@ constexpr int kRows = 128;                  // query rows per CTA (256 per pair)
 constexpr int kPairSeqs = 2 * kRows / kGqa; // 32
 constexpr int kTileN = 64;
 constexpr int kThreads = 512;
-constexpr int kRowThreads = 256, kConvWarp0 = 8, kIssueWarp = 12;
+constexpr int kConvWarp0 = 8, kIssueWarp = 12, kLoadWarp = 13;
 constexpr int kChain = 8;                   // tiles accumulated in one TMEM O tile
 constexpr float kSlack = 8.0f;              // log2 headroom of P above its row's reference maximum
 constexpr uint32_t kWaitDefaultNs = 1000000000u;
-// registers per thread after the split; 2 * 208 + 72 + 24 = 4 * 128, what the block launches with
-constexpr int kRowRegs = 208, kConvRegs = 72, kIssueRegs = 24;
+// registers per thread after the split; 2 * 216 + 56 + 24 = 4 * 128, what the block launches with
+constexpr int kRowRegs = 216, kConvRegs = 56, kIssueRegs = 24;
 static_assert(2 * kRowRegs + kConvRegs + kIssueRegs <= 4 * 128, "register split");
 
 // shared memory (bytes); operand tiles 1024-byte aligned, the same in both CTAs
@@ -65,19 +68,26 @@ constexpr int kKOff = kQOff + 65536;                  // K fp16, 2 buffers x [4 
 constexpr int kKBuf = 16384;
 constexpr int kVOff = kKOff + 2 * kKBuf;              // V fp16, 2 buffers x 2 planes x [2 atoms][64 cells][128 B]
 constexpr int kVPlane = 16384, kVBuf = 2 * kVPlane;
-constexpr int kKsOff = kVOff + 2 * kVBuf;             // K scales, 4 tiles x [64][2] f32
+constexpr int kKsOff = kVOff + 2 * kVBuf;             // K scales, 4 tiles x [2][64] f32
 constexpr int kRedOff = kKsOff + 4 * 512;             // [2][128] f32 exchange, [128] score factors
 constexpr int kBarOff = kRedOff + 2 * 512 + 512;
-constexpr int kCtlOff = kBarOff + 128;                // tmem slot, failure word, largest visible count, bad tiles
-constexpr int kSmemBytes = kCtlOff + 64;
+constexpr int kCtlOff = kBarOff + 192;                // tmem slot, failure word, bad groups of 4 tiles, valid groups of the stages
+constexpr int kRawOff = (kCtlOff + 64 + 1023) / 1024 * 1024;   // raw tiles, as many stages as fit (3, or 2 from 4 KV heads on)
+constexpr int kSmemMax = 227 * 1024;
+// a raw tile: K codes of the CTA's 32 cells (2 groups x 2 boxes of 16 cells x 128 B), V nibbles of the 64
+// cells (4 boxes), and the runs of K and V scales of all heads (4 groups x 128 H and 256 H bytes)
+constexpr int kRawV = 8192, kRawKs = 16384;
+constexpr int raw_bytes(int H) { return (kRawKs + 1536 * H + 1023) / 1024 * 1024; }
+constexpr int raw_stages(int H) { return (kSmemMax - kRawOff) / raw_bytes(H) < 3 ? (kSmemMax - kRawOff) / raw_bytes(H) : 3; }
+static_assert(raw_stages(8) >= 2, "raw stages");
 // the epilogue reuses the operand tiles as a fp32 [128][256] row buffer
 static_assert(kKsOff - kQOff >= kRows * 256 * 4, "row buffer");
-static_assert(kSmemBytes <= 227 * 1024, "shared memory");
 
 // mbarriers, at kBarOff + 8 * index
-enum { kBarKFull = 0, kBarVFull = 2, kBarPFull = 4, kBarSFull = 6, kBarODone = 8, kBarKsFull = 10, kBarDrain = 14 };
+enum { kBarKFull = 0, kBarVFull = 2, kBarPFull = 4, kBarSFull = 6, kBarODone = 8, kBarKsFull = 10,
+       kBarDrain = 14, kBarRawFull = 16, kBarRawEmpty = 20 };
 
-constexpr uint32_t kTmemCols = 512, kSBuf = 128, kS1Col = 64, kOCol = 256, kP2Col = 32;
+constexpr uint32_t kTmemCols = 512, kSBuf = 128, kS1Col = 64, kOCol = 256, kP2Col = 16;
 
 struct SharedParams {
   CacheView C;
@@ -94,6 +104,7 @@ struct SharedParams {
   int* status;
   uint32_t wait_ns;
   FastDiv page_div;
+  int stages, stage_bytes;  // raw tiles in flight
 };
 
 // ---------------------------------------------------------------- pair PTX
@@ -110,32 +121,15 @@ __device__ __forceinline__ uint32_t map_to(uint32_t saddr, uint32_t rank) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(saddr), "r"(rank));
   return a;
 }
+// The arrivals that hand operand tiles to the products carry no wider release than
+// the CTA's: what the tensor core reads is made visible by the proxy and tcgen05
+// fences ahead of them, and a cluster-wide release would also wait for the
+// global loads of the next tile (measured: 723 us against the figure at the top).
 __device__ __forceinline__ void arrive_cluster(uint32_t cluster_addr) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 __device__ __forceinline__ void arrive_local(uint32_t bar) {
-  asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-__device__ __forceinline__ bool try_cluster(uint32_t bar, uint32_t parity, uint32_t sleep_ns) {
-  uint32_t done;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(done)
-      : "r"(bar), "r"(parity), "r"(sleep_ns)
-      : "memory");
-  return done != 0;
-}
-// as mbar_wait, acquiring from both CTAs of the pair
-__device__ __forceinline__ bool wait_pair(uint32_t bar, uint32_t parity, uint32_t limit_ns) {
-  if (try_cluster(bar, parity, 0)) return true;
-  if (limit_ns < 1000u) return false;
-  const uint64_t t0 = global_ns();
-  for (;;) {
-    if (global_ns() - t0 >= limit_ns) return false;
-    if (try_cluster(bar, parity, 20000u)) return true;
-  }
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 __device__ __forceinline__ void tmem_alloc_pair(uint32_t slot, uint32_t ncols) {
   asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(slot), "r"(ncols) : "memory");
@@ -168,6 +162,29 @@ __device__ __forceinline__ void commit_pair(uint32_t bar) {
       "h"(both)
       : "memory");
 }
+// one lane of a converged warp
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
+}
+// the same over the two warps that share 32 rows (warps w and w + 4, w < 4)
+__device__ __forceinline__ bool pair_any(int w, bool pred) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %2, 0;\n\t"
+      "barrier.cta.red.or.pred q, %1, 64, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(w + 3), "r"(pred ? 1u : 0u)
+      : "memory");
+  return r != 0;
+}
 // a barrier over the row warps that also ORs a predicate
 __device__ __forceinline__ bool rows_any(bool pred) {
   uint32_t r;
@@ -182,22 +199,38 @@ __device__ __forceinline__ bool rows_any(bool pred) {
   return r != 0;
 }
 __device__ __forceinline__ void rows_barrier() { asm volatile("barrier.cta.sync 2, 256;" ::: "memory"); }
-__device__ __forceinline__ void tmem_ld8x2(uint32_t ta, uint32_t tb, float a[8], float b[8]) {
-  uint32_t r[16];
+// two runs of 16 fp32 columns of this thread's TMEM lane
+__device__ __forceinline__ void tmem_ld16x2(uint32_t ta, uint32_t tb, float a[16], float b[16]) {
+  uint32_t r[32];
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%16];\n\t"
-      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%8,%9,%10,%11,%12,%13,%14,%15}, [%17];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%32];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%33];\n\t"
       "tcgen05.wait::ld.sync.aligned;"
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(ta), "r"(tb)
       : "memory");
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
+  for (int i = 0; i < 16; ++i) {
     a[i] = __uint_as_float(r[i]);
-    b[i] = __uint_as_float(r[8 + i]);
+    b[i] = __uint_as_float(r[16 + i]);
   }
 }
+// two runs of 8 columns; the caller waits (tmem_wait_st)
+__device__ __forceinline__ void tmem_st8x2(uint32_t ta, uint32_t tb, const float a[8], const float b[8]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%2,%3,%4,%5,%6,%7,%8,%9};\n\t"
+      "tcgen05.st.sync.aligned.32x32b.x8.b32 [%1], {%10,%11,%12,%13,%14,%15,%16,%17};"
+      ::"r"(ta), "r"(tb), "r"(__float_as_uint(a[0])), "r"(__float_as_uint(a[1])), "r"(__float_as_uint(a[2])),
+        "r"(__float_as_uint(a[3])), "r"(__float_as_uint(a[4])), "r"(__float_as_uint(a[5])), "r"(__float_as_uint(a[6])),
+        "r"(__float_as_uint(a[7])), "r"(__float_as_uint(b[0])), "r"(__float_as_uint(b[1])), "r"(__float_as_uint(b[2])),
+        "r"(__float_as_uint(b[3])), "r"(__float_as_uint(b[4])), "r"(__float_as_uint(b[5])), "r"(__float_as_uint(b[6])),
+        "r"(__float_as_uint(b[7]))
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_ld8(uint32_t taddr, float v[8]) {
   uint32_t r[8];
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
@@ -211,7 +244,9 @@ __device__ __forceinline__ void tmem_ld8(uint32_t taddr, float v[8]) {
 
 // ---------------------------------------------------------------- the kernel
 // grid: x = 2 * (split * groups + group), y = KV head; clusters of two along x.
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) shared_prefix_kernel(const SharedParams p) {
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) shared_prefix_kernel(const __grid_constant__ CUtensorMap tm_k,
+                                                                                            const __grid_constant__ CUtensorMap tm_v,
+                                                                                            const SharedParams p) {
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sb = smem_u32(smem);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -243,6 +278,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) shared_
     }
     for (int i = 0; i < 4; ++i) mbar_init(bars + 8 * (kBarKsFull + i), 4);
     mbar_init(bars + 8 * kBarDrain, 1);
+    for (int i = 0; i < p.stages; ++i) {
+      mbar_init(bars + 8 * (kBarRawFull + i), 1);       // the loader, and the bytes of its copies
+      mbar_init(bars + 8 * (kBarRawEmpty + i), 4);      // 4 conversion warps
+    }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     ctl[1] = 0;
     for (int i = 4; i < 8; ++i) ctl[i] = 0;
@@ -329,15 +368,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) shared_
     auto fold = [&](float a) {                             // o_run = (o_run + O tile) * a
       const float2 a2 = make_float2(a, a);
 #pragma unroll
-      for (int h = 0; h < 16; ++h) {
-        float o[8];
-        tmem_ld8(o_tile + 8 * h, o);
+      for (int h = 0; h < 4; ++h) {
+        float o[32];
+        tmem_ld32(o_tile + 32 * h, o);
 #pragma unroll
-        for (int i = 0; i < 8; i += 2) {
-          const float2 r = __fmul2_rn(__fadd2_rn(make_float2(o_run[8 * h + i], o_run[8 * h + i + 1]),
+        for (int i = 0; i < 32; i += 2) {
+          const float2 r = __fmul2_rn(__fadd2_rn(make_float2(o_run[32 * h + i], o_run[32 * h + i + 1]),
                                                  make_float2(o[i], o[i + 1])), a2);
-          o_run[8 * h + i] = r.x;
-          o_run[8 * h + i + 1] = r.y;
+          o_run[32 * h + i] = r.x;
+          o_run[32 * h + i + 1] = r.y;
         }
       }
     };
@@ -357,46 +396,51 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) shared_
     for (int i = 0; i < n_tiles; ++i) {
       const int buf = i & 1;
       const uint32_t parity = (i >> 1) & 1;
-      if (!wait_pair(bars + 8 * (kBarSFull + buf), parity, p.wait_ns) ||
+      if (!mbar_wait(bars + 8 * (kBarSFull + buf), parity, p.wait_ns) ||
           !mbar_wait(bars + 8 * (kBarKsFull + (i & 3)), (i >> 2) & 1, p.wait_ns)) {
         failed = true;
         ctl[1] = 1;
       }
       tc_fence_after();
+      // scores, unscaled (my_f > 0, so the maximum commutes with it); cell c of this half
       const uint32_t sbase = tmem + lane_base + kSBuf * buf + 32 * half;
-      const float* ks = ksbuf + 128 * (i & 3) + 64 * half;
-      float sc[32];
-      float mx = -INFINITY;
+      const float* ks = ksbuf + 128 * (i & 3) + 32 * half;             // s0 of the tile's cells, then s1
+      float2 sc[16];
 #pragma unroll
-      for (int h = 0; h < 4; ++h) {
-        float a[8], b[8];
-        tmem_ld8x2(sbase + 8 * h, sbase + kS1Col + 8 * h, a, b);
+      for (int h = 0; h < 2; ++h) {
+        float a[16], b[16];
+        tmem_ld16x2(sbase + 16 * h, sbase + kS1Col + 16 * h, a, b);
 #pragma unroll
-        for (int c = 0; c < 8; c += 2) {
-          const float4 k2 = *reinterpret_cast<const float4*>(ks + 16 * h + 2 * c);
-          sc[8 * h + c] = k2.x * a[c] + k2.y * b[c];
-          sc[8 * h + c + 1] = k2.z * a[c + 1] + k2.w * b[c + 1];
+        for (int c = 0; c < 16; c += 4) {
+          const float4 k0 = *reinterpret_cast<const float4*>(ks + 16 * h + c);
+          const float4 k1 = *reinterpret_cast<const float4*>(ks + 64 + 16 * h + c);
+          sc[8 * h + c / 2] = __ffma2_rn(make_float2(k1.x, k1.y), make_float2(b[c], b[c + 1]),
+                                         __fmul2_rn(make_float2(k0.x, k0.y), make_float2(a[c], a[c + 1])));
+          sc[8 * h + c / 2 + 1] = __ffma2_rn(make_float2(k1.z, k1.w), make_float2(b[c + 2], b[c + 3]),
+                                             __fmul2_rn(make_float2(k0.z, k0.w), make_float2(a[c + 2], a[c + 3])));
         }
       }
       const int vis = my_vis - (tile0 + i) * kTileN - 32 * half;       // cells [0, vis) of this half
       const int bad = ctl[4 + (i & 3)];                                // 16-cell groups on a page out of range
       if (vis < 32 || bad) {
 #pragma unroll
-        for (int c = 0; c < 32; ++c)
-          if (c >= vis || ((bad >> (8 * half + (c >> 4))) & 1)) sc[c] = -INFINITY;
+        for (int c = 0; c < 32; c += 2) {
+          const bool off = ((bad >> (2 * half + (c >> 4))) & 1) != 0;
+          if (c >= vis || off) sc[c / 2].x = -INFINITY;
+          if (c + 1 >= vis || off) sc[c / 2].y = -INFINITY;
+        }
       }
+      float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-      for (int c = 0; c < 32; ++c) mx = fmaxf(mx, sc[c]);
-      const float top = mx * my_f;
-      tc_fence_before();
-      // every thread's scores are in registers past this vote, so P may overlay S
-      const bool any = rows_any(failed || top > m_run + kSlack);
-      tc_fence_after();
+      for (int c = 0; c < 16; ++c) mx[c & 3] = fmaxf(mx[c & 3], fmaxf(sc[c].x, sc[c].y));
+      const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * my_f;
+      // the two threads of a row agree on its reference: a vote of their two warps
+      const bool any = pair_any(warp & 3, failed || top > m_run + kSlack);
       float alpha = 1.0f;
       if (any) {
         red[half * kRows + row] = top;
-        // the row warps leave together: the failure word is read once, ahead of a vote
-        if (rows_any(failed || ctl[1] != 0)) { failed = true; break; }
+        // both warps leave together: the failure word is read once, ahead of a vote
+        if (pair_any(warp & 3, failed || ctl[1] != 0)) { failed = true; break; }
         const float mt = fmaxf(red[row], red[kRows + row]);
         if (mt > m_run + kSlack) {
           alpha = exp2f(m_run - mt);                                   // 0 on the first visible tile
@@ -404,46 +448,49 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) shared_
           l_part *= alpha;
         }
       }
-      const bool folds = i > 0 && i % kChain == 0;
-      if (i > 0 && (folds || any)) {
-        if (folds || __any_sync(kFull, alpha != 1.0f)) {
-          if (!wait_pair(bars + 8 * (kBarODone + (buf ^ 1)), ((i - 1) >> 1) & 1, p.wait_ns)) {
-            failed = true;
-            ctl[1] = 1;
-          }
-          tc_fence_after();
-          if (folds) fold(alpha);
-          else rescale(alpha);
-        }
-      }
+      // P * 2^7 in two fp16 terms: the top 11 bits of p, and the rest of it rounded.
+      // They overlay this thread's own S0 columns, P1 in the first 16, P2 behind it
       const float mu = (m_run == -INFINITY ? 0.0f : m_run) - 7.0f;
+      const float2 f2 = make_float2(my_f, my_f), mu2 = make_float2(-mu, -mu);
       float2 psum = make_float2(0.0f, 0.0f);
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         float p1[8], p2[8];
 #pragma unroll
-        for (int c = 0; c < 16; c += 2) {
-          const float a = ex2_ftz(fmaf(sc[16 * h + c], my_f, -mu)), b = ex2_ftz(fmaf(sc[16 * h + c + 1], my_f, -mu));
-          const __half2 h1 = __floats2half2_rn(a, b);
-          const float2 f1 = __half22float2(h1);
-          const float2 r = __ffma2_rn(f1, make_float2(-1.0f, -1.0f), make_float2(a, b));   // exact
-          const __half2 h2 = __floats2half2_rn(r.x, r.y);
-          psum = __fadd2_rn(psum, make_float2(a, b));
-          p1[c >> 1] = __uint_as_float(*reinterpret_cast<const uint32_t*>(&h1));
-          p2[c >> 1] = __uint_as_float(*reinterpret_cast<const uint32_t*>(&h2));
+        for (int c = 0; c < 8; ++c) {
+          const float2 e = __ffma2_rn(sc[8 * h + c], f2, mu2);
+          const float2 q = make_float2(ex2_ftz(e.x), ex2_ftz(e.y));
+          const float2 t = make_float2(__uint_as_float(__float_as_uint(q.x) & 0xffffe000u),
+                                       __uint_as_float(__float_as_uint(q.y) & 0xffffe000u));
+          const float2 r = __fadd2_rn(q, make_float2(-t.x, -t.y));     // exact
+          const __half2 h1 = __floats2half2_rn(t.x, t.y), h2 = __floats2half2_rn(r.x, r.y);
+          psum = __fadd2_rn(psum, q);
+          p1[c] = __uint_as_float(*reinterpret_cast<const uint32_t*>(&h1));
+          p2[c] = __uint_as_float(*reinterpret_cast<const uint32_t*>(&h2));
         }
-        const uint32_t pb = tmem + lane_base + kSBuf * buf + 16 * half + 8 * h;
-        tmem_st8(pb, p1);
-        tmem_st8(pb + kP2Col, p2);
+        tmem_st8x2(sbase + 8 * h, sbase + kP2Col + 8 * h, p1, p2);
       }
       l_part += psum.x + psum.y;
+      tmem_wait_st();
+      // O of the tiles so far: into the registers at every kChain-th tile (both
+      // CTAs), rescaled in place where a reference moved in between
+      const bool folds = i > 0 && i % kChain == 0;
+      if (folds || (i > 0 && any && __any_sync(kFull, alpha != 1.0f))) {
+        if (!mbar_wait(bars + 8 * (kBarODone + (buf ^ 1)), ((i - 1) >> 1) & 1, p.wait_ns)) {
+          failed = true;
+          ctl[1] = 1;
+        }
+        tc_fence_after();
+        if (folds) fold(alpha);
+        else rescale(alpha);
+      }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) arrive_cluster(p_full0 + 8 * buf);
     }
     // ---- the last O tile, then o / m / l of the rows
     if (!failed && n_tiles > 0) {
-      if (wait_pair(bars + 8 * (kBarODone + ((n_tiles - 1) & 1)), ((n_tiles - 1) >> 1) & 1, p.wait_ns)) {
+      if (mbar_wait(bars + 8 * (kBarODone + ((n_tiles - 1) & 1)), ((n_tiles - 1) >> 1) & 1, p.wait_ns)) {
         tc_fence_after();
         fold(1.0f);
         tc_fence_before();
@@ -458,6 +505,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) shared_
     const bool stop = rows_any(failed);
     if (!stop) {
       const float l = red[row] + red[kRows + row];
+      // inverse Walsh-Hadamard transform: seven stages over the thread's own 128
+      // dims in registers, the eighth (dims d and d + 128) as the rows are written
+#pragma unroll
+      for (int h = 1; h < 128; h <<= 1) {
+#pragma unroll
+        for (int i = 0; i < 128; ++i) {
+          if (i & h) continue;
+          const float a = o_run[i], b = o_run[i + h];
+          o_run[i] = a + b;
+          o_run[i + h] = a - b;
+        }
+      }
       float* rowbuf = reinterpret_cast<float*>(smem + kQOff);          // [128][256] fp32, rotated by 4 * row
 #pragma unroll
       for (int i = 0; i < 128; i += 4) {
@@ -477,34 +536,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) shared_
       for (int r = warp; r < kRows; r += 8) {
         const int s = seq0 + r / kGqa;
         if (s >= p.n_seqs) break;
-        float v[8];
-#pragma unroll
-        for (int e = 0; e < 8; e += 4) {
-          const float4 x = *reinterpret_cast<const float4*>(rowbuf + r * 256 + ((8 * lane + e + 4 * r) & 255));
-          v[e] = x.x; v[e + 1] = x.y; v[e + 2] = x.z; v[e + 3] = x.w;
-        }
-#pragma unroll
-        for (int hh = 1; hh < 8; hh <<= 1) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            if (e & hh) continue;
-            const float a = v[e], b = v[e + hh];
-            v[e] = a + b;
-            v[e + hh] = a - b;
-          }
-        }
-#pragma unroll
-        for (int m = 1; m < 32; m <<= 1) {
-          const bool upper = (lane & m) != 0;
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float x = __shfl_xor_sync(kFull, v[e], m);
-            v[e] = upper ? x - v[e] : v[e] + x;
-          }
-        }
-        float* dst = p.ws + ((static_cast<int64_t>(s) * p.ws_splits + split) * HQ + g * kGqa + r % kGqa) * kPStride + 8 * lane;
-        reinterpret_cast<float4*>(dst)[0] = make_float4(v[0] * 0.0625f, v[1] * 0.0625f, v[2] * 0.0625f, v[3] * 0.0625f);
-        reinterpret_cast<float4*>(dst)[1] = make_float4(v[4] * 0.0625f, v[5] * 0.0625f, v[6] * 0.0625f, v[7] * 0.0625f);
+        const float4 a = *reinterpret_cast<const float4*>(rowbuf + r * 256 + ((4 * lane + 4 * r) & 255));
+        const float4 b = *reinterpret_cast<const float4*>(rowbuf + r * 256 + ((128 + 4 * lane + 4 * r) & 255));
+        float* dst = p.ws + ((static_cast<int64_t>(s) * p.ws_splits + split) * HQ + g * kGqa + r % kGqa) * kPStride + 4 * lane;
+        constexpr float kInv = 0.0625f;
+        *reinterpret_cast<float4*>(dst) = make_float4((a.x + b.x) * kInv, (a.y + b.y) * kInv, (a.z + b.z) * kInv, (a.w + b.w) * kInv);
+        *reinterpret_cast<float4*>(dst + 128) = make_float4((a.x - b.x) * kInv, (a.y - b.y) * kInv, (a.z - b.z) * kInv, (a.w - b.w) * kInv);
       }
     }
   } else if (warp < kIssueWarp) {
@@ -512,97 +549,71 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) shared_
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kConvRegs));
     const int t = tid - 32 * kConvWarp0;                   // 0..127
     const int cw = t >> 5;
-    // K: cell 32 rank + lane, dims [64 cw, +64); V: cell t & 63, blocks 4 rank + 2 (t >> 6) + {0, 1}
-    const int kcell = 32 * static_cast<int>(rank) + lane, vcell = t & 63, vblk = 4 * static_cast<int>(rank) + 2 * (t >> 6);
+    // K: cell 32 rank + lane, dims [64 cw, +64); V: cell t & 63, blocks 4 rank + 2 (t >> 6) + {0, 1}.
+    // The copies put 16-byte unit u of a row at u ^ (row & 7) (128-byte swizzle).
+    const int vcell = t & 63, vblk = 4 * static_cast<int>(rank) + 2 * (t >> 6), vrow = vcell & 15;
     const uint32_t k_full0 = map_to(bars + 8 * kBarKFull, 0), v_full0 = map_to(bars + 8 * kBarVFull, 0);
-    auto page_of = [&](int i, int cell) -> int {           // page id of a cell of tile i, -1 past the prefix, -2 if out of range
-      const int c = (tile0 + i) * kTileN + cell;
-      if (i >= n_tiles || c >= p.cells) return -1;
-      const int64_t pidx = p.page_div.div(static_cast<uint32_t>(c));
-      const int page = pidx < p.max_pages ? p.pt[pidx] : -2;
-      return page >= 0 && page < C.n_pages ? page : -2;
-    };
-    auto slot_of = [&](int i, int cell) -> int {
-      const int c = (tile0 + i) * kTileN + cell;
-      return c - static_cast<int>(p.page_div.div(static_cast<uint32_t>(c))) * C.P;
-    };
-    uint4 kraw[4], vraw[2];
-    uint32_t vd;
-    float2 ksc;
-    int kpage = page_of(0, kcell), vpage = page_of(0, vcell);
-    bool kbad = false;                                     // (threads of the first two conversion warps) this cell's page
-    auto load_k = [&](int i) {                             // K codes; the scales of cell vcell come with V's page
-      if (kpage >= 0) {
-        const uint8_t* src = C.pages + static_cast<int64_t>(kpage) * C.page_bytes +
-                             (static_cast<int64_t>(slot_of(i, kcell)) * C.H + g) * 256 + 64 * cw;
-#pragma unroll
-        for (int u = 0; u < 4; ++u) kraw[u] = __ldg(reinterpret_cast<const uint4*>(src) + u);
-      } else {
-#pragma unroll
-        for (int u = 0; u < 4; ++u) kraw[u] = make_uint4(0, 0, 0, 0);
-      }
-      kpage = page_of(i + 1, kcell);
-    };
-    auto load_v = [&](int i) {
-      kbad = vpage == -2;
-      ksc = make_float2(0.0f, 0.0f);
-      if (vpage >= 0) {
-        const int64_t r = static_cast<int64_t>(slot_of(i, vcell)) * C.H + g;
-        const uint8_t* base = C.pages + static_cast<int64_t>(vpage) * C.page_bytes;
-        const uint4* src = reinterpret_cast<const uint4*>(base + C.v_off() + r * 128 + 16 * vblk);
-        vraw[0] = __ldg(src);
-        vraw[1] = __ldg(src + 1);
-        vd = __ldg(reinterpret_cast<const uint32_t*>(base + C.vs_off() + r * 16 + 2 * vblk));
-        if (t < 64) ksc = __ldg(reinterpret_cast<const float2*>(base + C.ks_off() + r * 8));
-      } else {
-        vraw[0] = vraw[1] = make_uint4(0x88888888u, 0x88888888u, 0x88888888u, 0x88888888u);
-        vd = 0;
-      }
-      vpage = page_of(i + 1, vcell);
-    };
-    load_k(0);
-    load_v(0);
+    const uint32_t kraw = (lane >> 4) * 4096 + (cw >> 1) * 2048 + (lane & 15) * 128;
+    const uint32_t vraw = kRawV + (vcell >> 4) * 2048 + vrow * 128;
+    const uint32_t ksraw = kRawKs + (vcell >> 4) * 128 * C.H + (vrow * C.H + g) * 8;
+    const uint32_t vsraw = kRawKs + 512 * C.H + (vcell >> 4) * 256 * C.H + (vrow * C.H + g) * 16 + 2 * vblk;
+    int stage = 0;
+    uint32_t raw_phase = 0;
     for (int i = 0; i < n_tiles; ++i) {
       const int buf = i & 1;
       const uint32_t last = ((i - 2) >> 1) & 1;            // phase of tile i - 2 on the buffers' barriers
+      const uint32_t raw = sb + kRawOff + stage * p.stage_bytes;
+      if (!mbar_wait(bars + 8 * (kBarRawFull + stage), raw_phase, p.wait_ns)) { ctl[1] = 1; break; }
+      const int valid = ctl[8 + stage];                    // the tile's 16-cell groups that were copied; bits 4..7: on a bad page
       // ---- K(i) and its scales, once QK(i - 2) has read the buffer
-      if (i >= 2 && !wait_pair(bars + 8 * (kBarSFull + buf), last, p.wait_ns)) { ctl[1] = 1; break; }
+      if (i >= 2 && !mbar_wait(bars + 8 * (kBarSFull + buf), last, p.wait_ns)) { ctl[1] = 1; break; }
       {
         const uint32_t dst = sb + kKOff + buf * kKBuf + cw * 4096;
+        uint4 kw[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) kw[u] = lds128(raw + kraw + (((4 * (cw & 1) + u) ^ (lane & 7)) << 4));
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
+          const uint4 w = kw[u];
           uint32_t h[8];
-          i8x4_to_f16(kraw[u].x, h[0], h[1]);
-          i8x4_to_f16(kraw[u].y, h[2], h[3]);
-          i8x4_to_f16(kraw[u].z, h[4], h[5]);
-          i8x4_to_f16(kraw[u].w, h[6], h[7]);
+          i8x4_to_f16(w.x, h[0], h[1]);
+          i8x4_to_f16(w.y, h[2], h[3]);
+          i8x4_to_f16(w.z, h[4], h[5]);
+          i8x4_to_f16(w.w, h[6], h[7]);
           sts128(dst + swz(lane, 2 * u), h[0], h[1], h[2], h[3]);
           sts128(dst + swz(lane, 2 * u + 1), h[4], h[5], h[6], h[7]);
         }
         if (t < 64) {
-          reinterpret_cast<float2*>(ksbuf + 128 * (i & 3))[t] = ksc;
-          const unsigned b = __ballot_sync(kFull, kbad);   // lanes 0 and 16 stand for their 16-cell groups
-          if (b && lane == 0) record_status(p.status, K8V4_ERANGE);
-          if (lane == 0) reinterpret_cast<volatile uint8_t*>(smem + kCtlOff + 16)[4 * (i & 3) + cw] =
-              static_cast<uint8_t>((b & 1u) | ((b >> 15) & 2u));
+          float2 ksc;
+          asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(ksc.x), "=f"(ksc.y) : "r"(raw + ksraw));
+          ksbuf[128 * (i & 3) + t] = ksc.x;
+          ksbuf[128 * (i & 3) + 64 + t] = ksc.y;
+          if (t == 0) ctl[4 + (i & 3)] = valid >> 4;
         }
-        asm volatile("fence.proxy.async;" ::: "memory");
+        fence_async_smem();
         __syncwarp();
         if (lane == 0) {
           arrive_local(bars + 8 * (kBarKsFull + (i & 3)));
           arrive_cluster(k_full0 + 8 * buf);
         }
       }
-      if (i + 1 < n_tiles) load_k(i + 1);
       // ---- V(i), once PV(i - 2) has read the buffer
-      if (i >= 2 && !wait_pair(bars + 8 * (kBarODone + buf), last, p.wait_ns)) { ctl[1] = 1; break; }
+      if (i >= 2 && !mbar_wait(bars + 8 * (kBarODone + buf), last, p.wait_ns)) { ctl[1] = 1; break; }
       {
         const uint32_t dst = sb + kVOff + buf * kVBuf + (t >> 6) * 8192;
+        // a group that was not copied counts with V = 0 (its P is 0, its bytes are anything)
+        uint32_t vd;
+        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(vd) : "r"(raw + vsraw));
+        const uint4 vw[2] = {lds128(raw + vraw + ((vblk ^ (vrow & 7)) << 4)), lds128(raw + vraw + (((vblk + 1) ^ (vrow & 7)) << 4))};
+        if (!((valid >> (vcell >> 4)) & 1)) vd = 0;
+        __syncwarp();
+        if (lane == 0) arrive_local(bars + 8 * (kBarRawEmpty + stage));
 #pragma unroll
         for (int blk = 0; blk < 2; ++blk) {
           const __half dh = __ushort_as_half(static_cast<unsigned short>(vd >> (16 * blk)));
           const __half2 d2 = __halves2half2(dh, dh);
-          const uint32_t ws4[4] = {vraw[blk].x, vraw[blk].y, vraw[blk].z, vraw[blk].w};
+          const uint4 w = vw[blk];
+          const uint32_t ws4[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
           for (int hn = 0; hn < 2; ++hn) {                 // low nibbles: dims 0..15 of the block, high: 16..31
             uint32_t v1[8], v2[8];
@@ -618,72 +629,140 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) shared_
             sts128(dst + kVPlane + swz(vcell, u0 + 1), v2[4], v2[5], v2[6], v2[7]);
           }
         }
-        asm volatile("fence.proxy.async;" ::: "memory");
+        fence_async_smem();
         __syncwarp();
         if (lane == 0) arrive_cluster(v_full0 + 8 * buf);
       }
-      if (i + 1 < n_tiles) load_v(i + 1);
+      if (++stage == p.stages) {
+        stage = 0;
+        raw_phase ^= 1;
+      }
     }
   } else {
     // ================================================================ issue
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
-    if (warp == kIssueWarp && rank == 0 && lane == 0) {
+    // The whole warp runs the loop, and one elected lane executes the products:
+    // with the control flow uniform the descriptors live in uniform registers,
+    // where a lone thread's would be moved there one by one ahead of every product
+    // (about 100 clocks each: 2,800 a tile, more than the products take).
+    if (__shfl_sync(kFull, warp, 0) == kIssueWarp && rank == 0) {
       constexpr uint32_t idS = idesc_f16(256, 64, false, false);
       constexpr uint32_t idO = idesc_f16(256, 256, false, true);
+      const uint32_t tm = __shfl_sync(kFull, tmem, 0);
       const uint64_t dq0 = smem_desc(sb + kQOff, 16, 1024);
       const uint64_t dk0 = smem_desc(sb + kKOff, 16, 1024);
       const uint64_t dv0 = smem_desc(sb + kVOff, 8192, 1024);
+      const bool leader = elect_one();
+      auto ready = [&](int bar, uint32_t parity) -> bool {
+        return __all_sync(kFull, mbar_wait(bars + 8 * bar, parity, p.wait_ns)) != 0;
+      };
       auto qk_half = [&](int buf, int h) {                 // S[buf]_h = Q_h K_h^T
-        uint64_t a = dq0 + ((h * 32768) >> 4), b = dk0 + ((buf * kKBuf + h * 8192) >> 4);
-        const uint32_t d = tmem + kSBuf * buf + kS1Col * h;
-#pragma unroll 1
-        for (int c = 0; c < 2; ++c) {                      // 64-dim chunks of the half
+        const uint64_t a = dq0 + ((h * 32768) >> 4), b = dk0 + ((buf * kKBuf + h * 8192) >> 4);
+        const uint32_t d = tm + kSBuf * buf + kS1Col * h;
+        if (leader) {
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk) mma_pair(d, a + 2 * kk, b + 2 * kk, idS, (c | kk) ? 1u : 0u);
-          a += 16384 >> 4;
-          b += 4096 >> 4;
+          for (int kk = 0; kk < 8; ++kk)
+            mma_pair(d, a + (((kk >> 2) * 16384 + (kk & 3) * 32) >> 4), b + (((kk >> 2) * 4096 + (kk & 3) * 32) >> 4), idS,
+                     kk ? 1u : 0u);
         }
       };
       bool ok = true;
-      for (int i = 0; ok && i < min(2, n_tiles); ++i) {
-        if (!wait_pair(bars + 8 * (kBarKFull + i), 0, p.wait_ns)) { ok = false; break; }
+      for (int i = 0; i < min(2, n_tiles); ++i) {
+        if (!ready(kBarKFull + i, 0)) { ok = false; break; }
         tc_fence_after();
-        qk_half(i, 1);
         qk_half(i, 0);
-        commit_pair(bars + 8 * (kBarSFull + i));
+        qk_half(i, 1);
+        if (leader) commit_pair(bars + 8 * (kBarSFull + i));
       }
       for (int i = 0; ok && i < n_tiles; ++i) {
         const int buf = i & 1;
         const uint32_t parity = (i >> 1) & 1;
-        if (!wait_pair(bars + 8 * (kBarVFull + buf), parity, p.wait_ns) ||
-            !wait_pair(bars + 8 * (kBarPFull + buf), parity, p.wait_ns)) { ok = false; break; }
+        if (!ready(kBarVFull + buf, parity) || !ready(kBarPFull + buf, parity)) { ok = false; break; }
         tc_fence_after();
-        const bool fresh = i % kChain == 0;
-        uint32_t pa = tmem + kSBuf * buf;
-        uint64_t v1 = dv0 + ((buf * kVBuf) >> 4);
-#pragma unroll 1
-        for (int kk = 0; kk < 4; ++kk) {                   // 16 cells = 8 TMEM columns of fp16 pairs
-          mma_pair_ta(tmem + kOCol, pa, v1, idO, (kk > 0 || !fresh) ? 1u : 0u);
-          mma_pair_ta(tmem + kOCol, pa, v1 + (kVPlane >> 4), idO, 1u);
-          mma_pair_ta(tmem + kOCol, pa + kP2Col, v1, idO, 1u);
-          pa += 8;
-          v1 += 2048 >> 4;
+        const uint32_t more = i % kChain != 0 ? 1u : 0u;   // O of this chain so far is kept
+        const uint32_t pa = tm + kSBuf * buf;
+        const uint64_t v1 = dv0 + ((buf * kVBuf) >> 4);
+        if (leader) {
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) {                 // 16 cells = 8 TMEM columns of fp16 pairs
+            const uint64_t v = v1 + ((kk * 2048) >> 4);
+            const uint32_t p1 = pa + 32 * (kk >> 1) + 8 * (kk & 1);   // of half kk / 2
+            mma_pair_ta(tm + kOCol, p1, v, idO, kk ? 1u : more);
+            mma_pair_ta(tm + kOCol, p1, v + (kVPlane >> 4), idO, 1u);
+            mma_pair_ta(tm + kOCol, p1 + kP2Col, v, idO, 1u);
+          }
+          commit_pair(bars + 8 * (kBarODone + buf));
         }
-        commit_pair(bars + 8 * (kBarODone + buf));
         if (i + 2 < n_tiles) {
-          if (!wait_pair(bars + 8 * (kBarKFull + buf), parity ^ 1, p.wait_ns)) { ok = false; break; }
-          tc_fence_after();
-          qk_half(buf, 1);
-          if (!wait_pair(bars + 8 * (kBarODone + buf), parity, p.wait_ns)) { ok = false; break; }
+          // QK(i + 2) overwrites P(i).  It is not queued behind PV(i): a product that
+          // finds the queue full holds up the other warps of this scheduler
+          if (!ready(kBarKFull + buf, parity ^ 1) || !ready(kBarODone + buf, parity)) { ok = false; break; }
           tc_fence_after();
           qk_half(buf, 0);
-          commit_pair(bars + 8 * (kBarSFull + buf));
+          qk_half(buf, 1);
+          if (leader) commit_pair(bars + 8 * (kBarSFull + buf));
         }
       }
       if (!ok) ctl[1] = 1;
-      // nothing of this thread's is in flight past here (after a failure too)
-      commit_pair(bars + 8 * kBarDrain);
-      (void)wait_pair(bars + 8 * kBarDrain, 0, kWaitDefaultNs);
+      // nothing of this warp's is in flight past here (after a failure too)
+      if (leader) commit_pair(bars + 8 * kBarDrain);
+      (void)mbar_wait(bars + 8 * kBarDrain, 0, kWaitDefaultNs);
+    } else if (__shfl_sync(kFull, warp, 0) == kLoadWarp) {
+      // ============================================================== copies
+      // raw tiles by TMA, p.stages ahead of the conversion (per-thread copies cost
+      // the conversion warps 870 clocks a tile: each touches 32 rows).  Page ids of
+      // eight tiles, four groups each, are held one per lane.
+      const bool leader = elect_one();
+      const int H = C.H;
+      int page_mine = -1, stage = 0;
+      uint32_t phase = 1;                                  // the first round finds every stage empty
+      int i = 0;
+      for (; i < n_tiles; ++i) {
+        if ((i & 7) == 0) {
+          const int c = (tile0 + i + (lane >> 2)) * kTileN + 16 * (lane & 3);
+          page_mine = INT32_MIN;                           // behind the prefix
+          if (i + (lane >> 2) < n_tiles && c < p.cells) {
+            const int64_t pidx = p.page_div.div(static_cast<uint32_t>(c));
+            const int page = pidx < p.max_pages ? p.pt[pidx] : -1;
+            page_mine = page >= 0 && page < C.n_pages ? page : -1;
+          }
+        }
+        if (!__all_sync(kFull, mbar_wait(bars + 8 * (kBarRawEmpty + stage), phase, p.wait_ns))) { ctl[1] = 1; break; }
+        const uint32_t dst = sb + kRawOff + stage * p.stage_bytes, bar = bars + 8 * (kBarRawFull + stage);
+        const int my_group_page = __shfl_sync(kFull, page_mine, 4 * (i & 7) + (lane & 3));
+        const unsigned good = __ballot_sync(kFull, my_group_page >= 0) & 15u;
+        const unsigned bad = __ballot_sync(kFull, my_group_page == -1) & 15u;
+        const unsigned kgood = (good >> (2 * rank)) & 3u;
+        if (leader) {
+          if (bad) record_status(p.status, K8V4_ERANGE);
+          ctl[8 + stage] = static_cast<int>(good | (bad << 4));
+          mbar_expect_tx(bar, __popc(good) * (2048u + 384u * H) + __popc(kgood) * 4096u);
+        }
+#pragma unroll 1
+        for (int q = 0; q < 4; ++q) {
+          const int page = __shfl_sync(kFull, my_group_page, q);
+          if (!leader || page < 0) continue;
+          const int cell = (tile0 + i) * kTileN + 16 * q;
+          const int slot = cell - static_cast<int>(p.page_div.div(static_cast<uint32_t>(cell))) * C.P;
+          const int kq = q - 2 * static_cast<int>(rank);
+          if (kq == 0 || kq == 1) {
+            tma_load_4d(dst + kq * 4096, &tm_k, 0, g, slot, page, bar);
+            tma_load_4d(dst + kq * 4096 + 2048, &tm_k, 128, g, slot, page, bar);
+          }
+          tma_load_4d(dst + kRawV + q * 2048, &tm_v, 0, g, slot, page, bar);
+          const uint8_t* pg = C.pages + static_cast<int64_t>(page) * C.page_bytes;
+          bulk_load(dst + kRawKs + q * 128 * H, pg + C.ks_off() + static_cast<int64_t>(slot) * 8 * H, 128 * H, bar);
+          bulk_load(dst + kRawKs + 512 * H + q * 256 * H, pg + C.vs_off() + static_cast<int64_t>(slot) * 16 * H, 256 * H, bar);
+        }
+        __syncwarp();
+        if (++stage == p.stages) {
+          stage = 0;
+          phase ^= 1;
+        }
+      }
+      // no copy is in flight past here (after a failure too): the last tiles' stages
+      for (int j = max(0, i - p.stages); j < i; ++j)
+        (void)mbar_wait(bars + 8 * (kBarRawFull + j % p.stages), (j / p.stages) & 1, kWaitDefaultNs);
     }
     __syncwarp();
   }
@@ -700,10 +779,51 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) shared_
 }  // namespace
 
 // ---------------------------------------------------------------- host side
-bool shared_prefix_supported(const CacheView& C) { return C.fmt == K8V4_FORMAT_K8V4; }
+bool shared_prefix_supported(const CacheView& C) { return C.fmt == K8V4_FORMAT_K8V4 && decode_ws_supported(C); }
 
 // The prefix cells that the pair kernel takes (0: none, every cell goes through
 // the per-sequence decode) and its splits.
+namespace {
+// Set-up of the kernel on the current device, once: its shared memory, its
+// registers at launch (the split hands out that many) and the CTA pairs that the
+// device runs at a time (an odd SM in a cluster's reach stays without a partner,
+// so 152 SMs need not give 76).
+struct PairSetup {
+  bool done = false, ok = false;
+  int slots = 0;
+};
+std::mutex g_setup_mu;
+PairSetup g_setup[64];
+PairSetup pair_setup() {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) {
+    cudaGetLastError();
+    return PairSetup{};
+  }
+  std::lock_guard<std::mutex> lock(g_setup_mu);
+  PairSetup& s = g_setup[dev];
+  if (s.done) return s;
+  cudaFuncAttributes fa;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmemMax;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  s.ok = cudaFuncGetAttributes(&fa, shared_prefix_kernel) == cudaSuccess &&
+         fa.numRegs * 4 >= 2 * kRowRegs + kConvRegs + kIssueRegs &&
+         cudaFuncSetAttribute(shared_prefix_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax) == cudaSuccess &&
+         cudaOccupancyMaxActiveClusters(&s.slots, shared_prefix_kernel, &cfg) == cudaSuccess && s.slots > 0;
+  if (!s.ok) cudaGetLastError();
+  s.done = true;
+  return s;
+}
+}  // namespace
+
 SharedPlan plan_shared(const CacheView& C, int n_seqs, int shared_len, int max_seq_len, int num_sms) {
   SharedPlan pl{};
   const int cells = std::min(shared_len, max_seq_len) / 16 * 16;
@@ -711,7 +831,8 @@ SharedPlan plan_shared(const CacheView& C, int n_seqs, int shared_len, int max_s
   pl.cells = cells;
   const int tiles = (cells + kTileN - 1) / kTileN;
   const int64_t units = static_cast<int64_t>((n_seqs + kPairSeqs - 1) / kPairSeqs) * C.H;
-  const int slots = std::max(1, num_sms / 2);
+  const PairSetup setup = pair_setup();
+  const int slots = setup.ok ? setup.slots : std::max(1, num_sms / 2);
   // one pair per two SMs at a time: the split count that minimises waves x (tiles
   // a pair sweeps + the fixed cost of a pair, worth about kFixedTiles tiles)
   constexpr int kFixedTiles = 10;
@@ -748,17 +869,14 @@ int launch_shared_prefix(const Launch& L, const CacheView& C, const SharedPlan& 
   p.status = L.status;
   p.wait_ns = wait_limit_ns() ? wait_limit_ns() : kWaitDefaultNs;
   p.page_div = FastDiv(static_cast<uint32_t>(C.P));
-  // the register split needs the registers it hands out at launch
-  static const int launch_regs = [] {
-    cudaFuncAttributes attr;
-    return cudaFuncGetAttributes(&attr, shared_prefix_kernel) == cudaSuccess ? attr.numRegs : 0;
-  }();
-  if (launch_regs * 4 < 2 * kRowRegs + kConvRegs + kIssueRegs) return K8V4_ECUDA;
-  if (cudaFuncSetAttribute(shared_prefix_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes) != cudaSuccess)
-    return K8V4_ECUDA;
+  p.stages = raw_stages(C.H);
+  p.stage_bytes = raw_bytes(C.H);
+  if (!pair_setup().ok) return K8V4_ECUDA;
+  CUtensorMap mk, mv;
+  if (!tensor_maps_of(C, &mk, &mv)) return K8V4_ECUDA;
   const int groups = (n_seqs + kPairSeqs - 1) / kPairSeqs;
   const dim3 grid(2u * static_cast<unsigned>(groups) * static_cast<unsigned>(plan.splits), C.H);
-  shared_prefix_kernel<<<grid, kThreads, kSmemBytes, L.stream>>>(p);
+  shared_prefix_kernel<<<grid, kThreads, kRawOff + p.stages * p.stage_bytes, L.stream>>>(mk, mv, p);
   return cudaGetLastError() == cudaSuccess ? K8V4_OK : K8V4_ECUDA;
 }
 
