@@ -315,7 +315,7 @@ static SharedPlan shared_plans(const CacheView& C, int n_seqs, int shared_len, i
   const SharedPlan pre = plan_shared(C, n_seqs, shared_len, max_seq_len, sms);
   *own = AttendPlan{};
   if (pre.cells == 0) *own = plan_attend(C, n_seqs, 1, max_seq_len, sms);
-  else if (max_seq_len > pre.cells) *own = plan_decode(C, n_seqs, max_seq_len - pre.cells, sms);
+  else if (max_seq_len > pre.cells) *own = plan_decode_splits(C, n_seqs, max_seq_len - pre.cells, sms);
   return pre;
 }
 static size_t shared_ws_bytes(const CacheView& C, const SharedPlan& pre, const AttendPlan& own, int n_seqs) {
@@ -360,14 +360,16 @@ int attn_k8v4_decode_shared(const k8v4_cache* cache, const void* q, int32_t q_dt
                          workspace);
   float* ws = static_cast<float*>(workspace);
   const int splits = pre.splits + own.splits;
-  rc = launch_shared_prefix(L, C, pre, q, page_table, max_pages, seq_lens, n_seqs, max_seq_len, sm_scale, ws, splits);
-  if (rc) return rc;
+  // the sequences' own cells, then the prefix, whose CTAs start as those of the first leave
   if (own.splits > 0) {
     rc = launch_decode_splits(L, C, own, q, q_dtype, page_table, max_pages, seq_lens, n_seqs, max_seq_len, pre.cells,
                               sm_scale, ws, splits, pre.splits, wait_limit_ns());
     if (rc) return rc;
   }
-  return launch_combine(L, ws, splits, n_seqs, 1, C.H, out);
+  rc = launch_shared_prefix(L, C, pre, q, page_table, max_pages, seq_lens, n_seqs, max_seq_len, sm_scale, ws, splits,
+                            own.splits > 0);
+  if (rc) return rc;
+  return launch_combine_rows(L, ws, splits, n_seqs, C.H, out);
 }
 
 size_t attn_k8v4_partial_workspace_bytes(const k8v4_cache* cache, int32_t n_seqs, int32_t cell_begin,

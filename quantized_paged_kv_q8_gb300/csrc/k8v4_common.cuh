@@ -164,6 +164,8 @@ uint32_t wait_limit_ns();
 int withheld_copy();
 // weighted sum of split partials (o[256], m, l rows of 260 floats) -> out, launched programmatically dependent
 int launch_combine(const Launch& L, const float* ws, int splits, int n_seqs, int n_q, int H, float* out);
+// the same for one query per sequence, a CTA per row: many rows of tens of splits
+int launch_combine_rows(const Launch& L, const float* ws, int splits, int n_seqs, int H, float* out);
 // the splits of a one-query decode merged into one unnormalised partial row per (sequence, query head)
 int launch_combine_partial(const Launch& L, const float* ws, int splits, int n_seqs, int H, float* partial);
 // gathered partials [n_parts][n_seqs][rows][260] -> out [n_seqs][rows][256]
@@ -179,7 +181,10 @@ bool shared_prefix_supported(const CacheView& C);
 SharedPlan plan_shared(const CacheView& C, int n_seqs, int shared_len, int max_seq_len, int num_sms);
 int launch_shared_prefix(const Launch& L, const CacheView& C, const SharedPlan& plan, const void* q, const int32_t* pt,
                          int64_t max_pages, const int32_t* lens, int n_seqs, int max_seq_len, float sm_scale, float* ws,
-                         int ws_splits);
+                         int ws_splits, bool behind_splits);
+// the plan of launch_decode_splits over `cells` cells: short ranges of many
+// sequences in small CTAs (pl.warps workers)
+AttendPlan plan_decode_splits(const CacheView& C, int n_seqs, int cells, int num_sms);
 // the cells from cell_begin on of every sequence as split partials (no merge):
 // splits first_split .. of [n_seqs][ws_splits][8 H][260]
 int launch_decode_splits(const Launch& L, const CacheView& C, const AttendPlan& plan, const void* q, int q_dtype,

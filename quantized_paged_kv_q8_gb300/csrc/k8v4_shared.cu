@@ -55,7 +55,7 @@ constexpr int kPairSeqs = 2 * kRows / kGqa; // 32
 constexpr int kTileN = 64;
 constexpr int kThreads = 512;
 constexpr int kConvWarp0 = 8, kIssueWarp = 12, kLoadWarp = 13;
-constexpr int kChain = 8;                   // tiles accumulated in one TMEM O tile
+constexpr int kChain = 16;                  // tiles accumulated in one TMEM O tile
 constexpr float kSlack = 8.0f;              // log2 headroom of P above its row's reference maximum
 constexpr uint32_t kWaitDefaultNs = 1000000000u;
 // registers per thread after the split; 2 * 216 + 56 + 24 = 4 * 128, what the block launches with
@@ -85,7 +85,7 @@ static_assert(kKsOff - kQOff >= kRows * 256 * 4, "row buffer");
 
 // mbarriers, at kBarOff + 8 * index
 enum { kBarKFull = 0, kBarVFull = 2, kBarPFull = 4, kBarSFull = 6, kBarODone = 8, kBarKsFull = 10,
-       kBarDrain = 14, kBarRawFull = 16, kBarRawEmpty = 20 };
+       kBarDrain = 14, kBarMost = 15, kBarRawFull = 16, kBarRawEmpty = 20 };
 
 constexpr uint32_t kTmemCols = 512, kSBuf = 128, kS1Col = 64, kOCol = 256, kP2Col = 16;
 
@@ -268,25 +268,75 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) shared_
   const int tile0 = split * p.tiles_per_split;
   const int n_tiles = min(p.tiles_per_split, (p.cells + kTileN - 1) / kTileN - tile0);
 
-  if (tid == 0) {
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(bars + 8 * (kBarKFull + i), 8);       // 4 conversion warps of both CTAs
-      mbar_init(bars + 8 * (kBarVFull + i), 8);
-      mbar_init(bars + 8 * (kBarPFull + i), 16);      // 8 row warps of both CTAs
-      mbar_init(bars + 8 * (kBarSFull + i), 1);
-      mbar_init(bars + 8 * (kBarODone + i), 1);
-    }
-    for (int i = 0; i < 4; ++i) mbar_init(bars + 8 * (kBarKsFull + i), 4);
-    mbar_init(bars + 8 * kBarDrain, 1);
-    for (int i = 0; i < p.stages; ++i) {
-      mbar_init(bars + 8 * (kBarRawFull + i), 1);       // the loader, and the bytes of its copies
-      mbar_init(bars + 8 * (kBarRawEmpty + i), 4);      // 4 conversion warps
-    }
+  if (warp == kLoadWarp) {
+    // one barrier per lane
+    int count = 0;
+    if (lane < kBarPFull) count = 8;                       // K, V tiles: 4 conversion warps of both CTAs
+    else if (lane < kBarSFull) count = 16;                 // P: 8 row warps of both CTAs
+    else if (lane < kBarKsFull) count = 1;                 // S done, O done: one commit
+    else if (lane < kBarDrain) count = 4;                  // K scales: the CTA's conversion warps
+    else if (lane < kBarRawFull) count = 1;                // everything done, three quarters of PV: one commit
+    else if (lane < kBarRawEmpty) count = 1;               // raw tile: the loader, and the bytes of its copies
+    else if (lane < kBarRawEmpty + 4) count = 4;
+    if (count) mbar_init(bars + 8 * lane, count);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    ctl[1] = 0;
-    for (int i = 4; i < 8; ++i) ctl[i] = 0;
+    if (lane < 8) ctl[1 + lane] = 0;
+    if (lane == 0) {
+      asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_k)) : "memory");
+      asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_v)) : "memory");
+    }
+    __syncwarp();
   }
   if (warp == kIssueWarp) tmem_alloc_pair(sb + kCtlOff, kTmemCols);
+
+  // ---- the load warp's copies of tile i into a stage: raw tiles by TMA (per-thread
+  // copies cost the conversion warps 870 clocks a tile: each touches 32 rows).  Page
+  // ids of eight tiles, four 16-cell groups each, are held one per lane.
+  int page_mine = INT32_MIN;
+  auto load_tile = [&](int i, int stage, bool leader) {
+    const int H = C.H;
+    if ((i & 7) == 0) {
+      const int c = (tile0 + i + (lane >> 2)) * kTileN + 16 * (lane & 3);
+      page_mine = INT32_MIN;                               // behind the prefix
+      if (i + (lane >> 2) < n_tiles && c < p.cells) {
+        const int64_t pidx = p.page_div.div(static_cast<uint32_t>(c));
+        const int page = pidx < p.max_pages ? p.pt[pidx] : -1;
+        page_mine = page >= 0 && page < C.n_pages ? page : -1;
+      }
+    }
+    const uint32_t dst = sb + kRawOff + stage * p.stage_bytes, bar = bars + 8 * (kBarRawFull + stage);
+    const int my_group_page = __shfl_sync(kFull, page_mine, 4 * (i & 7) + (lane & 3));
+    const unsigned good = __ballot_sync(kFull, my_group_page >= 0) & 15u;
+    const unsigned bad = __ballot_sync(kFull, my_group_page == -1) & 15u;
+    const unsigned kgood = (good >> (2 * rank)) & 3u;
+    if (leader) {
+      if (bad) record_status(p.status, K8V4_ERANGE);
+      ctl[8 + stage] = static_cast<int>(good | (bad << 4));
+      mbar_expect_tx(bar, __popc(good) * (2048u + 384u * H) + __popc(kgood) * 4096u);
+    }
+#pragma unroll 1
+    for (int q = 0; q < 4; ++q) {
+      const int page = __shfl_sync(kFull, my_group_page, q);
+      if (!leader || page < 0) continue;
+      const int cell = (tile0 + i) * kTileN + 16 * q;
+      const int slot = cell - static_cast<int>(p.page_div.div(static_cast<uint32_t>(cell))) * C.P;
+      const int kq = q - 2 * static_cast<int>(rank);
+      if (kq == 0 || kq == 1) {
+        tma_load_4d(dst + kq * 4096, &tm_k, 0, g, slot, page, bar);
+        tma_load_4d(dst + kq * 4096 + 2048, &tm_k, 128, g, slot, page, bar);
+      }
+      tma_load_4d(dst + kRawV + q * 2048, &tm_v, 0, g, slot, page, bar);
+      const uint8_t* pg = C.pages + static_cast<int64_t>(page) * C.page_bytes;
+      bulk_load(dst + kRawKs + q * 128 * H, pg + C.ks_off() + static_cast<int64_t>(slot) * 8 * H, 128 * H, bar);
+      bulk_load(dst + kRawKs + 512 * H + q * 256 * H, pg + C.vs_off() + static_cast<int64_t>(slot) * 16 * H, 256 * H, bar);
+    }
+    __syncwarp();
+  };
+  if (warp == kLoadWarp) {                                 // the first tiles, while the others set Q up
+    const bool leader = elect_one();
+#pragma unroll 1
+    for (int i = 0; i < min(p.stages, n_tiles); ++i) load_tile(i, i, leader);
+  }
 
   // ---- visibility of this thread's row
   int my_vis = 0;
@@ -301,40 +351,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) shared_
       my_vis = min(v, p.cells);
     }
   }
-  // ---- Q rows -> fp16 with a per-row power-of-two scale, swizzled K-major; the
-  // four parts of a row take dims [64 part, 64 part + 64)
-  {
-    const int s = seq0 + row / kGqa, h = row % kGqa;
-    uint4 raw[8];
-    if (s < p.n_seqs) {
-      const uint4* src = reinterpret_cast<const uint4*>(p.q + (static_cast<int64_t>(s) * HQ + g * kGqa + h) * kD + 64 * part);
+  // ---- Q rows -> fp16 with a per-row power-of-two scale, swizzled K-major: a warp
+  // takes a row at a time (16 B a lane); the load warp starts on the raw tiles meanwhile
+  if (warp < kLoadWarp) {
+    constexpr int kPer = (kRows + kLoadWarp - 1) / kLoadWarp;
+    uint4 raw[kPer];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) raw[i] = src[i];
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) raw[i] = make_uint4(0, 0, 0, 0);
+    for (int j = 0; j < kPer; ++j) {
+      const int r = warp + kLoadWarp * j, s = seq0 + r / kGqa;
+      raw[j] = make_uint4(0, 0, 0, 0);
+      if (r < kRows && s < p.n_seqs)
+        raw[j] = __ldg(reinterpret_cast<const uint4*>(p.q + (static_cast<int64_t>(s) * HQ + g * kGqa + r % kGqa) * kD) + lane);
     }
-    float amax = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+    for (int j = 0; j < kPer; ++j) {
+      const int r = warp + kLoadWarp * j;
+      if (r >= kRows) break;
+      const uint32_t w[4] = {raw[j].x, raw[j].y, raw[j].z, raw[j].w};
+      float amax = 0.0f;
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        amax = fmaxf(amax, fabsf(__uint_as_float(w[u] << 16)));
-        amax = fmaxf(amax, fabsf(__uint_as_float(w[u] & 0xffff0000u)));
-      }
-    }
-    float* qmax = ksbuf;                                // [4][128]: the scale buffers are not in use yet
-    qmax[part * kRows + row] = amax;
-    __syncthreads();
-    amax = fmaxf(fmaxf(qmax[row], qmax[kRows + row]), fmaxf(qmax[2 * kRows + row], qmax[3 * kRows + row]));
-    const int ex = amax > 0.0f ? static_cast<int>((__float_as_uint(amax) >> 23) & 0xffu) - 127 : 0;
-    const int sh = max(-100, min(100, 14 - ex));
-    const float up = ldexpf(1.0f, sh);
-    if (part == 0) fsc[row] = p.sm_scale_log2 * ldexpf(1.0f, -sh);
+      for (int u = 0; u < 4; ++u)
+        amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(w[u] << 16)), fabsf(__uint_as_float(w[u] & 0xffff0000u))));
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+      for (int o = 16; o >= 1; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, o));
+      const int ex = amax > 0.0f ? static_cast<int>((__float_as_uint(amax) >> 23) & 0xffu) - 127 : 0;
+      const int sh = max(-100, min(100, 14 - ex));
+      const float up = __uint_as_float(static_cast<uint32_t>(sh + 127) << 23);                       // 2^sh
+      if (lane == 0) fsc[r] = p.sm_scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - sh) << 23);
       uint32_t hv[4];
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
@@ -342,7 +385,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) shared_
                                              __fmul_rn(__uint_as_float(w[u] & 0xffff0000u), up));
         hv[u] = *reinterpret_cast<const uint32_t*>(&h2);
       }
-      sts128(sb + kQOff + part * 16384 + swz(row, i), hv[0], hv[1], hv[2], hv[3]);
+      // dims 8 lane .. +7: chunk lane / 8, unit lane % 8
+      sts128(sb + kQOff + (lane >> 3) * 16384 + swz(r, lane & 7), hv[0], hv[1], hv[2], hv[3]);
     }
   }
   asm volatile("fence.proxy.async;" ::: "memory");
@@ -677,29 +721,38 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) shared_
       for (int i = 0; ok && i < n_tiles; ++i) {
         const int buf = i & 1;
         const uint32_t parity = (i >> 1) & 1;
+        // Products are handed over a few at a time, the next ones when the last of the
+        // ones ahead are still running: an instruction that finds the queue full holds
+        // up the other warps of this scheduler (a row warp and a conversion warp).
         if (!ready(kBarVFull + buf, parity) || !ready(kBarPFull + buf, parity)) { ok = false; break; }
         tc_fence_after();
         const uint32_t more = i % kChain != 0 ? 1u : 0u;   // O of this chain so far is kept
         const uint32_t pa = tm + kSBuf * buf;
         const uint64_t v1 = dv0 + ((buf * kVBuf) >> 4);
+        auto pv = [&](int kk, uint32_t acc) {              // 16 cells = 8 TMEM columns of fp16 pairs, of half kk / 2
+          const uint64_t v = v1 + ((kk * 2048) >> 4);
+          const uint32_t p1 = pa + 32 * (kk >> 1) + 8 * (kk & 1);
+          mma_pair_ta(tm + kOCol, p1, v, idO, acc);
+          mma_pair_ta(tm + kOCol, p1, v + (kVPlane >> 4), idO, 1u);
+          mma_pair_ta(tm + kOCol, p1 + kP2Col, v, idO, 1u);
+        };
+        if (leader) pv(0, more);
+        if (i + 1 < n_tiles && !ready(kBarSFull + (buf ^ 1), ((i + 1) >> 1) & 1)) { ok = false; break; }   // QK(i + 1)
         if (leader) {
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk) {                 // 16 cells = 8 TMEM columns of fp16 pairs
-            const uint64_t v = v1 + ((kk * 2048) >> 4);
-            const uint32_t p1 = pa + 32 * (kk >> 1) + 8 * (kk & 1);   // of half kk / 2
-            mma_pair_ta(tm + kOCol, p1, v, idO, kk ? 1u : more);
-            mma_pair_ta(tm + kOCol, p1, v + (kVPlane >> 4), idO, 1u);
-            mma_pair_ta(tm + kOCol, p1 + kP2Col, v, idO, 1u);
-          }
+          pv(1, 1u);
+          pv(2, 1u);
+          commit_pair(bars + 8 * kBarMost);
+          pv(3, 1u);
           commit_pair(bars + 8 * (kBarODone + buf));
         }
         if (i + 2 < n_tiles) {
-          // QK(i + 2) overwrites P(i).  It is not queued behind PV(i): a product that
-          // finds the queue full holds up the other warps of this scheduler
-          if (!ready(kBarKFull + buf, parity ^ 1) || !ready(kBarODone + buf, parity)) { ok = false; break; }
+          // QK(i + 2) overwrites P(i) with its S0 half; the S1 half goes ahead
+          if (!ready(kBarKFull + buf, parity ^ 1) || !ready(kBarMost, i & 1)) { ok = false; break; }
+          tc_fence_after();
+          qk_half(buf, 1);
+          if (!ready(kBarODone + buf, parity)) { ok = false; break; }
           tc_fence_after();
           qk_half(buf, 0);
-          qk_half(buf, 1);
           if (leader) commit_pair(bars + 8 * (kBarSFull + buf));
         }
       }
@@ -709,52 +762,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) shared_
       (void)mbar_wait(bars + 8 * kBarDrain, 0, kWaitDefaultNs);
     } else if (__shfl_sync(kFull, warp, 0) == kLoadWarp) {
       // ============================================================== copies
-      // raw tiles by TMA, p.stages ahead of the conversion (per-thread copies cost
-      // the conversion warps 870 clocks a tile: each touches 32 rows).  Page ids of
-      // eight tiles, four groups each, are held one per lane.
       const bool leader = elect_one();
-      const int H = C.H;
-      int page_mine = -1, stage = 0;
-      uint32_t phase = 1;                                  // the first round finds every stage empty
-      int i = 0;
+      int stage = 0, i = min(p.stages, n_tiles);
+      uint32_t phase = 0;
       for (; i < n_tiles; ++i) {
-        if ((i & 7) == 0) {
-          const int c = (tile0 + i + (lane >> 2)) * kTileN + 16 * (lane & 3);
-          page_mine = INT32_MIN;                           // behind the prefix
-          if (i + (lane >> 2) < n_tiles && c < p.cells) {
-            const int64_t pidx = p.page_div.div(static_cast<uint32_t>(c));
-            const int page = pidx < p.max_pages ? p.pt[pidx] : -1;
-            page_mine = page >= 0 && page < C.n_pages ? page : -1;
-          }
-        }
         if (!__all_sync(kFull, mbar_wait(bars + 8 * (kBarRawEmpty + stage), phase, p.wait_ns))) { ctl[1] = 1; break; }
-        const uint32_t dst = sb + kRawOff + stage * p.stage_bytes, bar = bars + 8 * (kBarRawFull + stage);
-        const int my_group_page = __shfl_sync(kFull, page_mine, 4 * (i & 7) + (lane & 3));
-        const unsigned good = __ballot_sync(kFull, my_group_page >= 0) & 15u;
-        const unsigned bad = __ballot_sync(kFull, my_group_page == -1) & 15u;
-        const unsigned kgood = (good >> (2 * rank)) & 3u;
-        if (leader) {
-          if (bad) record_status(p.status, K8V4_ERANGE);
-          ctl[8 + stage] = static_cast<int>(good | (bad << 4));
-          mbar_expect_tx(bar, __popc(good) * (2048u + 384u * H) + __popc(kgood) * 4096u);
-        }
-#pragma unroll 1
-        for (int q = 0; q < 4; ++q) {
-          const int page = __shfl_sync(kFull, my_group_page, q);
-          if (!leader || page < 0) continue;
-          const int cell = (tile0 + i) * kTileN + 16 * q;
-          const int slot = cell - static_cast<int>(p.page_div.div(static_cast<uint32_t>(cell))) * C.P;
-          const int kq = q - 2 * static_cast<int>(rank);
-          if (kq == 0 || kq == 1) {
-            tma_load_4d(dst + kq * 4096, &tm_k, 0, g, slot, page, bar);
-            tma_load_4d(dst + kq * 4096 + 2048, &tm_k, 128, g, slot, page, bar);
-          }
-          tma_load_4d(dst + kRawV + q * 2048, &tm_v, 0, g, slot, page, bar);
-          const uint8_t* pg = C.pages + static_cast<int64_t>(page) * C.page_bytes;
-          bulk_load(dst + kRawKs + q * 128 * H, pg + C.ks_off() + static_cast<int64_t>(slot) * 8 * H, 128 * H, bar);
-          bulk_load(dst + kRawKs + 512 * H + q * 256 * H, pg + C.vs_off() + static_cast<int64_t>(slot) * 16 * H, 256 * H, bar);
-        }
-        __syncwarp();
+        load_tile(i, stage, leader);
         if (++stage == p.stages) {
           stage = 0;
           phase ^= 1;
@@ -770,6 +783,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) shared_
   __syncthreads();
   if (tid == 0 && ctl[1]) record_status(p.status, K8V4_ECUDA);
   cluster_barrier();          // no product, commit or arrival of the pair is in flight
+  // launched behind the splits of the sequences' own cells, this kernel starts as
+  // their CTAs leave (all of them have then seen the kernels before them complete);
+  // the combine waits for this one alone, so this one ends after them
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   if (warp == kIssueWarp) {
     tc_fence_after();
     tmem_dealloc_pair(tmem, kTmemCols);
@@ -834,12 +851,14 @@ SharedPlan plan_shared(const CacheView& C, int n_seqs, int shared_len, int max_s
   const PairSetup setup = pair_setup();
   const int slots = setup.ok ? setup.slots : std::max(1, num_sms / 2);
   // one pair per two SMs at a time: the split count that minimises waves x (tiles
-  // a pair sweeps + the fixed cost of a pair, worth about kFixedTiles tiles)
-  constexpr int kFixedTiles = 10;
-  int64_t best = INT64_MAX;
+  // a pair sweeps + the fixed cost of a pair, worth about kFixedTiles tiles) + the
+  // partial rows of a split, written and read again (4,096 rows take a tile's time)
+  constexpr int kFixedTiles = 9;
+  const double rows = static_cast<double>(n_seqs) * C.H * kGqa;
+  double best = 1e300;
   for (int sp = 1; sp <= std::min(tiles, 256); ++sp) {
-    const int tps = (tiles + sp - 1) / sp;
-    const int64_t cost = (units * ((tiles + tps - 1) / tps) + slots - 1) / slots * (tps + kFixedTiles);
+    const int tps = (tiles + sp - 1) / sp, real = (tiles + tps - 1) / tps;
+    const double cost = static_cast<double>((units * real + slots - 1) / slots) * (tps + kFixedTiles) + real * rows / 4096.0;
     if (cost < best) {
       best = cost;
       pl.tiles_per_split = tps;
@@ -851,7 +870,7 @@ SharedPlan plan_shared(const CacheView& C, int n_seqs, int shared_len, int max_s
 
 int launch_shared_prefix(const Launch& L, const CacheView& C, const SharedPlan& plan, const void* q, const int32_t* pt,
                          int64_t max_pages, const int32_t* lens, int n_seqs, int max_seq_len, float sm_scale, float* ws,
-                         int ws_splits) {
+                         int ws_splits, bool behind_splits) {
   SharedParams p;
   p.C = C;
   p.q = static_cast<const uint16_t*>(q);
@@ -876,7 +895,17 @@ int launch_shared_prefix(const Launch& L, const CacheView& C, const SharedPlan& 
   if (!tensor_maps_of(C, &mk, &mv)) return K8V4_ECUDA;
   const int groups = (n_seqs + kPairSeqs - 1) / kPairSeqs;
   const dim3 grid(2u * static_cast<unsigned>(groups) * static_cast<unsigned>(plan.splits), C.H);
-  shared_prefix_kernel<<<grid, kThreads, kRawOff + p.stages * p.stage_bytes, L.stream>>>(mk, mv, p);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kRawOff + p.stages * p.stage_bytes;
+  cfg.stream = L.stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = behind_splits ? 1 : 0;
+  if (cudaLaunchKernelEx(&cfg, shared_prefix_kernel, mk, mv, p) != cudaSuccess) return K8V4_ECUDA;
   return cudaGetLastError() == cudaSuccess ? K8V4_OK : K8V4_ECUDA;
 }
 
