@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -56,7 +57,7 @@ def lib():
             raise RuntimeError(f"libk8v4.so is not built ({LIB_PATH}); call quantized_paged_kv_q8_gb300.build()")
         L = ctypes.CDLL(LIB_PATH)
         P, I32, I64, F, SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float, ctypes.c_size_t
-        C, R = ctypes.POINTER(k8v4_cache), ctypes.POINTER(k8v4_rope)
+        C = ctypes.POINTER(k8v4_cache)
         sigs = {
             "k8v4_bytes_per_cell": ([I32, I32], SZ),
             "k8v4_status_string": ([ctypes.c_int], ctypes.c_char_p),
@@ -79,8 +80,8 @@ def lib():
             "attn_k8v4_combine_partials": ([P, I32, I32, I32, P, P], ctypes.c_int),
             "attn_k8v4_shared_workspace_bytes": ([C, I32, I32, I32], SZ),
             "attn_k8v4_decode_shared": ([C, P, I32, P, I64, P, I32, I32, I32, F, P, P, SZ, P], ctypes.c_int),
-            "qk_norm_rope_k8v4": ([P, I64, I32, P, I64, I32, I32, P, P, F, P, I32, I32, R, P, P, P], ctypes.c_int),
-            "kv_append_k8v4_rope": ([C, P, I64, I32, P, I32, P, I64, P, I64, I32, P, F, R, P], ctypes.c_int),
+            "qk_norm_rope_k8v4": ([P, I64, I32, P, I64, I32, I32, P, P, F, P, I32, I32, P, P, P, P], ctypes.c_int),
+            "kv_append_k8v4_rope": ([C, P, I64, I32, P, I32, P, I64, P, I64, I32, P, F, P, P], ctypes.c_int),
             "spec_accept_k8v4": ([P, P, I32, P, P, P, P, I32, I32, I32, P, P, P], ctypes.c_int),
             "k8v4_set_wait_limit_ns": ([ctypes.c_uint32], None),
             "k8v4_set_withheld_copy": ([ctypes.c_int32], None),
@@ -118,13 +119,13 @@ def _check(rc: int, what: str) -> None:
 
 
 def _ptr(t: torch.Tensor | None):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
-def _stream(stream) -> ctypes.c_void_p:
+def _stream(stream) -> int:
     if stream is None:
         stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def _dtype(t: torch.Tensor) -> int:
@@ -181,37 +182,70 @@ def kv_append_k8v4(cache: PagedCache, page_table: torch.Tensor, pos: torch.Tenso
 
 
 # ---------------------------------------------------------------- around the attention
-def _need(ok: bool, what: str) -> None:
-    if not ok:
-        raise ValueError(what)
+# A decode step makes these calls once per layer with kernels of a few
+# microseconds, so what the binding itself does counts: each property of a tensor
+# is asked for once, and no Python object is made for a pointer or a stream.
+_pack_rope = struct.Struct("@Pqii").pack          # k8v4_rope
+_F32, _BF16, _I32, _I64, _U8 = torch.float32, torch.bfloat16, torch.int32, torch.int64, torch.uint8
+
+
+def _bad(what: str) -> None:
+    raise ValueError(what)
 
 
 def _token_stride(x: torch.Tensor, heads: int, what: str) -> int:
     """Elements between the tokens of x [n_seqs, n_tok, heads, 256]; heads are
     contiguous, tokens evenly spaced over the sequences (a slice of a packed
     projection qualifies)."""
-    _need(x.dim() == 4 and x.shape[2] == heads and x.shape[3] == HEAD_DIM, f"{what}: [n_seqs, n_tok, heads, 256] expected")
-    n_seqs, n_tok = x.shape[0], x.shape[1]
-    _need(heads == 0 or (x.stride(3) == 1 and (heads == 1 or x.stride(2) == HEAD_DIM)), f"{what}: heads must be contiguous")
-    step = x.stride(1) if n_tok > 1 else x.stride(0) if n_seqs > 1 else heads * HEAD_DIM
-    _need(n_seqs <= 1 or n_tok == 0 or x.stride(0) == n_tok * step, f"{what}: tokens must be evenly spaced")
-    return step
+    n_seqs, n_tok, h, d = x.shape if x.dim() == 4 else _bad(f"{what}: [n_seqs, n_tok, heads, 256] expected")
+    s0, s1, s2, s3 = x.stride()
+    if h != heads or d != HEAD_DIM:
+        _bad(f"{what}: [n_seqs, n_tok, {heads}, 256] expected")
+    if heads and (s3 != 1 or (heads != 1 and s2 != HEAD_DIM)):
+        _bad(f"{what}: heads must be contiguous")
+    if n_tok <= 1:
+        return s0 if n_seqs > 1 else heads * HEAD_DIM
+    if n_seqs > 1 and s0 != n_tok * s1:
+        _bad(f"{what}: tokens must be evenly spaced")
+    return s1
 
 
-def _rope(table: torch.Tensor, interleaved: bool) -> k8v4_rope:
-    _need(table.dtype == torch.float32 and table.dim() == 2 and table.is_contiguous(),
-          "rope_table: contiguous float32 [n_pos, rot_dim] expected")
-    return k8v4_rope(_ptr(table), table.shape[0], table.shape[1], 1 if interleaved else 0)
+def _rope(table: torch.Tensor, interleaved: bool) -> bytes:
+    """The k8v4_rope descriptor of a table, as the bytes of the C struct."""
+    if table.dtype is not _F32 or table.dim() != 2 or not table.is_contiguous():
+        _bad("rope_table: contiguous float32 [n_pos, rot_dim] expected")
+    n_pos, rot = table.shape
+    return _pack_rope(table.data_ptr(), n_pos, rot, 1 if interleaved else 0)
 
 
-def _weight(w: torch.Tensor | None, what: str):
-    _need(w is None or (w.dtype == torch.float32 and w.shape == (HEAD_DIM,) and w.is_contiguous()),
-          f"{what}: contiguous float32 [256] expected")
-    return _ptr(w)
+def _weight(w: torch.Tensor | None, dev: int, what: str):
+    if w is None:
+        return None
+    if w.dtype is not _F32 or w.shape != (HEAD_DIM,) or not w.is_contiguous() or w.get_device() != dev:
+        _bad(f"{what}: contiguous float32 [256] on the tensors' device expected")
+    return w.data_ptr()
 
 
-def _same_device(*tensors) -> None:
-    _need(len({t.device for t in tensors if t is not None}) == 1, "tensors on different devices")
+def _vector(x: torch.Tensor, n: int, dtype: torch.dtype, dev: int, what: str) -> int:
+    """The address of a contiguous vector (or array) of n elements."""
+    if x.dtype is not dtype or x.numel() != n or not x.is_contiguous() or x.get_device() != dev:
+        _bad(f"{what}: {n} contiguous {dtype} on the tensors' device expected")
+    return x.data_ptr()
+
+
+def _on(dev: int, stream, name: str, *args) -> None:
+    """Call a library function with the tensors' device current, on `stream` or that
+    device's current stream; raises what it returns."""
+    fn = getattr(_lib or lib(), name)
+    if dev < 0:
+        rc = fn(*args, _stream(stream) if stream is not None else None)
+    elif torch._C._cuda_getDevice() == dev:
+        rc = fn(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream))
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream))
+    if rc:
+        raise K8V4Error(rc, name)
 
 
 def qk_norm_rope_k8v4(q: torch.Tensor, k: torch.Tensor | None, pos: torch.Tensor, rope_table: torch.Tensor,
@@ -221,22 +255,27 @@ def qk_norm_rope_k8v4(q: torch.Tensor, k: torch.Tensor | None, pos: torch.Tensor
     """Per-head RMS norm (with a weight) and position rotation of q [n_seqs, n_tok, HQ, 256]
     and k [n_seqs, n_tok, H, 256] (or None) into contiguous q_out, k_out.  pos int64 [n_seqs];
     rope_table float32 [n_pos, rot_dim]: cosines, then sines, of each position."""
-    n_seqs, n_tok, n_q = q.shape[0], q.shape[1], q.shape[2]
-    n_k = 0 if k is None else k.shape[2]
+    n_seqs, n_tok, n_q, _ = shape = q.shape if q.dim() == 4 else _bad("q: [n_seqs, n_tok, heads, 256] expected")
+    dev, dtype = q.get_device(), q.dtype
     q_stride = _token_stride(q, n_q, "q")
-    k_stride = 0 if k is None else _token_stride(k, n_k, "k")
-    _need(q_out.shape == q.shape and q_out.dtype == q.dtype and q_out.is_contiguous(), "q_out: contiguous, like q")
+    if q_out.shape != shape or q_out.dtype is not dtype or not q_out.is_contiguous() or q_out.get_device() != dev:
+        _bad("q_out: contiguous, like q")
+    n_k, k_stride, kp, kop = 0, 0, None, None
     if k is not None:
-        _need(k.dtype == q.dtype and k.shape[:2] == q.shape[:2], "k: same dtype and tokens as q")
-        _need(k_out is not None and k_out.shape == k.shape and k_out.dtype == k.dtype and k_out.is_contiguous(),
-              "k_out: contiguous, like k")
-    _need(pos.dtype == torch.int64 and pos.numel() == n_seqs and pos.is_contiguous(), "pos: int64 [n_seqs]")
-    _same_device(q, k, pos, rope_table, q_out, None if k is None else k_out, q_weight, k_weight)
-    r = _rope(rope_table, interleaved)
-    rc = lib().qk_norm_rope_k8v4(_ptr(q), q_stride, n_q, _ptr(k), k_stride, n_k, _dtype(q), _weight(q_weight, "q_weight"),
-                                 _weight(k_weight, "k_weight"), eps, _ptr(pos), n_seqs, n_tok, ctypes.byref(r),
-                                 _ptr(q_out), None if k is None else _ptr(k_out), _stream(stream))
-    _check(rc, "qk_norm_rope_k8v4")
+        kshape = k.shape if k.dim() == 4 else _bad("k: [n_seqs, n_tok, heads, 256] expected")
+        n_k = kshape[2]
+        k_stride = _token_stride(k, n_k, "k")
+        if kshape[0] != n_seqs or kshape[1] != n_tok or k.dtype is not dtype or k.get_device() != dev:
+            _bad("k: same dtype, device and tokens as q")
+        if (k_out is None or k_out.shape != kshape or k_out.dtype is not dtype or not k_out.is_contiguous()
+                or k_out.get_device() != dev):
+            _bad("k_out: contiguous, like k")
+        kp, kop = k.data_ptr(), k_out.data_ptr()
+    if rope_table.get_device() != dev:
+        _bad("rope_table: on another device")
+    _on(dev, stream, "qk_norm_rope_k8v4", q.data_ptr(), q_stride, n_q, kp, k_stride, n_k, _dtype(q),
+        _weight(q_weight, dev, "q_weight"), _weight(k_weight, dev, "k_weight"), eps,
+        _vector(pos, n_seqs, _I64, dev, "pos"), n_seqs, n_tok, _rope(rope_table, interleaved), q_out.data_ptr(), kop)
 
 
 def attn_k8v4_shared_workspace_bytes(cache: PagedCache, n_seqs: int, shared_len: int, max_seq_len: int) -> int:
@@ -254,18 +293,16 @@ def attn_k8v4_decode_shared(cache: PagedCache, q: torch.Tensor, page_table: torc
     """attn_k8v4_decode for a batch whose first shared_len cells are the same in every
     sequence, read once for all of them.  q: bf16 [n_seqs, 8H, 256]; page_table int32
     [n_seqs, max_pages]; seq_lens int32 [n_seqs]; out float32 like q."""
-    n_seqs = q.shape[0]
-    _need(tuple(q.shape[1:]) == (GQA * cache.n_kv_heads, HEAD_DIM) and q.is_contiguous(), "q: contiguous [n_seqs, 8H, 256]")
-    _need(page_table.dtype == torch.int32 and page_table.dim() == 2 and page_table.shape[0] == n_seqs
-          and page_table.is_contiguous(), "page_table: contiguous int32 [n_seqs, max_pages]")
-    _need(seq_lens.dtype == torch.int32 and seq_lens.numel() == n_seqs and seq_lens.is_contiguous(), "seq_lens: int32 [n_seqs]")
-    _need(out.shape == q.shape and out.dtype == torch.float32 and out.is_contiguous(), "out: contiguous float32, like q")
-    _need(ws.dtype == torch.uint8 and ws.is_contiguous(), "ws: uint8")
-    _same_device(cache.pages, q, page_table, seq_lens, out, ws)
-    rc = lib().attn_k8v4_decode_shared(cache.ref(), _ptr(q), _dtype(q), _ptr(page_table), page_table.shape[1],
-                                       _ptr(seq_lens), n_seqs, max_seq_len, shared_len, sm_scale, _ptr(out), _ptr(ws),
-                                       ws.numel(), _stream(stream))
-    _check(rc, "attn_k8v4_decode_shared")
+    shape, dev = q.shape, q.get_device()
+    n_seqs = shape[0] if len(shape) == 3 else _bad("q: [n_seqs, 8H, 256] expected")
+    rows = GQA * cache.n_kv_heads
+    if shape[1] != rows or shape[2] != HEAD_DIM or not q.is_contiguous() or cache.pages.get_device() != dev:
+        _bad("q: contiguous [n_seqs, 8H, 256] on the cache's device")
+    pages = page_table.shape[1] if page_table.dim() == 2 else _bad("page_table: [n_seqs, max_pages] expected")
+    _on(dev, stream, "attn_k8v4_decode_shared", cache.ref(), q.data_ptr(), _dtype(q),
+        _vector(page_table, n_seqs * pages, _I32, dev, "page_table"), pages,
+        _vector(seq_lens, n_seqs, _I32, dev, "seq_lens"), n_seqs, max_seq_len, shared_len, sm_scale,
+        _vector(out, n_seqs * rows * HEAD_DIM, _F32, dev, "out"), _vector(ws, ws.numel(), _U8, dev, "ws"), ws.numel())
     return out
 
 
@@ -274,17 +311,17 @@ def kv_append_k8v4_rope(cache: PagedCache, page_table: torch.Tensor, pos: torch.
                         eps: float = 1e-6, interleaved: bool = False, stream=None) -> None:
     """kv_append_k8v4 with k normed (with a weight) and rotated to its cell's position on the
     way.  k, v: [n_seqs, n_tok, H, 256], possibly slices of a packed projection."""
-    n_seqs, n_tok, h = k.shape[0], k.shape[1], cache.n_kv_heads
-    _need(k.shape == v.shape and k.dtype == v.dtype, "k and v: same shape and dtype")
-    _need(page_table.dtype == torch.int32 and page_table.dim() == 2 and page_table.shape[0] == n_seqs
-          and page_table.is_contiguous(), "page_table: contiguous int32 [n_seqs, max_pages]")
-    _need(pos.dtype == torch.int64 and pos.numel() == n_seqs and pos.is_contiguous(), "pos: int64 [n_seqs]")
-    _same_device(cache.pages, page_table, pos, k, v, rope_table, k_weight)
-    r = _rope(rope_table, interleaved)
-    rc = lib().kv_append_k8v4_rope(cache.ref(), _ptr(page_table), page_table.shape[-1], n_seqs, _ptr(pos), n_tok,
-                                   _ptr(k), _token_stride(k, h, "k"), _ptr(v), _token_stride(v, h, "v"), _dtype(k),
-                                   _weight(k_weight, "k_weight"), eps, ctypes.byref(r), _stream(stream))
-    _check(rc, "kv_append_k8v4_rope")
+    n_seqs, n_tok = (shape := k.shape)[:2]
+    dev, h = k.get_device(), cache.n_kv_heads
+    if v.shape != shape or v.dtype is not k.dtype or v.get_device() != dev or cache.pages.get_device() != dev:
+        _bad("k and v: same shape, dtype and device, the cache's")
+    pages = page_table.shape[1] if page_table.dim() == 2 else _bad("page_table: [n_seqs, max_pages] expected")
+    if rope_table.get_device() != dev:
+        _bad("rope_table: on another device")
+    _on(dev, stream, "kv_append_k8v4_rope", cache.ref(), _vector(page_table, n_seqs * pages, _I32, dev, "page_table"),
+        pages, n_seqs, _vector(pos, n_seqs, _I64, dev, "pos"), n_tok, k.data_ptr(), _token_stride(k, h, "k"),
+        v.data_ptr(), _token_stride(v, h, "v"), _dtype(k), _weight(k_weight, dev, "k_weight"), eps,
+        _rope(rope_table, interleaved))
 
 
 def spec_accept_k8v4(target_probs: torch.Tensor, draft_probs: torch.Tensor | None, draft_tokens: torch.Tensor,
@@ -294,20 +331,20 @@ def spec_accept_k8v4(target_probs: torch.Tensor, draft_probs: torch.Tensor | Non
     [n_seqs, n, vocab] or None (certain drafts), draft_tokens int32 [n_seqs, n], u_accept
     float32 [n_seqs, n], u_sample float32 [n_seqs] -> tokens int32 [n_seqs, n + 1] (accepted
     drafts, the drawn token, then -1), n_accepted int32 [n_seqs]."""
-    _need(target_probs.dim() == 3 and target_probs.is_contiguous(), "target_probs: contiguous [n_seqs, n + 1, vocab]")
-    b, n, vocab = target_probs.shape[0], target_probs.shape[1] - 1, target_probs.shape[2]
-    _need(draft_probs is None or (draft_probs.shape == (b, n, vocab) and draft_probs.dtype == target_probs.dtype
-                                  and draft_probs.is_contiguous()), "draft_probs: contiguous [n_seqs, n, vocab], like target_probs")
-    for t, shape, dtype, what in ((draft_tokens, (b, n), torch.int32, "draft_tokens"), (u_accept, (b, n), torch.float32, "u_accept"),
-                                  (u_sample, (b,), torch.float32, "u_sample"), (tokens, (b, n + 1), torch.int32, "tokens"),
-                                  (n_accepted, (b,), torch.int32, "n_accepted"), (n_drafts, (b,), torch.int32, "n_drafts")):
-        _need(t is None and what == "n_drafts" or (tuple(t.shape) == shape and t.dtype == dtype and t.is_contiguous()),
-              f"{what}: contiguous {dtype} {shape} expected")
-    _same_device(target_probs, draft_probs, draft_tokens, u_accept, u_sample, tokens, n_accepted, n_drafts)
-    rc = lib().spec_accept_k8v4(_ptr(target_probs), _ptr(draft_probs), _dtype(target_probs), _ptr(draft_tokens),
-                                _ptr(n_drafts), _ptr(u_accept), _ptr(u_sample), b, n, vocab, _ptr(tokens),
-                                _ptr(n_accepted), _stream(stream))
-    _check(rc, "spec_accept_k8v4")
+    b, n1, vocab = target_probs.shape if target_probs.dim() == 3 else _bad("target_probs: [n_seqs, n + 1, vocab] expected")
+    n, dev = n1 - 1, target_probs.get_device()
+    if not target_probs.is_contiguous():
+        _bad("target_probs: contiguous [n_seqs, n + 1, vocab] expected")
+    if draft_probs is not None and draft_probs.shape != (b, n, vocab):
+        _bad("draft_probs: [n_seqs, n, vocab] expected")
+    if draft_tokens.shape != (b, n) or tokens.shape != (b, n1):
+        _bad("draft_tokens: [n_seqs, n], tokens: [n_seqs, n + 1] expected")
+    _on(dev, stream, "spec_accept_k8v4", target_probs.data_ptr(),
+        None if draft_probs is None else _vector(draft_probs, b * n * vocab, target_probs.dtype, dev, "draft_probs"),
+        _dtype(target_probs), _vector(draft_tokens, b * n, _I32, dev, "draft_tokens"),
+        None if n_drafts is None else _vector(n_drafts, b, _I32, dev, "n_drafts"),
+        _vector(u_accept, b * n, _F32, dev, "u_accept"), _vector(u_sample, b, _F32, dev, "u_sample"), b, n, vocab,
+        _vector(tokens, b * n1, _I32, dev, "tokens"), _vector(n_accepted, b, _I32, dev, "n_accepted"))
 
 
 def attn_k8v4_workspace_bytes(cache: PagedCache, n_seqs: int, n_q: int, max_seq_len: int) -> int:

@@ -100,9 +100,8 @@ def test_norm_rope_refuses_overlapping_in_place():
     pos = torch.zeros(1, dtype=torch.int64, device="cuda")
     table = torch.from_numpy(table_of(64, 128)).cuda()
     r = k8._rope(table, False)
-    import ctypes
     rc = k8.lib().qk_norm_rope_k8v4(k8._ptr(parts[0]), 18 * 256, 16, None, 0, 0, k8.BF16, None, None, 0.0, k8._ptr(pos),
-                                    1, 3, ctypes.byref(r), k8._ptr(parts[0]), None, k8._stream(None))
+                                    1, 3, r, k8._ptr(parts[0]), None, k8._stream(None))
     assert rc == k8.EINVAL
 
 
