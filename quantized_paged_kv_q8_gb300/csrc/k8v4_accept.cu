@@ -19,6 +19,7 @@
 // sequence alone keeps eight SMs loading; CTA totals meet in distributed shared
 // memory, and only the CTA that holds the token reads its part (from L2) again.
 #include <algorithm>
+#include <type_traits>
 
 #include "k8v4_common.cuh"
 
@@ -90,7 +91,7 @@ __device__ __forceinline__ void store_remote(Pair* local, int rank, const Pair& 
 }
 
 template <bool BF16>
-__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kAccThreads) accept_kernel(const AcceptParams a) {
+__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kAccThreads, 4) accept_kernel(const AcceptParams a) {
   __shared__ __align__(8) Pair cta_total[2][kCluster];   // every CTA's sums (w, then p alone), written by each to all
   __shared__ Pair warp_total[kAccWarps], s_ahead;
   __shared__ int s_acc, s_hit, s_last;
@@ -139,16 +140,17 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kAccThreads) 
   const bool rejected = acc < n;
   const int64_t q_row = (b * n_max + acc) * V;
   const bool has_q = rejected && a.q != nullptr;
-  // the token's weight: max(p - q, 0), or p with the certain draft left out, or p.
-  // fmaxf also turns a NaN into 0
-  auto weight = [&](int64_t j, bool residual) -> float {
-    float w = prob<BF16>(a.p, p_row + j);
-    if (residual) {
-      if (has_q) w = __fsub_rn(w, prob<BF16>(a.q, q_row + j));
-      else if (j == refused) w = 0.0f;
-    }
-    return fmaxf(w, 0.0f);
+  // the token's weight: max(p - q, 0), or p with the certain draft left out (with
+  // `refused` outside the row: p).  fmaxf also turns a NaN into 0.  Two loops below
+  // rather than a test per entry: with the test every entry's loads would wait for the
+  // one before
+  auto weight = [&](int64_t j, auto with_q, int left_out) -> float {
+    const float w = prob<BF16>(a.p, p_row + j);
+    if constexpr (decltype(with_q)::value) return fmaxf(__fsub_rn(w, prob<BF16>(a.q, q_row + j)), 0.0f);
+    else return j == left_out ? 0.0f : fmaxf(w, 0.0f);
   };
+  const std::true_type kWithQ{};
+  const std::false_type kAlone{};
   // ---- sums: CTA `rank` owns kAccWarps runs of the vocabulary, a warp each
   const int per_warp = (V + kCluster * kAccWarps - 1) / (kCluster * kAccWarps);
   auto run_begin = [&](int w) {
@@ -160,15 +162,19 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kAccThreads) 
   cluster_wait();
   for (int pass = 0; pass < 2; ++pass) {
     Pair s{0.0f, 0.0f};
-    int j = w0 + lane;
-    for (; j + 32 * (kUnroll - 1) < w1; j += 32 * kUnroll) {
-      float x[kUnroll];
+    auto sum_run = [&](auto with_q, int left_out) {
+      int j = w0 + lane;
+      for (; j + 32 * (kUnroll - 1) < w1; j += 32 * kUnroll) {
+        float x[kUnroll];
 #pragma unroll
-      for (int i = 0; i < kUnroll; ++i) x[i] = weight(j + 32 * i, residual);
+        for (int i = 0; i < kUnroll; ++i) x[i] = weight(j + 32 * i, with_q, left_out);
 #pragma unroll
-      for (int i = 0; i < kUnroll; ++i) add(s, x[i]);
-    }
-    for (; j < w1; j += 32) add(s, weight(j, residual));
+        for (int i = 0; i < kUnroll; ++i) add(s, x[i]);
+      }
+      for (; j < w1; j += 32) add(s, weight(j, with_q, left_out));
+    };
+    if (residual && has_q) sum_run(kWithQ, -1);
+    else sum_run(kAlone, residual ? refused : -1);
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) add(s, shfl_xor(s, o));
     if (lane == 0) warp_total[warp] = s;
@@ -236,7 +242,10 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kAccThreads) 
     float x[kPerThread];
     Pair s{0.0f, 0.0f};
 #pragma unroll
-    for (int i = 0; i < kPerThread; ++i) x[i] = j + i < r1 ? weight(j + i, residual) : 0.0f;
+    for (int i = 0; i < kPerThread; ++i) {
+      if (residual && has_q) x[i] = j + i < r1 ? weight(j + i, kWithQ, -1) : 0.0f;
+      else x[i] = j + i < r1 ? weight(j + i, kAlone, residual ? refused : -1) : 0.0f;
+    }
 #pragma unroll
     for (int i = 0; i < kPerThread; ++i) add(s, x[i]);
     const Pair incl = scan_warp(s, lane);

@@ -193,19 +193,50 @@ __device__ __forceinline__ void read_q4_row(const uint8_t* nib, const uint8_t* s
   }
 }
 
+// The values of one row as a lane writes them when nothing is rotated: elements
+// 4 lane + e (x[0..3]) and 128 + 4 lane + e (x[4..7]), so that a store of 16 B a lane
+// covers 512 contiguous bytes (elements 8 lane + r would cover every other 16 B)
+__device__ __forceinline__ void read_q4_row_wide(const uint8_t* nib, const uint8_t* scales, int lane, float x[8]) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int e = 128 * h + 4 * lane, blk = e >> 5;
+    const float d = __half2float(*reinterpret_cast<const __half*>(scales + 2 * blk));
+    const uint32_t w = *reinterpret_cast<const uint32_t*>(nib + 16 * blk + (e & 15)) >> ((e & 16) ? 4 : 0);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) x[4 * h + q] = __fmul_rn(static_cast<float>(static_cast<int>((w >> (8 * q)) & 0xfu) - 8), d);
+  }
+}
+__device__ __forceinline__ void read_int8_row_wide(const uint8_t* codes, const uint8_t* scales, int lane, float x[8]) {
+  const float2 s = *reinterpret_cast<const float2*>(scales);
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const uint32_t w = *reinterpret_cast<const uint32_t*>(codes + 128 * h + 4 * lane);
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      x[4 * h + q] = __fmul_rn(static_cast<float>(static_cast<int8_t>((w >> (8 * q)) & 0xffu)), h ? s.y : s.x);
+  }
+}
+__device__ __forceinline__ void write_row_wide(float* row, int lane, const float x[8]) {
+  __stcs(reinterpret_cast<float4*>(row) + lane, make_float4(x[0], x[1], x[2], x[3]));
+  __stcs(reinterpret_cast<float4*>(row) + 32 + lane, make_float4(x[4], x[5], x[6], x[7]));
+}
+
 template <int FMT>
 __global__ void __launch_bounds__(kWarps * 32) dequant_kernel(CacheView C, const int32_t* __restrict__ pt,
                                                               int64_t max_pages, int64_t start, int64_t n_cells,
                                                               float* __restrict__ k_out, float* __restrict__ v_rot_out,
-                                                              float* __restrict__ v_out, int* status) {
+                                                              float* __restrict__ v_out, FastDiv div_h, FastDiv div_p,
+                                                              int* status) {
   __shared__ long long stage[kWarps][kRotScratch];
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int64_t item = static_cast<int64_t>(blockIdx.x) * kWarps + w;   // (cell, head)
   if (item >= n_cells * C.H) return;
-  const int g = static_cast<int>(item % C.H);
-  const int64_t cell = start + item / C.H;
-  const int64_t pidx = cell / C.P;
-  const int64_t page = (cell >= 0 && pidx < max_pages) ? pt[pidx] : -1;
+  // cells are below 2^31 (the host checks the table); so are the items of most calls
+  const int64_t nth = item < (int64_t(1) << 31) ? static_cast<int64_t>(div_h.div(static_cast<uint32_t>(item))) : item / C.H;
+  const int g = static_cast<int>(item - nth * C.H);
+  const int64_t cell = start + nth;
+  const int64_t pidx = div_p.div(static_cast<uint32_t>(cell));
+  const int64_t page = pidx < max_pages ? pt[pidx] : -1;
   float* ko = k_out + item * kD + 8 * lane;
   float* vr = v_rot_out + item * kD + 8 * lane;
   float* vo = v_out ? v_out + item * kD + 8 * lane : nullptr;
@@ -213,9 +244,17 @@ __global__ void __launch_bounds__(kWarps * 32) dequant_kernel(CacheView C, const
     if (lane == 0) record_status(status, K8V4_ERANGE);
     return;
   }
-  const int64_t r = (cell % C.P) * C.H + g;
+  const int64_t r = (cell - pidx * C.P) * C.H + g;
   const uint8_t* base = C.pages + page * C.page_bytes;
   float x[8];
+  if (FMT != K8V4_FORMAT_Q4 && vo == nullptr) {
+    read_int8_row_wide(base + r * 256, base + C.ks_off() + r * 8, lane, x);
+    write_row_wide(k_out + item * kD, lane, x);
+    if (FMT == K8V4_FORMAT_INT8) read_int8_row_wide(base + C.v_off() + r * 256, base + C.vs_off() + r * 8, lane, x);
+    else read_q4_row_wide(base + C.v_off() + r * 128, base + C.vs_off() + r * 16, lane, x);
+    write_row_wide(v_rot_out + item * kD, lane, x);
+    return;
+  }
   if (FMT == K8V4_FORMAT_Q4) {
     // rotated-space K, then the exact inverse rotation (H/16 is its own inverse)
     read_q4_row(base + r * 128, base + C.ks_off() + r * 16, lane, x);
@@ -231,8 +270,8 @@ __global__ void __launch_bounds__(kWarps * 32) dequant_kernel(CacheView C, const
       x[q] = __fmul_rn(static_cast<float>(c), s);
     }
   }
-  reinterpret_cast<float4*>(ko)[0] = make_float4(x[0], x[1], x[2], x[3]);
-  reinterpret_cast<float4*>(ko)[1] = make_float4(x[4], x[5], x[6], x[7]);
+  __stcs(reinterpret_cast<float4*>(ko) + 0, make_float4(x[0], x[1], x[2], x[3]));
+  __stcs(reinterpret_cast<float4*>(ko) + 1, make_float4(x[4], x[5], x[6], x[7]));
   if (FMT != K8V4_FORMAT_INT8) {
     read_q4_row(base + C.v_off() + r * 128, base + C.vs_off() + r * 16, lane, x);
   } else {
@@ -246,12 +285,12 @@ __global__ void __launch_bounds__(kWarps * 32) dequant_kernel(CacheView C, const
       x[q] = __fmul_rn(static_cast<float>(c), sv);
     }
   }
-  reinterpret_cast<float4*>(vr)[0] = make_float4(x[0], x[1], x[2], x[3]);
-  reinterpret_cast<float4*>(vr)[1] = make_float4(x[4], x[5], x[6], x[7]);
+  __stcs(reinterpret_cast<float4*>(vr) + 0, make_float4(x[0], x[1], x[2], x[3]));
+  __stcs(reinterpret_cast<float4*>(vr) + 1, make_float4(x[4], x[5], x[6], x[7]));
   if (vo) {
     if (FMT != K8V4_FORMAT_INT8) rotate_exact(x, lane, stage[w]);
-    reinterpret_cast<float4*>(vo)[0] = make_float4(x[0], x[1], x[2], x[3]);
-    reinterpret_cast<float4*>(vo)[1] = make_float4(x[4], x[5], x[6], x[7]);
+    __stcs(reinterpret_cast<float4*>(vo) + 0, make_float4(x[0], x[1], x[2], x[3]));
+    __stcs(reinterpret_cast<float4*>(vo) + 1, make_float4(x[4], x[5], x[6], x[7]));
   }
 }
 
@@ -311,12 +350,13 @@ int launch_dequant(const Launch& L, const CacheView& C, const int32_t* pt, int64
   const int64_t blocks = (items + kWarps - 1) / kWarps;
   if (blocks > 0x7fffffffll) return K8V4_EINVAL;
   const dim3 grid(static_cast<unsigned>(blocks)), block(kWarps * 32);
+  const FastDiv dh(static_cast<uint32_t>(C.H)), dp(static_cast<uint32_t>(C.P));
   if (C.fmt == K8V4_FORMAT_K8V4)
-    dequant_kernel<K8V4_FORMAT_K8V4><<<grid, block, 0, L.stream>>>(C, pt, max_pages, start, n_cells, k_out, v_rot_out, v_out, L.status);
+    dequant_kernel<K8V4_FORMAT_K8V4><<<grid, block, 0, L.stream>>>(C, pt, max_pages, start, n_cells, k_out, v_rot_out, v_out, dh, dp, L.status);
   else if (C.fmt == K8V4_FORMAT_Q4)
-    dequant_kernel<K8V4_FORMAT_Q4><<<grid, block, 0, L.stream>>>(C, pt, max_pages, start, n_cells, k_out, v_rot_out, v_out, L.status);
+    dequant_kernel<K8V4_FORMAT_Q4><<<grid, block, 0, L.stream>>>(C, pt, max_pages, start, n_cells, k_out, v_rot_out, v_out, dh, dp, L.status);
   else
-    dequant_kernel<K8V4_FORMAT_INT8><<<grid, block, 0, L.stream>>>(C, pt, max_pages, start, n_cells, k_out, v_rot_out, v_out, L.status);
+    dequant_kernel<K8V4_FORMAT_INT8><<<grid, block, 0, L.stream>>>(C, pt, max_pages, start, n_cells, k_out, v_rot_out, v_out, dh, dp, L.status);
   return cudaGetLastError() == cudaSuccess ? K8V4_OK : K8V4_ECUDA;
 }
 

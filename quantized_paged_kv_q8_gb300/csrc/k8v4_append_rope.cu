@@ -19,6 +19,7 @@ namespace k8v4 {
 namespace {
 
 constexpr int kWarps = 8;
+constexpr int kBulkCtas = 3;      // resident CTAs per SM of the bulk kernel
 
 struct AppendRopeParams {
   CacheView C;
@@ -80,8 +81,10 @@ __global__ void __launch_bounds__(kWarps * 32) append_rope_kernel(const AppendRo
       float wt[8];
       load_weight8(p.k_weight, lane, wt);
       rms_row(x, wt, p.eps);
+      rope_row<INTER, false>(x, rl, f);
+    } else {
+      rope_row<INTER, true>(x, rl, f);
     }
-    rope_row<INTER>(x, rl, f);
     if (BF16) bf16x8_to_f32(f32x8_to_bf16(x), x);           // rounded to K's type
     if (FMT == K8V4_FORMAT_Q4) {
       rotate_exact(x, lane, ts);
@@ -102,9 +105,11 @@ __global__ void __launch_bounds__(kWarps * 32) append_rope_kernel(const AppendRo
 
 // Long appends of bf16 rows: the persistent structure of append_bf16_kernel (a
 // warp steps through a contiguous run of (seq, token, head) items and loads the
-// next item's K, V and table factors before it works on the current one).
-template <int FMT, bool INTER>
-__global__ void __launch_bounds__(kWarps * 32, 2) append_rope_bf16_kernel(const AppendRopeParams p) {
+// next item's K and V before it works on the current one).  The 16 cosines and
+// sines of a lane are read when they are used (the next token's row is prefetched):
+// held across the quantisers they leave room for two CTAs per SM only.
+template <int FMT, bool INTER, bool NORM>
+__global__ void __launch_bounds__(kWarps * 32, kBulkCtas) append_rope_bf16_kernel(const AppendRopeParams p) {
   __shared__ __align__(16) long long stage[kWarps][kRotScratch];
   __shared__ float scale_tab[128];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -130,8 +135,13 @@ __global__ void __launch_bounds__(kWarps * 32, 2) append_rope_bf16_kernel(const 
   const int64_t k_next = p.k_stride - (C.H - 1) * kD, v_next = p.v_stride - (C.H - 1) * kD;   // last head -> next token
   const RopeLane rl = rope_lane<INTER>(lane, p.half);
   uint4 kr = __ldcs(reinterpret_cast<const uint4*>(kp)), vr = __ldcs(reinterpret_cast<const uint4*>(vp));
-  RopeFactors<INTER> f;
-  if (cell >= 0 && cell < cell_limit) rope_load<INTER>(p.table + cell * (2 * p.half), rl, p.half, f);
+  auto prefetch_row = [&](int64_t c) {                   // the table row of a cell, towards L1
+    if (rl.on && c >= 0 && c < cell_limit) {
+      const float* row = p.table + c * (2 * p.half);
+      if (INTER || lane * 8 < p.half) asm volatile("prefetch.global.L1 [%0];" ::"l"(row + rl.at));
+      if (INTER || lane * 8 >= p.half) asm volatile("prefetch.global.L1 [%0];" ::"l"(row + p.half + rl.at));
+    }
+  };
   bool lookup = true;
   int cslot = 0;
   uint8_t* base = nullptr;
@@ -156,12 +166,14 @@ __global__ void __launch_bounds__(kWarps * 32, 2) append_rope_bf16_kernel(const 
     if (in_range) {
       float x[8];
       bf16x8_to_f32(kc, x);
-      if (p.k_weight) {
+      RopeFactors<INTER> f;
+      rope_load<INTER>(p.table + cell * (2 * p.half), rl, p.half, f);
+      if (NORM) {
         float wt[8];
         load_weight8(p.k_weight, lane, wt);
         rms_row(x, wt, p.eps);
       }
-      rope_row<INTER>(x, rl, f);
+      rope_row<INTER, !NORM>(x, rl, f);
       krot = f32x8_to_bf16(x);
     }
     const bool ok = in_range && base != nullptr;
@@ -178,7 +190,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) append_rope_bf16_kernel(const 
         ++cell;
         if (++cslot == C.P) lookup = true;
       }
-      if (item + 1 < item_end && cell >= 0 && cell < cell_limit) rope_load<INTER>(p.table + cell * (2 * p.half), rl, p.half, f);
+      if (item + 1 < item_end) prefetch_row(cell);
     }
     if (!ok) {
       if (lane == 0) record_status(p.status, K8V4_ERANGE);
@@ -196,8 +208,9 @@ int launch_fmt(const Launch& L, const AppendRopeParams& p, bool bf, int split, i
   const dim3 block(kWarps * 32);
   if (bf && !split) {
     const int64_t want = (items + kWarps - 1) / kWarps;
-    const dim3 grid(static_cast<unsigned>(std::min<int64_t>(want, static_cast<int64_t>(L.num_sms) * 2)));
-    append_rope_bf16_kernel<FMT, INTER><<<grid, block, 0, L.stream>>>(p);
+    const dim3 grid(static_cast<unsigned>(std::min<int64_t>(want, static_cast<int64_t>(L.num_sms) * kBulkCtas)));
+    if (p.k_weight) append_rope_bf16_kernel<FMT, INTER, true><<<grid, block, 0, L.stream>>>(p);
+    else append_rope_bf16_kernel<FMT, INTER, false><<<grid, block, 0, L.stream>>>(p);
   } else {
     const dim3 grid(static_cast<unsigned>(((split ? 2 : 1) * items + kWarps - 1) / kWarps));
     if (bf) append_rope_kernel<true, FMT, INTER><<<grid, block, 0, L.stream>>>(p, split);

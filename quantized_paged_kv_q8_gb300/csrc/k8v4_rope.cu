@@ -42,7 +42,7 @@ struct RopeParams {
 
 // PER: heads of one token that a warp takes
 template <bool BF16, bool INTER, int PER>
-__global__ void __launch_bounds__(kRopeWarps * 32) norm_rope_kernel(const RopeParams p) {
+__global__ void __launch_bounds__(kRopeWarps * 32, 4) norm_rope_kernel(const RopeParams p) {
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int64_t wi = static_cast<int64_t>(blockIdx.x) * kRopeWarps + w;
   if (wi >= p.n_tokens * p.units) return;
@@ -94,8 +94,12 @@ __global__ void __launch_bounds__(kRopeWarps * 32) norm_rope_kernel(const RopePa
       x[0] = __uint_as_float(a.x); x[1] = __uint_as_float(a.y); x[2] = __uint_as_float(a.z); x[3] = __uint_as_float(a.w);
       x[4] = __uint_as_float(c.x); x[5] = __uint_as_float(c.y); x[6] = __uint_as_float(c.z); x[7] = __uint_as_float(c.w);
     }
-    if (weight) rms_row(x, wt, p.eps);
-    rope_row<INTER>(x, rl, f);
+    if (weight) {                                           // the same for the warp
+      rms_row(x, wt, p.eps);
+      rope_row<INTER, false>(x, rl, f);
+    } else {
+      rope_row<INTER, true>(x, rl, f);
+    }
     if (BF16) {
       reinterpret_cast<uint4*>(static_cast<uint16_t*>(dst) + out0 + i * kD)[lane] = f32x8_to_bf16(x);
     } else {

@@ -9,11 +9,13 @@
 // the elements (i, i + rot_dim / 2) or (2i, 2i + 1) of the first rot_dim
 // elements; the others pass through.
 //
-// Rounding: y is the exact x1 c - x2 s rounded to fp32 (to 2^-46 of the
-// larger product before that rounding), then to the row's type.  The stored K codes
-// are rints of quotients of these values, so one fp32 unit here moves a code
-// now and then; with the products' errors carried, the result does not depend
-// on how a compiler fuses the multiply and the subtraction.
+// Rounding: without a norm, y is the exact x1 c - x2 s rounded to fp32 (to 2^-46 of
+// the larger product before that rounding), then to the row's type.  The stored K
+// codes are rints of quotients of these values, so one fp32 unit here moves a
+// code now and then; with the products' errors carried, the result does not
+// depend on how a compiler fuses the multiply and the subtraction.  Behind a norm,
+// whose own result is a few fp32 units off, one product is rounded and the other
+// fused (2 packed instructions where the carried form takes 13).
 #pragma once
 
 #include "k8v4_common.cuh"
@@ -21,18 +23,23 @@
 namespace k8v4 {
 namespace {
 
-// a + b and a * b on two fp32 lanes at once (the packed fp32 pipe)
-__device__ __forceinline__ float2 neg2(float2 a) { return make_float2(-a.x, -a.y); }
-
-// x c + o s for two elements, the error terms of both products and of their sum
-// carried: p + pe = x c and q + qe = o s exactly, d + de = p + q exactly.
+// x c + o s for two elements (the packed fp32 instructions), the error terms of
+// both products and of their sum carried: p - npe = x c and q - nqe = o s exactly,
+// d + de = p + q exactly.  Differences are fused multiplies by -1: the packed
+// forms negate no operand.
 __device__ __forceinline__ float2 dot2_carried(float2 x, float2 c, float2 o, float2 s) {
+  const float2 m1 = make_float2(-1.0f, -1.0f);
   const float2 p = __fmul2_rn(x, c), q = __fmul2_rn(o, s);
-  const float2 pe = __ffma2_rn(x, c, neg2(p)), qe = __ffma2_rn(o, s, neg2(q));
+  const float2 npe = __ffma2_rn(__fmul2_rn(x, m1), c, p), nqe = __ffma2_rn(__fmul2_rn(o, m1), s, q);
   const float2 d = __fadd2_rn(p, q);
-  const float2 bb = __fadd2_rn(d, neg2(p));
-  const float2 de = __fadd2_rn(__fadd2_rn(p, neg2(__fadd2_rn(d, neg2(bb)))), __fadd2_rn(q, neg2(bb)));
-  return __fadd2_rn(d, __fadd2_rn(de, __fadd2_rn(pe, qe)));
+  const float2 bb = __ffma2_rn(p, m1, d);
+  const float2 de = __fadd2_rn(__ffma2_rn(__ffma2_rn(bb, m1, d), m1, p), __ffma2_rn(bb, m1, q));
+  return __fadd2_rn(d, __ffma2_rn(__fadd2_rn(npe, nqe), m1, de));
+}
+
+// the same with one product rounded
+__device__ __forceinline__ float2 dot2_plain(float2 x, float2 c, float2 o, float2 s) {
+  return __ffma2_rn(x, c, __fmul2_rn(o, s));
 }
 
 // Where a lane's 8 elements get their cosines and sines from, and which lane
@@ -81,15 +88,16 @@ __device__ __forceinline__ void rope_load(const float* __restrict__ row, const R
 }
 
 // Rotate the row in place (all lanes call; lanes past rot_dim keep their values)
-template <bool INTER>
+template <bool INTER, bool CARRIED>
 __device__ __forceinline__ void rope_row(float x[8], const RopeLane& rl, const RopeFactors<INTER>& f) {
   constexpr unsigned kAll = 0xffffffffu;
+  auto dot2 = [](float2 v, float2 c, float2 o, float2 s) { return CARRIED ? dot2_carried(v, c, o, s) : dot2_plain(v, c, o, s); };
   if (INTER) {
     if (!rl.on) return;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const float2 v = make_float2(x[2 * i], x[2 * i + 1]);
-      const float2 y = dot2_carried(v, make_float2(f.c[i], f.c[i]), make_float2(v.y, v.x), make_float2(-f.s[i], f.s[i]));
+      const float2 y = dot2(v, make_float2(f.c[i], f.c[i]), make_float2(v.y, v.x), make_float2(-f.s[i], f.s[i]));
       x[2 * i] = y.x;
       x[2 * i + 1] = y.y;
     }
@@ -100,7 +108,7 @@ __device__ __forceinline__ void rope_row(float x[8], const RopeLane& rl, const R
     if (!rl.on) return;
 #pragma unroll
     for (int r = 0; r < 8; r += 2) {
-      const float2 y = dot2_carried(make_float2(x[r], x[r + 1]), make_float2(f.c[r], f.c[r + 1]),
+      const float2 y = dot2(make_float2(x[r], x[r + 1]), make_float2(f.c[r], f.c[r + 1]),
                                     make_float2(o[r], o[r + 1]), make_float2(f.s[r], f.s[r + 1]));
       x[r] = y.x;
       x[r + 1] = y.y;
@@ -113,14 +121,19 @@ __device__ __forceinline__ void rope_row(float x[8], const RopeLane& rl, const R
 // caller)
 __device__ __forceinline__ void rms_row(float x[8], const float w[8], float eps) {
   constexpr unsigned kAll = 0xffffffffu;
-  float s = __fmul_rn(x[0], x[0]);
+  float2 s2 = __fmul2_rn(make_float2(x[0], x[1]), make_float2(x[0], x[1]));
 #pragma unroll
-  for (int r = 1; r < 8; ++r) s = __fmaf_rn(x[r], x[r], s);
+  for (int r = 2; r < 8; r += 2) s2 = __ffma2_rn(make_float2(x[r], x[r + 1]), make_float2(x[r], x[r + 1]), s2);
+  float s = __fadd_rn(s2.x, s2.y);
 #pragma unroll
   for (int o = 16; o >= 1; o >>= 1) s = __fadd_rn(s, __shfl_xor_sync(kAll, s, o));
   const float inv = rsqrtf(__fmaf_rn(s, 1.0f / kD, eps));
 #pragma unroll
-  for (int r = 0; r < 8; ++r) x[r] = __fmul_rn(__fmul_rn(x[r], inv), w[r]);
+  for (int r = 0; r < 8; r += 2) {
+    const float2 y = __fmul2_rn(__fmul2_rn(make_float2(x[r], x[r + 1]), make_float2(inv, inv)), make_float2(w[r], w[r + 1]));
+    x[r] = y.x;
+    x[r + 1] = y.y;
+  }
 }
 
 __device__ __forceinline__ void load_weight8(const float* __restrict__ w, int lane, float out[8]) {
