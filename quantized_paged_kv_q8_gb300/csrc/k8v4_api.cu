@@ -318,9 +318,12 @@ static SharedPlan shared_plans(const CacheView& C, int n_seqs, int shared_len, i
   else if (max_seq_len > pre.cells) *own = plan_decode_splits(C, n_seqs, max_seq_len - pre.cells, sms);
   return pre;
 }
+static size_t shared_rows_bytes(const CacheView& C, const SharedPlan& pre, const AttendPlan& own, int n_seqs) {
+  return static_cast<size_t>(n_seqs) * (pre.splits + own.splits) * C.H * kGqa * 260 * sizeof(float);   // a multiple of 16
+}
 static size_t shared_ws_bytes(const CacheView& C, const SharedPlan& pre, const AttendPlan& own, int n_seqs) {
   if (pre.cells == 0) return own.ws_bytes;
-  return static_cast<size_t>(n_seqs) * (pre.splits + own.splits) * C.H * kGqa * 260 * sizeof(float);
+  return shared_rows_bytes(C, pre, own, n_seqs) + pre.acc_bytes;
 }
 
 size_t attn_k8v4_shared_workspace_bytes(const k8v4_cache* cache, int32_t n_seqs, int32_t shared_len,
@@ -367,7 +370,7 @@ int attn_k8v4_decode_shared(const k8v4_cache* cache, const void* q, int32_t q_dt
     if (rc) return rc;
   }
   rc = launch_shared_prefix(L, C, pre, q, page_table, max_pages, seq_lens, n_seqs, max_seq_len, sm_scale, ws, splits,
-                            own.splits > 0);
+                            ws + shared_rows_bytes(C, pre, own, n_seqs) / sizeof(float), own.splits > 0);
   if (rc) return rc;
   return launch_combine_rows(L, ws, splits, n_seqs, C.H, out);
 }

@@ -176,12 +176,13 @@ int launch_combine_parts(const Launch& L, const float* parts, int n_parts, int n
 // plan.splits of each sequence
 struct SharedPlan {
   int cells = 0, splits = 0, tiles_per_split = 0;
+  size_t acc_bytes = 0;      // running sums of the kernel's CTAs, behind the partial rows
 };
 bool shared_prefix_supported(const CacheView& C);
 SharedPlan plan_shared(const CacheView& C, int n_seqs, int shared_len, int max_seq_len, int num_sms);
 int launch_shared_prefix(const Launch& L, const CacheView& C, const SharedPlan& plan, const void* q, const int32_t* pt,
                          int64_t max_pages, const int32_t* lens, int n_seqs, int max_seq_len, float sm_scale, float* ws,
-                         int ws_splits, bool behind_splits);
+                         int ws_splits, float* acc, bool behind_splits);
 // the plan of launch_decode_splits over `cells` cells: short ranges of many
 // sequences in small CTAs (pl.warps workers)
 AttendPlan plan_decode_splits(const CacheView& C, int n_seqs, int cells, int num_sms);

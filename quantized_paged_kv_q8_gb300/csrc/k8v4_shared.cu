@@ -20,16 +20,19 @@
 //    longer than the products;
 //  - warps have roles, handing over through mbarriers, so the tensor pipe, the
 //    softmax and the conversion of neighbouring tiles overlap:
-//      warps 0-7    rows: two threads per row (32 cells, and 128 of O's dims, each)
-//      warps 8-11   conversion: raw tile -> registers -> operand tiles
-//      warp 12      (leader CTA) issues every product of the pair
-//      warp 13      copies the raw tiles (TMA)
-//    The row warps hold O in fp32 registers (216 a thread, from the others' share);
+//      warps 0-15   rows: four threads per row (16 cells, and 64 of O's dims, each)
+//      warps 16-19  conversion: raw tile -> registers -> operand tiles
+//      warp 20      (leader CTA) issues every product of the pair
+//      warp 21      copies the raw tiles (TMA)
+//    With O in the registers of eight row warps (216 a thread) these were the slowest
+//    part, two of them per scheduler with nothing to hide their latency behind;
+//    sixteen leave no room for O, so the running O lives in global memory (L2),
+//    where it goes every kChain tiles;
 //  - the reference maximum of a row moves only when a tile exceeds it by 2^8, and
 //    then its O tile is rescaled in tensor memory, so the two CTAs need not agree;
-//    every kChain tiles O is folded into the registers, in both CTAs at the same
+//    every kChain tiles O is added to the running O, in both CTAs at the same
 //    tile, because the tensor core's accumulation is not rounded to nearest (2.9e-5
-//    after 2,048 cells without the fold).
+//    after 2,048 cells without that).
 //
 // Tensor memory (512 columns): S buffers [0,128), [128,256) (S0 | S1 each; a
 // thread's P terms overlay its own columns of S0), O [256,512).  QK(i+2) overwrites P(i): its S1 half, which
@@ -53,14 +56,18 @@ constexpr int kPStride = 260;               // floats per partial row: o[256], m
 constexpr int kRows = 128;                  // query rows per CTA (256 per pair)
 constexpr int kPairSeqs = 2 * kRows / kGqa; // 32
 constexpr int kTileN = 64;
-constexpr int kThreads = 512;
-constexpr int kConvWarp0 = 8, kIssueWarp = 12, kLoadWarp = 13;
+constexpr int kRowWarps = 16, kRowThreads = 32 * kRowWarps;
+constexpr int kThreads = kRowThreads + 256;
+constexpr int kConvWarp0 = kRowWarps, kIssueWarp = kConvWarp0 + 4, kLoadWarp = kIssueWarp + 1;
+// the register split waits for whole warpgroups: roles begin at multiples of four warps
+static_assert(kConvWarp0 % 4 == 0 && kIssueWarp % 4 == 0 && kLoadWarp < kIssueWarp + 4 && kThreads == 32 * (kIssueWarp + 4), "roles");
 constexpr int kChain = 16;                  // tiles accumulated in one TMEM O tile
 constexpr float kSlack = 8.0f;              // log2 headroom of P above its row's reference maximum
 constexpr uint32_t kWaitDefaultNs = 1000000000u;
-// registers per thread after the split; 2 * 216 + 56 + 24 = 4 * 128, what the block launches with
-constexpr int kRowRegs = 216, kConvRegs = 56, kIssueRegs = 24;
-static_assert(2 * kRowRegs + kConvRegs + kIssueRegs <= 4 * 128, "register split");
+// registers per thread after the split (16 row, 4 conversion and 4 other warps), out
+// of the 80 of 24 warps that the block launches with
+constexpr int kLaunchRegs = 80, kRowRegs = 96, kConvRegs = 72, kIssueRegs = 24;
+static_assert(4 * kRowRegs + kConvRegs + kIssueRegs <= 6 * kLaunchRegs, "register split");
 
 // shared memory (bytes); operand tiles 1024-byte aligned, the same in both CTAs
 constexpr int kQOff = 0;                              // Q fp16 [4 chunks][128 rows][128 B]
@@ -69,8 +76,8 @@ constexpr int kKBuf = 16384;
 constexpr int kVOff = kKOff + 2 * kKBuf;              // V fp16, 2 buffers x 2 planes x [2 atoms][64 cells][128 B]
 constexpr int kVPlane = 16384, kVBuf = 2 * kVPlane;
 constexpr int kKsOff = kVOff + 2 * kVBuf;             // K scales, 4 tiles x [2][64] f32
-constexpr int kRedOff = kKsOff + 4 * 512;             // [2][128] f32 exchange, [128] score factors
-constexpr int kBarOff = kRedOff + 2 * 512 + 512;
+constexpr int kRedOff = kKsOff + 4 * 512;             // [4][128] f32 exchange, [128] score factors
+constexpr int kBarOff = kRedOff + 4 * 512 + 512;
 constexpr int kCtlOff = kBarOff + 192;                // tmem slot, failure word, bad groups of 4 tiles, valid groups of the stages
 constexpr int kRawOff = (kCtlOff + 64 + 1023) / 1024 * 1024;   // raw tiles, as many stages as fit (3, or 2 from 4 KV heads on)
 constexpr int kSmemMax = 227 * 1024;
@@ -87,7 +94,7 @@ static_assert(kKsOff - kQOff >= kRows * 256 * 4, "row buffer");
 enum { kBarKFull = 0, kBarVFull = 2, kBarPFull = 4, kBarSFull = 6, kBarODone = 8, kBarKsFull = 10,
        kBarDrain = 14, kBarMost = 15, kBarRawFull = 16, kBarRawEmpty = 20 };
 
-constexpr uint32_t kTmemCols = 512, kSBuf = 128, kS1Col = 64, kOCol = 256, kP2Col = 16;
+constexpr uint32_t kTmemCols = 512, kSBuf = 128, kS1Col = 64, kOCol = 256, kP2Col = 8;
 
 struct SharedParams {
   CacheView C;
@@ -101,6 +108,7 @@ struct SharedParams {
   int ws_splits;            // partial rows per sequence in ws (this kernel writes the first `splits`)
   float sm_scale_log2;
   float* ws;
+  float* acc;               // [CTA][128 rows x 256] running O, for sweeps of more than kChain tiles
   int* status;
   uint32_t wait_ns;
   FastDiv page_div;
@@ -172,13 +180,13 @@ __device__ __forceinline__ bool elect_one() {
       : "=r"(r));
   return r != 0;
 }
-// the same over the two warps that share 32 rows (warps w and w + 4, w < 4)
-__device__ __forceinline__ bool pair_any(int w, bool pred) {
+// the same over the four warps that share 32 rows (warps w, w + 4, w + 8, w + 12; w < 4)
+__device__ __forceinline__ bool quad_any(int w, bool pred) {
   uint32_t r;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.u32 p, %2, 0;\n\t"
-      "barrier.cta.red.or.pred q, %1, 64, p;\n\t"
+      "barrier.cta.red.or.pred q, %1, 128, p;\n\t"
       "selp.u32 %0, 1, 0, q;\n\t}"
       : "=r"(r)
       : "r"(w + 3), "r"(pred ? 1u : 0u)
@@ -191,14 +199,14 @@ __device__ __forceinline__ bool rows_any(bool pred) {
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.u32 p, %1, 0;\n\t"
-      "barrier.cta.red.or.pred q, 1, 256, p;\n\t"
+      "barrier.cta.red.or.pred q, 1, 512, p;\n\t"
       "selp.u32 %0, 1, 0, q;\n\t}"
       : "=r"(r)
       : "r"(pred ? 1u : 0u)
       : "memory");
   return r != 0;
 }
-__device__ __forceinline__ void rows_barrier() { asm volatile("barrier.cta.sync 2, 256;" ::: "memory"); }
+__device__ __forceinline__ void rows_barrier() { asm volatile("barrier.cta.sync 2, 512;" ::: "memory"); }
 // two runs of 16 fp32 columns of this thread's TMEM lane
 __device__ __forceinline__ void tmem_ld16x2(uint32_t ta, uint32_t tb, float a[16], float b[16]) {
   uint32_t r[32];
@@ -258,11 +266,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) shared_
   const int seq0 = (unit - split * groups) * kPairSeqs + static_cast<int>(rank) * (kRows / kGqa);   // this CTA's first sequence
   const CacheView& C = p.C;
   const int HQ = C.H * kGqa;
-  const int row = tid & (kRows - 1), part = tid >> 7;
+  const int row = tid & (kRows - 1), part = tid >> 7;      // (row warps) 16 cells of a tile and 64 dims of O per part
   const uint32_t bars = sb + kBarOff;
   volatile int* ctl = reinterpret_cast<volatile int*>(smem + kCtlOff);   // [0] tmem, [1] failed, [4..7] bad groups of 4 tiles
-  float* red = reinterpret_cast<float*>(smem + kRedOff);                 // [2][128]
-  float* fsc = red + 2 * kRows;                                          // [128]
+  float* red = reinterpret_cast<float*>(smem + kRedOff);                 // [4][128]
+  float* fsc = red + 4 * kRows;                                          // [128]
   float* ksbuf = reinterpret_cast<float*>(smem + kKsOff);
 
   const int tile0 = split * p.tiles_per_split;
@@ -272,7 +280,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) shared_
     // one barrier per lane
     int count = 0;
     if (lane < kBarPFull) count = 8;                       // K, V tiles: 4 conversion warps of both CTAs
-    else if (lane < kBarSFull) count = 16;                 // P: 8 row warps of both CTAs
+    else if (lane < kBarSFull) count = 2 * kRowWarps;      // P: the row warps of both CTAs
     else if (lane < kBarKsFull) count = 1;                 // S done, O done: one commit
     else if (lane < kBarDrain) count = 4;                  // K scales: the CTA's conversion warps
     else if (lane < kBarRawFull) count = 1;                // everything done, three quarters of PV: one commit
@@ -342,7 +350,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) shared_
   int my_vis = 0;
   {
     const int s = seq0 + row / kGqa;
-    if (s < p.n_seqs) {
+    if (warp < kRowWarps && s < p.n_seqs) {
       int v = p.lens[s];
       if (v < 0 || v > p.max_seq_len) {
         if (part == 0) record_status(p.status, K8V4_ERANGE);
@@ -396,47 +404,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) shared_
   tc_fence_after();
   const uint32_t tmem = static_cast<uint32_t>(ctl[0]);
 
-  if (warp < 8) {
+  if (warp < kRowWarps) {
     // ================================================================ rows
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRowRegs));
-    const int half = part;                                 // cells [32 half, +32) of a tile, dims [128 half, +128) of O
     const uint32_t lane_base = static_cast<uint32_t>(32 * (warp & 3)) << 16;
     const float my_f = fsc[row];
     const uint32_t p_full0 = map_to(bars + 8 * kBarPFull, 0);
-    float o_run[128];
-#pragma unroll
-    for (int i = 0; i < 128; ++i) o_run[i] = 0.0f;
-    float m_run = -INFINITY, l_part = 0.0f;
-    bool failed = false;
-    const uint32_t o_tile = tmem + lane_base + kOCol + 128 * half;
-    auto fold = [&](float a) {                             // o_run = (o_run + O tile) * a
-      const float2 a2 = make_float2(a, a);
-#pragma unroll
-      for (int h = 0; h < 4; ++h) {
-        float o[32];
-        tmem_ld32(o_tile + 32 * h, o);
-#pragma unroll
-        for (int i = 0; i < 32; i += 2) {
-          const float2 r = __fmul2_rn(__fadd2_rn(make_float2(o_run[32 * h + i], o_run[32 * h + i + 1]),
-                                                 make_float2(o[i], o[i + 1])), a2);
-          o_run[32 * h + i] = r.x;
-          o_run[32 * h + i + 1] = r.y;
-        }
-      }
-    };
-    auto rescale = [&](float a) {                          // O tile *= a, o_run *= a
-#pragma unroll
-      for (int h = 0; h < 16; ++h) {
-        float o[8];
-        tmem_ld8(o_tile + 8 * h, o);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          o[i] *= a;
-          o_run[8 * h + i] *= a;
-        }
-        tmem_st8(o_tile + 8 * h, o);
-      }
-    };
+    const uint32_t o_tile = tmem + lane_base + kOCol + 64 * part;
+    // the running O of this thread's 64 dims: float4 number c at acc[512 c]
+    float4* const acc = reinterpret_cast<float4*>(p.acc) +
+                        (n_tiles > kChain ? (static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x) * (kRows * 64) + tid : 0);
+    float m_run = -INFINITY, l_part = 0.0f, acc_scale = 1.0f;          // acc counts times acc_scale
+    bool failed = false, have_acc = false;
     for (int i = 0; i < n_tiles; ++i) {
       const int buf = i & 1;
       const uint32_t parity = (i >> 1) & 1;
@@ -446,46 +425,47 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) shared_
         ctl[1] = 1;
       }
       tc_fence_after();
-      // scores, unscaled (my_f > 0, so the maximum commutes with it); cell c of this half
-      const uint32_t sbase = tmem + lane_base + kSBuf * buf + 32 * half;
-      const float* ks = ksbuf + 128 * (i & 3) + 32 * half;             // s0 of the tile's cells, then s1
-      float2 sc[16];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
+      // scores, unscaled (my_f > 0, so the maximum commutes with it); cell c of this part
+      const uint32_t sbase = tmem + lane_base + kSBuf * buf + 16 * part;
+      const float* ks = ksbuf + 128 * (i & 3) + 16 * part;             // s0 of the tile's cells, then s1
+      float2 sc[8];
+      {
         float a[16], b[16];
-        tmem_ld16x2(sbase + 16 * h, sbase + kS1Col + 16 * h, a, b);
+        tmem_ld16x2(sbase, sbase + kS1Col, a, b);
 #pragma unroll
         for (int c = 0; c < 16; c += 4) {
-          const float4 k0 = *reinterpret_cast<const float4*>(ks + 16 * h + c);
-          const float4 k1 = *reinterpret_cast<const float4*>(ks + 64 + 16 * h + c);
-          sc[8 * h + c / 2] = __ffma2_rn(make_float2(k1.x, k1.y), make_float2(b[c], b[c + 1]),
-                                         __fmul2_rn(make_float2(k0.x, k0.y), make_float2(a[c], a[c + 1])));
-          sc[8 * h + c / 2 + 1] = __ffma2_rn(make_float2(k1.z, k1.w), make_float2(b[c + 2], b[c + 3]),
-                                             __fmul2_rn(make_float2(k0.z, k0.w), make_float2(a[c + 2], a[c + 3])));
+          const float4 k0 = *reinterpret_cast<const float4*>(ks + c);
+          const float4 k1 = *reinterpret_cast<const float4*>(ks + 64 + c);
+          sc[c / 2] = __ffma2_rn(make_float2(k1.x, k1.y), make_float2(b[c], b[c + 1]),
+                                 __fmul2_rn(make_float2(k0.x, k0.y), make_float2(a[c], a[c + 1])));
+          sc[c / 2 + 1] = __ffma2_rn(make_float2(k1.z, k1.w), make_float2(b[c + 2], b[c + 3]),
+                                     __fmul2_rn(make_float2(k0.z, k0.w), make_float2(a[c + 2], a[c + 3])));
         }
       }
-      const int vis = my_vis - (tile0 + i) * kTileN - 32 * half;       // cells [0, vis) of this half
-      const int bad = ctl[4 + (i & 3)];                                // 16-cell groups on a page out of range
-      if (vis < 32 || bad) {
+      const int vis = my_vis - (tile0 + i) * kTileN - 16 * part;       // cells [0, vis) of this part
+      const bool bad = (ctl[4 + (i & 3)] >> part) & 1;                 // its 16 cells are on a page out of range
+      if (vis < 16 || bad) {
 #pragma unroll
-        for (int c = 0; c < 32; c += 2) {
-          const bool off = ((bad >> (2 * half + (c >> 4))) & 1) != 0;
-          if (c >= vis || off) sc[c / 2].x = -INFINITY;
-          if (c + 1 >= vis || off) sc[c / 2].y = -INFINITY;
+        for (int c = 0; c < 16; c += 2) {
+          if (c >= vis || bad) sc[c / 2].x = -INFINITY;
+          if (c + 1 >= vis || bad) sc[c / 2].y = -INFINITY;
         }
       }
-      float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+      float mx0 = -INFINITY, mx1 = -INFINITY;
 #pragma unroll
-      for (int c = 0; c < 16; ++c) mx[c & 3] = fmaxf(mx[c & 3], fmaxf(sc[c].x, sc[c].y));
-      const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * my_f;
-      // the two threads of a row agree on its reference: a vote of their two warps
-      const bool any = pair_any(warp & 3, failed || top > m_run + kSlack);
+      for (int c = 0; c < 8; c += 2) {
+        mx0 = fmaxf(mx0, fmaxf(sc[c].x, sc[c].y));
+        mx1 = fmaxf(mx1, fmaxf(sc[c + 1].x, sc[c + 1].y));
+      }
+      const float top = fmaxf(mx0, mx1) * my_f;
+      // the four threads of a row agree on its reference: a vote of their four warps
+      const bool any = quad_any(warp & 3, failed || top > m_run + kSlack);
       float alpha = 1.0f;
       if (any) {
-        red[half * kRows + row] = top;
-        // both warps leave together: the failure word is read once, ahead of a vote
-        if (pair_any(warp & 3, failed || ctl[1] != 0)) { failed = true; break; }
-        const float mt = fmaxf(red[row], red[kRows + row]);
+        red[part * kRows + row] = top;
+        // the four leave together: the failure word is read once, ahead of a vote
+        if (quad_any(warp & 3, failed || ctl[1] != 0)) { failed = true; break; }
+        const float mt = fmaxf(fmaxf(red[row], red[kRows + row]), fmaxf(red[2 * kRows + row], red[3 * kRows + row]));
         if (mt > m_run + kSlack) {
           alpha = exp2f(m_run - mt);                                   // 0 on the first visible tile
           m_run = mt;
@@ -493,31 +473,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) shared_
         }
       }
       // P * 2^7 in two fp16 terms: the top 11 bits of p, and the rest of it rounded.
-      // They overlay this thread's own S0 columns, P1 in the first 16, P2 behind it
+      // They overlay this thread's own S0 columns, P1 in the first 8, P2 behind it
       const float mu = (m_run == -INFINITY ? 0.0f : m_run) - 7.0f;
       const float2 f2 = make_float2(my_f, my_f), mu2 = make_float2(-mu, -mu);
       float2 psum = make_float2(0.0f, 0.0f);
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
+      {
         float p1[8], p2[8];
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
-          const float2 e = __ffma2_rn(sc[8 * h + c], f2, mu2);
+          const float2 e = __ffma2_rn(sc[c], f2, mu2);
           const float2 q = make_float2(ex2_ftz(e.x), ex2_ftz(e.y));
           const float2 t = make_float2(__uint_as_float(__float_as_uint(q.x) & 0xffffe000u),
                                        __uint_as_float(__float_as_uint(q.y) & 0xffffe000u));
-          const float2 r = __fadd2_rn(q, make_float2(-t.x, -t.y));     // exact
+          const float2 r = __ffma2_rn(t, make_float2(-1.0f, -1.0f), q);   // q - t, exact
           const __half2 h1 = __floats2half2_rn(t.x, t.y), h2 = __floats2half2_rn(r.x, r.y);
           psum = __fadd2_rn(psum, q);
           p1[c] = __uint_as_float(*reinterpret_cast<const uint32_t*>(&h1));
           p2[c] = __uint_as_float(*reinterpret_cast<const uint32_t*>(&h2));
         }
-        tmem_st8x2(sbase + 8 * h, sbase + kP2Col + 8 * h, p1, p2);
+        tmem_st8x2(sbase, sbase + kP2Col, p1, p2);
       }
       l_part += psum.x + psum.y;
       tmem_wait_st();
-      // O of the tiles so far: into the registers at every kChain-th tile (both
-      // CTAs), rescaled in place where a reference moved in between
+      // O of the tiles so far: into acc at every kChain-th tile (both CTAs), rescaled
+      // in place where a reference moved in between
       const bool folds = i > 0 && i % kChain == 0;
       if (folds || (i > 0 && any && __any_sync(kFull, alpha != 1.0f))) {
         if (!mbar_wait(bars + 8 * (kBarODone + (buf ^ 1)), ((i - 1) >> 1) & 1, p.wait_ns)) {
@@ -525,18 +504,55 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) shared_
           ctl[1] = 1;
         }
         tc_fence_after();
-        if (folds) fold(alpha);
-        else rescale(alpha);
+        if (folds) {                                                   // acc = (acc + O) * alpha
+          const float a = alpha * acc_scale;
+#pragma unroll
+          for (int h = 0; h < 4; ++h) {
+            float4 old[4];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) old[c] = have_acc ? acc[512 * (4 * h + c)] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            float o[16];
+            tmem_ld16(o_tile + 16 * h, o);
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+              acc[512 * (4 * h + c)] = make_float4(old[c].x * a + o[4 * c] * alpha, old[c].y * a + o[4 * c + 1] * alpha,
+                                                   old[c].z * a + o[4 * c + 2] * alpha, old[c].w * a + o[4 * c + 3] * alpha);
+          }
+          have_acc = true;
+          acc_scale = 1.0f;
+        } else {                                                       // O *= alpha
+#pragma unroll
+          for (int h = 0; h < 8; ++h) {
+            float o[8];
+            tmem_ld8(o_tile + 8 * h, o);
+#pragma unroll
+            for (int c = 0; c < 8; ++c) o[c] *= alpha;
+            tmem_st8(o_tile + 8 * h, o);
+          }
+          acc_scale *= alpha;
+        }
       }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) arrive_cluster(p_full0 + 8 * buf);
     }
     // ---- the last O tile, then o / m / l of the rows
-    if (!failed && n_tiles > 0) {
+    float o[64];
+    if (!failed) {
       if (mbar_wait(bars + 8 * (kBarODone + ((n_tiles - 1) & 1)), ((n_tiles - 1) >> 1) & 1, p.wait_ns)) {
         tc_fence_after();
-        fold(1.0f);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) tmem_ld32(o_tile + 32 * h, o + 32 * h);
+        if (have_acc) {
+#pragma unroll
+          for (int c = 0; c < 16; ++c) {
+            const float4 old = acc[512 * c];
+            o[4 * c] += old.x * acc_scale;
+            o[4 * c + 1] += old.y * acc_scale;
+            o[4 * c + 2] += old.z * acc_scale;
+            o[4 * c + 3] += old.w * acc_scale;
+          }
+        }
         tc_fence_before();
       } else {
         failed = true;
@@ -545,30 +561,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) shared_
     }
     // PV of the last tile is done in both CTAs (one commit covers the pair), and
     // with it every read of this CTA's operand tiles
-    red[half * kRows + row] = l_part;
+    red[part * kRows + row] = l_part;
     const bool stop = rows_any(failed);
     if (!stop) {
-      const float l = red[row] + red[kRows + row];
-      // inverse Walsh-Hadamard transform: seven stages over the thread's own 128
-      // dims in registers, the eighth (dims d and d + 128) as the rows are written
+      const float l = (red[row] + red[kRows + row]) + (red[2 * kRows + row] + red[3 * kRows + row]);
+      // inverse Walsh-Hadamard transform: six stages over the thread's own 64 dims in
+      // registers, the last two (dims d + 64 k) as the rows are written
 #pragma unroll
-      for (int h = 1; h < 128; h <<= 1) {
+      for (int h = 1; h < 64; h <<= 1) {
 #pragma unroll
-        for (int i = 0; i < 128; ++i) {
+        for (int i = 0; i < 64; ++i) {
           if (i & h) continue;
-          const float a = o_run[i], b = o_run[i + h];
-          o_run[i] = a + b;
-          o_run[i + h] = a - b;
+          const float a = o[i], b = o[i + h];
+          o[i] = a + b;
+          o[i + h] = a - b;
         }
       }
       float* rowbuf = reinterpret_cast<float*>(smem + kQOff);          // [128][256] fp32, rotated by 4 * row
 #pragma unroll
-      for (int i = 0; i < 128; i += 4) {
-        const int d = 128 * half + i;
-        *reinterpret_cast<float4*>(rowbuf + row * 256 + ((d + 4 * row) & 255)) =
-            make_float4(o_run[i], o_run[i + 1], o_run[i + 2], o_run[i + 3]);
-      }
-      if (half == 0) {
+      for (int i = 0; i < 64; i += 4)
+        *reinterpret_cast<float4*>(rowbuf + row * 256 + ((64 * part + i + 4 * row) & 255)) =
+            make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+      if (part == 0) {
         const int s = seq0 + row / kGqa;
         if (s < p.n_seqs) {
           float* dst = p.ws + ((static_cast<int64_t>(s) * p.ws_splits + split) * HQ + g * kGqa + row % kGqa) * kPStride;
@@ -577,15 +591,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) shared_
         }
       }
       rows_barrier();
-      for (int r = warp; r < kRows; r += 8) {
+      for (int r = warp; r < kRows; r += kRowWarps) {
         const int s = seq0 + r / kGqa;
         if (s >= p.n_seqs) break;
-        const float4 a = *reinterpret_cast<const float4*>(rowbuf + r * 256 + ((4 * lane + 4 * r) & 255));
-        const float4 b = *reinterpret_cast<const float4*>(rowbuf + r * 256 + ((128 + 4 * lane + 4 * r) & 255));
-        float* dst = p.ws + ((static_cast<int64_t>(s) * p.ws_splits + split) * HQ + g * kGqa + r % kGqa) * kPStride + 4 * lane;
+        float2 x[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) x[k] = *reinterpret_cast<const float2*>(rowbuf + r * 256 + ((64 * k + 2 * lane + 4 * r) & 255));
+        float* dst = p.ws + ((static_cast<int64_t>(s) * p.ws_splits + split) * HQ + g * kGqa + r % kGqa) * kPStride + 2 * lane;
+        const float2 s01 = make_float2(x[0].x + x[1].x, x[0].y + x[1].y), d01 = make_float2(x[0].x - x[1].x, x[0].y - x[1].y);
+        const float2 s23 = make_float2(x[2].x + x[3].x, x[2].y + x[3].y), d23 = make_float2(x[2].x - x[3].x, x[2].y - x[3].y);
         constexpr float kInv = 0.0625f;
-        *reinterpret_cast<float4*>(dst) = make_float4((a.x + b.x) * kInv, (a.y + b.y) * kInv, (a.z + b.z) * kInv, (a.w + b.w) * kInv);
-        *reinterpret_cast<float4*>(dst + 128) = make_float4((a.x - b.x) * kInv, (a.y - b.y) * kInv, (a.z - b.z) * kInv, (a.w - b.w) * kInv);
+        *reinterpret_cast<float2*>(dst) = make_float2((s01.x + s23.x) * kInv, (s01.y + s23.y) * kInv);
+        *reinterpret_cast<float2*>(dst + 64) = make_float2((d01.x + d23.x) * kInv, (d01.y + d23.y) * kInv);
+        *reinterpret_cast<float2*>(dst + 128) = make_float2((s01.x - s23.x) * kInv, (s01.y - s23.y) * kInv);
+        *reinterpret_cast<float2*>(dst + 192) = make_float2((d01.x - d23.x) * kInv, (d01.y - d23.y) * kInv);
       }
     }
   } else if (warp < kIssueWarp) {
@@ -700,23 +719,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) shared_
       auto ready = [&](int bar, uint32_t parity) -> bool {
         return __all_sync(kFull, mbar_wait(bars + 8 * bar, parity, p.wait_ns)) != 0;
       };
-      auto qk_half = [&](int buf, int h) {                 // S[buf]_h = Q_h K_h^T
-        const uint64_t a = dq0 + ((h * 32768) >> 4), b = dk0 + ((buf * kKBuf + h * 8192) >> 4);
-        const uint32_t d = tm + kSBuf * buf + kS1Col * h;
-        if (leader) {
-#pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            mma_pair(d, a + (((kk >> 2) * 16384 + (kk & 3) * 32) >> 4), b + (((kk >> 2) * 4096 + (kk & 3) * 32) >> 4), idS,
-                     kk ? 1u : 0u);
-        }
+      // S[buf]_h += Q_h K_h^T over 16 dims, the two halves in turn.  Such a product takes
+      // about 98 clocks (32 are its work): it reads 4 KB of Q for 64 columns
+      auto qk = [&](int buf, int h, int kk) {
+        const uint32_t off = (kk & 3) * 32;
+        mma_pair(tm + kSBuf * buf + kS1Col * h, dq0 + (((2 * h + (kk >> 2)) * 16384 + off) >> 4),
+                 dk0 + ((buf * kKBuf + (2 * h + (kk >> 2)) * 4096 + off) >> 4), idS, kk ? 1u : 0u);
       };
+      constexpr int kAhead = 2;                            // products of the S1 half that go ahead
       bool ok = true;
       for (int i = 0; i < min(2, n_tiles); ++i) {
         if (!ready(kBarKFull + i, 0)) { ok = false; break; }
         tc_fence_after();
-        qk_half(i, 0);
-        qk_half(i, 1);
-        if (leader) commit_pair(bars + 8 * (kBarSFull + i));
+        if (leader) {
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk) {
+            qk(i, 0, kk);
+            qk(i, 1, kk);
+          }
+          commit_pair(bars + 8 * (kBarSFull + i));
+        }
       }
       for (int i = 0; ok && i < n_tiles; ++i) {
         const int buf = i & 1;
@@ -729,9 +751,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) shared_
         const uint32_t more = i % kChain != 0 ? 1u : 0u;   // O of this chain so far is kept
         const uint32_t pa = tm + kSBuf * buf;
         const uint64_t v1 = dv0 + ((buf * kVBuf) >> 4);
-        auto pv = [&](int kk, uint32_t acc) {              // 16 cells = 8 TMEM columns of fp16 pairs, of half kk / 2
+        auto pv = [&](int kk, uint32_t acc) {              // 16 cells = 8 TMEM columns of fp16 pairs, of part kk
           const uint64_t v = v1 + ((kk * 2048) >> 4);
-          const uint32_t p1 = pa + 32 * (kk >> 1) + 8 * (kk & 1);
+          const uint32_t p1 = pa + 16 * kk;
           mma_pair_ta(tm + kOCol, p1, v, idO, acc);
           mma_pair_ta(tm + kOCol, p1, v + (kVPlane >> 4), idO, 1u);
           mma_pair_ta(tm + kOCol, p1 + kP2Col, v, idO, 1u);
@@ -746,14 +768,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) shared_
           commit_pair(bars + 8 * (kBarODone + buf));
         }
         if (i + 2 < n_tiles) {
-          // QK(i + 2) overwrites P(i) with its S0 half; the S1 half goes ahead
+          // QK(i + 2) overwrites P(i) with its S0 half; the S1 half begins behind PV(i)
           if (!ready(kBarKFull + buf, parity ^ 1) || !ready(kBarMost, i & 1)) { ok = false; break; }
           tc_fence_after();
-          qk_half(buf, 1);
+          if (leader) {
+#pragma unroll
+            for (int kk = 0; kk < kAhead; ++kk) qk(buf, 1, kk);
+          }
           if (!ready(kBarODone + buf, parity)) { ok = false; break; }
           tc_fence_after();
-          qk_half(buf, 0);
-          if (leader) commit_pair(bars + 8 * (kBarSFull + buf));
+          if (leader) {
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk) {
+              qk(buf, 0, kk);
+              if (kk + kAhead < 8) qk(buf, 1, kk + kAhead);
+            }
+            commit_pair(bars + 8 * (kBarSFull + buf));
+          }
         }
       }
       if (!ok) ctl[1] = 1;
@@ -832,7 +863,7 @@ PairSetup pair_setup() {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   s.ok = cudaFuncGetAttributes(&fa, shared_prefix_kernel) == cudaSuccess &&
-         fa.numRegs * 4 >= 2 * kRowRegs + kConvRegs + kIssueRegs &&
+         fa.numRegs * 6 >= 4 * kRowRegs + kConvRegs + kIssueRegs &&
          cudaFuncSetAttribute(shared_prefix_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax) == cudaSuccess &&
          cudaOccupancyMaxActiveClusters(&s.slots, shared_prefix_kernel, &cfg) == cudaSuccess && s.slots > 0;
   if (!s.ok) cudaGetLastError();
@@ -844,10 +875,18 @@ PairSetup pair_setup() {
 SharedPlan plan_shared(const CacheView& C, int n_seqs, int shared_len, int max_seq_len, int num_sms) {
   SharedPlan pl{};
   const int cells = std::min(shared_len, max_seq_len) / 16 * 16;
-  if (!shared_prefix_supported(C) || n_seqs < 2 || cells < kTileN) return pl;
+  if (!shared_prefix_supported(C) || cells < kTileN) return pl;
+  // Worth it where reading the prefix n_seqs times costs more than this kernel does.
+  // Measured at 2 KV heads (64 own cells): the per-sequence decode takes 11 us + 0.23 us
+  // per 1,000 cells of all sequences, this path 22 us + 0.72 us per 1,000 prefix
+  // cells and 32 sequences.  At 8 sequences they meet between 8,192 cells (21.8 us
+  // against 27.4) and 16,384 (34.8 against 32.2), at 32 between 1,024 (19.4, 24.0) and
+  // 2,048 (26.9, 24.4), at 128 below 512 (43.2, 27.1); up to 3 sequences never.
+  const int64_t groups = (n_seqs + kPairSeqs - 1) / kPairSeqs;
+  if (static_cast<int64_t>(C.H) * cells * (23ll * n_seqs - 72ll * groups) <= 2200000ll) return pl;
   pl.cells = cells;
   const int tiles = (cells + kTileN - 1) / kTileN;
-  const int64_t units = static_cast<int64_t>((n_seqs + kPairSeqs - 1) / kPairSeqs) * C.H;
+  const int64_t units = groups * C.H;
   const PairSetup setup = pair_setup();
   const int slots = setup.ok ? setup.slots : std::max(1, num_sms / 2);
   // one pair per two SMs at a time: the split count that minimises waves x (tiles
@@ -865,12 +904,14 @@ SharedPlan plan_shared(const CacheView& C, int n_seqs, int shared_len, int max_s
     }
   }
   pl.splits = (tiles + pl.tiles_per_split - 1) / pl.tiles_per_split;
+  // the running O of each CTA, where a sweep is longer than a chain
+  pl.acc_bytes = pl.tiles_per_split > kChain ? static_cast<size_t>(2 * units * pl.splits) * kRows * 256 * sizeof(float) : 0;
   return pl;
 }
 
 int launch_shared_prefix(const Launch& L, const CacheView& C, const SharedPlan& plan, const void* q, const int32_t* pt,
                          int64_t max_pages, const int32_t* lens, int n_seqs, int max_seq_len, float sm_scale, float* ws,
-                         int ws_splits, bool behind_splits) {
+                         int ws_splits, float* acc, bool behind_splits) {
   SharedParams p;
   p.C = C;
   p.q = static_cast<const uint16_t*>(q);
@@ -885,6 +926,7 @@ int launch_shared_prefix(const Launch& L, const CacheView& C, const SharedPlan& 
   p.ws_splits = ws_splits;
   p.sm_scale_log2 = sm_scale * 1.4426950408889634f;
   p.ws = ws;
+  p.acc = acc;
   p.status = L.status;
   p.wait_ns = wait_limit_ns() ? wait_limit_ns() : kWaitDefaultNs;
   p.page_div = FastDiv(static_cast<uint32_t>(C.P));

@@ -131,6 +131,7 @@ def test_decode_shared_workspace(L):
     d = _desc(n_pages=1 << 20, page_size=64)
     size = L.attn_k8v4_shared_workspace_bytes
     assert size(d, 32, 32768, 34101) > size(d, 16, 32768, 34101) > 0
-    assert size(d, 32, 0, 1000) == L.attn_k8v4_workspace_bytes(d, 32, 1, 1000)
+    for n, shared in ((32, 0), (3, 100000), (8, 4096), (128, 63)):     # the per-sequence decode's
+        assert size(d, n, shared, shared + 1000) == L.attn_k8v4_workspace_bytes(d, n, 1, shared + 1000)
     assert size(_desc(format=k8.FORMAT_Q4), 32, 64, 64) == 0 and size(d, -1, 64, 64) == 0 and size(d, 4, -1, 64) == 0
     assert L.attn_k8v4_decode_shared(d, None, k8.BF16, FAKE, 4, None, 0, 64, 64, 0.0625, None, None, 0, None) == k8.OK

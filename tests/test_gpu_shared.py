@@ -31,12 +31,14 @@ def build(seed, n_seqs, shared, own, P, H=2, with_oracle=True):
     ref = oracle.Cache(n_pages, P, H) if with_oracle else None
     kv = [synth.kv_values(seed, t, 0, shared, H, 3, "bf16") for t in (synth.T_K, synth.T_V)]
     pos = torch.zeros(1, dtype=torch.int64, device="cuda")
-    for b in range(n_seqs if shared % P else 1):    # every copy of the shared cells
-        kd, vd = (dev_tensor(t, (1, shared, H, 256)) for t in kv)
+    for b in range(n_seqs if shared % P else 1):    # the shared cells, and every copy of the page they end in
+        lo = full * P if b else 0
+        part = [t.f32[lo:].reshape(1, shared - lo, H, 256) for t in kv]
+        kd, vd = (torch.from_numpy(np.ascontiguousarray(x)).bfloat16().cuda() for x in part)
         row = pt[b:b + 1]
-        k8.kv_append_k8v4(gpu, torch.from_numpy(row.copy()).cuda(), pos, kd, vd)
+        k8.kv_append_k8v4(gpu, torch.from_numpy(row.copy()).cuda(), pos + lo, kd, vd)
         if ref is not None:
-            ref.append(row, np.array([0]), kv[0].f32.reshape(1, shared, H, 256), kv[1].f32.reshape(1, shared, H, 256))
+            ref.append(row, np.array([lo]), np.ascontiguousarray(part[0]), np.ascontiguousarray(part[1]))
     if own:
         for b in range(n_seqs):
             mine = [synth.kv_values(seed + 1 + b, t, 1, own, H, 3, "bf16") for t in (synth.T_K, synth.T_V)]
@@ -57,13 +59,20 @@ def run(gpu, q, pt, lens, max_len, shared):
     return out
 
 
-@pytest.mark.parametrize("n_seqs,shared,own,P,H", [
-    (2, 64, 0, 64, 2), (3, 128, 5, 16, 1), (5, 1000, 40, 16, 2), (8, 333, 70, 48, 2), (16, 640, 17, 64, 2),
-    (17, 2064, 33, 128, 2), (32, 1531, 100, 64, 2), (33, 777, 1, 16, 3), (70, 700, 30, 64, 2), (4, 64, 200, 32, 2),
-    (6, 79, 3, 64, 2), (9, 15, 100, 16, 2)])
-def test_shared_decode_against_oracle(n_seqs, shared, own, P, H):
+@pytest.mark.parametrize("n_seqs,shared,own,P,H,pair", [
+    # enough sequences and cells for the pair kernel: around 16 and 32 sequences of a CTA and a pair, prefixes that end
+    # inside a tile, a 16-cell group or a page, every page size class, one to eight KV heads
+    (128, 1000, 5, 16, 1, True), (16, 4096, 0, 64, 2, True), (17, 5001, 33, 128, 2, True), (32, 2064, 100, 64, 2, True),
+    (33, 2111, 1, 16, 3, True), (70, 1531, 30, 48, 2, True), (9, 9999, 17, 64, 2, True), (5, 27008, 40, 4096, 2, True),
+    (100, 640, 700, 32, 2, True), (40, 1027, 3, 64, 8, True), (65, 2048, 0, 16, 4, True),
+    # too few for it: the per-sequence decode
+    (2, 64, 0, 64, 2, False), (3, 128, 5, 16, 1, False), (5, 1000, 40, 16, 2, False), (4, 64, 200, 32, 2, False),
+    (9, 15, 100, 16, 2, False), (1, 3000, 9, 64, 2, False), (200, 40, 9, 64, 2, False)])
+def test_shared_decode_against_oracle(n_seqs, shared, own, P, H, pair):
     seed = synth.config_seed(3) + 31 * n_seqs + shared
     gpu, ref, pt = build(seed, n_seqs, shared, own, P, H)
+    assert pair == (k8.attn_k8v4_shared_workspace_bytes(gpu, n_seqs, shared, shared + own)
+                    != k8.attn_k8v4_workspace_bytes(gpu, n_seqs, 1, shared + own))
     rng = np.random.default_rng(seed)
     lens = shared + rng.integers(0, own + 1, n_seqs)
     lens[0] = shared + own
@@ -124,22 +133,46 @@ def test_shared_decode_moving_maxima_and_extreme_queries():
     assert rel_err(got.cpu().numpy().reshape(-1, 256), want) <= TOL
 
 
+@pytest.mark.parametrize("n_seqs,shared", [(40, 24000), (100, 12345)])
+def test_shared_decode_moving_maxima_long(n_seqs, shared):
+    """Scores growing in jumps along a prefix that every CTA pair sweeps for tens of tiles: the reference maxima move
+    inside a chain of tiles, at its end and at its beginning.  Against attn_k8v4_decode (2 TOL)."""
+    P, H = 64, 2
+    rng = np.random.default_rng(n_seqs)
+    n_pages = -(-shared // P)
+    pt = rng.permutation(n_pages).astype(np.int32)[None]
+    gpu = k8.PagedCache(n_pages, P, H)
+    gen = torch.Generator(device="cuda").manual_seed(n_seqs)
+    k = torch.randn(1, shared, H, 256, generator=gen, device="cuda")
+    v = torch.randn(1, shared, H, 256, generator=gen, device="cuda")
+    k *= torch.from_numpy((np.linspace(0.1, 5, shared) * rng.choice([0.1, 0.5, 1.0], shared)).astype(np.float32)).cuda()[None, :, None, None]
+    q = torch.randn(n_seqs, 16, 256, generator=gen, device="cuda").bfloat16()
+    k8.kv_append_k8v4(gpu, torch.from_numpy(pt).cuda(), torch.zeros(1, dtype=torch.int64, device="cuda"), k.bfloat16(), v.bfloat16())
+    ptd = torch.from_numpy(np.repeat(pt, n_seqs, 0)).cuda()
+    lens = rng.integers(shared // 2, shared + 1, n_seqs).astype(np.int32)
+    got = run(gpu, q, ptd, lens, shared, shared)
+    want = torch.empty_like(got)
+    k8.attn_k8v4_decode(gpu, q, ptd, torch.from_numpy(lens).cuda(), shared, want, k8.workspace(gpu, n_seqs, 1, shared))
+    assert k8.k8v4_last_device_status() == 0
+    assert rel_err(got.cpu().numpy(), want.cpu().numpy()) <= 2 * TOL
+
+
 def test_shared_decode_bad_pages_and_lengths():
     """A page id out of range inside the prefix: its cells are skipped and recorded; a length past max_seq_len is
     clipped, one below 0 counts as 0."""
-    n_seqs, shared, P = 20, 640, 16
+    n_seqs, shared, P = 60, 1600, 16
     seed = synth.config_seed(3) + 6
     gpu, ref, pt = build(seed, n_seqs, shared, 0, P)
     q = synth.q_values(seed, 7, n_seqs, 2, "bf16")
     qd = dev_tensor(q, (n_seqs, 16, 256))
     bad = pt.copy()
     bad[:, 2] = gpu.n_pages + 3
-    bad[:, 21] = -1
+    bad[:, 61] = -1
     lens = np.full(n_seqs, shared)
     got = run(gpu, qd, torch.from_numpy(bad).cuda(), lens, shared, shared)
     assert k8.k8v4_last_device_status() == k8.ERANGE
     # the same attention with those cells cut out: a table without the two pages
-    keep = np.delete(pt, [2, 21], 1)
+    keep = np.delete(pt, [2, 61], 1)
     rs, rh, rv = oracle.decode_rows(n_seqs, 16, np.full(n_seqs, shared - 2 * P))
     want = ref.attention(keep, rs, rh, rv, q.f32.reshape(-1, 256))
     assert rel_err(got.cpu().numpy().reshape(-1, 256), want) <= TOL
@@ -177,7 +210,7 @@ def test_shared_decode_wait_timeout_then_recovery():
 
 def test_shared_decode_captured_and_repeatable():
     """Captured and replayed with new queries and lengths in place; equal bits each time and on another stream."""
-    n_seqs, shared, own = 24, 3000, 200
+    n_seqs, shared, own = 24, 4000, 200
     seed = synth.config_seed(3) + 9
     gpu, _, pt = build(seed, n_seqs, shared, own, 64, with_oracle=False)
     q = dev_tensor(synth.q_values(seed, 7, n_seqs, 2, "bf16"), (n_seqs, 16, 256))
