@@ -10,8 +10,8 @@ or PyTorch fallback.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
-import struct
 
 import torch
 
@@ -123,8 +123,8 @@ def _ptr(t: torch.Tensor | None):
 
 
 def _stream(stream) -> int:
-    if stream is None:
-        stream = torch.cuda.current_stream()
+    if stream is None:        # the current device's current stream, without a Stream object for it
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -164,6 +164,7 @@ class PagedCache:
         assert pages.dtype == torch.uint8 and pages.numel() == nbytes and pages.is_contiguous()
         self.pages = pages
         self.desc = k8v4_cache(ctypes.c_void_p(pages.data_ptr()), n_pages, page_size, n_kv_heads, HEAD_DIM, fmt)
+        self.address = ctypes.addressof(self.desc)
 
     def ref(self):
         return ctypes.byref(self.desc)
@@ -183,69 +184,26 @@ def kv_append_k8v4(cache: PagedCache, page_table: torch.Tensor, pos: torch.Tenso
 
 # ---------------------------------------------------------------- around the attention
 # A decode step makes these calls once per layer with kernels of a few
-# microseconds, so what the binding itself does counts: each property of a tensor
-# is asked for once, and no Python object is made for a pointer or a stream.
-_pack_rope = struct.Struct("@Pqii").pack          # k8v4_rope
-_F32, _BF16, _I32, _I64, _U8 = torch.float32, torch.bfloat16, torch.int32, torch.int64, torch.uint8
+# microseconds; csrc/k8v4_binding.cpp checks their tensors (ValueError) and makes the
+# C call with the tensors' device current, on `stream` or that device's current stream.
+_binding = None
 
 
-def _bad(what: str) -> None:
-    raise ValueError(what)
-
-
-def _token_stride(x: torch.Tensor, heads: int, what: str) -> int:
-    """Elements between the tokens of x [n_seqs, n_tok, heads, 256]; heads are
-    contiguous, tokens evenly spaced over the sequences (a slice of a packed
-    projection qualifies)."""
-    n_seqs, n_tok, h, d = x.shape if x.dim() == 4 else _bad(f"{what}: [n_seqs, n_tok, heads, 256] expected")
-    s0, s1, s2, s3 = x.stride()
-    if h != heads or d != HEAD_DIM:
-        _bad(f"{what}: [n_seqs, n_tok, {heads}, 256] expected")
-    if heads and (s3 != 1 or (heads != 1 and s2 != HEAD_DIM)):
-        _bad(f"{what}: heads must be contiguous")
-    if n_tok <= 1:
-        return s0 if n_seqs > 1 else heads * HEAD_DIM
-    if n_seqs > 1 and s0 != n_tok * s1:
-        _bad(f"{what}: tokens must be evenly spaced")
-    return s1
-
-
-def _rope(table: torch.Tensor, interleaved: bool) -> bytes:
-    """The k8v4_rope descriptor of a table, as the bytes of the C struct."""
-    if table.dtype is not _F32 or table.dim() != 2 or not table.is_contiguous():
-        _bad("rope_table: contiguous float32 [n_pos, rot_dim] expected")
-    n_pos, rot = table.shape
-    return _pack_rope(table.data_ptr(), n_pos, rot, 1 if interleaved else 0)
-
-
-def _weight(w: torch.Tensor | None, dev: int, what: str):
-    if w is None:
-        return None
-    if w.dtype is not _F32 or w.shape != (HEAD_DIM,) or not w.is_contiguous() or w.get_device() != dev:
-        _bad(f"{what}: contiguous float32 [256] on the tensors' device expected")
-    return w.data_ptr()
-
-
-def _vector(x: torch.Tensor, n: int, dtype: torch.dtype, dev: int, what: str) -> int:
-    """The address of a contiguous vector (or array) of n elements."""
-    if x.dtype is not dtype or x.numel() != n or not x.is_contiguous() or x.get_device() != dev:
-        _bad(f"{what}: {n} contiguous {dtype} on the tensors' device expected")
-    return x.data_ptr()
-
-
-def _on(dev: int, stream, name: str, *args) -> None:
-    """Call a library function with the tensors' device current, on `stream` or that
-    device's current stream; raises what it returns."""
-    fn = getattr(_lib or lib(), name)
-    if dev < 0:
-        rc = fn(*args, _stream(stream) if stream is not None else None)
-    elif torch._C._cuda_getDevice() == dev:
-        rc = fn(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream))
-    else:
-        with torch.cuda.device(dev):
-            rc = fn(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream))
-    if rc:
-        raise K8V4Error(rc, name)
+def _native():
+    """The loaded extension module (raises if it has not been built)."""
+    global _binding
+    if _binding is None:
+        L = lib()
+        path = os.path.join(HERE, "_build", "_k8v4_binding.so")
+        if not os.path.exists(path):
+            raise RuntimeError(f"{path} is not built; call quantized_paged_kv_q8_gb300.build()")
+        spec = importlib.util.spec_from_file_location("_k8v4_binding", path)
+        m = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(m)
+        m.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in
+                 (L.qk_norm_rope_k8v4, L.kv_append_k8v4_rope, L.spec_accept_k8v4, L.attn_k8v4_decode_shared)))
+        _binding = m
+    return _binding
 
 
 def qk_norm_rope_k8v4(q: torch.Tensor, k: torch.Tensor | None, pos: torch.Tensor, rope_table: torch.Tensor,
@@ -253,29 +211,13 @@ def qk_norm_rope_k8v4(q: torch.Tensor, k: torch.Tensor | None, pos: torch.Tensor
                       k_weight: torch.Tensor | None = None, eps: float = 1e-6, interleaved: bool = False,
                       stream=None) -> None:
     """Per-head RMS norm (with a weight) and position rotation of q [n_seqs, n_tok, HQ, 256]
-    and k [n_seqs, n_tok, H, 256] (or None) into contiguous q_out, k_out.  pos int64 [n_seqs];
+    and k [n_seqs, n_tok, H, 256] (or None) into contiguous q_out, k_out; both may be slices of
+    a packed projection.  pos int64 [n_seqs]: token t of sequence b is at pos[b] + t;
     rope_table float32 [n_pos, rot_dim]: cosines, then sines, of each position."""
-    n_seqs, n_tok, n_q, _ = shape = q.shape if q.dim() == 4 else _bad("q: [n_seqs, n_tok, heads, 256] expected")
-    dev, dtype = q.get_device(), q.dtype
-    q_stride = _token_stride(q, n_q, "q")
-    if q_out.shape != shape or q_out.dtype is not dtype or not q_out.is_contiguous() or q_out.get_device() != dev:
-        _bad("q_out: contiguous, like q")
-    n_k, k_stride, kp, kop = 0, 0, None, None
-    if k is not None:
-        kshape = k.shape if k.dim() == 4 else _bad("k: [n_seqs, n_tok, heads, 256] expected")
-        n_k = kshape[2]
-        k_stride = _token_stride(k, n_k, "k")
-        if kshape[0] != n_seqs or kshape[1] != n_tok or k.dtype is not dtype or k.get_device() != dev:
-            _bad("k: same dtype, device and tokens as q")
-        if (k_out is None or k_out.shape != kshape or k_out.dtype is not dtype or not k_out.is_contiguous()
-                or k_out.get_device() != dev):
-            _bad("k_out: contiguous, like k")
-        kp, kop = k.data_ptr(), k_out.data_ptr()
-    if rope_table.get_device() != dev:
-        _bad("rope_table: on another device")
-    _on(dev, stream, "qk_norm_rope_k8v4", q.data_ptr(), q_stride, n_q, kp, k_stride, n_k, _dtype(q),
-        _weight(q_weight, dev, "q_weight"), _weight(k_weight, dev, "k_weight"), eps,
-        _vector(pos, n_seqs, _I64, dev, "pos"), n_seqs, n_tok, _rope(rope_table, interleaved), q_out.data_ptr(), kop)
+    rc = (_binding or _native()).norm_rope(q, k, pos, rope_table, q_out, k_out, q_weight, k_weight, eps, interleaved,
+                                           stream if stream is None else _stream(stream))
+    if rc:
+        raise K8V4Error(rc, "qk_norm_rope_k8v4")
 
 
 def attn_k8v4_shared_workspace_bytes(cache: PagedCache, n_seqs: int, shared_len: int, max_seq_len: int) -> int:
@@ -293,16 +235,10 @@ def attn_k8v4_decode_shared(cache: PagedCache, q: torch.Tensor, page_table: torc
     """attn_k8v4_decode for a batch whose first shared_len cells are the same in every
     sequence, read once for all of them.  q: bf16 [n_seqs, 8H, 256]; page_table int32
     [n_seqs, max_pages]; seq_lens int32 [n_seqs]; out float32 like q."""
-    shape, dev = q.shape, q.get_device()
-    n_seqs = shape[0] if len(shape) == 3 else _bad("q: [n_seqs, 8H, 256] expected")
-    rows = GQA * cache.n_kv_heads
-    if shape[1] != rows or shape[2] != HEAD_DIM or not q.is_contiguous() or cache.pages.get_device() != dev:
-        _bad("q: contiguous [n_seqs, 8H, 256] on the cache's device")
-    pages = page_table.shape[1] if page_table.dim() == 2 else _bad("page_table: [n_seqs, max_pages] expected")
-    _on(dev, stream, "attn_k8v4_decode_shared", cache.ref(), q.data_ptr(), _dtype(q),
-        _vector(page_table, n_seqs * pages, _I32, dev, "page_table"), pages,
-        _vector(seq_lens, n_seqs, _I32, dev, "seq_lens"), n_seqs, max_seq_len, shared_len, sm_scale,
-        _vector(out, n_seqs * rows * HEAD_DIM, _F32, dev, "out"), _vector(ws, ws.numel(), _U8, dev, "ws"), ws.numel())
+    rc = (_binding or _native()).decode_shared(cache.address, cache.pages, q, page_table, seq_lens, max_seq_len,
+                                               shared_len, out, ws, sm_scale, stream if stream is None else _stream(stream))
+    if rc:
+        raise K8V4Error(rc, "attn_k8v4_decode_shared")
     return out
 
 
@@ -311,17 +247,10 @@ def kv_append_k8v4_rope(cache: PagedCache, page_table: torch.Tensor, pos: torch.
                         eps: float = 1e-6, interleaved: bool = False, stream=None) -> None:
     """kv_append_k8v4 with k normed (with a weight) and rotated to its cell's position on the
     way.  k, v: [n_seqs, n_tok, H, 256], possibly slices of a packed projection."""
-    n_seqs, n_tok = (shape := k.shape)[:2]
-    dev, h = k.get_device(), cache.n_kv_heads
-    if v.shape != shape or v.dtype is not k.dtype or v.get_device() != dev or cache.pages.get_device() != dev:
-        _bad("k and v: same shape, dtype and device, the cache's")
-    pages = page_table.shape[1] if page_table.dim() == 2 else _bad("page_table: [n_seqs, max_pages] expected")
-    if rope_table.get_device() != dev:
-        _bad("rope_table: on another device")
-    _on(dev, stream, "kv_append_k8v4_rope", cache.ref(), _vector(page_table, n_seqs * pages, _I32, dev, "page_table"),
-        pages, n_seqs, _vector(pos, n_seqs, _I64, dev, "pos"), n_tok, k.data_ptr(), _token_stride(k, h, "k"),
-        v.data_ptr(), _token_stride(v, h, "v"), _dtype(k), _weight(k_weight, dev, "k_weight"), eps,
-        _rope(rope_table, interleaved))
+    rc = (_binding or _native()).append_rope(cache.address, cache.pages, page_table, pos, k, v, rope_table, k_weight,
+                                             eps, interleaved, stream if stream is None else _stream(stream))
+    if rc:
+        raise K8V4Error(rc, "kv_append_k8v4_rope")
 
 
 def spec_accept_k8v4(target_probs: torch.Tensor, draft_probs: torch.Tensor | None, draft_tokens: torch.Tensor,
@@ -331,20 +260,10 @@ def spec_accept_k8v4(target_probs: torch.Tensor, draft_probs: torch.Tensor | Non
     [n_seqs, n, vocab] or None (certain drafts), draft_tokens int32 [n_seqs, n], u_accept
     float32 [n_seqs, n], u_sample float32 [n_seqs] -> tokens int32 [n_seqs, n + 1] (accepted
     drafts, the drawn token, then -1), n_accepted int32 [n_seqs]."""
-    b, n1, vocab = target_probs.shape if target_probs.dim() == 3 else _bad("target_probs: [n_seqs, n + 1, vocab] expected")
-    n, dev = n1 - 1, target_probs.get_device()
-    if not target_probs.is_contiguous():
-        _bad("target_probs: contiguous [n_seqs, n + 1, vocab] expected")
-    if draft_probs is not None and draft_probs.shape != (b, n, vocab):
-        _bad("draft_probs: [n_seqs, n, vocab] expected")
-    if draft_tokens.shape != (b, n) or tokens.shape != (b, n1):
-        _bad("draft_tokens: [n_seqs, n], tokens: [n_seqs, n + 1] expected")
-    _on(dev, stream, "spec_accept_k8v4", target_probs.data_ptr(),
-        None if draft_probs is None else _vector(draft_probs, b * n * vocab, target_probs.dtype, dev, "draft_probs"),
-        _dtype(target_probs), _vector(draft_tokens, b * n, _I32, dev, "draft_tokens"),
-        None if n_drafts is None else _vector(n_drafts, b, _I32, dev, "n_drafts"),
-        _vector(u_accept, b * n, _F32, dev, "u_accept"), _vector(u_sample, b, _F32, dev, "u_sample"), b, n, vocab,
-        _vector(tokens, b * n1, _I32, dev, "tokens"), _vector(n_accepted, b, _I32, dev, "n_accepted"))
+    rc = (_binding or _native()).accept(target_probs, draft_probs, draft_tokens, u_accept, u_sample, tokens,
+                                        n_accepted, n_drafts, stream if stream is None else _stream(stream))
+    if rc:
+        raise K8V4Error(rc, "spec_accept_k8v4")
 
 
 def attn_k8v4_workspace_bytes(cache: PagedCache, n_seqs: int, n_q: int, max_seq_len: int) -> int:

@@ -87,28 +87,66 @@ def test_accept_refuses(L, bad, code):
 
 
 def test_binding_checks_its_tensors(L):
-    """Shapes, types and spacing are checked before the library is called (CPU tensors suffice)."""
+    """Shapes, types, spacing and devices are checked before the library is called (CPU tensors suffice: the last
+    check refuses them)."""
     q = torch.zeros(2, 3, 16, 256, dtype=torch.bfloat16)
     pos = torch.zeros(2, dtype=torch.int64)
     tab = torch.zeros(8, 64)
-    with pytest.raises(ValueError):
-        k8.qk_norm_rope_k8v4(q[:, :, :, :128], None, pos, tab, q, None)
-    with pytest.raises(ValueError):
-        k8.qk_norm_rope_k8v4(q.transpose(0, 1), None, torch.zeros(3, dtype=torch.int64), tab, q.transpose(0, 1).contiguous(), None)
-    with pytest.raises(ValueError):
-        k8.qk_norm_rope_k8v4(q, None, pos, tab, q[:, :2], None)
-    with pytest.raises(ValueError):
-        k8.qk_norm_rope_k8v4(q, None, pos.int(), tab, torch.empty_like(q), None)
-    with pytest.raises(ValueError):
-        k8.qk_norm_rope_k8v4(q, None, pos, tab.double(), torch.empty_like(q), None)
-    with pytest.raises(ValueError):
-        k8.spec_accept_k8v4(torch.zeros(2, 3, 50), torch.zeros(2, 2, 49), torch.zeros(2, 2, dtype=torch.int32),
-                            torch.zeros(2, 2), torch.zeros(2), torch.zeros(2, 3, dtype=torch.int32), torch.zeros(2, dtype=torch.int32))
-    # tokens of several sequences in one packed buffer are evenly spaced, a sequence-strided slice is not
+
+    def norm_rope(match, q=q, k=None, pos=pos, tab=tab, qo=None, ko=None, **kw):
+        with pytest.raises(ValueError, match=match):
+            k8.qk_norm_rope_k8v4(q, k, pos, tab, torch.empty(q.shape, dtype=q.dtype) if qo is None else qo, ko, **kw)
+
+    norm_rope("256", q=q[:, :, :, :128])
+    norm_rope("n_tok", q=q[0])
+    norm_rope("bfloat16", q=q.half())
+    norm_rope("heads must be contiguous", q=q[:, :, ::2])
+    norm_rope("evenly spaced", q=q[:, :2])
+    norm_rope("shape of q", qo=q[:, :2])
+    norm_rope("q_out", qo=torch.empty(2, 16, 3, 256, dtype=q.dtype).transpose(1, 2))
+    norm_rope("q_out", qo=torch.empty(q.shape))
+    norm_rope("pos", pos=pos.int())
+    norm_rope("pos", pos=pos[:1])
+    norm_rope("rope_table", tab=tab.double())
+    norm_rope("rope_table", tab=tab[:, ::2])
+    norm_rope("tokens of q", k=q[:, :2], ko=q[:, :2])
+    norm_rope("k_out", k=q, ko=q[:, :2])
+    norm_rope("q_weight", q_weight=torch.zeros(255))
+    norm_rope("k_weight", k_weight=torch.zeros(256, dtype=torch.bfloat16))
+    with pytest.raises(ValueError, match="q: a tensor"):
+        k8.qk_norm_rope_k8v4(None, None, pos, tab, q, None)
+    # heads of a packed projection's tokens are fine: what is left to refuse is the CPU
     packed = torch.zeros(2, 3, 20, 256)
-    assert k8._token_stride(packed[:, :, 16:18], 2, "k") == 20 * 256
-    with pytest.raises(ValueError):
-        k8._token_stride(packed[:, :2, 16:18], 2, "k")
+    norm_rope("CUDA tensors", q=packed[:, :, :16], k=packed[:, :, 16:18], ko=torch.empty(2, 3, 2, 256))
+
+    cache = k8.PagedCache(4, 16, device="cpu")
+    kv, pt = torch.zeros(2, 3, 2, 256), torch.zeros(2, 4, dtype=torch.int32)
+    for match, args in (("one shape", (pt, pos, kv, kv[:1], tab)), (r"\[n_seqs, n_tok, 2, 256\]", (pt, pos, kv[:, :, :1], kv[:, :, :1], tab)),
+                        ("page_table", (pt[:1], pos, kv, kv, tab)), ("page_table", (pt.long(), pos, kv, kv, tab)),
+                        ("pos", (pt, pos[:1], kv, kv, tab)), ("rope_table", (pt, pos, kv, kv, tab.half())),
+                        ("CUDA tensors", (pt, pos, kv, kv, tab))):
+        with pytest.raises(ValueError, match=match):
+            k8.kv_append_k8v4_rope(cache, *args)
+
+    q1, out, lens, ws = torch.zeros(2, 16, 256), torch.zeros(2, 16, 256), torch.zeros(2, dtype=torch.int32), torch.zeros(512, dtype=torch.uint8)
+    for match, args in (("q:", (q1[:, :8], pt, lens, 64, 64, out, ws)), ("page_table", (q1, pt[:1], lens, 64, 64, out, ws)),
+                        ("seq_lens", (q1, pt, lens.long(), 64, 64, out, ws)), ("out", (q1, pt, lens, 64, 64, out[:1], ws)),
+                        ("ws", (q1, pt, lens, 64, 64, out, ws.float())), ("max_seq_len", (q1, pt, lens, -1, 64, out, ws)),
+                        ("CUDA tensors", (q1, pt, lens, 64, 64, out, ws))):
+        with pytest.raises(ValueError, match=match):
+            k8.attn_k8v4_decode_shared(cache, *args)
+
+    p, d, tok = torch.zeros(2, 3, 50), torch.zeros(2, 2, 50), torch.zeros(2, 2, dtype=torch.int32)
+    u, us, o, acc = torch.zeros(2, 2), torch.zeros(2), torch.zeros(2, 3, dtype=torch.int32), torch.zeros(2, dtype=torch.int32)
+    for match, args in (("target_probs", (p[0], d, tok, u, us, o, acc)), ("draft_probs", (p, d[:, :, :49], tok, u, us, o, acc)),
+                        ("draft_probs", (p, d.bfloat16(), tok, u, us, o, acc)), ("draft_tokens", (p, d, tok.long(), u, us, o, acc)),
+                        ("u_accept", (p, d, tok, u.double(), us, o, acc)), ("u_sample", (p, d, tok, u, us[:1], o, acc)),
+                        ("tokens", (p, d, tok, u, us, o[:, :2], acc)), ("n_accepted", (p, d, tok, u, us, o, acc.long())),
+                        ("CUDA tensors", (p, d, tok, u, us, o, acc))):
+        with pytest.raises(ValueError, match=match):
+            k8.spec_accept_k8v4(*args)
+    with pytest.raises(ValueError, match="n_drafts"):
+        k8.spec_accept_k8v4(p, d, tok, u, us, o, acc, n_drafts=acc.long())
 
 
 @pytest.mark.parametrize("bad,code", [

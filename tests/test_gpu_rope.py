@@ -2,6 +2,7 @@
 pairings, partial rotation, strided tokens, norms, far positions, odd sizes, the
 positions and pages that are refused, and the equality of the rotating append
 with the rotation followed by the plain append (bytes)."""
+import ctypes
 import functools
 
 import numpy as np
@@ -99,7 +100,7 @@ def test_norm_rope_refuses_overlapping_in_place():
     parts, _ = case(1, 1, 3, [16, 2], "bf16", True)
     pos = torch.zeros(1, dtype=torch.int64, device="cuda")
     table = torch.from_numpy(table_of(64, 128)).cuda()
-    r = k8._rope(table, False)
+    r = ctypes.byref(k8.k8v4_rope(table.data_ptr(), 64, 128, 0))
     rc = k8.lib().qk_norm_rope_k8v4(k8._ptr(parts[0]), 18 * 256, 16, None, 0, 0, k8.BF16, None, None, 0.0, k8._ptr(pos),
                                     1, 3, r, k8._ptr(parts[0]), None, k8._stream(None))
     assert rc == k8.EINVAL
