@@ -81,10 +81,11 @@ __global__ void __launch_bounds__(kWarps * 32) append_rope_kernel(const AppendRo
       float wt[8];
       load_weight8(p.k_weight, lane, wt);
       rms_row(x, wt, p.eps);
-      rope_row<INTER, false>(x, rl, f);
-    } else {
-      rope_row<INTER, true>(x, rl, f);
     }
+    float o[8];
+    rope_partners<INTER>(x, rl, o);
+    if (p.k_weight) rope_row<INTER, false>(x, o, rl, f);
+    else rope_row<INTER, true>(x, o, rl, f);
     if (BF16) bf16x8_to_f32(f32x8_to_bf16(x), x);           // rounded to K's type
     if (FMT == K8V4_FORMAT_Q4) {
       rotate_exact(x, lane, ts);
@@ -173,7 +174,10 @@ __global__ void __launch_bounds__(kWarps * 32, kBulkCtas) append_rope_bf16_kerne
         load_weight8(p.k_weight, lane, wt);
         rms_row(x, wt, p.eps);
       }
-      rope_row<INTER, !NORM>(x, rl, f);
+      float o[8];
+      if (NORM) rope_partners<INTER>(x, rl, o);
+      else rope_partners<INTER>(kc, rl, o);
+      rope_row<INTER, !NORM>(x, o, rl, f);
       krot = f32x8_to_bf16(x);
     }
     const bool ok = in_range && base != nullptr;

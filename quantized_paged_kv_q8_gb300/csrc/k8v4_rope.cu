@@ -94,18 +94,22 @@ __global__ void __launch_bounds__(kRopeWarps * 32, 4) norm_rope_kernel(const Rop
       x[0] = __uint_as_float(a.x); x[1] = __uint_as_float(a.y); x[2] = __uint_as_float(a.z); x[3] = __uint_as_float(a.w);
       x[4] = __uint_as_float(c.x); x[5] = __uint_as_float(c.y); x[6] = __uint_as_float(c.z); x[7] = __uint_as_float(c.w);
     }
+    float o[8];
     if (weight) {                                           // the same for the warp
       rms_row(x, wt, p.eps);
-      rope_row<INTER, false>(x, rl, f);
+      rope_partners<INTER>(x, rl, o);
+      rope_row<INTER, false>(x, o, rl, f);
     } else {
-      rope_row<INTER, true>(x, rl, f);
+      if (BF16) rope_partners<INTER>(raw[i][0], rl, o);
+      else rope_partners<INTER>(x, rl, o);
+      rope_row<INTER, true>(x, o, rl, f);
     }
     if (BF16) {
       reinterpret_cast<uint4*>(static_cast<uint16_t*>(dst) + out0 + i * kD)[lane] = f32x8_to_bf16(x);
     } else {
-      float4* o = reinterpret_cast<float4*>(static_cast<float*>(dst) + out0 + i * kD) + 2 * lane;
-      o[0] = make_float4(x[0], x[1], x[2], x[3]);
-      o[1] = make_float4(x[4], x[5], x[6], x[7]);
+      float4* to = reinterpret_cast<float4*>(static_cast<float*>(dst) + out0 + i * kD) + 2 * lane;
+      to[0] = make_float4(x[0], x[1], x[2], x[3]);
+      to[1] = make_float4(x[4], x[5], x[6], x[7]);
     }
   }
 }

@@ -87,13 +87,13 @@ __device__ __forceinline__ void rope_load(const float* __restrict__ row, const R
   }
 }
 
-// Rotate the row in place (all lanes call; lanes past rot_dim keep their values)
+// Rotate the row in place (all lanes call; lanes past rot_dim keep their values).
+// o: the partners' values (split pairs; adjacent ones are the lane's own).
 template <bool INTER, bool CARRIED>
-__device__ __forceinline__ void rope_row(float x[8], const RopeLane& rl, const RopeFactors<INTER>& f) {
-  constexpr unsigned kAll = 0xffffffffu;
-  auto dot2 = [](float2 v, float2 c, float2 o, float2 s) { return CARRIED ? dot2_carried(v, c, o, s) : dot2_plain(v, c, o, s); };
+__device__ __forceinline__ void rope_row(float x[8], const float o[8], const RopeLane& rl, const RopeFactors<INTER>& f) {
+  auto dot2 = [](float2 v, float2 c, float2 w, float2 s) { return CARRIED ? dot2_carried(v, c, w, s) : dot2_plain(v, c, w, s); };
+  if (!rl.on) return;
   if (INTER) {
-    if (!rl.on) return;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const float2 v = make_float2(x[2 * i], x[2 * i + 1]);
@@ -102,17 +102,29 @@ __device__ __forceinline__ void rope_row(float x[8], const RopeLane& rl, const R
       x[2 * i + 1] = y.y;
     }
   } else {
-    float o[8];
-#pragma unroll
-    for (int r = 0; r < 8; ++r) o[r] = __shfl_sync(kAll, x[r], rl.partner);
-    if (!rl.on) return;
 #pragma unroll
     for (int r = 0; r < 8; r += 2) {
-      const float2 y = dot2(make_float2(x[r], x[r + 1]), make_float2(f.c[r], f.c[r + 1]),
-                                    make_float2(o[r], o[r + 1]), make_float2(f.s[r], f.s[r + 1]));
+      const float2 y = dot2(make_float2(x[r], x[r + 1]), make_float2(f.c[r], f.c[r + 1]), make_float2(o[r], o[r + 1]),
+                            make_float2(f.s[r], f.s[r + 1]));
       x[r] = y.x;
       x[r + 1] = y.y;
     }
+  }
+}
+// the partners of split pairs: by value, or (bf16 rows as they were loaded) two to a word
+template <bool INTER>
+__device__ __forceinline__ void rope_partners(const float x[8], const RopeLane& rl, float o[8]) {
+#pragma unroll
+  for (int r = 0; r < 8; ++r) o[r] = INTER ? 0.0f : __shfl_sync(0xffffffffu, x[r], rl.partner);
+}
+template <bool INTER>
+__device__ __forceinline__ void rope_partners(const uint4& raw, const RopeLane& rl, float o[8]) {
+  const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t y = INTER ? 0u : __shfl_sync(0xffffffffu, w[i], rl.partner);
+    o[2 * i] = __uint_as_float(y << 16);
+    o[2 * i + 1] = __uint_as_float(y & 0xffff0000u);
   }
 }
 
