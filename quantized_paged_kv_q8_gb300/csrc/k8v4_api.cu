@@ -315,7 +315,7 @@ static SharedPlan shared_plans(const CacheView& C, int n_seqs, int shared_len, i
   const SharedPlan pre = plan_shared(C, n_seqs, shared_len, max_seq_len, sms);
   *own = AttendPlan{};
   if (pre.cells == 0) *own = plan_attend(C, n_seqs, 1, max_seq_len, sms);
-  else if (max_seq_len > pre.cells) *own = plan_decode_splits(C, n_seqs, max_seq_len - pre.cells, sms);
+  else if (max_seq_len > pre.cells) *own = plan_decode(C, n_seqs, max_seq_len - pre.cells, sms);
   return pre;
 }
 static size_t shared_rows_bytes(const CacheView& C, const SharedPlan& pre, const AttendPlan& own, int n_seqs) {

@@ -183,11 +183,9 @@ SharedPlan plan_shared(const CacheView& C, int n_seqs, int shared_len, int max_s
 int launch_shared_prefix(const Launch& L, const CacheView& C, const SharedPlan& plan, const void* q, const int32_t* pt,
                          int64_t max_pages, const int32_t* lens, int n_seqs, int max_seq_len, float sm_scale, float* ws,
                          int ws_splits, float* acc, bool behind_splits);
-// the plan of launch_decode_splits over `cells` cells: short ranges of many
-// sequences in small CTAs (pl.warps workers)
-AttendPlan plan_decode_splits(const CacheView& C, int n_seqs, int cells, int num_sms);
 // the cells from cell_begin on of every sequence as split partials (no merge):
-// splits first_split .. of [n_seqs][ws_splits][8 H][260]
+// splits first_split .. of [n_seqs][ws_splits][8 H][260]; the plan is plan_decode
+// over those cells
 int launch_decode_splits(const Launch& L, const CacheView& C, const AttendPlan& plan, const void* q, int q_dtype,
                          const int32_t* pt, int64_t max_pages, const int32_t* steps, int n_seqs, int max_seq_len,
                          int cell_begin, float sm_scale, float* ws, int ws_splits, int first_split, uint32_t wait_ns);

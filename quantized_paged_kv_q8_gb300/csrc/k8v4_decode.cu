@@ -106,7 +106,6 @@ struct DecodeParams {
   int64_t max_pages;
   const int32_t* steps;
   int max_seq_len, cells_per_split, splits;
-  int workers;                // worker warps of a CTA at most
   int ws_splits;              // partial rows per sequence in ws (the splits, or more where others write theirs beside them)
   int cell_base, cell_limit;  // the cell range the splits cover: [cell_base, cell_limit)
   float sm_scale_log2;
@@ -1407,7 +1406,7 @@ enum class Join { kFinal, kPartial, kNone };
 
 template <int FMT, bool QF32>
 int launch_impl(const Launch& L, DecodeParams p, int n_seqs, float* out, Join join) {
-  p.L = layout_of(FMT, p.C.H, std::min(p.workers, QF32 ? kMaxWorkersF32 : kMaxWorkers));
+  p.L = layout_of(FMT, p.C.H, QF32 ? kMaxWorkersF32 : kMaxWorkers);
   CUtensorMap mk, mv;
   if (!maps_of(p.C, &mk, &mv)) return K8V4_ECUDA;
   auto kern = decode_kernel<FMT, QF32>;
@@ -1487,7 +1486,6 @@ DecodeParams params_of(const Launch& L, const CacheView& C, const AttendPlan& pl
   p.cells_per_split = plan.cells_per_split;
   p.splits = plan.splits;
   p.ws_splits = plan.splits;
-  p.workers = plan.warps;
   p.cell_base = 0;
   p.cell_limit = max_seq_len;
   p.sm_scale_log2 = sm_scale * 1.4426950408889634f;
@@ -1554,34 +1552,6 @@ int launch_decode_partial(const Launch& L, const CacheView& C, const AttendPlan&
   p.cell_base = cell_begin;
   p.cell_limit = cell_end;
   return dispatch(L, p, C.fmt, q_dtype == K8V4_F32, n_seqs, partial, Join::kPartial);
-}
-
-AttendPlan plan_decode_splits(const CacheView& C, int n_seqs, int cells, int num_sms) {
-  AttendPlan pl = plan_decode(C, n_seqs, cells, num_sms);
-  // A CTA of 12 workers fills an SM, and its fixed cost (q set-up, pipeline fill,
-  // merge: about four rounds of its workers' tiles) leaves the SM idle; with 6, 4
-  // or 3 workers two to four CTAs share the SM and overlap theirs.  Per worker
-  // count and split count: waves x (rounds + 4).  128 sequences of up to 512 cells
-  // (256 CTAs): two waves of 12-worker CTAs 31 us, one of 6-worker CTAs 19 us.
-  const int tiles = std::max(1, (cells + 15) / 16);
-  const int64_t pairs = static_cast<int64_t>(C.H) * n_seqs;
-  int64_t best = INT64_MAX;
-  for (int w : {12, 6, 4, 3}) {
-    const int slots = num_sms * (kMaxWorkers / w);
-    for (int sp = 1; sp <= std::max(1, std::min(64, tiles / w)); ++sp) {
-      const int64_t waves = (pairs * sp + slots - 1) / slots;
-      const int64_t cost = waves * (((tiles + sp - 1) / sp + w - 1) / w + 4);
-      if (cost < best) {
-        best = cost;
-        const int tps = (tiles + sp - 1) / sp;
-        pl.warps = w;
-        pl.cells_per_split = 16 * tps;
-        pl.splits = (tiles + tps - 1) / tps;
-      }
-    }
-  }
-  pl.ws_bytes = static_cast<size_t>(n_seqs) * pl.splits * C.H * kGqa * kPStride * sizeof(float);
-  return pl;
 }
 
 int launch_decode_splits(const Launch& L, const CacheView& C, const AttendPlan& plan, const void* q, int q_dtype,
