@@ -150,10 +150,11 @@ int kv_append_k8v4(const k8v4_cache* cache, const int32_t* page_table, int64_t m
  *
  * Rotation: a pair (x1, x2) at position t becomes
  *   (x1 c - x2 s, x2 c + x1 s),  c and s the pair's entries of table row t;
- * each result is the exact value rounded to fp32, then to the row's type (the
- * errors of the products and of their sum are carried).  Norm, where a weight w
- * is given: x -> x / sqrt(mean(x^2) + eps) * w over the head's 256 elements, in
- * fp32, ahead of the rotation (|x| < 2^60 there).  Inputs are finite. */
+ * each result is the exact value rounded to fp32 (the errors of the products and
+ * of their sum are carried), then to the row's type.  Norm, where a weight w is
+ * given: x -> x / sqrt(mean(x^2) + eps) * w over the head's 256 elements, in
+ * fp32, ahead of the rotation (|x| < 2^60 there), which then rounds one product
+ * and fuses the other.  Inputs are finite. */
 
 /* Norm (optional) and rotation of every query and key head, one pass.
  *   q, k:     [n_seqs][n_tok] tokens of n_q_heads (n_k_heads) heads x 256 of
@@ -269,14 +270,18 @@ size_t attn_k8v4_shared_workspace_bytes(const k8v4_cache* cache, int32_t n_seqs,
  * attn_k8v4_decode, with the shared cells read once for the batch.
  *   shared_len: host-side number of leading cells that are the same for every
  *             sequence, >= 0 (it may exceed max_seq_len).  Every sequence's page-table
- *             row names these cells (same pages, or pages with the same
- *             bytes); which rows the shared cells are read through is the library's
- *             choice.
+ *             row names these cells, up to the longest seq_lens (same pages, or
+ *             pages with the same bytes); which rows the shared cells are read
+ *             through is the library's choice.  Their stored scales are finite
+ *             (those of appended values up to 32,000 are).
  *   seq_lens: may be shorter than shared_len (such a row sees its own first
  *             seq_lens[b] cells), or 0 (zero output).
  *   workspace: >= attn_k8v4_shared_workspace_bytes(cache, n_seqs, shared_len,
  *             max_seq_len) bytes, 256-byte aligned.
- * Other arguments as attn_k8v4_decode.  K8V4 format, bf16 q. */
+ * Other arguments as attn_k8v4_decode, in device memory.  K8V4 format, bf16 q.
+ * Where the prefix is short or the sequences few, the call is attn_k8v4_decode;
+ * else results agree with it to the attention's 2e-5 and are the same bits from
+ * call to call. */
 int attn_k8v4_decode_shared(const k8v4_cache* cache, const void* q, int32_t q_dtype, const int32_t* page_table,
                             int64_t max_pages, const int32_t* seq_lens, int32_t n_seqs, int32_t max_seq_len,
                             int32_t shared_len, float sm_scale, float* out, void* workspace, size_t workspace_bytes,

@@ -132,7 +132,8 @@ __device__ __forceinline__ uint32_t map_to(uint32_t saddr, uint32_t rank) {
 // The arrivals that hand operand tiles to the products carry no wider release than
 // the CTA's: what the tensor core reads is made visible by the proxy and tcgen05
 // fences ahead of them, and a cluster-wide release would also wait for the
-// global loads of the next tile (measured: 723 us against the figure at the top).
+// global loads of the next tile (32 sequences on 32,768 cells: 107 us with it, 92
+// without, when those were loads by thread).
 __device__ __forceinline__ void arrive_cluster(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
@@ -263,7 +264,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) shared_
   const int groups = (p.n_seqs + kPairSeqs - 1) / kPairSeqs;
   const int unit = blockIdx.x >> 1;
   const int split = unit / groups;
-  const int seq0 = (unit - split * groups) * kPairSeqs + static_cast<int>(rank) * (kRows / kGqa);   // this CTA's first sequence
+  const int pair_seq0 = (unit - split * groups) * kPairSeqs;
+  const int seq0 = pair_seq0 + static_cast<int>(rank) * (kRows / kGqa);   // this CTA's first sequence
   const CacheView& C = p.C;
   const int HQ = C.H * kGqa;
   const int row = tid & (kRows - 1), part = tid >> 7;      // (row warps) 16 cells of a tile and 64 dims of O per part
@@ -274,7 +276,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) shared_
   float* ksbuf = reinterpret_cast<float*>(smem + kKsOff);
 
   const int tile0 = split * p.tiles_per_split;
-  const int n_tiles = min(p.tiles_per_split, (p.cells + kTileN - 1) / kTileN - tile0);
+  // the prefix cells that any of the pair's sequences sees: those behind are neither
+  // looked up nor read (their pages may be unwritten, their table entries padding), and
+  // a range of nothing else still runs one tile, of no cells.  The same in every warp of
+  // both CTAs
+  int limit = pair_seq0 + lane < p.n_seqs ? __ldcg(p.lens + pair_seq0 + lane) : 0;
+  limit = min(p.cells, min(p.max_seq_len, __reduce_max_sync(kFull, max(limit, 0))));
+  const int n_tiles = max(1, min(p.tiles_per_split, (limit + kTileN - 1) / kTileN - tile0));
 
   if (warp == kLoadWarp) {
     // one barrier per lane
@@ -289,6 +297,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) shared_
     if (count) mbar_init(bars + 8 * lane, count);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     if (lane < 8) ctl[1 + lane] = 0;
+    if (lane == 0) ctl[12] = limit;
     if (lane == 0) {
       asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_k)) : "memory");
       asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_v)) : "memory");
@@ -305,12 +314,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) shared_
     const int H = C.H;
     if ((i & 7) == 0) {
       const int c = (tile0 + i + (lane >> 2)) * kTileN + 16 * (lane & 3);
-      page_mine = INT32_MIN;                               // behind the prefix
-      if (i + (lane >> 2) < n_tiles && c < p.cells) {
-        const int64_t pidx = p.page_div.div(static_cast<uint32_t>(c));
-        const int page = pidx < p.max_pages ? p.pt[pidx] : -1;
-        page_mine = page >= 0 && page < C.n_pages ? page : -1;
-      }
+      const int64_t pidx = p.page_div.div(static_cast<uint32_t>(c));
+      const int page = pidx < p.max_pages ? __ldcg(p.pt + pidx) : -1;
+      page_mine = INT32_MIN;                               // behind the limit, or another range's
+      if (i + (lane >> 2) < n_tiles && c < limit) page_mine = page >= 0 && page < C.n_pages ? page : -1;
     }
     const uint32_t dst = sb + kRawOff + stage * p.stage_bytes, bar = bars + 8 * (kBarRawFull + stage);
     const int my_group_page = __shfl_sync(kFull, page_mine, 4 * (i & 7) + (lane & 3));
@@ -351,7 +358,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) shared_
   {
     const int s = seq0 + row / kGqa;
     if (warp < kRowWarps && s < p.n_seqs) {
-      int v = p.lens[s];
+      int v = __ldcg(p.lens + s);
       if (v < 0 || v > p.max_seq_len) {
         if (part == 0) record_status(p.status, K8V4_ERANGE);
         v = v < 0 ? 0 : p.max_seq_len;
@@ -369,7 +376,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) shared_
       const int r = warp + kLoadWarp * j, s = seq0 + r / kGqa;
       raw[j] = make_uint4(0, 0, 0, 0);
       if (r < kRows && s < p.n_seqs)
-        raw[j] = __ldg(reinterpret_cast<const uint4*>(p.q + (static_cast<int64_t>(s) * HQ + g * kGqa + r % kGqa) * kD) + lane);
+        raw[j] = __ldcg(reinterpret_cast<const uint4*>(p.q + (static_cast<int64_t>(s) * HQ + g * kGqa + r % kGqa) * kD) + lane);
     }
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
@@ -383,9 +390,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) shared_
 #pragma unroll
       for (int o = 16; o >= 1; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, o));
       const int ex = amax > 0.0f ? static_cast<int>((__float_as_uint(amax) >> 23) & 0xffu) - 127 : 0;
-      const int sh = max(-100, min(100, 14 - ex));
+      const int sh = min(100, 14 - ex);                    // from -114 on
       const float up = __uint_as_float(static_cast<uint32_t>(sh + 127) << 23);                       // 2^sh
-      if (lane == 0) fsc[r] = p.sm_scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - sh) << 23);
+      // above 0 also where the product underflows: a masked score is -inf times it
+      if (lane == 0) fsc[r] = fmaxf(p.sm_scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - sh) << 23), 1.2e-38f);
       uint32_t hv[4];
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
@@ -664,11 +672,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) shared_
       if (i >= 2 && !mbar_wait(bars + 8 * (kBarODone + buf), last, p.wait_ns)) { ctl[1] = 1; break; }
       {
         const uint32_t dst = sb + kVOff + buf * kVBuf + (t >> 6) * 8192;
-        // a group that was not copied counts with V = 0 (its P is 0, its bytes are anything)
+        // a cell that was not copied, or that nobody sees, counts with V = 0 (its P is 0,
+        // its bytes are anything)
         uint32_t vd;
         asm volatile("ld.shared.u32 %0, [%1];" : "=r"(vd) : "r"(raw + vsraw));
         const uint4 vw[2] = {lds128(raw + vraw + ((vblk ^ (vrow & 7)) << 4)), lds128(raw + vraw + (((vblk + 1) ^ (vrow & 7)) << 4))};
-        if (!((valid >> (vcell >> 4)) & 1)) vd = 0;
+        if (!((valid >> (vcell >> 4)) & 1) || (tile0 + i) * kTileN + vcell >= ctl[12]) vd = 0;
         __syncwarp();
         if (lane == 0) arrive_local(bars + 8 * (kBarRawEmpty + stage));
 #pragma unroll
@@ -815,8 +824,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) shared_
   if (tid == 0 && ctl[1]) record_status(p.status, K8V4_ECUDA);
   cluster_barrier();          // no product, commit or arrival of the pair is in flight
   // launched behind the splits of the sequences' own cells, this kernel starts as
-  // their CTAs leave (all of them have then seen the kernels before them complete);
-  // the combine waits for this one alone, so this one ends after them
+  // their CTAs leave: all of them have then seen the kernels before them complete,
+  // whose results are read here through L2 (ld.cg, TMA); what those CTAs write is not
+  // read.  (With this wait ahead of the first read: 56.2 us where this takes 54.9, 32
+  // sequences on 32,768 cells.)  The combine waits for this kernel alone, so this one
+  // ends after them
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (warp == kIssueWarp) {
     tc_fence_after();

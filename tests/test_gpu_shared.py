@@ -157,6 +157,58 @@ def test_shared_decode_moving_maxima_long(n_seqs, shared):
     assert rel_err(got.cpu().numpy(), want.cpu().numpy()) <= 2 * TOL
 
 
+@pytest.mark.parametrize("n_seqs,shared,longest", [(40, 4096, 3001), (70, 2000, 1999), (64, 6400, 17), (33, 8192, 0)])
+def test_shared_decode_nothing_behind_the_lengths_is_read(n_seqs, shared, longest):
+    """Every sequence ends inside the prefix (each pair's somewhere else): pages behind hold NaN scales, and the table
+    has no page there at all."""
+    P, H = 16, 2
+    seed = synth.config_seed(3) + 11
+    n_pages = -(-shared // P)
+    pt = np.random.default_rng(seed).permutation(n_pages).astype(np.int32)[None]
+    gpu, ref = k8.PagedCache(n_pages, P, H), oracle.Cache(n_pages, P, H)
+    gpu.pages.fill_(0xFF)                           # NaN fp16 and fp32 scales
+    if longest:
+        kv = [synth.kv_values(seed, t, 0, longest, H, 3, "bf16") for t in (synth.T_K, synth.T_V)]
+        kd, vd = (dev_tensor(t, (1, longest, H, 256)) for t in kv)
+        k8.kv_append_k8v4(gpu, torch.from_numpy(pt).cuda(), torch.zeros(1, dtype=torch.int64, device="cuda"), kd, vd)
+        ref.append(pt, np.array([0]), *(t.f32.reshape(1, longest, H, 256) for t in kv))
+    pt[:, -(-longest // P):] = -1
+    pt = np.repeat(pt, n_seqs, 0)
+    lens = np.random.default_rng(seed).integers(0, longest + 1, n_seqs)
+    lens[:32] = np.minimum(lens[:32], longest // 2)  # the first pair's sequences are the shorter ones
+    lens[-1] = longest
+    q = synth.q_values(seed, 7, n_seqs, H, "bf16")
+    assert k8.attn_k8v4_shared_workspace_bytes(gpu, n_seqs, shared, shared) != k8.attn_k8v4_workspace_bytes(gpu, n_seqs, 1, shared)
+    got = run(gpu, dev_tensor(q, (n_seqs, 16, 256)), torch.from_numpy(pt).cuda(), lens, shared, shared)
+    assert k8.k8v4_last_device_status() == 0
+    rs, rh, rv = oracle.decode_rows(n_seqs, 16, lens)
+    want = ref.attention(np.maximum(pt, 0), rs, rh, rv, q.f32.reshape(-1, 256))
+    assert rel_err(got.cpu().numpy().reshape(-1, 256), want) <= TOL
+
+
+def test_shared_decode_scale_carried_by_the_queries():
+    """Queries times 2^e with sm_scale times 2^-e are the same scores exactly, so the output has the same bits; a
+    product of the two scales that underflows leaves all visible cells alike and hides the others."""
+    n_seqs, shared = 40, 2048
+    seed = synth.config_seed(3) + 12
+    gpu, _, pt = build(seed, n_seqs, shared, 0, 64, with_oracle=False)
+    q = dev_tensor(synth.q_values(seed, 7, n_seqs, 2, "bf16"), (n_seqs, 16, 256))
+    ptd = torch.from_numpy(pt).cuda()
+    lens = torch.from_numpy(np.random.default_rng(2).integers(0, shared + 1, n_seqs).astype(np.int32)).cuda()
+    ws = k8.shared_workspace(gpu, n_seqs, shared, shared)
+    outs = {}
+    for e in (0, 90, 120, -60):
+        outs[e] = torch.empty(q.shape, device="cuda")
+        k8.attn_k8v4_decode_shared(gpu, q * 2.0 ** e, ptd, lens, shared, shared, outs[e], ws, sm_scale=2.0 ** (-4 - e))
+        assert torch.equal(outs[e], outs[0])
+    flat = torch.empty_like(outs[0])
+    k8.attn_k8v4_decode_shared(gpu, q * 2.0 ** -90, ptd, lens, shared, shared, flat, ws, sm_scale=2.0 ** -60)
+    zero = torch.empty_like(flat)
+    k8.attn_k8v4_decode_shared(gpu, torch.zeros_like(q), ptd, lens, shared, shared, zero, ws)
+    assert k8.k8v4_last_device_status() == 0
+    assert rel_err(flat.cpu().numpy(), zero.cpu().numpy()) <= 2 * TOL
+
+
 def test_shared_decode_bad_pages_and_lengths():
     """A page id out of range inside the prefix: its cells are skipped and recorded; a length past max_seq_len is
     clipped, one below 0 counts as 0."""
