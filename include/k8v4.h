@@ -277,7 +277,8 @@ size_t attn_k8v4_shared_workspace_bytes(const k8v4_cache* cache, int32_t n_seqs,
  *   seq_lens: may be shorter than shared_len (such a row sees its own first
  *             seq_lens[b] cells), or 0 (zero output).
  *   workspace: >= attn_k8v4_shared_workspace_bytes(cache, n_seqs, shared_len,
- *             max_seq_len) bytes, 256-byte aligned.
+ *             max_seq_len) bytes, 256-byte aligned; calls that may run at the
+ *             same time (two streams, two graphs) need one each.
  * Other arguments as attn_k8v4_decode, in device memory.  K8V4 format, bf16 q.
  * Where the prefix is short or the sequences few, the call is attn_k8v4_decode;
  * else results agree with it to the attention's 2e-5 and are the same bits from

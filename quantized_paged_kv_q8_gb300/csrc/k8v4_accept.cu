@@ -96,6 +96,8 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kAccThreads, 
   __shared__ Pair warp_total[kAccWarps], s_ahead;
   __shared__ int s_acc, s_hit, s_last;
   cluster_arrive();                            // waited for before the first store to another CTA
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = blockIdx.x % kCluster;
   const int64_t b = blockIdx.x / kCluster;
@@ -301,9 +303,7 @@ int launch_accept(const Launch& L, const void* p, const void* q, int dtype, cons
   a.n_accepted = n_accepted;
   a.status = L.status;
   const dim3 grid(static_cast<unsigned>(n_seqs) * kCluster), block(kAccThreads);
-  if (dtype == K8V4_BF16) accept_kernel<true><<<grid, block, 0, L.stream>>>(a);
-  else accept_kernel<false><<<grid, block, 0, L.stream>>>(a);
-  return cudaGetLastError() == cudaSuccess ? K8V4_OK : K8V4_ECUDA;
+  return launch_behind(L, dtype == K8V4_BF16 ? accept_kernel<true> : accept_kernel<false>, grid, block, a);
 }
 
 }  // namespace k8v4

@@ -228,6 +228,8 @@ __global__ void __launch_bounds__(kWarps * 32) dequant_kernel(CacheView C, const
                                                               float* __restrict__ v_out, FastDiv div_h, FastDiv div_p,
                                                               int* status) {
   __shared__ long long stage[kWarps][kRotScratch];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int64_t item = static_cast<int64_t>(blockIdx.x) * kWarps + w;   // (cell, head)
   if (item >= n_cells * C.H) return;
@@ -351,13 +353,10 @@ int launch_dequant(const Launch& L, const CacheView& C, const int32_t* pt, int64
   if (blocks > 0x7fffffffll) return K8V4_EINVAL;
   const dim3 grid(static_cast<unsigned>(blocks)), block(kWarps * 32);
   const FastDiv dh(static_cast<uint32_t>(C.H)), dp(static_cast<uint32_t>(C.P));
-  if (C.fmt == K8V4_FORMAT_K8V4)
-    dequant_kernel<K8V4_FORMAT_K8V4><<<grid, block, 0, L.stream>>>(C, pt, max_pages, start, n_cells, k_out, v_rot_out, v_out, dh, dp, L.status);
-  else if (C.fmt == K8V4_FORMAT_Q4)
-    dequant_kernel<K8V4_FORMAT_Q4><<<grid, block, 0, L.stream>>>(C, pt, max_pages, start, n_cells, k_out, v_rot_out, v_out, dh, dp, L.status);
-  else
-    dequant_kernel<K8V4_FORMAT_INT8><<<grid, block, 0, L.stream>>>(C, pt, max_pages, start, n_cells, k_out, v_rot_out, v_out, dh, dp, L.status);
-  return cudaGetLastError() == cudaSuccess ? K8V4_OK : K8V4_ECUDA;
+  const auto kern = C.fmt == K8V4_FORMAT_K8V4 ? dequant_kernel<K8V4_FORMAT_K8V4>
+                    : C.fmt == K8V4_FORMAT_Q4 ? dequant_kernel<K8V4_FORMAT_Q4>
+                                              : dequant_kernel<K8V4_FORMAT_INT8>;
+  return launch_behind(L, kern, grid, block, C, pt, max_pages, start, n_cells, k_out, v_rot_out, v_out, dh, dp, L.status);
 }
 
 }  // namespace k8v4

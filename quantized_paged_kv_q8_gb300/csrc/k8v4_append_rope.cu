@@ -45,6 +45,7 @@ template <bool BF16, int FMT, bool INTER>
 __global__ void __launch_bounds__(kWarps * 32) append_rope_kernel(const AppendRopeParams p, int split_kv) {
   __shared__ __align__(16) long long stage[kWarps][kRotScratch];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const CacheView& C = p.C;
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int64_t wi = static_cast<int64_t>(blockIdx.x) * kWarps + w;
@@ -119,6 +120,7 @@ __global__ void __launch_bounds__(kWarps * 32, kBulkCtas) append_rope_bf16_kerne
   long long* ts = stage[w];
   fill_int8_scale_table(scale_tab);
   __syncthreads();
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const uint32_t total = static_cast<uint32_t>(p.n_seqs) * static_cast<uint32_t>(p.n_tok) * static_cast<uint32_t>(C.H);
   const uint32_t n_warps = gridDim.x * kWarps;
   const uint32_t per = (total + n_warps - 1) / n_warps;
@@ -213,14 +215,10 @@ int launch_fmt(const Launch& L, const AppendRopeParams& p, bool bf, int split, i
   if (bf && !split) {
     const int64_t want = (items + kWarps - 1) / kWarps;
     const dim3 grid(static_cast<unsigned>(std::min<int64_t>(want, static_cast<int64_t>(L.num_sms) * kBulkCtas)));
-    if (p.k_weight) append_rope_bf16_kernel<FMT, INTER, true><<<grid, block, 0, L.stream>>>(p);
-    else append_rope_bf16_kernel<FMT, INTER, false><<<grid, block, 0, L.stream>>>(p);
-  } else {
-    const dim3 grid(static_cast<unsigned>(((split ? 2 : 1) * items + kWarps - 1) / kWarps));
-    if (bf) append_rope_kernel<true, FMT, INTER><<<grid, block, 0, L.stream>>>(p, split);
-    else append_rope_kernel<false, FMT, INTER><<<grid, block, 0, L.stream>>>(p, split);
+    return launch_behind(L, p.k_weight ? append_rope_bf16_kernel<FMT, INTER, true> : append_rope_bf16_kernel<FMT, INTER, false>, grid, block, p);
   }
-  return cudaGetLastError() == cudaSuccess ? K8V4_OK : K8V4_ECUDA;
+  const dim3 grid(static_cast<unsigned>(((split ? 2 : 1) * items + kWarps - 1) / kWarps));
+  return launch_behind(L, bf ? append_rope_kernel<true, FMT, INTER> : append_rope_kernel<false, FMT, INTER>, grid, block, p, split);
 }
 
 }  // namespace

@@ -103,6 +103,25 @@ struct Launch {
   int num_sms;
 };
 
+// Launch a kernel whose first act on memory is griddepcontrol.wait: its CTAs may
+// take their places while the kernel before it in the stream drains.  (Its own
+// launch, about 1 us, is then hidden behind that kernel: a decode step is a chain
+// of kernels of a few microseconds.)
+template <typename... P, typename... A>
+int launch_behind(const Launch& L, void (*kernel)(P...), dim3 grid, dim3 block, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.stream = L.stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, kernel, args...) != cudaSuccess) return K8V4_ECUDA;
+  return cudaGetLastError() == cudaSuccess ? K8V4_OK : K8V4_ECUDA;
+}
+
 // mirror != null: a streamed cache -- pt holds host-mirror page ids, every row is
 // written to the mirror and, where slot_of_page[page] >= 0, to that slot of C
 int launch_append(const Launch& L, const CacheView& C, const int32_t* pt, int64_t max_pages, int n_seqs,

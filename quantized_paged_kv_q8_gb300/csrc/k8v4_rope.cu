@@ -43,6 +43,8 @@ struct RopeParams {
 // PER: heads of one token that a warp takes
 template <bool BF16, bool INTER, int PER>
 __global__ void __launch_bounds__(kRopeWarps * 32, 4) norm_rope_kernel(const RopeParams p) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int64_t wi = static_cast<int64_t>(blockIdx.x) * kRopeWarps + w;
   if (wi >= p.n_tokens * p.units) return;
@@ -117,9 +119,7 @@ __global__ void __launch_bounds__(kRopeWarps * 32, 4) norm_rope_kernel(const Rop
 template <bool BF16, bool INTER>
 int launch_per(const Launch& L, RopeParams p, int per, int64_t warps) {
   const dim3 grid(static_cast<unsigned>((warps + kRopeWarps - 1) / kRopeWarps)), block(kRopeWarps * 32);
-  if (per == 1) norm_rope_kernel<BF16, INTER, 1><<<grid, block, 0, L.stream>>>(p);
-  else norm_rope_kernel<BF16, INTER, BF16 ? 4 : 2><<<grid, block, 0, L.stream>>>(p);
-  return cudaGetLastError() == cudaSuccess ? K8V4_OK : K8V4_ECUDA;
+  return launch_behind(L, per == 1 ? norm_rope_kernel<BF16, INTER, 1> : norm_rope_kernel<BF16, INTER, BF16 ? 4 : 2>, grid, block, p);
 }
 
 }  // namespace
