@@ -13,9 +13,10 @@
 // kept as pairs of fp32 numbers with the additions' errors carried (about 46
 // bits, far below the spacing of the random numbers).
 //
-// What bounds it: reading the two rows (2 x 4 B a vocabulary entry), and for few
-// sequences the latency of three dependent steps (drafts' probabilities, sums,
-// search).  One cluster of eight CTAs per sequence splits the vocabulary, so one
+// What bounds it: reading the two rows (2 x 4 B a vocabulary entry; 64 sequences of
+// 262,144 entries: 134 MB in 26.6 us, 5.0 TB/s), and for few sequences the latency of
+// three dependent steps (drafts' probabilities, sums, search; 5.2 us in all, one
+// sequence of 32,768).  One cluster of eight CTAs per sequence splits the vocabulary, so one
 // sequence alone keeps eight SMs loading; CTA totals meet in distributed shared
 // memory, and only the CTA that holds the token reads its part (from L2) again.
 #include <algorithm>
@@ -29,7 +30,8 @@ namespace {
 constexpr int kCluster = 8;
 constexpr int kAccThreads = 512;
 constexpr int kAccWarps = kAccThreads / 32;
-constexpr int kUnroll = 8;
+constexpr int kUnroll = 8;        // loads of a thread in flight
+constexpr int kUnrollFew = 16;    // of few sequences over a large vocabulary (launch_accept)
 
 struct AcceptParams {
   const void* p;             // [n_seqs][max_drafts + 1][vocab]
@@ -90,8 +92,9 @@ __device__ __forceinline__ void store_remote(Pair* local, int rank, const Pair& 
   asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(a), "f"(v.hi), "f"(v.lo) : "memory");
 }
 
-template <bool BF16>
-__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kAccThreads, 4) accept_kernel(const AcceptParams a) {
+template <bool BF16, int UNROLL>
+__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kAccThreads, UNROLL == kUnrollFew ? 2 : 4)
+    accept_kernel(const AcceptParams a) {
   __shared__ __align__(8) Pair cta_total[2][kCluster];   // every CTA's sums (w, then p alone), written by each to all
   __shared__ Pair warp_total[kAccWarps], s_ahead;
   __shared__ int s_acc, s_hit, s_last;
@@ -166,14 +169,20 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kAccThreads, 
     Pair s{0.0f, 0.0f};
     auto sum_run = [&](auto with_q, int left_out) {
       int j = w0 + lane;
-      for (; j + 32 * (kUnroll - 1) < w1; j += 32 * kUnroll) {
-        float x[kUnroll];
+      for (; j + 32 * (UNROLL - 1) < w1; j += 32 * UNROLL) {
+        float x[UNROLL];
 #pragma unroll
-        for (int i = 0; i < kUnroll; ++i) x[i] = weight(j + 32 * i, with_q, left_out);
+        for (int i = 0; i < UNROLL; ++i) x[i] = weight(j + 32 * i, with_q, left_out);
 #pragma unroll
-        for (int i = 0; i < kUnroll; ++i) add(s, x[i]);
+        for (int i = 0; i < UNROLL; ++i) add(s, x[i]);
       }
-      for (; j < w1; j += 32) add(s, weight(j, with_q, left_out));
+      if (j < w1) {                              // the rest, its loads together as well
+        float x[UNROLL];
+#pragma unroll
+        for (int i = 0; i < UNROLL; ++i) x[i] = j + 32 * i < w1 ? weight(j + 32 * i, with_q, left_out) : 0.0f;
+#pragma unroll
+        for (int i = 0; i < UNROLL; ++i) add(s, x[i]);
+      }
     };
     if (residual && has_q) sum_run(kWithQ, -1);
     else sum_run(kAlone, residual ? refused : -1);
@@ -303,7 +312,13 @@ int launch_accept(const Launch& L, const void* p, const void* q, int dtype, cons
   a.n_accepted = n_accepted;
   a.status = L.status;
   const dim3 grid(static_cast<unsigned>(n_seqs) * kCluster), block(kAccThreads);
-  return launch_behind(L, dtype == K8V4_BF16 ? accept_kernel<true> : accept_kernel<false>, grid, block, a);
+  // Few CTAs (all at once with two per SM) whose threads have more than kUnroll entries:
+  // twice the loads in flight per thread.  24 sequences of 262,144 entries 15.4 -> 11.1 us,
+  // 38 17.9 -> 17.3 (8.7 either way at 32,768); 64 sequences would lose (24.3 -> 25.0:
+  // four CTAs of fewer registers per SM read more at a time)
+  if (static_cast<int64_t>(n_seqs) * kCluster <= 2 * L.num_sms && vocab > kCluster * kAccThreads * kUnroll)
+    return launch_behind(L, dtype == K8V4_BF16 ? accept_kernel<true, kUnrollFew> : accept_kernel<false, kUnrollFew>, grid, block, a);
+  return launch_behind(L, dtype == K8V4_BF16 ? accept_kernel<true, kUnroll> : accept_kernel<false, kUnroll>, grid, block, a);
 }
 
 }  // namespace k8v4

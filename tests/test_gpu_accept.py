@@ -73,7 +73,7 @@ def inputs(seed, B, n, V, spread=2.0, noise=0.5):
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("certain", [False, True])
 @pytest.mark.parametrize("B,n,V", [(1, 1, 1), (3, 2, 2), (5, 4, 31), (40, 7, 33), (9, 4, 1000), (6, 32, 777),
-                                   (4, 3, 4099), (17, 5, 20011), (2, 4, 131071), (1, 1, 300001)])
+                                   (4, 3, 4099), (17, 5, 20011), (2, 4, 131071), (1, 1, 300001), (45, 1, 40003)])
 def test_accept_against_64_bits(dtype, certain, B, n, V):
     p, q, drafts, counts, u, us = inputs(B + 7 * n + V, B, n, V)
     r = lambda x: torch.from_numpy(x).to(dtype).double().numpy()
