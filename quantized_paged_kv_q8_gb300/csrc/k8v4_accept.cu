@@ -52,6 +52,15 @@ __device__ __forceinline__ float prob(const void* base, int64_t i) {
   return __ldg(static_cast<const float*>(base) + i);
 }
 
+// four entries from an index that is a multiple of four, in rows that begin at one
+template <bool BF16>
+__device__ __forceinline__ float4 prob4(const void* base, int64_t i) {
+  if (!BF16) return __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(base) + i));
+  const uint2 w = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(base) + i));
+  return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u), __uint_as_float(w.y << 16),
+                     __uint_as_float(w.y & 0xffff0000u));
+}
+
 // A sum as hi + lo, |lo| small beside hi: about 46 bits, no fp64 instruction (that
 // unit takes 16 clocks a warp instruction here, and every warp would queue for it)
 struct Pair {
@@ -92,7 +101,7 @@ __device__ __forceinline__ void store_remote(Pair* local, int rank, const Pair& 
   asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(a), "f"(v.hi), "f"(v.lo) : "memory");
 }
 
-template <bool BF16, int UNROLL>
+template <bool BF16, int UNROLL, bool WIDE>
 __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kAccThreads, UNROLL == kUnrollFew ? 2 : 4)
     accept_kernel(const AcceptParams a) {
   __shared__ __align__(8) Pair cta_total[2][kCluster];   // every CTA's sums (w, then p alone), written by each to all
@@ -157,7 +166,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kAccThreads, 
   const std::true_type kWithQ{};
   const std::false_type kAlone{};
   // ---- sums: CTA `rank` owns kAccWarps runs of the vocabulary, a warp each
-  const int per_warp = (V + kCluster * kAccWarps - 1) / (kCluster * kAccWarps);
+  const int per_warp = ((V + kCluster * kAccWarps - 1) / (kCluster * kAccWarps) + 3) & ~3;
   auto run_begin = [&](int w) {
     return static_cast<int>(min(static_cast<int64_t>(V), static_cast<int64_t>(rank * kAccWarps + w) * per_warp));
   };
@@ -167,22 +176,45 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kAccThreads, 
   cluster_wait();
   for (int pass = 0; pass < 2; ++pass) {
     Pair s{0.0f, 0.0f};
+    // UNROLL entries of a lane from j on: consecutive fours 128 apart (a quarter of the
+    // load instructions), or single ones 32 apart; guard: only those ahead of w1
+    auto add_chunk = [&](int j, auto with_q, auto guard, int left_out) {
+      float x[UNROLL];
+      if constexpr (WIDE) {
+#pragma unroll
+        for (int i = 0; i < UNROLL; i += 4) {
+          const int at = j + 32 * i;
+          float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          if (!decltype(guard)::value || at < w1) {
+            v = prob4<BF16>(a.p, p_row + at);
+            if constexpr (decltype(with_q)::value) {
+              const float4 q = prob4<BF16>(a.q, q_row + at);
+              v = make_float4(__fsub_rn(v.x, q.x), __fsub_rn(v.y, q.y), __fsub_rn(v.z, q.z), __fsub_rn(v.w, q.w));
+            } else {
+              if (at == (left_out & ~3)) {
+                const int k = left_out & 3;
+                v = make_float4(k == 0 ? 0.0f : v.x, k == 1 ? 0.0f : v.y, k == 2 ? 0.0f : v.z, k == 3 ? 0.0f : v.w);
+              }
+            }
+          }
+          x[i] = fmaxf(v.x, 0.0f);
+          x[i + 1] = fmaxf(v.y, 0.0f);
+          x[i + 2] = fmaxf(v.z, 0.0f);
+          x[i + 3] = fmaxf(v.w, 0.0f);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < UNROLL; ++i)
+          x[i] = !decltype(guard)::value || j + 32 * i < w1 ? weight(j + 32 * i, with_q, left_out) : 0.0f;
+      }
+#pragma unroll
+      for (int i = 0; i < UNROLL; ++i) add(s, x[i]);
+    };
     auto sum_run = [&](auto with_q, int left_out) {
-      int j = w0 + lane;
-      for (; j + 32 * (UNROLL - 1) < w1; j += 32 * UNROLL) {
-        float x[UNROLL];
-#pragma unroll
-        for (int i = 0; i < UNROLL; ++i) x[i] = weight(j + 32 * i, with_q, left_out);
-#pragma unroll
-        for (int i = 0; i < UNROLL; ++i) add(s, x[i]);
-      }
-      if (j < w1) {                              // the rest, its loads together as well
-        float x[UNROLL];
-#pragma unroll
-        for (int i = 0; i < UNROLL; ++i) x[i] = j + 32 * i < w1 ? weight(j + 32 * i, with_q, left_out) : 0.0f;
-#pragma unroll
-        for (int i = 0; i < UNROLL; ++i) add(s, x[i]);
-      }
+      int j = w0 + (WIDE ? 4 * lane : lane);
+      constexpr int kLast = 32 * (UNROLL - (WIDE ? 4 : 1));
+      for (; j + kLast < w1; j += 32 * UNROLL) add_chunk(j, with_q, std::false_type{}, left_out);
+      if (j < w1) add_chunk(j, with_q, std::true_type{}, left_out);
     };
     if (residual && has_q) sum_run(kWithQ, -1);
     else sum_run(kAlone, residual ? refused : -1);
@@ -312,13 +344,20 @@ int launch_accept(const Launch& L, const void* p, const void* q, int dtype, cons
   a.n_accepted = n_accepted;
   a.status = L.status;
   const dim3 grid(static_cast<unsigned>(n_seqs) * kCluster), block(kAccThreads);
+  const bool bf = dtype == K8V4_BF16;
   // Few CTAs (all at once with two per SM) whose threads have more than kUnroll entries:
   // twice the loads in flight per thread.  24 sequences of 262,144 entries 15.4 -> 11.1 us,
   // 38 17.9 -> 17.3 (8.7 either way at 32,768); 64 sequences would lose (24.3 -> 25.0:
-  // four CTAs of fewer registers per SM read more at a time)
-  if (static_cast<int64_t>(n_seqs) * kCluster <= 2 * L.num_sms && vocab > kCluster * kAccThreads * kUnroll)
-    return launch_behind(L, dtype == K8V4_BF16 ? accept_kernel<true, kUnrollFew> : accept_kernel<false, kUnrollFew>, grid, block, a);
-  return launch_behind(L, dtype == K8V4_BF16 ? accept_kernel<true, kUnroll> : accept_kernel<false, kUnroll>, grid, block, a);
+  // four CTAs of fewer registers per SM read more at a time).  Of those, rows that are whole and
+  // aligned groups of four entries are read by fours: 24 of 262,144 11.0 -> 10.0 us, 38 17.1 -> 15.3
+  // (at 32 registers that form spills: 64 of 32,768 entries 8.8 -> 10.0, so the others stay single)
+  if (static_cast<int64_t>(n_seqs) * kCluster <= 2 * L.num_sms && vocab > kCluster * kAccThreads * kUnroll) {
+    const uintptr_t four = dtype == K8V4_BF16 ? 8 : 16;
+    const bool wide = vocab % 4 == 0 && reinterpret_cast<uintptr_t>(p) % four == 0 && reinterpret_cast<uintptr_t>(q) % four == 0;
+    if (bf) return launch_behind(L, wide ? accept_kernel<true, kUnrollFew, true> : accept_kernel<true, kUnrollFew, false>, grid, block, a);
+    return launch_behind(L, wide ? accept_kernel<false, kUnrollFew, true> : accept_kernel<false, kUnrollFew, false>, grid, block, a);
+  }
+  return launch_behind(L, bf ? accept_kernel<true, kUnroll, false> : accept_kernel<false, kUnroll, false>, grid, block, a);
 }
 
 }  // namespace k8v4

@@ -73,7 +73,7 @@ def inputs(seed, B, n, V, spread=2.0, noise=0.5):
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("certain", [False, True])
 @pytest.mark.parametrize("B,n,V", [(1, 1, 1), (3, 2, 2), (5, 4, 31), (40, 7, 33), (9, 4, 1000), (6, 32, 777),
-                                   (4, 3, 4099), (17, 5, 20011), (2, 4, 131071), (1, 1, 300001), (45, 1, 40003)])
+                                   (4, 3, 4099), (17, 5, 20011), (2, 4, 131071), (1, 1, 300001), (45, 1, 40003), (3, 2, 40004), (1, 2, 70000)])
 def test_accept_against_64_bits(dtype, certain, B, n, V):
     p, q, drafts, counts, u, us = inputs(B + 7 * n + V, B, n, V)
     r = lambda x: torch.from_numpy(x).to(dtype).double().numpy()
@@ -83,6 +83,20 @@ def test_accept_against_64_bits(dtype, certain, B, n, V):
         want = plain(p64, q64, drafts, np.full(B, n) if c is None else c, u, us)
         assert np.array_equal(got[0], want[0]) and np.array_equal(got[1], want[1])
     assert k8.k8v4_last_device_status() == 0
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_accept_rows_at_any_element(dtype):
+    """Probabilities that begin one element behind an aligned address, beside drafts' that do not."""
+    B, n, V = 2, 3, 50000
+    p, q, drafts, counts, u, us = inputs(11, B, n, V)
+    shift = torch.empty(B * (n + 1) * V + 1, dtype=dtype, device="cuda")[1:].view(B, n + 1, V)
+    shift.copy_(torch.from_numpy(p))
+    qd = torch.from_numpy(q).to(dtype).cuda()
+    tokens, acc = torch.empty(B, n + 1, dtype=torch.int32, device="cuda"), torch.empty(B, dtype=torch.int32, device="cuda")
+    k8.spec_accept_k8v4(shift, qd, torch.from_numpy(drafts).cuda(), torch.from_numpy(u).cuda(), torch.from_numpy(us).cuda(), tokens, acc)
+    want = plain(shift.double().cpu().numpy(), qd.double().cpu().numpy(), drafts, np.full(B, n), u, us)
+    assert np.array_equal(tokens.cpu().numpy(), want[0]) and np.array_equal(acc.cpu().numpy(), want[1])
 
 
 def test_accept_no_drafts():
