@@ -9,7 +9,10 @@
 // warp owns a row (16 B a lane in bf16), so the norm is one butterfly and the
 // partner of a pair one shuffle away; a warp takes `per` heads of one token, so
 // that the table row and the norm weight are loaded once for them, and issues
-// the loads of all of them before it uses the first.
+// the loads of all of them before it uses the first.  Measured: 8,192 tokens of
+// 16 + 2 heads in bf16, normed, out of a packed projection (153 MB): 27.3 us, 5.6 TB/s;
+// a copy of as many bytes takes 26.2.  One token: 2.8 us, the latency of a launch and
+// two dependent reads.
 #include <algorithm>
 
 #include "k8v4_quant.cuh"
@@ -18,7 +21,8 @@
 namespace k8v4 {
 namespace {
 
-constexpr int kRopeWarps = 8;
+constexpr int kRopeWarps = 2;     // per CTA (8,192 tokens x 18 heads, us: 8 28.9, 4 27.8, 2 27.3)
+constexpr int kRopeCtas = 16;     // per SM: 64 registers a thread
 
 struct RopeParams {
   const void* q;
@@ -42,7 +46,7 @@ struct RopeParams {
 
 // PER: heads of one token that a warp takes
 template <bool BF16, bool INTER, int PER>
-__global__ void __launch_bounds__(kRopeWarps * 32, 4) norm_rope_kernel(const RopeParams p) {
+__global__ void __launch_bounds__(kRopeWarps * 32, kRopeCtas) norm_rope_kernel(const RopeParams p) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
