@@ -284,15 +284,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) shared_
   float* ksbuf = reinterpret_cast<float*>(smem + kKsOff);
 
   const int tile0 = split * p.tiles_per_split;
-  // the prefix cells that any of the pair's sequences sees: those behind are neither
+  // The prefix cells that any of the pair's sequences sees: those behind are neither
   // looked up nor read (their pages may be unwritten, their table entries padding), and
-  // a range of nothing else still runs one tile, of no cells.  The same in every warp of
-  // both CTAs
-  int limit = pair_seq0 + lane < p.n_seqs ? __ldcg(p.lens + pair_seq0 + lane) : 0;
-  limit = min(p.cells, min(p.max_seq_len, __reduce_max_sync(kFull, max(limit, 0))));
-  const int n_tiles = max(1, min(p.tiles_per_split, (limit + kTileN - 1) / kTileN - tile0));
-
+  // a range of nothing else still runs one tile, of no cells.  The same in both CTAs; the
+  // load warp tells the others
+  auto tiles_of = [&](int cells) { return max(1, min(p.tiles_per_split, (cells + kTileN - 1) / kTileN - tile0)); };
+  int limit = 0;
   if (warp == kLoadWarp) {
+    limit = pair_seq0 + lane < p.n_seqs ? __ldcg(p.lens + pair_seq0 + lane) : 0;
     // one barrier per lane
     int count = 0;
     if (lane < kBarPFull) count = 8;                       // K, V tiles: 4 conversion warps of both CTAs
@@ -305,8 +304,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) shared_
     if (count) mbar_init(bars + 8 * lane, count);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     if (lane < 8) ctl[1 + lane] = 0;
-    if (lane == 0) ctl[12] = limit;
+    limit = min(p.cells, min(p.max_seq_len, __reduce_max_sync(kFull, max(limit, 0))));
     if (lane == 0) {
+      ctl[12] = limit;
+      ctl[13] = tiles_of(limit);
       asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_k)) : "memory");
       asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_v)) : "memory");
     }
@@ -325,7 +326,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) shared_
       const int64_t pidx = p.page_div.div(static_cast<uint32_t>(c));
       const int page = pidx < p.max_pages ? __ldcg(p.pt + pidx) : -1;
       page_mine = INT32_MIN;                               // behind the limit, or another range's
-      if (i + (lane >> 2) < n_tiles && c < limit) page_mine = page >= 0 && page < C.n_pages ? page : -1;
+      if (i + (lane >> 2) < tiles_of(limit) && c < limit) page_mine = page >= 0 && page < C.n_pages ? page : -1;
     }
     const uint32_t dst = sb + kRawOff + stage * p.stage_bytes, bar = bars + 8 * (kBarRawFull + stage);
     const int my_group_page = __shfl_sync(kFull, page_mine, 4 * (i & 7) + (lane & 3));
@@ -355,11 +356,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) shared_
     }
     __syncwarp();
   };
-  if (warp == kLoadWarp) {                                 // the first tiles, while the others set Q up
-    const bool leader = elect_one();
-#pragma unroll 1
-    for (int i = 0; i < min(p.stages, n_tiles); ++i) load_tile(i, i, leader);
-  }
+  // The first tile, while the others set Q up.  The next ones only behind that: all CTAs
+  // begin at once, and their first copies would wait for everyone's second and third
+  if (warp == kLoadWarp) load_tile(0, 0, elect_one());
 
   // ---- visibility of this thread's row
   int my_vis = 0;
@@ -419,6 +418,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) shared_
   cluster_barrier();          // barriers, tensor memory and Q of both CTAs are ready
   tc_fence_after();
   const uint32_t tmem = static_cast<uint32_t>(ctl[0]);
+  const int n_tiles = ctl[13];
 
   if (warp < kRowWarps) {
     // ================================================================ rows
@@ -811,10 +811,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) shared_
     } else if (__shfl_sync(kFull, warp, 0) == kLoadWarp) {
       // ============================================================== copies
       const bool leader = elect_one();
-      int stage = 0, i = min(p.stages, n_tiles);
-      uint32_t phase = 0;
+      int stage = 1, i = 1;
+      uint32_t phase = 1;                                  // of the stage's last use, from its second on
       for (; i < n_tiles; ++i) {
-        if (!__all_sync(kFull, mbar_wait(bars + 8 * (kBarRawEmpty + stage), phase, p.wait_ns))) { ctl[1] = 1; break; }
+        if (i >= p.stages && !__all_sync(kFull, mbar_wait(bars + 8 * (kBarRawEmpty + stage), phase, p.wait_ns))) { ctl[1] = 1; break; }
         load_tile(i, stage, leader);
         if (++stage == p.stages) {
           stage = 0;
