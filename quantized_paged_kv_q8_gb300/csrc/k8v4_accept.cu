@@ -48,15 +48,15 @@ struct AcceptParams {
 
 template <bool BF16>
 __device__ __forceinline__ float prob(const void* base, int64_t i) {
-  if (BF16) return __uint_as_float(static_cast<uint32_t>(__ldg(static_cast<const uint16_t*>(base) + i)) << 16);
-  return __ldg(static_cast<const float*>(base) + i);
+  if (BF16) return __uint_as_float(static_cast<uint32_t>(__ldca(static_cast<const uint16_t*>(base) + i)) << 16);
+  return __ldca(static_cast<const float*>(base) + i);
 }
 
 // four entries from an index that is a multiple of four, in rows that begin at one
 template <bool BF16>
 __device__ __forceinline__ float4 prob4(const void* base, int64_t i) {
-  if (!BF16) return __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(base) + i));
-  const uint2 w = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(base) + i));
+  if (!BF16) return __ldca(reinterpret_cast<const float4*>(static_cast<const float*>(base) + i));
+  const uint2 w = __ldca(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(base) + i));
   return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u), __uint_as_float(w.y << 16),
                      __uint_as_float(w.y & 0xffff0000u));
 }

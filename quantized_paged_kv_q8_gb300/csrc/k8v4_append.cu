@@ -222,7 +222,7 @@ __device__ __forceinline__ void write_row_wide(float* row, int lane, const float
 }
 
 template <int FMT>
-__global__ void __launch_bounds__(kWarps * 32) dequant_kernel(CacheView C, const int32_t* __restrict__ pt,
+__global__ void __launch_bounds__(kWarps * 32) dequant_kernel(CacheView C, const int32_t* pt,
                                                               int64_t max_pages, int64_t start, int64_t n_cells,
                                                               float* __restrict__ k_out, float* __restrict__ v_rot_out,
                                                               float* __restrict__ v_out, FastDiv div_h, FastDiv div_p,

@@ -111,7 +111,7 @@ __global__ void __launch_bounds__(256, R <= kRoundFew ? 8 : 4)
 // first o rows are under way, and a warp reads 1 KB of a split at a time.
 constexpr int kRowWarps = 4, kRowUnroll = 4, kRowMaxSplits = 2048;
 
-__global__ void __launch_bounds__(32 * kRowWarps) combine_rows_kernel(const float* __restrict__ src, int splits,
+__global__ void __launch_bounds__(32 * kRowWarps) combine_rows_kernel(const float* src, int splits,
                                                                       int64_t split_stride, int64_t b_stride,
                                                                       int rows_per_b, float* __restrict__ out) {
   __shared__ float wt[kRowMaxSplits];

@@ -106,7 +106,9 @@ struct Launch {
 // Launch a kernel whose first act on memory is griddepcontrol.wait: its CTAs may
 // take their places while the kernel before it in the stream drains.  (Its own
 // launch, about 1 us, is then hidden behind that kernel: a decode step is a chain
-// of kernels of a few microseconds.)
+// of kernels of a few microseconds.)  Such a kernel is on the device while that one
+// still writes, so nothing it reads may go through the read-only path (__ldg, const
+// __restrict__ pointers).
 template <typename... P, typename... A>
 int launch_behind(const Launch& L, void (*kernel)(P...), dim3 grid, dim3 block, A... args) {
   cudaLaunchConfig_t cfg = {};

@@ -74,14 +74,14 @@ struct RopeFactors {
   float c[INTER ? 4 : 8], s[INTER ? 4 : 8];
 };
 template <bool INTER>
-__device__ __forceinline__ void rope_load(const float* __restrict__ row, const RopeLane& rl, int half,
+__device__ __forceinline__ void rope_load(const float* row, const RopeLane& rl, int half,
                                           RopeFactors<INTER>& f) {
   if (!rl.on) return;
   const float4* c4 = reinterpret_cast<const float4*>(row + rl.at);
   const float4* s4 = reinterpret_cast<const float4*>(row + half + rl.at);
 #pragma unroll
   for (int i = 0; i < (INTER ? 1 : 2); ++i) {
-    const float4 a = __ldg(c4 + i), b = __ldg(s4 + i);
+    const float4 a = __ldca(c4 + i), b = __ldca(s4 + i);
     f.c[4 * i] = a.x; f.c[4 * i + 1] = a.y; f.c[4 * i + 2] = a.z; f.c[4 * i + 3] = a.w;
     f.s[4 * i] = rl.sign * b.x; f.s[4 * i + 1] = rl.sign * b.y; f.s[4 * i + 2] = rl.sign * b.z; f.s[4 * i + 3] = rl.sign * b.w;
   }
@@ -148,8 +148,8 @@ __device__ __forceinline__ void rms_row(float x[8], const float w[8], float eps)
   }
 }
 
-__device__ __forceinline__ void load_weight8(const float* __restrict__ w, int lane, float out[8]) {
-  const float4 a = __ldg(reinterpret_cast<const float4*>(w) + 2 * lane), b = __ldg(reinterpret_cast<const float4*>(w) + 2 * lane + 1);
+__device__ __forceinline__ void load_weight8(const float* w, int lane, float out[8]) {
+  const float4 a = __ldca(reinterpret_cast<const float4*>(w) + 2 * lane), b = __ldca(reinterpret_cast<const float4*>(w) + 2 * lane + 1);
   out[0] = a.x; out[1] = a.y; out[2] = a.z; out[3] = a.w;
   out[4] = b.x; out[5] = b.y; out[6] = b.z; out[7] = b.w;
 }

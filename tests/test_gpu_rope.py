@@ -236,3 +236,37 @@ def test_rope_calls_captured_replayed_and_on_another_stream():
         torch.cuda.synchronize()
         assert torch.equal(cache.pages, eager.pages) and all(torch.equal(a, b) for a, b in zip(outs, want))
     assert k8.k8v4_last_device_status() == 0
+
+
+def test_calls_back_to_back_read_what_the_call_before_wrote():
+    """Chains of these calls on one stream with nothing between them (each starts while the one before it drains):
+    rows rotated to and fro between two buffers, cells overwritten and read back, equal to the same calls one by one."""
+    n_tok, H, P = 700, 2, 16
+    table = torch.from_numpy(table_of(n_tok, 128)).cuda()
+    pos = torch.zeros(1, dtype=torch.int64, device="cuda")
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    start = torch.randn(1, n_tok, H, 256, generator=gen, device="cuda")
+    v = torch.randn(1, n_tok, H, 256, generator=gen, device="cuda")
+    n_pages = -(-n_tok // P)
+    pt = torch.randperm(n_pages, device="cuda").int()[None].contiguous()
+    rounds = 24
+
+    def chain(pause):
+        a, b = start.clone(), torch.empty_like(start)
+        cache = k8.PagedCache(n_pages, P, H)
+        back = torch.empty(rounds, 2, n_tok, H, 256, device="cuda")
+        torch.cuda.synchronize()
+        for i in range(rounds):
+            for call in (lambda: k8.qk_norm_rope_k8v4(a, None, pos, table, b, None),
+                         lambda: k8.qk_norm_rope_k8v4(b, None, pos, table, a, None, interleaved=True),
+                         lambda: k8.kv_append_k8v4_rope(cache, pt, pos, a, v, table),
+                         lambda: k8.kv_dequant_k8v4(cache, pt[0], 0, n_tok, back[i, 0], back[i, 1])):
+                call()
+                if pause:
+                    torch.cuda.synchronize()
+        torch.cuda.synchronize()
+        return a, back
+
+    got, want = chain(False), chain(True)
+    assert k8.k8v4_last_device_status() == 0
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
