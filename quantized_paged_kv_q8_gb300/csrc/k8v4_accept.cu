@@ -250,14 +250,20 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kAccThreads, 
   // ---- the smallest j whose running sum passes T = u W
   float u = a.u_sample[b];
   u = u >= 0.0f ? fminf(u, 0x1.fffffep-1f) : 0.0f;          // NaN and below 0: 0; from 1 on: below 1
+  // Sums below 2^40 are compared times 2^80 (both exact): a residual may be a few units of
+  // 2^-149, of which the product with u, and the error that T.lo carries, keep no bit
+  const float up = total.hi < 0x1p40f ? 0x1p80f : 1.0f;
+  auto scaled = [&](const Pair& s) { return Pair{__fmul_rn(s.hi, up), __fmul_rn(s.lo, up)}; };
+  const Pair W = scaled(total);
   Pair T;
-  T.hi = __fmul_rn(u, total.hi);
-  T.lo = __fadd_rn(__fmaf_rn(u, total.hi, -T.hi), __fmul_rn(u, total.lo));
+  T.hi = __fmul_rn(u, W.hi);
+  T.lo = __fadd_rn(__fmaf_rn(u, W.hi, -T.hi), __fmul_rn(u, W.lo));
+  auto passes = [&](const Pair& s) { return greater(scaled(s), T); };
   // before + this CTA's sum is, bit for bit, the next CTA's `before`: the first
   // CTA whose end passes T is the one that holds the token (the last one if none)
   Pair after = before;
   add(after, cta_total[residual == rejected ? 0 : 1][rank]);
-  if (greater(before, T) || (!greater(after, T) && rank != kCluster - 1)) return;
+  if (passes(before) || (!passes(after) && rank != kCluster - 1)) return;
   // the warp run that holds T, and the sum ahead of it
   if (warp == 0) {
     Pair s = lane < kAccWarps ? warp_total[lane] : Pair{0.0f, 0.0f};
@@ -265,7 +271,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kAccThreads, 
     s = scan_warp(s, lane);
     Pair end = before;
     add(end, s);
-    const unsigned past = __ballot_sync(0xffffffffu, some && greater(end, T));
+    const unsigned past = __ballot_sync(0xffffffffu, some && passes(end));
     const unsigned any = __ballot_sync(0xffffffffu, some);
     const int hit = past ? __ffs(past) - 1 : any ? 31 - __clz(any) : 0;
     const Pair prev{__shfl_sync(0xffffffffu, end.hi, max(hit - 1, 0)), __shfl_sync(0xffffffffu, end.lo, max(hit - 1, 0))};
@@ -310,7 +316,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kAccThreads, 
       add(run, x[i]);
       if (x[i] > 0.0f) {
         last = j + i;
-        if (found == 0x7fffffff && greater(run, T)) found = j + i;
+        if (found == 0x7fffffff && passes(run)) found = j + i;
       }
     }
     if (found != 0x7fffffff) atomicMin(&s_hit, found);
