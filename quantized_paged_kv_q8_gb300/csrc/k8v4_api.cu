@@ -363,7 +363,7 @@ int attn_k8v4_decode_shared(const k8v4_cache* cache, const void* q, int32_t q_dt
                          workspace);
   float* ws = static_cast<float*>(workspace);
   const int splits = pre.splits + own.splits;
-  // the sequences' own cells, then the prefix, whose CTAs start as those of the first leave
+  // the sequences' own cells, then the prefix, whose CTAs take their places as those of the first leave
   if (own.splits > 0) {
     rc = launch_decode_splits(L, C, own, q, q_dtype, page_table, max_pages, seq_lens, n_seqs, max_seq_len, pre.cells,
                               sm_scale, ws, splits, pre.splits, wait_limit_ns());

@@ -291,7 +291,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) shared_
   auto tiles_of = [&](int cells) { return max(1, min(p.tiles_per_split, (cells + kTileN - 1) / kTileN - tile0)); };
   int limit = 0;
   if (warp == kLoadWarp) {
-    limit = pair_seq0 + lane < p.n_seqs ? __ldcg(p.lens + pair_seq0 + lane) : 0;
     // one barrier per lane
     int count = 0;
     if (lane < kBarPFull) count = 8;                       // K, V tiles: 4 conversion warps of both CTAs
@@ -304,16 +303,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) shared_
     if (count) mbar_init(bars + 8 * lane, count);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     if (lane < 8) ctl[1 + lane] = 0;
+    if (lane == 0) {
+      asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_k)) : "memory");
+      asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_v)) : "memory");
+    }
+  }
+  if (warp == kIssueWarp) tmem_alloc_pair(sb + kCtlOff, kTmemCols);
+  // Launched behind the splits of the sequences' own cells, this kernel takes its places
+  // as their CTAs leave.  Lengths, page table, queries and pages come from the kernels
+  // before that one, which only this wait makes visible here
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (warp == kLoadWarp) {
+    limit = pair_seq0 + lane < p.n_seqs ? __ldcg(p.lens + pair_seq0 + lane) : 0;
     limit = min(p.cells, min(p.max_seq_len, __reduce_max_sync(kFull, max(limit, 0))));
     if (lane == 0) {
       ctl[12] = limit;
       ctl[13] = tiles_of(limit);
-      asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_k)) : "memory");
-      asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_v)) : "memory");
     }
     __syncwarp();
   }
-  if (warp == kIssueWarp) tmem_alloc_pair(sb + kCtlOff, kTmemCols);
 
   // ---- the load warp's copies of tile i into a stage: raw tiles by TMA (per-thread
   // copies cost the conversion warps 870 clocks a tile: each touches 32 rows).  Page
@@ -831,13 +839,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) shared_
   __syncthreads();
   if (tid == 0 && ctl[1]) record_status(p.status, K8V4_ECUDA);
   cluster_barrier();          // no product, commit or arrival of the pair is in flight
-  // launched behind the splits of the sequences' own cells, this kernel starts as
-  // their CTAs leave: all of them have then seen the kernels before them complete,
-  // whose results are read here through L2 (ld.cg, TMA); what those CTAs write is not
-  // read.  (With this wait ahead of the first read: 56.2 us where this takes 54.9, 32
-  // sequences on 32,768 cells.)  The combine waits for this kernel alone, so this one
-  // ends after them
-  asm volatile("griddepcontrol.wait;" ::: "memory");
   if (warp == kIssueWarp) {
     tc_fence_after();
     tmem_dealloc_pair(tmem, kTmemCols);
