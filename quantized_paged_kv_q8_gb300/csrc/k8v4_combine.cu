@@ -29,7 +29,7 @@ constexpr int kRoundFew = 3;
 // src + b * b_stride + s * split_stride + rr * kPStride
 template <int R>
 __global__ void __launch_bounds__(256, R <= kRoundFew ? 8 : 4)
-    combine_kernel(const float* __restrict__ src, int splits, int64_t split_stride, int64_t b_stride, int rows_per_b,
+    combine_kernel(const float* src, int splits, int64_t split_stride, int64_t b_stride, int rows_per_b,
                    float* __restrict__ out, int write_partial) {
   __shared__ float wm[8], wl[8], wacc[8][32];
   asm volatile("griddepcontrol.wait;" ::: "memory");

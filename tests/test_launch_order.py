@@ -51,3 +51,12 @@ def test_nothing_is_read_ahead_of_the_wait(name, params, body):
     reads = re.findall(r"__ld\w+\(|\bld\.\w*\.?global|tma_load\w*\(|bulk_load\(|load_tile\(|cp_async\w*\(|cp\.async|"
                        r"prefetch\.global|load\w*8\w*\(|\b(?:p|a|C)\.(?:pt|lens|pos|steps|q|k|v|pages|table)\b", ahead)
     assert not reads, reads
+
+
+@each
+def test_nothing_goes_through_the_read_only_path(name, params, body):
+    """The read-only path may keep what it read before the writes of the grid before it: neither const __restrict__
+    parameters nor its load instructions in such a kernel."""
+    for p in params.split(","):
+        assert not ("const" in p.split("*")[0] and "*" in p and "__restrict__" in p), p
+    assert not re.findall(r"__ldg\(|\.nc\b", body)
