@@ -109,7 +109,7 @@ __global__ void __launch_bounds__(256, R <= kRoundFew ? 8 : 4)
 // o, and 16,384 such CTAs took 28 us for 2,048 rows of 20 splits (1.5 TB/s).  Here
 // the weights 2^(m_s - M) are worked out once per row in shared memory while the
 // first o rows are under way, and a warp reads 1 KB of a split at a time.
-constexpr int kRowWarps = 4, kRowUnroll = 4, kRowMaxSplits = 2048;
+constexpr int kRowWarps = 4, kRowUnroll = 4, kRowMaxSplits = kPrefixMaxSplits + kDecodeMaxSplits;
 
 __global__ void __launch_bounds__(32 * kRowWarps) combine_rows_kernel(const float* src, int splits,
                                                                       int64_t split_stride, int64_t b_stride,
@@ -218,7 +218,6 @@ int launch_combine(const Launch& L, const float* ws, int splits, int n_seqs, int
 int launch_combine_rows(const Launch& L, const float* ws, int splits, int n_seqs, int H, float* out) {
   const int rows_per_b = H * kGqa;
   const int64_t split_stride = static_cast<int64_t>(rows_per_b) * kPStride;
-  if (splits > kRowMaxSplits) return launch_combine(L, ws, splits, n_seqs, 1, H, out);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(n_seqs * rows_per_b);
   cfg.blockDim = dim3(32 * kRowWarps);

@@ -143,6 +143,8 @@ struct AttendPlan {
   int n_q, n_groups, warps, splits, cells_per_split;
   size_t ws_bytes;
 };
+// most cell ranges that a sequence's decode, and a shared prefix, are split into
+constexpr int kDecodeMaxSplits = 1024, kPrefixMaxSplits = 256;
 AttendPlan plan_attend(const CacheView& C, int n_seqs, int n_q, int max_seq_len, int num_sms);
 // k_new / v_new (n_q = 1 only): append each sequence's newest token (cell
 // steps[b] - 1) from them before attending -- the fused decode step

@@ -1454,7 +1454,7 @@ AttendPlan plan_decode(const CacheView& C, int n_seqs, int max_seq_len, int num_
   // a CTA's streaming: without it, 32 sequences of 8,192 cells chose 8 waves of
   // 27-tile CTAs (120 us) over one wave of 256-tile CTAs (75 us).
   constexpr int kCtaFixedTiles = 32;
-  const int max_splits = std::max(1, std::min(1024, tiles / (2 * kMaxWorkers)));
+  const int max_splits = std::max(1, std::min(kDecodeMaxSplits, tiles / (2 * kMaxWorkers)));
   int64_t best_cost = INT64_MAX;
   int best = 1;
   for (int sp = 1; sp <= max_splits; ++sp) {

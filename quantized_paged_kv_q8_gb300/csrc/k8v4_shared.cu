@@ -916,7 +916,7 @@ SharedPlan plan_shared(const CacheView& C, int n_seqs, int shared_len, int max_s
   constexpr int kFixedTiles = 9;
   const double rows = static_cast<double>(n_seqs) * C.H * kGqa;
   double best = 1e300;
-  for (int sp = 1; sp <= std::min(tiles, 256); ++sp) {
+  for (int sp = 1; sp <= std::min(tiles, kPrefixMaxSplits); ++sp) {
     const int tps = (tiles + sp - 1) / sp, real = (tiles + tps - 1) / tps;
     const double cost = static_cast<double>((units * real + slots - 1) / slots) * (tps + kFixedTiles) + real * rows / 4096.0;
     if (cost < best) {
