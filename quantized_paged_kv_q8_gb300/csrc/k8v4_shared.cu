@@ -171,12 +171,13 @@ __device__ __forceinline__ void mma_pair_ta(uint32_t d, uint32_t a, uint64_t b, 
       ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc)
       : "memory");
 }
-// completion of this thread's products so far -> the barrier at this offset of both CTAs
-__device__ __forceinline__ void commit_pair(uint32_t bar) {
-  const uint16_t both = 3;
+// completion of this thread's products so far -> the barrier at this offset of the CTAs
+// in the mask: both, or the leader alone
+constexpr uint16_t kBothCtas = 3, kLeaderCta = 1;
+__device__ __forceinline__ void commit_to(uint32_t bar, uint16_t ctas) {
   asm volatile(
       "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
-      "h"(both)
+      "h"(ctas)
       : "memory");
 }
 // one lane of a converged warp
@@ -762,7 +763,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) shared_
             qk(i, 0, kk);
             qk(i, 1, kk);
           }
-          commit_pair(bars + 8 * (kBarSFull + i));
+          commit_to(bars + 8 * (kBarSFull + i), kBothCtas);
         }
       }
       for (int i = 0; ok && i < n_tiles; ++i) {
@@ -788,9 +789,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) shared_
         if (leader) {
           pv(1, 1u);
           pv(2, 1u);
-          commit_pair(bars + 8 * kBarMost);
+          commit_to(bars + 8 * kBarMost, kLeaderCta);
           pv(3, 1u);
-          commit_pair(bars + 8 * (kBarODone + buf));
+          commit_to(bars + 8 * (kBarODone + buf), kBothCtas);
         }
         if (i + 2 < n_tiles) {
           // QK(i + 2) overwrites P(i) with its S0 half; the S1 half begins behind PV(i)
@@ -808,14 +809,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) shared_
               qk(buf, 0, kk);
               if (kk + kAhead < 8) qk(buf, 1, kk + kAhead);
             }
-            commit_pair(bars + 8 * (kBarSFull + buf));
+            commit_to(bars + 8 * (kBarSFull + buf), kBothCtas);
           }
         }
       }
       if (!ok) ctl[1] = 1;
-      // nothing of this warp's is in flight past here (after a failure too)
-      if (leader) commit_pair(bars + 8 * kBarDrain);
-      (void)mbar_wait(bars + 8 * kBarDrain, 0, kWaitDefaultNs);
+      // all of this warp's products, waited for below (after a failure too)
+      if (leader) commit_to(bars + 8 * kBarDrain, kBothCtas);
     } else if (__shfl_sync(kFull, warp, 0) == kLoadWarp) {
       // ============================================================== copies
       const bool leader = elect_one();
@@ -837,6 +837,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) shared_
   }
   tc_fence_before();
   __syncthreads();
+  // The commits arrive at the barriers of both CTAs, and each CTA waits for its own copies of
+  // the last ones: shared memory that an arrival is still on its way to must not be given
+  // to the next CTA.  (The row warps have waited for every S and the last O.)
+  if (warp == kIssueWarp) {
+    if (n_tiles > 1 && !ctl[1])
+      (void)mbar_wait(bars + 8 * (kBarODone + (n_tiles & 1)), ((n_tiles - 2) >> 1) & 1, kWaitDefaultNs);
+    (void)mbar_wait(bars + 8 * kBarDrain, 0, kWaitDefaultNs);
+    __syncwarp();
+  }
   if (tid == 0 && ctl[1]) record_status(p.status, K8V4_ECUDA);
   cluster_barrier();          // no product, commit or arrival of the pair is in flight
   if (warp == kIssueWarp) {

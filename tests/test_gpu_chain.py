@@ -6,6 +6,7 @@ import pytest
 import torch
 
 import quantized_paged_kv_q8_gb300 as k8
+from gpu_util import TOL, rel_err
 from test_gpu_rope import table_of
 
 pytestmark = pytest.mark.gpu
@@ -86,3 +87,30 @@ def test_steps_back_to_back(n_seqs, shared):
         assert torch.equal(got[0][name], want[0][name]), name
     assert torch.equal(got[1], want[1])
     assert all(bool(torch.isfinite(x).all()) for x in want[0].values())
+
+
+@pytest.mark.parametrize("n_seqs,shared,heads", [(128, 640, 2), (40, 1984, 2), (70, 1090, 8), (33, 4160, 1)])
+def test_short_sweeps_back_to_back(n_seqs, shared, heads):
+    """CTA pairs that sweep one to a few tiles, hundreds of such grids in a row: a pair's shared memory passes to the
+    next pair at once, and no completion of the first may reach it.  Every call gives the bits of the first."""
+    gen = torch.Generator(device="cuda").manual_seed(shared)
+    n_pages = -(-shared // P)
+    cache = k8.PagedCache(n_pages, P, heads)
+    pt = torch.randperm(n_pages, generator=gen, device="cuda").int()[None]
+    k, v = (torch.randn(1, shared, heads, 256, generator=gen, device="cuda").bfloat16() for _ in range(2))
+    k8.kv_append_k8v4(cache, pt, torch.zeros(1, dtype=torch.int64, device="cuda"), k, v)
+    ptd = pt.expand(n_seqs, -1).contiguous()
+    q = torch.randn(n_seqs, 8 * heads, 256, generator=gen, device="cuda").bfloat16()
+    lens = torch.randint(0, shared + 1, (n_seqs,), generator=gen, device="cuda").int()
+    assert k8.attn_k8v4_shared_workspace_bytes(cache, n_seqs, shared, shared) != k8.attn_k8v4_workspace_bytes(cache, n_seqs, 1, shared)
+    ws = k8.shared_workspace(cache, n_seqs, shared, shared)
+    outs = torch.full((200, n_seqs, 8 * heads, 256), float("nan"), device="cuda")
+    torch.cuda.synchronize()
+    for o in outs:
+        k8.attn_k8v4_decode_shared(cache, q, ptd, lens, shared, shared, o, ws)
+    torch.cuda.synchronize()
+    assert k8.k8v4_last_device_status() == 0
+    want = torch.empty_like(outs[0])
+    k8.attn_k8v4_decode(cache, q, ptd, lens, shared, want, k8.workspace(cache, n_seqs, 1, shared))
+    assert rel_err(outs[0].cpu().numpy(), want.cpu().numpy()) <= 2 * TOL     # each is within TOL of the exact result
+    assert bool((outs == outs[:1]).all())
