@@ -455,7 +455,9 @@ int kv_dequant_k8v4(const k8v4_cache* cache, const int32_t* page_table, int64_t 
   int rc = view_of(cache, &C);
   if (rc) return rc;
   if ((rc = check_table(C, page_table, max_pages))) return rc;
-  if (start < 0 || n_cells < 0 || start + n_cells > max_pages * C.P) return K8V4_EINVAL;
+  // no sum that can pass 64 bits; the kernel takes cells to be inside the table, below 2^31
+  const int64_t cells = max_pages * C.P;
+  if (start < 0 || n_cells < 0 || start > cells || n_cells > cells - start) return K8V4_EINVAL;
   if (n_cells == 0) return K8V4_OK;
   if (!k_out || !v_rot_out) return K8V4_EINVAL;
   if (!aligned(k_out, 16) || !aligned(v_rot_out, 16) || (v_out && !aligned(v_out, 16))) return K8V4_EALIGN;
