@@ -92,6 +92,12 @@ int check_table(const CacheView& v, const int32_t* pt, int64_t max_pages) {
   return K8V4_OK;
 }
 
+// (token, head) items that an append indexes in 32 bits; no product that passes 64
+bool too_many(int32_t n_seqs, int32_t n_tok, int H) {
+  const int64_t tokens = static_cast<int64_t>(n_seqs) * n_tok, limit = int64_t(1) << 31;
+  return tokens >= limit || tokens * H >= limit;
+}
+
 // The host mirror of a streamed cache: the same format, P and H as the device
 // cache, pages in page-locked host memory that the device can address.  Called
 // after make_launch (needs the device context); `M` gets the device-side address.
@@ -157,6 +163,7 @@ int kv_append_k8v4(const k8v4_cache* cache, const int32_t* page_table, int64_t m
   if (n_seqs == 0 || n_tok == 0) return K8V4_OK;
   if (!pos || !k || !v) return K8V4_EINVAL;
   if (!aligned(k, 16) || !aligned(v, 16) || !aligned(pos, 8)) return K8V4_EALIGN;
+  if (too_many(n_seqs, n_tok, C.H)) return K8V4_EINVAL;
   Launch L;
   if ((rc = make_launch(stream, &L))) return rc;
   return launch_append(L, C, page_table, max_pages, n_seqs, pos, n_tok, k, v, dtype);
@@ -222,7 +229,7 @@ int kv_append_k8v4_rope(const k8v4_cache* cache, const int32_t* page_table, int6
   if ((rc = check_rows(k, k_stride, C.H, dtype)) || (rc = check_rows(v, v_stride, C.H, dtype))) return rc;
   if (!aligned(pos, 8)) return K8V4_EALIGN;
   if ((rc = check_weight(k_weight, eps))) return rc;
-  if (static_cast<int64_t>(n_seqs) * n_tok * C.H >= (int64_t(1) << 31)) return K8V4_EINVAL;
+  if (too_many(n_seqs, n_tok, C.H)) return K8V4_EINVAL;
   Launch L;
   if ((rc = make_launch(stream, &L))) return rc;
   return launch_append_rope(L, C, page_table, max_pages, n_seqs, pos, n_tok, k, k_stride, v, v_stride, dtype, k_weight,
@@ -478,6 +485,7 @@ int kv_append_k8v4_mirrored(const k8v4_cache* host, const k8v4_cache* dev, const
   if (n_seqs == 0 || n_tok == 0) return K8V4_OK;
   if (!pos || !k || !v || !slot_of_page) return K8V4_EINVAL;
   if (!aligned(k, 16) || !aligned(v, 16) || !aligned(pos, 8) || !aligned(slot_of_page, 4)) return K8V4_EALIGN;
+  if (too_many(n_seqs, n_tok, C.H)) return K8V4_EINVAL;
   Launch L;
   if ((rc = make_launch(stream, &L))) return rc;
   if ((rc = mirror_address(host, &M))) return rc;

@@ -29,3 +29,16 @@ def test_dequant_refuses_cells_behind_the_table(L, fmt, start, n):
 
 def test_dequant_takes_the_end_of_the_table(L):
     assert L.kv_dequant_k8v4(_desc(), FAKE, 4, 64, 0, FAKE, FAKE, None, None) == k8.OK
+
+
+@pytest.mark.parametrize("heads", [1, 2, 4, 8])
+@pytest.mark.parametrize("n,t", [(MAX32, MAX32), (1 << 30, MAX32), (1 << 30, 1 << 30), (1 << 15, 1 << 16), (MAX32, 2)])
+def test_appends_refuse_more_tokens_than_they_index(L, n, t, heads):
+    """n_seqs * n_tok * heads of 2^64 and more; the mirrored append takes the same sizes."""
+    d, rope = _desc(heads=heads), ctypes.byref(k8.k8v4_rope(FAKE, 64, 64, 0))
+    assert L.kv_append_k8v4(d, FAKE, 4, n, FAKE, t, FAKE, FAKE, k8.BF16, None) == k8.EINVAL
+    assert L.kv_append_k8v4_mirrored(d, d, FAKE, FAKE, 4, n, FAKE, t, FAKE, FAKE, k8.BF16, None) == k8.EINVAL
+    assert L.kv_append_k8v4_rope(d, FAKE, 4, n, FAKE, t, FAKE, 256 * heads, FAKE, 256 * heads, k8.BF16, None, 0.0, rope,
+                                 None) == k8.EINVAL
+    assert L.qk_norm_rope_k8v4(FAKE, 256 * heads, heads, None, 0, 0, k8.BF16, None, None, 0.0, FAKE, n, t, rope,
+                               ctypes.c_void_p(0x90000), None, None) == k8.EINVAL
