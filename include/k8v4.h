@@ -280,8 +280,9 @@ size_t attn_k8v4_shared_workspace_bytes(const k8v4_cache* cache, int32_t n_seqs,
  *             max_seq_len) bytes, 256-byte aligned; calls that may run at the
  *             same time (two streams, two graphs) need one each.
  * Other arguments as attn_k8v4_decode, in device memory.  K8V4 format, bf16 q.
- * Where the prefix is short or the sequences few, the call is attn_k8v4_decode;
- * else results agree with it to the attention's 2e-5 and are the same bits from
+ * Where the prefix is short or the sequences few, or while the runtime refuses the
+ * prefix kernel its shared memory, the call is attn_k8v4_decode (the workspace covers
+ * either); else results agree with it to the attention's 2e-5 and are the same bits from
  * call to call. */
 int attn_k8v4_decode_shared(const k8v4_cache* cache, const void* q, int32_t q_dtype, const int32_t* page_table,
                             int64_t max_pages, const int32_t* seq_lens, int32_t n_seqs, int32_t max_seq_len,

@@ -1,5 +1,6 @@
 // The extern "C" entry points declared in include/k8v4.h: host-side argument
 // validation, the per-device status word, and the launches.
+#include <algorithm>
 #include <atomic>
 #include <mutex>
 
@@ -318,8 +319,9 @@ int attn_k8v4_verify(const k8v4_cache* cache, const void* q, int32_t q_dtype, co
 
 // the splits of a shared-prefix decode: the prefix's, and those of the sequences'
 // own cells behind it
-static SharedPlan shared_plans(const CacheView& C, int n_seqs, int shared_len, int max_seq_len, int sms, AttendPlan* own) {
-  const SharedPlan pre = plan_shared(C, n_seqs, shared_len, max_seq_len, sms);
+static SharedPlan shared_plans(const CacheView& C, int n_seqs, int shared_len, int max_seq_len, int slots, int sms,
+                               AttendPlan* own) {
+  const SharedPlan pre = plan_shared(C, n_seqs, shared_len, max_seq_len, slots);
   *own = AttendPlan{};
   if (pre.cells == 0) *own = plan_attend(C, n_seqs, 1, max_seq_len, sms);
   else if (max_seq_len > pre.cells) *own = plan_decode(C, n_seqs, max_seq_len - pre.cells, sms);
@@ -339,10 +341,18 @@ size_t attn_k8v4_shared_workspace_bytes(const k8v4_cache* cache, int32_t n_seqs,
   if (view_of(cache, &C) != K8V4_OK || !shared_prefix_supported(C)) return 0;
   if (n_seqs < 0 || n_seqs > 65535 || shared_len < 0 || max_seq_len < 0) return 0;
   DeviceState* s = nullptr;
-  const int sms = device_state(&s) == K8V4_OK ? s->num_sms : 152;
+  const bool device = device_state(&s) == K8V4_OK;
+  const int sms = device ? s->num_sms : 152;
+  // For either route: the pair kernel's set-up may fail in one call and work in another. While
+  // it fails, for any number of pairs that the device may turn out to run at a time
+  const int slots = device ? shared_prefix_slots() : sms / 2;
   AttendPlan own;
-  const SharedPlan pre = shared_plans(C, n_seqs, shared_len, max_seq_len, sms, &own);
-  return shared_ws_bytes(C, pre, own, n_seqs);
+  size_t bytes = plan_attend(C, n_seqs, 1, max_seq_len, sms).ws_bytes;
+  for (int n = slots ? slots : 1; n <= (slots ? slots : sms / 2); ++n) {
+    const SharedPlan pre = shared_plans(C, n_seqs, shared_len, max_seq_len, n, sms, &own);
+    bytes = std::max(bytes, shared_ws_bytes(C, pre, own, n_seqs));
+  }
+  return bytes;
 }
 
 int attn_k8v4_decode_shared(const k8v4_cache* cache, const void* q, int32_t q_dtype, const int32_t* page_table,
@@ -363,7 +373,7 @@ int attn_k8v4_decode_shared(const k8v4_cache* cache, const void* q, int32_t q_dt
   Launch L;
   if ((rc = make_launch(stream, &L))) return rc;
   AttendPlan own;
-  const SharedPlan pre = shared_plans(C, n_seqs, shared_len, max_seq_len, L.num_sms, &own);
+  const SharedPlan pre = shared_plans(C, n_seqs, shared_len, max_seq_len, shared_prefix_slots(), L.num_sms, &own);
   if (workspace_bytes < shared_ws_bytes(C, pre, own, n_seqs)) return K8V4_ENOSPACE;
   if (pre.cells == 0)
     return launch_attend(L, C, own, q, q_dtype, page_table, max_pages, seq_lens, n_seqs, max_seq_len, sm_scale, out,

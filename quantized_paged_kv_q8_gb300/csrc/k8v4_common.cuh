@@ -202,7 +202,8 @@ struct SharedPlan {
   size_t acc_bytes = 0;      // running sums of the kernel's CTAs, behind the partial rows
 };
 bool shared_prefix_supported(const CacheView& C);
-SharedPlan plan_shared(const CacheView& C, int n_seqs, int shared_len, int max_seq_len, int num_sms);
+int shared_prefix_slots();   // CTA pairs at a time on the current device; 0 while the kernel's set-up fails
+SharedPlan plan_shared(const CacheView& C, int n_seqs, int shared_len, int max_seq_len, int slots);
 int launch_shared_prefix(const Launch& L, const CacheView& C, const SharedPlan& plan, const void* q, const int32_t* pt,
                          int64_t max_pages, const int32_t* lens, int n_seqs, int max_seq_len, float sm_scale, float* ws,
                          int ws_splits, float* acc, bool behind_splits);

@@ -859,28 +859,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) shared_
 // ---------------------------------------------------------------- host side
 bool shared_prefix_supported(const CacheView& C) { return C.fmt == K8V4_FORMAT_K8V4 && decode_ws_supported(C); }
 
-// The prefix cells that the pair kernel takes (0: none, every cell goes through
-// the per-sequence decode) and its splits.
+// Set-up of the kernel on the current device: its shared memory, its registers at launch
+// (the split hands out that many) and the CTA pairs that the device runs at a time (an
+// odd SM in a cluster's reach stays without a partner, so 152 SMs need not give 76).
+// Kept once it has worked; a failure is not, and the next call tries again.
 namespace {
-// Set-up of the kernel on the current device, once: its shared memory, its
-// registers at launch (the split hands out that many) and the CTA pairs that the
-// device runs at a time (an odd SM in a cluster's reach stays without a partner,
-// so 152 SMs need not give 76).
-struct PairSetup {
-  bool done = false, ok = false;
-  int slots = 0;
-};
-std::mutex g_setup_mu;
-PairSetup g_setup[64];
-PairSetup pair_setup() {
+std::mutex g_slots_mu;
+int g_slots[64];
+}  // namespace
+int shared_prefix_slots() {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) {
     cudaGetLastError();
-    return PairSetup{};
+    return 0;
   }
-  std::lock_guard<std::mutex> lock(g_setup_mu);
-  PairSetup& s = g_setup[dev];
-  if (s.done) return s;
+  std::lock_guard<std::mutex> lock(g_slots_mu);
+  if (g_slots[dev] > 0) return g_slots[dev];
   cudaFuncAttributes fa;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2);
@@ -892,20 +886,24 @@ PairSetup pair_setup() {
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  s.ok = cudaFuncGetAttributes(&fa, shared_prefix_kernel) == cudaSuccess &&
-         fa.numRegs * 6 >= 4 * kRowRegs + kConvRegs + kIssueRegs &&
-         cudaFuncSetAttribute(shared_prefix_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax) == cudaSuccess &&
-         cudaOccupancyMaxActiveClusters(&s.slots, shared_prefix_kernel, &cfg) == cudaSuccess && s.slots > 0;
-  if (!s.ok) cudaGetLastError();
-  s.done = true;
-  return s;
+  int slots = 0;
+  if (cudaFuncGetAttributes(&fa, shared_prefix_kernel) != cudaSuccess ||
+      fa.numRegs * 6 < 4 * kRowRegs + kConvRegs + kIssueRegs ||
+      cudaFuncSetAttribute(shared_prefix_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax) != cudaSuccess ||
+      cudaOccupancyMaxActiveClusters(&slots, shared_prefix_kernel, &cfg) != cudaSuccess || slots < 1) {
+    cudaGetLastError();                   // clear the error state that the failed call left
+    return 0;
+  }
+  return g_slots[dev] = slots;
 }
-}  // namespace
 
-SharedPlan plan_shared(const CacheView& C, int n_seqs, int shared_len, int max_seq_len, int num_sms) {
+// The prefix cells that the pair kernel takes (0: none, every cell goes through
+// the per-sequence decode) and its splits, for a device that runs `slots` CTA pairs at
+// a time (0: its set-up failed, none).
+SharedPlan plan_shared(const CacheView& C, int n_seqs, int shared_len, int max_seq_len, int slots) {
   SharedPlan pl{};
   const int cells = std::min(shared_len, max_seq_len) / 16 * 16;
-  if (!shared_prefix_supported(C) || cells < kTileN) return pl;
+  if (!shared_prefix_supported(C) || cells < kTileN || slots < 1) return pl;
   // Worth it where reading the prefix n_seqs times costs more than this kernel does.
   // Measured at 2 KV heads (64 own cells): the per-sequence decode takes 11 us + 0.23 us
   // per 1,000 cells of all sequences, this path 22 us + 0.72 us per 1,000 prefix
@@ -917,8 +915,6 @@ SharedPlan plan_shared(const CacheView& C, int n_seqs, int shared_len, int max_s
   pl.cells = cells;
   const int tiles = (cells + kTileN - 1) / kTileN;
   const int64_t units = groups * C.H;
-  const PairSetup setup = pair_setup();
-  const int slots = setup.ok ? setup.slots : std::max(1, num_sms / 2);
   // one pair per two SMs at a time: the split count that minimises waves x (tiles
   // a pair sweeps + the fixed cost of a pair, worth about kFixedTiles tiles) + the
   // partial rows of a split, written and read again (4,096 rows take a tile's time)
@@ -962,7 +958,6 @@ int launch_shared_prefix(const Launch& L, const CacheView& C, const SharedPlan& 
   p.page_div = FastDiv(static_cast<uint32_t>(C.P));
   p.stages = raw_stages(C.H);
   p.stage_bytes = raw_bytes(C.H);
-  if (!pair_setup().ok) return K8V4_ECUDA;
   CUtensorMap mk, mv;
   if (!tensor_maps_of(C, &mk, &mv)) return K8V4_ECUDA;
   const int groups = (n_seqs + kPairSeqs - 1) / kPairSeqs;
