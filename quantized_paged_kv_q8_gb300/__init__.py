@@ -190,14 +190,18 @@ _binding = None
 
 
 def _native():
-    """The loaded extension module (raises if it has not been built)."""
+    """The loaded extension module (raises if it has not been built, with the compiler's reason)."""
     global _binding
     if _binding is None:
+        from . import buildlib
         L = lib()
-        path = os.path.join(HERE, "_build", "_k8v4_binding.so")
-        if not os.path.exists(path):
-            raise RuntimeError(f"{path} is not built; call quantized_paged_kv_q8_gb300.build()")
-        spec = importlib.util.spec_from_file_location("_k8v4_binding", path)
+        if not os.path.exists(buildlib.BINDING):
+            why = "call quantized_paged_kv_q8_gb300.build()"
+            if os.path.exists(buildlib.BINDING_ERROR):
+                with open(buildlib.BINDING_ERROR) as f:
+                    why = f.read()
+            raise RuntimeError(f"{buildlib.BINDING} is not built; {why}")
+        spec = importlib.util.spec_from_file_location("_k8v4_binding", buildlib.BINDING)
         m = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(m)
         m.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in

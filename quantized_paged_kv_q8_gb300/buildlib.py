@@ -9,12 +9,14 @@ import shutil
 import subprocess
 import sys
 import sysconfig
+import warnings
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libk8v4.so")
 BINDING = os.path.join(BUILD, "_k8v4_binding.so")
+BINDING_ERROR = os.path.join(BUILD, "binding_error.log")      # why the module could not be built, if so
 SOURCES = ["k8v4_api.cu", "k8v4_append.cu", "k8v4_attend.cu", "k8v4_decode.cu", "k8v4_verify.cu", "k8v4_combine.cu", "k8v4_prefill.cu", "k8v4_noalloc.cu",
            "k8v4_stream.cu", "k8v4_rope.cu", "k8v4_append_rope.cu", "k8v4_accept.cu", "k8v4_shared.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -37,42 +39,41 @@ def _compile(src: str) -> tuple[str, str]:
     return obj, r.stderr
 
 
-def _compile_binding() -> str:
-    """The extension module that checks tensors for the calls of csrc/k8v4_binding.cpp."""
-    import torch
-    base = os.path.dirname(torch.__file__)
-    inc = [os.path.join(base, "include"), sysconfig.get_paths()["include"],
-           os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")]
+def _compile_binding() -> str | None:
+    """Build the extension module that checks tensors for the calls of csrc/k8v4_binding.cpp.
+    Returns why it could not be built (no Python headers, a torch whose headers do not
+    compile, ...), or None."""
     tmp = BINDING + f".tmp{os.getpid()}"
-    cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-w",
-           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *[f"-I{d}" for d in inc],
-           os.path.join(CSRC, "k8v4_binding.cpp"), "-o", tmp, f"-L{os.path.join(base, 'lib')}", "-ltorch_python",
-           "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"g++ failed on k8v4_binding.cpp:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, BINDING)
-    return BINDING
+    try:
+        import torch
+        base = os.path.dirname(torch.__file__)
+        inc = [os.path.join(base, "include"), sysconfig.get_paths()["include"],
+               os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")]
+        cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-w",
+               f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *[f"-I{d}" for d in inc],
+               os.path.join(CSRC, "k8v4_binding.cpp"), "-o", tmp, f"-L{os.path.join(base, 'lib')}", "-ltorch_python",
+               "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            return f"g++ failed on k8v4_binding.cpp:\n{r.stdout}\n{r.stderr}"
+        os.replace(tmp, BINDING)
+        return None
+    except (ImportError, OSError, RuntimeError) as e:
+        return f"k8v4_binding.cpp could not be compiled: {e}"
 
 
-def _stale() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(BINDING):
+def _stale(target: str) -> bool:
+    if not os.path.exists(target):
         return True
-    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
+    t = os.path.getmtime(target)
     deps = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
     deps.append(os.path.join(HERE, "..", "include", "k8v4.h"))
     deps.append(__file__)
     return any(os.path.getmtime(d) > t for d in deps if os.path.exists(d))
 
 
-def build(force: bool = False, verbose: bool = False) -> str:
-    os.makedirs(BUILD, exist_ok=True)
-    if not force and not _stale():
-        return LIB
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
-        binding = ex.submit(_compile_binding)
-        results = list(ex.map(_compile, SOURCES))
-        binding.result()
+def _build_library(ex: cf.Executor, verbose: bool) -> None:
+    results = list(ex.map(_compile, SOURCES))
     if verbose:
         for _, log in results:
             sys.stderr.write(log)
@@ -85,6 +86,25 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+
+
+def build(force: bool = False, verbose: bool = False) -> str:
+    """Build what is out of date.  The library needs nvcc alone: where the extension
+    module cannot be built, that is a warning here and an error in the calls that use it."""
+    os.makedirs(BUILD, exist_ok=True)
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        binding = ex.submit(_compile_binding) if force or _stale(BINDING) else None
+        if force or _stale(LIB):
+            _build_library(ex, verbose)
+        failed = binding.result() if binding else None
+    if binding and os.path.exists(BINDING_ERROR):
+        os.remove(BINDING_ERROR)
+    if failed:
+        if os.path.exists(BINDING):         # of older sources
+            os.remove(BINDING)
+        with open(BINDING_ERROR, "w") as f:
+            f.write(failed)
+        warnings.warn(f"libk8v4.so is built, its extension module is not: {failed}")
     return LIB
 
 
