@@ -195,12 +195,12 @@ def _native():
     if _binding is None:
         from . import buildlib
         L = lib()
-        if not os.path.exists(buildlib.BINDING):
+        if not buildlib.binding_built():
             why = "call quantized_paged_kv_q8_gb300.build()"
             if os.path.exists(buildlib.BINDING_ERROR):
                 with open(buildlib.BINDING_ERROR) as f:
                     why = f.read()
-            raise RuntimeError(f"{buildlib.BINDING} is not built; {why}")
+            raise RuntimeError(f"{buildlib.BINDING} is not built for this torch; {why}")
         spec = importlib.util.spec_from_file_location("_k8v4_binding", buildlib.BINDING)
         m = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(m)

@@ -39,6 +39,20 @@ def _compile(src: str) -> tuple[str, str]:
     return obj, r.stderr
 
 
+def _binding_tag() -> str:
+    """What the extension module is compiled against: another torch or Python has other C++ symbols."""
+    import torch
+    return f"torch {torch.__version__}, {sysconfig.get_config_var('SOABI')}"
+
+
+def binding_built() -> bool:
+    """Whether the extension module is there, for this torch and Python."""
+    if not os.path.exists(BINDING) or not os.path.exists(BINDING + ".tag"):
+        return False
+    with open(BINDING + ".tag") as f:
+        return f.read() == _binding_tag()
+
+
 def _compile_binding() -> str | None:
     """Build the extension module that checks tensors for the calls of csrc/k8v4_binding.cpp.
     Returns why it could not be built (no Python headers, a torch whose headers do not
@@ -56,7 +70,11 @@ def _compile_binding() -> str | None:
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
             return f"g++ failed on k8v4_binding.cpp:\n{r.stdout}\n{r.stderr}"
+        if os.path.exists(BINDING + ".tag"):
+            os.remove(BINDING + ".tag")
         os.replace(tmp, BINDING)
+        with open(BINDING + ".tag", "w") as f:
+            f.write(_binding_tag())
         return None
     except (ImportError, OSError, RuntimeError) as e:
         return f"k8v4_binding.cpp could not be compiled: {e}"
@@ -93,14 +111,14 @@ def build(force: bool = False, verbose: bool = False) -> str:
     module cannot be built, that is a warning here and an error in the calls that use it."""
     os.makedirs(BUILD, exist_ok=True)
     with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
-        binding = ex.submit(_compile_binding) if force or _stale(BINDING) else None
+        binding = ex.submit(_compile_binding) if force or _stale(BINDING) or not binding_built() else None
         if force or _stale(LIB):
             _build_library(ex, verbose)
         failed = binding.result() if binding else None
     if binding and os.path.exists(BINDING_ERROR):
         os.remove(BINDING_ERROR)
     if failed:
-        if os.path.exists(BINDING):         # of older sources
+        if os.path.exists(BINDING):         # of older sources, or for another torch
             os.remove(BINDING)
         with open(BINDING_ERROR, "w") as f:
             f.write(failed)

@@ -92,3 +92,27 @@ def test_a_library_that_does_not_compile_is_an_error(tools):
     with pytest.raises(RuntimeError, match="nvcc failed"):
         buildlib.build()
     assert not os.path.exists(buildlib.LIB)
+
+
+def test_the_extension_module_follows_torch_and_python(tools, monkeypatch):
+    """A module built against another torch or Python is not taken: their C++ symbols differ."""
+    import sysconfig
+
+    import torch
+    buildlib.build()
+    tools.calls("nvcc"), tools.calls("g++")
+    monkeypatch.setattr(torch, "__version__", "9.8.7+other")
+    buildlib.build()
+    assert tools.calls("nvcc") == 0 and tools.calls("g++") == 1
+    buildlib.build()
+    assert tools.calls("g++") == 0
+    real = sysconfig.get_config_var
+    monkeypatch.setattr(sysconfig, "get_config_var", lambda name: "cpython-999" if name == "SOABI" else real(name))
+    buildlib.build()
+    assert tools.calls("nvcc") == 0 and tools.calls("g++") == 1
+    # not built for this pair, and not to be loaded for it
+    monkeypatch.setattr(torch, "__version__", "9.8.8")
+    monkeypatch.setattr(k8, "_binding", None)
+    monkeypatch.setattr(k8, "lib", lambda: None)
+    with pytest.raises(RuntimeError, match="not built"):
+        k8.spec_accept_k8v4(None, None, None, None, None, None, None)
