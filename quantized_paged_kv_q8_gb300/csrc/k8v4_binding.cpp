@@ -78,6 +78,12 @@ int64_t token_stride(const at::Tensor& t, int64_t heads, const char* name) {
   return t.stride(1);
 }
 
+bool truth(PyObject* o) {
+  const int v = PyObject_IsTrue(o);
+  if (v < 0) throw Raised{};
+  return v == 1;
+}
+
 k8v4_rope rope_of(PyObject* table, PyObject* interleaved, int dev) {
   const at::Tensor& t = tensor(table, "rope_table");
   if (t.dim() != 2) bad("rope_table: [n_pos, rot_dim] expected");
@@ -85,7 +91,7 @@ k8v4_rope rope_of(PyObject* table, PyObject* interleaved, int dev) {
   r.table = static_cast<const float*>(flat(t, t.numel(), at::kFloat, dev, "rope_table"));
   r.n_pos = t.size(0);
   r.rot_dim = fits(t.size(1), "rope_table");
-  r.interleaved = PyObject_IsTrue(interleaved) == 1;
+  r.interleaved = truth(interleaved);
   return r;
 }
 
