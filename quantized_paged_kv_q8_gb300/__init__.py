@@ -164,10 +164,13 @@ class PagedCache:
         assert pages.dtype == torch.uint8 and pages.numel() == nbytes and pages.is_contiguous()
         self.pages = pages
         self.desc = k8v4_cache(ctypes.c_void_p(pages.data_ptr()), n_pages, page_size, n_kv_heads, HEAD_DIM, fmt)
-        self.address = ctypes.addressof(self.desc)
 
     def ref(self):
         return ctypes.byref(self.desc)
+
+    @property
+    def address(self) -> int:
+        return ctypes.addressof(self.desc)
 
 
 def kv_append_k8v4(cache: PagedCache, page_table: torch.Tensor, pos: torch.Tensor, k: torch.Tensor,
