@@ -7,11 +7,13 @@
 // written to memory nor read back (1,024 B a cell each way in bf16).  K and V
 // rows may be slices of a packed projection (a stride between tokens).
 //
-// What bounds it: as the plain append, instruction issue (the exact rotation
-// and quantisation of V) with HBM behind it; the rotation of K adds one table
-// row per token, which the heads of the token share through L1.  Measured: 32,768
-// tokens of 2 heads in bf16, all 256 elements rotated: 64 us (127 MB, 2.0 TB/s; 62% of
-// the issue slots), 46 for the plain append; 32 sequences of one token: 4.3 us.
+// What bounds it: the instructions of a row (the exact rotation and quantisation of
+// V, as in the plain append, and the rotation of K with its errors carried), issued on
+// 69% of the clocks while CTAs are resident; on the others the 24 warps of an SM wait
+// for one another's fixed latencies or for loads.  No single unit is full.  The table
+// row of a token is shared by its heads through L1.  Measured: 32,768 tokens of 2 heads
+// in bf16, all 256 elements rotated: 64 us (127 MB, 2.0 TB/s), 46 for the plain append;
+// 32 sequences of one token: 4.3 us.
 #include <algorithm>
 
 #include "k8v4_quant.cuh"
@@ -186,8 +188,8 @@ __global__ void __launch_bounds__(kWarps * 32, kBulkCtas) append_rope_bf16_kerne
     }
     const bool ok = in_range && base != nullptr;
     const int r = cslot * C.H + g;
-    // the next item: head, then token (its cell), then sequence; its table
-    // factors are loaded while this item is quantised
+    // the next item: head, then token (its cell), then sequence; its table row is
+    // prefetched while this item is quantised
     if (++g == C.H) {
       g = 0;
       if (++t == p.n_tok) {

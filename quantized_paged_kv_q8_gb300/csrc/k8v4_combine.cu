@@ -107,8 +107,8 @@ __global__ void __launch_bounds__(256, R <= kRoundFew ? 8 : 4)
 // Many rows with tens of splits each (a batch on a shared prefix): one CTA per row.
 // combine_kernel's eight CTAs per row each read every split's m and l for 128 B of
 // o, and 16,384 such CTAs took 28 us for 2,048 rows of 20 splits (1.5 TB/s).  Here
-// the weights 2^(m_s - M) are worked out once per row in shared memory while the
-// first o rows are under way, and a warp reads 1 KB of a split at a time.
+// the weights 2^(m_s - M) are worked out once per row in shared memory, and then a
+// warp reads 1 KB of a split at a time, only of splits with a weight.
 constexpr int kRowWarps = 4, kRowUnroll = 4, kRowMaxSplits = kPrefixMaxSplits + kDecodeMaxSplits;
 
 __global__ void __launch_bounds__(32 * kRowWarps) combine_rows_kernel(const float* src, int splits,

@@ -148,7 +148,6 @@ int launch_norm_rope(const Launch& L, const void* q, int64_t q_stride, int n_q, 
   p.half = rope.rot_dim / 2;
   p.q_out = q_out;
   p.k_out = k_out;
-  p.div_tok = FastDiv(static_cast<uint32_t>(n_tok));
   p.status = L.status;
   // one head per warp while the rows leave SMs idle (latency), else several
   const int64_t rows = p.n_tokens * (n_q + n_k);
