@@ -909,7 +909,7 @@ SharedPlan plan_shared(const CacheView& C, int n_seqs, int shared_len, int max_s
   // per 1,000 cells of all sequences, this path 22 us + 0.72 us per 1,000 prefix
   // cells and 32 sequences.  At 8 sequences they meet between 8,192 cells (21.8 us
   // against 27.4) and 16,384 (34.8 against 32.2), at 32 between 1,024 (19.4, 24.0) and
-  // 2,048 (26.9, 24.4), at 128 below 512 (43.2, 27.1); up to 3 sequences never.
+  // 2,048 (26.9, 24.4), at 128 below 512 (43.2, 31.7); up to 3 sequences never.
   const int64_t groups = (n_seqs + kPairSeqs - 1) / kPairSeqs;
   if (static_cast<int64_t>(C.H) * cells * (23ll * n_seqs - 72ll * groups) <= 2200000ll) return pl;
   pl.cells = cells;
