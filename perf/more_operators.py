@@ -310,8 +310,8 @@ def _plain_plan(s):
     total = n_free + back_ends[-1:]
     stack = torch.where(j < n_free, free, given[(j - n_free).clamp(min=0)])
     ok = fits & ((need == 0) | (asked <= total))
-    taken = torch.where(ok, asked, 0).amax()
     got = torch.where(ok, need, 0)
+    taken = got.sum()
     # entry k of the pages handed out is k below the top of the stack
     col = torch.arange(max_pages, device="cuda")
     k = (asked - need)[:, None] + col - have[:, None]
