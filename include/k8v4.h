@@ -112,6 +112,25 @@ typedef struct {
   int32_t interleaved; /* 0: pairs (i, i + rot_dim / 2); nonzero: pairs (2i, 2i + 1) */
 } k8v4_rope;
 
+/* The learned weights of a layer's differential heads (plain data, no ownership).
+ * Query head h's weight is
+ *   lambda_h = exp(q1_h . k1_h) - exp(q2_h . k2_h) + lambda_init
+ * over the four 128-vectors, or lambda_init alone where the vectors are NULL. */
+typedef struct {
+  const float* lambda_q1;   /* device, fp32 [n_lambda][128], 16-byte aligned; all four, or */
+  const float* lambda_k1;   /* none (NULL) */
+  const float* lambda_q2;
+  const float* lambda_k2;
+  int32_t n_lambda;         /* with vectors: 1 (one set for every query head) or 8 H (one each) */
+  float lambda_init;        /* finite */
+  const float* norm_weight; /* device, fp32 [256], 16-byte aligned, or NULL for no norm */
+  float eps;                /* >= 0, read only with a norm weight */
+  float out_scale;          /* finite; (1 - lambda_init) as published */
+} k8v4_diff;
+
+/* What a block's gate goes through before it multiplies. */
+typedef enum { K8V4_GATE_NONE = 0, K8V4_GATE_SIGMOID = 1, K8V4_GATE_SILU = 2 } k8v4_gate;
+
 /* Bytes per cell (all H heads) of a format: 816 for K8V4, 1,056 for INT8 and
  * 576 for Q4 at H = 2 (the three sizes the k8v4 PR compares in "What").
  * Returns 0 for an unknown format or H outside 1..8. */
@@ -374,6 +393,123 @@ int attn_k8v4_verify(const k8v4_cache* cache, const void* q, int32_t q_dtype, co
 int attn_k8v4_prefill(const k8v4_cache* cache, const void* q, int32_t q_dtype, const int32_t* page_table,
                       int64_t max_pages, int32_t seq_len, int32_t n_q_tok, const int32_t* step_arrays,
                       float sm_scale, float* out, void* stream);
+
+/* ---------------------------------------------------------------- a ragged batch's step
+ * The calls that let a step take prompts, chunks and single tokens of many
+ * sequences side by side: the tokens of all sequences are packed one behind the
+ * other, in the sequences' order, and no length comes back to the host. */
+
+/* Plan a step on the device: take back the pages of finished sequences, hand out
+ * pages for the new tokens, and write the block table's new entries and each new
+ * token's place.
+ *   n_new:     int32 [n_seqs]: tokens that sequence b gets (>= 0), or -1: it has
+ *              finished and gives its pages back.
+ *   seq_lens:  int32 [n_seqs], cells so far; its pages are the first
+ *              ceil(seq_lens[b] / page_size) entries of its table row.
+ *   n_borrowed: int32 [n_seqs] or NULL (0): leading pages of the row that are not the
+ *              sequence's own (a shared prefix), never given back.
+ *   free_pages, n_free: a stack of free page ids, int32 [n_pages], and its height.
+ *   page_table: int32 [n_seqs][max_pages]; only the entries of pages handed out are
+ *              written, behind those that the row has.
+ * Given-back pages go on the stack first, in (sequence, entry) order; then each
+ * sequence in order takes the pages it needs from the top.  A sequence whose pages
+ * are no longer all there gets none of its tokens (a later one that needs no page
+ * still does), nor does one that would pass max_pages pages or max_tokens packed
+ * tokens; its length stays and its tokens keep their place in the packing.
+ *   token_offsets: int32 [n_seqs + 1], where each sequence's n_new tokens begin (at
+ *              most max_tokens).
+ *   positions: int64 [max_tokens], the cell index of each token in its sequence (0 for
+ *              a token without a place);
+ *   slots:     int64 [max_tokens], page * page_size + slot of its cell, or -1 for a
+ *              token without a place (of a refused sequence, or behind the last token).
+ *   granted:   int32 [n_seqs], n_new where the tokens got their place, else 0.
+ *   new_lens:  int32 [n_seqs] (0 for a finished sequence); may be seq_lens.
+ *   n_free_out: int32 [1]; may be n_free.
+ * Apart from those two no two arrays overlap; no page is in two places of the stack and the own
+ * entries of the tables.  1 <= n_pages < 2^31, n_seqs <= 8192, n_seqs * max_pages < 2^31,
+ * 0 <= max_tokens.  Device-side (K8V4_ERANGE): a length or count out of range refuses
+ * the sequence, a page id outside [0, n_pages) in a finished row leaves the row as it is.
+ * K8V4_ENOSPACE is recorded when a sequence was refused for want of pages or
+ * max_tokens. */
+int kv_plan_k8v4(int32_t page_size, int64_t n_pages, int32_t* free_pages, const int32_t* n_free, int32_t* page_table,
+                 int64_t max_pages, const int32_t* seq_lens, const int32_t* n_new, const int32_t* n_borrowed,
+                 int32_t n_seqs, int32_t max_tokens, int32_t* token_offsets, int64_t* positions, int64_t* slots,
+                 int32_t* granted, int32_t* new_lens, int32_t* n_free_out, void* stream);
+
+/* Quantise packed tokens and write each to its slot: the bytes are those of
+ * kv_append_k8v4 at the cell that the slot names.
+ *   slots: int64 [n_tok], page * P + slot in [0, n_pages * P), all different, or -1: the
+ *          token is skipped.
+ *   k, v:  n_tok tokens of H heads x 256 of `dtype`, strides between tokens as in
+ *          qk_norm_rope_k8v4.
+ * Every format.  Device-side: any other slot is skipped and recorded (K8V4_ERANGE). */
+int kv_append_k8v4_slots(const k8v4_cache* cache, const int64_t* slots, int32_t n_tok, const void* k, int64_t k_stride,
+                         const void* v, int64_t v_stride, int32_t dtype, void* stream);
+
+/* ---------------------------------------------------------------- differential attention
+ * A query head and its keys are two heads of 128 lanes side by side, the halves of
+ * the cell's 256 (each has its own K scale), over one value of 256:
+ *   A_m = softmax(sm_scale * q_m . Khat_m),  m = 1, 2 (lanes [0, 128), [128, 256))
+ *   x   = A_1 . Vhat - lambda_h * A_2 . Vhat
+ *   out = out_scale * (x, or x / sqrt(mean(x^2) + eps) * norm_weight), in bf16.
+ * K8V4 format.  The maps are scored exactly as in the attention above; their
+ * probabilities and Vhat enter the products as fp16 (relative error 2^-12 each, a
+ * fraction of the result's own rounding), every sum is fp32.  q is bf16 or fp32 (rounded
+ * to fp16 after a power of two per row and map; bf16 is exact).  Rows that see no cell
+ * are 0.  The stored scales are finite. */
+
+/* Workspace bytes of attn_k8v4_diff_decode; 0 for another format or a bad size. */
+size_t attn_k8v4_diff_decode_workspace_bytes(const k8v4_cache* cache, int32_t n_seqs, int32_t max_seq_len);
+
+/* One query per sequence over its seq_lens[b] cells.
+ *   q:   [n_seqs][8 H][256] of q_dtype, 16-byte aligned; out: bf16 [n_seqs][8 H][256],
+ *        16-byte aligned.
+ *   sm_scale: (0, 1e30], 1 / sqrt(128) as published.
+ * Lengths, table and workspace as in attn_k8v4_decode (a workspace for each call that
+ * may run at the same time). */
+int attn_k8v4_diff_decode(const k8v4_cache* cache, const void* q, int32_t q_dtype, const int32_t* page_table,
+                          int64_t max_pages, const int32_t* seq_lens, int32_t n_seqs, int32_t max_seq_len,
+                          float sm_scale, const k8v4_diff* diff, void* out, void* workspace, size_t workspace_bytes,
+                          void* stream);
+
+/* Workspace bytes of attn_k8v4_diff; 0 for another format or a bad size. */
+size_t attn_k8v4_diff_workspace_bytes(const k8v4_cache* cache, int32_t n_seqs, int32_t n_tok, int32_t max_seq_len);
+
+/* A ragged batch: the queries of sequence b are the packed tokens token_offsets[b] ..
+ * token_offsets[b + 1] - 1, n_b of them, and stand for its last n_b cells: token t of
+ * them sees seq_lens[b] - n_b + t + 1 cells (causal), or, with steps, steps[token].
+ *   q:   [n_tok][8 H][256] of q_dtype; out: bf16 [n_tok][8 H][256]; 16-byte aligned.
+ *   token_offsets: int32 [n_seqs + 1] (device), from 0, not decreasing, at most n_tok;
+ *        rows of out behind the last sequence's are left as they were.
+ *   seq_lens: int32 [n_seqs] (device), each in [0, max_seq_len], the new cells included.
+ *   steps: int32 [n_tok] (device) or NULL; a count outside [0, seq_lens[b]] is clipped
+ *        and recorded.  Without steps, tokens ahead of the sequence's first cell (n_b >
+ *        seq_lens[b]) see none.
+ * n_seqs <= 65535, n_tok < 2^24.  Device-side: offsets out of order or out of range leave
+ * their sequence out (K8V4_ERANGE). */
+int attn_k8v4_diff(const k8v4_cache* cache, const void* q, int32_t q_dtype, const int32_t* token_offsets, int32_t n_tok,
+                   const int32_t* page_table, int64_t max_pages, const int32_t* seq_lens, const int32_t* steps,
+                   int32_t n_seqs, int32_t max_seq_len, float sm_scale, const k8v4_diff* diff, void* out,
+                   void* workspace, size_t workspace_bytes, void* stream);
+
+/* Between two blocks: a block's output normed, gated and scaled into the residual
+ * stream, and the next block's norm of the sum, one pass.  Per token, over dim elements:
+ *   a = y, or y / sqrt(mean(y^2) + eps) * post_weight
+ *   a = a * act(gate)                    (with a gate)
+ *   h = residual + residual_scale * a    (residual NULL: residual_scale * a)
+ *   n = h / sqrt(mean(h^2) + eps) * pre_weight   (with pre_weight; h as stored)
+ *   y:        n_tok rows of y_dtype, y_stride elements apart (>= dim).
+ *   gate:     rows of `dtype`, gate_stride apart (>= dim, or 0: one row for all), or NULL.
+ *   residual, h_out, n_out: contiguous [n_tok][dim] of `dtype`; h_out may be residual (in
+ *             place), or y where their types and layouts agree; no other two arrays
+ *             overlap.
+ *   post_weight, pre_weight: fp32 [dim] or NULL; n_out is written only with pre_weight.
+ * 1 <= dim <= 32768, any alignment of the element types (16-byte aligned rows are faster).
+ * All arithmetic is fp32; h and n are rounded once. */
+int block_norm_k8v4(const void* y, int64_t y_stride, int32_t y_dtype, int32_t n_tok, int32_t dim,
+                    const float* post_weight, const void* gate, int64_t gate_stride, int32_t gate_act,
+                    const void* residual, float residual_scale, const float* pre_weight, float eps, int32_t dtype,
+                    void* h_out, void* n_out, void* stream);
 
 /* Dequantise cells [start, start + n_cells) of one sequence, for checking (the
  * PR's gather entry points, "Tests": appends and gathers checked bitwise).

@@ -41,6 +41,12 @@ class k8v4_rope(ctypes.Structure):
                 ("interleaved", ctypes.c_int32)]
 
 
+class k8v4_diff(ctypes.Structure):
+    _fields_ = [("lambda_q1", ctypes.c_void_p), ("lambda_k1", ctypes.c_void_p), ("lambda_q2", ctypes.c_void_p),
+                ("lambda_k2", ctypes.c_void_p), ("n_lambda", ctypes.c_int32), ("lambda_init", ctypes.c_float),
+                ("norm_weight", ctypes.c_void_p), ("eps", ctypes.c_float), ("out_scale", ctypes.c_float)]
+
+
 _lib = None
 
 
@@ -83,6 +89,13 @@ def lib():
             "qk_norm_rope_k8v4": ([P, I64, I32, P, I64, I32, I32, P, P, F, P, I32, I32, P, P, P, P], ctypes.c_int),
             "kv_append_k8v4_rope": ([C, P, I64, I32, P, I32, P, I64, P, I64, I32, P, F, P, P], ctypes.c_int),
             "spec_accept_k8v4": ([P, P, I32, P, P, P, P, I32, I32, I32, P, P, P], ctypes.c_int),
+            "kv_plan_k8v4": ([I32, I64, P, P, P, I64, P, P, P, I32, I32, P, P, P, P, P, P, P], ctypes.c_int),
+            "kv_append_k8v4_slots": ([C, P, I32, P, I64, P, I64, I32, P], ctypes.c_int),
+            "attn_k8v4_diff_decode_workspace_bytes": ([C, I32, I32], SZ),
+            "attn_k8v4_diff_decode": ([C, P, I32, P, I64, P, I32, I32, F, P, P, P, SZ, P], ctypes.c_int),
+            "attn_k8v4_diff_workspace_bytes": ([C, I32, I32, I32], SZ),
+            "attn_k8v4_diff": ([C, P, I32, P, I32, P, I64, P, P, I32, I32, F, P, P, P, SZ, P], ctypes.c_int),
+            "block_norm_k8v4": ([P, I64, I32, I32, I32, P, P, I64, I32, P, F, P, F, I32, P, P, P], ctypes.c_int),
             "k8v4_set_wait_limit_ns": ([ctypes.c_uint32], None),
             "k8v4_set_withheld_copy": ([ctypes.c_int32], None),
         }
@@ -103,6 +116,8 @@ EXPORTED = ("k8v4_bytes_per_cell", "k8v4_status_string", "k8v4_device_check", "k
             "attn_k8v4_partial_workspace_bytes", "attn_k8v4_decode_partial", "attn_k8v4_combine_partials",
             "attn_k8v4_shared_workspace_bytes", "attn_k8v4_decode_shared",
             "qk_norm_rope_k8v4", "kv_append_k8v4_rope", "spec_accept_k8v4",
+            "kv_plan_k8v4", "kv_append_k8v4_slots", "attn_k8v4_diff_decode_workspace_bytes", "attn_k8v4_diff_decode",
+            "attn_k8v4_diff_workspace_bytes", "attn_k8v4_diff", "block_norm_k8v4",
             "k8v4_set_wait_limit_ns", "k8v4_set_withheld_copy")
 
 
@@ -208,7 +223,8 @@ def _native():
         m = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(m)
         m.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in
-                 (L.qk_norm_rope_k8v4, L.kv_append_k8v4_rope, L.spec_accept_k8v4, L.attn_k8v4_decode_shared)))
+                 (L.qk_norm_rope_k8v4, L.kv_append_k8v4_rope, L.spec_accept_k8v4, L.attn_k8v4_decode_shared, L.kv_plan_k8v4,
+                  L.kv_append_k8v4_slots, L.attn_k8v4_diff_decode, L.attn_k8v4_diff, L.block_norm_k8v4)))
         _binding = m
     return _binding
 
@@ -271,6 +287,124 @@ def spec_accept_k8v4(target_probs: torch.Tensor, draft_probs: torch.Tensor | Non
                                         n_accepted, n_drafts, stream if stream is None else _stream(stream))
     if rc:
         raise K8V4Error(rc, "spec_accept_k8v4")
+
+
+# ---------------------------------------------------------------- a ragged batch's step
+# The tokens of all sequences packed one behind the other; no length comes back to the host.
+def kv_plan_k8v4(page_size: int, free_pages: torch.Tensor, n_free: torch.Tensor, page_table: torch.Tensor,
+                 seq_lens: torch.Tensor, n_new: torch.Tensor, token_offsets: torch.Tensor, positions: torch.Tensor,
+                 slots: torch.Tensor, granted: torch.Tensor, new_lens: torch.Tensor | None = None,
+                 n_free_out: torch.Tensor | None = None, n_borrowed: torch.Tensor | None = None, stream=None) -> None:
+    """Pages for the new tokens of a step, and back from finished sequences (n_new -1), on the device.  int32: free_pages
+    [n_pages] (a stack), n_free [1], page_table [n_seqs, max_pages], seq_lens, n_new, granted, new_lens, n_borrowed
+    [n_seqs], token_offsets [n_seqs + 1], n_free_out [1]; int64: positions, slots [max_tokens].  Without new_lens and
+    n_free_out, seq_lens and n_free are moved on in place."""
+    rc = (_binding or _native()).plan(page_size, free_pages, n_free, page_table, seq_lens, n_new, n_borrowed, token_offsets,
+                                      positions, slots, granted, seq_lens if new_lens is None else new_lens,
+                                      n_free if n_free_out is None else n_free_out,
+                                      stream if stream is None else _stream(stream))
+    if rc:
+        raise K8V4Error(rc, "kv_plan_k8v4")
+
+
+def kv_append_k8v4_slots(cache: PagedCache, slots: torch.Tensor, k: torch.Tensor, v: torch.Tensor, stream=None) -> None:
+    """Packed tokens k, v [n_tok, H, 256] (possibly slices of a packed projection) written to their slots, int64 [n_tok]
+    (page * page_size + cell of the page, all different, or -1: skipped)."""
+    rc = (_binding or _native()).append_slots(cache.address, cache.pages, slots, k, v,
+                                              stream if stream is None else _stream(stream))
+    if rc:
+        raise K8V4Error(rc, "kv_append_k8v4_slots")
+
+
+class DifferentialHeads:
+    """The learned weights of a layer's differential heads: lambdas, the four vectors (q1, k1, q2, k2) as float32
+    [128] or [1, 128] (one set for all heads) or [8H, 128], or None; norm_weight float32 [256] or None.  The tensors
+    are kept, not copied: a change of their values counts from the next call on."""
+
+    def __init__(self, lambdas=None, lambda_init: float = 0.8, norm_weight: torch.Tensor | None = None, eps: float = 1e-6,
+                 out_scale: float = 1.0):
+        vectors = [] if lambdas is None else list(lambdas)
+        if vectors and (len(vectors) != 4 or any(x.shape != vectors[0].shape for x in vectors) or
+                        vectors[0].shape[-1:] != (128,) or vectors[0].dim() not in (1, 2)):
+            raise ValueError("lambdas: four tensors [128] or [n, 128] expected")
+        if norm_weight is not None and tuple(norm_weight.shape) != (HEAD_DIM,):
+            raise ValueError("norm_weight: [256] expected")
+        every = vectors + ([] if norm_weight is None else [norm_weight])
+        if any(x.dtype != torch.float32 or not x.is_contiguous() or x.device != every[0].device for x in every):
+            raise ValueError("lambdas, norm_weight: contiguous float32 tensors of one device expected")
+        if every and not every[0].is_cuda:
+            raise ValueError("lambdas, norm_weight: CUDA tensors expected")
+        self.tensors = every
+        self.device = every[0].get_device() if every else -1
+        at = [x.data_ptr() for x in vectors] or [None] * 4
+        n = vectors[0].numel() // 128 if vectors else 0
+        self.desc = k8v4_diff(*at, n, lambda_init, _ptr(norm_weight), eps, out_scale)
+
+    @property
+    def address(self) -> int:
+        return ctypes.addressof(self.desc)
+
+
+def attn_k8v4_diff_decode_workspace_bytes(cache: PagedCache, n_seqs: int, max_seq_len: int) -> int:
+    return int(lib().attn_k8v4_diff_decode_workspace_bytes(cache.ref(), n_seqs, max_seq_len))
+
+
+def diff_decode_workspace(cache: PagedCache, n_seqs: int, max_seq_len: int, device="cuda") -> torch.Tensor:
+    n = attn_k8v4_diff_decode_workspace_bytes(cache, n_seqs, max_seq_len)
+    return torch.empty(max(n, 256), dtype=torch.uint8, device=device)
+
+
+def attn_k8v4_diff_decode(cache: PagedCache, q: torch.Tensor, page_table: torch.Tensor, seq_lens: torch.Tensor,
+                          max_seq_len: int, heads: DifferentialHeads, out: torch.Tensor, ws: torch.Tensor,
+                          sm_scale: float = 128 ** -0.5, stream=None) -> torch.Tensor:
+    """Differential attention of one query per sequence: q [n_seqs, 8H, 256] (bf16 or f32); page_table int32
+    [n_seqs, max_pages]; seq_lens int32 [n_seqs]; out bfloat16 like q."""
+    rc = (_binding or _native()).diff_decode(cache.address, cache.pages, q, page_table, seq_lens, max_seq_len, heads.address,
+                                             heads.device, out, ws, sm_scale, stream if stream is None else _stream(stream))
+    if rc:
+        raise K8V4Error(rc, "attn_k8v4_diff_decode")
+    return out
+
+
+def attn_k8v4_diff_workspace_bytes(cache: PagedCache, n_seqs: int, n_tok: int, max_seq_len: int) -> int:
+    return int(lib().attn_k8v4_diff_workspace_bytes(cache.ref(), n_seqs, n_tok, max_seq_len))
+
+
+def diff_workspace(cache: PagedCache, n_seqs: int, n_tok: int, max_seq_len: int, device="cuda") -> torch.Tensor:
+    n = attn_k8v4_diff_workspace_bytes(cache, n_seqs, n_tok, max_seq_len)
+    return torch.empty(max(n, 256), dtype=torch.uint8, device=device)
+
+
+def attn_k8v4_diff(cache: PagedCache, q: torch.Tensor, token_offsets: torch.Tensor, page_table: torch.Tensor,
+                   seq_lens: torch.Tensor, max_seq_len: int, heads: DifferentialHeads, out: torch.Tensor, ws: torch.Tensor,
+                   steps: torch.Tensor | None = None, sm_scale: float = 128 ** -0.5, stream=None) -> torch.Tensor:
+    """Differential attention of a ragged batch: q [n_tok, 8H, 256] (bf16 or f32), the tokens of sequence b at
+    token_offsets[b] .. token_offsets[b + 1] - 1 (int32 [n_seqs + 1]), the last cells of its seq_lens[b] (int32, the new
+    ones included), causal or seeing steps int32 [n_tok] cells; page_table int32 [n_seqs, max_pages]; out bfloat16 like q."""
+    rc = (_binding or _native()).diff(cache.address, cache.pages, q, token_offsets, page_table, seq_lens, steps, max_seq_len,
+                                      heads.address, heads.device, out, ws, sm_scale,
+                                      stream if stream is None else _stream(stream))
+    if rc:
+        raise K8V4Error(rc, "attn_k8v4_diff")
+    return out
+
+
+_GATES = {"none": 0, "sigmoid": 1, "silu": 2}
+
+
+def block_norm_k8v4(y: torch.Tensor, residual: torch.Tensor | None, h: torch.Tensor, post_weight: torch.Tensor | None = None,
+                    gate: torch.Tensor | None = None, gate_act: str = "none", residual_scale: float = 1.0,
+                    pre_weight: torch.Tensor | None = None, normed: torch.Tensor | None = None, eps: float = 1e-6,
+                    stream=None) -> None:
+    """h = residual + residual_scale * act(gate) * norm(y) * post_weight and normed = norm(h) * pre_weight, each part but h
+    optional.  y [n_tok, dim] (rows may be spaced); residual, h, normed contiguous of one dtype; gate of that dtype
+    [n_tok, dim] or [dim] (one row for all); weights float32 [dim].  h may be residual."""
+    if gate_act not in _GATES:
+        raise ValueError(f"gate_act: one of {', '.join(_GATES)} expected")
+    rc = (_binding or _native()).block_norm(y, residual, h, post_weight, gate, _GATES[gate_act], residual_scale, pre_weight,
+                                            normed, eps, stream if stream is None else _stream(stream))
+    if rc:
+        raise K8V4Error(rc, "block_norm_k8v4")
 
 
 def attn_k8v4_workspace_bytes(cache: PagedCache, n_seqs: int, n_q: int, max_seq_len: int) -> int:

@@ -2,9 +2,10 @@
 // validation, the per-device status word, and the launches.
 #include <algorithm>
 #include <atomic>
+#include <cmath>
 #include <mutex>
 
-#include "k8v4_common.cuh"
+#include "k8v4_ops.cuh"
 
 namespace k8v4 {
 namespace {
@@ -481,6 +482,152 @@ int kv_dequant_k8v4(const k8v4_cache* cache, const int32_t* page_table, int64_t 
   Launch L;
   if ((rc = make_launch(stream, &L))) return rc;
   return launch_dequant(L, C, page_table, max_pages, start, n_cells, k_out, v_rot_out, v_out);
+}
+
+// ---------------------------------------------------------------- a ragged batch's step
+int kv_plan_k8v4(int32_t page_size, int64_t n_pages, int32_t* free_pages, const int32_t* n_free, int32_t* page_table,
+                 int64_t max_pages, const int32_t* seq_lens, const int32_t* n_new, const int32_t* n_borrowed,
+                 int32_t n_seqs, int32_t max_tokens, int32_t* token_offsets, int64_t* positions, int64_t* slots,
+                 int32_t* granted, int32_t* new_lens, int32_t* n_free_out, void* stream) {
+  if (page_size < 16 || page_size > 4096 || page_size % 16) return K8V4_EINVAL;
+  if (n_pages < 1 || n_pages >= (int64_t(1) << 31)) return K8V4_EINVAL;
+  if (n_seqs < 0 || n_seqs > kPlanMaxSeqs || max_tokens < 0) return K8V4_EINVAL;
+  if (max_pages < 1 || max_pages > (int64_t(1) << 31) / page_size) return K8V4_EINVAL;
+  if (n_seqs * max_pages >= (int64_t(1) << 31)) return K8V4_EINVAL;
+  if (!free_pages || !n_free || !n_free_out || !token_offsets) return K8V4_EINVAL;
+  if (n_seqs > 0 && (!page_table || !seq_lens || !n_new || !granted || !new_lens)) return K8V4_EINVAL;
+  if (max_tokens > 0 && (!positions || !slots)) return K8V4_EINVAL;
+  if (!aligned(free_pages, 4) || !aligned(n_free, 4) || !aligned(page_table, 4) || !aligned(seq_lens, 4) ||
+      !aligned(n_new, 4) || !aligned(n_borrowed, 4) || !aligned(token_offsets, 4) || !aligned(positions, 8) ||
+      !aligned(slots, 8) || !aligned(granted, 4) || !aligned(new_lens, 4) || !aligned(n_free_out, 4))
+    return K8V4_EALIGN;
+  Launch L;
+  int rc = make_launch(stream, &L);
+  if (rc) return rc;
+  return launch_plan(L, PlanArgs{page_size, n_pages, free_pages, n_free, page_table, max_pages, seq_lens, n_new, n_borrowed,
+                                 n_seqs, max_tokens, token_offsets, positions, slots, granted, new_lens, n_free_out});
+}
+
+int kv_append_k8v4_slots(const k8v4_cache* cache, const int64_t* slots, int32_t n_tok, const void* k, int64_t k_stride,
+                         const void* v, int64_t v_stride, int32_t dtype, void* stream) {
+  CacheView C;
+  int rc = view_of(cache, &C);
+  if (rc) return rc;
+  if (n_tok < 0 || (dtype != K8V4_F32 && dtype != K8V4_BF16)) return K8V4_EINVAL;
+  if (n_tok == 0) return K8V4_OK;
+  if (!slots) return K8V4_EINVAL;
+  if ((rc = check_rows(k, k_stride, C.H, dtype)) || (rc = check_rows(v, v_stride, C.H, dtype))) return rc;
+  if (!aligned(slots, 8)) return K8V4_EALIGN;
+  if (too_many(2, n_tok, C.H)) return K8V4_EINVAL;        // warp indices stay below 2^31
+  Launch L;
+  if ((rc = make_launch(stream, &L))) return rc;
+  return launch_append_slots(L, C, slots, n_tok, k, k_stride, v, v_stride, dtype);
+}
+
+static int check_diff(const k8v4_diff* d, int H) {
+  if (!d) return K8V4_EINVAL;
+  const float* v[4] = {d->lambda_q1, d->lambda_k1, d->lambda_q2, d->lambda_k2};
+  for (const float* x : v) {
+    if (!x != !v[0]) return K8V4_EINVAL;
+    if (!aligned(x, 16)) return K8V4_EALIGN;
+  }
+  if (v[0] && d->n_lambda != 1 && d->n_lambda != kGqa * H) return K8V4_EINVAL;
+  if (!(std::abs(d->lambda_init) <= 3e38f) || !(std::abs(d->out_scale) <= 3e38f)) return K8V4_EINVAL;
+  return check_weight(d->norm_weight, d->eps);
+}
+
+size_t attn_k8v4_diff_decode_workspace_bytes(const k8v4_cache* cache, int32_t n_seqs, int32_t max_seq_len) {
+  CacheView C;
+  if (view_of(cache, &C) != K8V4_OK || !diff_supported(C)) return 0;
+  if (n_seqs < 0 || n_seqs > 65535 || max_seq_len < 0) return 0;
+  DeviceState* s = nullptr;
+  const int sms = device_state(&s) == K8V4_OK ? s->num_sms : 152;
+  return plan_diff_decode(C, n_seqs, max_seq_len, sms).ws_bytes;
+}
+
+int attn_k8v4_diff_decode(const k8v4_cache* cache, const void* q, int32_t q_dtype, const int32_t* page_table,
+                          int64_t max_pages, const int32_t* seq_lens, int32_t n_seqs, int32_t max_seq_len,
+                          float sm_scale, const k8v4_diff* diff, void* out, void* workspace, size_t workspace_bytes,
+                          void* stream) {
+  CacheView C;
+  int rc = view_of(cache, &C);
+  if (rc) return rc;
+  if (!diff_supported(C) || (q_dtype != K8V4_F32 && q_dtype != K8V4_BF16)) return K8V4_EINVAL;
+  if ((rc = check_table(C, page_table, max_pages)) || (rc = check_diff(diff, C.H))) return rc;
+  if (n_seqs < 0 || n_seqs > 65535) return K8V4_EINVAL;
+  if (max_seq_len < 0 || static_cast<int64_t>(max_seq_len) > max_pages * C.P) return K8V4_EINVAL;
+  if (!(sm_scale > 0.0f) || sm_scale > 1e30f) return K8V4_EINVAL;
+  if (n_seqs == 0) return K8V4_OK;
+  if (!q || !seq_lens || !out || !workspace) return K8V4_EINVAL;
+  if (!aligned(q, 16) || !aligned(out, 16) || !aligned(workspace, 256) || !aligned(seq_lens, 4)) return K8V4_EALIGN;
+  Launch L;
+  if ((rc = make_launch(stream, &L))) return rc;
+  const DiffPlan plan = plan_diff_decode(C, n_seqs, max_seq_len, L.num_sms);
+  if (workspace_bytes < plan.ws_bytes) return K8V4_ENOSPACE;
+  return launch_diff_decode(L, C, plan, q, q_dtype, page_table, max_pages, seq_lens, n_seqs, max_seq_len, sm_scale, *diff,
+                            out, workspace);
+}
+
+size_t attn_k8v4_diff_workspace_bytes(const k8v4_cache* cache, int32_t n_seqs, int32_t n_tok, int32_t max_seq_len) {
+  CacheView C;
+  if (view_of(cache, &C) != K8V4_OK || !diff_supported(C)) return 0;
+  if (n_seqs < 0 || n_seqs > 65535 || n_tok < 0 || n_tok >= (1 << 24) || max_seq_len < 0) return 0;
+  DeviceState* s = nullptr;
+  const int sms = device_state(&s) == K8V4_OK ? s->num_sms : 152;
+  return diff_ws_bytes(C, n_seqs, n_tok, max_seq_len, sms);
+}
+
+int attn_k8v4_diff(const k8v4_cache* cache, const void* q, int32_t q_dtype, const int32_t* token_offsets, int32_t n_tok,
+                   const int32_t* page_table, int64_t max_pages, const int32_t* seq_lens, const int32_t* steps,
+                   int32_t n_seqs, int32_t max_seq_len, float sm_scale, const k8v4_diff* diff, void* out,
+                   void* workspace, size_t workspace_bytes, void* stream) {
+  CacheView C;
+  int rc = view_of(cache, &C);
+  if (rc) return rc;
+  if (!diff_supported(C) || (q_dtype != K8V4_F32 && q_dtype != K8V4_BF16)) return K8V4_EINVAL;
+  if ((rc = check_table(C, page_table, max_pages)) || (rc = check_diff(diff, C.H))) return rc;
+  if (n_seqs < 0 || n_seqs > 65535 || n_tok < 0 || n_tok >= (1 << 24)) return K8V4_EINVAL;
+  if (max_seq_len < 0 || static_cast<int64_t>(max_seq_len) > max_pages * C.P) return K8V4_EINVAL;
+  if (!(sm_scale > 0.0f) || sm_scale > 1e30f) return K8V4_EINVAL;
+  if (n_seqs == 0 || n_tok == 0) return K8V4_OK;
+  if (!q || !token_offsets || !seq_lens || !out || !workspace) return K8V4_EINVAL;
+  if (!aligned(q, 16) || !aligned(out, 16) || !aligned(workspace, 256) || !aligned(seq_lens, 4) ||
+      !aligned(token_offsets, 4) || !aligned(steps, 4))
+    return K8V4_EALIGN;
+  Launch L;
+  if ((rc = make_launch(stream, &L))) return rc;
+  if (workspace_bytes < diff_ws_bytes(C, n_seqs, n_tok, max_seq_len, L.num_sms)) return K8V4_ENOSPACE;
+  return launch_diff(L, C, q, q_dtype, token_offsets, n_tok, page_table, max_pages, seq_lens, steps, n_seqs, max_seq_len,
+                     sm_scale, *diff, out, workspace);
+}
+
+int block_norm_k8v4(const void* y, int64_t y_stride, int32_t y_dtype, int32_t n_tok, int32_t dim,
+                    const float* post_weight, const void* gate, int64_t gate_stride, int32_t gate_act,
+                    const void* residual, float residual_scale, const float* pre_weight, float eps, int32_t dtype,
+                    void* h_out, void* n_out, void* stream) {
+  if ((y_dtype != K8V4_F32 && y_dtype != K8V4_BF16) || (dtype != K8V4_F32 && dtype != K8V4_BF16)) return K8V4_EINVAL;
+  if (n_tok < 0 || dim < 1 || dim > kBlockNormMaxDim) return K8V4_EINVAL;
+  if (gate_act != K8V4_GATE_NONE && gate_act != K8V4_GATE_SIGMOID && gate_act != K8V4_GATE_SILU) return K8V4_EINVAL;
+  if (!(std::abs(residual_scale) <= 3e38f)) return K8V4_EINVAL;
+  if ((post_weight || pre_weight) && (!(eps >= 0.0f) || eps > 1e30f)) return K8V4_EINVAL;
+  if (n_tok == 0) return K8V4_OK;
+  if (!y || !h_out || (pre_weight && !n_out)) return K8V4_EINVAL;
+  constexpr int64_t kMostStride = int64_t(1) << 31;
+  if (y_stride < dim || y_stride > kMostStride) return K8V4_EINVAL;
+  if (gate && gate_stride != 0 && (gate_stride < dim || gate_stride > kMostStride)) return K8V4_EINVAL;
+  const uintptr_t ye = y_dtype == K8V4_BF16 ? 2 : 4, e = dtype == K8V4_BF16 ? 2 : 4;
+  if (!aligned(y, ye) || !aligned(gate, e) || !aligned(residual, e) || !aligned(h_out, e) ||
+      (pre_weight && !aligned(n_out, e)) || !aligned(post_weight, 4) || !aligned(pre_weight, 4))
+    return K8V4_EALIGN;
+  // in place: h over the residual, or over a y of its own layout; n over neither
+  if (h_out == gate || (h_out == y && (y_dtype != dtype || y_stride != dim))) return K8V4_EINVAL;
+  if (pre_weight && (n_out == h_out || n_out == residual || n_out == y || n_out == gate)) return K8V4_EINVAL;
+  Launch L;
+  int rc = make_launch(stream, &L);
+  if (rc) return rc;
+  return launch_block_norm(L, BlockNormArgs{y, y_stride, n_tok, dim, post_weight, gate, gate_stride, gate_act, residual,
+                                            residual_scale, pre_weight, eps, h_out, n_out},
+                           y_dtype, dtype);
 }
 
 int kv_append_k8v4_mirrored(const k8v4_cache* host, const k8v4_cache* dev, const int32_t* slot_of_page,

@@ -28,6 +28,11 @@ struct Api {
   decltype(&kv_append_k8v4_rope) append_rope = nullptr;
   decltype(&spec_accept_k8v4) accept = nullptr;
   decltype(&attn_k8v4_decode_shared) decode_shared = nullptr;
+  decltype(&kv_plan_k8v4) plan = nullptr;
+  decltype(&kv_append_k8v4_slots) append_slots = nullptr;
+  decltype(&attn_k8v4_diff_decode) diff_decode = nullptr;
+  decltype(&attn_k8v4_diff) diff = nullptr;
+  decltype(&block_norm_k8v4) block_norm = nullptr;
 } g_api;
 
 struct Bad {                       // a refused argument: what to say
@@ -271,20 +276,204 @@ PyObject* decode_shared(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
-// the addresses of the four C entry points, in the order of Api
+// tokens [n_tok, heads, 256], heads contiguous (a slice of a packed projection qualifies); the spacing in elements
+int64_t packed_stride(const at::Tensor& t, int64_t heads, const char* name) {
+  if (t.dim() != 3 || t.size(1) != heads || t.size(2) != 256)
+    bad(std::string(name) + ": [n_tok, " + std::to_string(heads) + ", 256] expected");
+  if (t.numel() > 0 && (t.stride(2) != 1 || (heads > 1 && t.stride(1) != 256)))
+    bad(std::string(name) + ": heads must be contiguous");
+  return t.size(0) > 1 ? t.stride(0) : heads * 256;
+}
+
+// page_size, free_pages, n_free, page_table, seq_lens, n_new, n_borrowed, token_offsets, positions, slots, granted,
+// new_lens, n_free_out, stream
+PyObject* plan(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 14, [&]() -> PyObject* {
+    const int32_t P = fits(integer(a[0]), "page_size");
+    const at::Tensor& pages = tensor(a[1], "free_pages");
+    const at::Tensor& table = tensor(a[3], "page_table");
+    if (table.dim() != 2) bad("page_table: [n_seqs, max_pages] expected");
+    const int dev = device_of(table);
+    const int32_t b = fits(table.size(0), "page_table");
+    const int64_t max_pages = table.size(1);
+    auto* free_pages = static_cast<int32_t*>(flat(pages, pages.numel(), at::kInt, dev, "free_pages"));
+    const auto* n_free = static_cast<const int32_t*>(flat(a[2], 1, at::kInt, dev, "n_free"));
+    auto* pt = static_cast<int32_t*>(flat(table, b * max_pages, at::kInt, dev, "page_table"));
+    auto* lens = static_cast<int32_t*>(flat(a[4], b, at::kInt, dev, "seq_lens"));
+    const auto* n_new = static_cast<const int32_t*>(flat(a[5], b, at::kInt, dev, "n_new"));
+    const auto* borrowed = static_cast<const int32_t*>(flat_or_null(a[6], b, at::kInt, dev, "n_borrowed"));
+    auto* offsets = static_cast<int32_t*>(flat(a[7], b + int64_t(1), at::kInt, dev, "token_offsets"));
+    const at::Tensor& positions = tensor(a[8], "positions");
+    const int32_t max_tokens = fits(positions.numel(), "positions");
+    auto* pos = static_cast<int64_t*>(flat(positions, max_tokens, at::kLong, dev, "positions"));
+    auto* slots = static_cast<int64_t*>(flat(a[9], max_tokens, at::kLong, dev, "slots"));
+    auto* granted = static_cast<int32_t*>(flat(a[10], b, at::kInt, dev, "granted"));
+    auto* new_lens = static_cast<int32_t*>(flat(a[11], b, at::kInt, dev, "new_lens"));
+    auto* n_free_out = static_cast<int32_t*>(flat(a[12], 1, at::kInt, dev, "n_free_out"));
+    return call(dev, a[13], [&](void* s) {
+      return g_api.plan(P, pages.numel(), free_pages, n_free, pt, max_pages, lens, n_new, borrowed, b, max_tokens, offsets, pos,
+                        slots, granted, new_lens, n_free_out, s);
+    });
+  });
+}
+
+// cache (address of its descriptor), pages, slots, k, v, stream
+PyObject* append_slots(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 6, [&]() -> PyObject* {
+    const auto* cache = address<const k8v4_cache>(a[0]);
+    const at::Tensor& k = tensor(a[3], "k");
+    const at::Tensor& v = tensor(a[4], "v");
+    const int dev = device_of(k), dtype = dtype_of(k, "k");
+    if (k.sizes() != v.sizes() || v.scalar_type() != k.scalar_type() || device_of(v) != dev ||
+        device_of(tensor(a[1], "pages")) != dev)
+      bad("k and v: one shape, dtype and device, the cache's");
+    const int64_t k_stride = packed_stride(k, cache->n_kv_heads, "k"), v_stride = packed_stride(v, cache->n_kv_heads, "v");
+    const int32_t n_tok = fits(k.size(0), "k");
+    const auto* slots = static_cast<const int64_t*>(flat(a[2], n_tok, at::kLong, dev, "slots"));
+    const void *kp = k.data_ptr(), *vp = v.data_ptr();
+    return call(dev, a[5], [&](void* s) { return g_api.append_slots(cache, slots, n_tok, kp, k_stride, vp, v_stride, dtype, s); });
+  });
+}
+
+// queries [n, 8H, 256] on the cache's device, contiguous, and their bf16 result
+struct Queries {
+  const void* q;
+  void* out;
+  int32_t n;
+  int dev, dtype;
+};
+Queries queries(const k8v4_cache* cache, PyObject* pages, PyObject* qo, PyObject* oo) {
+  const at::Tensor& q = tensor(qo, "q");
+  Queries r;
+  r.dev = device_of(q);
+  r.dtype = dtype_of(q, "q");
+  if (q.dim() != 3 || q.size(1) != 8 * static_cast<int64_t>(cache->n_kv_heads) || q.size(2) != 256 ||
+      device_of(tensor(pages, "pages")) != r.dev)
+    bad("q: [n, 8H, 256] on the cache's device expected");
+  r.n = fits(q.size(0), "q");
+  r.q = flat(q, q.numel(), q.scalar_type(), r.dev, "q");
+  r.out = flat(oo, q.numel(), at::kBFloat16, r.dev, "out");
+  return r;
+}
+// the weights of the heads: their struct's address, and the device that their tensors are on (-1: they have none)
+const k8v4_diff* heads_of(PyObject* addr, PyObject* device, int dev) {
+  const int64_t on = integer(device);
+  if (on >= 0 && on != dev) bad("heads: tensors on the device of q expected");
+  return address<const k8v4_diff>(addr);
+}
+
+// cache (address), pages, q, page_table, seq_lens, max_seq_len, heads (address), their device, out, ws, sm_scale, stream
+PyObject* diff_decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 12, [&]() -> PyObject* {
+    const auto* cache = address<const k8v4_cache>(a[0]);
+    const Queries q = queries(cache, a[1], a[2], a[8]);
+    const at::Tensor& table = tensor(a[3], "page_table");
+    if (table.dim() != 2 || table.size(0) != q.n) bad("page_table: [n_seqs, max_pages] expected");
+    const int64_t max_pages = table.size(1);
+    const auto* pt = static_cast<const int32_t*>(flat(table, q.n * max_pages, at::kInt, q.dev, "page_table"));
+    const auto* lens = static_cast<const int32_t*>(flat(a[4], q.n, at::kInt, q.dev, "seq_lens"));
+    const int32_t max_len = fits(integer(a[5]), "max_seq_len");
+    const k8v4_diff* heads = heads_of(a[6], a[7], q.dev);
+    const at::Tensor& ws = tensor(a[9], "ws");
+    void* wp = flat(ws, ws.numel(), at::kByte, q.dev, "ws");
+    const float scale = static_cast<float>(number(a[10]));
+    return call(q.dev, a[11], [&](void* s) {
+      return g_api.diff_decode(cache, q.q, q.dtype, pt, max_pages, lens, q.n, max_len, scale, heads, q.out, wp,
+                               static_cast<size_t>(ws.numel()), s);
+    });
+  });
+}
+
+// cache (address), pages, q, token_offsets, page_table, seq_lens, steps, max_seq_len, heads (address), their device, out, ws,
+// sm_scale, stream
+PyObject* diff(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 14, [&]() -> PyObject* {
+    const auto* cache = address<const k8v4_cache>(a[0]);
+    const Queries q = queries(cache, a[1], a[2], a[10]);
+    const at::Tensor& table = tensor(a[4], "page_table");
+    if (table.dim() != 2) bad("page_table: [n_seqs, max_pages] expected");
+    const int32_t n_seqs = fits(table.size(0), "page_table");
+    const int64_t max_pages = table.size(1);
+    const auto* offsets = static_cast<const int32_t*>(flat(a[3], n_seqs + int64_t(1), at::kInt, q.dev, "token_offsets"));
+    const auto* pt = static_cast<const int32_t*>(flat(table, n_seqs * max_pages, at::kInt, q.dev, "page_table"));
+    const auto* lens = static_cast<const int32_t*>(flat(a[5], n_seqs, at::kInt, q.dev, "seq_lens"));
+    const auto* steps = static_cast<const int32_t*>(flat_or_null(a[6], q.n, at::kInt, q.dev, "steps"));
+    const int32_t max_len = fits(integer(a[7]), "max_seq_len");
+    const k8v4_diff* heads = heads_of(a[8], a[9], q.dev);
+    const at::Tensor& ws = tensor(a[11], "ws");
+    void* wp = flat(ws, ws.numel(), at::kByte, q.dev, "ws");
+    const float scale = static_cast<float>(number(a[12]));
+    return call(q.dev, a[13], [&](void* s) {
+      return g_api.diff(cache, q.q, q.dtype, offsets, q.n, pt, max_pages, lens, steps, n_seqs, max_len, scale, heads, q.out, wp,
+                        static_cast<size_t>(ws.numel()), s);
+    });
+  });
+}
+
+// rows [n_tok, dim] with contiguous elements; the spacing of the rows
+int64_t row_stride(const at::Tensor& t, int64_t n_tok, int64_t dim, const char* name) {
+  if (t.dim() != 2 || t.size(0) != n_tok || t.size(1) != dim || (dim > 1 && t.numel() > 0 && t.stride(1) != 1))
+    bad(std::string(name) + ": [n_tok, dim] with contiguous rows expected");
+  return n_tok > 1 ? t.stride(0) : dim;
+}
+
+// y, residual, h, post_weight, gate, gate_act, residual_scale, pre_weight, normed, eps, stream
+PyObject* block_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 11, [&]() -> PyObject* {
+    const at::Tensor& y = tensor(a[0], "y");
+    const at::Tensor& h = tensor(a[2], "h");
+    if (y.dim() != 2) bad("y: [n_tok, dim] expected");
+    const int dev = device_of(y), y_dtype = dtype_of(y, "y"), dtype = dtype_of(h, "h");
+    const int32_t n_tok = fits(y.size(0), "y"), dim = fits(y.size(1), "y");
+    const int64_t y_stride = row_stride(y, n_tok, dim, "y");
+    if (h.sizes() != y.sizes()) bad("h: the shape of y expected");
+    const at::ScalarType type = h.scalar_type();
+    void* hp = flat(h, y.numel(), type, dev, "h");
+    const void* rp = flat_or_null(a[1], y.numel(), type, dev, "residual");
+    const auto* post = static_cast<const float*>(flat_or_null(a[3], dim, at::kFloat, dev, "post_weight"));
+    const auto* pre = static_cast<const float*>(flat_or_null(a[7], dim, at::kFloat, dev, "pre_weight"));
+    void* np = pre ? flat(a[8], y.numel(), type, dev, "normed") : nullptr;
+    const void* gp = nullptr;
+    int64_t g_stride = 0;
+    if (a[4] != Py_None) {
+      const at::Tensor& g = tensor(a[4], "gate");
+      if (g.scalar_type() != type || device_of(g) != dev) bad("gate: the dtype and device of h expected");
+      if (g.numel() == dim && (g.dim() == 1 || n_tok != 1)) {   // one row for all tokens
+        if (!g.is_contiguous()) bad("gate: [n_tok, dim] with contiguous rows, or [dim], expected");
+      } else {
+        g_stride = row_stride(g, n_tok, dim, "gate");
+      }
+      gp = g.data_ptr();
+    }
+    const int32_t act = fits(integer(a[5]), "gate_act");
+    const float alpha = static_cast<float>(number(a[6])), eps = static_cast<float>(number(a[9]));
+    const void* yp = y.data_ptr();
+    return call(dev, a[10], [&](void* s) {
+      return g_api.block_norm(yp, y_stride, y_dtype, n_tok, dim, post, gp, g_stride, act, rp, alpha, pre, eps, dtype, hp, np, s);
+    });
+  });
+}
+
+// the addresses of the C entry points, in the order of Api
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return guarded(n, 4, [&]() -> PyObject* {
+  return guarded(n, 9, [&]() -> PyObject* {
     g_api.norm_rope = reinterpret_cast<decltype(g_api.norm_rope)>(address<void>(a[0]));
     g_api.append_rope = reinterpret_cast<decltype(g_api.append_rope)>(address<void>(a[1]));
     g_api.accept = reinterpret_cast<decltype(g_api.accept)>(address<void>(a[2]));
     g_api.decode_shared = reinterpret_cast<decltype(g_api.decode_shared)>(address<void>(a[3]));
+    g_api.plan = reinterpret_cast<decltype(g_api.plan)>(address<void>(a[4]));
+    g_api.append_slots = reinterpret_cast<decltype(g_api.append_slots)>(address<void>(a[5]));
+    g_api.diff_decode = reinterpret_cast<decltype(g_api.diff_decode)>(address<void>(a[6]));
+    g_api.diff = reinterpret_cast<decltype(g_api.diff)>(address<void>(a[7]));
+    g_api.block_norm = reinterpret_cast<decltype(g_api.block_norm)>(address<void>(a[8]));
     Py_RETURN_NONE;
   });
 }
 
 #define K8V4_METHOD(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(name)), METH_FASTCALL, nullptr}
 PyMethodDef g_methods[] = {K8V4_METHOD(norm_rope), K8V4_METHOD(append_rope), K8V4_METHOD(accept),
-                           K8V4_METHOD(decode_shared), K8V4_METHOD(bind), {nullptr, nullptr, 0, nullptr}};
+                           K8V4_METHOD(decode_shared), K8V4_METHOD(plan), K8V4_METHOD(append_slots), K8V4_METHOD(diff_decode),
+                           K8V4_METHOD(diff), K8V4_METHOD(block_norm), K8V4_METHOD(bind), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_k8v4_binding", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

@@ -1,0 +1,832 @@
+// Differential attention of single queries over the k8v4 cache, split over the cells,
+// and the combine of its partial rows:
+//
+//   x = A_1 V - lambda A_2 V,  A_m = softmax(scale q_m K_m^T) over lanes [128 m, 128 m + 128)
+//   out = out_scale * x / sqrt(mean(x^2) + eps) * w        (bf16)
+//
+// The two maps of a head score the two halves of the same key rows and weigh the same
+// values, so a cell's 408 bytes are read and converted once for both.  Each map has its
+// own softmax statistics; they are known only at the end, so both products with V are kept
+// (they share the converted V).  Per 16-cell tile a warp does
+//   S_m^T = K_m q_m^T    8 + 8 products m16n8k16 (cells x 8 heads)
+//   O_m^T += V^T P_m^T   16 + 16 products (dims x 8 heads), V converted once
+// with K codes exact in fp16, q in fp16 (bf16 is exact after a power of two per row and
+// map), P and V rounded to fp16 once each: 2^-12 of each term, against the 2^-9 of the bf16
+// result, where the plain decode carries both in two terms (48 products of V, not 32, and
+// for one map).
+//
+// The structure is the decode kernel's: a CTA owns a (row, KV head, cell range), its
+// worker warps take the tiles in turn, each with a ring of its own filled by TMA.
+#include <algorithm>
+#include <climits>
+
+#include "k8v4_diff.cuh"
+#include "k8v4_tc.cuh"
+#include "k8v4_tma.cuh"
+
+namespace k8v4 {
+namespace {
+
+constexpr unsigned kFull = 0xffffffffu;
+constexpr int kMaxWorkers = 8;                // 255 registers a thread
+constexpr int kStages = 3;
+constexpr int kSmemCap = 227 * 1024;
+constexpr uint32_t kWaitDefaultNs = 1000000000u;
+constexpr int kBucketClamp = 1 << 24;
+// a worker's partial in the epilogue: [8 heads x 2 maps][kHeadStride] floats of o, then
+// 16 buckets and 16 sums (a stride of 4 mod 16 floats: conflict-free fragment stores)
+constexpr int kHeadStride = 260;
+constexpr int kPartBucket = 16 * kHeadStride;
+constexpr int kPartSum = kPartBucket + 16;
+constexpr int kPartFloats = kPartSum + 16;
+
+struct Layout {
+  int workers;
+  int ksc_bytes, vsc_bytes, ksc_off, vsc_off;       // within a stage: K 4096, V 2048, K scales, V scales
+  int stage_bytes, tx_bytes;
+  int q_off, bar_off, total;
+};
+constexpr int kVOff = 4096, kQBytes = 16 * 32 * 8;  // q fragments [16 k-steps][32 lanes][2 words]
+
+inline Layout layout_of(int H) {
+  Layout L;
+  L.ksc_bytes = 128 * H;
+  L.vsc_bytes = 256 * H;
+  L.ksc_off = kVOff + 2048;
+  L.vsc_off = L.ksc_off + L.ksc_bytes;
+  L.tx_bytes = L.vsc_off + L.vsc_bytes;
+  L.stage_bytes = (std::max(L.tx_bytes, (kPartFloats * 4 + kStages - 1) / kStages) + 1023) & ~1023;
+  for (L.workers = kMaxWorkers;; --L.workers) {
+    L.q_off = L.workers * kStages * L.stage_bytes;
+    L.bar_off = L.q_off + kQBytes;
+    L.total = L.bar_off + 8 * kStages * L.workers + 16 + 1024;
+    if (L.total <= kSmemCap || L.workers == 1) break;
+  }
+  return L;
+}
+
+struct DiffParams {
+  CacheView C;
+  const void* q;
+  int q_f32;
+  const int32_t* pt;
+  int64_t max_pages;
+  const int32_t* lens;        // visible cells of each row
+  const int32_t* row_seq;     // table row of each row, or null: its own index
+  int max_seq_len, cells_per_split, splits;
+  float sm_scale_log2;
+  float* ws;
+  int* status;
+  uint32_t wait_ns;
+  FastDiv page_div;
+  Layout L;
+};
+
+__device__ __forceinline__ void mma16(float c[4], const uint32_t a[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t movmatrix_t(uint32_t a) {
+  uint32_t d;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  return d;
+}
+__device__ __forceinline__ void ldmatrix_x4_t(uint32_t r[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr));
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t addr) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+// 2^e exactly for e >= -126, 0 below
+__device__ __forceinline__ float pow2i(int e) { return e < -126 ? 0.0f : __int_as_float((e + 127) << 23); }
+// one word of nibble bytes b0..b3 -> four fp16x2 of (n - 8) / 8, exact: {b0, b2} and {b1, b3}
+// of the low nibbles, then of the high ones.  0x640n is 1024 + n and 0x64n0 is 1024 + 16 n in
+// fp16; (1024 + n) / 8 - 129 and (1024 + 16 n) / 128 - 9 are both (n - 8) / 8
+__device__ __forceinline__ void nibs_8th(uint32_t r, __half2 v[4]) {
+  const uint32_t r8 = r >> 8;
+  const __half2 eighth = __halves2half2(__ushort_as_half(0x3000), __ushort_as_half(0x3000));    // 1/8
+  const __half2 m129 = __halves2half2(__ushort_as_half(0xd808), __ushort_as_half(0xd808));      // -129
+  const __half2 c128th = __halves2half2(__ushort_as_half(0x2000), __ushort_as_half(0x2000));    // 1/128
+  const __half2 m9 = __halves2half2(__ushort_as_half(0xc880), __ushort_as_half(0xc880));        // -9
+  uint32_t t0 = (r & 0x000f000fu) | 0x64006400u, t1 = (r8 & 0x000f000fu) | 0x64006400u;
+  uint32_t t2 = (r & 0x00f000f0u) | 0x64006400u, t3 = (r8 & 0x00f000f0u) | 0x64006400u;
+  v[0] = __hfma2(*reinterpret_cast<__half2*>(&t0), eighth, m129);
+  v[1] = __hfma2(*reinterpret_cast<__half2*>(&t1), eighth, m129);
+  v[2] = __hfma2(*reinterpret_cast<__half2*>(&t2), c128th, m9);
+  v[3] = __hfma2(*reinterpret_cast<__half2*>(&t3), c128th, m9);
+}
+__device__ __forceinline__ uint32_t times(__half2 a, uint32_t d) {
+  const __half2 r = __hmul2(a, *reinterpret_cast<const __half2*>(&d));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+// MMA row r (0..7) of a tile holds cell sigma(r), row r + 8 cell 8 + sigma(r): the two cells a
+// quarter-warp reads in one 128-bit shared load then differ in bit 2, which the 128-byte
+// swizzle turns into disjoint bank groups
+__device__ __forceinline__ int sigma(int r) { return (r >> 1) | ((r & 1) << 2); }
+
+// Wait for a phase: false once the bound has passed, or the CTA's abort flag is up
+__device__ __forceinline__ bool wait_or_abort(uint32_t bar, uint32_t parity, uint32_t limit_ns, const volatile int* abort) {
+  if (mbar_test(bar, parity)) return true;
+  if (limit_ns < 1000u) return false;
+  const uint64_t t0 = global_ns();
+  for (;;) {
+    if (global_ns() - t0 >= limit_ns) return false;
+    if (mbar_try(bar, parity, 20000u)) return true;
+    if (*abort) return false;
+  }
+}
+
+// ---------------------------------------------------------------- the split kernel
+// grid: (splits, KV heads, rows)
+__global__ void __launch_bounds__(32 * kMaxWorkers, 1)
+    diff_split_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const DiffParams p) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  const uint32_t raw_s = smem_u32(smem_raw);
+  const uint32_t sb = (raw_s + 1023u) & ~1023u;
+  uint8_t* sm = smem_raw + (sb - raw_s);
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const int W = blockDim.x >> 5;
+  const Layout& LY = p.L;
+  const uint32_t full = sb + LY.bar_off + 8 * kStages * w;               // this worker's stage barriers
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + LY.bar_off + 8 * kStages * W);
+  if (threadIdx.x == 0) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_k)) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_v)) : "memory");
+    *abort_flag = 0;
+  }
+  if (lane == 0) {
+    for (int i = 0; i < kStages; ++i) mbar_init(full + 8 * i, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+
+  const int split = blockIdx.x, g = blockIdx.y, row = blockIdx.z;
+  const CacheView& C = p.C;
+  const int H = C.H, HQ = H * kGqa;
+  const int r0 = lane >> 2, c = lane & 3;
+  const int b = p.row_seq ? p.row_seq[row] : row;
+  int n_vis = b >= 0 ? p.lens[row] : 0;
+  if (n_vis < 0 || n_vis > p.max_seq_len) {
+    if (threadIdx.x == 0 && split == 0 && g == 0) record_status(p.status, K8V4_ERANGE);
+    n_vis = n_vis < 0 ? 0 : p.max_seq_len;
+  }
+  const int c_begin = split * p.cells_per_split;
+  const int c_end = min(c_begin + p.cells_per_split, n_vis);
+  const int n_tiles = c_end > c_begin ? (c_end - c_begin + 15) >> 4 : 0;
+  const int n_my = n_tiles > w ? (n_tiles - w + W - 1) / W : 0;          // tiles w + W u
+  const uint32_t ring = sb + w * kStages * LY.stage_bytes;
+  float* const rows = p.ws + (static_cast<int64_t>(row) * H + g) * p.splits * 16 * kDiffRow + static_cast<int64_t>(split) * 16 * kDiffRow;
+  // a range past the row's visible cells only marks its partial rows empty
+  if (n_tiles == 0) {
+    if (threadIdx.x < 16) {
+      rows[threadIdx.x * kDiffRow + 256] = -INFINITY;
+      rows[threadIdx.x * kDiffRow + 257] = 0.0f;
+    }
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    return;
+  }
+
+  // ---- this worker's copies: local tile u -> stage u % kStages
+  const int32_t* pt_row = p.pt + static_cast<int64_t>(b) * p.max_pages;
+  int win0 = -1000000, win_page = -1;
+  auto page_of = [&](int u) -> int {         // warp-uniform u; all lanes call
+    if (u < win0 || u >= win0 + 32) {
+      win0 = u;
+      const int cell = c_begin + 16 * (w + W * (u + lane));
+      const int64_t pidx = cell >= 0 ? static_cast<int64_t>(p.page_div.div(static_cast<uint32_t>(cell))) : 0;
+      win_page = (u + lane < n_my && pidx < p.max_pages) ? pt_row[pidx] : -1;
+    }
+    const int page = __shfl_sync(kFull, win_page, u - win0);
+    return (page >= 0 && page < C.n_pages) ? page : -1;
+  };
+  // an out-of-range page issues no copy; its tile is skipped and recorded
+  auto issue = [&](int u, int stage, int page) {
+    if (lane == 0) {
+      const uint32_t st = ring + stage * LY.stage_bytes, bar = full + 8 * stage;
+      if (page >= 0) {
+        const int cell0 = c_begin + 16 * (w + W * u);
+        const int slot0 = cell0 - static_cast<int>(p.page_div.div(static_cast<uint32_t>(cell0))) * C.P;
+        mbar_expect_tx(bar, LY.tx_bytes);
+        tma_load_4d(st, &tm_k, 0, g, slot0, page, bar);
+        tma_load_4d(st + 2048, &tm_k, 128, g, slot0, page, bar);
+        tma_load_4d(st + kVOff, &tm_v, 0, g, slot0, page, bar);
+        const uint8_t* pg = C.pages + static_cast<int64_t>(page) * C.page_bytes;
+        bulk_load(st + LY.ksc_off, pg + C.ks_off() + static_cast<int64_t>(slot0) * 8 * H, LY.ksc_bytes, bar);
+        bulk_load(st + LY.vsc_off, pg + C.vs_off() + static_cast<int64_t>(slot0) * 16 * H, LY.vsc_bytes, bar);
+      } else {
+        record_status(p.status, K8V4_ERANGE);
+        asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+      }
+    }
+  };
+  int issued = 0;
+  for (; issued < min(kStages, n_my); ++issued) issue(issued, issued, page_of(issued));
+
+  // ---- q fragments (B operand of S^T = K q^T) into shared memory, every warp the same
+  // ones for itself to find: warp 0 writes them.  Lane (r0, c): head r0, dims 64 i + 16 c +
+  // 4 j + e of k-step 4 i + j; k-steps 0..7 are map 0, 8..15 map 1, each with its own
+  // power of two
+  float f[2][2];                       // score factors: [map][heads 2c, 2c + 1]
+  {
+    const int64_t qrow = (static_cast<int64_t>(row) * HQ + g * kGqa + r0) * kD;
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+      float qv[32];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int64_t e0 = qrow + 128 * m + 64 * i + 16 * c;
+        if (p.q_f32) {
+          const float4* src = reinterpret_cast<const float4*>(static_cast<const float*>(p.q) + e0);
+#pragma unroll
+          for (int t = 0; t < 4; ++t) {
+            const float4 v = src[t];
+            qv[16 * i + 4 * t] = v.x; qv[16 * i + 4 * t + 1] = v.y;
+            qv[16 * i + 4 * t + 2] = v.z; qv[16 * i + 4 * t + 3] = v.w;
+          }
+        } else {
+          const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + e0);
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            const uint4 v = src[t];
+            const uint32_t wv[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              qv[16 * i + 8 * t + 2 * u] = __uint_as_float(wv[u] << 16);
+              qv[16 * i + 8 * t + 2 * u + 1] = __uint_as_float(wv[u] & 0xffff0000u);
+            }
+          }
+        }
+      }
+      float amax = 0.0f;
+#pragma unroll
+      for (int t = 0; t < 32; ++t) amax = fmaxf(amax, fabsf(qv[t]));
+      amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, 1));
+      amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, 2));
+      const int ex = amax > 0.0f ? static_cast<int>((__float_as_uint(amax) >> 23) & 0xffu) - 127 : 0;
+      const int sh = max(-100, min(100, 14 - ex));              // amax * 2^sh in [2^14, 2^15)
+      const float up = ldexpf(1.0f, sh);
+      const float fscale = p.sm_scale_log2 * ldexpf(1.0f, -sh);
+      if (w == 0) {
+#pragma unroll
+        for (int ks = 0; ks < 8; ++ks) {
+          const int o = 16 * (ks >> 2) + 4 * (ks & 3);
+          const uint32_t h0 = pack_f16(qv[o] * up, qv[o + 1] * up), h1 = pack_f16(qv[o + 2] * up, qv[o + 3] * up);
+          asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(sb + LY.q_off + ((8 * m + ks) * 32 + lane) * 8), "r"(h0), "r"(h1) : "memory");
+        }
+      }
+      f[m][0] = __shfl_sync(kFull, fscale, 8 * c);
+      f[m][1] = __shfl_sync(kFull, fscale, 8 * c + 4);
+    }
+  }
+  __syncthreads();
+
+  // K fragment addresses within a stage (two 128-byte-swizzled [16][128] halves)
+  const int rowA = sigma(r0), rowB = 8 + sigma(r0);
+  uint32_t offA[2], offB[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    offA[i] = rowA * 128 + 16 * ((4 * i + c) ^ (rowA & 7));
+    offB[i] = rowB * 128 + 16 * ((4 * i + c) ^ (rowB & 7));
+  }
+  const uint32_t ksA = LY.ksc_off + (rowA * H + g) * 8, ksB = LY.ksc_off + (rowB * H + g) * 8;
+  // V fragment rows: matrix mi = lane >> 3 holds cells 8 (mi & 1) + sigma(0..7)
+  const int mi = lane >> 3;
+  const int vcell = 8 * (mi & 1) + sigma(lane & 7);
+  const uint32_t vrow = kVOff + vcell * 128;
+  const int vsw = vcell & 7;
+  // the V scales of the fragment's four cells k = 2c, 2c+1, 2c+8, 2c+9
+  const uint32_t soff0 = LY.vsc_off + (sigma(2 * c) * H + g) * 16, soff1 = LY.vsc_off + (sigma(2 * c + 1) * H + g) * 16;
+  const uint32_t s8 = 8 * H * 16;
+  const uint32_t qf = sb + LY.q_off + 8 * lane;
+
+  float o[2][16][4];                   // [map][16-dim m-tile][fragment]: heads 2c, 2c+1 of dims r0 (+8)
+#pragma unroll
+  for (int m = 0; m < 2; ++m)
+#pragma unroll
+    for (int mt = 0; mt < 16; ++mt) o[m][mt][0] = o[m][mt][1] = o[m][mt][2] = o[m][mt][3] = 0.0f;
+  int M[2][2] = {{INT_MIN, INT_MIN}, {INT_MIN, INT_MIN}};    // running buckets
+  float l[2][2] = {{0.0f, 0.0f}, {0.0f, 0.0f}};
+  bool aborted = false;
+  int stage = 0;
+  uint32_t phase = 0;
+
+  for (int u = 0; u < n_my; ++u) {
+    if (!__all_sync(kFull, wait_or_abort(full + 8 * stage, phase, p.wait_ns, abort_flag))) {
+      if (lane == 0) {
+        *abort_flag = 1;
+        record_status(p.status, K8V4_ECUDA);
+      }
+      aborted = true;
+      break;
+    }
+    const uint32_t st = ring + stage * LY.stage_bytes;
+    if (page_of(u) >= 0) {
+      const uint2 kAu = lds64(st + ksA), kBu = lds64(st + ksB);
+      const int cell0 = c_begin + 16 * (w + W * u);
+      const bool vA = cell0 + rowA < c_end, vB = cell0 + rowB < c_end;
+      uint32_t ph[2][2];
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        // ---- S_m^T[cell][head], two accumulators
+        float acc[2][4];
+#pragma unroll
+        for (int a4 = 0; a4 < 2; ++a4) acc[a4][0] = acc[a4][1] = acc[a4][2] = acc[a4][3] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint4 ka = lds128(st + 2048 * m + offA[i]);
+          const uint4 kb = lds128(st + 2048 * m + offB[i]);
+          const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            uint32_t a[4];
+            i8x4_to_f16(wa[j], a[0], a[2]);
+            i8x4_to_f16(wb[j], a[1], a[3]);
+            const uint2 qb = lds64(qf + (8 * m + 4 * i + j) * 256);
+            mma16(acc[j & 1], a, qb.x, qb.y);
+          }
+        }
+        const float kA = __uint_as_float(m ? kAu.y : kAu.x), kB = __uint_as_float(m ? kBu.y : kBu.x);
+        float sc[4];
+        sc[0] = vA ? kA * (acc[0][0] + acc[1][0]) * f[m][0] : -INFINITY;
+        sc[1] = vA ? kA * (acc[0][1] + acc[1][1]) * f[m][1] : -INFINITY;
+        sc[2] = vB ? kB * (acc[0][2] + acc[1][2]) * f[m][0] : -INFINITY;
+        sc[3] = vB ? kB * (acc[0][3] + acc[1][3]) * f[m][1] : -INFINITY;
+        // ---- softmax against the running bucket of each head (the decode kernel's)
+        const bool up0 = sc[0] > 8.0f * M[m][0] || sc[2] > 8.0f * M[m][0], up1 = sc[1] > 8.0f * M[m][1] || sc[3] > 8.0f * M[m][1];
+        if (__any_sync(kFull, up0 || up1)) {
+          float t0 = fmaxf(sc[0], sc[2]), t1 = fmaxf(sc[1], sc[3]);
+#pragma unroll
+          for (int off = 4; off < 32; off <<= 1) {
+            t0 = fmaxf(t0, __shfl_xor_sync(kFull, t0, off));
+            t1 = fmaxf(t1, __shfl_xor_sync(kFull, t1, off));
+          }
+          const int nb0 = max(M[m][0], static_cast<int>(fminf(fmaxf(ceilf(t0 * 0.125f), -kBucketClamp), kBucketClamp)));
+          const int nb1 = max(M[m][1], static_cast<int>(fminf(fmaxf(ceilf(t1 * 0.125f), -kBucketClamp), kBucketClamp)));
+          const float g0 = M[m][0] == INT_MIN ? 0.0f : pow2i(8 * (M[m][0] - nb0));
+          const float g1 = M[m][1] == INT_MIN ? 0.0f : pow2i(8 * (M[m][1] - nb1));
+#pragma unroll
+          for (int mt = 0; mt < 16; ++mt) {
+            o[m][mt][0] *= g0; o[m][mt][2] *= g0;
+            o[m][mt][1] *= g1; o[m][mt][3] *= g1;
+          }
+          l[m][0] *= g0;
+          l[m][1] *= g1;
+          M[m][0] = nb0;
+          M[m][1] = nb1;
+        }
+        const float rf0 = static_cast<float>(8 * M[m][0] - 14), rf1 = static_cast<float>(8 * M[m][1] - 14);
+        const float p0 = ex2_ftz(sc[0] - rf0), p1 = ex2_ftz(sc[1] - rf1);      // p' = 2^(s - ref + 14) <= 2^14
+        const float p2 = ex2_ftz(sc[2] - rf0), p3 = ex2_ftz(sc[3] - rf1);
+        l[m][0] += p0 + p2;
+        l[m][1] += p1 + p3;
+        // to the B layout (head r0; cells 2c, 2c+1 | 2c+8, 2c+9)
+        ph[m][0] = movmatrix_t(pack_f16(p0, p1));
+        ph[m][1] = movmatrix_t(pack_f16(p2, p3));
+      }
+      // ---- PV of both maps in rotated space: V = RN((n - 8) / 8 * d), m-tile 2 blk + hf = block
+      // blk, dims 16 hf .. 16 hf + 15
+#pragma unroll
+      for (int bp = 0; bp < 4; ++bp) {
+        uint32_t R[4];
+        ldmatrix_x4_t(R, st + vrow + 16 * ((2 * bp + (mi >> 1)) ^ vsw));
+        const uint32_t w0 = lds32(st + soff0 + 4 * bp), w1 = lds32(st + soff1 + 4 * bp);
+        const uint32_t w2 = lds32(st + soff0 + s8 + 4 * bp), w3 = lds32(st + soff1 + s8 + 4 * bp);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t sel = h ? 0x7632u : 0x5410u;
+          const uint32_t d01 = prmt(w0, w1, sel), d89 = prmt(w2, w3, sel);     // d of block 2bp+h, cell pairs
+          __half2 xa[4], xb[4];
+          nibs_8th(R[2 * h], xa);
+          nibs_8th(R[2 * h + 1], xb);
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf) {
+            const uint32_t a[4] = {times(xa[2 * hf], d01), times(xa[2 * hf + 1], d01), times(xb[2 * hf], d89), times(xb[2 * hf + 1], d89)};
+            mma16(o[0][2 * (2 * bp + h) + hf], a, ph[0][0], ph[0][1]);
+            mma16(o[1][2 * (2 * bp + h) + hf], a, ph[1][0], ph[1][1]);
+          }
+        }
+      }
+    }
+    __syncwarp();
+    if (issued < n_my) {
+      issue(issued, stage, page_of(issued));
+      ++issued;
+    }
+    if (++stage == kStages) {
+      stage = 0;
+      phase ^= 1;
+    }
+  }
+#pragma unroll
+  for (int off = 4; off < 32; off <<= 1) {
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+      l[m][0] += __shfl_xor_sync(kFull, l[m][0], off);
+      l[m][1] += __shfl_xor_sync(kFull, l[m][1], off);
+    }
+  }
+
+  // ---------------------------------------------------------------- epilogue
+  // a worker that left early first waits (bounded) for its copies in flight
+  if (aborted && lane == 0) {
+    for (int u = max(0, issued - kStages); u < issued; ++u) {
+      const uint64_t t0 = global_ns();
+      while (!mbar_try(full + 8 * (u % kStages), (u / kStages) & 1, 20000u) && global_ns() - t0 < kWaitDefaultNs) {
+      }
+    }
+  }
+  __syncwarp();
+  float* mine = reinterpret_cast<float*>(sm + w * kStages * LY.stage_bytes);
+#pragma unroll
+  for (int m = 0; m < 2; ++m) {
+    const bool live0 = M[m][0] != INT_MIN, live1 = M[m][1] != INT_MIN;
+    float* base = mine + 8 * m * kHeadStride;
+#pragma unroll
+    for (int mt = 0; mt < 16; ++mt) {
+      const int d0 = 32 * (mt >> 1) + 16 * (mt & 1) + 2 * r0;
+      *reinterpret_cast<float2*>(base + (2 * c) * kHeadStride + d0) =
+          live0 ? make_float2(o[m][mt][0], o[m][mt][2]) : make_float2(0.0f, 0.0f);
+      *reinterpret_cast<float2*>(base + (2 * c + 1) * kHeadStride + d0) =
+          live1 ? make_float2(o[m][mt][1], o[m][mt][3]) : make_float2(0.0f, 0.0f);
+    }
+    if (r0 == 0) {
+      reinterpret_cast<int*>(mine + kPartBucket)[8 * m + 2 * c] = M[m][0];
+      reinterpret_cast<int*>(mine + kPartBucket)[8 * m + 2 * c + 1] = M[m][1];
+      mine[kPartSum + 8 * m + 2 * c] = l[m][0];
+      mine[kPartSum + 8 * m + 2 * c + 1] = l[m][1];
+    }
+  }
+  __syncthreads();
+  // a warp per (map, head): the workers' partials at the largest bucket, in rotated space
+  for (int h = w; h < 16; h += W) {
+    const float* mj_part = reinterpret_cast<const float*>(sm + min(lane, W - 1) * kStages * LY.stage_bytes);
+    const int mj = lane < W ? reinterpret_cast<const int*>(mj_part + kPartBucket)[h] : INT_MIN;
+    const float lj = lane < W ? mj_part[kPartSum + h] : 0.0f;
+    const int Mx = __reduce_max_sync(kFull, mj);
+    const float fj = mj == INT_MIN ? 0.0f : pow2i(8 * (mj - Mx));
+    float v[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+    float Ls = 0.0f;
+#pragma unroll
+    for (int j = 0; j < kMaxWorkers; ++j) {
+      const float fw = __shfl_sync(kFull, fj, j), lw = __shfl_sync(kFull, lj, j);   // 0 for j >= W
+      if (j < W) {
+        const float* src = reinterpret_cast<const float*>(sm + j * kStages * LY.stage_bytes) + h * kHeadStride;
+        const float4 x0 = *reinterpret_cast<const float4*>(src + 4 * lane);
+        const float4 x1 = *reinterpret_cast<const float4*>(src + 128 + 4 * lane);
+        v[0] += x0.x * fw; v[1] += x0.y * fw; v[2] += x0.z * fw; v[3] += x0.w * fw;
+        v[4] += x1.x * fw; v[5] += x1.y * fw; v[6] += x1.z * fw; v[7] += x1.w * fw;
+        Ls += lw * fw;
+      }
+    }
+    constexpr float kInv = 1.0f / 2048.0f;     // 2^-14 of p', 2^3 of (n - 8) / 8
+    float* dst = rows + h * kDiffRow;
+    reinterpret_cast<float4*>(dst)[lane] = make_float4(v[0] * kInv, v[1] * kInv, v[2] * kInv, v[3] * kInv);
+    reinterpret_cast<float4*>(dst)[32 + lane] = make_float4(v[4] * kInv, v[5] * kInv, v[6] * kInv, v[7] * kInv);
+    if (lane == 0) {
+      dst[256] = Mx == INT_MIN ? -INFINITY : static_cast<float>(8 * Mx);
+      dst[257] = Ls * (1.0f / 16384.0f);
+    }
+  }
+  __syncthreads();
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+// ---------------------------------------------------------------- the combine
+struct CombineParams {
+  const float* ws;
+  const int32_t* row_seq;     // rows without a sequence (< 0) are left as they are; or null
+  int splits, H;
+  k8v4_diff d;
+  uint16_t* out;
+};
+constexpr int kCombineWarps = 4, kMaxSplits = kDecodeMaxSplits;
+
+// One CTA per (row, query head): the splits of both maps joined, their difference
+// brought back from rotated space (linear, so once for both), normed and rounded.
+__global__ void __launch_bounds__(32 * kCombineWarps) diff_combine_kernel(const CombineParams p) {
+  __shared__ float wt[2][kMaxSplits];
+  __shared__ float red[2][2][kCombineWarps];
+  __shared__ float4 part[2][kCombineWarps][64];
+  __shared__ float lam_s[2];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+  const int HQ = p.H * kGqa;
+  const int row = blockIdx.x / HQ, hq = blockIdx.x - row * HQ;
+  const int g = hq / kGqa, h = hq % kGqa;
+  if (p.row_seq && p.row_seq[row] < 0) return;
+  const float* base = p.ws + ((static_cast<int64_t>(row) * p.H + g) * p.splits * 16 + h) * kDiffRow;
+  constexpr int64_t kSplitStride = 16 * kDiffRow;
+  float Mx[2], L[2];
+#pragma unroll
+  for (int m = 0; m < 2; ++m) {
+    Mx[m] = -INFINITY;
+    for (int s = t; s < p.splits; s += 32 * kCombineWarps) {
+      const float v = base[s * kSplitStride + 8 * m * kDiffRow + 256];
+      wt[m][s] = v;
+      Mx[m] = fmaxf(Mx[m], v);
+    }
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) Mx[m] = fmaxf(Mx[m], __shfl_xor_sync(kFull, Mx[m], o));
+    if (lane == 0) red[0][m][warp] = Mx[m];
+  }
+  // lambda of the head: warp m takes map m's dot product
+  if (warp < 2) {
+    float dot = 0.0f;
+    if (p.d.lambda_q1) {
+      const int64_t at = (p.d.n_lambda > 1 ? hq * 128 : 0) + 4 * lane;
+      const float4 a = *reinterpret_cast<const float4*>((warp ? p.d.lambda_q2 : p.d.lambda_q1) + at);
+      const float4 b = *reinterpret_cast<const float4*>((warp ? p.d.lambda_k2 : p.d.lambda_k1) + at);
+      dot = a.x * b.x + a.y * b.y + a.z * b.z + a.w * b.w;
+#pragma unroll
+      for (int o = 16; o >= 1; o >>= 1) dot += __shfl_xor_sync(kFull, dot, o);
+      dot = expf(dot);
+    }
+    if (lane == 0) lam_s[warp] = dot;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int m = 0; m < 2; ++m) {
+#pragma unroll
+    for (int w = 0; w < kCombineWarps; ++w) Mx[m] = fmaxf(Mx[m], red[0][m][w]);
+    L[m] = 0.0f;
+    for (int s = t; s < p.splits; s += 32 * kCombineWarps) {
+      const float w = wt[m][s] == -INFINITY ? 0.0f : exp2f(wt[m][s] - Mx[m]);
+      if (w != 0.0f) L[m] += w * base[s * kSplitStride + 8 * m * kDiffRow + 257];
+      wt[m][s] = w;
+    }
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) L[m] += __shfl_xor_sync(kFull, L[m], o);
+    if (lane == 0) red[1][m][warp] = L[m];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int m = 0; m < 2; ++m) {
+    float acc[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+    constexpr int kUnroll = 4;
+    for (int s0 = warp; s0 < p.splits; s0 += kCombineWarps * kUnroll) {
+      float4 x[kUnroll][2];
+      float w[kUnroll];
+#pragma unroll
+      for (int k = 0; k < kUnroll; ++k) {
+        const int s = s0 + kCombineWarps * k;
+        w[k] = s < p.splits ? wt[m][s] : 0.0f;
+        if (w[k] != 0.0f) {
+          const float4* src = reinterpret_cast<const float4*>(base + s * kSplitStride + 8 * m * kDiffRow);
+          x[k][0] = src[lane];
+          x[k][1] = src[32 + lane];
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < kUnroll; ++k) {
+        if (w[k] == 0.0f) continue;
+        acc[0] += x[k][0].x * w[k]; acc[1] += x[k][0].y * w[k]; acc[2] += x[k][0].z * w[k]; acc[3] += x[k][0].w * w[k];
+        acc[4] += x[k][1].x * w[k]; acc[5] += x[k][1].y * w[k]; acc[6] += x[k][1].z * w[k]; acc[7] += x[k][1].w * w[k];
+      }
+    }
+    part[m][warp][lane] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+    part[m][warp][32 + lane] = make_float4(acc[4], acc[5], acc[6], acc[7]);
+  }
+  __syncthreads();
+  if (warp) return;
+  // lane: dims 4 lane + e and 128 + 4 lane + e
+  const float lambda = p.d.lambda_q1 ? lam_s[0] - lam_s[1] + p.d.lambda_init : p.d.lambda_init;
+  float v[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+  for (int m = 0; m < 2; ++m) {
+    float Lt = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kCombineWarps; ++w) Lt += red[1][m][w];
+    const float inv = Lt > 0.0f ? (m ? -lambda : 1.0f) / Lt : 0.0f;
+    float s[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int w = 0; w < kCombineWarps; ++w) {
+      const float4 a = part[m][w][lane], b = part[m][w][32 + lane];
+      s[0] += a.x; s[1] += a.y; s[2] += a.z; s[3] += a.w;
+      s[4] += b.x; s[5] += b.y; s[6] += b.z; s[7] += b.w;
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] += s[e] * inv;
+  }
+#pragma unroll
+  for (int hh = 1; hh < 8; hh <<= 1) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      if (e & hh) continue;
+      const float a = v[e], bb = v[e + hh];
+      v[e] = a + bb;
+      v[e + hh] = a - bb;
+    }
+  }
+#pragma unroll
+  for (int mm = 1; mm < 32; mm <<= 1) {
+    const bool upper = (lane & mm) != 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float tt = __shfl_xor_sync(kFull, v[e], mm);
+      v[e] = upper ? tt - v[e] : v[e] + tt;
+    }
+  }
+  float s2 = 0.0f;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    v[e] *= 0.0625f;
+    s2 += v[e] * v[e];
+  }
+  if (p.d.norm_weight) {
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) s2 += __shfl_xor_sync(kFull, s2, o);
+    const float scale = rsqrtf(s2 * (1.0f / kD) + p.d.eps) * p.d.out_scale;
+    const float4 wa = reinterpret_cast<const float4*>(p.d.norm_weight)[lane], wb = reinterpret_cast<const float4*>(p.d.norm_weight)[32 + lane];
+    const bool seen = s2 != 0.0f;        // a row of zeros stays one where eps is 0
+    v[0] = seen ? v[0] * scale * wa.x : 0.0f; v[1] = seen ? v[1] * scale * wa.y : 0.0f;
+    v[2] = seen ? v[2] * scale * wa.z : 0.0f; v[3] = seen ? v[3] * scale * wa.w : 0.0f;
+    v[4] = seen ? v[4] * scale * wb.x : 0.0f; v[5] = seen ? v[5] * scale * wb.y : 0.0f;
+    v[6] = seen ? v[6] * scale * wb.z : 0.0f; v[7] = seen ? v[7] * scale * wb.w : 0.0f;
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] *= p.d.out_scale;
+  }
+  auto two = [](float lo, float hi) {
+    const __nv_bfloat162 x = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&x);
+  };
+  uint2* dst = reinterpret_cast<uint2*>(p.out + static_cast<int64_t>(blockIdx.x) * kD);
+  dst[lane] = make_uint2(two(v[0], v[1]), two(v[2], v[3]));
+  dst[32 + lane] = make_uint2(two(v[4], v[5]), two(v[6], v[7]));
+}
+
+}  // namespace
+
+// ---------------------------------------------------------------- host side
+bool diff_supported(const CacheView& C) {
+  return C.fmt == K8V4_FORMAT_K8V4 && C.n_pages < (int64_t(1) << 31) && C.page_bytes < (int64_t(1) << 39);
+}
+
+DiffPlan plan_diff_decode(const CacheView& C, int n_seqs, int max_seq_len, int num_sms) {
+  DiffPlan pl;
+  const int tiles = std::max(1, (max_seq_len + 15) / 16);
+  const int64_t pairs = static_cast<int64_t>(C.H) * n_seqs;
+  // the split count that minimises waves x (tiles per range + a CTA's fixed cost), each
+  // range keeping at least 2 tiles per worker warp, as the plain decode's plan
+  constexpr int kCtaFixedTiles = 32;
+  const int max_splits = std::max(1, std::min(kDecodeMaxSplits, tiles / (2 * kMaxWorkers)));
+  int64_t best_cost = INT64_MAX;
+  int best = 1;
+  for (int sp = 1; sp <= max_splits; ++sp) {
+    const int64_t waves = (pairs * sp + num_sms - 1) / num_sms;
+    const int64_t cost = waves * ((tiles + sp - 1) / sp + kCtaFixedTiles);
+    if (cost < best_cost) {
+      best_cost = cost;
+      best = sp;
+    }
+  }
+  const int tps = (tiles + best - 1) / best;
+  pl.cells_per_split = 16 * tps;
+  pl.splits = (tiles + tps - 1) / tps;
+  pl.ws_bytes = static_cast<size_t>(n_seqs) * pl.splits * C.H * 16 * kDiffRow * sizeof(float);
+  return pl;
+}
+
+int launch_diff_combine(const Launch& L, const float* ws, int splits, const int32_t* row_seq, int n_rows, int H, const k8v4_diff& diff, void* out) {
+  CombineParams p;
+  p.ws = ws;
+  p.row_seq = row_seq;
+  p.splits = splits;
+  p.H = H;
+  p.d = diff;
+  p.out = static_cast<uint16_t*>(out);
+  return launch_behind(L, diff_combine_kernel, dim3(static_cast<unsigned>(n_rows) * H * kGqa), dim3(32 * kCombineWarps), p);
+}
+
+namespace {
+int launch_rows(const Launch& L, const CacheView& C, const DiffPlan& plan, const void* q, int q_dtype, const int32_t* pt,
+                int64_t max_pages, const int32_t* lens, const int32_t* row_seq, int n_rows, int max_seq_len, float sm_scale,
+                const k8v4_diff& diff, void* out, void* ws) {
+  DiffParams p;
+  p.C = C;
+  p.q = q;
+  p.q_f32 = q_dtype == K8V4_F32;
+  p.pt = pt;
+  p.max_pages = max_pages;
+  p.lens = lens;
+  p.row_seq = row_seq;
+  p.max_seq_len = max_seq_len;
+  p.cells_per_split = plan.cells_per_split;
+  p.splits = plan.splits;
+  p.sm_scale_log2 = sm_scale * 1.4426950408889634f;
+  p.ws = static_cast<float*>(ws);
+  p.status = L.status;
+  p.wait_ns = wait_limit_ns() ? wait_limit_ns() : kWaitDefaultNs;
+  p.page_div = FastDiv(static_cast<uint32_t>(C.P));
+  p.L = layout_of(C.H);
+  CUtensorMap mk, mv;
+  if (!tensor_maps_of(C, &mk, &mv)) return K8V4_ECUDA;
+  if (cudaFuncSetAttribute(diff_split_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, p.L.total) != cudaSuccess ||
+      cudaFuncSetAttribute(diff_split_kernel, cudaFuncAttributePreferredSharedMemoryCarveout, 100) != cudaSuccess)
+    return K8V4_ECUDA;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(p.splits, C.H, n_rows);
+  cfg.blockDim = dim3(32 * p.L.workers);
+  cfg.dynamicSmemBytes = p.L.total;
+  cfg.stream = L.stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, diff_split_kernel, mk, mv, p) != cudaSuccess) return K8V4_ECUDA;
+  if (cudaGetLastError() != cudaSuccess) return K8V4_ECUDA;
+  return launch_diff_combine(L, p.ws, p.splits, row_seq, n_rows, C.H, diff, out);
+}
+}  // namespace
+
+int launch_diff_decode(const Launch& L, const CacheView& C, const DiffPlan& plan, const void* q, int q_dtype,
+                       const int32_t* pt, int64_t max_pages, const int32_t* lens, int n_seqs, int max_seq_len,
+                       float sm_scale, const k8v4_diff& diff, void* out, void* ws) {
+  return launch_rows(L, C, plan, q, q_dtype, pt, max_pages, lens, nullptr, n_seqs, max_seq_len, sm_scale, diff, out, ws);
+}
+
+// ---------------------------------------------------------------- a ragged batch
+namespace {
+constexpr int kRowsAtOnce = 65535;
+
+// the sequence of each packed token (-1: none) and the cells that it sees
+__global__ void __launch_bounds__(256) diff_tokens_kernel(const int32_t* offsets, const int32_t* lens, const int32_t* steps,
+                                                          int n_seqs, int n_tok, int max_seq_len, int32_t* row_seq,
+                                                          int32_t* row_vis, int* status) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int t = blockIdx.x * 256 + threadIdx.x;
+  if (t >= n_tok) return;
+  // the last sequence that begins at or ahead of the token
+  int lo = 0, hi = n_seqs;
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (offsets[mid] > t) hi = mid;
+    else lo = mid + 1;
+  }
+  const int b = lo - 1;
+  int seq = -1, vis = 0;
+  if (b >= 0) {
+    const int first = offsets[b], end = offsets[b + 1];
+    if (first < 0 || end < first || end > n_tok) record_status(status, K8V4_ERANGE);
+    else if (t < end) {
+      seq = b;
+      int len = lens[b];
+      if (len < 0 || len > max_seq_len) {
+        record_status(status, K8V4_ERANGE);
+        len = len < 0 ? 0 : max_seq_len;
+      }
+      vis = steps ? steps[t] : max(len - (end - t) + 1, 0);
+      if (vis < 0 || vis > len) {
+        record_status(status, K8V4_ERANGE);
+        vis = vis < 0 ? 0 : len;
+      }
+    }
+  }
+  row_seq[t] = seq;
+  row_vis[t] = vis;
+}
+}  // namespace
+
+size_t diff_ws_bytes(const CacheView& C, int n_seqs, int n_tok, int max_seq_len, int num_sms) {
+  const int rows = std::min(n_tok, kRowsAtOnce);
+  return plan_diff_decode(C, std::max(rows, 1), max_seq_len, num_sms).ws_bytes + static_cast<size_t>(n_tok) * 8;
+}
+
+int launch_diff(const Launch& L, const CacheView& C, const void* q, int q_dtype, const int32_t* offsets, int n_tok,
+                const int32_t* pt, int64_t max_pages, const int32_t* lens, const int32_t* steps, int n_seqs,
+                int max_seq_len, float sm_scale, const k8v4_diff& diff, void* out, void* ws) {
+  const int rows = std::min(n_tok, kRowsAtOnce);
+  const DiffPlan plan = plan_diff_decode(C, rows, max_seq_len, L.num_sms);
+  int32_t* row_seq = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(ws) + plan.ws_bytes);
+  int32_t* row_vis = row_seq + n_tok;
+  int rc = launch_behind(L, diff_tokens_kernel, dim3((n_tok + 255) / 256), dim3(256), offsets, lens, steps, n_seqs, n_tok,
+                         max_seq_len, row_seq, row_vis, L.status);
+  const int64_t row_elems = static_cast<int64_t>(C.H) * kGqa * kD;
+  for (int first = 0; rc == K8V4_OK && first < n_tok; first += rows) {
+    const int n = std::min(rows, n_tok - first);
+    rc = launch_rows(L, C, plan, static_cast<const uint8_t*>(q) + first * row_elems * (q_dtype == K8V4_F32 ? 4 : 2), q_dtype, pt,
+                     max_pages, row_vis + first, row_seq + first, n, max_seq_len, sm_scale, diff,
+                     static_cast<uint16_t*>(out) + first * row_elems, ws);
+  }
+  return rc;
+}
+
+}  // namespace k8v4
