@@ -19,7 +19,7 @@ BINDING = os.path.join(BUILD, "_k8v4_binding.so")
 BINDING_ERROR = os.path.join(BUILD, "binding_error.log")      # why the module could not be built, if so
 SOURCES = ["k8v4_api.cu", "k8v4_append.cu", "k8v4_attend.cu", "k8v4_decode.cu", "k8v4_verify.cu", "k8v4_combine.cu", "k8v4_prefill.cu", "k8v4_noalloc.cu",
            "k8v4_stream.cu", "k8v4_rope.cu", "k8v4_append_rope.cu", "k8v4_accept.cu", "k8v4_shared.cu",
-           "k8v4_plan.cu", "k8v4_slots.cu", "k8v4_diff.cu", "k8v4_block_norm.cu"]
+           "k8v4_plan.cu", "k8v4_slots.cu", "k8v4_diff.cu", "k8v4_diff_tc.cu", "k8v4_block_norm.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr", "-Xptxas", "-v"]
 

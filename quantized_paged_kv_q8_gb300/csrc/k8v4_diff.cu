@@ -72,7 +72,6 @@ struct DiffParams {
   const int32_t* pt;
   int64_t max_pages;
   const int32_t* lens;        // visible cells of each row
-  const int32_t* row_seq;     // table row of each row, or null: its own index
   int max_seq_len, cells_per_split, splits;
   float sm_scale_log2;
   float* ws;
@@ -180,8 +179,7 @@ __global__ void __launch_bounds__(32 * kMaxWorkers, 1)
   const CacheView& C = p.C;
   const int H = C.H, HQ = H * kGqa;
   const int r0 = lane >> 2, c = lane & 3;
-  const int b = p.row_seq ? p.row_seq[row] : row;
-  int n_vis = b >= 0 ? p.lens[row] : 0;
+  int n_vis = p.lens[row];
   if (n_vis < 0 || n_vis > p.max_seq_len) {
     if (threadIdx.x == 0 && split == 0 && g == 0) record_status(p.status, K8V4_ERANGE);
     n_vis = n_vis < 0 ? 0 : p.max_seq_len;
@@ -203,7 +201,7 @@ __global__ void __launch_bounds__(32 * kMaxWorkers, 1)
   }
 
   // ---- this worker's copies: local tile u -> stage u % kStages
-  const int32_t* pt_row = p.pt + static_cast<int64_t>(b) * p.max_pages;
+  const int32_t* pt_row = p.pt + static_cast<int64_t>(row) * p.max_pages;
   int win0 = -1000000, win_page = -1;
   auto page_of = [&](int u) -> int {         // warp-uniform u; all lanes call
     if (u < win0 || u >= win0 + 32) {
@@ -510,120 +508,29 @@ __global__ void __launch_bounds__(32 * kMaxWorkers, 1)
 // ---------------------------------------------------------------- the combine
 struct CombineParams {
   const float* ws;
-  const int32_t* row_seq;     // rows without a sequence (< 0) are left as they are; or null
-  int splits, H;
+  DiffRagged r;               // a ragged batch's rows
+  int splits;                 // else: ranges of every row
+  int H, n_rows;              // rows: (sequence or token, query head)
   k8v4_diff d;
   uint16_t* out;
 };
-constexpr int kCombineWarps = 4, kMaxSplits = kDecodeMaxSplits;
+constexpr int kCombineWarps = 4;
 
-// One CTA per (row, query head): the splits of both maps joined, their difference
-// brought back from rotated space (linear, so once for both), normed and rounded.
-__global__ void __launch_bounds__(32 * kCombineWarps) diff_combine_kernel(const CombineParams p) {
-  __shared__ float wt[2][kMaxSplits];
-  __shared__ float red[2][2][kCombineWarps];
-  __shared__ float4 part[2][kCombineWarps][64];
-  __shared__ float lam_s[2];
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
-  const int HQ = p.H * kGqa;
-  const int row = blockIdx.x / HQ, hq = blockIdx.x - row * HQ;
-  const int g = hq / kGqa, h = hq % kGqa;
-  if (p.row_seq && p.row_seq[row] < 0) return;
-  const float* base = p.ws + ((static_cast<int64_t>(row) * p.H + g) * p.splits * 16 + h) * kDiffRow;
-  constexpr int64_t kSplitStride = 16 * kDiffRow;
-  float Mx[2], L[2];
+// the first warps of a row: exp(q1 . k1) and exp(q2 . k2) of its head (0 without vectors)
+__device__ __forceinline__ float lambda_term(const k8v4_diff& d, int hq, int term, int lane) {
+  if (!d.lambda_q1) return 0.0f;
+  const int64_t at = (d.n_lambda > 1 ? hq * 128 : 0) + 4 * lane;
+  const float4 a = *reinterpret_cast<const float4*>((term ? d.lambda_q2 : d.lambda_q1) + at);
+  const float4 b = *reinterpret_cast<const float4*>((term ? d.lambda_k2 : d.lambda_k1) + at);
+  float dot = a.x * b.x + a.y * b.y + a.z * b.z + a.w * b.w;
 #pragma unroll
-  for (int m = 0; m < 2; ++m) {
-    Mx[m] = -INFINITY;
-    for (int s = t; s < p.splits; s += 32 * kCombineWarps) {
-      const float v = base[s * kSplitStride + 8 * m * kDiffRow + 256];
-      wt[m][s] = v;
-      Mx[m] = fmaxf(Mx[m], v);
-    }
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) Mx[m] = fmaxf(Mx[m], __shfl_xor_sync(kFull, Mx[m], o));
-    if (lane == 0) red[0][m][warp] = Mx[m];
-  }
-  // lambda of the head: warp m takes map m's dot product
-  if (warp < 2) {
-    float dot = 0.0f;
-    if (p.d.lambda_q1) {
-      const int64_t at = (p.d.n_lambda > 1 ? hq * 128 : 0) + 4 * lane;
-      const float4 a = *reinterpret_cast<const float4*>((warp ? p.d.lambda_q2 : p.d.lambda_q1) + at);
-      const float4 b = *reinterpret_cast<const float4*>((warp ? p.d.lambda_k2 : p.d.lambda_k1) + at);
-      dot = a.x * b.x + a.y * b.y + a.z * b.z + a.w * b.w;
-#pragma unroll
-      for (int o = 16; o >= 1; o >>= 1) dot += __shfl_xor_sync(kFull, dot, o);
-      dot = expf(dot);
-    }
-    if (lane == 0) lam_s[warp] = dot;
-  }
-  __syncthreads();
-#pragma unroll
-  for (int m = 0; m < 2; ++m) {
-#pragma unroll
-    for (int w = 0; w < kCombineWarps; ++w) Mx[m] = fmaxf(Mx[m], red[0][m][w]);
-    L[m] = 0.0f;
-    for (int s = t; s < p.splits; s += 32 * kCombineWarps) {
-      const float w = wt[m][s] == -INFINITY ? 0.0f : exp2f(wt[m][s] - Mx[m]);
-      if (w != 0.0f) L[m] += w * base[s * kSplitStride + 8 * m * kDiffRow + 257];
-      wt[m][s] = w;
-    }
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) L[m] += __shfl_xor_sync(kFull, L[m], o);
-    if (lane == 0) red[1][m][warp] = L[m];
-  }
-  __syncthreads();
-#pragma unroll
-  for (int m = 0; m < 2; ++m) {
-    float acc[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-    constexpr int kUnroll = 4;
-    for (int s0 = warp; s0 < p.splits; s0 += kCombineWarps * kUnroll) {
-      float4 x[kUnroll][2];
-      float w[kUnroll];
-#pragma unroll
-      for (int k = 0; k < kUnroll; ++k) {
-        const int s = s0 + kCombineWarps * k;
-        w[k] = s < p.splits ? wt[m][s] : 0.0f;
-        if (w[k] != 0.0f) {
-          const float4* src = reinterpret_cast<const float4*>(base + s * kSplitStride + 8 * m * kDiffRow);
-          x[k][0] = src[lane];
-          x[k][1] = src[32 + lane];
-        }
-      }
-#pragma unroll
-      for (int k = 0; k < kUnroll; ++k) {
-        if (w[k] == 0.0f) continue;
-        acc[0] += x[k][0].x * w[k]; acc[1] += x[k][0].y * w[k]; acc[2] += x[k][0].z * w[k]; acc[3] += x[k][0].w * w[k];
-        acc[4] += x[k][1].x * w[k]; acc[5] += x[k][1].y * w[k]; acc[6] += x[k][1].z * w[k]; acc[7] += x[k][1].w * w[k];
-      }
-    }
-    part[m][warp][lane] = make_float4(acc[0], acc[1], acc[2], acc[3]);
-    part[m][warp][32 + lane] = make_float4(acc[4], acc[5], acc[6], acc[7]);
-  }
-  __syncthreads();
-  if (warp) return;
-  // lane: dims 4 lane + e and 128 + 4 lane + e
-  const float lambda = p.d.lambda_q1 ? lam_s[0] - lam_s[1] + p.d.lambda_init : p.d.lambda_init;
-  float v[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-  for (int m = 0; m < 2; ++m) {
-    float Lt = 0.0f;
-#pragma unroll
-    for (int w = 0; w < kCombineWarps; ++w) Lt += red[1][m][w];
-    const float inv = Lt > 0.0f ? (m ? -lambda : 1.0f) / Lt : 0.0f;
-    float s[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-    for (int w = 0; w < kCombineWarps; ++w) {
-      const float4 a = part[m][w][lane], b = part[m][w][32 + lane];
-      s[0] += a.x; s[1] += a.y; s[2] += a.z; s[3] += a.w;
-      s[4] += b.x; s[5] += b.y; s[6] += b.z; s[7] += b.w;
-    }
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] += s[e] * inv;
-  }
+  for (int o = 16; o >= 1; o >>= 1) dot += __shfl_xor_sync(kFull, dot, o);
+  return expf(dot);
+}
+
+// a warp: the difference in rotated space (lane: dims 4 lane + e and 128 + 4 lane + e) brought
+// back (linear, so once for both maps), normed, scaled, rounded and written
+__device__ __forceinline__ void finish_row(float v[8], const k8v4_diff& d, int lane, uint16_t* out) {
 #pragma unroll
   for (int hh = 1; hh < 8; hh <<= 1) {
 #pragma unroll
@@ -649,27 +556,160 @@ __global__ void __launch_bounds__(32 * kCombineWarps) diff_combine_kernel(const 
     v[e] *= 0.0625f;
     s2 += v[e] * v[e];
   }
-  if (p.d.norm_weight) {
+  if (d.norm_weight) {
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) s2 += __shfl_xor_sync(kFull, s2, o);
-    const float scale = rsqrtf(s2 * (1.0f / kD) + p.d.eps) * p.d.out_scale;
-    const float4 wa = reinterpret_cast<const float4*>(p.d.norm_weight)[lane], wb = reinterpret_cast<const float4*>(p.d.norm_weight)[32 + lane];
     const bool seen = s2 != 0.0f;        // a row of zeros stays one where eps is 0
-    v[0] = seen ? v[0] * scale * wa.x : 0.0f; v[1] = seen ? v[1] * scale * wa.y : 0.0f;
-    v[2] = seen ? v[2] * scale * wa.z : 0.0f; v[3] = seen ? v[3] * scale * wa.w : 0.0f;
-    v[4] = seen ? v[4] * scale * wb.x : 0.0f; v[5] = seen ? v[5] * scale * wb.y : 0.0f;
-    v[6] = seen ? v[6] * scale * wb.z : 0.0f; v[7] = seen ? v[7] * scale * wb.w : 0.0f;
+    const float scale = seen ? rsqrtf(s2 * (1.0f / kD) + d.eps) * d.out_scale : 0.0f;
+    const float4 wa = reinterpret_cast<const float4*>(d.norm_weight)[lane], wb = reinterpret_cast<const float4*>(d.norm_weight)[32 + lane];
+    v[0] *= scale * wa.x; v[1] *= scale * wa.y; v[2] *= scale * wa.z; v[3] *= scale * wa.w;
+    v[4] *= scale * wb.x; v[5] *= scale * wb.y; v[6] *= scale * wb.z; v[7] *= scale * wb.w;
   } else {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] *= p.d.out_scale;
+    for (int e = 0; e < 8; ++e) v[e] *= d.out_scale;
   }
   auto two = [](float lo, float hi) {
     const __nv_bfloat162 x = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&x);
   };
-  uint2* dst = reinterpret_cast<uint2*>(p.out + static_cast<int64_t>(blockIdx.x) * kD);
+  uint2* dst = reinterpret_cast<uint2*>(out);
   dst[lane] = make_uint2(two(v[0], v[1]), two(v[2], v[3]));
   dst[32 + lane] = make_uint2(two(v[4], v[5]), two(v[6], v[7]));
+}
+
+// WARPS to a (row, query head), rows of 4 / WARPS a CTA: four warps where a row has tens of
+// ranges, one where thousands of rows have a few each.
+template <int WARPS, bool RAGGED>
+__global__ void __launch_bounds__(32 * kCombineWarps) diff_combine_kernel(const CombineParams p) {
+  constexpr int kRowsCta = kCombineWarps / WARPS;
+  constexpr int kMost = RAGGED ? kDiffMostRanges : kDecodeMaxSplits;
+  __shared__ float wt[kRowsCta][2][kMost];
+  __shared__ float red[kRowsCta][2][2][WARPS];
+  __shared__ float4 part[WARPS > 1 ? kRowsCta : 1][2][WARPS][64];
+  __shared__ float lam_s[2];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int lane = threadIdx.x & 31, slot = (threadIdx.x >> 5) / WARPS, warp = (threadIdx.x >> 5) % WARPS;
+  const int t = warp * 32 + lane;                       // of the row's threads
+  const int rr = blockIdx.x * kRowsCta + slot;
+  if (rr >= p.n_rows) return;
+  const int HQ = p.H * kGqa;
+  const int row = rr / HQ, hq = rr - row * HQ;
+  const int g = hq / kGqa, h = hq % kGqa;
+  const float* base;                                    // range s of map m: base + m * m_stride + s * s_stride
+  int64_t m_stride, s_stride;
+  int splits;
+  if (RAGGED) {
+    const int i = p.r.tok_tile[row];
+    if (i < 0) return;                                  // no sequence's: left as it is
+    const int32_t* tile = p.r.tiles + 8 * static_cast<int64_t>(i);
+    splits = min(tile[3], kMost);
+    s_stride = 256 * kDiffRow;
+    m_stride = s_stride * splits;
+    base = p.ws + (static_cast<int64_t>(tile[4]) + 2 * g * splits) * s_stride + ((row - tile[1]) * kGqa + h) * kDiffRow;
+  } else {
+    splits = p.splits;
+    m_stride = kGqa * kDiffRow;
+    s_stride = 2 * m_stride;
+    base = p.ws + (static_cast<int64_t>(row) * p.H + g) * splits * s_stride + h * kDiffRow;
+  }
+  auto sync = [] {
+    if (WARPS == 1) __syncwarp();
+    else __syncthreads();
+  };
+  float Mx[2], L[2];
+#pragma unroll
+  for (int m = 0; m < 2; ++m) {
+    Mx[m] = -INFINITY;
+    for (int s = t; s < splits; s += 32 * WARPS) {
+      const float v = base[m * m_stride + s * s_stride + 256];
+      wt[slot][m][s] = v;
+      Mx[m] = fmaxf(Mx[m], v);
+    }
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) Mx[m] = fmaxf(Mx[m], __shfl_xor_sync(kFull, Mx[m], o));
+    if (WARPS > 1 && lane == 0) red[slot][0][m][warp] = Mx[m];
+  }
+  float term[2] = {0.0f, 0.0f};
+  if (WARPS == 1) {
+    term[0] = lambda_term(p.d, hq, 0, lane);
+    term[1] = lambda_term(p.d, hq, 1, lane);
+  } else if (warp < 2) {
+    const float e = lambda_term(p.d, hq, warp, lane);
+    if (lane == 0) lam_s[warp] = e;
+  }
+  sync();
+#pragma unroll
+  for (int m = 0; m < 2; ++m) {
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w)
+      if (WARPS > 1) Mx[m] = fmaxf(Mx[m], red[slot][0][m][w]);
+    L[m] = 0.0f;
+    for (int s = t; s < splits; s += 32 * WARPS) {
+      const float v = wt[slot][m][s], w = v == -INFINITY ? 0.0f : exp2f(v - Mx[m]);
+      if (w != 0.0f) L[m] += w * base[m * m_stride + s * s_stride + 257];
+      wt[slot][m][s] = w;
+    }
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) L[m] += __shfl_xor_sync(kFull, L[m], o);
+    if (WARPS > 1 && lane == 0) red[slot][1][m][warp] = L[m];
+  }
+  sync();
+  float acc[2][8];
+#pragma unroll
+  for (int m = 0; m < 2; ++m) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) acc[m][e] = 0.0f;
+    constexpr int kUnroll = WARPS == 1 ? 2 : 4;
+    for (int s0 = warp; s0 < splits; s0 += WARPS * kUnroll) {
+      float4 x[kUnroll][2];
+      float w[kUnroll];
+#pragma unroll
+      for (int k = 0; k < kUnroll; ++k) {
+        const int s = s0 + WARPS * k;
+        w[k] = s < splits ? wt[slot][m][s] : 0.0f;
+        if (w[k] != 0.0f) {                             // a range with nothing seen has no o either
+          const float4* src = reinterpret_cast<const float4*>(base + m * m_stride + s * s_stride);
+          x[k][0] = src[lane];
+          x[k][1] = src[32 + lane];
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < kUnroll; ++k) {
+        if (w[k] == 0.0f) continue;
+        acc[m][0] += x[k][0].x * w[k]; acc[m][1] += x[k][0].y * w[k]; acc[m][2] += x[k][0].z * w[k]; acc[m][3] += x[k][0].w * w[k];
+        acc[m][4] += x[k][1].x * w[k]; acc[m][5] += x[k][1].y * w[k]; acc[m][6] += x[k][1].z * w[k]; acc[m][7] += x[k][1].w * w[k];
+      }
+    }
+    if (WARPS > 1) {
+      part[slot][m][warp][lane] = make_float4(acc[m][0], acc[m][1], acc[m][2], acc[m][3]);
+      part[slot][m][warp][32 + lane] = make_float4(acc[m][4], acc[m][5], acc[m][6], acc[m][7]);
+    }
+  }
+  if (WARPS > 1) {
+    __syncthreads();
+    if (warp) return;
+    term[0] = lam_s[0];
+    term[1] = lam_s[1];
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+      L[m] = 0.0f;
+#pragma unroll
+      for (int w = 0; w < WARPS; ++w) {
+        L[m] += red[slot][1][m][w];
+        if (w == 0) continue;
+        const float4 a = part[slot][m][w][lane], b = part[slot][m][w][32 + lane];
+        acc[m][0] += a.x; acc[m][1] += a.y; acc[m][2] += a.z; acc[m][3] += a.w;
+        acc[m][4] += b.x; acc[m][5] += b.y; acc[m][6] += b.z; acc[m][7] += b.w;
+      }
+    }
+  }
+  const float lambda = p.d.lambda_q1 ? term[0] - term[1] + p.d.lambda_init : p.d.lambda_init;
+  const float f0 = L[0] > 0.0f ? 1.0f / L[0] : 0.0f, f1 = L[1] > 0.0f ? -lambda / L[1] : 0.0f;
+  float v[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] = acc[0][e] * f0 + acc[1][e] * f1;
+  finish_row(v, p.d, lane, p.out + static_cast<int64_t>(rr) * kD);
 }
 
 }  // namespace
@@ -704,21 +744,23 @@ DiffPlan plan_diff_decode(const CacheView& C, int n_seqs, int max_seq_len, int n
   return pl;
 }
 
-int launch_diff_combine(const Launch& L, const float* ws, int splits, const int32_t* row_seq, int n_rows, int H, const k8v4_diff& diff, void* out) {
+int launch_diff_combine_ragged(const Launch& L, const float* ws, const DiffRagged& r, int n_tok, int H, bool wide,
+                               const k8v4_diff& diff, void* out) {
   CombineParams p;
   p.ws = ws;
-  p.row_seq = row_seq;
-  p.splits = splits;
+  p.r = r;
+  p.splits = 0;
   p.H = H;
+  p.n_rows = n_tok * H * kGqa;                          // below 2^30
   p.d = diff;
   p.out = static_cast<uint16_t*>(out);
-  return launch_behind(L, diff_combine_kernel, dim3(static_cast<unsigned>(n_rows) * H * kGqa), dim3(32 * kCombineWarps), p);
+  if (wide) return launch_behind(L, diff_combine_kernel<4, true>, dim3(p.n_rows), dim3(32 * kCombineWarps), p);
+  return launch_behind(L, diff_combine_kernel<1, true>, dim3((p.n_rows + kCombineWarps - 1) / kCombineWarps), dim3(32 * kCombineWarps), p);
 }
 
-namespace {
-int launch_rows(const Launch& L, const CacheView& C, const DiffPlan& plan, const void* q, int q_dtype, const int32_t* pt,
-                int64_t max_pages, const int32_t* lens, const int32_t* row_seq, int n_rows, int max_seq_len, float sm_scale,
-                const k8v4_diff& diff, void* out, void* ws) {
+int launch_diff_decode(const Launch& L, const CacheView& C, const DiffPlan& plan, const void* q, int q_dtype,
+                       const int32_t* pt, int64_t max_pages, const int32_t* lens, int n_seqs, int max_seq_len,
+                       float sm_scale, const k8v4_diff& diff, void* out, void* ws) {
   DiffParams p;
   p.C = C;
   p.q = q;
@@ -726,7 +768,6 @@ int launch_rows(const Launch& L, const CacheView& C, const DiffPlan& plan, const
   p.pt = pt;
   p.max_pages = max_pages;
   p.lens = lens;
-  p.row_seq = row_seq;
   p.max_seq_len = max_seq_len;
   p.cells_per_split = plan.cells_per_split;
   p.splits = plan.splits;
@@ -742,7 +783,7 @@ int launch_rows(const Launch& L, const CacheView& C, const DiffPlan& plan, const
       cudaFuncSetAttribute(diff_split_kernel, cudaFuncAttributePreferredSharedMemoryCarveout, 100) != cudaSuccess)
     return K8V4_ECUDA;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(p.splits, C.H, n_rows);
+  cfg.gridDim = dim3(p.splits, C.H, n_seqs);
   cfg.blockDim = dim3(32 * p.L.workers);
   cfg.dynamicSmemBytes = p.L.total;
   cfg.stream = L.stream;
@@ -753,80 +794,15 @@ int launch_rows(const Launch& L, const CacheView& C, const DiffPlan& plan, const
   cfg.numAttrs = 1;
   if (cudaLaunchKernelEx(&cfg, diff_split_kernel, mk, mv, p) != cudaSuccess) return K8V4_ECUDA;
   if (cudaGetLastError() != cudaSuccess) return K8V4_ECUDA;
-  return launch_diff_combine(L, p.ws, p.splits, row_seq, n_rows, C.H, diff, out);
-}
-}  // namespace
-
-int launch_diff_decode(const Launch& L, const CacheView& C, const DiffPlan& plan, const void* q, int q_dtype,
-                       const int32_t* pt, int64_t max_pages, const int32_t* lens, int n_seqs, int max_seq_len,
-                       float sm_scale, const k8v4_diff& diff, void* out, void* ws) {
-  return launch_rows(L, C, plan, q, q_dtype, pt, max_pages, lens, nullptr, n_seqs, max_seq_len, sm_scale, diff, out, ws);
-}
-
-// ---------------------------------------------------------------- a ragged batch
-namespace {
-constexpr int kRowsAtOnce = 65535;
-
-// the sequence of each packed token (-1: none) and the cells that it sees
-__global__ void __launch_bounds__(256) diff_tokens_kernel(const int32_t* offsets, const int32_t* lens, const int32_t* steps,
-                                                          int n_seqs, int n_tok, int max_seq_len, int32_t* row_seq,
-                                                          int32_t* row_vis, int* status) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int t = blockIdx.x * 256 + threadIdx.x;
-  if (t >= n_tok) return;
-  // the last sequence that begins at or ahead of the token
-  int lo = 0, hi = n_seqs;
-  while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
-    if (offsets[mid] > t) hi = mid;
-    else lo = mid + 1;
-  }
-  const int b = lo - 1;
-  int seq = -1, vis = 0;
-  if (b >= 0) {
-    const int first = offsets[b], end = offsets[b + 1];
-    if (first < 0 || end < first || end > n_tok) record_status(status, K8V4_ERANGE);
-    else if (t < end) {
-      seq = b;
-      int len = lens[b];
-      if (len < 0 || len > max_seq_len) {
-        record_status(status, K8V4_ERANGE);
-        len = len < 0 ? 0 : max_seq_len;
-      }
-      vis = steps ? steps[t] : max(len - (end - t) + 1, 0);
-      if (vis < 0 || vis > len) {
-        record_status(status, K8V4_ERANGE);
-        vis = vis < 0 ? 0 : len;
-      }
-    }
-  }
-  row_seq[t] = seq;
-  row_vis[t] = vis;
-}
-}  // namespace
-
-size_t diff_ws_bytes(const CacheView& C, int n_seqs, int n_tok, int max_seq_len, int num_sms) {
-  const int rows = std::min(n_tok, kRowsAtOnce);
-  return plan_diff_decode(C, std::max(rows, 1), max_seq_len, num_sms).ws_bytes + static_cast<size_t>(n_tok) * 8;
-}
-
-int launch_diff(const Launch& L, const CacheView& C, const void* q, int q_dtype, const int32_t* offsets, int n_tok,
-                const int32_t* pt, int64_t max_pages, const int32_t* lens, const int32_t* steps, int n_seqs,
-                int max_seq_len, float sm_scale, const k8v4_diff& diff, void* out, void* ws) {
-  const int rows = std::min(n_tok, kRowsAtOnce);
-  const DiffPlan plan = plan_diff_decode(C, rows, max_seq_len, L.num_sms);
-  int32_t* row_seq = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(ws) + plan.ws_bytes);
-  int32_t* row_vis = row_seq + n_tok;
-  int rc = launch_behind(L, diff_tokens_kernel, dim3((n_tok + 255) / 256), dim3(256), offsets, lens, steps, n_seqs, n_tok,
-                         max_seq_len, row_seq, row_vis, L.status);
-  const int64_t row_elems = static_cast<int64_t>(C.H) * kGqa * kD;
-  for (int first = 0; rc == K8V4_OK && first < n_tok; first += rows) {
-    const int n = std::min(rows, n_tok - first);
-    rc = launch_rows(L, C, plan, static_cast<const uint8_t*>(q) + first * row_elems * (q_dtype == K8V4_F32 ? 4 : 2), q_dtype, pt,
-                     max_pages, row_vis + first, row_seq + first, n, max_seq_len, sm_scale, diff,
-                     static_cast<uint16_t*>(out) + first * row_elems, ws);
-  }
-  return rc;
+  CombineParams c;
+  c.ws = p.ws;
+  c.r = DiffRagged{nullptr, nullptr};
+  c.splits = p.splits;
+  c.H = C.H;
+  c.n_rows = n_seqs * C.H * kGqa;
+  c.d = diff;
+  c.out = static_cast<uint16_t*>(out);
+  return launch_behind(L, diff_combine_kernel<4, false>, dim3(c.n_rows), dim3(32 * kCombineWarps), c);
 }
 
 }  // namespace k8v4

@@ -1,5 +1,5 @@
 // What the kernels of differential attention share: the layout of their partial rows
-// and the combine that joins them.
+// and the combines that join them.
 #pragma once
 
 #include "k8v4_ops.cuh"
@@ -10,10 +10,19 @@ namespace k8v4 {
 // exponent, -inf: no cell seen), l (the sum of 2^(score - m)), two unused floats.
 constexpr int kDiffRow = 260;
 
-// Where the partial rows of a (row, KV head) are: split s of map m and query head h (of the
-// head's 8) at ws + (((first + s) * 2 + m) * 8 + h) * kDiffRow.
-// The rows of single queries: first = (row * H + g) * splits, all with `splits` splits.
-int launch_diff_combine(const Launch& L, const float* ws, int splits, const int32_t* row_seq, int n_rows, int H,
-                        const k8v4_diff& diff, void* out);
+// the CTA pairs that a ragged batch is planned for, at most, and the ranges that a row has
+// then (2 * pairs / H, rounded up)
+constexpr int kDiffMostPairs = 128, kDiffMostRanges = 2 * kDiffMostPairs + 2;
+
+// A ragged batch's rows: each packed token's tile (-1: no sequence's), and the tiles of 8
+// words: [1] the first token, [3] ranges, [4] the first block.  Range s of map m of query head
+// h, KV head g, is in block first + (2 g + m) * ranges + s, row (token - first token) * 8 + h,
+// blocks of 256 rows.
+struct DiffRagged {
+  const int32_t* tok_tile;
+  const int32_t* tiles;
+};
+int launch_diff_combine_ragged(const Launch& L, const float* ws, const DiffRagged& r, int n_tok, int H, bool wide,
+                               const k8v4_diff& diff, void* out);
 
 }  // namespace k8v4

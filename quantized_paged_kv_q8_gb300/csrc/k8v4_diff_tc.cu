@@ -1,0 +1,1033 @@
+// Differential attention of a ragged batch over the k8v4 cache on the 5th-generation
+// tensor cores:
+//
+//   O_m = softmax(scale q_m K_m^T) V,  m = 1, 2,   x = O_1 - lambda O_2
+//
+// Both maps of a row weigh the same values, but their sums are known only when the last
+// cell is scored, so each map keeps an O of its own: 2 x 256 fp32 columns a row, all of
+// tensor memory.  A unit of work is therefore ONE map of a tile of 32 tokens (x the 8 query
+// heads of a KV head = 256 rows) over a range of the cells: a CTA pair (tcgen05
+// cta_group::2, M = 256, 128 rows per SM) keeps its O in tensor memory and sweeps the range
+// in tiles of 128 cells
+//   S  = Q_m K_m^T        128 lanes, N = 128
+//   P  = 2^(s - ref) 2^7  online softmax in the log2 domain, fp16
+//   O += P V              N = 256, V = RN((n - 8) / 8 d) in fp16
+// and writes its partial rows (o, m, l); the combine joins ranges and maps.  The two maps'
+// units read and convert the same V; a pair that kept both maps of 16 tokens instead would
+// need both key halves too, and twice the conversions per product.
+//
+// Each CTA of the pair dequantises half of every tile (64 of the 128 cells of K, 128 of the
+// 256 dims of V); the pair reads both halves as one operand.  P and V are rounded to fp16
+// once (2^-12 of each term; the result is bf16), so a tile takes 8 products of 64 clocks for
+// S and 8 of 128 for O where the exact kernels' two terms each would take three times the
+// latter.
+//
+// Roles, handing over through mbarriers:
+//      warps 0-15   rows: four threads per row (32 cells, and 64 of O's dims, each)
+//      warps 16-19  conversion: raw tile -> registers -> operand tiles
+//      warp 20      (leader CTA) issues every product of the pair
+//      warp 21      copies the raw tiles (TMA)
+// The reference maximum of a row moves only when a tile exceeds it by 2^8, and then its O
+// is rescaled in tensor memory.  Every kChain tiles O is added to a running sum in
+// global memory (the unit's own partial rows serve as its place), because the tensor core's
+// accumulation is not rounded to nearest: measured 2.9e-5 after 2,048 cells in three products
+// each, so about 4e-5 after kChain tiles here.
+//
+// The units come from a schedule that one CTA works out on the device from the lengths:
+// token tiles, heaviest first within a sequence, cut into ranges so that the pairs of the
+// device are evenly loaded.
+//
+// Tensor memory (512 columns): S buffers [0,128), [128,256) (a thread's P overlays its
+// own columns), O [256,512).
+//
+// Every mbarrier wait is bounded: on timeout the warp raises the CTA's failure word and
+// leaves its loop (the row warps together, at their next vote); the kernel records an
+// error, waits for its own products (bounded), frees its tensor memory and returns.
+#include <algorithm>
+#include <mutex>
+
+#include "k8v4_diff.cuh"
+#include "k8v4_tc.cuh"
+#include "k8v4_tma.cuh"
+
+namespace k8v4 {
+namespace {
+
+constexpr unsigned kFull = 0xffffffffu;
+constexpr int kRows = 128;                    // query rows per CTA (256 per pair)
+constexpr int kTileN = 128;                   // cells per tile
+constexpr int kRowWarps = 16, kRowThreads = 32 * kRowWarps;
+constexpr int kThreads = kRowThreads + 256;
+constexpr int kConvWarp0 = kRowWarps, kIssueWarp = kConvWarp0 + 4, kLoadWarp = kIssueWarp + 1;
+static_assert(kConvWarp0 % 4 == 0 && kIssueWarp % 4 == 0 && kLoadWarp < kIssueWarp + 4 && kThreads == 32 * (kIssueWarp + 4), "roles");
+constexpr int kChain = 64;                    // tiles accumulated in tensor memory (8,192 cells)
+constexpr float kSlack = 8.0f;                // log2 headroom of P above its row's reference maximum
+constexpr uint32_t kWaitDefaultNs = 1000000000u;
+constexpr int kLaunchRegs = 80, kRowRegs = 96, kConvRegs = 72, kIssueRegs = 24;
+static_assert(4 * kRowRegs + kConvRegs + kIssueRegs <= 6 * kLaunchRegs, "register split");
+
+// shared memory (bytes); operand tiles 1024-byte aligned, the same in both CTAs
+constexpr int kQOff = 0;                              // Q fp16 [2 chunks][128 rows][128 B]
+constexpr int kKOff = kQOff + 32768;                  // K fp16, 2 buffers x [2 chunks][64 cells][128 B]
+constexpr int kKBuf = 16384;
+constexpr int kVOff = kKOff + 2 * kKBuf;              // V fp16, 2 buffers x [2 atoms][128 cells][128 B]
+constexpr int kVBuf = 32768, kVAtom = 16384;
+constexpr int kKsOff = kVOff + 2 * kVBuf;             // K scales, 4 tiles x [128] f32
+constexpr int kRedOff = kKsOff + 4 * 512;             // [4][128] f32 exchange, [128] score factors
+constexpr int kBarOff = kRedOff + 4 * 512 + 512;
+constexpr int kCtlOff = kBarOff + 192;                // tmem slot, failure word, bad groups of 4 tiles, valid groups of the stages
+constexpr int kRawOff = (kCtlOff + 64 + 1023) / 1024 * 1024;
+constexpr int kSmemMax = 227 * 1024;
+// a raw tile: K codes of the CTA's 64 cells (4 boxes of 16 cells x 128 B), V nibbles of the 128 cells (8 boxes),
+// and the runs of K and V scales of all heads (8 groups x 128 H and 256 H bytes)
+constexpr int kRawV = 8192, kRawKs = 24576;
+constexpr int raw_bytes(int H) { return (kRawKs + 3072 * H + 1023) / 1024 * 1024; }
+constexpr int raw_stages(int H) { return (kSmemMax - kRawOff) / raw_bytes(H) < 3 ? (kSmemMax - kRawOff) / raw_bytes(H) : 3; }
+static_assert(raw_stages(2) == 3 && raw_stages(7) >= 2 && raw_stages(8) >= 1, "raw stages");
+// the epilogue reuses the operand tiles as a fp32 [128][256] row buffer
+static_assert(kKsOff - kQOff >= kRows * 256 * 4, "row buffer");
+
+// mbarriers, at kBarOff + 8 * index
+enum { kBarKFull = 0, kBarVFull = 2, kBarPFull = 4, kBarSFull = 6, kBarODone = 8, kBarKsFull = 10, kBarDrain = 14,
+       kBarRawFull = 16, kBarRawEmpty = 20 };
+
+constexpr uint32_t kTmemCols = 512, kSBuf = 128, kOCol = 256;
+
+// ---------------------------------------------------------------- the schedule
+constexpr int kTileTok = 32;                  // tokens of a token tile
+constexpr int kMostWaves = 4;                 // ranges: at most this many per pair of the device, on average
+struct TokenTile {
+  int seq, tok0, n, splits, first, cell_tiles, per_split, vis0;   // vis0: cells that its first token sees (causal)
+};
+
+struct Schedule {                             // places in the workspace
+  int32_t* head;                              // [0] units, [1] token tiles
+  int32_t* tile_end;                          // [n_seqs] token tiles up to each sequence
+  TokenTile* tiles;
+  int32_t* tok_tile;                          // [n_tok], -1: no sequence
+  int2* units;                                // {token tile, (split << 4) | (KV head << 1) | map}
+  float* rows;                                // partial blocks of 256 rows
+};
+int64_t most_tiles(int n_seqs, int n_tok) { return n_tok / kTileTok + std::min(n_seqs, n_tok); }
+int64_t most_units(int n_seqs, int n_tok, int max_seq_len, int H, int pairs) {
+  const int64_t base = most_tiles(n_seqs, n_tok) * 2 * H;
+  return std::min(base * std::max(1, (max_seq_len + kTileN - 1) / kTileN), base + static_cast<int64_t>(kMostWaves) * pairs);
+}
+size_t place(Schedule* s, uint8_t* ws, int n_seqs, int n_tok, int max_seq_len, int H, int pairs) {
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    uint8_t* p = ws + at;
+    at += (bytes + 255) / 256 * 256;
+    return p;
+  };
+  const int64_t tiles = most_tiles(n_seqs, n_tok), units = most_units(n_seqs, n_tok, max_seq_len, H, pairs);
+  Schedule t;
+  t.head = reinterpret_cast<int32_t*>(take(8));
+  t.tile_end = reinterpret_cast<int32_t*>(take(4 * static_cast<size_t>(n_seqs)));
+  t.tiles = reinterpret_cast<TokenTile*>(take(sizeof(TokenTile) * tiles));
+  t.tok_tile = reinterpret_cast<int32_t*>(take(4 * static_cast<size_t>(n_tok)));
+  t.units = reinterpret_cast<int2*>(take(8 * units));
+  t.rows = reinterpret_cast<float*>(take(static_cast<size_t>(units) * 2 * kRows * kDiffRow * sizeof(float)));
+  if (s) *s = t;
+  return at;
+}
+
+struct ScheduleParams {
+  Schedule s;
+  const int32_t* offsets;
+  const int32_t* lens;
+  const int32_t* steps;
+  int n_seqs, n_tok, max_seq_len, H, pairs;
+  int64_t most;                               // units that there is room for
+  int* status;
+};
+
+__device__ __forceinline__ int scan_block(int v, int* red, int* total) {   // 1,024 threads
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int s = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(kFull, s, o);
+    if (lane >= o) s += u;
+  }
+  __syncthreads();
+  if (lane == 31) red[warp] = s;
+  __syncthreads();
+  int w = red[lane];
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(kFull, w, o);
+    if (lane >= o) w += u;
+  }
+  *total = __shfl_sync(kFull, w, 31);
+  const int ahead = __shfl_sync(kFull, w, max(warp - 1, 0));
+  return s - v + (warp ? ahead : 0);
+}
+
+// One CTA.  Token tiles of each sequence, the last first (it sees the most cells); the range
+// length that keeps the pairs of the device evenly loaded; the units in the tiles' order.
+__global__ void __launch_bounds__(1024, 1) diff_schedule_kernel(const ScheduleParams p) {
+  __shared__ int red[32];
+  __shared__ float cost_s[32];
+  __shared__ int top_s;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const Schedule& s = p.s;
+  if (tid == 0) top_s = 0;
+  for (int t = tid; t < p.n_tok; t += 1024) s.tok_tile[t] = -1;
+  // ---- token tiles of the sequences
+  const int per = (p.n_seqs + 1023) / 1024;
+  const int b0 = min(p.n_seqs, tid * per), b1 = min(p.n_seqs, b0 + per);
+  auto tokens_of = [&](int b, int& first) {
+    first = p.offsets[b];
+    const int end = p.offsets[b + 1];
+    return first < 0 || end < first || end > p.n_tok ? -1 : end - first;
+  };
+  int sum = 0, n_tiles;
+  for (int b = b0; b < b1; ++b) {
+    int first;
+    const int n = tokens_of(b, first);
+    if (n < 0) record_status(p.status, K8V4_ERANGE);
+    sum += (max(n, 0) + kTileTok - 1) / kTileTok;
+  }
+  int at = scan_block(sum, red, &n_tiles);
+  for (int b = b0; b < b1; ++b) {
+    int first;
+    at += (max(tokens_of(b, first), 0) + kTileTok - 1) / kTileTok;
+    s.tile_end[b] = at;
+  }
+  // offsets that do not follow one another can claim more tiles than there is room for
+  if (n_tiles > p.n_tok / kTileTok + min(p.n_seqs, p.n_tok)) {
+    if (tid == 0) record_status(p.status, K8V4_ERANGE);
+    n_tiles = 0;
+  }
+  __syncthreads();
+  // ---- each tile's tokens and cells
+  int cells = 0, top = 0;
+  for (int i = tid; i < n_tiles; i += 1024) {
+    int lo = 0, hi = p.n_seqs - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (s.tile_end[mid] > i) hi = mid;
+      else lo = mid + 1;
+    }
+    TokenTile t;
+    t.seq = lo;
+    int first;
+    const int n = tokens_of(lo, first);
+    const int j = s.tile_end[lo] - 1 - i;                      // the last tile first
+    t.tok0 = first + j * kTileTok;
+    t.n = min(kTileTok, n - j * kTileTok);
+    int len = p.lens[lo];
+    if (len < 0 || len > p.max_seq_len) {
+      record_status(p.status, K8V4_ERANGE);
+      len = len < 0 ? 0 : p.max_seq_len;
+    }
+    t.vis0 = len - n + j * kTileTok + 1;
+    int most = max(t.vis0 + t.n - 1, 0);
+    if (p.steps) {
+      most = 0;
+      for (int k = 0; k < t.n; ++k) {
+        const int v = p.steps[t.tok0 + k];
+        if (v < 0 || v > len) record_status(p.status, K8V4_ERANGE);
+        most = max(most, min(v, len));
+      }
+      t.vis0 = len;                                            // the bound of the steps
+    }
+    t.cell_tiles = (most + kTileN - 1) / kTileN;
+    t.splits = t.first = t.per_split = 0;
+    s.tiles[i] = t;
+    for (int k = 0; k < t.n; ++k) s.tok_tile[t.tok0 + k] = i;
+    cells += t.cell_tiles;
+    top = max(top, t.cell_tiles);
+  }
+  int total;
+  (void)scan_block(cells, red, &total);
+  top = __reduce_max_sync(kFull, top);
+  if (lane == 0) atomicMax(&top_s, top);
+  __syncthreads();
+  top = max(top_s, 1);
+  // ---- the range length: 32 candidates from what fills every pair kMostWaves times to no
+  // cut at all, each worked out by a warp: rounds x (range + a unit's fixed cost)
+  const float units_per = 2.0f * p.H;
+  const int least = max(1, min(top, static_cast<int>(ceilf(units_per * total / (static_cast<float>(kMostWaves) * p.pairs)))));
+  constexpr float kFixedTiles = 6.0f;
+  const int cand = max(least, min(top, static_cast<int>(ceilf(least * exp2f(log2f(static_cast<float>(top) / least) * warp / 31.0f)))));
+  int units = 0;
+  const bool many = n_tiles > 4096;                            // long lists are not cut
+  if (!many)
+    for (int i = lane; i < n_tiles; i += 32) units += (s.tiles[i].cell_tiles + cand - 1) / cand;
+  units = __reduce_add_sync(kFull, units);
+  if (lane == 0) cost_s[warp] = ceilf(units * units_per / p.pairs) * (cand + kFixedTiles);
+  __syncthreads();
+  float best = cost_s[lane];
+#pragma unroll
+  for (int o = 16; o >= 1; o >>= 1) best = fminf(best, __shfl_xor_sync(kFull, best, o));
+  const int pick = 31 - __clz(__ballot_sync(kFull, cost_s[lane] == best));
+  const int range = many ? top : max(least, min(top, static_cast<int>(ceilf(least * exp2f(log2f(static_cast<float>(top) / least) * pick / 31.0f)))));
+  // ---- the units
+  const int tiles_per = (n_tiles + 1023) / 1024;
+  const int i0 = min(n_tiles, tid * tiles_per), i1 = min(n_tiles, i0 + tiles_per);
+  int mine = 0, all;
+  for (int i = i0; i < i1; ++i) mine += (s.tiles[i].cell_tiles + range - 1) / range * 2 * p.H;
+  int u = scan_block(mine, red, &all);
+  for (int i = i0; i < i1; ++i) {
+    const int ct = s.tiles[i].cell_tiles, sp = (ct + range - 1) / range;
+    s.tiles[i].splits = sp;
+    s.tiles[i].first = u;
+    s.tiles[i].per_split = sp ? (ct + sp - 1) / sp : 0;
+    for (int k = 0; k < 2 * p.H; ++k)
+      for (int c = 0; c < sp; ++c, ++u)
+        if (u < p.most) s.units[u] = make_int2(i, c << 4 | k);
+  }
+  if (tid == 0) {
+    s.head[0] = static_cast<int>(min(static_cast<int64_t>(all), p.most));
+    s.head[1] = n_tiles;
+  }
+}
+
+// ---------------------------------------------------------------- pair PTX
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_barrier() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t map_to(uint32_t saddr, uint32_t rank) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(saddr), "r"(rank));
+  return a;
+}
+// (no wider release than the CTA's: what the tensor core reads is made visible by the proxy and
+// tcgen05 fences ahead of the arrival)
+__device__ __forceinline__ void arrive_cluster(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+__device__ __forceinline__ void arrive_local(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void tmem_alloc_pair(uint32_t slot, uint32_t ncols) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(slot), "r"(ncols) : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+}
+__device__ __forceinline__ void mma_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+      ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void mma_pair_ta(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+      ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+// completion of this thread's products so far -> the barrier at this offset of both CTAs
+__device__ __forceinline__ void commit_both(uint32_t bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+      "h"(static_cast<uint16_t>(3))
+      : "memory");
+}
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
+}
+// OR over the four warps that share 32 rows (warps w, w + 4, w + 8, w + 12; w < 4)
+__device__ __forceinline__ bool quad_any(int w, bool pred) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %2, 0;\n\t"
+      "barrier.cta.red.or.pred q, %1, 128, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(w + 3), "r"(pred ? 1u : 0u)
+      : "memory");
+  return r != 0;
+}
+// a barrier over the row warps that also ORs a predicate
+__device__ __forceinline__ bool rows_any(bool pred) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.or.pred q, 1, 512, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(pred ? 1u : 0u)
+      : "memory");
+  return r != 0;
+}
+__device__ __forceinline__ void rows_barrier() { asm volatile("barrier.cta.sync 2, 512;" ::: "memory"); }
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t v[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
+      ::"r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]),
+        "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, float v[8]) {
+  uint32_t r[8];
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr)
+               : "memory");
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
+}
+// two nibbles at bits k and k + 16 of t -> (n - 8) / 8 (exact) times d, rounded to fp16
+__device__ __forceinline__ uint32_t nib_times(uint32_t t, int k, __half2 d2) {
+  const uint32_t x = ((t >> k) & 0x000f000fu) | 0x64006400u;                                  // 1024 + n
+  const __half2 eighth = __halves2half2(__ushort_as_half(0x3000), __ushort_as_half(0x3000));   // 1/8
+  const __half2 m129 = __halves2half2(__ushort_as_half(0xd808), __ushort_as_half(0xd808));     // -129
+  const __half2 r = __hmul2(__hfma2(*reinterpret_cast<const __half2*>(&x), eighth, m129), d2);
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+// ---------------------------------------------------------------- the kernel
+struct PairParams {
+  CacheView C;
+  const void* q;            // [n_tok][HQ][256]
+  int q_f32;
+  const int32_t* pt;        // [n_seqs][max_pages]
+  int64_t max_pages;
+  const int32_t* steps;     // or null
+  Schedule s;
+  float sm_scale_log2;
+  int* status;
+  uint32_t wait_ns;
+  FastDiv page_div;
+  int stages, stage_bytes;  // raw tiles in flight
+};
+
+// grid: 2 CTAs per unit
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    diff_pair_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const PairParams p) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const uint32_t sb = smem_u32(smem);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const uint32_t rank = cluster_rank();
+  const CacheView& C = p.C;
+  const int HQ = C.H * kGqa;
+  const int row = tid & (kRows - 1), part = tid >> 7;      // (row warps) 32 cells of a tile and 64 dims of O per part
+  const uint32_t bars = sb + kBarOff;
+  volatile int* ctl = reinterpret_cast<volatile int*>(smem + kCtlOff);   // [0] tmem, [1] failed, [4..7] bad groups of 4 tiles, [8..10] valid groups
+  float* red = reinterpret_cast<float*>(smem + kRedOff);                 // [4][128]
+  float* fsc = red + 4 * kRows;                                          // [128]
+  float* ksbuf = reinterpret_cast<float*>(smem + kKsOff);
+
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int unit = blockIdx.x >> 1;
+  if (unit >= __ldcg(p.s.head)) return;                                  // both CTAs of the pair
+  const int2 what = __ldcg(p.s.units + unit);
+  const int map = what.y & 1, g = (what.y >> 1) & 7, split = what.y >> 4;
+  TokenTile tt;
+  {
+    const int4* src = reinterpret_cast<const int4*>(p.s.tiles + what.x);
+    const int4 a = __ldcg(src), b = __ldcg(src + 1);
+    tt = TokenTile{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  }
+  const int tile0 = split * tt.per_split;
+  const int n_tiles = min(tt.per_split, tt.cell_tiles - tile0);          // >= 1
+  const int tok_first = tt.tok0 + 16 * static_cast<int>(rank);           // this CTA's tokens
+  const int tok_n = max(0, min(16, tt.n - 16 * static_cast<int>(rank)));
+  const int32_t* pt = p.pt + static_cast<int64_t>(tt.seq) * p.max_pages;
+  // cells that any row of the pair sees (those behind are neither looked up nor read)
+  const int limit = p.steps ? min(tt.cell_tiles * kTileN, tt.vis0) : tt.vis0 + tt.n - 1;
+
+  if (warp == kLoadWarp) {
+    int count = 0;
+    if (lane < kBarPFull) count = 8;                       // K, V tiles: 4 conversion warps of both CTAs
+    else if (lane < kBarSFull) count = 2 * kRowWarps;      // P: the row warps of both CTAs
+    else if (lane < kBarKsFull) count = 1;                 // S done, O done: one commit
+    else if (lane < kBarDrain) count = 4;                  // K scales: the CTA's conversion warps
+    else if (lane == kBarDrain) count = 1;                 // everything done: one commit
+    else if (lane >= kBarRawFull && lane < kBarRawEmpty) count = 1;   // raw tile: the loader, and the bytes of its copies
+    else if (lane >= kBarRawEmpty && lane < kBarRawEmpty + 4) count = 4;
+    if (count) mbar_init(bars + 8 * lane, count);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    if (lane < 15) ctl[1 + lane] = 0;
+    if (lane == 0) {
+      asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_k)) : "memory");
+      asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_v)) : "memory");
+    }
+    __syncwarp();
+  }
+  if (warp == kIssueWarp) tmem_alloc_pair(sb + kCtlOff, kTmemCols);
+
+  // ---- the load warp's copies of tile i into a stage: page ids of four tiles, eight
+  // 16-cell groups each, are held one per lane
+  int page_mine = -1;
+  auto load_tile = [&](int i, int stage, bool leader) {
+    const int H = C.H;
+    if ((i & 3) == 0) {
+      const int c = (tile0 + i + (lane >> 3)) * kTileN + 16 * (lane & 7);
+      const int64_t pidx = p.page_div.div(static_cast<uint32_t>(c));
+      page_mine = INT32_MIN;                               // behind the limit, or another range's
+      if (i + (lane >> 3) < n_tiles && c < limit) {
+        const int page = pidx < p.max_pages ? __ldcg(pt + pidx) : -1;
+        page_mine = page >= 0 && page < C.n_pages ? page : -1;
+      }
+    }
+    const uint32_t dst = sb + kRawOff + stage * p.stage_bytes, bar = bars + 8 * (kBarRawFull + stage);
+    const int my_group_page = __shfl_sync(kFull, page_mine, 8 * (i & 3) + (lane & 7));
+    const unsigned good = __ballot_sync(kFull, my_group_page >= 0) & 255u;
+    const unsigned bad = __ballot_sync(kFull, my_group_page == -1) & 255u;
+    const unsigned kgood = (good >> (4 * rank)) & 15u;
+    if (leader) {
+      if (bad) record_status(p.status, K8V4_ERANGE);
+      ctl[8 + stage] = static_cast<int>(good | (bad << 8));
+      mbar_expect_tx(bar, __popc(good) * (2048u + 384u * H) + __popc(kgood) * 2048u);
+    }
+#pragma unroll 1
+    for (int q = 0; q < 8; ++q) {
+      const int page = __shfl_sync(kFull, my_group_page, q);
+      if (!leader || page < 0) continue;
+      const int cell = (tile0 + i) * kTileN + 16 * q;
+      const int slot = cell - static_cast<int>(p.page_div.div(static_cast<uint32_t>(cell))) * C.P;
+      const int kq = q - 4 * static_cast<int>(rank);
+      if (kq >= 0 && kq < 4) tma_load_4d(dst + kq * 2048, &tm_k, 128 * map, g, slot, page, bar);
+      tma_load_4d(dst + kRawV + q * 2048, &tm_v, 0, g, slot, page, bar);
+      const uint8_t* pg = C.pages + static_cast<int64_t>(page) * C.page_bytes;
+      bulk_load(dst + kRawKs + q * 128 * H, pg + C.ks_off() + static_cast<int64_t>(slot) * 8 * H, 128 * H, bar);
+      bulk_load(dst + kRawKs + 1024 * H + q * 256 * H, pg + C.vs_off() + static_cast<int64_t>(slot) * 16 * H, 256 * H, bar);
+    }
+    __syncwarp();
+  };
+  if (warp == kLoadWarp) load_tile(0, 0, elect_one());     // while the others set Q up
+
+  // ---- visibility of this thread's row
+  int my_vis = 0;
+  if (warp < kRowWarps && row / kGqa < tok_n) {
+    const int t = tok_first + row / kGqa;
+    my_vis = p.steps ? max(0, min(__ldcg(p.steps + t), tt.vis0)) : max(0, tt.vis0 + t - tt.tok0);
+  }
+  // ---- Q rows of this map -> fp16 with a power of two per row, swizzled K-major: half a warp
+  // takes a row at a time (8 elements a lane)
+  if (warp < kLoadWarp) {
+    constexpr int kPer = (kRows + 2 * kLoadWarp - 1) / (2 * kLoadWarp);
+    const int sub = lane >> 4, l16 = lane & 15;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const int r = 2 * (warp + kLoadWarp * j) + sub;
+      float x[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+      if (r < kRows && r / kGqa < tok_n) {
+        const int64_t e0 = (static_cast<int64_t>(tok_first + r / kGqa) * HQ + g * kGqa + r % kGqa) * kD + 128 * map + 8 * l16;
+        if (p.q_f32) {
+          const float4* src = reinterpret_cast<const float4*>(static_cast<const float*>(p.q) + e0);
+          const float4 a = __ldcg(src), b = __ldcg(src + 1);
+          x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+          x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+        } else {
+          const uint4 a = __ldcg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + e0));
+          const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            x[2 * u] = __uint_as_float(w[u] << 16);
+            x[2 * u + 1] = __uint_as_float(w[u] & 0xffff0000u);
+          }
+        }
+      }
+      float amax = 0.0f;
+#pragma unroll
+      for (int u = 0; u < 8; ++u) amax = fmaxf(amax, fabsf(x[u]));
+#pragma unroll
+      for (int o = 8; o >= 1; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, o));
+      if (r >= kRows) continue;
+      const int ex = amax > 0.0f ? static_cast<int>((__float_as_uint(amax) >> 23) & 0xffu) - 127 : 0;
+      const int sh = max(-100, min(100, 14 - ex));
+      const float up = ldexpf(1.0f, sh);
+      // above 0 also where the product underflows: a masked score is -inf times it
+      if (l16 == 0) fsc[r] = fmaxf(p.sm_scale_log2 * ldexpf(1.0f, -sh), 1.2e-38f);
+      uint32_t hv[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const __half2 h2 = __floats2half2_rn(__fmul_rn(x[2 * u], up), __fmul_rn(x[2 * u + 1], up));
+        hv[u] = *reinterpret_cast<const uint32_t*>(&h2);
+      }
+      sts128(sb + kQOff + (l16 >> 3) * 16384 + swz(r, l16 & 7), hv[0], hv[1], hv[2], hv[3]);
+    }
+  }
+  asm volatile("fence.proxy.async;" ::: "memory");
+  tc_fence_before();
+  __syncthreads();
+  cluster_barrier();          // barriers, tensor memory and Q of both CTAs are ready
+  tc_fence_after();
+  const uint32_t tmem = static_cast<uint32_t>(ctl[0]);
+  float* const block = p.s.rows + (static_cast<int64_t>(unit) * 2 + rank) * kRows * kDiffRow;   // this CTA's partial rows
+
+  if (warp < kRowWarps) {
+    // ================================================================ rows
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRowRegs));
+    const uint32_t lane_base = static_cast<uint32_t>(32 * (warp & 3)) << 16;
+    const float my_f = fsc[row];
+    const uint32_t p_full0 = map_to(bars + 8 * kBarPFull, 0);
+    const uint32_t o_tile = tmem + lane_base + kOCol + 64 * part;
+    // the running O of this thread's 64 dims: float4 number c at acc[512 c] (the block is 128 x 260 floats)
+    float4* const acc = reinterpret_cast<float4*>(block) + tid;
+    float m_run = -INFINITY, l_part = 0.0f, acc_scale = 1.0f;          // acc counts times acc_scale
+    bool failed = false, have_acc = false;
+    for (int i = 0; i < n_tiles; ++i) {
+      const int buf = i & 1;
+      const uint32_t parity = (i >> 1) & 1;
+      if (!mbar_wait(bars + 8 * (kBarSFull + buf), parity, p.wait_ns) ||
+          !mbar_wait(bars + 8 * (kBarKsFull + (i & 3)), (i >> 2) & 1, p.wait_ns)) {
+        failed = true;
+        ctl[1] = 1;
+      }
+      tc_fence_after();
+      // scores, unscaled (my_f > 0, so the maximum commutes with it); cell c of this part
+      const uint32_t sbase = tmem + lane_base + kSBuf * buf + 32 * part;
+      const float* ks = ksbuf + 128 * (i & 3) + 32 * part;
+      float2 sc[16];
+      {
+        float a[32];
+        tmem_ld32(sbase, a);
+#pragma unroll
+        for (int c = 0; c < 32; c += 4) {
+          const float4 k4 = *reinterpret_cast<const float4*>(ks + c);
+          sc[c / 2] = __fmul2_rn(make_float2(k4.x, k4.y), make_float2(a[c], a[c + 1]));
+          sc[c / 2 + 1] = __fmul2_rn(make_float2(k4.z, k4.w), make_float2(a[c + 2], a[c + 3]));
+        }
+      }
+      const int vis = my_vis - (tile0 + i) * kTileN - 32 * part;       // cells [0, vis) of this part
+      const int bad = (ctl[4 + (i & 3)] >> (2 * part)) & 3;            // its groups of 16 cells on a page out of range
+      if (vis < 32 || bad) {
+#pragma unroll
+        for (int c = 0; c < 32; c += 2) {
+          const bool off = (bad >> (c >> 4)) & 1;
+          if (c >= vis || off) sc[c / 2].x = -INFINITY;
+          if (c + 1 >= vis || off) sc[c / 2].y = -INFINITY;
+        }
+      }
+      float mx0 = -INFINITY, mx1 = -INFINITY;
+#pragma unroll
+      for (int c = 0; c < 16; c += 2) {
+        mx0 = fmaxf(mx0, fmaxf(sc[c].x, sc[c].y));
+        mx1 = fmaxf(mx1, fmaxf(sc[c + 1].x, sc[c + 1].y));
+      }
+      const float top = fmaxf(mx0, mx1) * my_f;
+      // the four threads of a row agree on its reference: a vote of their four warps
+      const bool any = quad_any(warp & 3, failed || top > m_run + kSlack);
+      float alpha = 1.0f;
+      if (any) {
+        red[part * kRows + row] = top;
+        // the four leave together: the failure word is read once, ahead of a vote
+        if (quad_any(warp & 3, failed || ctl[1] != 0)) { failed = true; break; }
+        const float mt = fmaxf(fmaxf(red[row], red[kRows + row]), fmaxf(red[2 * kRows + row], red[3 * kRows + row]));
+        if (mt > m_run + kSlack) {
+          alpha = exp2f(m_run - mt);                                   // 0 on the first visible tile
+          m_run = mt;
+          l_part *= alpha;
+        }
+      }
+      const float mu = (m_run == -INFINITY ? 0.0f : m_run) - 7.0f;
+      const float2 f2 = make_float2(my_f, my_f), mu2 = make_float2(-mu, -mu);
+      float2 psum = make_float2(0.0f, 0.0f);
+      {
+        uint32_t ph[16];
+#pragma unroll
+        for (int c = 0; c < 16; ++c) {
+          const float2 e = __ffma2_rn(sc[c], f2, mu2);
+          const float2 q = make_float2(ex2_ftz(e.x), ex2_ftz(e.y));
+          const __half2 h = __floats2half2_rn(q.x, q.y);
+          psum = __fadd2_rn(psum, q);
+          ph[c] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+        tmem_st16(sbase, ph);
+      }
+      l_part += psum.x + psum.y;
+      tmem_wait_st();
+      // O of the tiles so far: into acc at every kChain-th tile (both CTAs), rescaled
+      // in place where a reference moved in between
+      const bool folds = i > 0 && i % kChain == 0;
+      if (folds || (i > 0 && any && __any_sync(kFull, alpha != 1.0f))) {
+        if (!mbar_wait(bars + 8 * (kBarODone + (buf ^ 1)), ((i - 1) >> 1) & 1, p.wait_ns)) {
+          failed = true;
+          ctl[1] = 1;
+        }
+        tc_fence_after();
+        if (folds) {                                                   // acc = (acc + O) * alpha
+          const float a = alpha * acc_scale;
+#pragma unroll
+          for (int h = 0; h < 4; ++h) {
+            float4 old[4];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) old[c] = have_acc ? acc[512 * (4 * h + c)] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            float o[16];
+            tmem_ld16(o_tile + 16 * h, o);
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+              acc[512 * (4 * h + c)] = make_float4(old[c].x * a + o[4 * c] * alpha, old[c].y * a + o[4 * c + 1] * alpha,
+                                                   old[c].z * a + o[4 * c + 2] * alpha, old[c].w * a + o[4 * c + 3] * alpha);
+          }
+          have_acc = true;
+          acc_scale = 1.0f;
+        } else {                                                       // O *= alpha
+#pragma unroll
+          for (int h = 0; h < 8; ++h) {
+            float o[8];
+            tmem_ld8(o_tile + 8 * h, o);
+#pragma unroll
+            for (int c = 0; c < 8; ++c) o[c] *= alpha;
+            tmem_st8(o_tile + 8 * h, o);
+          }
+          acc_scale *= alpha;
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) arrive_cluster(p_full0 + 8 * buf);
+    }
+    // ---- the last O, then o / m / l of the rows
+    float o[64];
+    if (!failed) {
+      if (mbar_wait(bars + 8 * (kBarODone + ((n_tiles - 1) & 1)), ((n_tiles - 1) >> 1) & 1, p.wait_ns)) {
+        tc_fence_after();
+#pragma unroll
+        for (int h = 0; h < 2; ++h) tmem_ld32(o_tile + 32 * h, o + 32 * h);
+        if (have_acc) {
+#pragma unroll
+          for (int c = 0; c < 16; ++c) {
+            const float4 old = acc[512 * c];
+            o[4 * c] += old.x * acc_scale;
+            o[4 * c + 1] += old.y * acc_scale;
+            o[4 * c + 2] += old.z * acc_scale;
+            o[4 * c + 3] += old.w * acc_scale;
+          }
+        }
+        tc_fence_before();
+      } else {
+        failed = true;
+        ctl[1] = 1;
+      }
+    }
+    // PV of the last tile is done in both CTAs (one commit covers the pair), and with it every
+    // read of this CTA's operand tiles; every thread has read its running sum
+    red[part * kRows + row] = l_part;
+    const bool stop = rows_any(failed);
+    if (!stop) {
+      const float l = (red[row] + red[kRows + row]) + (red[2 * kRows + row] + red[3 * kRows + row]);
+      float* rowbuf = reinterpret_cast<float*>(smem + kQOff);          // [128][256] fp32, rotated by 4 * row
+#pragma unroll
+      for (int i = 0; i < 64; i += 4)
+        *reinterpret_cast<float4*>(rowbuf + row * 256 + ((64 * part + i + 4 * row) & 255)) =
+            make_float4(8.0f * o[i], 8.0f * o[i + 1], 8.0f * o[i + 2], 8.0f * o[i + 3]);
+      if (part == 0 && row / kGqa < tok_n) {
+        block[row * kDiffRow + 256] = m_run - 7.0f;                    // o and l are relative to 2^(m - 7)
+        block[row * kDiffRow + 257] = l;
+      }
+      rows_barrier();
+      for (int r = warp; r < kGqa * tok_n; r += kRowWarps) {
+        float4* dst = reinterpret_cast<float4*>(block + r * kDiffRow);
+        dst[lane] = *reinterpret_cast<const float4*>(rowbuf + r * 256 + ((4 * lane + 4 * r) & 255));
+        dst[32 + lane] = *reinterpret_cast<const float4*>(rowbuf + r * 256 + ((128 + 4 * lane + 4 * r) & 255));
+      }
+    } else if (part == 0 && row / kGqa < tok_n) {                      // nothing to join of a unit that failed
+      block[row * kDiffRow + 256] = -INFINITY;
+      block[row * kDiffRow + 257] = 0.0f;
+    }
+  } else if (warp < kIssueWarp) {
+    // ================================================================ conversion
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kConvRegs));
+    const int t = tid - 32 * kConvWarp0;                   // 0..127
+    // K: cell 64 rank + (t & 63), dims [64 (t >> 6), +64); V: cell t, blocks 4 rank .. 4 rank + 3.
+    // The copies put 16-byte unit u of a row at u ^ (row & 7) (128-byte swizzle).
+    const int kcell = t & 63, kchunk = t >> 6;
+    const uint32_t k_full0 = map_to(bars + 8 * kBarKFull, 0), v_full0 = map_to(bars + 8 * kBarVFull, 0);
+    const uint32_t kraw = (kcell >> 4) * 2048 + (kcell & 15) * 128;
+    const uint32_t vraw = kRawV + (t >> 4) * 2048 + (t & 15) * 128;
+    const uint32_t ksraw = kRawKs + (t >> 4) * 128 * C.H + ((t & 15) * C.H + g) * 8 + 4 * map;
+    const uint32_t vsraw = kRawKs + 1024 * C.H + (t >> 4) * 256 * C.H + ((t & 15) * C.H + g) * 16 + 8 * rank;
+    int stage = 0;
+    uint32_t raw_phase = 0;
+    for (int i = 0; i < n_tiles; ++i) {
+      const int buf = i & 1;
+      const uint32_t last = ((i - 2) >> 1) & 1;            // phase of tile i - 2 on the buffers' barriers
+      const uint32_t raw = sb + kRawOff + stage * p.stage_bytes;
+      if (!mbar_wait(bars + 8 * (kBarRawFull + stage), raw_phase, p.wait_ns)) { ctl[1] = 1; break; }
+      const int valid = ctl[8 + stage];                    // the tile's 16-cell groups that were copied; bits 8..15: on a bad page
+      // ---- K(i) and its scales, once QK(i - 2) has read the buffer
+      if (i >= 2 && !mbar_wait(bars + 8 * (kBarSFull + buf), last, p.wait_ns)) { ctl[1] = 1; break; }
+      {
+        const uint32_t dst = sb + kKOff + buf * kKBuf + kchunk * 8192;
+        uint4 kw[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) kw[u] = lds128(raw + kraw + (((4 * kchunk + u) ^ (kcell & 7)) << 4));
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const uint4 w = kw[u];
+          uint32_t h[8];
+          i8x4_to_f16(w.x, h[0], h[1]);
+          i8x4_to_f16(w.y, h[2], h[3]);
+          i8x4_to_f16(w.z, h[4], h[5]);
+          i8x4_to_f16(w.w, h[6], h[7]);
+          sts128(dst + swz(kcell, 2 * u), h[0], h[1], h[2], h[3]);
+          sts128(dst + swz(kcell, 2 * u + 1), h[4], h[5], h[6], h[7]);
+        }
+        float ksc;
+        asm volatile("ld.shared.f32 %0, [%1];" : "=f"(ksc) : "r"(raw + ksraw));
+        ksbuf[128 * (i & 3) + t] = ksc;
+        if (t == 0) ctl[4 + (i & 3)] = valid >> 8;
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          arrive_local(bars + 8 * (kBarKsFull + (i & 3)));
+          arrive_cluster(k_full0 + 8 * buf);
+        }
+      }
+      // ---- V(i), once PV(i - 2) has read the buffer
+      if (i >= 2 && !mbar_wait(bars + 8 * (kBarODone + buf), last, p.wait_ns)) { ctl[1] = 1; break; }
+      {
+        const uint32_t dst = sb + kVOff + buf * kVBuf;
+        // a cell that was not copied, or that nobody sees, counts with V = 0 (its P is 0, its bytes are anything)
+        uint32_t vd[2];
+        asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(vd[0]), "=r"(vd[1]) : "r"(raw + vsraw));
+        uint4 vw[4];
+#pragma unroll
+        for (int b = 0; b < 4; ++b) vw[b] = lds128(raw + vraw + (((4 * rank + b) ^ (t & 7)) << 4));
+        if (!((valid >> (t >> 4)) & 1) || (tile0 + i) * kTileN + t >= limit) vd[0] = vd[1] = 0;
+        __syncwarp();
+        if (lane == 0) arrive_local(bars + 8 * (kBarRawEmpty + stage));
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          const __half dh = __ushort_as_half(static_cast<unsigned short>(vd[b >> 1] >> (16 * (b & 1))));
+          const __half2 d2 = __halves2half2(dh, dh);
+          const uint32_t ws4[4] = {vw[b].x, vw[b].y, vw[b].z, vw[b].w};
+          const uint32_t at = dst + (b >> 1) * kVAtom;     // 64 dims an atom
+#pragma unroll
+          for (int hn = 0; hn < 2; ++hn) {                 // low nibbles: dims 0..15 of the block, high: 16..31
+            uint32_t v[8];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              v[2 * q] = nib_times(prmt(ws4[q], 0u, 0x5140u), 4 * hn, d2);
+              v[2 * q + 1] = nib_times(prmt(ws4[q], 0u, 0x5342u), 4 * hn, d2);
+            }
+            const int u0 = 4 * (b & 1) + 2 * hn;
+            sts128(at + swz(t, u0), v[0], v[1], v[2], v[3]);
+            sts128(at + swz(t, u0 + 1), v[4], v[5], v[6], v[7]);
+          }
+        }
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) arrive_cluster(v_full0 + 8 * buf);
+      }
+      if (++stage == p.stages) {
+        stage = 0;
+        raw_phase ^= 1;
+      }
+    }
+  } else {
+    // ================================================================ issue
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
+    // The whole warp runs the loop and one elected lane executes the products: with the
+    // control flow uniform the descriptors live in uniform registers
+    if (__shfl_sync(kFull, warp, 0) == kIssueWarp && rank == 0) {
+      constexpr uint32_t idS = idesc_f16(256, 128, false, false);
+      constexpr uint32_t idO = idesc_f16(256, 256, false, true);
+      const uint32_t tm = __shfl_sync(kFull, tmem, 0);
+      const uint64_t dq0 = smem_desc(sb + kQOff, 16, 1024);
+      const uint64_t dk0 = smem_desc(sb + kKOff, 16, 1024);
+      const uint64_t dv0 = smem_desc(sb + kVOff, kVAtom, 1024);
+      const bool leader = elect_one();
+      auto ready = [&](int bar, uint32_t parity) -> bool {
+        return __all_sync(kFull, mbar_wait(bars + 8 * bar, parity, p.wait_ns)) != 0;
+      };
+      auto qk = [&](int buf) {                             // S[buf] = Q K^T
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk) {
+          const uint32_t off = (kk & 3) * 32;
+          mma_pair(tm + kSBuf * buf, dq0 + (((kk >> 2) * 16384 + off) >> 4), dk0 + ((buf * kKBuf + (kk >> 2) * 8192 + off) >> 4), idS,
+                   kk ? 1u : 0u);
+        }
+        commit_both(bars + 8 * (kBarSFull + buf));
+      };
+      bool ok = true;
+      for (int i = 0; i < min(2, n_tiles); ++i) {
+        if (!ready(kBarKFull + i, 0)) { ok = false; break; }
+        tc_fence_after();
+        if (leader) qk(i);
+      }
+      for (int i = 0; ok && i < n_tiles; ++i) {
+        const int buf = i & 1;
+        const uint32_t parity = (i >> 1) & 1;
+        if (!ready(kBarVFull + buf, parity) || !ready(kBarPFull + buf, parity)) { ok = false; break; }
+        tc_fence_after();
+        if (leader) {
+          const uint32_t more = i % kChain != 0 ? 1u : 0u;  // O of this chain so far is kept
+          const uint32_t pa = tm + kSBuf * buf;
+          const uint64_t v0 = dv0 + ((buf * kVBuf) >> 4);
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)                   // 16 cells = 8 columns of fp16 pairs, two steps to a part's 32 columns
+            mma_pair_ta(tm + kOCol, pa + 32 * (kk >> 1) + 8 * (kk & 1), v0 + ((kk * 2048) >> 4), idO, kk ? 1u : more);
+          commit_both(bars + 8 * (kBarODone + buf));
+        }
+        if (i + 2 < n_tiles) {
+          // QK(i + 2) overwrites P(i)
+          if (!ready(kBarKFull + buf, parity ^ 1) || !ready(kBarODone + buf, parity)) { ok = false; break; }
+          tc_fence_after();
+          if (leader) qk(buf);
+        }
+      }
+      if (!ok) ctl[1] = 1;
+      // all of this warp's products, waited for below (after a failure too)
+      if (leader) commit_both(bars + 8 * kBarDrain);
+    } else if (__shfl_sync(kFull, warp, 0) == kLoadWarp) {
+      // ============================================================== copies
+      const bool leader = elect_one();
+      int stage = p.stages > 1 ? 1 : 0, i = 1;
+      uint32_t phase = p.stages > 1 ? 1 : 0;               // of the stage's last use, from its second on
+      for (; i < n_tiles; ++i) {
+        if (i >= p.stages && !__all_sync(kFull, mbar_wait(bars + 8 * (kBarRawEmpty + stage), phase, p.wait_ns))) { ctl[1] = 1; break; }
+        load_tile(i, stage, leader);
+        if (++stage == p.stages) {
+          stage = 0;
+          phase ^= 1;
+        }
+      }
+      // no copy is in flight past here (after a failure too): the last tiles' stages
+      for (int j = max(0, i - p.stages); j < i; ++j)
+        (void)mbar_wait(bars + 8 * (kBarRawFull + j % p.stages), (j / p.stages) & 1, kWaitDefaultNs);
+    }
+    __syncwarp();
+  }
+  tc_fence_before();
+  __syncthreads();
+  // The commits arrive at the barriers of both CTAs, and each CTA waits for its own copies of the
+  // last ones: shared memory that an arrival is still on its way to must not be given to the
+  // next CTA.  (The row warps have waited for every S and the last O.)
+  if (warp == kIssueWarp) {
+    if (n_tiles > 1 && !ctl[1])
+      (void)mbar_wait(bars + 8 * (kBarODone + (n_tiles & 1)), ((n_tiles - 2) >> 1) & 1, kWaitDefaultNs);
+    (void)mbar_wait(bars + 8 * kBarDrain, 0, kWaitDefaultNs);
+    __syncwarp();
+  }
+  if (tid == 0 && ctl[1]) record_status(p.status, K8V4_ECUDA);
+  cluster_barrier();          // no product, commit or arrival of the pair is in flight
+  if (warp == kIssueWarp) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, kTmemCols);
+  }
+}
+
+// ---------------------------------------------------------------- host side
+// Set-up of the pair kernel on the current device: its shared memory, its registers at launch (the
+// split hands out that many) and the CTA pairs that the device runs at a time.  Kept once it has
+// worked; a failure is not, and the next call tries again.
+std::mutex g_pairs_mu;
+int g_pairs[64];
+int device_pairs() {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) {
+    cudaGetLastError();
+    return 0;
+  }
+  std::lock_guard<std::mutex> lock(g_pairs_mu);
+  if (g_pairs[dev] > 0) return g_pairs[dev];
+  cudaFuncAttributes fa;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmemMax;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int pairs = 0;
+  if (cudaFuncGetAttributes(&fa, diff_pair_kernel) != cudaSuccess ||
+      fa.numRegs * 6 < 4 * kRowRegs + kConvRegs + kIssueRegs ||
+      cudaFuncSetAttribute(diff_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax) != cudaSuccess ||
+      cudaOccupancyMaxActiveClusters(&pairs, diff_pair_kernel, &cfg) != cudaSuccess || pairs < 1) {
+    cudaGetLastError();                   // clear the error state that the failed call left
+    return 0;
+  }
+  return g_pairs[dev] = pairs;
+}
+// the pairs that a workspace and its schedule are sized for: of the device's SMs, the same whether or
+// not the set-up has worked yet
+int planned_pairs(int num_sms) { return std::max(1, std::min(num_sms / 2, kDiffMostPairs)); }
+
+}  // namespace
+
+size_t diff_ws_bytes(const CacheView& C, int n_seqs, int n_tok, int max_seq_len, int num_sms) {
+  return place(nullptr, nullptr, n_seqs, n_tok, max_seq_len, C.H, planned_pairs(num_sms));
+}
+
+int launch_diff(const Launch& L, const CacheView& C, const void* q, int q_dtype, const int32_t* offsets, int n_tok,
+                const int32_t* pt, int64_t max_pages, const int32_t* lens, const int32_t* steps, int n_seqs,
+                int max_seq_len, float sm_scale, const k8v4_diff& diff, void* out, void* ws) {
+  if (device_pairs() < 1) return K8V4_ECUDA;
+  const int pairs = planned_pairs(L.num_sms);
+  ScheduleParams sp;
+  place(&sp.s, static_cast<uint8_t*>(ws), n_seqs, n_tok, max_seq_len, C.H, pairs);
+  sp.offsets = offsets;
+  sp.lens = lens;
+  sp.steps = steps;
+  sp.n_seqs = n_seqs;
+  sp.n_tok = n_tok;
+  sp.max_seq_len = max_seq_len;
+  sp.H = C.H;
+  sp.pairs = pairs;
+  sp.most = most_units(n_seqs, n_tok, max_seq_len, C.H, pairs);
+  sp.status = L.status;
+  int rc = launch_behind(L, diff_schedule_kernel, dim3(1), dim3(1024), sp);
+  if (rc) return rc;
+  PairParams p;
+  p.C = C;
+  p.q = q;
+  p.q_f32 = q_dtype == K8V4_F32;
+  p.pt = pt;
+  p.max_pages = max_pages;
+  p.steps = steps;
+  p.s = sp.s;
+  p.sm_scale_log2 = sm_scale * 1.4426950408889634f;
+  p.status = L.status;
+  p.wait_ns = wait_limit_ns() ? wait_limit_ns() : kWaitDefaultNs;
+  p.page_div = FastDiv(static_cast<uint32_t>(C.P));
+  p.stages = raw_stages(C.H);
+  p.stage_bytes = raw_bytes(C.H);
+  CUtensorMap mk, mv;
+  if (!tensor_maps_of(C, &mk, &mv)) return K8V4_ECUDA;
+  if (2 * sp.most > INT32_MAX) return K8V4_EINVAL;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(2 * sp.most));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kRawOff + p.stages * p.stage_bytes;
+  cfg.stream = L.stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, diff_pair_kernel, mk, mv, p) != cudaSuccess) return K8V4_ECUDA;
+  if (cudaGetLastError() != cudaSuccess) return K8V4_ECUDA;
+  DiffRagged r;
+  r.tok_tile = sp.s.tok_tile;
+  r.tiles = reinterpret_cast<const int32_t*>(sp.s.tiles);
+  // few token tiles: their rows have tens of ranges each, and a row gets four warps
+  const bool wide = most_tiles(n_seqs, n_tok) * 2 * C.H < pairs;
+  return launch_diff_combine_ragged(L, sp.s.rows, r, n_tok, C.H, wide, diff, out);
+}
+
+}  // namespace k8v4
