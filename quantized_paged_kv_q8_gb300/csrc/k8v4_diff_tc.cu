@@ -10,7 +10,7 @@
 // cta_group::2, M = 256, 128 rows per SM) keeps its O in tensor memory and sweeps the range
 // in tiles of 128 cells
 //   S  = Q_m K_m^T        128 lanes, N = 128
-//   P  = 2^(s - ref) 2^7  online softmax in the log2 domain, fp16
+//   P  = 2^(s - ref) 2^4  online softmax in the log2 domain, fp16
 //   O += P V              N = 256, V = RN((n - 8) / 8 d) in fp16
 // and writes its partial rows (o, m, l); the combine joins ranges and maps.  The two maps'
 // units read and convert the same V; a pair that kept both maps of 16 tokens instead would
@@ -23,26 +23,36 @@
 // latter.
 //
 // Roles, handing over through mbarriers:
-//      warps 0-15   rows: four threads per row (32 cells, and 64 of O's dims, each)
-//      warps 16-19  conversion: raw tile -> registers -> operand tiles
-//      warp 20      (leader CTA) issues every product of the pair
-//      warp 21      copies the raw tiles (TMA)
-// The reference maximum of a row moves only when a tile exceeds it by 2^8, and then its O
-// is rescaled in tensor memory.  Every kChain tiles O is added to a running sum in
-// global memory (the unit's own partial rows serve as its place), because the tensor core's
-// accumulation is not rounded to nearest: measured 2.9e-5 after 2,048 cells in three products
-// each, so about 4e-5 after kChain tiles here.
+//      warps 0-7    rows: a thread per row; warps 0-3 take the even tiles, 4-7 the odd ones, so
+//                   that one group's exponentials run beside the other's maxima and waits
+//      warps 8-15   conversion: raw tile -> registers -> operand tiles, K (8-11) and V (12-15)
+//      warp 16      (leader CTA) issues every product of the pair
+//      warps 17-19  copy the raw tiles (TMA, boxes of 64, 32 or 16 cells as the page size allows; a
+//                   copy takes its warp about 100 clocks to issue, and 16-cell boxes need 28 a tile)
+// The products alternate S(i + 2), O(i): a row's thread takes its 128 scores into registers at
+// once and frees S, P has two buffers of its own, so neither product waits for the other's
+// reader and the tensor pipe is never handed an empty queue by the order of things.
+// The reference maximum of a row moves only when a tile exceeds it by 2^11, and then its O
+// is rescaled in tensor memory, which holds the pair up for about 1,500 clocks (at 2^8 it took a
+// sixth of the time); the two groups hand the reference on from tile to tile.  P is kept
+// 2^4 above it: fp16 drops what is 2^-29 of the reference and less.
+// Every kChain tiles O is added to a running sum in global memory (the unit's own partial
+// rows serve as its place), because the tensor core's accumulation is not rounded to
+// nearest: measured 2.9e-5 after 2,048 cells in three products each, so about 4e-5 after
+// kChain tiles here.
 //
 // The units come from a schedule that one CTA works out on the device from the lengths:
 // token tiles, heaviest first within a sequence, cut into ranges so that the pairs of the
 // device are evenly loaded.
 //
-// Tensor memory (512 columns): S buffers [0,128), [128,256) (a thread's P overlays its
-// own columns), O [256,512).
+// Tensor memory (512 columns): S [0,128), P [128,192) and [192,256), O [256,512).
 //
 // Every mbarrier wait is bounded: on timeout the warp raises the CTA's failure word and
-// leaves its loop (the row warps together, at their next vote); the kernel records an
-// error, waits for its own products (bounded), frees its tensor memory and returns.
+// leaves its loop; the kernel records an error, waits for its own products (bounded), frees
+// its tensor memory and returns.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
 #include <algorithm>
 #include <mutex>
 
@@ -56,15 +66,19 @@ namespace {
 constexpr unsigned kFull = 0xffffffffu;
 constexpr int kRows = 128;                    // query rows per CTA (256 per pair)
 constexpr int kTileN = 128;                   // cells per tile
-constexpr int kRowWarps = 16, kRowThreads = 32 * kRowWarps;
-constexpr int kThreads = kRowThreads + 256;
-constexpr int kConvWarp0 = kRowWarps, kIssueWarp = kConvWarp0 + 4, kLoadWarp = kIssueWarp + 1;
-static_assert(kConvWarp0 % 4 == 0 && kIssueWarp % 4 == 0 && kLoadWarp < kIssueWarp + 4 && kThreads == 32 * (kIssueWarp + 4), "roles");
+constexpr int kRowWarps = 8;
+constexpr int kConvWarp0 = kRowWarps, kVConvWarp0 = kConvWarp0 + 4, kIssueWarp = kConvWarp0 + 8, kLoadWarp0 = kIssueWarp + 1;
+constexpr int kLoadWarps = 3, kThreads = 32 * (kLoadWarp0 + kLoadWarps);
+// the register split waits for whole warpgroups: roles begin at multiples of four warps
+static_assert(kConvWarp0 % 4 == 0 && kIssueWarp % 4 == 0 && kThreads == 32 * (kIssueWarp + 4), "roles");
 constexpr int kChain = 64;                    // tiles accumulated in tensor memory (8,192 cells)
-constexpr float kSlack = 8.0f;                // log2 headroom of P above its row's reference maximum
+constexpr float kSlack = 11.0f, kLift = 4.0f; // log2 headroom of P above its row's reference maximum, and what P is lifted by
+static_assert(kSlack + kLift <= 15.0f, "P in fp16");
 constexpr uint32_t kWaitDefaultNs = 1000000000u;
-constexpr int kLaunchRegs = 80, kRowRegs = 96, kConvRegs = 72, kIssueRegs = 24;
-static_assert(4 * kRowRegs + kConvRegs + kIssueRegs <= 6 * kLaunchRegs, "register split");
+// registers per thread after the split (8 row, 8 conversion and 4 other warps), out of those of
+// the 20 warps that the block launches with
+constexpr int kLaunchRegs = 96, kRowRegs = 160, kConvRegs = 64, kIssueRegs = 24;
+static_assert(2 * kRowRegs + 2 * kConvRegs + kIssueRegs <= 5 * kLaunchRegs, "register split");
 
 // shared memory (bytes); operand tiles 1024-byte aligned, the same in both CTAs
 constexpr int kQOff = 0;                              // Q fp16 [2 chunks][128 rows][128 B]
@@ -73,9 +87,9 @@ constexpr int kKBuf = 16384;
 constexpr int kVOff = kKOff + 2 * kKBuf;              // V fp16, 2 buffers x [2 atoms][128 cells][128 B]
 constexpr int kVBuf = 32768, kVAtom = 16384;
 constexpr int kKsOff = kVOff + 2 * kVBuf;             // K scales, 4 tiles x [128] f32
-constexpr int kRedOff = kKsOff + 4 * 512;             // [4][128] f32 exchange, [128] score factors
-constexpr int kBarOff = kRedOff + 4 * 512 + 512;
-constexpr int kCtlOff = kBarOff + 192;                // tmem slot, failure word, bad groups of 4 tiles, valid groups of the stages
+constexpr int kRedOff = kKsOff + 4 * 512;             // [128] f32 each: score factors, references, sums of the two groups
+constexpr int kBarOff = kRedOff + 4 * 512;
+constexpr int kCtlOff = kBarOff + 256;                // tmem slot, failure word, bad groups of 4 tiles, valid groups of the stages
 constexpr int kRawOff = (kCtlOff + 64 + 1023) / 1024 * 1024;
 constexpr int kSmemMax = 227 * 1024;
 // a raw tile: K codes of the CTA's 64 cells (4 boxes of 16 cells x 128 B), V nibbles of the 128 cells (8 boxes),
@@ -88,10 +102,10 @@ static_assert(raw_stages(2) == 3 && raw_stages(7) >= 2 && raw_stages(8) >= 1, "r
 static_assert(kKsOff - kQOff >= kRows * 256 * 4, "row buffer");
 
 // mbarriers, at kBarOff + 8 * index
-enum { kBarKFull = 0, kBarVFull = 2, kBarPFull = 4, kBarSFull = 6, kBarODone = 8, kBarKsFull = 10, kBarDrain = 14,
-       kBarRawFull = 16, kBarRawEmpty = 20 };
+enum { kBarKFull = 0, kBarVFull = 2, kBarPFull = 4, kBarSFull = 6, kBarODone = 8, kBarKsFull = 10, kBarSFree = 14,
+       kBarDrain = 15, kBarRawFull = 16, kBarRawEmpty = 20, kBarRef = 24 };
 
-constexpr uint32_t kTmemCols = 512, kSBuf = 128, kOCol = 256;
+constexpr uint32_t kTmemCols = 512, kPCol = 128, kPBuf = 64, kOCol = 256;
 
 // ---------------------------------------------------------------- the schedule
 constexpr int kTileTok = 32;                  // tokens of a token tile
@@ -287,6 +301,14 @@ __global__ void __launch_bounds__(1024, 1) diff_schedule_kernel(const SchedulePa
   }
 }
 
+// ---------------------------------------------------------------- waits
+// mbar_wait for waits that nearly always end soon: the barrier's own bounded sleep first, the
+// clock only behind it
+__device__ __forceinline__ bool wait_soon(uint32_t bar, uint32_t parity, uint32_t limit_ns) {
+  if (limit_ns >= 1000u && mbar_try(bar, parity, 20000u)) return true;
+  return mbar_wait(bar, parity, limit_ns);
+}
+
 // ---------------------------------------------------------------- pair PTX
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
@@ -348,33 +370,39 @@ __device__ __forceinline__ bool elect_one() {
       : "=r"(r));
   return r != 0;
 }
-// OR over the four warps that share 32 rows (warps w, w + 4, w + 8, w + 12; w < 4)
-__device__ __forceinline__ bool quad_any(int w, bool pred) {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
-      "setp.ne.u32 p, %2, 0;\n\t"
-      "barrier.cta.red.or.pred q, %1, 128, p;\n\t"
-      "selp.u32 %0, 1, 0, q;\n\t}"
-      : "=r"(r)
-      : "r"(w + 3), "r"(pred ? 1u : 0u)
-      : "memory");
-  return r != 0;
-}
 // a barrier over the row warps that also ORs a predicate
 __device__ __forceinline__ bool rows_any(bool pred) {
   uint32_t r;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.u32 p, %1, 0;\n\t"
-      "barrier.cta.red.or.pred q, 1, 512, p;\n\t"
+      "barrier.cta.red.or.pred q, 1, 256, p;\n\t"
       "selp.u32 %0, 1, 0, q;\n\t}"
       : "=r"(r)
       : "r"(pred ? 1u : 0u)
       : "memory");
   return r != 0;
 }
-__device__ __forceinline__ void rows_barrier() { asm volatile("barrier.cta.sync 2, 512;" ::: "memory"); }
+__device__ __forceinline__ void rows_barrier() { asm volatile("barrier.cta.sync 2, 256;" ::: "memory"); }
+// 128 consecutive fp32 columns of this thread's TMEM lane: four loads in flight, one wait
+__device__ __forceinline__ void tmem_ld128(uint32_t taddr, float v[128]) {
+#pragma unroll
+  for (int h = 0; h < 4; ++h) {
+    float* x = v + 32 * h;
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3]), "=f"(x[4]), "=f"(x[5]), "=f"(x[6]), "=f"(x[7]), "=f"(x[8]), "=f"(x[9]),
+          "=f"(x[10]), "=f"(x[11]), "=f"(x[12]), "=f"(x[13]), "=f"(x[14]), "=f"(x[15]), "=f"(x[16]), "=f"(x[17]), "=f"(x[18]),
+          "=f"(x[19]), "=f"(x[20]), "=f"(x[21]), "=f"(x[22]), "=f"(x[23]), "=f"(x[24]), "=f"(x[25]), "=f"(x[26]), "=f"(x[27]),
+          "=f"(x[28]), "=f"(x[29]), "=f"(x[30]), "=f"(x[31])
+        : "r"(taddr + 32 * h)
+        : "memory");
+  }
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < 128; ++i) asm volatile("" : "+f"(v[i]));       // no use of them moves ahead of the wait
+}
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t v[16]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
@@ -383,23 +411,26 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t v[16]) 
       : "memory");
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-__device__ __forceinline__ void tmem_ld8(uint32_t taddr, float v[8]) {
-  uint32_t r[8];
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-               : "r"(taddr)
-               : "memory");
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
-}
-// two nibbles at bits k and k + 16 of t -> (n - 8) / 8 (exact) times d, rounded to fp16
-__device__ __forceinline__ uint32_t nib_times(uint32_t t, int k, __half2 d2) {
-  const uint32_t x = ((t >> k) & 0x000f000fu) | 0x64006400u;                                  // 1024 + n
-  const __half2 eighth = __halves2half2(__ushort_as_half(0x3000), __ushort_as_half(0x3000));   // 1/8
-  const __half2 m129 = __halves2half2(__ushort_as_half(0xd808), __ushort_as_half(0xd808));     // -129
-  const __half2 r = __hmul2(__hfma2(*reinterpret_cast<const __half2*>(&x), eighth, m129), d2);
-  return *reinterpret_cast<const uint32_t*>(&r);
+// A word of nibble bytes b0..b3 -> fp16 pairs of V = RN((n - 8) / 8 * d): lo {b0, b2}, {b1, b3} of the
+// low nibbles, hi of the high ones.  0x640n is 1024 + n and 0x64n0 is 1024 + 16 n in fp16;
+// (1024 + n) / 8 - 129 and (1024 + 16 n) / 128 - 9 are both (n - 8) / 8, exactly.  (Elements 1 and
+// 2 of each four come out swapped; the rows are put right as they are written.)
+__device__ __forceinline__ void nib_word(uint32_t r, __half2 d2, uint32_t lo[2], uint32_t hi[2]) {
+  const uint32_t r8 = r >> 8;
+  const __half2 eighth = __halves2half2(__ushort_as_half(0x3000), __ushort_as_half(0x3000));    // 1/8
+  const __half2 m129 = __halves2half2(__ushort_as_half(0xd808), __ushort_as_half(0xd808));      // -129
+  const __half2 c128th = __halves2half2(__ushort_as_half(0x2000), __ushort_as_half(0x2000));    // 1/128
+  const __half2 m9 = __halves2half2(__ushort_as_half(0xc880), __ushort_as_half(0xc880));        // -9
+  const uint32_t t0 = (r & 0x000f000fu) | 0x64006400u, t1 = (r8 & 0x000f000fu) | 0x64006400u;
+  const uint32_t t2 = (r & 0x00f000f0u) | 0x64006400u, t3 = (r8 & 0x00f000f0u) | 0x64006400u;
+  const __half2 v0 = __hmul2(__hfma2(*reinterpret_cast<const __half2*>(&t0), eighth, m129), d2);
+  const __half2 v1 = __hmul2(__hfma2(*reinterpret_cast<const __half2*>(&t1), eighth, m129), d2);
+  const __half2 v2 = __hmul2(__hfma2(*reinterpret_cast<const __half2*>(&t2), c128th, m9), d2);
+  const __half2 v3 = __hmul2(__hfma2(*reinterpret_cast<const __half2*>(&t3), c128th, m9), d2);
+  lo[0] = *reinterpret_cast<const uint32_t*>(&v0);
+  lo[1] = *reinterpret_cast<const uint32_t*>(&v1);
+  hi[0] = *reinterpret_cast<const uint32_t*>(&v2);
+  hi[1] = *reinterpret_cast<const uint32_t*>(&v3);
 }
 
 // ---------------------------------------------------------------- the kernel
@@ -416,6 +447,7 @@ struct PairParams {
   uint32_t wait_ns;
   FastDiv page_div;
   int stages, stage_bytes;  // raw tiles in flight
+  int box_shift;            // log2 of the cells of a copy: 4, 5 or 6
 };
 
 // grid: 2 CTAs per unit
@@ -427,11 +459,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const uint32_t rank = cluster_rank();
   const CacheView& C = p.C;
   const int HQ = C.H * kGqa;
-  const int row = tid & (kRows - 1), part = tid >> 7;      // (row warps) 32 cells of a tile and 64 dims of O per part
+  const int row = tid & (kRows - 1), group = tid >> 7;     // (row warps) tiles group, group + 2, ...
   const uint32_t bars = sb + kBarOff;
   volatile int* ctl = reinterpret_cast<volatile int*>(smem + kCtlOff);   // [0] tmem, [1] failed, [4..7] bad groups of 4 tiles, [8..10] valid groups
-  float* red = reinterpret_cast<float*>(smem + kRedOff);                 // [4][128]
-  float* fsc = red + 4 * kRows;                                          // [128]
+  float* fsc = reinterpret_cast<float*>(smem + kRedOff);                 // [128] score factors
+  float* ref = fsc + kRows;                                              // [128] reference maxima
+  float* sums = fsc + 2 * kRows;                                         // [2][128]
   float* ksbuf = reinterpret_cast<float*>(smem + kKsOff);
 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -454,66 +487,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   // cells that any row of the pair sees (those behind are neither looked up nor read)
   const int limit = p.steps ? min(tt.cell_tiles * kTileN, tt.vis0) : tt.vis0 + tt.n - 1;
 
-  if (warp == kLoadWarp) {
+  if (warp == kLoadWarp0) {
     int count = 0;
     if (lane < kBarPFull) count = 8;                       // K, V tiles: 4 conversion warps of both CTAs
-    else if (lane < kBarSFull) count = 2 * kRowWarps;      // P: the row warps of both CTAs
+    else if (lane < kBarSFull) count = 8;                  // P: a tile's 4 row warps of both CTAs
     else if (lane < kBarKsFull) count = 1;                 // S done, O done: one commit
-    else if (lane < kBarDrain) count = 4;                  // K scales: the CTA's conversion warps
+    else if (lane < kBarSFree) count = 4;                  // K scales: the CTA's K conversion warps
+    else if (lane == kBarSFree) count = 8;                 // S read: 4 row warps of both CTAs
     else if (lane == kBarDrain) count = 1;                 // everything done: one commit
-    else if (lane >= kBarRawFull && lane < kBarRawEmpty) count = 1;   // raw tile: the loader, and the bytes of its copies
-    else if (lane >= kBarRawEmpty && lane < kBarRawEmpty + 4) count = 4;
-    if (count) mbar_init(bars + 8 * lane, count);
+    else if (lane < kBarRawEmpty) count = kLoadWarps;      // raw tile: the loaders, and the bytes of their copies
+    else if (lane < kBarRef) count = 8;                    // raw tile read: the CTA's conversion warps
+    else count = 1;                                        // a warp's references: [quarter of the rows][tile & 1]
+    mbar_init(bars + 8 * lane, count);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     if (lane < 15) ctl[1 + lane] = 0;
     if (lane == 0) {
       asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_k)) : "memory");
       asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_v)) : "memory");
     }
-    __syncwarp();
   }
   if (warp == kIssueWarp) tmem_alloc_pair(sb + kCtlOff, kTmemCols);
-
-  // ---- the load warp's copies of tile i into a stage: page ids of four tiles, eight
-  // 16-cell groups each, are held one per lane
-  int page_mine = -1;
-  auto load_tile = [&](int i, int stage, bool leader) {
-    const int H = C.H;
-    if ((i & 3) == 0) {
-      const int c = (tile0 + i + (lane >> 3)) * kTileN + 16 * (lane & 7);
-      const int64_t pidx = p.page_div.div(static_cast<uint32_t>(c));
-      page_mine = INT32_MIN;                               // behind the limit, or another range's
-      if (i + (lane >> 3) < n_tiles && c < limit) {
-        const int page = pidx < p.max_pages ? __ldcg(pt + pidx) : -1;
-        page_mine = page >= 0 && page < C.n_pages ? page : -1;
-      }
-    }
-    const uint32_t dst = sb + kRawOff + stage * p.stage_bytes, bar = bars + 8 * (kBarRawFull + stage);
-    const int my_group_page = __shfl_sync(kFull, page_mine, 8 * (i & 3) + (lane & 7));
-    const unsigned good = __ballot_sync(kFull, my_group_page >= 0) & 255u;
-    const unsigned bad = __ballot_sync(kFull, my_group_page == -1) & 255u;
-    const unsigned kgood = (good >> (4 * rank)) & 15u;
-    if (leader) {
-      if (bad) record_status(p.status, K8V4_ERANGE);
-      ctl[8 + stage] = static_cast<int>(good | (bad << 8));
-      mbar_expect_tx(bar, __popc(good) * (2048u + 384u * H) + __popc(kgood) * 2048u);
-    }
-#pragma unroll 1
-    for (int q = 0; q < 8; ++q) {
-      const int page = __shfl_sync(kFull, my_group_page, q);
-      if (!leader || page < 0) continue;
-      const int cell = (tile0 + i) * kTileN + 16 * q;
-      const int slot = cell - static_cast<int>(p.page_div.div(static_cast<uint32_t>(cell))) * C.P;
-      const int kq = q - 4 * static_cast<int>(rank);
-      if (kq >= 0 && kq < 4) tma_load_4d(dst + kq * 2048, &tm_k, 128 * map, g, slot, page, bar);
-      tma_load_4d(dst + kRawV + q * 2048, &tm_v, 0, g, slot, page, bar);
-      const uint8_t* pg = C.pages + static_cast<int64_t>(page) * C.page_bytes;
-      bulk_load(dst + kRawKs + q * 128 * H, pg + C.ks_off() + static_cast<int64_t>(slot) * 8 * H, 128 * H, bar);
-      bulk_load(dst + kRawKs + 1024 * H + q * 256 * H, pg + C.vs_off() + static_cast<int64_t>(slot) * 16 * H, 256 * H, bar);
-    }
-    __syncwarp();
-  };
-  if (warp == kLoadWarp) load_tile(0, 0, elect_one());     // while the others set Q up
 
   // ---- visibility of this thread's row
   int my_vis = 0;
@@ -523,14 +516,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   }
   // ---- Q rows of this map -> fp16 with a power of two per row, swizzled K-major: half a warp
   // takes a row at a time (8 elements a lane)
-  if (warp < kLoadWarp) {
-    constexpr int kPer = (kRows + 2 * kLoadWarp - 1) / (2 * kLoadWarp);
+  if (warp < kIssueWarp) {
+    constexpr int kPer = kRows / (2 * kIssueWarp);
     const int sub = lane >> 4, l16 = lane & 15;
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
-      const int r = 2 * (warp + kLoadWarp * j) + sub;
+      const int r = 2 * (warp + kIssueWarp * j) + sub;
       float x[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-      if (r < kRows && r / kGqa < tok_n) {
+      if (r / kGqa < tok_n) {
         const int64_t e0 = (static_cast<int64_t>(tok_first + r / kGqa) * HQ + g * kGqa + r % kGqa) * kD + 128 * map + 8 * l16;
         if (p.q_f32) {
           const float4* src = reinterpret_cast<const float4*>(static_cast<const float*>(p.q) + e0);
@@ -552,7 +545,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       for (int u = 0; u < 8; ++u) amax = fmaxf(amax, fabsf(x[u]));
 #pragma unroll
       for (int o = 8; o >= 1; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, o));
-      if (r >= kRows) continue;
       const int ex = amax > 0.0f ? static_cast<int>((__float_as_uint(amax) >> 23) & 0xffu) - 127 : 0;
       const int sh = max(-100, min(100, 14 - ex));
       const float up = ldexpf(1.0f, sh);
@@ -580,199 +572,213 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRowRegs));
     const uint32_t lane_base = static_cast<uint32_t>(32 * (warp & 3)) << 16;
     const float my_f = fsc[row];
-    const uint32_t p_full0 = map_to(bars + 8 * kBarPFull, 0);
-    const uint32_t o_tile = tmem + lane_base + kOCol + 64 * part;
-    // the running O of this thread's 64 dims: float4 number c at acc[512 c] (the block is 128 x 260 floats)
-    float4* const acc = reinterpret_cast<float4*>(block) + tid;
-    float m_run = -INFINITY, l_part = 0.0f, acc_scale = 1.0f;          // acc counts times acc_scale
-    bool failed = false, have_acc = false;
-    for (int i = 0; i < n_tiles; ++i) {
-      const int buf = i & 1;
+    const uint32_t p_full0 = map_to(bars + 8 * kBarPFull, 0), s_free0 = map_to(bars + 8 * kBarSFree, 0);
+    const uint32_t refs = bars + 8 * (kBarRef + 2 * (warp & 3));
+    // the running O of this row: float4 number c at acc[128 c] (the block is 128 x 260 floats)
+    float4* const acc = reinterpret_cast<float4*>(block) + row;
+    // l counts relative to 2^l_ref; the running O times acc_scale (kept by the even tiles' group, which folds)
+    float l = 0.0f, l_ref = -INFINITY;
+    bool failed = false;
+    for (int i = group; i < n_tiles; i += 2) {
       const uint32_t parity = (i >> 1) & 1;
-      if (!mbar_wait(bars + 8 * (kBarSFull + buf), parity, p.wait_ns) ||
-          !mbar_wait(bars + 8 * (kBarKsFull + (i & 3)), (i >> 2) & 1, p.wait_ns)) {
+      if (!wait_soon(bars + 8 * (kBarSFull + group), parity, p.wait_ns) ||
+          !wait_soon(bars + 8 * (kBarKsFull + (i & 3)), (i >> 2) & 1, p.wait_ns)) {
         failed = true;
-        ctl[1] = 1;
+        break;
       }
       tc_fence_after();
-      // scores, unscaled (my_f > 0, so the maximum commutes with it); cell c of this part
-      const uint32_t sbase = tmem + lane_base + kSBuf * buf + 32 * part;
-      const float* ks = ksbuf + 128 * (i & 3) + 32 * part;
-      float2 sc[16];
-      {
-        float a[32];
-        tmem_ld32(sbase, a);
+      float sc[kTileN];
+      tmem_ld128(tmem + lane_base, sc);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) arrive_cluster(s_free0);
+      // scores, unscaled (my_f > 0, so the maximum commutes with it)
+      const float* ks = ksbuf + 128 * (i & 3);
 #pragma unroll
-        for (int c = 0; c < 32; c += 4) {
-          const float4 k4 = *reinterpret_cast<const float4*>(ks + c);
-          sc[c / 2] = __fmul2_rn(make_float2(k4.x, k4.y), make_float2(a[c], a[c + 1]));
-          sc[c / 2 + 1] = __fmul2_rn(make_float2(k4.z, k4.w), make_float2(a[c + 2], a[c + 3]));
-        }
+      for (int c = 0; c < kTileN; c += 4) {
+        const float4 k4 = *reinterpret_cast<const float4*>(ks + c);
+        const float2 a = __fmul2_rn(make_float2(k4.x, k4.y), make_float2(sc[c], sc[c + 1]));
+        const float2 b = __fmul2_rn(make_float2(k4.z, k4.w), make_float2(sc[c + 2], sc[c + 3]));
+        sc[c] = a.x; sc[c + 1] = a.y;
+        sc[c + 2] = b.x; sc[c + 3] = b.y;
       }
-      const int vis = my_vis - (tile0 + i) * kTileN - 32 * part;       // cells [0, vis) of this part
-      const int bad = (ctl[4 + (i & 3)] >> (2 * part)) & 3;            // its groups of 16 cells on a page out of range
-      if (vis < 32 || bad) {
+      const int vis = my_vis - (tile0 + i) * kTileN;                   // cells [0, vis) of the tile
+      const int bad = ctl[4 + (i & 3)];                                // its groups of 16 cells on a page out of range
+      if (vis < kTileN || bad) {
 #pragma unroll
-        for (int c = 0; c < 32; c += 2) {
-          const bool off = (bad >> (c >> 4)) & 1;
-          if (c >= vis || off) sc[c / 2].x = -INFINITY;
-          if (c + 1 >= vis || off) sc[c / 2].y = -INFINITY;
-        }
+        for (int c = 0; c < kTileN; ++c)
+          if (c >= vis || ((bad >> (c >> 4)) & 1)) sc[c] = -INFINITY;
       }
-      float mx0 = -INFINITY, mx1 = -INFINITY;
+      float mx[4] = {sc[0], sc[1], sc[2], sc[3]};
 #pragma unroll
-      for (int c = 0; c < 16; c += 2) {
-        mx0 = fmaxf(mx0, fmaxf(sc[c].x, sc[c].y));
-        mx1 = fmaxf(mx1, fmaxf(sc[c + 1].x, sc[c + 1].y));
+      for (int c = 4; c < kTileN - 4; c += 8) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) mx[k] = fmaxf(mx[k], fmaxf(sc[c + 2 * k], sc[c + 2 * k + 1]));
       }
-      const float top = fmaxf(mx0, mx1) * my_f;
-      // the four threads of a row agree on its reference: a vote of their four warps
-      const bool any = quad_any(warp & 3, failed || top > m_run + kSlack);
-      float alpha = 1.0f;
-      if (any) {
-        red[part * kRows + row] = top;
-        // the four leave together: the failure word is read once, ahead of a vote
-        if (quad_any(warp & 3, failed || ctl[1] != 0)) { failed = true; break; }
-        const float mt = fmaxf(fmaxf(red[row], red[kRows + row]), fmaxf(red[2 * kRows + row], red[3 * kRows + row]));
-        if (mt > m_run + kSlack) {
-          alpha = exp2f(m_run - mt);                                   // 0 on the first visible tile
-          m_run = mt;
-          l_part *= alpha;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) mx[k] = fmaxf(mx[k], sc[kTileN - 4 + k]);
+      const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * my_f;
+      // the row's reference, as the tile before left it
+      float m_run = -INFINITY, alpha = 1.0f;
+      if (i > 0) {
+        if (!wait_soon(refs + 8 * (group ^ 1), ((i - 1) >> 1) & 1, p.wait_ns)) {
+          failed = true;
+          break;
         }
+        m_run = ref[row];
       }
-      const float mu = (m_run == -INFINITY ? 0.0f : m_run) - 7.0f;
+      if (top > m_run + kSlack) {
+        alpha = ex2_ftz(m_run - top);                                   // 0 on the first visible tile
+        m_run = top;
+      }
+      ref[row] = m_run;
+      __syncwarp();
+      if (lane == 0) arrive_local(refs + 8 * group);
+      if (l_ref != m_run) {                                            // moved, by this tile or the one before
+        l = l_ref > -INFINITY ? l * ex2_ftz(l_ref - m_run) : 0.0f;
+        l_ref = m_run;
+      }
+      const float mu = (m_run == -INFINITY ? 0.0f : m_run) - kLift;
       const float2 f2 = make_float2(my_f, my_f), mu2 = make_float2(-mu, -mu);
+      // P(i - 2) has been read
+      if (i >= 2 && !wait_soon(bars + 8 * (kBarODone + group), ((i - 2) >> 1) & 1, p.wait_ns)) {
+        failed = true;
+        break;
+      }
       float2 psum = make_float2(0.0f, 0.0f);
-      {
+      const uint32_t pcol = tmem + lane_base + kPCol + kPBuf * group;
+#pragma unroll
+      for (int h = 0; h < 4; ++h) {
         uint32_t ph[16];
 #pragma unroll
         for (int c = 0; c < 16; ++c) {
-          const float2 e = __ffma2_rn(sc[c], f2, mu2);
+          const float2 e = __ffma2_rn(make_float2(sc[32 * h + 2 * c], sc[32 * h + 2 * c + 1]), f2, mu2);
           const float2 q = make_float2(ex2_ftz(e.x), ex2_ftz(e.y));
-          const __half2 h = __floats2half2_rn(q.x, q.y);
+          const __half2 hq = __floats2half2_rn(q.x, q.y);
           psum = __fadd2_rn(psum, q);
-          ph[c] = *reinterpret_cast<const uint32_t*>(&h);
+          ph[c] = *reinterpret_cast<const uint32_t*>(&hq);
         }
-        tmem_st16(sbase, ph);
+        tmem_st16(pcol + 16 * h, ph);
       }
-      l_part += psum.x + psum.y;
-      tmem_wait_st();
-      // O of the tiles so far: into acc at every kChain-th tile (both CTAs), rescaled
+      l += psum.x + psum.y;
+      // O of the tiles so far: into the running sum at every kChain-th tile (both CTAs), rescaled
       // in place where a reference moved in between
       const bool folds = i > 0 && i % kChain == 0;
-      if (folds || (i > 0 && any && __any_sync(kFull, alpha != 1.0f))) {
-        if (!mbar_wait(bars + 8 * (kBarODone + (buf ^ 1)), ((i - 1) >> 1) & 1, p.wait_ns)) {
+      if (folds || (i > 0 && __any_sync(kFull, alpha != 1.0f))) {
+        if (!wait_soon(bars + 8 * (kBarODone + (group ^ 1)), ((i - 1) >> 1) & 1, p.wait_ns)) {
           failed = true;
-          ctl[1] = 1;
+          break;
         }
         tc_fence_after();
-        if (folds) {                                                   // acc = (acc + O) * alpha
-          const float a = alpha * acc_scale;
+        // the running sum is relative to the reference too: both move
+        const bool have = i > kChain;
+#pragma unroll 1
+        for (int h = 0; h < 8; ++h) {
+          float o[32];
+          tmem_ld32(tmem + lane_base + kOCol + 32 * h, o);
+          if (folds) {                                                 // acc = (acc + O) * alpha
 #pragma unroll
-          for (int h = 0; h < 4; ++h) {
-            float4 old[4];
+            for (int c = 0; c < 8; ++c) {
+              const float4 old = have ? acc[128 * (8 * h + c)] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+              acc[128 * (8 * h + c)] = make_float4((old.x + o[4 * c]) * alpha, (old.y + o[4 * c + 1]) * alpha,
+                                                   (old.z + o[4 * c + 2]) * alpha, (old.w + o[4 * c + 3]) * alpha);
+            }
+          } else {                                                     // O *= alpha
 #pragma unroll
-            for (int c = 0; c < 4; ++c) old[c] = have_acc ? acc[512 * (4 * h + c)] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            float o[16];
-            tmem_ld16(o_tile + 16 * h, o);
+            for (int c = 0; c < 32; c += 8) {
+              float x[8];
 #pragma unroll
-            for (int c = 0; c < 4; ++c)
-              acc[512 * (4 * h + c)] = make_float4(old[c].x * a + o[4 * c] * alpha, old[c].y * a + o[4 * c + 1] * alpha,
-                                                   old[c].z * a + o[4 * c + 2] * alpha, old[c].w * a + o[4 * c + 3] * alpha);
+              for (int k = 0; k < 8; ++k) x[k] = o[c + k] * alpha;
+              tmem_st8(tmem + lane_base + kOCol + 32 * h + c, x);
+            }
+            if (have) {
+#pragma unroll
+              for (int c = 0; c < 8; ++c) {
+                const float4 old = acc[128 * (8 * h + c)];
+                acc[128 * (8 * h + c)] = make_float4(old.x * alpha, old.y * alpha, old.z * alpha, old.w * alpha);
+              }
+            }
           }
-          have_acc = true;
-          acc_scale = 1.0f;
-        } else {                                                       // O *= alpha
+        }
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) arrive_cluster(p_full0 + 8 * group);
+    }
+    if (!failed && !wait_soon(bars + 8 * (kBarODone + ((n_tiles - 1) & 1)), ((n_tiles - 1) >> 1) & 1, p.wait_ns)) failed = true;
+    if (failed) ctl[1] = 1;
+    // PV of the last tile is done in both CTAs (one commit covers the pair), and with it every
+    // read of this CTA's operand tiles; past the barrier the last reference is known
+    const bool stop = rows_any(failed);
+    if (!stop) {
+      tc_fence_after();
+      const float m_run = ref[row];
+      sums[group * kRows + row] = l_ref > -INFINITY ? l * exp2f(l_ref - m_run) : 0.0f;
+      float* rowbuf = reinterpret_cast<float*>(smem + kQOff);          // [128][256] fp32, rotated by 4 * row
+      const bool have = n_tiles > kChain;
+#pragma unroll 1
+      for (int h = 4 * group; h < 4 * group + 4; ++h) {                // 128 of the dims to a group
+        float o[32];
+        tmem_ld32(tmem + lane_base + kOCol + 32 * h, o);
 #pragma unroll
-          for (int h = 0; h < 8; ++h) {
-            float o[8];
-            tmem_ld8(o_tile + 8 * h, o);
-#pragma unroll
-            for (int c = 0; c < 8; ++c) o[c] *= alpha;
-            tmem_st8(o_tile + 8 * h, o);
+        for (int c = 0; c < 8; ++c) {
+          float4 x = make_float4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
+          if (have) {
+            const float4 old = acc[128 * (8 * h + c)];
+            x.x += old.x; x.y += old.y; x.z += old.z; x.w += old.w;
           }
-          acc_scale *= alpha;
+          *reinterpret_cast<float4*>(rowbuf + row * 256 + ((32 * h + 4 * c + 4 * row) & 255)) =
+              make_float4(8.0f * x.x, 8.0f * x.z, 8.0f * x.y, 8.0f * x.w);   // (dims 1 and 2 of each four are swapped)
         }
       }
       tc_fence_before();
-      __syncwarp();
-      if (lane == 0) arrive_cluster(p_full0 + 8 * buf);
-    }
-    // ---- the last O, then o / m / l of the rows
-    float o[64];
-    if (!failed) {
-      if (mbar_wait(bars + 8 * (kBarODone + ((n_tiles - 1) & 1)), ((n_tiles - 1) >> 1) & 1, p.wait_ns)) {
-        tc_fence_after();
-#pragma unroll
-        for (int h = 0; h < 2; ++h) tmem_ld32(o_tile + 32 * h, o + 32 * h);
-        if (have_acc) {
-#pragma unroll
-          for (int c = 0; c < 16; ++c) {
-            const float4 old = acc[512 * c];
-            o[4 * c] += old.x * acc_scale;
-            o[4 * c + 1] += old.y * acc_scale;
-            o[4 * c + 2] += old.z * acc_scale;
-            o[4 * c + 3] += old.w * acc_scale;
-          }
-        }
-        tc_fence_before();
-      } else {
-        failed = true;
-        ctl[1] = 1;
+      rows_barrier();                                                  // rows and sums written, running sums read
+      if (group == 0 && row / kGqa < tok_n) {
+        block[row * kDiffRow + 256] = m_run - kLift;                   // o and l are relative to 2^(m - kLift)
+        block[row * kDiffRow + 257] = sums[row] + sums[kRows + row];
       }
-    }
-    // PV of the last tile is done in both CTAs (one commit covers the pair), and with it every
-    // read of this CTA's operand tiles; every thread has read its running sum
-    red[part * kRows + row] = l_part;
-    const bool stop = rows_any(failed);
-    if (!stop) {
-      const float l = (red[row] + red[kRows + row]) + (red[2 * kRows + row] + red[3 * kRows + row]);
-      float* rowbuf = reinterpret_cast<float*>(smem + kQOff);          // [128][256] fp32, rotated by 4 * row
-#pragma unroll
-      for (int i = 0; i < 64; i += 4)
-        *reinterpret_cast<float4*>(rowbuf + row * 256 + ((64 * part + i + 4 * row) & 255)) =
-            make_float4(8.0f * o[i], 8.0f * o[i + 1], 8.0f * o[i + 2], 8.0f * o[i + 3]);
-      if (part == 0 && row / kGqa < tok_n) {
-        block[row * kDiffRow + 256] = m_run - 7.0f;                    // o and l are relative to 2^(m - 7)
-        block[row * kDiffRow + 257] = l;
-      }
-      rows_barrier();
       for (int r = warp; r < kGqa * tok_n; r += kRowWarps) {
         float4* dst = reinterpret_cast<float4*>(block + r * kDiffRow);
         dst[lane] = *reinterpret_cast<const float4*>(rowbuf + r * 256 + ((4 * lane + 4 * r) & 255));
         dst[32 + lane] = *reinterpret_cast<const float4*>(rowbuf + r * 256 + ((128 + 4 * lane + 4 * r) & 255));
       }
-    } else if (part == 0 && row / kGqa < tok_n) {                      // nothing to join of a unit that failed
+    } else if (group == 0 && row / kGqa < tok_n) {                     // nothing to join of a unit that failed
       block[row * kDiffRow + 256] = -INFINITY;
       block[row * kDiffRow + 257] = 0.0f;
     }
   } else if (warp < kIssueWarp) {
     // ================================================================ conversion
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kConvRegs));
-    const int t = tid - 32 * kConvWarp0;                   // 0..127
+    const int t = tid & 127;
+    const bool is_v = warp >= kVConvWarp0;
     // K: cell 64 rank + (t & 63), dims [64 (t >> 6), +64); V: cell t, blocks 4 rank .. 4 rank + 3.
     // The copies put 16-byte unit u of a row at u ^ (row & 7) (128-byte swizzle).
     const int kcell = t & 63, kchunk = t >> 6;
-    const uint32_t k_full0 = map_to(bars + 8 * kBarKFull, 0), v_full0 = map_to(bars + 8 * kBarVFull, 0);
+    const uint32_t full0 = map_to(bars + 8 * (is_v ? kBarVFull : kBarKFull), 0);
     const uint32_t kraw = (kcell >> 4) * 2048 + (kcell & 15) * 128;
     const uint32_t vraw = kRawV + (t >> 4) * 2048 + (t & 15) * 128;
     const uint32_t ksraw = kRawKs + (t >> 4) * 128 * C.H + ((t & 15) * C.H + g) * 8 + 4 * map;
     const uint32_t vsraw = kRawKs + 1024 * C.H + (t >> 4) * 256 * C.H + ((t & 15) * C.H + g) * 16 + 8 * rank;
+    // a tile's buffers are free once the product of tile i - 2 has read them
+    const uint32_t freed = bars + 8 * (is_v ? kBarODone : kBarSFull);
     int stage = 0;
     uint32_t raw_phase = 0;
     for (int i = 0; i < n_tiles; ++i) {
       const int buf = i & 1;
-      const uint32_t last = ((i - 2) >> 1) & 1;            // phase of tile i - 2 on the buffers' barriers
       const uint32_t raw = sb + kRawOff + stage * p.stage_bytes;
-      if (!mbar_wait(bars + 8 * (kBarRawFull + stage), raw_phase, p.wait_ns)) { ctl[1] = 1; break; }
+      if (!wait_soon(bars + 8 * (kBarRawFull + stage), raw_phase, p.wait_ns)) { ctl[1] = 1; break; }
       const int valid = ctl[8 + stage];                    // the tile's 16-cell groups that were copied; bits 8..15: on a bad page
-      // ---- K(i) and its scales, once QK(i - 2) has read the buffer
-      if (i >= 2 && !mbar_wait(bars + 8 * (kBarSFull + buf), last, p.wait_ns)) { ctl[1] = 1; break; }
-      {
-        const uint32_t dst = sb + kKOff + buf * kKBuf + kchunk * 8192;
+      if (!is_v) {
         uint4 kw[4];
 #pragma unroll
         for (int u = 0; u < 4; ++u) kw[u] = lds128(raw + kraw + (((4 * kchunk + u) ^ (kcell & 7)) << 4));
+        float ksc;
+        asm volatile("ld.shared.f32 %0, [%1];" : "=f"(ksc) : "r"(raw + ksraw));
+        if (i >= 2 && !wait_soon(freed + 8 * buf, ((i - 2) >> 1) & 1, p.wait_ns)) { ctl[1] = 1; break; }
+        __syncwarp();
+        if (lane == 0) arrive_local(bars + 8 * (kBarRawEmpty + stage));
+        const uint32_t dst = sb + kKOff + buf * kKBuf + kchunk * 8192;
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
           const uint4 w = kw[u];
@@ -784,20 +790,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           sts128(dst + swz(kcell, 2 * u), h[0], h[1], h[2], h[3]);
           sts128(dst + swz(kcell, 2 * u + 1), h[4], h[5], h[6], h[7]);
         }
-        float ksc;
-        asm volatile("ld.shared.f32 %0, [%1];" : "=f"(ksc) : "r"(raw + ksraw));
         ksbuf[128 * (i & 3) + t] = ksc;
         if (t == 0) ctl[4 + (i & 3)] = valid >> 8;
         fence_async_smem();
         __syncwarp();
         if (lane == 0) {
           arrive_local(bars + 8 * (kBarKsFull + (i & 3)));
-          arrive_cluster(k_full0 + 8 * buf);
+          arrive_cluster(full0 + 8 * buf);
         }
-      }
-      // ---- V(i), once PV(i - 2) has read the buffer
-      if (i >= 2 && !mbar_wait(bars + 8 * (kBarODone + buf), last, p.wait_ns)) { ctl[1] = 1; break; }
-      {
+      } else {
         const uint32_t dst = sb + kVOff + buf * kVBuf;
         // a cell that was not copied, or that nobody sees, counts with V = 0 (its P is 0, its bytes are anything)
         uint32_t vd[2];
@@ -806,30 +807,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int b = 0; b < 4; ++b) vw[b] = lds128(raw + vraw + (((4 * rank + b) ^ (t & 7)) << 4));
         if (!((valid >> (t >> 4)) & 1) || (tile0 + i) * kTileN + t >= limit) vd[0] = vd[1] = 0;
+        if (i >= 2 && !wait_soon(freed + 8 * buf, ((i - 2) >> 1) & 1, p.wait_ns)) { ctl[1] = 1; break; }
         __syncwarp();
         if (lane == 0) arrive_local(bars + 8 * (kBarRawEmpty + stage));
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
           const __half dh = __ushort_as_half(static_cast<unsigned short>(vd[b >> 1] >> (16 * (b & 1))));
           const __half2 d2 = __halves2half2(dh, dh);
-          const uint32_t ws4[4] = {vw[b].x, vw[b].y, vw[b].z, vw[b].w};
+          uint32_t lo[8], hi[8];                           // dims 0..15 of the block, and 16..31
+          nib_word(vw[b].x, d2, lo, hi);
+          nib_word(vw[b].y, d2, lo + 2, hi + 2);
+          nib_word(vw[b].z, d2, lo + 4, hi + 4);
+          nib_word(vw[b].w, d2, lo + 6, hi + 6);
           const uint32_t at = dst + (b >> 1) * kVAtom;     // 64 dims an atom
-#pragma unroll
-          for (int hn = 0; hn < 2; ++hn) {                 // low nibbles: dims 0..15 of the block, high: 16..31
-            uint32_t v[8];
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              v[2 * q] = nib_times(prmt(ws4[q], 0u, 0x5140u), 4 * hn, d2);
-              v[2 * q + 1] = nib_times(prmt(ws4[q], 0u, 0x5342u), 4 * hn, d2);
-            }
-            const int u0 = 4 * (b & 1) + 2 * hn;
-            sts128(at + swz(t, u0), v[0], v[1], v[2], v[3]);
-            sts128(at + swz(t, u0 + 1), v[4], v[5], v[6], v[7]);
-          }
+          const int u0 = 4 * (b & 1);
+          sts128(at + swz(t, u0), lo[0], lo[1], lo[2], lo[3]);
+          sts128(at + swz(t, u0 + 1), lo[4], lo[5], lo[6], lo[7]);
+          sts128(at + swz(t, u0 + 2), hi[0], hi[1], hi[2], hi[3]);
+          sts128(at + swz(t, u0 + 3), hi[4], hi[5], hi[6], hi[7]);
         }
         fence_async_smem();
         __syncwarp();
-        if (lane == 0) arrive_cluster(v_full0 + 8 * buf);
+        if (lane == 0) arrive_cluster(full0 + 8 * buf);
       }
       if (++stage == p.stages) {
         stage = 0;
@@ -841,64 +840,110 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
     // The whole warp runs the loop and one elected lane executes the products: with the
     // control flow uniform the descriptors live in uniform registers
-    if (__shfl_sync(kFull, warp, 0) == kIssueWarp && rank == 0) {
-      constexpr uint32_t idS = idesc_f16(256, 128, false, false);
-      constexpr uint32_t idO = idesc_f16(256, 256, false, true);
-      const uint32_t tm = __shfl_sync(kFull, tmem, 0);
-      const uint64_t dq0 = smem_desc(sb + kQOff, 16, 1024);
-      const uint64_t dk0 = smem_desc(sb + kKOff, 16, 1024);
-      const uint64_t dv0 = smem_desc(sb + kVOff, kVAtom, 1024);
-      const bool leader = elect_one();
-      auto ready = [&](int bar, uint32_t parity) -> bool {
-        return __all_sync(kFull, mbar_wait(bars + 8 * bar, parity, p.wait_ns)) != 0;
-      };
-      auto qk = [&](int buf) {                             // S[buf] = Q K^T
+    if (__shfl_sync(kFull, warp, 0) == kIssueWarp) {
+      if (rank == 0) {
+        constexpr uint32_t idS = idesc_f16(256, 128, false, false);
+        constexpr uint32_t idO = idesc_f16(256, 256, false, true);
+        const uint32_t tm = __shfl_sync(kFull, tmem, 0);
+        const uint64_t dq0 = smem_desc(sb + kQOff, 16, 1024);
+        const uint64_t dk0 = smem_desc(sb + kKOff, 16, 1024);
+        const uint64_t dv0 = smem_desc(sb + kVOff, kVAtom, 1024);
+        const bool leader = elect_one();
+        auto ready = [&](int bar, uint32_t parity) -> bool {
+          return __all_sync(kFull, wait_soon(bars + 8 * bar, parity, p.wait_ns)) != 0;
+        };
+        auto qk = [&](int buf) {                           // S = Q K^T
 #pragma unroll
-        for (int kk = 0; kk < 8; ++kk) {
-          const uint32_t off = (kk & 3) * 32;
-          mma_pair(tm + kSBuf * buf, dq0 + (((kk >> 2) * 16384 + off) >> 4), dk0 + ((buf * kKBuf + (kk >> 2) * 8192 + off) >> 4), idS,
-                   kk ? 1u : 0u);
-        }
-        commit_both(bars + 8 * (kBarSFull + buf));
-      };
-      bool ok = true;
-      for (int i = 0; i < min(2, n_tiles); ++i) {
-        if (!ready(kBarKFull + i, 0)) { ok = false; break; }
-        tc_fence_after();
-        if (leader) qk(i);
-      }
-      for (int i = 0; ok && i < n_tiles; ++i) {
-        const int buf = i & 1;
-        const uint32_t parity = (i >> 1) & 1;
-        if (!ready(kBarVFull + buf, parity) || !ready(kBarPFull + buf, parity)) { ok = false; break; }
-        tc_fence_after();
-        if (leader) {
-          const uint32_t more = i % kChain != 0 ? 1u : 0u;  // O of this chain so far is kept
-          const uint32_t pa = tm + kSBuf * buf;
-          const uint64_t v0 = dv0 + ((buf * kVBuf) >> 4);
-#pragma unroll
-          for (int kk = 0; kk < 8; ++kk)                   // 16 cells = 8 columns of fp16 pairs, two steps to a part's 32 columns
-            mma_pair_ta(tm + kOCol, pa + 32 * (kk >> 1) + 8 * (kk & 1), v0 + ((kk * 2048) >> 4), idO, kk ? 1u : more);
-          commit_both(bars + 8 * (kBarODone + buf));
-        }
-        if (i + 2 < n_tiles) {
-          // QK(i + 2) overwrites P(i)
-          if (!ready(kBarKFull + buf, parity ^ 1) || !ready(kBarODone + buf, parity)) { ok = false; break; }
+          for (int kk = 0; kk < 8; ++kk) {
+            const uint32_t off = (kk & 3) * 32;
+            mma_pair(tm, dq0 + (((kk >> 2) * 16384 + off) >> 4), dk0 + ((buf * kKBuf + (kk >> 2) * 8192 + off) >> 4), idS, kk ? 1u : 0u);
+          }
+          commit_both(bars + 8 * (kBarSFull + buf));
+        };
+        // S runs two tiles ahead of O: it is scored as soon as the rows have the one before in their registers,
+        // so that a group finds its next tile's when it is done with this one's
+        bool ok = true;
+        auto score = [&](int i) {                          // S(i), once S(i - 1) is in the rows' registers
+          if (!ready(kBarKFull + (i & 1), (i >> 1) & 1) || (i > 0 && !ready(kBarSFree, (i - 1) & 1))) {
+            ok = false;
+            return;
+          }
           tc_fence_after();
-          if (leader) qk(buf);
+          if (leader) qk(i & 1);
+        };
+        score(0);
+        if (ok && n_tiles > 1) score(1);
+        for (int i = 0; ok && i < n_tiles; ++i) {
+          const int buf = i & 1;
+          const uint32_t parity = (i >> 1) & 1;
+          if (i + 2 < n_tiles) {
+            score(i + 2);
+            if (!ok) break;
+          }
+          if (!ready(kBarVFull + buf, parity) || !ready(kBarPFull + buf, parity)) { ok = false; break; }
+          tc_fence_after();
+          if (leader) {
+            const uint32_t more = i % kChain != 0 ? 1u : 0u;  // O of this chain so far is kept
+            const uint32_t pa = tm + kPCol + kPBuf * buf;
+            const uint64_t v0 = dv0 + ((buf * kVBuf) >> 4);
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk)                 // 16 cells = 8 columns of fp16 pairs
+              mma_pair_ta(tm + kOCol, pa + 8 * kk, v0 + ((kk * 2048) >> 4), idO, kk ? 1u : more);
+            commit_both(bars + 8 * (kBarODone + buf));
+          }
         }
+        if (!ok) ctl[1] = 1;
+        // all of this warp's products, waited for below (after a failure too)
+        if (leader) commit_both(bars + 8 * kBarDrain);
       }
-      if (!ok) ctl[1] = 1;
-      // all of this warp's products, waited for below (after a failure too)
-      if (leader) commit_both(bars + 8 * kBarDrain);
-    } else if (__shfl_sync(kFull, warp, 0) == kLoadWarp) {
+    } else {
       // ============================================================== copies
-      const bool leader = elect_one();
-      int stage = p.stages > 1 ? 1 : 0, i = 1;
-      uint32_t phase = p.stages > 1 ? 1 : 0;               // of the stage's last use, from its second on
+      // Warp 0 of the three takes the V rows, 1 the V scales, 2 the K rows of this CTA's half and the K scales, a
+      // lane to a copy.  Page ids of four tiles, eight 16-cell groups each (those of the copy that brings the
+      // group), are held one per lane, and those of the next four are on their way.
+      const int which = warp - kLoadWarp0, H = C.H, per = p.box_shift - 4, copies = 8 >> per;   // 1 << per groups a copy
+      auto lookup = [&](int i) -> int {
+        const int c = (tile0 + i + (lane >> 3)) * kTileN + 16 * ((lane & 7) >> per << per);
+        if (i + (lane >> 3) >= n_tiles || c >= limit) return INT32_MIN;   // behind the limit, or another range's
+        const int64_t pidx = p.page_div.div(static_cast<uint32_t>(c));
+        return pidx < p.max_pages ? __ldcg(pt + pidx) : -1;
+      };
+      int page_next = lookup(0), page_mine = 0;
+      int stage = 0, i = 0;
+      uint32_t phase = 1;                                  // of the stage's last use, from its second on
       for (; i < n_tiles; ++i) {
-        if (i >= p.stages && !__all_sync(kFull, mbar_wait(bars + 8 * (kBarRawEmpty + stage), phase, p.wait_ns))) { ctl[1] = 1; break; }
-        load_tile(i, stage, leader);
+        if ((i & 3) == 0) {
+          page_mine = page_next == INT32_MIN || (page_next >= 0 && page_next < C.n_pages) ? page_next : -1;
+          page_next = lookup(i + 4);
+        }
+        if (i >= p.stages && !__all_sync(kFull, wait_soon(bars + 8 * (kBarRawEmpty + stage), phase, p.wait_ns))) { ctl[1] = 1; break; }
+        const uint32_t dst = sb + kRawOff + stage * p.stage_bytes, bar = bars + 8 * (kBarRawFull + stage);
+        const int my_group_page = __shfl_sync(kFull, page_mine, 8 * (i & 3) + (lane & 7));
+        const unsigned good = __ballot_sync(kFull, my_group_page >= 0) & 255u;
+        const unsigned bad = __ballot_sync(kFull, my_group_page == -1) & 255u;
+        if (lane == 0) {
+          if (which == 0) {
+            if (bad) record_status(p.status, K8V4_ERANGE);
+            ctl[8 + stage] = static_cast<int>(good | (bad << 8));
+          }
+          const uint32_t n = __popc(good), nk = __popc((good >> (4 * rank)) & 15u);
+          mbar_expect_tx(bar, which == 0 ? n * 2048u : which == 1 ? n * 256u * H : n * 128u * H + nk * 2048u);
+        }
+        __syncwarp();
+        // lanes 0-7 a run of 1 << per groups each; the K rows lanes 8-11
+        const bool k_rows = which == 2 && lane >= 8;
+        const int q = (k_rows ? 4 * static_cast<int>(rank) + ((lane & 3) << per) : lane << per) & 7;
+        const int page = __shfl_sync(kFull, page_mine, 8 * (i & 3) + q);
+        if (page >= 0 && (k_rows ? lane - 8 < (copies + 1) >> 1 : lane < copies)) {
+          const int cell = (tile0 + i) * kTileN + 16 * q;
+          const int slot = cell - static_cast<int>(p.page_div.div(static_cast<uint32_t>(cell))) * C.P;
+          const uint8_t* pg = C.pages + static_cast<int64_t>(page) * C.page_bytes;
+          if (which == 0) tma_load_4d(dst + kRawV + q * 2048, &tm_v, 0, g, slot, page, bar);
+          else if (which == 1) bulk_load(dst + kRawKs + 1024 * H + q * 256 * H, pg + C.vs_off() + static_cast<int64_t>(slot) * 16 * H, 256 * H << per, bar);
+          else if (k_rows) tma_load_4d(dst + (q & 3) * 2048, &tm_k, 128 * map, g, slot, page, bar);
+          else bulk_load(dst + kRawKs + q * 128 * H, pg + C.ks_off() + static_cast<int64_t>(slot) * 8 * H, 128 * H << per, bar);
+        }
+        __syncwarp();
         if (++stage == p.stages) {
           stage = 0;
           phase ^= 1;
@@ -956,13 +1001,68 @@ int device_pairs() {
   cfg.numAttrs = 1;
   int pairs = 0;
   if (cudaFuncGetAttributes(&fa, diff_pair_kernel) != cudaSuccess ||
-      fa.numRegs * 6 < 4 * kRowRegs + kConvRegs + kIssueRegs ||
+      fa.numRegs * 5 < 2 * kRowRegs + 2 * kConvRegs + kIssueRegs ||
       cudaFuncSetAttribute(diff_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax) != cudaSuccess ||
       cudaOccupancyMaxActiveClusters(&pairs, diff_pair_kernel, &cfg) != cudaSuccess || pairs < 1) {
     cudaGetLastError();                   // clear the error state that the failed call left
     return 0;
   }
   return g_pairs[dev] = pairs;
+}
+// The tensor maps of a cache's K and V rows as the decode's, with boxes of `box` cells; those of
+// the last caches are kept (encoding is host work)
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+  });
+  return fn;
+}
+bool encode_rows(CUtensorMap* m, const CacheView& C, int64_t run_off, int row_bytes, int box) {
+  const auto fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(row_bytes), static_cast<cuuint64_t>(C.H), static_cast<cuuint64_t>(C.P),
+                              static_cast<cuuint64_t>(C.n_pages)};
+  const cuuint64_t strides[3] = {static_cast<cuuint64_t>(row_bytes), static_cast<cuuint64_t>(row_bytes) * C.H,
+                                 static_cast<cuuint64_t>(C.page_bytes)};
+  const cuuint32_t shape[4] = {128, 1, static_cast<cuuint32_t>(box), 1}, one[4] = {1, 1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, C.pages + run_off, dims, strides, shape, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+struct MapEntry {
+  const uint8_t* pages = nullptr;
+  int64_t n_pages = 0;
+  int P = 0, H = 0;
+  CUtensorMap k, v;
+};
+std::mutex g_map_mu;
+MapEntry g_maps[64];
+int g_map_next = 0;
+bool boxed_maps(const CacheView& C, int box, CUtensorMap* k, CUtensorMap* v) {
+  std::lock_guard<std::mutex> lock(g_map_mu);
+  for (const MapEntry& e : g_maps) {
+    if (e.pages == C.pages && e.n_pages == C.n_pages && e.P == C.P && e.H == C.H) {   // the box goes by P
+      *k = e.k;
+      *v = e.v;
+      return true;
+    }
+  }
+  MapEntry& e = g_maps[g_map_next];
+  e.pages = nullptr;
+  if (!encode_rows(&e.k, C, 0, 256, box) || !encode_rows(&e.v, C, C.v_off(), 128, box)) return false;
+  e.pages = C.pages;
+  e.n_pages = C.n_pages;
+  e.P = C.P;
+  e.H = C.H;
+  g_map_next = (g_map_next + 1) % 64;
+  *k = e.k;
+  *v = e.v;
+  return true;
 }
 // the pairs that a workspace and its schedule are sized for: of the device's SMs, the same whether or
 // not the set-up has worked yet
@@ -1007,8 +1107,9 @@ int launch_diff(const Launch& L, const CacheView& C, const void* q, int q_dtype,
   p.page_div = FastDiv(static_cast<uint32_t>(C.P));
   p.stages = raw_stages(C.H);
   p.stage_bytes = raw_bytes(C.H);
+  p.box_shift = C.P % 64 == 0 ? 6 : C.P % 32 == 0 ? 5 : 4;
   CUtensorMap mk, mv;
-  if (!tensor_maps_of(C, &mk, &mv)) return K8V4_ECUDA;
+  if (!boxed_maps(C, 1 << p.box_shift, &mk, &mv)) return K8V4_ECUDA;
   if (2 * sp.most > INT32_MAX) return K8V4_EINVAL;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(2 * sp.most));
