@@ -10,7 +10,7 @@
 // cta_group::2, M = 256, 128 rows per SM) keeps its O in tensor memory and sweeps the range
 // in tiles of 128 cells
 //   S  = Q_m K_m^T        128 lanes, N = 128
-//   P  = 2^(s - ref) 2^4  online softmax in the log2 domain, fp16
+//   P  = 2^(s - ref) 2^2  online softmax in the log2 domain, fp16
 //   O += P V              N = 256, V = RN((n - 8) / 8 d) in fp16
 // and writes its partial rows (o, m, l); the combine joins ranges and maps.  The two maps'
 // units read and convert the same V; a pair that kept both maps of 16 tokens instead would
@@ -29,13 +29,15 @@
 //      warp 16      (leader CTA) issues every product of the pair
 //      warps 17-19  copy the raw tiles (TMA, boxes of 64, 32 or 16 cells as the page size allows; a
 //                   copy takes its warp about 100 clocks to issue, and 16-cell boxes need 28 a tile)
-// The products alternate S(i + 2), O(i): a row's thread takes its 128 scores into registers at
-// once and frees S, P has two buffers of its own, so neither product waits for the other's
-// reader and the tensor pipe is never handed an empty queue by the order of things.
-// The reference maximum of a row moves only when a tile exceeds it by 2^11, and then its O
-// is rescaled in tensor memory, which holds the pair up for about 1,500 clocks (at 2^8 it took a
-// sixth of the time); the two groups hand the reference on from tile to tile.  P is kept
-// 2^4 above it: fp16 drops what is 2^-29 of the reference and less.
+// The issuing warp hands over whichever product is ready, S or O (in a fixed order of the two
+// one waits for the other's reader: 4,096 tokens on 32,768 cells 2.53 ms against 2.03 without
+// any rescaling): a row's thread takes its 128 scores into registers at once and frees S, and P
+// has two buffers of its own.
+// The reference maximum of a row moves only when a tile exceeds it by 2^13, and then its O
+// is rescaled in tensor memory, which holds the pair up for about 1,100 clocks; the two groups
+// hand the reference on from tile to tile.  P is kept 2^2 above it: fp16 drops what is 2^-27 of
+// the reference and less.  (At 2^11 and 2^4 the peaked scores of that case took 2.51 ms, at
+// 2^13 2.34.)
 // Every kChain tiles O is added to a running sum in global memory (the unit's own partial
 // rows serve as its place), because the tensor core's accumulation is not rounded to
 // nearest: measured 2.9e-5 after 2,048 cells in three products each, so about 4e-5 after
@@ -72,7 +74,7 @@ constexpr int kLoadWarps = 3, kThreads = 32 * (kLoadWarp0 + kLoadWarps);
 // the register split waits for whole warpgroups: roles begin at multiples of four warps
 static_assert(kConvWarp0 % 4 == 0 && kIssueWarp % 4 == 0 && kThreads == 32 * (kIssueWarp + 4), "roles");
 constexpr int kChain = 64;                    // tiles accumulated in tensor memory (8,192 cells)
-constexpr float kSlack = 11.0f, kLift = 4.0f; // log2 headroom of P above its row's reference maximum, and what P is lifted by
+constexpr float kSlack = 13.0f, kLift = 2.0f; // log2 headroom of P above its row's reference maximum, and what P is lifted by
 static_assert(kSlack + kLift <= 15.0f, "P in fp16");
 constexpr uint32_t kWaitDefaultNs = 1000000000u;
 // registers per thread after the split (8 row, 8 conversion and 4 other warps), out of those of
@@ -410,6 +412,16 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t v[16]) 
         "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
       : "memory");
 }
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const float v[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};"
+      ::"r"(taddr), "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]), "f"(v[8]), "f"(v[9]),
+        "f"(v[10]), "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15]), "f"(v[16]), "f"(v[17]), "f"(v[18]), "f"(v[19]),
+        "f"(v[20]), "f"(v[21]), "f"(v[22]), "f"(v[23]), "f"(v[24]), "f"(v[25]), "f"(v[26]), "f"(v[27]), "f"(v[28]), "f"(v[29]),
+        "f"(v[30]), "f"(v[31])
+      : "memory");
+}
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 // A word of nibble bytes b0..b3 -> fp16 pairs of V = RN((n - 8) / 8 * d): lo {b0, b2}, {b1, b3} of the
 // low nibbles, hi of the high ones.  0x640n is 1024 + n and 0x64n0 is 1024 + 16 n in fp16;
@@ -574,10 +586,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const float my_f = fsc[row];
     const uint32_t p_full0 = map_to(bars + 8 * kBarPFull, 0), s_free0 = map_to(bars + 8 * kBarSFree, 0);
     const uint32_t refs = bars + 8 * (kBarRef + 2 * (warp & 3));
-    // the running O of this row: float4 number c at acc[128 c] (the block is 128 x 260 floats)
-    float4* const acc = reinterpret_cast<float4*>(block) + row;
-    // l counts relative to 2^l_ref; the running O times acc_scale (kept by the even tiles' group, which folds)
-    float l = 0.0f, l_ref = -INFINITY;
+    // the running O of a row: float4 number c at acc[128 c] of the block (128 x 260 floats)
+    float l = 0.0f, l_ref = -INFINITY;                                 // l counts relative to 2^l_ref
     bool failed = false;
     for (int i = group; i < n_tiles; i += 2) {
       const uint32_t parity = (i >> 1) & 1;
@@ -645,7 +655,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         failed = true;
         break;
       }
-      float2 psum = make_float2(0.0f, 0.0f);
+      float2 psum[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) psum[k] = make_float2(0.0f, 0.0f);
       const uint32_t pcol = tmem + lane_base + kPCol + kPBuf * group;
 #pragma unroll
       for (int h = 0; h < 4; ++h) {
@@ -655,12 +667,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           const float2 e = __ffma2_rn(make_float2(sc[32 * h + 2 * c], sc[32 * h + 2 * c + 1]), f2, mu2);
           const float2 q = make_float2(ex2_ftz(e.x), ex2_ftz(e.y));
           const __half2 hq = __floats2half2_rn(q.x, q.y);
-          psum = __fadd2_rn(psum, q);
+          psum[c & 3] = __fadd2_rn(psum[c & 3], q);
           ph[c] = *reinterpret_cast<const uint32_t*>(&hq);
         }
         tmem_st16(pcol + 16 * h, ph);
       }
-      l += psum.x + psum.y;
+      psum[0] = __fadd2_rn(__fadd2_rn(psum[0], psum[1]), __fadd2_rn(psum[2], psum[3]));
+      l += psum[0].x + psum[0].y;
       // O of the tiles so far: into the running sum at every kChain-th tile (both CTAs), rescaled
       // in place where a reference moved in between
       const bool folds = i > 0 && i % kChain == 0;
@@ -672,30 +685,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         tc_fence_after();
         // the running sum is relative to the reference too: both move
         const bool have = i > kChain;
+        float4* const acc = reinterpret_cast<float4*>(block) + row;
 #pragma unroll 1
-        for (int h = 0; h < 8; ++h) {
-          float o[32];
-          tmem_ld32(tmem + lane_base + kOCol + 32 * h, o);
+        for (int h = 0; h < 2; ++h) {
+          float o[128];                                                // (the scores are done with)
+          tmem_ld128(tmem + lane_base + kOCol + 128 * h, o);
           if (folds) {                                                 // acc = (acc + O) * alpha
 #pragma unroll
-            for (int c = 0; c < 8; ++c) {
-              const float4 old = have ? acc[128 * (8 * h + c)] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-              acc[128 * (8 * h + c)] = make_float4((old.x + o[4 * c]) * alpha, (old.y + o[4 * c + 1]) * alpha,
-                                                   (old.z + o[4 * c + 2]) * alpha, (old.w + o[4 * c + 3]) * alpha);
+            for (int c = 0; c < 32; ++c) {
+              const float4 old = have ? acc[128 * (32 * h + c)] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+              acc[128 * (32 * h + c)] = make_float4((old.x + o[4 * c]) * alpha, (old.y + o[4 * c + 1]) * alpha,
+                                                    (old.z + o[4 * c + 2]) * alpha, (old.w + o[4 * c + 3]) * alpha);
             }
           } else {                                                     // O *= alpha
 #pragma unroll
-            for (int c = 0; c < 32; c += 8) {
-              float x[8];
+            for (int c = 0; c < 128; ++c) o[c] *= alpha;
 #pragma unroll
-              for (int k = 0; k < 8; ++k) x[k] = o[c + k] * alpha;
-              tmem_st8(tmem + lane_base + kOCol + 32 * h + c, x);
-            }
+            for (int c = 0; c < 128; c += 32) tmem_st32(tmem + lane_base + kOCol + 128 * h + c, o + c);
             if (have) {
-#pragma unroll
-              for (int c = 0; c < 8; ++c) {
-                const float4 old = acc[128 * (8 * h + c)];
-                acc[128 * (8 * h + c)] = make_float4(old.x * alpha, old.y * alpha, old.z * alpha, old.w * alpha);
+#pragma unroll 4
+              for (int c = 0; c < 32; ++c) {
+                const float4 old = acc[128 * (32 * h + c)];
+                acc[128 * (32 * h + c)] = make_float4(old.x * alpha, old.y * alpha, old.z * alpha, old.w * alpha);
               }
             }
           }
@@ -717,6 +728,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       sums[group * kRows + row] = l_ref > -INFINITY ? l * exp2f(l_ref - m_run) : 0.0f;
       float* rowbuf = reinterpret_cast<float*>(smem + kQOff);          // [128][256] fp32, rotated by 4 * row
       const bool have = n_tiles > kChain;
+      const float4* const acc = reinterpret_cast<const float4*>(block) + row;
 #pragma unroll 1
       for (int h = 4 * group; h < 4 * group + 4; ++h) {                // 128 of the dims to a group
         float o[32];
@@ -849,9 +861,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const uint64_t dk0 = smem_desc(sb + kKOff, 16, 1024);
         const uint64_t dv0 = smem_desc(sb + kVOff, kVAtom, 1024);
         const bool leader = elect_one();
-        auto ready = [&](int bar, uint32_t parity) -> bool {
-          return __all_sync(kFull, wait_soon(bars + 8 * bar, parity, p.wait_ns)) != 0;
-        };
         auto qk = [&](int buf) {                           // S = Q K^T
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk) {
@@ -860,37 +869,45 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
           commit_both(bars + 8 * (kBarSFull + buf));
         };
-        // S runs two tiles ahead of O: it is scored as soon as the rows have the one before in their registers,
-        // so that a group finds its next tile's when it is done with this one's
+        // Whatever is ready goes out: S(si) once S(si - 1) is in the rows' registers (so that a group finds its next
+        // tile scored when it is done with this one), O(oi) once P and V are there.  A fixed order of the two
+        // holds one back for the other
+        auto test = [&](int bar, uint32_t parity) -> bool { return __all_sync(kFull, mbar_test(bars + 8 * bar, parity)) != 0; };
         bool ok = true;
-        auto score = [&](int i) {                          // S(i), once S(i - 1) is in the rows' registers
-          if (!ready(kBarKFull + (i & 1), (i >> 1) & 1) || (i > 0 && !ready(kBarSFree, (i - 1) & 1))) {
-            ok = false;
-            return;
+        uint64_t since = 0;                                // of a turn with nothing ready; 0: the last one had
+        for (int si = 0, oi = 0; oi < n_tiles;) {
+          bool idle = true;
+          if (si < n_tiles && test(kBarKFull + (si & 1), (si >> 1) & 1) && (si == 0 || test(kBarSFree, (si - 1) & 1))) {
+            tc_fence_after();
+            if (leader) qk(si & 1);
+            ++si;
+            idle = false;
           }
-          tc_fence_after();
-          if (leader) qk(i & 1);
-        };
-        score(0);
-        if (ok && n_tiles > 1) score(1);
-        for (int i = 0; ok && i < n_tiles; ++i) {
-          const int buf = i & 1;
-          const uint32_t parity = (i >> 1) & 1;
-          if (i + 2 < n_tiles) {
-            score(i + 2);
-            if (!ok) break;
-          }
-          if (!ready(kBarVFull + buf, parity) || !ready(kBarPFull + buf, parity)) { ok = false; break; }
-          tc_fence_after();
-          if (leader) {
-            const uint32_t more = i % kChain != 0 ? 1u : 0u;  // O of this chain so far is kept
-            const uint32_t pa = tm + kPCol + kPBuf * buf;
-            const uint64_t v0 = dv0 + ((buf * kVBuf) >> 4);
+          const int buf = oi & 1;
+          const uint32_t parity = (oi >> 1) & 1;
+          if (oi < si && test(kBarVFull + buf, parity) && test(kBarPFull + buf, parity)) {
+            tc_fence_after();
+            if (leader) {
+              const uint32_t more = oi % kChain != 0 ? 1u : 0u;   // O of this chain so far is kept
+              const uint32_t pa = tm + kPCol + kPBuf * buf;
+              const uint64_t v0 = dv0 + ((buf * kVBuf) >> 4);
 #pragma unroll
-            for (int kk = 0; kk < 8; ++kk)                 // 16 cells = 8 columns of fp16 pairs
-              mma_pair_ta(tm + kOCol, pa + 8 * kk, v0 + ((kk * 2048) >> 4), idO, kk ? 1u : more);
-            commit_both(bars + 8 * (kBarODone + buf));
+              for (int kk = 0; kk < 8; ++kk)                 // 16 cells = 8 columns of fp16 pairs
+                mma_pair_ta(tm + kOCol, pa + 8 * kk, v0 + ((kk * 2048) >> 4), idO, kk ? 1u : more);
+              commit_both(bars + 8 * (kBarODone + buf));
+            }
+            ++oi;
+            idle = false;
           }
+          if (!idle) {
+            since = 0;
+            continue;
+          }
+          const uint64_t now = __shfl_sync(kFull, global_ns(), 0);
+          if (since == 0) since = now;
+          if (p.wait_ns < 1000u || now - since >= p.wait_ns) { ok = false; break; }
+          (void)mbar_try(bars + 8 * (kBarPFull + buf), parity, 100u);
+          __syncwarp();
         }
         if (!ok) ctl[1] = 1;
         // all of this warp's products, waited for below (after a failure too)
