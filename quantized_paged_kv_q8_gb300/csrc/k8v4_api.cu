@@ -542,7 +542,7 @@ size_t attn_k8v4_diff_decode_workspace_bytes(const k8v4_cache* cache, int32_t n_
   if (n_seqs < 0 || n_seqs > 65535 || max_seq_len < 0) return 0;
   DeviceState* s = nullptr;
   const int sms = device_state(&s) == K8V4_OK ? s->num_sms : 152;
-  return plan_diff_decode(C, n_seqs, max_seq_len, sms).ws_bytes;
+  return diff_decode_ws_bytes(C, n_seqs, sms);
 }
 
 int attn_k8v4_diff_decode(const k8v4_cache* cache, const void* q, int32_t q_dtype, const int32_t* page_table,
@@ -562,9 +562,8 @@ int attn_k8v4_diff_decode(const k8v4_cache* cache, const void* q, int32_t q_dtyp
   if (!aligned(q, 16) || !aligned(out, 16) || !aligned(workspace, 256) || !aligned(seq_lens, 4)) return K8V4_EALIGN;
   Launch L;
   if ((rc = make_launch(stream, &L))) return rc;
-  const DiffPlan plan = plan_diff_decode(C, n_seqs, max_seq_len, L.num_sms);
-  if (workspace_bytes < plan.ws_bytes) return K8V4_ENOSPACE;
-  return launch_diff_decode(L, C, plan, q, q_dtype, page_table, max_pages, seq_lens, n_seqs, max_seq_len, sm_scale, *diff,
+  if (workspace_bytes < diff_decode_ws_bytes(C, n_seqs, L.num_sms)) return K8V4_ENOSPACE;
+  return launch_diff_decode(L, C, q, q_dtype, page_table, max_pages, seq_lens, n_seqs, max_seq_len, sm_scale, *diff,
                             out, workspace);
 }
 

@@ -15,8 +15,11 @@
 // result, where the plain decode carries both in two terms (48 products of V, not 32, and
 // for one map).
 //
-// The structure is the decode kernel's: a CTA owns a (row, KV head, cell range), its
-// worker warps take the tiles in turn, each with a ring of its own filled by TMA.
+// The worker warps are the decode kernel's: they take a range's tiles in turn, each with a ring of
+// its own filled by TMA.  The ranges are not: the tiles of all (sequence, KV head) pairs, laid
+// end to end, are cut into one equal piece for each SM, so that a ragged batch keeps every SM
+// busy to the end.  A piece covers one pair's cells or the end of one and the beginning of others;
+// each CTA finds its own from the lengths.
 #include <algorithm>
 #include <climits>
 
@@ -29,7 +32,7 @@ namespace {
 
 constexpr unsigned kFull = 0xffffffffu;
 constexpr int kMaxWorkers = 8;                // 255 registers a thread
-constexpr int kStages = 3;
+constexpr int kStages = 2;
 constexpr int kSmemCap = 227 * 1024;
 constexpr uint32_t kWaitDefaultNs = 1000000000u;
 constexpr int kBucketClamp = 1 << 24;
@@ -44,7 +47,7 @@ struct Layout {
   int workers;
   int ksc_bytes, vsc_bytes, ksc_off, vsc_off;       // within a stage: K 4096, V 2048, K scales, V scales
   int stage_bytes, tx_bytes;
-  int q_off, bar_off, total;
+  int q_off, bar_off, ctl_off, total;
 };
 constexpr int kVOff = 4096, kQBytes = 16 * 32 * 8;  // q fragments [16 k-steps][32 lanes][2 words]
 
@@ -59,10 +62,42 @@ inline Layout layout_of(int H) {
   for (L.workers = kMaxWorkers;; --L.workers) {
     L.q_off = L.workers * kStages * L.stage_bytes;
     L.bar_off = L.q_off + kQBytes;
-    L.total = L.bar_off + 8 * kStages * L.workers + 16 + 1024;
+    L.ctl_off = (L.bar_off + 8 * kStages * L.workers + 15) / 16 * 16;   // abort flag, the piece's sequence; sums of the warps
+    L.total = L.ctl_off + 256 + 1024;
     if (L.total <= kSmemCap || L.workers == 1) break;
   }
   return L;
+}
+
+// Places in the workspace: of each pair (sequence, KV head) its first block and their number, then the
+// blocks of 16 partial rows (map, query head).  The piece of CTA c of pair s has block c + s: along
+// the line of tiles a block begins where a piece or a pair does.
+struct Places {
+  int2* pairs;
+  float* rows;
+};
+constexpr int kMostCtas = kDiffMostRanges;
+// What a CTA spends on a pair beside its tiles (query, first copies, the workers' merge), in tiles:
+// each pair's tiles have that much empty line ahead of them, so that a piece with the end of one pair and
+// the beginning of another is as long as the rest (one sequence of 237,568 cells, 2 heads: 64.7 us without)
+constexpr int kPairTiles = 24;
+__device__ __forceinline__ int64_t line_of(int tiles, int H) {         // of a sequence
+  return tiles ? static_cast<int64_t>(H) * (tiles + kPairTiles) : 0;
+}
+// n / d for n, d >= 0, d > 0; the 64-bit routine only where it is needed
+__device__ __forceinline__ int64_t quot(int64_t n, int64_t d) {
+  if ((n | d) < (int64_t(1) << 31)) return static_cast<uint32_t>(n) / static_cast<uint32_t>(d);
+  return n / d;
+}
+
+int ctas_of(int num_sms) { return std::min(num_sms, kMostCtas); }
+size_t place(Places* p, uint8_t* ws, int64_t n_pairs, int ctas) {
+  const size_t head = (static_cast<size_t>(n_pairs) * sizeof(int2) + 255) / 256 * 256;
+  if (p) {
+    p->pairs = reinterpret_cast<int2*>(ws);
+    p->rows = reinterpret_cast<float*>(ws + head);
+  }
+  return head + (static_cast<size_t>(n_pairs) + ctas) * 16 * kDiffRow * sizeof(float);
 }
 
 struct DiffParams {
@@ -71,10 +106,10 @@ struct DiffParams {
   int q_f32;
   const int32_t* pt;
   int64_t max_pages;
-  const int32_t* lens;        // visible cells of each row
-  int max_seq_len, cells_per_split, splits;
+  const int32_t* lens;        // visible cells of each sequence
+  int n_seqs, max_seq_len;
   float sm_scale_log2;
-  float* ws;
+  Places ws;
   int* status;
   uint32_t wait_ns;
   FastDiv page_div;
@@ -152,7 +187,7 @@ __device__ __forceinline__ bool wait_or_abort(uint32_t bar, uint32_t parity, uin
 }
 
 // ---------------------------------------------------------------- the split kernel
-// grid: (splits, KV heads, rows)
+// grid: one CTA per SM
 __global__ void __launch_bounds__(32 * kMaxWorkers, 1)
     diff_split_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const DiffParams p) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -163,7 +198,8 @@ __global__ void __launch_bounds__(32 * kMaxWorkers, 1)
   const int W = blockDim.x >> 5;
   const Layout& LY = p.L;
   const uint32_t full = sb + LY.bar_off + 8 * kStages * w;               // this worker's stage barriers
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + LY.bar_off + 8 * kStages * W);
+  volatile int* ctl = reinterpret_cast<volatile int*>(sm + LY.ctl_off);  // [0] abort flag, [1] the piece's first sequence
+  volatile int* abort_flag = ctl;
   if (threadIdx.x == 0) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_k)) : "memory");
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_v)) : "memory");
@@ -175,33 +211,88 @@ __global__ void __launch_bounds__(32 * kMaxWorkers, 1)
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");
 
-  const int split = blockIdx.x, g = blockIdx.y, row = blockIdx.z;
   const CacheView& C = p.C;
   const int H = C.H, HQ = H * kGqa;
   const int r0 = lane >> 2, c = lane & 3;
-  int n_vis = p.lens[row];
-  if (n_vis < 0 || n_vis > p.max_seq_len) {
-    if (threadIdx.x == 0 && split == 0 && g == 0) record_status(p.status, K8V4_ERANGE);
-    n_vis = n_vis < 0 ? 0 : p.max_seq_len;
-  }
-  const int c_begin = split * p.cells_per_split;
-  const int c_end = min(c_begin + p.cells_per_split, n_vis);
-  const int n_tiles = c_end > c_begin ? (c_end - c_begin + 15) >> 4 : 0;
-  const int n_my = n_tiles > w ? (n_tiles - w + W - 1) / W : 0;          // tiles w + W u
-  const uint32_t ring = sb + w * kStages * LY.stage_bytes;
-  float* const rows = p.ws + (static_cast<int64_t>(row) * H + g) * p.splits * 16 * kDiffRow + static_cast<int64_t>(split) * 16 * kDiffRow;
-  // a range past the row's visible cells only marks its partial rows empty
-  if (n_tiles == 0) {
-    if (threadIdx.x < 16) {
-      rows[threadIdx.x * kDiffRow + 256] = -INFINITY;
-      rows[threadIdx.x * kDiffRow + 257] = 0.0f;
+  auto len_of = [&](int b) { return min(max(p.lens[b], 0), p.max_seq_len); };
+  // ---- this CTA's piece of the line of tiles
+  int b = 0, g = 0;                          // sequence and KV head
+  int64_t pos, end, per;                     // tiles of the line, [pos, end), and of a whole piece
+  int64_t begin_b = 0;                       // the line's tile where sequence b begins
+  {
+    int64_t* sums = reinterpret_cast<int64_t*>(sm + LY.ctl_off + 32);    // of the warps
+    int64_t* found = sums + kMaxWorkers;                                 // where the sequence of pos begins
+    const int per_t = (p.n_seqs + blockDim.x - 1) / blockDim.x;
+    const int s0 = min(p.n_seqs, static_cast<int>(threadIdx.x) * per_t), s1 = min(p.n_seqs, s0 + per_t);
+    int64_t sum = 0;
+    for (int i = s0; i < s1; ++i) {
+      const int n = p.lens[i];
+      if (blockIdx.x == 0 && (n < 0 || n > p.max_seq_len)) record_status(p.status, K8V4_ERANGE);
+      sum += line_of((len_of(i) + 15) >> 4, H);
     }
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    return;
+    int64_t scan = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t u = __shfl_up_sync(kFull, scan, o);
+      if (lane >= o) scan += u;
+    }
+    if (lane == 31) sums[w] = scan;
+    __syncthreads();
+    int64_t total = 0, ahead = scan - sum;
+    for (int i = 0; i < W; ++i) {
+      if (i < w) ahead += sums[i];
+      total += sums[i];
+    }
+    per = max(quot(total + gridDim.x - 1, gridDim.x), static_cast<int64_t>(2 * W));   // at least two tiles a warp
+    pos = min(blockIdx.x * per, total);
+    end = min(pos + per, total);
+    if (pos >= end) {                        // (the whole CTA)
+      asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+      return;
+    }
+    if (ahead <= pos && pos < ahead + sum) {
+      int i = s0;
+      for (;; ++i) {
+        const int64_t n = line_of((len_of(i) + 15) >> 4, H);
+        if (pos < ahead + n) break;
+        ahead += n;
+      }
+      ctl[1] = i;
+      *found = ahead;
+    }
+    __syncthreads();
+    b = ctl[1];
+    begin_b = *found;
+    g = static_cast<int>(quot(pos - begin_b, ((len_of(b) + 15) >> 4) + kPairTiles));
   }
+  int stage = 0;                             // of this worker's next tile, and its phase
+  uint32_t phase = 0;
+  bool aborted = false;                      // this warp left a loop with copies in flight
+  const uint32_t ring = sb + w * kStages * LY.stage_bytes;
+#pragma unroll 1
+  while (pos < end) {
+  // ---- a pair's part of the piece
+  const int n_vis = len_of(b), pair_tiles = (n_vis + 15) >> 4;
+  if (pair_tiles == 0) {                     // a sequence with nothing to see
+    ++b;
+    g = 0;
+    continue;
+  }
+  const int64_t line0 = begin_b + static_cast<int64_t>(g) * (pair_tiles + kPairTiles) + kPairTiles;   // where its tiles begin
+  pos = max(pos, line0);
+  const int n_tiles = static_cast<int>(min(line0 + pair_tiles, end) - pos);
+  if (n_tiles <= 0) break;                   // the piece ends ahead of them
+  const int c_begin = 16 * static_cast<int>(pos - line0), c_end = min(c_begin + 16 * n_tiles, n_vis);
+  const int pair = b * H + g;
+  float* const rows = p.ws.rows + (static_cast<int64_t>(blockIdx.x) + pair) * 16 * kDiffRow;
+  if (pos == line0 && threadIdx.x == 0) {
+    const int first = static_cast<int>(quot(line0, per)), last = static_cast<int>(quot(line0 + pair_tiles - 1, per));
+    p.ws.pairs[pair] = make_int2(first + pair, last - first + 1);
+  }
+  const int n_my = n_tiles > w ? (n_tiles - w + W - 1) / W : 0;          // tiles w + W u
 
-  // ---- this worker's copies: local tile u -> stage u % kStages
-  const int32_t* pt_row = p.pt + static_cast<int64_t>(row) * p.max_pages;
+  // ---- this worker's copies: local tile u -> the ring's next stage
+  const int32_t* pt_row = p.pt + static_cast<int64_t>(b) * p.max_pages;
   int win0 = -1000000, win_page = -1;
   auto page_of = [&](int u) -> int {         // warp-uniform u; all lanes call
     if (u < win0 || u >= win0 + 32) {
@@ -214,9 +305,9 @@ __global__ void __launch_bounds__(32 * kMaxWorkers, 1)
     return (page >= 0 && page < C.n_pages) ? page : -1;
   };
   // an out-of-range page issues no copy; its tile is skipped and recorded
-  auto issue = [&](int u, int stage, int page) {
+  auto issue = [&](int u, int to, int page) {
     if (lane == 0) {
-      const uint32_t st = ring + stage * LY.stage_bytes, bar = full + 8 * stage;
+      const uint32_t st = ring + to * LY.stage_bytes, bar = full + 8 * to;
       if (page >= 0) {
         const int cell0 = c_begin + 16 * (w + W * u);
         const int slot0 = cell0 - static_cast<int>(p.page_div.div(static_cast<uint32_t>(cell0))) * C.P;
@@ -233,16 +324,17 @@ __global__ void __launch_bounds__(32 * kMaxWorkers, 1)
       }
     }
   };
+  const int stage0 = stage;
   int issued = 0;
-  for (; issued < min(kStages, n_my); ++issued) issue(issued, issued, page_of(issued));
+  for (; issued < min(kStages, n_my); ++issued) issue(issued, (stage0 + issued) % kStages, page_of(issued));
 
-  // ---- q fragments (B operand of S^T = K q^T) into shared memory, every warp the same
-  // ones for itself to find: warp 0 writes them.  Lane (r0, c): head r0, dims 64 i + 16 c +
+  // ---- q fragments (B operand of S^T = K q^T) into shared memory: every warp works the factors out
+  // for itself, warp 0 writes the fragments.  Lane (r0, c): head r0, dims 64 i + 16 c +
   // 4 j + e of k-step 4 i + j; k-steps 0..7 are map 0, 8..15 map 1, each with its own
   // power of two
   float f[2][2];                       // score factors: [map][heads 2c, 2c + 1]
   {
-    const int64_t qrow = (static_cast<int64_t>(row) * HQ + g * kGqa + r0) * kD;
+    const int64_t qrow = (static_cast<int64_t>(b) * HQ + g * kGqa + r0) * kD;
 #pragma unroll
     for (int m = 0; m < 2; ++m) {
       float qv[32];
@@ -320,11 +412,9 @@ __global__ void __launch_bounds__(32 * kMaxWorkers, 1)
     for (int mt = 0; mt < 16; ++mt) o[m][mt][0] = o[m][mt][1] = o[m][mt][2] = o[m][mt][3] = 0.0f;
   int M[2][2] = {{INT_MIN, INT_MIN}, {INT_MIN, INT_MIN}};    // running buckets
   float l[2][2] = {{0.0f, 0.0f}, {0.0f, 0.0f}};
-  bool aborted = false;
-  int stage = 0;
-  uint32_t phase = 0;
 
-  for (int u = 0; u < n_my; ++u) {
+  int done = 0;
+  for (int u = 0; u < n_my; ++u, ++done) {
     if (!__all_sync(kFull, wait_or_abort(full + 8 * stage, phase, p.wait_ns, abort_flag))) {
       if (lane == 0) {
         *abort_flag = 1;
@@ -339,14 +429,16 @@ __global__ void __launch_bounds__(32 * kMaxWorkers, 1)
       const int cell0 = c_begin + 16 * (w + W * u);
       const bool vA = cell0 + rowA < c_end, vB = cell0 + rowB < c_end;
       uint32_t ph[2][2];
+      // ---- S_m^T[cell][head] of both maps, two accumulators each
+      float acc[2][2][4];
 #pragma unroll
-      for (int m = 0; m < 2; ++m) {
-        // ---- S_m^T[cell][head], two accumulators
-        float acc[2][4];
+      for (int m = 0; m < 2; ++m)
 #pragma unroll
-        for (int a4 = 0; a4 < 2; ++a4) acc[a4][0] = acc[a4][1] = acc[a4][2] = acc[a4][3] = 0.0f;
+        for (int a4 = 0; a4 < 2; ++a4) acc[m][a4][0] = acc[m][a4][1] = acc[m][a4][2] = acc[m][a4][3] = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
+      for (int i = 0; i < 2; ++i) {
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
           const uint4 ka = lds128(st + 2048 * m + offA[i]);
           const uint4 kb = lds128(st + 2048 * m + offB[i]);
           const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
@@ -356,19 +448,26 @@ __global__ void __launch_bounds__(32 * kMaxWorkers, 1)
             i8x4_to_f16(wa[j], a[0], a[2]);
             i8x4_to_f16(wb[j], a[1], a[3]);
             const uint2 qb = lds64(qf + (8 * m + 4 * i + j) * 256);
-            mma16(acc[j & 1], a, qb.x, qb.y);
+            mma16(acc[m][j & 1], a, qb.x, qb.y);
           }
         }
+      }
+      float sc[2][4];
+      bool up = false;
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
         const float kA = __uint_as_float(m ? kAu.y : kAu.x), kB = __uint_as_float(m ? kBu.y : kBu.x);
-        float sc[4];
-        sc[0] = vA ? kA * (acc[0][0] + acc[1][0]) * f[m][0] : -INFINITY;
-        sc[1] = vA ? kA * (acc[0][1] + acc[1][1]) * f[m][1] : -INFINITY;
-        sc[2] = vB ? kB * (acc[0][2] + acc[1][2]) * f[m][0] : -INFINITY;
-        sc[3] = vB ? kB * (acc[0][3] + acc[1][3]) * f[m][1] : -INFINITY;
-        // ---- softmax against the running bucket of each head (the decode kernel's)
-        const bool up0 = sc[0] > 8.0f * M[m][0] || sc[2] > 8.0f * M[m][0], up1 = sc[1] > 8.0f * M[m][1] || sc[3] > 8.0f * M[m][1];
-        if (__any_sync(kFull, up0 || up1)) {
-          float t0 = fmaxf(sc[0], sc[2]), t1 = fmaxf(sc[1], sc[3]);
+        sc[m][0] = vA ? kA * (acc[m][0][0] + acc[m][1][0]) * f[m][0] : -INFINITY;
+        sc[m][1] = vA ? kA * (acc[m][0][1] + acc[m][1][1]) * f[m][1] : -INFINITY;
+        sc[m][2] = vB ? kB * (acc[m][0][2] + acc[m][1][2]) * f[m][0] : -INFINITY;
+        sc[m][3] = vB ? kB * (acc[m][0][3] + acc[m][1][3]) * f[m][1] : -INFINITY;
+        up = up || sc[m][0] > 8.0f * M[m][0] || sc[m][2] > 8.0f * M[m][0] || sc[m][1] > 8.0f * M[m][1] || sc[m][3] > 8.0f * M[m][1];
+      }
+      // ---- softmax against the running bucket of each head (the decode kernel's), both maps at a time
+      if (__any_sync(kFull, up)) {
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+          float t0 = fmaxf(sc[m][0], sc[m][2]), t1 = fmaxf(sc[m][1], sc[m][3]);
 #pragma unroll
           for (int off = 4; off < 32; off <<= 1) {
             t0 = fmaxf(t0, __shfl_xor_sync(kFull, t0, off));
@@ -388,9 +487,12 @@ __global__ void __launch_bounds__(32 * kMaxWorkers, 1)
           M[m][0] = nb0;
           M[m][1] = nb1;
         }
+      }
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
         const float rf0 = static_cast<float>(8 * M[m][0] - 14), rf1 = static_cast<float>(8 * M[m][1] - 14);
-        const float p0 = ex2_ftz(sc[0] - rf0), p1 = ex2_ftz(sc[1] - rf1);      // p' = 2^(s - ref + 14) <= 2^14
-        const float p2 = ex2_ftz(sc[2] - rf0), p3 = ex2_ftz(sc[3] - rf1);
+        const float p0 = ex2_ftz(sc[m][0] - rf0), p1 = ex2_ftz(sc[m][1] - rf1);      // p' = 2^(s - ref + 14) <= 2^14
+        const float p2 = ex2_ftz(sc[m][2] - rf0), p3 = ex2_ftz(sc[m][3] - rf1);
         l[m][0] += p0 + p2;
         l[m][1] += p1 + p3;
         // to the B layout (head r0; cells 2c, 2c+1 | 2c+8, 2c+9)
@@ -441,11 +543,13 @@ __global__ void __launch_bounds__(32 * kMaxWorkers, 1)
   }
 
   // ---------------------------------------------------------------- epilogue
-  // a worker that left early first waits (bounded) for its copies in flight
+  // a worker that left early first waits (bounded) for its copies in flight: the stages from its next one on
   if (aborted && lane == 0) {
-    for (int u = max(0, issued - kStages); u < issued; ++u) {
+    const int left = issued - done;
+    for (int k = 0; k < left; ++k) {
+      const uint32_t ph = stage + k >= kStages ? phase ^ 1 : phase;
       const uint64_t t0 = global_ns();
-      while (!mbar_try(full + 8 * (u % kStages), (u / kStages) & 1, 20000u) && global_ns() - t0 < kWaitDefaultNs) {
+      while (!mbar_try(full + 8 * ((stage + k) % kStages), ph, 20000u) && global_ns() - t0 < kWaitDefaultNs) {
       }
     }
   }
@@ -501,7 +605,43 @@ __global__ void __launch_bounds__(32 * kMaxWorkers, 1)
       dst[257] = Ls * (1.0f / 16384.0f);
     }
   }
+  // the next pair's copies overwrite what the workers wrote and the merge read; after a failure the CTA leaves (its
+  // other pieces' rows would be older ones: their blocks are marked empty)
+  fence_async_smem();
   __syncthreads();
+  pos += n_tiles;
+  if (++g == H) {
+    g = 0;
+    begin_b += line_of(pair_tiles, H);
+    ++b;
+  }
+  if (*abort_flag) break;
+  }
+#pragma unroll 1
+  while (pos < end) {                        // (only after a failure)
+    const int pair_tiles = (len_of(b) + 15) >> 4;
+    if (pair_tiles) {
+      const int64_t line0 = begin_b + static_cast<int64_t>(g) * (pair_tiles + kPairTiles) + kPairTiles;
+      const int pair = b * H + g;
+      pos = max(pos, line0);
+      if (pos >= end) break;
+      float* const rows = p.ws.rows + (static_cast<int64_t>(blockIdx.x) + pair) * 16 * kDiffRow;
+      if (threadIdx.x < 16) {
+        rows[threadIdx.x * kDiffRow + 256] = -INFINITY;
+        rows[threadIdx.x * kDiffRow + 257] = 0.0f;
+      }
+      if (pos == line0 && threadIdx.x == 0) {
+        const int first = static_cast<int>(quot(line0, per)), last = static_cast<int>(quot(line0 + pair_tiles - 1, per));
+        p.ws.pairs[pair] = make_int2(first + pair, last - first + 1);
+      }
+      pos = min(line0 + pair_tiles, end);
+    }
+    if (pair_tiles == 0 || ++g == H) {
+      g = 0;
+      begin_b += line_of(pair_tiles, H);
+      ++b;
+    }
+  }
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
@@ -509,12 +649,13 @@ __global__ void __launch_bounds__(32 * kMaxWorkers, 1)
 struct CombineParams {
   const float* ws;
   DiffRagged r;               // a ragged batch's rows
-  int splits;                 // else: ranges of every row
+  const int2* pairs;          // else: the first block and their number of each (sequence, KV head)
+  const int32_t* lens;        // and the cells that a sequence sees
   int H, n_rows;              // rows: (sequence or token, query head)
   k8v4_diff d;
   uint16_t* out;
 };
-constexpr int kCombineWarps = 4;
+constexpr int kCombineThreads = 128;        // or 32 WARPS, where a row takes more
 
 // the first warps of a row: exp(q1 . k1) and exp(q2 . k2) of its head (0 without vectors)
 __device__ __forceinline__ float lambda_term(const k8v4_diff& d, int hq, int term, int lane) {
@@ -577,12 +718,12 @@ __device__ __forceinline__ void finish_row(float v[8], const k8v4_diff& d, int l
   dst[32 + lane] = make_uint2(two(v[4], v[5]), two(v[6], v[7]));
 }
 
-// WARPS to a (row, query head), rows of 4 / WARPS a CTA: four warps where a row has tens of
-// ranges, one where thousands of rows have a few each.
+// WARPS to a (row, query head): sixteen where a few rows have tens of ranges each (one sequence of
+// 237,568 cells: 16 rows of 76), one where there are thousands of rows of a few.
 template <int WARPS, bool RAGGED>
-__global__ void __launch_bounds__(32 * kCombineWarps) diff_combine_kernel(const CombineParams p) {
-  constexpr int kRowsCta = kCombineWarps / WARPS;
-  constexpr int kMost = RAGGED ? kDiffMostRanges : kDecodeMaxSplits;
+__global__ void __launch_bounds__(WARPS > 4 ? 32 * WARPS : kCombineThreads, WARPS == 1 ? 10 : 1) diff_combine_kernel(const CombineParams p) {
+  constexpr int kRowsCta = WARPS > 4 ? 1 : kCombineThreads / 32 / WARPS;
+  constexpr int kMost = kDiffMostRanges;
   __shared__ float wt[kRowsCta][2][kMost];
   __shared__ float red[kRowsCta][2][2][WARPS];
   __shared__ float4 part[WARPS > 1 ? kRowsCta : 1][2][WARPS][64];
@@ -608,15 +749,42 @@ __global__ void __launch_bounds__(32 * kCombineWarps) diff_combine_kernel(const 
     m_stride = s_stride * splits;
     base = p.ws + (static_cast<int64_t>(tile[4]) + 2 * g * splits) * s_stride + ((row - tile[1]) * kGqa + h) * kDiffRow;
   } else {
-    splits = p.splits;
+    const int len = p.lens[row];
+    int2 at = p.pairs[row * p.H + g];                   // not written where there is nothing to see
+    if (len <= 0) at = make_int2(0, 0);
+    splits = min(at.y, kMost);
     m_stride = kGqa * kDiffRow;
     s_stride = 2 * m_stride;
-    base = p.ws + (static_cast<int64_t>(row) * p.H + g) * splits * s_stride + h * kDiffRow;
+    base = p.ws + at.x * s_stride + h * kDiffRow;
   }
   auto sync = [] {
     if (WARPS == 1) __syncwarp();
     else __syncthreads();
   };
+  // one range, as most rows of a long batch have: no weights to work out, every load at once
+  if (WARPS == 1 && splits == 1) {
+    float4 x[2][2];
+    float l[2];
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+      const float4* src = reinterpret_cast<const float4*>(base + m * m_stride);
+      x[m][0] = __ldcs(src + lane);
+      x[m][1] = __ldcs(src + 32 + lane);
+      l[m] = base[m * m_stride + 257];
+    }
+    const float t0 = lambda_term(p.d, hq, 0, lane), t1 = lambda_term(p.d, hq, 1, lane);
+    const float lambda = p.d.lambda_q1 ? t0 - t1 + p.d.lambda_init : p.d.lambda_init;
+    const float f0 = l[0] > 0.0f ? 1.0f / l[0] : 0.0f, f1 = l[1] > 0.0f ? -lambda / l[1] : 0.0f;
+    // (what a range in which the row sees nothing left in o counts with 0)
+    float v[8];
+    auto join = [&](float a, float b) { return (f0 != 0.0f ? a * f0 : 0.0f) + (f1 != 0.0f ? b * f1 : 0.0f); };
+    v[0] = join(x[0][0].x, x[1][0].x); v[1] = join(x[0][0].y, x[1][0].y);
+    v[2] = join(x[0][0].z, x[1][0].z); v[3] = join(x[0][0].w, x[1][0].w);
+    v[4] = join(x[0][1].x, x[1][1].x); v[5] = join(x[0][1].y, x[1][1].y);
+    v[6] = join(x[0][1].z, x[1][1].z); v[7] = join(x[0][1].w, x[1][1].w);
+    finish_row(v, p.d, lane, p.out + static_cast<int64_t>(rr) * kD);
+    return;
+  }
   float Mx[2], L[2];
 #pragma unroll
   for (int m = 0; m < 2; ++m) {
@@ -719,29 +887,8 @@ bool diff_supported(const CacheView& C) {
   return C.fmt == K8V4_FORMAT_K8V4 && C.n_pages < (int64_t(1) << 31) && C.page_bytes < (int64_t(1) << 39);
 }
 
-DiffPlan plan_diff_decode(const CacheView& C, int n_seqs, int max_seq_len, int num_sms) {
-  DiffPlan pl;
-  const int tiles = std::max(1, (max_seq_len + 15) / 16);
-  const int64_t pairs = static_cast<int64_t>(C.H) * n_seqs;
-  // the split count that minimises waves x (tiles per range + a CTA's fixed cost), each
-  // range keeping at least 2 tiles per worker warp, as the plain decode's plan
-  constexpr int kCtaFixedTiles = 32;
-  const int max_splits = std::max(1, std::min(kDecodeMaxSplits, tiles / (2 * kMaxWorkers)));
-  int64_t best_cost = INT64_MAX;
-  int best = 1;
-  for (int sp = 1; sp <= max_splits; ++sp) {
-    const int64_t waves = (pairs * sp + num_sms - 1) / num_sms;
-    const int64_t cost = waves * ((tiles + sp - 1) / sp + kCtaFixedTiles);
-    if (cost < best_cost) {
-      best_cost = cost;
-      best = sp;
-    }
-  }
-  const int tps = (tiles + best - 1) / best;
-  pl.cells_per_split = 16 * tps;
-  pl.splits = (tiles + tps - 1) / tps;
-  pl.ws_bytes = static_cast<size_t>(n_seqs) * pl.splits * C.H * 16 * kDiffRow * sizeof(float);
-  return pl;
+size_t diff_decode_ws_bytes(const CacheView& C, int n_seqs, int num_sms) {
+  return place(nullptr, nullptr, static_cast<int64_t>(n_seqs) * C.H, ctas_of(num_sms));
 }
 
 int launch_diff_combine_ragged(const Launch& L, const float* ws, const DiffRagged& r, int n_tok, int H, bool wide,
@@ -749,18 +896,19 @@ int launch_diff_combine_ragged(const Launch& L, const float* ws, const DiffRagge
   CombineParams p;
   p.ws = ws;
   p.r = r;
-  p.splits = 0;
+  p.pairs = nullptr;
+  p.lens = nullptr;
   p.H = H;
   p.n_rows = n_tok * H * kGqa;                          // below 2^30
   p.d = diff;
   p.out = static_cast<uint16_t*>(out);
-  if (wide) return launch_behind(L, diff_combine_kernel<4, true>, dim3(p.n_rows), dim3(32 * kCombineWarps), p);
-  return launch_behind(L, diff_combine_kernel<1, true>, dim3((p.n_rows + kCombineWarps - 1) / kCombineWarps), dim3(32 * kCombineWarps), p);
+  if (wide) return launch_behind(L, diff_combine_kernel<16, true>, dim3(p.n_rows), dim3(512), p);
+  return launch_behind(L, diff_combine_kernel<1, true>, dim3((p.n_rows + 3) / 4), dim3(kCombineThreads), p);
 }
 
-int launch_diff_decode(const Launch& L, const CacheView& C, const DiffPlan& plan, const void* q, int q_dtype,
-                       const int32_t* pt, int64_t max_pages, const int32_t* lens, int n_seqs, int max_seq_len,
-                       float sm_scale, const k8v4_diff& diff, void* out, void* ws) {
+int launch_diff_decode(const Launch& L, const CacheView& C, const void* q, int q_dtype, const int32_t* pt, int64_t max_pages,
+                       const int32_t* lens, int n_seqs, int max_seq_len, float sm_scale, const k8v4_diff& diff, void* out,
+                       void* ws) {
   DiffParams p;
   p.C = C;
   p.q = q;
@@ -768,11 +916,11 @@ int launch_diff_decode(const Launch& L, const CacheView& C, const DiffPlan& plan
   p.pt = pt;
   p.max_pages = max_pages;
   p.lens = lens;
+  p.n_seqs = n_seqs;
   p.max_seq_len = max_seq_len;
-  p.cells_per_split = plan.cells_per_split;
-  p.splits = plan.splits;
   p.sm_scale_log2 = sm_scale * 1.4426950408889634f;
-  p.ws = static_cast<float*>(ws);
+  const int ctas = ctas_of(L.num_sms);
+  place(&p.ws, static_cast<uint8_t*>(ws), static_cast<int64_t>(n_seqs) * C.H, ctas);
   p.status = L.status;
   p.wait_ns = wait_limit_ns() ? wait_limit_ns() : kWaitDefaultNs;
   p.page_div = FastDiv(static_cast<uint32_t>(C.P));
@@ -783,7 +931,7 @@ int launch_diff_decode(const Launch& L, const CacheView& C, const DiffPlan& plan
       cudaFuncSetAttribute(diff_split_kernel, cudaFuncAttributePreferredSharedMemoryCarveout, 100) != cudaSuccess)
     return K8V4_ECUDA;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(p.splits, C.H, n_seqs);
+  cfg.gridDim = dim3(ctas);
   cfg.blockDim = dim3(32 * p.L.workers);
   cfg.dynamicSmemBytes = p.L.total;
   cfg.stream = L.stream;
@@ -795,14 +943,17 @@ int launch_diff_decode(const Launch& L, const CacheView& C, const DiffPlan& plan
   if (cudaLaunchKernelEx(&cfg, diff_split_kernel, mk, mv, p) != cudaSuccess) return K8V4_ECUDA;
   if (cudaGetLastError() != cudaSuccess) return K8V4_ECUDA;
   CombineParams c;
-  c.ws = p.ws;
+  c.ws = p.ws.rows;
   c.r = DiffRagged{nullptr, nullptr};
-  c.splits = p.splits;
+  c.pairs = p.ws.pairs;
+  c.lens = lens;
   c.H = C.H;
   c.n_rows = n_seqs * C.H * kGqa;
   c.d = diff;
   c.out = static_cast<uint16_t*>(out);
-  return launch_behind(L, diff_combine_kernel<4, false>, dim3(c.n_rows), dim3(32 * kCombineWarps), c);
+  // the pieces are one to an SM: few pairs have many each
+  if (n_seqs * C.H * 8 <= ctas) return launch_behind(L, diff_combine_kernel<16, false>, dim3(c.n_rows), dim3(512), c);
+  return launch_behind(L, diff_combine_kernel<4, false>, dim3(c.n_rows), dim3(kCombineThreads), c);
 }
 
 }  // namespace k8v4

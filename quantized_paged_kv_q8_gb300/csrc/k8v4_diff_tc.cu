@@ -113,7 +113,12 @@ constexpr uint32_t kTmemCols = 512, kPCol = 128, kPBuf = 64, kOCol = 256;
 constexpr int kTileTok = 32;                  // tokens of a token tile
 constexpr int kMostWaves = 4;                 // ranges: at most this many per pair of the device, on average
 struct TokenTile {
-  int seq, tok0, n, splits, first, cell_tiles, per_split, vis0;   // vis0: cells that its first token sees (causal)
+  int seq, tok0, n, splits, first, cell_tiles, vis0, most;   // vis0: cells that its first token sees (causal), or the steps' bound
+};
+// what a CTA pair needs to know, in one read: its tokens, its cell tiles [tile0, tile0 + n_tiles), the cells that any of its
+// rows sees, and which map (bit 0) of which KV head
+struct Unit {
+  int seq, tok0, n, vis0, tile0, n_tiles, limit, what;
 };
 
 struct Schedule {                             // places in the workspace
@@ -121,7 +126,7 @@ struct Schedule {                             // places in the workspace
   int32_t* tile_end;                          // [n_seqs] token tiles up to each sequence
   TokenTile* tiles;
   int32_t* tok_tile;                          // [n_tok], -1: no sequence
-  int2* units;                                // {token tile, (split << 4) | (KV head << 1) | map}
+  Unit* units;
   float* rows;                                // partial blocks of 256 rows
 };
 int64_t most_tiles(int n_seqs, int n_tok) { return n_tok / kTileTok + std::min(n_seqs, n_tok); }
@@ -142,7 +147,7 @@ size_t place(Schedule* s, uint8_t* ws, int n_seqs, int n_tok, int max_seq_len, i
   t.tile_end = reinterpret_cast<int32_t*>(take(4 * static_cast<size_t>(n_seqs)));
   t.tiles = reinterpret_cast<TokenTile*>(take(sizeof(TokenTile) * tiles));
   t.tok_tile = reinterpret_cast<int32_t*>(take(4 * static_cast<size_t>(n_tok)));
-  t.units = reinterpret_cast<int2*>(take(8 * units));
+  t.units = reinterpret_cast<Unit*>(take(sizeof(Unit) * units));
   t.rows = reinterpret_cast<float*>(take(static_cast<size_t>(units) * 2 * kRows * kDiffRow * sizeof(float)));
   if (s) *s = t;
   return at;
@@ -181,11 +186,15 @@ __device__ __forceinline__ int scan_block(int v, int* red, int* total) {   // 1,
 }
 
 // One CTA.  Token tiles of each sequence, the last first (it sees the most cells); the range
-// length that keeps the pairs of the device evenly loaded; the units in the tiles' order.
+// length that keeps the pairs of the device evenly loaded; the units in the tiles' order.  What
+// is searched and counted stays in shared memory while the lists are short (a search of a
+// list in global memory is a chain of reads of 300 ns each).
+constexpr int kShortList = 4096;
 __global__ void __launch_bounds__(1024, 1) diff_schedule_kernel(const ScheduleParams p) {
   __shared__ int red[32];
   __shared__ float cost_s[32];
   __shared__ int top_s;
+  __shared__ int ends_s[kShortList], cells_s[kShortList];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -193,6 +202,7 @@ __global__ void __launch_bounds__(1024, 1) diff_schedule_kernel(const SchedulePa
   if (tid == 0) top_s = 0;
   for (int t = tid; t < p.n_tok; t += 1024) s.tok_tile[t] = -1;
   // ---- token tiles of the sequences
+  int* const ends = p.n_seqs <= kShortList ? ends_s : s.tile_end;
   const int per = (p.n_seqs + 1023) / 1024;
   const int b0 = min(p.n_seqs, tid * per), b1 = min(p.n_seqs, b0 + per);
   auto tokens_of = [&](int b, int& first) {
@@ -206,13 +216,10 @@ __global__ void __launch_bounds__(1024, 1) diff_schedule_kernel(const SchedulePa
     const int n = tokens_of(b, first);
     if (n < 0) record_status(p.status, K8V4_ERANGE);
     sum += (max(n, 0) + kTileTok - 1) / kTileTok;
+    ends[b] = sum;                                             // of this thread's sequences so far
   }
-  int at = scan_block(sum, red, &n_tiles);
-  for (int b = b0; b < b1; ++b) {
-    int first;
-    at += (max(tokens_of(b, first), 0) + kTileTok - 1) / kTileTok;
-    s.tile_end[b] = at;
-  }
+  const int at = scan_block(sum, red, &n_tiles);
+  for (int b = b0; b < b1; ++b) ends[b] += at;
   // offsets that do not follow one another can claim more tiles than there is room for
   if (n_tiles > p.n_tok / kTileTok + min(p.n_seqs, p.n_tok)) {
     if (tid == 0) record_status(p.status, K8V4_ERANGE);
@@ -220,19 +227,20 @@ __global__ void __launch_bounds__(1024, 1) diff_schedule_kernel(const SchedulePa
   }
   __syncthreads();
   // ---- each tile's tokens and cells
+  const bool brief = n_tiles <= kShortList;
   int cells = 0, top = 0;
   for (int i = tid; i < n_tiles; i += 1024) {
     int lo = 0, hi = p.n_seqs - 1;
     while (lo < hi) {
       const int mid = (lo + hi) >> 1;
-      if (s.tile_end[mid] > i) hi = mid;
+      if (ends[mid] > i) hi = mid;
       else lo = mid + 1;
     }
     TokenTile t;
     t.seq = lo;
     int first;
     const int n = tokens_of(lo, first);
-    const int j = s.tile_end[lo] - 1 - i;                      // the last tile first
+    const int j = ends[lo] - 1 - i;                            // the last tile first
     t.tok0 = first + j * kTileTok;
     t.n = min(kTileTok, n - j * kTileTok);
     int len = p.lens[lo];
@@ -249,11 +257,13 @@ __global__ void __launch_bounds__(1024, 1) diff_schedule_kernel(const SchedulePa
         if (v < 0 || v > len) record_status(p.status, K8V4_ERANGE);
         most = max(most, min(v, len));
       }
-      t.vis0 = len;                                            // the bound of the steps
+      t.vis0 = len;
     }
     t.cell_tiles = (most + kTileN - 1) / kTileN;
-    t.splits = t.first = t.per_split = 0;
+    t.splits = t.first = 0;
+    t.most = most;
     s.tiles[i] = t;
+    if (brief) cells_s[i] = t.cell_tiles;
     for (int k = 0; k < t.n; ++k) s.tok_tile[t.tok0 + k] = i;
     cells += t.cell_tiles;
     top = max(top, t.cell_tiles);
@@ -268,34 +278,37 @@ __global__ void __launch_bounds__(1024, 1) diff_schedule_kernel(const SchedulePa
   // cut at all, each worked out by a warp: rounds x (range + a unit's fixed cost)
   const float units_per = 2.0f * p.H;
   const int least = max(1, min(top, static_cast<int>(ceilf(units_per * total / (static_cast<float>(kMostWaves) * p.pairs)))));
-  constexpr float kFixedTiles = 6.0f;
-  const int cand = max(least, min(top, static_cast<int>(ceilf(least * exp2f(log2f(static_cast<float>(top) / least) * warp / 31.0f)))));
-  int units = 0;
-  const bool many = n_tiles > 4096;                            // long lists are not cut
-  if (!many)
-    for (int i = lane; i < n_tiles; i += 32) units += (s.tiles[i].cell_tiles + cand - 1) / cand;
-  units = __reduce_add_sync(kFull, units);
-  if (lane == 0) cost_s[warp] = ceilf(units * units_per / p.pairs) * (cand + kFixedTiles);
-  __syncthreads();
-  float best = cost_s[lane];
+  constexpr float kFixedTiles = 8.0f;
+  auto candidate = [&](int k) {
+    return max(least, min(top, static_cast<int>(ceilf(least * exp2f(log2f(static_cast<float>(top) / least) * k / 31.0f)))));
+  };
+  int range = top;
+  if (brief) {                                                 // long lists are not cut
+    const int cand = candidate(warp);
+    int units = 0;
+    for (int i = lane; i < n_tiles; i += 32) units += (cells_s[i] + cand - 1) / cand;
+    units = __reduce_add_sync(kFull, units);
+    if (lane == 0) cost_s[warp] = ceilf(units * units_per / p.pairs) * (cand + kFixedTiles);
+    __syncthreads();
+    float best = cost_s[lane];
 #pragma unroll
-  for (int o = 16; o >= 1; o >>= 1) best = fminf(best, __shfl_xor_sync(kFull, best, o));
-  const int pick = 31 - __clz(__ballot_sync(kFull, cost_s[lane] == best));
-  const int range = many ? top : max(least, min(top, static_cast<int>(ceilf(least * exp2f(log2f(static_cast<float>(top) / least) * pick / 31.0f)))));
+    for (int o = 16; o >= 1; o >>= 1) best = fminf(best, __shfl_xor_sync(kFull, best, o));
+    range = candidate(31 - __clz(__ballot_sync(kFull, cost_s[lane] == best)));
+  }
   // ---- the units
   const int tiles_per = (n_tiles + 1023) / 1024;
   const int i0 = min(n_tiles, tid * tiles_per), i1 = min(n_tiles, i0 + tiles_per);
   int mine = 0, all;
-  for (int i = i0; i < i1; ++i) mine += (s.tiles[i].cell_tiles + range - 1) / range * 2 * p.H;
+  for (int i = i0; i < i1; ++i) mine += ((brief ? cells_s[i] : s.tiles[i].cell_tiles) + range - 1) / range * 2 * p.H;
   int u = scan_block(mine, red, &all);
   for (int i = i0; i < i1; ++i) {
-    const int ct = s.tiles[i].cell_tiles, sp = (ct + range - 1) / range;
+    const TokenTile t = s.tiles[i];
+    const int sp = (t.cell_tiles + range - 1) / range, len = sp ? (t.cell_tiles + sp - 1) / sp : 0;
     s.tiles[i].splits = sp;
     s.tiles[i].first = u;
-    s.tiles[i].per_split = sp ? (ct + sp - 1) / sp : 0;
     for (int k = 0; k < 2 * p.H; ++k)
       for (int c = 0; c < sp; ++c, ++u)
-        if (u < p.most) s.units[u] = make_int2(i, c << 4 | k);
+        if (u < p.most) s.units[u] = Unit{t.seq, t.tok0, t.n, t.vis0, c * len, min(len, t.cell_tiles - c * len), t.most, k};
   }
   if (tid == 0) {
     s.head[0] = static_cast<int>(min(static_cast<int64_t>(all), p.most));
@@ -482,22 +495,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int unit = blockIdx.x >> 1;
+  const int4* src = reinterpret_cast<const int4*>(p.s.units + unit);
+  const int4 ua = __ldcg(src), ub = __ldcg(src + 1);                     // (read beside the count: one latency)
   if (unit >= __ldcg(p.s.head)) return;                                  // both CTAs of the pair
-  const int2 what = __ldcg(p.s.units + unit);
-  const int map = what.y & 1, g = (what.y >> 1) & 7, split = what.y >> 4;
-  TokenTile tt;
-  {
-    const int4* src = reinterpret_cast<const int4*>(p.s.tiles + what.x);
-    const int4 a = __ldcg(src), b = __ldcg(src + 1);
-    tt = TokenTile{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-  }
-  const int tile0 = split * tt.per_split;
-  const int n_tiles = min(tt.per_split, tt.cell_tiles - tile0);          // >= 1
-  const int tok_first = tt.tok0 + 16 * static_cast<int>(rank);           // this CTA's tokens
-  const int tok_n = max(0, min(16, tt.n - 16 * static_cast<int>(rank)));
-  const int32_t* pt = p.pt + static_cast<int64_t>(tt.seq) * p.max_pages;
-  // cells that any row of the pair sees (those behind are neither looked up nor read)
-  const int limit = p.steps ? min(tt.cell_tiles * kTileN, tt.vis0) : tt.vis0 + tt.n - 1;
+  const int seq = ua.x, tok0 = ua.y, vis0 = ua.w, tile0 = ub.x, n_tiles = ub.y;   // n_tiles >= 1
+  const int limit = ub.z;                                                // cells that any row of the pair sees (those behind are neither looked up nor read)
+  const int map = ub.w & 1, g = ub.w >> 1;
+  const int tok_first = tok0 + 16 * static_cast<int>(rank);              // this CTA's tokens
+  const int tok_n = max(0, min(16, ua.z - 16 * static_cast<int>(rank)));
+  const int32_t* pt = p.pt + static_cast<int64_t>(seq) * p.max_pages;
 
   if (warp == kLoadWarp0) {
     int count = 0;
@@ -520,11 +526,64 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   }
   if (warp == kIssueWarp) tmem_alloc_pair(sb + kCtlOff, kTmemCols);
 
+  // ---- the load warps' copies of tile i into a stage.  Warp 0 of the three takes the V rows, 1 the V scales, 2 the K rows of
+  // this CTA's half and the K scales, a lane to a copy.  Page ids of four tiles, eight 16-cell groups each (those of the
+  // copy that brings the group), are held one per lane, and those of the next four are on their way.
+  const int which = warp - kLoadWarp0, per = p.box_shift - 4, copies = 8 >> per;   // 1 << per groups a copy
+  int page_next = 0, page_mine = 0;
+  auto lookup = [&](int i) -> int {
+    const int c = (tile0 + i + (lane >> 3)) * kTileN + 16 * ((lane & 7) >> per << per);
+    if (i + (lane >> 3) >= n_tiles || c >= limit) return INT32_MIN;        // behind the limit, or another range's
+    const int64_t pidx = p.page_div.div(static_cast<uint32_t>(c));
+    return pidx < p.max_pages ? __ldcg(pt + pidx) : -1;
+  };
+  auto load_tile = [&](int i, int stage) {
+    const int H = C.H;
+    if ((i & 3) == 0) {
+      page_mine = page_next == INT32_MIN || (page_next >= 0 && page_next < C.n_pages) ? page_next : -1;
+      page_next = lookup(i + 4);
+    }
+    const uint32_t dst = sb + kRawOff + stage * p.stage_bytes, bar = bars + 8 * (kBarRawFull + stage);
+    const int my_group_page = __shfl_sync(kFull, page_mine, 8 * (i & 3) + (lane & 7));
+    const unsigned good = __ballot_sync(kFull, my_group_page >= 0) & 255u;
+    const unsigned bad = __ballot_sync(kFull, my_group_page == -1) & 255u;
+    if (lane == 0) {
+      if (which == 0) {
+        if (bad) record_status(p.status, K8V4_ERANGE);
+        ctl[8 + stage] = static_cast<int>(good | (bad << 8));
+      }
+      const uint32_t n = __popc(good), nk = __popc((good >> (4 * rank)) & 15u);
+      mbar_expect_tx(bar, which == 0 ? n * 2048u : which == 1 ? n * 256u * H : n * 128u * H + nk * 2048u);
+    }
+    __syncwarp();
+    // lanes 0-7 a run of 1 << per groups each; the K rows lanes 8-11
+    const bool k_rows = which == 2 && lane >= 8;
+    const int q = (k_rows ? 4 * static_cast<int>(rank) + ((lane & 3) << per) : lane << per) & 7;
+    const int page = __shfl_sync(kFull, page_mine, 8 * (i & 3) + q);
+    if (page >= 0 && (k_rows ? lane - 8 < (copies + 1) >> 1 : lane < copies)) {
+      const int cell = (tile0 + i) * kTileN + 16 * q;
+      const int slot = cell - static_cast<int>(p.page_div.div(static_cast<uint32_t>(cell))) * C.P;
+      const uint8_t* pg = C.pages + static_cast<int64_t>(page) * C.page_bytes;
+      if (which == 0) tma_load_4d(dst + kRawV + q * 2048, &tm_v, 0, g, slot, page, bar);
+      else if (which == 1) bulk_load(dst + kRawKs + 1024 * H + q * 256 * H, pg + C.vs_off() + static_cast<int64_t>(slot) * 16 * H, 256 * H << per, bar);
+      else if (k_rows) tma_load_4d(dst + (q & 3) * 2048, &tm_k, 128 * map, g, slot, page, bar);
+      else bulk_load(dst + kRawKs + q * 128 * H, pg + C.ks_off() + static_cast<int64_t>(slot) * 8 * H, 128 * H << per, bar);
+    }
+    __syncwarp();
+  };
+  // the first tiles, while the others set Q up: their barriers are the CTA's own, and the three warps
+  // see them initialised
+  if (warp >= kLoadWarp0) {
+    asm volatile("barrier.cta.sync 3, %0;" ::"n"(32 * kLoadWarps) : "memory");
+    page_next = lookup(0);
+    for (int i = 0; i < min(n_tiles, p.stages); ++i) load_tile(i, i);
+  }
+
   // ---- visibility of this thread's row
   int my_vis = 0;
   if (warp < kRowWarps && row / kGqa < tok_n) {
     const int t = tok_first + row / kGqa;
-    my_vis = p.steps ? max(0, min(__ldcg(p.steps + t), tt.vis0)) : max(0, tt.vis0 + t - tt.tok0);
+    my_vis = p.steps ? max(0, min(__ldcg(p.steps + t), vis0)) : max(0, vis0 + t - tok0);
   }
   // ---- Q rows of this map -> fp16 with a power of two per row, swizzled K-major: half a warp
   // takes a row at a time (8 elements a lane)
@@ -915,52 +974,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
     } else {
       // ============================================================== copies
-      // Warp 0 of the three takes the V rows, 1 the V scales, 2 the K rows of this CTA's half and the K scales, a
-      // lane to a copy.  Page ids of four tiles, eight 16-cell groups each (those of the copy that brings the
-      // group), are held one per lane, and those of the next four are on their way.
-      const int which = warp - kLoadWarp0, H = C.H, per = p.box_shift - 4, copies = 8 >> per;   // 1 << per groups a copy
-      auto lookup = [&](int i) -> int {
-        const int c = (tile0 + i + (lane >> 3)) * kTileN + 16 * ((lane & 7) >> per << per);
-        if (i + (lane >> 3) >= n_tiles || c >= limit) return INT32_MIN;   // behind the limit, or another range's
-        const int64_t pidx = p.page_div.div(static_cast<uint32_t>(c));
-        return pidx < p.max_pages ? __ldcg(pt + pidx) : -1;
-      };
-      int page_next = lookup(0), page_mine = 0;
-      int stage = 0, i = 0;
-      uint32_t phase = 1;                                  // of the stage's last use, from its second on
+      int i = min(n_tiles, p.stages), stage = i == p.stages ? 0 : i;
+      uint32_t phase = 0;                                  // of the stage's last use
       for (; i < n_tiles; ++i) {
-        if ((i & 3) == 0) {
-          page_mine = page_next == INT32_MIN || (page_next >= 0 && page_next < C.n_pages) ? page_next : -1;
-          page_next = lookup(i + 4);
-        }
-        if (i >= p.stages && !__all_sync(kFull, wait_soon(bars + 8 * (kBarRawEmpty + stage), phase, p.wait_ns))) { ctl[1] = 1; break; }
-        const uint32_t dst = sb + kRawOff + stage * p.stage_bytes, bar = bars + 8 * (kBarRawFull + stage);
-        const int my_group_page = __shfl_sync(kFull, page_mine, 8 * (i & 3) + (lane & 7));
-        const unsigned good = __ballot_sync(kFull, my_group_page >= 0) & 255u;
-        const unsigned bad = __ballot_sync(kFull, my_group_page == -1) & 255u;
-        if (lane == 0) {
-          if (which == 0) {
-            if (bad) record_status(p.status, K8V4_ERANGE);
-            ctl[8 + stage] = static_cast<int>(good | (bad << 8));
-          }
-          const uint32_t n = __popc(good), nk = __popc((good >> (4 * rank)) & 15u);
-          mbar_expect_tx(bar, which == 0 ? n * 2048u : which == 1 ? n * 256u * H : n * 128u * H + nk * 2048u);
-        }
-        __syncwarp();
-        // lanes 0-7 a run of 1 << per groups each; the K rows lanes 8-11
-        const bool k_rows = which == 2 && lane >= 8;
-        const int q = (k_rows ? 4 * static_cast<int>(rank) + ((lane & 3) << per) : lane << per) & 7;
-        const int page = __shfl_sync(kFull, page_mine, 8 * (i & 3) + q);
-        if (page >= 0 && (k_rows ? lane - 8 < (copies + 1) >> 1 : lane < copies)) {
-          const int cell = (tile0 + i) * kTileN + 16 * q;
-          const int slot = cell - static_cast<int>(p.page_div.div(static_cast<uint32_t>(cell))) * C.P;
-          const uint8_t* pg = C.pages + static_cast<int64_t>(page) * C.page_bytes;
-          if (which == 0) tma_load_4d(dst + kRawV + q * 2048, &tm_v, 0, g, slot, page, bar);
-          else if (which == 1) bulk_load(dst + kRawKs + 1024 * H + q * 256 * H, pg + C.vs_off() + static_cast<int64_t>(slot) * 16 * H, 256 * H << per, bar);
-          else if (k_rows) tma_load_4d(dst + (q & 3) * 2048, &tm_k, 128 * map, g, slot, page, bar);
-          else bulk_load(dst + kRawKs + q * 128 * H, pg + C.ks_off() + static_cast<int64_t>(slot) * 8 * H, 128 * H << per, bar);
-        }
-        __syncwarp();
+        if (!__all_sync(kFull, wait_soon(bars + 8 * (kBarRawEmpty + stage), phase, p.wait_ns))) { ctl[1] = 1; break; }
+        load_tile(i, stage);
         if (++stage == p.stages) {
           stage = 0;
           phase ^= 1;

@@ -30,16 +30,12 @@ int launch_plan(const Launch& L, const PlanArgs& a);
 int launch_append_slots(const Launch& L, const CacheView& C, const int64_t* slots, int n_tok, const void* k,
                         int64_t k_stride, const void* v, int64_t v_stride, int dtype);
 
-// differential attention: one query per row; rows are sequences, or tokens of a ragged batch
+// differential attention: one query per sequence, and a ragged batch
 bool diff_supported(const CacheView& C);
-struct DiffPlan {
-  int splits = 0, cells_per_split = 0;
-  size_t ws_bytes = 0;
-};
-DiffPlan plan_diff_decode(const CacheView& C, int n_seqs, int max_seq_len, int num_sms);
-int launch_diff_decode(const Launch& L, const CacheView& C, const DiffPlan& plan, const void* q, int q_dtype,
-                       const int32_t* pt, int64_t max_pages, const int32_t* lens, int n_seqs, int max_seq_len,
-                       float sm_scale, const k8v4_diff& diff, void* out, void* ws);
+size_t diff_decode_ws_bytes(const CacheView& C, int n_seqs, int num_sms);
+int launch_diff_decode(const Launch& L, const CacheView& C, const void* q, int q_dtype, const int32_t* pt, int64_t max_pages,
+                       const int32_t* lens, int n_seqs, int max_seq_len, float sm_scale, const k8v4_diff& diff, void* out,
+                       void* ws);
 size_t diff_ws_bytes(const CacheView& C, int n_seqs, int n_tok, int max_seq_len, int num_sms);
 int launch_diff(const Launch& L, const CacheView& C, const void* q, int q_dtype, const int32_t* offsets, int n_tok,
                 const int32_t* pt, int64_t max_pages, const int32_t* lens, const int32_t* steps, int n_seqs,
