@@ -69,13 +69,8 @@ inline Layout layout_of(int H) {
   return L;
 }
 
-// Places in the workspace: of each pair (sequence, KV head) its first block and their number, then the
-// blocks of 16 partial rows (map, query head).  The piece of CTA c of pair s has block c + s: along
-// the line of tiles a block begins where a piece or a pair does.
-struct Places {
-  int2* pairs;
-  float* rows;
-};
+// The piece of CTA c of pair s has block c + s of the partial rows: along the line of tiles a block
+// begins where a piece or a pair does.
 constexpr int kMostCtas = kDiffMostRanges;
 // What a CTA spends on a pair beside its tiles (query, first copies, the workers' merge), in tiles:
 // each pair's tiles have that much empty line ahead of them, so that a piece with the end of one pair and
@@ -91,14 +86,6 @@ __device__ __forceinline__ int64_t quot(int64_t n, int64_t d) {
 }
 
 int ctas_of(int num_sms) { return std::min(num_sms, kMostCtas); }
-size_t place(Places* p, uint8_t* ws, int64_t n_pairs, int ctas) {
-  const size_t head = (static_cast<size_t>(n_pairs) * sizeof(int2) + 255) / 256 * 256;
-  if (p) {
-    p->pairs = reinterpret_cast<int2*>(ws);
-    p->rows = reinterpret_cast<float*>(ws + head);
-  }
-  return head + (static_cast<size_t>(n_pairs) + ctas) * 16 * kDiffRow * sizeof(float);
-}
 
 struct DiffParams {
   CacheView C;
@@ -106,10 +93,13 @@ struct DiffParams {
   int q_f32;
   const int32_t* pt;
   int64_t max_pages;
-  const int32_t* lens;        // visible cells of each sequence
+  const int32_t* lens;        // visible cells of each query
+  const int32_t* row_seq;     // a ragged batch's: the sequence and the packed token of each query, and their
+  const int32_t* row_tok;     // number on the device; or null: query b is of sequence b, n_seqs of them
+  const int32_t* count;
   int n_seqs, max_seq_len;
   float sm_scale_log2;
-  Places ws;
+  DiffPieces ws;
   int* status;
   uint32_t wait_ns;
   FastDiv page_div;
@@ -222,8 +212,9 @@ __global__ void __launch_bounds__(32 * kMaxWorkers, 1)
   {
     int64_t* sums = reinterpret_cast<int64_t*>(sm + LY.ctl_off + 32);    // of the warps
     int64_t* found = sums + kMaxWorkers;                                 // where the sequence of pos begins
-    const int per_t = (p.n_seqs + blockDim.x - 1) / blockDim.x;
-    const int s0 = min(p.n_seqs, static_cast<int>(threadIdx.x) * per_t), s1 = min(p.n_seqs, s0 + per_t);
+    const int n_seqs = p.count ? *p.count : p.n_seqs;
+    const int per_t = (n_seqs + blockDim.x - 1) / blockDim.x;
+    const int s0 = min(n_seqs, static_cast<int>(threadIdx.x) * per_t), s1 = min(n_seqs, s0 + per_t);
     int64_t sum = 0;
     for (int i = s0; i < s1; ++i) {
       const int n = p.lens[i];
@@ -271,351 +262,352 @@ __global__ void __launch_bounds__(32 * kMaxWorkers, 1)
   const uint32_t ring = sb + w * kStages * LY.stage_bytes;
 #pragma unroll 1
   while (pos < end) {
-  // ---- a pair's part of the piece
-  const int n_vis = len_of(b), pair_tiles = (n_vis + 15) >> 4;
-  if (pair_tiles == 0) {                     // a sequence with nothing to see
-    ++b;
-    g = 0;
-    continue;
-  }
-  const int64_t line0 = begin_b + static_cast<int64_t>(g) * (pair_tiles + kPairTiles) + kPairTiles;   // where its tiles begin
-  pos = max(pos, line0);
-  const int n_tiles = static_cast<int>(min(line0 + pair_tiles, end) - pos);
-  if (n_tiles <= 0) break;                   // the piece ends ahead of them
-  const int c_begin = 16 * static_cast<int>(pos - line0), c_end = min(c_begin + 16 * n_tiles, n_vis);
-  const int pair = b * H + g;
-  float* const rows = p.ws.rows + (static_cast<int64_t>(blockIdx.x) + pair) * 16 * kDiffRow;
-  if (pos == line0 && threadIdx.x == 0) {
-    const int first = static_cast<int>(quot(line0, per)), last = static_cast<int>(quot(line0 + pair_tiles - 1, per));
-    p.ws.pairs[pair] = make_int2(first + pair, last - first + 1);
-  }
-  const int n_my = n_tiles > w ? (n_tiles - w + W - 1) / W : 0;          // tiles w + W u
-
-  // ---- this worker's copies: local tile u -> the ring's next stage
-  const int32_t* pt_row = p.pt + static_cast<int64_t>(b) * p.max_pages;
-  int win0 = -1000000, win_page = -1;
-  auto page_of = [&](int u) -> int {         // warp-uniform u; all lanes call
-    if (u < win0 || u >= win0 + 32) {
-      win0 = u;
-      const int cell = c_begin + 16 * (w + W * (u + lane));
-      const int64_t pidx = cell >= 0 ? static_cast<int64_t>(p.page_div.div(static_cast<uint32_t>(cell))) : 0;
-      win_page = (u + lane < n_my && pidx < p.max_pages) ? pt_row[pidx] : -1;
+    // ---- a pair's part of the piece
+    const int n_vis = len_of(b), pair_tiles = (n_vis + 15) >> 4;
+    if (pair_tiles == 0) {                     // a sequence with nothing to see
+      ++b;
+      g = 0;
+      continue;
     }
-    const int page = __shfl_sync(kFull, win_page, u - win0);
-    return (page >= 0 && page < C.n_pages) ? page : -1;
-  };
-  // an out-of-range page issues no copy; its tile is skipped and recorded
-  auto issue = [&](int u, int to, int page) {
-    if (lane == 0) {
-      const uint32_t st = ring + to * LY.stage_bytes, bar = full + 8 * to;
-      if (page >= 0) {
-        const int cell0 = c_begin + 16 * (w + W * u);
-        const int slot0 = cell0 - static_cast<int>(p.page_div.div(static_cast<uint32_t>(cell0))) * C.P;
-        mbar_expect_tx(bar, LY.tx_bytes);
-        tma_load_4d(st, &tm_k, 0, g, slot0, page, bar);
-        tma_load_4d(st + 2048, &tm_k, 128, g, slot0, page, bar);
-        tma_load_4d(st + kVOff, &tm_v, 0, g, slot0, page, bar);
-        const uint8_t* pg = C.pages + static_cast<int64_t>(page) * C.page_bytes;
-        bulk_load(st + LY.ksc_off, pg + C.ks_off() + static_cast<int64_t>(slot0) * 8 * H, LY.ksc_bytes, bar);
-        bulk_load(st + LY.vsc_off, pg + C.vs_off() + static_cast<int64_t>(slot0) * 16 * H, LY.vsc_bytes, bar);
-      } else {
-        record_status(p.status, K8V4_ERANGE);
-        asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+    const int64_t line0 = begin_b + static_cast<int64_t>(g) * (pair_tiles + kPairTiles) + kPairTiles;   // where its tiles begin
+    pos = max(pos, line0);
+    const int n_tiles = static_cast<int>(min(line0 + pair_tiles, end) - pos);
+    if (n_tiles <= 0) break;                   // the piece ends ahead of them
+    const int c_begin = 16 * static_cast<int>(pos - line0), c_end = min(c_begin + 16 * n_tiles, n_vis);
+    const int pair = b * H + g;
+    float* const rows = p.ws.rows + (static_cast<int64_t>(blockIdx.x) + pair) * 16 * kDiffRow;
+    if (pos == line0 && threadIdx.x == 0) {
+      const int first = static_cast<int>(quot(line0, per)), last = static_cast<int>(quot(line0 + pair_tiles - 1, per));
+      p.ws.pairs[pair] = make_int2(first + pair, last - first + 1);
+    }
+    const int n_my = n_tiles > w ? (n_tiles - w + W - 1) / W : 0;          // tiles w + W u
+
+    // ---- this worker's copies: local tile u -> the ring's next stage
+    const int seq = p.row_seq ? p.row_seq[b] : b, tok = p.row_tok ? p.row_tok[b] : b;
+    const int32_t* pt_row = p.pt + static_cast<int64_t>(seq) * p.max_pages;
+    int win0 = -1000000, win_page = -1;
+    auto page_of = [&](int u) -> int {         // warp-uniform u; all lanes call
+      if (u < win0 || u >= win0 + 32) {
+        win0 = u;
+        const int cell = c_begin + 16 * (w + W * (u + lane));
+        const int64_t pidx = cell >= 0 ? static_cast<int64_t>(p.page_div.div(static_cast<uint32_t>(cell))) : 0;
+        win_page = (u + lane < n_my && pidx < p.max_pages) ? pt_row[pidx] : -1;
+      }
+      const int page = __shfl_sync(kFull, win_page, u - win0);
+      return (page >= 0 && page < C.n_pages) ? page : -1;
+    };
+    // an out-of-range page issues no copy; its tile is skipped and recorded
+    auto issue = [&](int u, int to, int page) {
+      if (lane == 0) {
+        const uint32_t st = ring + to * LY.stage_bytes, bar = full + 8 * to;
+        if (page >= 0) {
+          const int cell0 = c_begin + 16 * (w + W * u);
+          const int slot0 = cell0 - static_cast<int>(p.page_div.div(static_cast<uint32_t>(cell0))) * C.P;
+          mbar_expect_tx(bar, LY.tx_bytes);
+          tma_load_4d(st, &tm_k, 0, g, slot0, page, bar);
+          tma_load_4d(st + 2048, &tm_k, 128, g, slot0, page, bar);
+          tma_load_4d(st + kVOff, &tm_v, 0, g, slot0, page, bar);
+          const uint8_t* pg = C.pages + static_cast<int64_t>(page) * C.page_bytes;
+          bulk_load(st + LY.ksc_off, pg + C.ks_off() + static_cast<int64_t>(slot0) * 8 * H, LY.ksc_bytes, bar);
+          bulk_load(st + LY.vsc_off, pg + C.vs_off() + static_cast<int64_t>(slot0) * 16 * H, LY.vsc_bytes, bar);
+        } else {
+          record_status(p.status, K8V4_ERANGE);
+          asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+        }
+      }
+    };
+    const int stage0 = stage;
+    int issued = 0;
+    for (; issued < min(kStages, n_my); ++issued) issue(issued, (stage0 + issued) % kStages, page_of(issued));
+
+    // ---- q fragments (B operand of S^T = K q^T) into shared memory: every warp works the factors out
+    // for itself, warp 0 writes the fragments.  Lane (r0, c): head r0, dims 64 i + 16 c +
+    // 4 j + e of k-step 4 i + j; k-steps 0..7 are map 0, 8..15 map 1, each with its own
+    // power of two
+    float f[2][2];                       // score factors: [map][heads 2c, 2c + 1]
+    {
+      const int64_t qrow = (static_cast<int64_t>(tok) * HQ + g * kGqa + r0) * kD;
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        float qv[32];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int64_t e0 = qrow + 128 * m + 64 * i + 16 * c;
+          if (p.q_f32) {
+            const float4* src = reinterpret_cast<const float4*>(static_cast<const float*>(p.q) + e0);
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+              const float4 v = src[t];
+              qv[16 * i + 4 * t] = v.x; qv[16 * i + 4 * t + 1] = v.y;
+              qv[16 * i + 4 * t + 2] = v.z; qv[16 * i + 4 * t + 3] = v.w;
+            }
+          } else {
+            const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + e0);
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+              const uint4 v = src[t];
+              const uint32_t wv[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+              for (int u = 0; u < 4; ++u) {
+                qv[16 * i + 8 * t + 2 * u] = __uint_as_float(wv[u] << 16);
+                qv[16 * i + 8 * t + 2 * u + 1] = __uint_as_float(wv[u] & 0xffff0000u);
+              }
+            }
+          }
+        }
+        float amax = 0.0f;
+#pragma unroll
+        for (int t = 0; t < 32; ++t) amax = fmaxf(amax, fabsf(qv[t]));
+        amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, 1));
+        amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, 2));
+        const int ex = amax > 0.0f ? static_cast<int>((__float_as_uint(amax) >> 23) & 0xffu) - 127 : 0;
+        const int sh = max(-100, min(100, 14 - ex));              // amax * 2^sh in [2^14, 2^15)
+        const float up = ldexpf(1.0f, sh);
+        const float fscale = p.sm_scale_log2 * ldexpf(1.0f, -sh);
+        if (w == 0) {
+#pragma unroll
+          for (int ks = 0; ks < 8; ++ks) {
+            const int o = 16 * (ks >> 2) + 4 * (ks & 3);
+            const uint32_t h0 = pack_f16(qv[o] * up, qv[o + 1] * up), h1 = pack_f16(qv[o + 2] * up, qv[o + 3] * up);
+            asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(sb + LY.q_off + ((8 * m + ks) * 32 + lane) * 8), "r"(h0), "r"(h1) : "memory");
+          }
+        }
+        f[m][0] = __shfl_sync(kFull, fscale, 8 * c);
+        f[m][1] = __shfl_sync(kFull, fscale, 8 * c + 4);
       }
     }
-  };
-  const int stage0 = stage;
-  int issued = 0;
-  for (; issued < min(kStages, n_my); ++issued) issue(issued, (stage0 + issued) % kStages, page_of(issued));
+    __syncthreads();
 
-  // ---- q fragments (B operand of S^T = K q^T) into shared memory: every warp works the factors out
-  // for itself, warp 0 writes the fragments.  Lane (r0, c): head r0, dims 64 i + 16 c +
-  // 4 j + e of k-step 4 i + j; k-steps 0..7 are map 0, 8..15 map 1, each with its own
-  // power of two
-  float f[2][2];                       // score factors: [map][heads 2c, 2c + 1]
-  {
-    const int64_t qrow = (static_cast<int64_t>(b) * HQ + g * kGqa + r0) * kD;
+    // K fragment addresses within a stage (two 128-byte-swizzled [16][128] halves)
+    const int rowA = sigma(r0), rowB = 8 + sigma(r0);
+    uint32_t offA[2], offB[2];
 #pragma unroll
-    for (int m = 0; m < 2; ++m) {
-      float qv[32];
+    for (int i = 0; i < 2; ++i) {
+      offA[i] = rowA * 128 + 16 * ((4 * i + c) ^ (rowA & 7));
+      offB[i] = rowB * 128 + 16 * ((4 * i + c) ^ (rowB & 7));
+    }
+    const uint32_t ksA = LY.ksc_off + (rowA * H + g) * 8, ksB = LY.ksc_off + (rowB * H + g) * 8;
+    // V fragment rows: matrix mi = lane >> 3 holds cells 8 (mi & 1) + sigma(0..7)
+    const int mi = lane >> 3;
+    const int vcell = 8 * (mi & 1) + sigma(lane & 7);
+    const uint32_t vrow = kVOff + vcell * 128;
+    const int vsw = vcell & 7;
+    // the V scales of the fragment's four cells k = 2c, 2c+1, 2c+8, 2c+9
+    const uint32_t soff0 = LY.vsc_off + (sigma(2 * c) * H + g) * 16, soff1 = LY.vsc_off + (sigma(2 * c + 1) * H + g) * 16;
+    const uint32_t s8 = 8 * H * 16;
+    const uint32_t qf = sb + LY.q_off + 8 * lane;
+
+    float o[2][16][4];                   // [map][16-dim m-tile][fragment]: heads 2c, 2c+1 of dims r0 (+8)
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int64_t e0 = qrow + 128 * m + 64 * i + 16 * c;
-        if (p.q_f32) {
-          const float4* src = reinterpret_cast<const float4*>(static_cast<const float*>(p.q) + e0);
+    for (int m = 0; m < 2; ++m)
 #pragma unroll
-          for (int t = 0; t < 4; ++t) {
-            const float4 v = src[t];
-            qv[16 * i + 4 * t] = v.x; qv[16 * i + 4 * t + 1] = v.y;
-            qv[16 * i + 4 * t + 2] = v.z; qv[16 * i + 4 * t + 3] = v.w;
+      for (int mt = 0; mt < 16; ++mt) o[m][mt][0] = o[m][mt][1] = o[m][mt][2] = o[m][mt][3] = 0.0f;
+    int M[2][2] = {{INT_MIN, INT_MIN}, {INT_MIN, INT_MIN}};    // running buckets
+    float l[2][2] = {{0.0f, 0.0f}, {0.0f, 0.0f}};
+
+    int done = 0;
+    for (int u = 0; u < n_my; ++u, ++done) {
+      if (!__all_sync(kFull, wait_or_abort(full + 8 * stage, phase, p.wait_ns, abort_flag))) {
+        if (lane == 0) {
+          *abort_flag = 1;
+          record_status(p.status, K8V4_ECUDA);
+        }
+        aborted = true;
+        break;
+      }
+      const uint32_t st = ring + stage * LY.stage_bytes;
+      if (page_of(u) >= 0) {
+        const uint2 kAu = lds64(st + ksA), kBu = lds64(st + ksB);
+        const int cell0 = c_begin + 16 * (w + W * u);
+        const bool vA = cell0 + rowA < c_end, vB = cell0 + rowB < c_end;
+        uint32_t ph[2][2];
+        // ---- S_m^T[cell][head] of both maps, two accumulators each
+        float acc[2][2][4];
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+          for (int a4 = 0; a4 < 2; ++a4) acc[m][a4][0] = acc[m][a4][1] = acc[m][a4][2] = acc[m][a4][3] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+#pragma unroll
+          for (int m = 0; m < 2; ++m) {
+            const uint4 ka = lds128(st + 2048 * m + offA[i]);
+            const uint4 kb = lds128(st + 2048 * m + offB[i]);
+            const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              uint32_t a[4];
+              i8x4_to_f16(wa[j], a[0], a[2]);
+              i8x4_to_f16(wb[j], a[1], a[3]);
+              const uint2 qb = lds64(qf + (8 * m + 4 * i + j) * 256);
+              mma16(acc[m][j & 1], a, qb.x, qb.y);
+            }
           }
-        } else {
-          const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + e0);
+        }
+        float sc[2][4];
+        bool up = false;
 #pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            const uint4 v = src[t];
-            const uint32_t wv[4] = {v.x, v.y, v.z, v.w};
+        for (int m = 0; m < 2; ++m) {
+          const float kA = __uint_as_float(m ? kAu.y : kAu.x), kB = __uint_as_float(m ? kBu.y : kBu.x);
+          sc[m][0] = vA ? kA * (acc[m][0][0] + acc[m][1][0]) * f[m][0] : -INFINITY;
+          sc[m][1] = vA ? kA * (acc[m][0][1] + acc[m][1][1]) * f[m][1] : -INFINITY;
+          sc[m][2] = vB ? kB * (acc[m][0][2] + acc[m][1][2]) * f[m][0] : -INFINITY;
+          sc[m][3] = vB ? kB * (acc[m][0][3] + acc[m][1][3]) * f[m][1] : -INFINITY;
+          up = up || sc[m][0] > 8.0f * M[m][0] || sc[m][2] > 8.0f * M[m][0] || sc[m][1] > 8.0f * M[m][1] || sc[m][3] > 8.0f * M[m][1];
+        }
+        // ---- softmax against the running bucket of each head (the decode kernel's), both maps at a time
+        if (__any_sync(kFull, up)) {
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-              qv[16 * i + 8 * t + 2 * u] = __uint_as_float(wv[u] << 16);
-              qv[16 * i + 8 * t + 2 * u + 1] = __uint_as_float(wv[u] & 0xffff0000u);
+          for (int m = 0; m < 2; ++m) {
+            float t0 = fmaxf(sc[m][0], sc[m][2]), t1 = fmaxf(sc[m][1], sc[m][3]);
+#pragma unroll
+            for (int off = 4; off < 32; off <<= 1) {
+              t0 = fmaxf(t0, __shfl_xor_sync(kFull, t0, off));
+              t1 = fmaxf(t1, __shfl_xor_sync(kFull, t1, off));
+            }
+            const int nb0 = max(M[m][0], static_cast<int>(fminf(fmaxf(ceilf(t0 * 0.125f), -kBucketClamp), kBucketClamp)));
+            const int nb1 = max(M[m][1], static_cast<int>(fminf(fmaxf(ceilf(t1 * 0.125f), -kBucketClamp), kBucketClamp)));
+            const float g0 = M[m][0] == INT_MIN ? 0.0f : pow2i(8 * (M[m][0] - nb0));
+            const float g1 = M[m][1] == INT_MIN ? 0.0f : pow2i(8 * (M[m][1] - nb1));
+#pragma unroll
+            for (int mt = 0; mt < 16; ++mt) {
+              o[m][mt][0] *= g0; o[m][mt][2] *= g0;
+              o[m][mt][1] *= g1; o[m][mt][3] *= g1;
+            }
+            l[m][0] *= g0;
+            l[m][1] *= g1;
+            M[m][0] = nb0;
+            M[m][1] = nb1;
+          }
+        }
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+          const float rf0 = 8.0f * M[m][0] - 14.0f, rf1 = 8.0f * M[m][1] - 14.0f;
+          const float p0 = ex2_ftz(sc[m][0] - rf0), p1 = ex2_ftz(sc[m][1] - rf1);      // p' = 2^(s - ref + 14) <= 2^14
+          const float p2 = ex2_ftz(sc[m][2] - rf0), p3 = ex2_ftz(sc[m][3] - rf1);
+          l[m][0] += p0 + p2;
+          l[m][1] += p1 + p3;
+          // to the B layout (head r0; cells 2c, 2c+1 | 2c+8, 2c+9)
+          ph[m][0] = movmatrix_t(pack_f16(p0, p1));
+          ph[m][1] = movmatrix_t(pack_f16(p2, p3));
+        }
+        // ---- PV of both maps in rotated space: V = RN((n - 8) / 8 * d), m-tile 2 blk + hf = block
+        // blk, dims 16 hf .. 16 hf + 15
+#pragma unroll
+        for (int bp = 0; bp < 4; ++bp) {
+          uint32_t R[4];
+          ldmatrix_x4_t(R, st + vrow + 16 * ((2 * bp + (mi >> 1)) ^ vsw));
+          const uint32_t w0 = lds32(st + soff0 + 4 * bp), w1 = lds32(st + soff1 + 4 * bp);
+          const uint32_t w2 = lds32(st + soff0 + s8 + 4 * bp), w3 = lds32(st + soff1 + s8 + 4 * bp);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t sel = h ? 0x7632u : 0x5410u;
+            const uint32_t d01 = prmt(w0, w1, sel), d89 = prmt(w2, w3, sel);     // d of block 2bp+h, cell pairs
+            __half2 xa[4], xb[4];
+            nibs_8th(R[2 * h], xa);
+            nibs_8th(R[2 * h + 1], xb);
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+              const uint32_t a[4] = {times(xa[2 * hf], d01), times(xa[2 * hf + 1], d01), times(xb[2 * hf], d89), times(xb[2 * hf + 1], d89)};
+              mma16(o[0][2 * (2 * bp + h) + hf], a, ph[0][0], ph[0][1]);
+              mma16(o[1][2 * (2 * bp + h) + hf], a, ph[1][0], ph[1][1]);
             }
           }
         }
       }
-      float amax = 0.0f;
-#pragma unroll
-      for (int t = 0; t < 32; ++t) amax = fmaxf(amax, fabsf(qv[t]));
-      amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, 1));
-      amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, 2));
-      const int ex = amax > 0.0f ? static_cast<int>((__float_as_uint(amax) >> 23) & 0xffu) - 127 : 0;
-      const int sh = max(-100, min(100, 14 - ex));              // amax * 2^sh in [2^14, 2^15)
-      const float up = ldexpf(1.0f, sh);
-      const float fscale = p.sm_scale_log2 * ldexpf(1.0f, -sh);
-      if (w == 0) {
-#pragma unroll
-        for (int ks = 0; ks < 8; ++ks) {
-          const int o = 16 * (ks >> 2) + 4 * (ks & 3);
-          const uint32_t h0 = pack_f16(qv[o] * up, qv[o + 1] * up), h1 = pack_f16(qv[o + 2] * up, qv[o + 3] * up);
-          asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(sb + LY.q_off + ((8 * m + ks) * 32 + lane) * 8), "r"(h0), "r"(h1) : "memory");
-        }
+      __syncwarp();
+      if (issued < n_my) {
+        issue(issued, stage, page_of(issued));
+        ++issued;
       }
-      f[m][0] = __shfl_sync(kFull, fscale, 8 * c);
-      f[m][1] = __shfl_sync(kFull, fscale, 8 * c + 4);
+      if (++stage == kStages) {
+        stage = 0;
+        phase ^= 1;
+      }
     }
-  }
-  __syncthreads();
-
-  // K fragment addresses within a stage (two 128-byte-swizzled [16][128] halves)
-  const int rowA = sigma(r0), rowB = 8 + sigma(r0);
-  uint32_t offA[2], offB[2];
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    offA[i] = rowA * 128 + 16 * ((4 * i + c) ^ (rowA & 7));
-    offB[i] = rowB * 128 + 16 * ((4 * i + c) ^ (rowB & 7));
-  }
-  const uint32_t ksA = LY.ksc_off + (rowA * H + g) * 8, ksB = LY.ksc_off + (rowB * H + g) * 8;
-  // V fragment rows: matrix mi = lane >> 3 holds cells 8 (mi & 1) + sigma(0..7)
-  const int mi = lane >> 3;
-  const int vcell = 8 * (mi & 1) + sigma(lane & 7);
-  const uint32_t vrow = kVOff + vcell * 128;
-  const int vsw = vcell & 7;
-  // the V scales of the fragment's four cells k = 2c, 2c+1, 2c+8, 2c+9
-  const uint32_t soff0 = LY.vsc_off + (sigma(2 * c) * H + g) * 16, soff1 = LY.vsc_off + (sigma(2 * c + 1) * H + g) * 16;
-  const uint32_t s8 = 8 * H * 16;
-  const uint32_t qf = sb + LY.q_off + 8 * lane;
-
-  float o[2][16][4];                   // [map][16-dim m-tile][fragment]: heads 2c, 2c+1 of dims r0 (+8)
-#pragma unroll
-  for (int m = 0; m < 2; ++m)
-#pragma unroll
-    for (int mt = 0; mt < 16; ++mt) o[m][mt][0] = o[m][mt][1] = o[m][mt][2] = o[m][mt][3] = 0.0f;
-  int M[2][2] = {{INT_MIN, INT_MIN}, {INT_MIN, INT_MIN}};    // running buckets
-  float l[2][2] = {{0.0f, 0.0f}, {0.0f, 0.0f}};
-
-  int done = 0;
-  for (int u = 0; u < n_my; ++u, ++done) {
-    if (!__all_sync(kFull, wait_or_abort(full + 8 * stage, phase, p.wait_ns, abort_flag))) {
-      if (lane == 0) {
-        *abort_flag = 1;
-        record_status(p.status, K8V4_ECUDA);
-      }
-      aborted = true;
-      break;
-    }
-    const uint32_t st = ring + stage * LY.stage_bytes;
-    if (page_of(u) >= 0) {
-      const uint2 kAu = lds64(st + ksA), kBu = lds64(st + ksB);
-      const int cell0 = c_begin + 16 * (w + W * u);
-      const bool vA = cell0 + rowA < c_end, vB = cell0 + rowB < c_end;
-      uint32_t ph[2][2];
-      // ---- S_m^T[cell][head] of both maps, two accumulators each
-      float acc[2][2][4];
-#pragma unroll
-      for (int m = 0; m < 2; ++m)
-#pragma unroll
-        for (int a4 = 0; a4 < 2; ++a4) acc[m][a4][0] = acc[m][a4][1] = acc[m][a4][2] = acc[m][a4][3] = 0.0f;
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-#pragma unroll
-        for (int m = 0; m < 2; ++m) {
-          const uint4 ka = lds128(st + 2048 * m + offA[i]);
-          const uint4 kb = lds128(st + 2048 * m + offB[i]);
-          const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            uint32_t a[4];
-            i8x4_to_f16(wa[j], a[0], a[2]);
-            i8x4_to_f16(wb[j], a[1], a[3]);
-            const uint2 qb = lds64(qf + (8 * m + 4 * i + j) * 256);
-            mma16(acc[m][j & 1], a, qb.x, qb.y);
-          }
-        }
-      }
-      float sc[2][4];
-      bool up = false;
+    for (int off = 4; off < 32; off <<= 1) {
 #pragma unroll
       for (int m = 0; m < 2; ++m) {
-        const float kA = __uint_as_float(m ? kAu.y : kAu.x), kB = __uint_as_float(m ? kBu.y : kBu.x);
-        sc[m][0] = vA ? kA * (acc[m][0][0] + acc[m][1][0]) * f[m][0] : -INFINITY;
-        sc[m][1] = vA ? kA * (acc[m][0][1] + acc[m][1][1]) * f[m][1] : -INFINITY;
-        sc[m][2] = vB ? kB * (acc[m][0][2] + acc[m][1][2]) * f[m][0] : -INFINITY;
-        sc[m][3] = vB ? kB * (acc[m][0][3] + acc[m][1][3]) * f[m][1] : -INFINITY;
-        up = up || sc[m][0] > 8.0f * M[m][0] || sc[m][2] > 8.0f * M[m][0] || sc[m][1] > 8.0f * M[m][1] || sc[m][3] > 8.0f * M[m][1];
+        l[m][0] += __shfl_xor_sync(kFull, l[m][0], off);
+        l[m][1] += __shfl_xor_sync(kFull, l[m][1], off);
       }
-      // ---- softmax against the running bucket of each head (the decode kernel's), both maps at a time
-      if (__any_sync(kFull, up)) {
-#pragma unroll
-        for (int m = 0; m < 2; ++m) {
-          float t0 = fmaxf(sc[m][0], sc[m][2]), t1 = fmaxf(sc[m][1], sc[m][3]);
-#pragma unroll
-          for (int off = 4; off < 32; off <<= 1) {
-            t0 = fmaxf(t0, __shfl_xor_sync(kFull, t0, off));
-            t1 = fmaxf(t1, __shfl_xor_sync(kFull, t1, off));
-          }
-          const int nb0 = max(M[m][0], static_cast<int>(fminf(fmaxf(ceilf(t0 * 0.125f), -kBucketClamp), kBucketClamp)));
-          const int nb1 = max(M[m][1], static_cast<int>(fminf(fmaxf(ceilf(t1 * 0.125f), -kBucketClamp), kBucketClamp)));
-          const float g0 = M[m][0] == INT_MIN ? 0.0f : pow2i(8 * (M[m][0] - nb0));
-          const float g1 = M[m][1] == INT_MIN ? 0.0f : pow2i(8 * (M[m][1] - nb1));
-#pragma unroll
-          for (int mt = 0; mt < 16; ++mt) {
-            o[m][mt][0] *= g0; o[m][mt][2] *= g0;
-            o[m][mt][1] *= g1; o[m][mt][3] *= g1;
-          }
-          l[m][0] *= g0;
-          l[m][1] *= g1;
-          M[m][0] = nb0;
-          M[m][1] = nb1;
-        }
-      }
-#pragma unroll
-      for (int m = 0; m < 2; ++m) {
-        const float rf0 = static_cast<float>(8 * M[m][0] - 14), rf1 = static_cast<float>(8 * M[m][1] - 14);
-        const float p0 = ex2_ftz(sc[m][0] - rf0), p1 = ex2_ftz(sc[m][1] - rf1);      // p' = 2^(s - ref + 14) <= 2^14
-        const float p2 = ex2_ftz(sc[m][2] - rf0), p3 = ex2_ftz(sc[m][3] - rf1);
-        l[m][0] += p0 + p2;
-        l[m][1] += p1 + p3;
-        // to the B layout (head r0; cells 2c, 2c+1 | 2c+8, 2c+9)
-        ph[m][0] = movmatrix_t(pack_f16(p0, p1));
-        ph[m][1] = movmatrix_t(pack_f16(p2, p3));
-      }
-      // ---- PV of both maps in rotated space: V = RN((n - 8) / 8 * d), m-tile 2 blk + hf = block
-      // blk, dims 16 hf .. 16 hf + 15
-#pragma unroll
-      for (int bp = 0; bp < 4; ++bp) {
-        uint32_t R[4];
-        ldmatrix_x4_t(R, st + vrow + 16 * ((2 * bp + (mi >> 1)) ^ vsw));
-        const uint32_t w0 = lds32(st + soff0 + 4 * bp), w1 = lds32(st + soff1 + 4 * bp);
-        const uint32_t w2 = lds32(st + soff0 + s8 + 4 * bp), w3 = lds32(st + soff1 + s8 + 4 * bp);
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint32_t sel = h ? 0x7632u : 0x5410u;
-          const uint32_t d01 = prmt(w0, w1, sel), d89 = prmt(w2, w3, sel);     // d of block 2bp+h, cell pairs
-          __half2 xa[4], xb[4];
-          nibs_8th(R[2 * h], xa);
-          nibs_8th(R[2 * h + 1], xb);
-#pragma unroll
-          for (int hf = 0; hf < 2; ++hf) {
-            const uint32_t a[4] = {times(xa[2 * hf], d01), times(xa[2 * hf + 1], d01), times(xb[2 * hf], d89), times(xb[2 * hf + 1], d89)};
-            mma16(o[0][2 * (2 * bp + h) + hf], a, ph[0][0], ph[0][1]);
-            mma16(o[1][2 * (2 * bp + h) + hf], a, ph[1][0], ph[1][1]);
-          }
+    }
+
+    // ---------------------------------------------------------------- epilogue
+    // a worker that left early first waits (bounded) for its copies in flight: the stages from its next one on
+    if (aborted && lane == 0) {
+      const int left = issued - done;
+      for (int k = 0; k < left; ++k) {
+        const uint32_t ph = stage + k >= kStages ? phase ^ 1 : phase;
+        const uint64_t t0 = global_ns();
+        while (!mbar_try(full + 8 * ((stage + k) % kStages), ph, 20000u) && global_ns() - t0 < kWaitDefaultNs) {
         }
       }
     }
     __syncwarp();
-    if (issued < n_my) {
-      issue(issued, stage, page_of(issued));
-      ++issued;
-    }
-    if (++stage == kStages) {
-      stage = 0;
-      phase ^= 1;
-    }
-  }
-#pragma unroll
-  for (int off = 4; off < 32; off <<= 1) {
+    float* mine = reinterpret_cast<float*>(sm + w * kStages * LY.stage_bytes);
 #pragma unroll
     for (int m = 0; m < 2; ++m) {
-      l[m][0] += __shfl_xor_sync(kFull, l[m][0], off);
-      l[m][1] += __shfl_xor_sync(kFull, l[m][1], off);
-    }
-  }
-
-  // ---------------------------------------------------------------- epilogue
-  // a worker that left early first waits (bounded) for its copies in flight: the stages from its next one on
-  if (aborted && lane == 0) {
-    const int left = issued - done;
-    for (int k = 0; k < left; ++k) {
-      const uint32_t ph = stage + k >= kStages ? phase ^ 1 : phase;
-      const uint64_t t0 = global_ns();
-      while (!mbar_try(full + 8 * ((stage + k) % kStages), ph, 20000u) && global_ns() - t0 < kWaitDefaultNs) {
+      const bool live0 = M[m][0] != INT_MIN, live1 = M[m][1] != INT_MIN;
+      float* base = mine + 8 * m * kHeadStride;
+#pragma unroll
+      for (int mt = 0; mt < 16; ++mt) {
+        const int d0 = 32 * (mt >> 1) + 16 * (mt & 1) + 2 * r0;
+        *reinterpret_cast<float2*>(base + (2 * c) * kHeadStride + d0) =
+            live0 ? make_float2(o[m][mt][0], o[m][mt][2]) : make_float2(0.0f, 0.0f);
+        *reinterpret_cast<float2*>(base + (2 * c + 1) * kHeadStride + d0) =
+            live1 ? make_float2(o[m][mt][1], o[m][mt][3]) : make_float2(0.0f, 0.0f);
+      }
+      if (r0 == 0) {
+        reinterpret_cast<int*>(mine + kPartBucket)[8 * m + 2 * c] = M[m][0];
+        reinterpret_cast<int*>(mine + kPartBucket)[8 * m + 2 * c + 1] = M[m][1];
+        mine[kPartSum + 8 * m + 2 * c] = l[m][0];
+        mine[kPartSum + 8 * m + 2 * c + 1] = l[m][1];
       }
     }
-  }
-  __syncwarp();
-  float* mine = reinterpret_cast<float*>(sm + w * kStages * LY.stage_bytes);
+    __syncthreads();
+    // a warp per (map, head): the workers' partials at the largest bucket, in rotated space
+    for (int h = w; h < 16; h += W) {
+      const float* mj_part = reinterpret_cast<const float*>(sm + min(lane, W - 1) * kStages * LY.stage_bytes);
+      const int mj = lane < W ? reinterpret_cast<const int*>(mj_part + kPartBucket)[h] : INT_MIN;
+      const float lj = lane < W ? mj_part[kPartSum + h] : 0.0f;
+      const int Mx = __reduce_max_sync(kFull, mj);
+      const float fj = mj == INT_MIN ? 0.0f : pow2i(8 * (mj - Mx));
+      float v[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+      float Ls = 0.0f;
 #pragma unroll
-  for (int m = 0; m < 2; ++m) {
-    const bool live0 = M[m][0] != INT_MIN, live1 = M[m][1] != INT_MIN;
-    float* base = mine + 8 * m * kHeadStride;
-#pragma unroll
-    for (int mt = 0; mt < 16; ++mt) {
-      const int d0 = 32 * (mt >> 1) + 16 * (mt & 1) + 2 * r0;
-      *reinterpret_cast<float2*>(base + (2 * c) * kHeadStride + d0) =
-          live0 ? make_float2(o[m][mt][0], o[m][mt][2]) : make_float2(0.0f, 0.0f);
-      *reinterpret_cast<float2*>(base + (2 * c + 1) * kHeadStride + d0) =
-          live1 ? make_float2(o[m][mt][1], o[m][mt][3]) : make_float2(0.0f, 0.0f);
-    }
-    if (r0 == 0) {
-      reinterpret_cast<int*>(mine + kPartBucket)[8 * m + 2 * c] = M[m][0];
-      reinterpret_cast<int*>(mine + kPartBucket)[8 * m + 2 * c + 1] = M[m][1];
-      mine[kPartSum + 8 * m + 2 * c] = l[m][0];
-      mine[kPartSum + 8 * m + 2 * c + 1] = l[m][1];
-    }
-  }
-  __syncthreads();
-  // a warp per (map, head): the workers' partials at the largest bucket, in rotated space
-  for (int h = w; h < 16; h += W) {
-    const float* mj_part = reinterpret_cast<const float*>(sm + min(lane, W - 1) * kStages * LY.stage_bytes);
-    const int mj = lane < W ? reinterpret_cast<const int*>(mj_part + kPartBucket)[h] : INT_MIN;
-    const float lj = lane < W ? mj_part[kPartSum + h] : 0.0f;
-    const int Mx = __reduce_max_sync(kFull, mj);
-    const float fj = mj == INT_MIN ? 0.0f : pow2i(8 * (mj - Mx));
-    float v[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-    float Ls = 0.0f;
-#pragma unroll
-    for (int j = 0; j < kMaxWorkers; ++j) {
-      const float fw = __shfl_sync(kFull, fj, j), lw = __shfl_sync(kFull, lj, j);   // 0 for j >= W
-      if (j < W) {
-        const float* src = reinterpret_cast<const float*>(sm + j * kStages * LY.stage_bytes) + h * kHeadStride;
-        const float4 x0 = *reinterpret_cast<const float4*>(src + 4 * lane);
-        const float4 x1 = *reinterpret_cast<const float4*>(src + 128 + 4 * lane);
-        v[0] += x0.x * fw; v[1] += x0.y * fw; v[2] += x0.z * fw; v[3] += x0.w * fw;
-        v[4] += x1.x * fw; v[5] += x1.y * fw; v[6] += x1.z * fw; v[7] += x1.w * fw;
-        Ls += lw * fw;
+      for (int j = 0; j < kMaxWorkers; ++j) {
+        const float fw = __shfl_sync(kFull, fj, j), lw = __shfl_sync(kFull, lj, j);   // 0 for j >= W
+        if (j < W) {
+          const float* src = reinterpret_cast<const float*>(sm + j * kStages * LY.stage_bytes) + h * kHeadStride;
+          const float4 x0 = *reinterpret_cast<const float4*>(src + 4 * lane);
+          const float4 x1 = *reinterpret_cast<const float4*>(src + 128 + 4 * lane);
+          v[0] += x0.x * fw; v[1] += x0.y * fw; v[2] += x0.z * fw; v[3] += x0.w * fw;
+          v[4] += x1.x * fw; v[5] += x1.y * fw; v[6] += x1.z * fw; v[7] += x1.w * fw;
+          Ls += lw * fw;
+        }
+      }
+      constexpr float kInv = 1.0f / 2048.0f;     // 2^-14 of p', 2^3 of (n - 8) / 8
+      float* dst = rows + h * kDiffRow;
+      reinterpret_cast<float4*>(dst)[lane] = make_float4(v[0] * kInv, v[1] * kInv, v[2] * kInv, v[3] * kInv);
+      reinterpret_cast<float4*>(dst)[32 + lane] = make_float4(v[4] * kInv, v[5] * kInv, v[6] * kInv, v[7] * kInv);
+      if (lane == 0) {
+        dst[256] = Mx == INT_MIN ? -INFINITY : static_cast<float>(8 * Mx);
+        dst[257] = Ls * (1.0f / 16384.0f);
       }
     }
-    constexpr float kInv = 1.0f / 2048.0f;     // 2^-14 of p', 2^3 of (n - 8) / 8
-    float* dst = rows + h * kDiffRow;
-    reinterpret_cast<float4*>(dst)[lane] = make_float4(v[0] * kInv, v[1] * kInv, v[2] * kInv, v[3] * kInv);
-    reinterpret_cast<float4*>(dst)[32 + lane] = make_float4(v[4] * kInv, v[5] * kInv, v[6] * kInv, v[7] * kInv);
-    if (lane == 0) {
-      dst[256] = Mx == INT_MIN ? -INFINITY : static_cast<float>(8 * Mx);
-      dst[257] = Ls * (1.0f / 16384.0f);
+    // the next pair's copies overwrite what the workers wrote and the merge read; after a failure the CTA leaves (its
+    // other pieces' rows would be older ones: their blocks are marked empty)
+    fence_async_smem();
+    __syncthreads();
+    pos += n_tiles;
+    if (++g == H) {
+      g = 0;
+      begin_b += line_of(pair_tiles, H);
+      ++b;
     }
-  }
-  // the next pair's copies overwrite what the workers wrote and the merge read; after a failure the CTA leaves (its
-  // other pieces' rows would be older ones: their blocks are marked empty)
-  fence_async_smem();
-  __syncthreads();
-  pos += n_tiles;
-  if (++g == H) {
-    g = 0;
-    begin_b += line_of(pair_tiles, H);
-    ++b;
-  }
-  if (*abort_flag) break;
+    if (*abort_flag) break;
   }
 #pragma unroll 1
   while (pos < end) {                        // (only after a failure)
@@ -649,8 +641,8 @@ __global__ void __launch_bounds__(32 * kMaxWorkers, 1)
 struct CombineParams {
   const float* ws;
   DiffRagged r;               // a ragged batch's rows
-  const int2* pairs;          // else: the first block and their number of each (sequence, KV head)
-  const int32_t* lens;        // and the cells that a sequence sees
+  DiffPieces pieces;          // those of single queries
+  const int32_t* lens;        // and the cells that each sees
   int H, n_rows;              // rows: (sequence or token, query head)
   k8v4_diff d;
   uint16_t* out;
@@ -740,22 +732,22 @@ __global__ void __launch_bounds__(WARPS > 4 ? 32 * WARPS : kCombineThreads, WARP
   const float* base;                                    // range s of map m: base + m * m_stride + s * s_stride
   int64_t m_stride, s_stride;
   int splits;
-  if (RAGGED) {
-    const int i = p.r.tok_tile[row];
-    if (i < 0) return;                                  // no sequence's: left as it is
+  const int i = RAGGED ? p.r.tok_tile[row] : -2 - row;
+  if (i == -1) return;                                  // no sequence's: left as it is
+  if (RAGGED && i >= 0) {
     const int32_t* tile = p.r.tiles + 8 * static_cast<int64_t>(i);
     splits = min(tile[3], kMost);
     s_stride = 256 * kDiffRow;
     m_stride = s_stride * splits;
     base = p.ws + (static_cast<int64_t>(tile[4]) + 2 * g * splits) * s_stride + ((row - tile[1]) * kGqa + h) * kDiffRow;
   } else {
-    const int len = p.lens[row];
-    int2 at = p.pairs[row * p.H + g];                   // not written where there is nothing to see
-    if (len <= 0) at = make_int2(0, 0);
+    const int len = p.lens[-2 - i];
+    int2 at = p.pieces.pairs[static_cast<int64_t>(-2 - i) * p.H + g];      // not written where there is nothing to see
+    if (len <= 0 || at.x < 0 || at.y < 0 || at.x > p.pieces.blocks - at.y) at = make_int2(0, 0);   // (nor behind a failed wait)
     splits = min(at.y, kMost);
     m_stride = kGqa * kDiffRow;
     s_stride = 2 * m_stride;
-    base = p.ws + at.x * s_stride + h * kDiffRow;
+    base = p.pieces.rows + at.x * s_stride + h * kDiffRow;
   }
   auto sync = [] {
     if (WARPS == 1) __syncwarp();
@@ -887,28 +879,39 @@ bool diff_supported(const CacheView& C) {
   return C.fmt == K8V4_FORMAT_K8V4 && C.n_pages < (int64_t(1) << 31) && C.page_bytes < (int64_t(1) << 39);
 }
 
+size_t place_pieces(DiffPieces* p, uint8_t* ws, int64_t n_pairs, int num_sms) {
+  const size_t head = (static_cast<size_t>(n_pairs) * sizeof(int2) + 255) / 256 * 256;
+  if (p) {
+    p->pairs = reinterpret_cast<int2*>(ws);
+    p->rows = reinterpret_cast<float*>(ws + head);
+    p->blocks = static_cast<int>(n_pairs) + ctas_of(num_sms);
+  }
+  return head + (static_cast<size_t>(n_pairs) + ctas_of(num_sms)) * 16 * kDiffRow * sizeof(float);
+}
 size_t diff_decode_ws_bytes(const CacheView& C, int n_seqs, int num_sms) {
-  return place(nullptr, nullptr, static_cast<int64_t>(n_seqs) * C.H, ctas_of(num_sms));
+  return place_pieces(nullptr, nullptr, static_cast<int64_t>(n_seqs) * C.H, num_sms);
 }
 
-int launch_diff_combine_ragged(const Launch& L, const float* ws, const DiffRagged& r, int n_tok, int H, bool wide,
-                               const k8v4_diff& diff, void* out) {
+int launch_diff_combine_ragged(const Launch& L, const float* ws, const DiffRagged& r, const DiffPieces& pieces,
+                               const int32_t* lens, int n_tok, int H, bool few, const k8v4_diff& diff, void* out) {
   CombineParams p;
   p.ws = ws;
   p.r = r;
-  p.pairs = nullptr;
-  p.lens = nullptr;
+  p.pieces = pieces;
+  p.lens = lens;
   p.H = H;
   p.n_rows = n_tok * H * kGqa;                          // below 2^30
   p.d = diff;
   p.out = static_cast<uint16_t*>(out);
-  if (wide) return launch_behind(L, diff_combine_kernel<16, true>, dim3(p.n_rows), dim3(512), p);
+  // (16 warps' registers leave an SM one row at a time)
+  if (few && p.n_rows <= L.num_sms) return launch_behind(L, diff_combine_kernel<16, true>, dim3(p.n_rows), dim3(512), p);
+  if (few) return launch_behind(L, diff_combine_kernel<4, true>, dim3(p.n_rows), dim3(kCombineThreads), p);
   return launch_behind(L, diff_combine_kernel<1, true>, dim3((p.n_rows + 3) / 4), dim3(kCombineThreads), p);
 }
 
-int launch_diff_decode(const Launch& L, const CacheView& C, const void* q, int q_dtype, const int32_t* pt, int64_t max_pages,
-                       const int32_t* lens, int n_seqs, int max_seq_len, float sm_scale, const k8v4_diff& diff, void* out,
-                       void* ws) {
+int launch_diff_split(const Launch& L, const CacheView& C, const void* q, int q_dtype, const int32_t* pt, int64_t max_pages,
+                      const int32_t* lens, const DiffQueries& rows, int n_seqs, int max_seq_len, float sm_scale,
+                      const DiffPieces& ws) {
   DiffParams p;
   p.C = C;
   p.q = q;
@@ -916,11 +919,13 @@ int launch_diff_decode(const Launch& L, const CacheView& C, const void* q, int q
   p.pt = pt;
   p.max_pages = max_pages;
   p.lens = lens;
+  p.row_seq = rows.seq;
+  p.row_tok = rows.tok;
+  p.count = rows.count;
   p.n_seqs = n_seqs;
   p.max_seq_len = max_seq_len;
   p.sm_scale_log2 = sm_scale * 1.4426950408889634f;
-  const int ctas = ctas_of(L.num_sms);
-  place(&p.ws, static_cast<uint8_t*>(ws), static_cast<int64_t>(n_seqs) * C.H, ctas);
+  p.ws = ws;
   p.status = L.status;
   p.wait_ns = wait_limit_ns() ? wait_limit_ns() : kWaitDefaultNs;
   p.page_div = FastDiv(static_cast<uint32_t>(C.P));
@@ -931,7 +936,7 @@ int launch_diff_decode(const Launch& L, const CacheView& C, const void* q, int q
       cudaFuncSetAttribute(diff_split_kernel, cudaFuncAttributePreferredSharedMemoryCarveout, 100) != cudaSuccess)
     return K8V4_ECUDA;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(ctas);
+  cfg.gridDim = dim3(ctas_of(L.num_sms));
   cfg.blockDim = dim3(32 * p.L.workers);
   cfg.dynamicSmemBytes = p.L.total;
   cfg.stream = L.stream;
@@ -941,18 +946,27 @@ int launch_diff_decode(const Launch& L, const CacheView& C, const void* q, int q
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   if (cudaLaunchKernelEx(&cfg, diff_split_kernel, mk, mv, p) != cudaSuccess) return K8V4_ECUDA;
-  if (cudaGetLastError() != cudaSuccess) return K8V4_ECUDA;
+  return cudaGetLastError() == cudaSuccess ? K8V4_OK : K8V4_ECUDA;
+}
+
+int launch_diff_decode(const Launch& L, const CacheView& C, const void* q, int q_dtype, const int32_t* pt, int64_t max_pages,
+                       const int32_t* lens, int n_seqs, int max_seq_len, float sm_scale, const k8v4_diff& diff, void* out,
+                       void* ws) {
+  DiffPieces pieces;
+  place_pieces(&pieces, static_cast<uint8_t*>(ws), static_cast<int64_t>(n_seqs) * C.H, L.num_sms);
+  const int rc = launch_diff_split(L, C, q, q_dtype, pt, max_pages, lens, DiffQueries{}, n_seqs, max_seq_len, sm_scale, pieces);
+  if (rc) return rc;
   CombineParams c;
-  c.ws = p.ws.rows;
+  c.ws = nullptr;
   c.r = DiffRagged{nullptr, nullptr};
-  c.pairs = p.ws.pairs;
+  c.pieces = pieces;
   c.lens = lens;
   c.H = C.H;
   c.n_rows = n_seqs * C.H * kGqa;
   c.d = diff;
   c.out = static_cast<uint16_t*>(out);
   // the pieces are one to an SM: few pairs have many each
-  if (n_seqs * C.H * 8 <= ctas) return launch_behind(L, diff_combine_kernel<16, false>, dim3(c.n_rows), dim3(512), c);
+  if (n_seqs * C.H * 8 <= ctas_of(L.num_sms)) return launch_behind(L, diff_combine_kernel<16, false>, dim3(c.n_rows), dim3(512), c);
   return launch_behind(L, diff_combine_kernel<4, false>, dim3(c.n_rows), dim3(kCombineThreads), c);
 }
 

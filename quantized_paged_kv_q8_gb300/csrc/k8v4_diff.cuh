@@ -14,15 +14,33 @@ constexpr int kDiffRow = 260;
 // then (2 * pairs / H, rounded up)
 constexpr int kDiffMostPairs = 128, kDiffMostRanges = 2 * kDiffMostPairs + 2;
 
-// A ragged batch's rows: each packed token's tile (-1: no sequence's), and the tiles of 8
-// words: [1] the first token, [3] ranges, [4] the first block.  Range s of map m of query head
-// h, KV head g, is in block first + (2 g + m) * ranges + s, row (token - first token) * 8 + h,
-// blocks of 256 rows.
+// Single queries over the line of their tiles (k8v4_diff.cu): of each pair (query, KV head) its
+// first block and their number, and the blocks of 16 partial rows (map, query head).
+struct DiffPieces {
+  int2* pairs;
+  float* rows;
+  int blocks;                 // that there is room for
+};
+size_t place_pieces(DiffPieces* p, uint8_t* ws, int64_t n_pairs, int num_sms);
+// a ragged batch's: the sequence and the packed token of each query, and how many there are (device)
+struct DiffQueries {
+  const int32_t* seq = nullptr;
+  const int32_t* tok = nullptr;
+  const int32_t* count = nullptr;
+};
+int launch_diff_split(const Launch& L, const CacheView& C, const void* q, int q_dtype, const int32_t* pt, int64_t max_pages,
+                      const int32_t* lens, const DiffQueries& rows, int n_seqs, int max_seq_len, float sm_scale,
+                      const DiffPieces& ws);
+
+// A ragged batch's rows: each packed token's tile, or -1 (no sequence's), or -2 - query (one of the
+// single queries above); and the tiles of 8 words: [1] the first token, [3] ranges, [4] the first
+// block.  Range s of map m of query head h, KV head g, is in block first + (2 g + m) * ranges + s,
+// row (token - first token) * 8 + h, blocks of 256 rows.
 struct DiffRagged {
   const int32_t* tok_tile;
   const int32_t* tiles;
 };
-int launch_diff_combine_ragged(const Launch& L, const float* ws, const DiffRagged& r, int n_tok, int H, bool wide,
-                               const k8v4_diff& diff, void* out);
+int launch_diff_combine_ragged(const Launch& L, const float* ws, const DiffRagged& r, const DiffPieces& pieces,
+                               const int32_t* lens, int n_tok, int H, bool few, const k8v4_diff& diff, void* out);
 
 }  // namespace k8v4

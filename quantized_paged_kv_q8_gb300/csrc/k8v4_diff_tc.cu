@@ -45,7 +45,9 @@
 //
 // The units come from a schedule that one CTA works out on the device from the lengths:
 // token tiles, heaviest first within a sequence, cut into ranges so that the pairs of the
-// device are evenly loaded.
+// device are evenly loaded.  Sequences of few tokens would leave most of a tile's 256 rows empty;
+// where it is estimated to be faster their tokens go through the single queries' kernel
+// (k8v4_diff.cu) one by one.
 //
 // Tensor memory (512 columns): S [0,128), P [128,192) and [192,256), O [256,512).
 //
@@ -111,7 +113,10 @@ constexpr uint32_t kTmemCols = 512, kPCol = 128, kPBuf = 64, kOCol = 256;
 
 // ---------------------------------------------------------------- the schedule
 constexpr int kTileTok = 32;                  // tokens of a token tile
-constexpr int kMostWaves = 4;                 // ranges: at most this many per pair of the device, on average
+// ranges: room for so many units more than token tiles, per pair of the device: four where there are
+// few tiles, two where the tiles alone are several rounds (every unit without work costs a launch of
+// two empty CTAs: 12 prompts of 900 tokens 208 us with four, 197 with two; 300 tokens behind 100,000 649 and 721)
+constexpr int kMostWaves = 4, kFewWaves = 2;
 struct TokenTile {
   int seq, tok0, n, splits, first, cell_tiles, vis0, most;   // vis0: cells that its first token sees (causal), or the steps' bound
 };
@@ -122,19 +127,28 @@ struct Unit {
 };
 
 struct Schedule {                             // places in the workspace
-  int32_t* head;                              // [0] units, [1] token tiles
+  int32_t* head;                              // [0] units, [1] token tiles, [2] single queries
   int32_t* tile_end;                          // [n_seqs] token tiles up to each sequence
   TokenTile* tiles;
-  int32_t* tok_tile;                          // [n_tok], -1: no sequence
+  int32_t* tok_tile;                          // [n_tok], -1: no sequence's, -2 - query: a single query
+  int32_t* row_seq;                           // of each single query
+  int32_t* row_tok;
+  int32_t* row_vis;
+  DiffPieces pieces;
   Unit* units;
   float* rows;                                // partial blocks of 256 rows
 };
+constexpr int kMostFew = 8;                   // tokens of a sequence that may go one by one
+int64_t most_rows(int n_seqs, int n_tok) { return std::min<int64_t>(n_tok, static_cast<int64_t>(kMostFew) * n_seqs); }
 int64_t most_tiles(int n_seqs, int n_tok) { return n_tok / kTileTok + std::min(n_seqs, n_tok); }
+int64_t more_units(int64_t base, int pairs) {
+  return std::max(static_cast<int64_t>(kFewWaves) * pairs, static_cast<int64_t>(kMostWaves) * pairs - base);
+}
 int64_t most_units(int n_seqs, int n_tok, int max_seq_len, int H, int pairs) {
   const int64_t base = most_tiles(n_seqs, n_tok) * 2 * H;
-  return std::min(base * std::max(1, (max_seq_len + kTileN - 1) / kTileN), base + static_cast<int64_t>(kMostWaves) * pairs);
+  return std::min(base * std::max(1, (max_seq_len + kTileN - 1) / kTileN), base + more_units(base, pairs));
 }
-size_t place(Schedule* s, uint8_t* ws, int n_seqs, int n_tok, int max_seq_len, int H, int pairs) {
+size_t place(Schedule* s, uint8_t* ws, int n_seqs, int n_tok, int max_seq_len, int H, int pairs, int num_sms) {
   size_t at = 0;
   auto take = [&](size_t bytes) {
     uint8_t* p = ws + at;
@@ -143,10 +157,15 @@ size_t place(Schedule* s, uint8_t* ws, int n_seqs, int n_tok, int max_seq_len, i
   };
   const int64_t tiles = most_tiles(n_seqs, n_tok), units = most_units(n_seqs, n_tok, max_seq_len, H, pairs);
   Schedule t;
-  t.head = reinterpret_cast<int32_t*>(take(8));
+  t.head = reinterpret_cast<int32_t*>(take(12));
   t.tile_end = reinterpret_cast<int32_t*>(take(4 * static_cast<size_t>(n_seqs)));
   t.tiles = reinterpret_cast<TokenTile*>(take(sizeof(TokenTile) * tiles));
   t.tok_tile = reinterpret_cast<int32_t*>(take(4 * static_cast<size_t>(n_tok)));
+  const int64_t rows = most_rows(n_seqs, n_tok);
+  t.row_seq = reinterpret_cast<int32_t*>(take(4 * static_cast<size_t>(rows)));
+  t.row_tok = reinterpret_cast<int32_t*>(take(4 * static_cast<size_t>(rows)));
+  t.row_vis = reinterpret_cast<int32_t*>(take(4 * static_cast<size_t>(rows)));
+  place_pieces(&t.pieces, take(place_pieces(nullptr, nullptr, rows * H, num_sms)), rows * H, num_sms);
   t.units = reinterpret_cast<Unit*>(take(sizeof(Unit) * units));
   t.rows = reinterpret_cast<float*>(take(static_cast<size_t>(units) * 2 * kRows * kDiffRow * sizeof(float)));
   if (s) *s = t;
@@ -159,7 +178,7 @@ struct ScheduleParams {
   const int32_t* lens;
   const int32_t* steps;
   int n_seqs, n_tok, max_seq_len, H, pairs;
-  int64_t most;                               // units that there is room for
+  int64_t most, more, most_rows;                    // units, units beyond one a tile, and single queries that there is room for
   int* status;
 };
 
@@ -193,15 +212,17 @@ constexpr int kShortList = 4096;
 __global__ void __launch_bounds__(1024, 1) diff_schedule_kernel(const ScheduleParams p) {
   __shared__ int red[32];
   __shared__ float cost_s[32];
-  __shared__ int top_s;
+  __shared__ int top_s, few_n;
   __shared__ int ends_s[kShortList], cells_s[kShortList];
+  __shared__ unsigned long long few_s[kMostFew + 1];           // sixteens of cells of the sequences of so many tokens; [0] of the others' token tiles
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (threadIdx.x <= kMostFew) few_s[threadIdx.x] = 0;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const Schedule& s = p.s;
-  if (tid == 0) top_s = 0;
   for (int t = tid; t < p.n_tok; t += 1024) s.tok_tile[t] = -1;
-  // ---- token tiles of the sequences
+  __syncthreads();
+  // ---- the sequences' tokens and cells
   int* const ends = p.n_seqs <= kShortList ? ends_s : s.tile_end;
   const int per = (p.n_seqs + 1023) / 1024;
   const int b0 = min(p.n_seqs, tid * per), b1 = min(p.n_seqs, b0 + per);
@@ -210,20 +231,79 @@ __global__ void __launch_bounds__(1024, 1) diff_schedule_kernel(const SchedulePa
     const int end = p.offsets[b + 1];
     return first < 0 || end < first || end > p.n_tok ? -1 : end - first;
   };
-  int sum = 0, n_tiles;
+  auto len_of = [&](int b) { return min(max(p.lens[b], 0), p.max_seq_len); };
+  for (int b = b0; b < b1; ++b) {
+    int first;
+    const int n = tokens_of(b, first), len = p.lens[b];
+    if (n < 0 || len < 0 || len > p.max_seq_len) record_status(p.status, K8V4_ERANGE);
+    const unsigned long long t16 = (len_of(b) + 15) >> 4;
+    if (n > 0) atomicAdd(few_s + (n <= kMostFew ? n : 0), n <= kMostFew ? t16 : t16 * ((n + kTileTok - 1) / kTileTok));
+  }
+  __syncthreads();
+  // ---- up to how many tokens a sequence's go one by one: what leaves the shorter time, by rates
+  // measured at 2 KV heads (16 cells of one KV head: 1.4 ns a query, 6 ns a token tile that is mostly empty; a kernel
+  // that has work: 8 us and 14).  32 sequences of 8,192 cells: 81 us one by one against 228 for one token each, 221
+  // against 226 for four, 313 against 229 for six.  (One warp: the conversions of 64-bit sums are slow.)
+  if (warp == 0) {
+    const float t = lane <= kMostFew ? static_cast<float>(few_s[lane]) : 0.f;
+    float one = 0.f, tile = 0.f;
+#pragma unroll
+    for (int n = 0; n <= kMostFew; ++n) {
+      const float tn = __shfl_sync(kFull, t, n);
+      if (n >= 1 && n <= lane) one += 1.4f * n * tn;
+      else tile += 6.f * tn;
+    }
+    const float cost = lane > kMostFew ? INFINITY : (one + tile) * p.H + (one > 0.f ? 8000.f : 0.f) + (tile > 0.f ? 14000.f : 0.f);
+    float best = cost;
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) best = fminf(best, __shfl_xor_sync(kFull, best, o));
+    if (lane == 0) top_s = 0;
+    const int at_best = 31 - __clz(__ballot_sync(kFull, cost == best));
+    if (lane == 0) few_n = at_best;
+  }
+  __syncthreads();
+  const int few = few_n;
+  // ---- their queries, and the others' token tiles
+  int sum = 0, rows = 0, n_tiles, n_rows;
   for (int b = b0; b < b1; ++b) {
     int first;
     const int n = tokens_of(b, first);
-    if (n < 0) record_status(p.status, K8V4_ERANGE);
-    sum += (max(n, 0) + kTileTok - 1) / kTileTok;
+    if (n > few) sum += (n + kTileTok - 1) / kTileTok;
+    else rows += max(n, 0);
     ends[b] = sum;                                             // of this thread's sequences so far
   }
   const int at = scan_block(sum, red, &n_tiles);
-  for (int b = b0; b < b1; ++b) ends[b] += at;
+  int row = scan_block(rows, red, &n_rows);
+  for (int b = b0; b < b1; ++b) {
+    ends[b] += at;
+    int first;
+    const int n = tokens_of(b, first);
+    if (n > few) continue;
+    const int len = len_of(b);
+    for (int k = 0; k < n; ++k, ++row) {
+      if (row >= p.most_rows) break;
+      int vis = p.steps ? p.steps[first + k] : max(len - n + k + 1, 0);
+      if (vis < 0 || vis > len) {
+        record_status(p.status, K8V4_ERANGE);
+        vis = vis < 0 ? 0 : len;
+      }
+      s.row_seq[row] = b;
+      s.row_tok[row] = first + k;
+      s.row_vis[row] = vis;
+      s.tok_tile[first + k] = -2 - row;
+    }
+  }
   // offsets that do not follow one another can claim more tiles than there is room for
   if (n_tiles > p.n_tok / kTileTok + min(p.n_seqs, p.n_tok)) {
     if (tid == 0) record_status(p.status, K8V4_ERANGE);
     n_tiles = 0;
+  }
+  if (n_tiles == 0) {
+    if (tid == 0) {
+      s.head[0] = s.head[1] = 0;
+      s.head[2] = static_cast<int>(min(static_cast<int64_t>(n_rows), p.most_rows));
+    }
+    return;
   }
   __syncthreads();
   // ---- each tile's tokens and cells
@@ -245,8 +325,7 @@ __global__ void __launch_bounds__(1024, 1) diff_schedule_kernel(const SchedulePa
     t.n = min(kTileTok, n - j * kTileTok);
     int len = p.lens[lo];
     if (len < 0 || len > p.max_seq_len) {
-      record_status(p.status, K8V4_ERANGE);
-      len = len < 0 ? 0 : p.max_seq_len;
+      len = len < 0 ? 0 : p.max_seq_len;                       // (recorded above)
     }
     t.vis0 = len - n + j * kTileTok + 1;
     int most = max(t.vis0 + t.n - 1, 0);
@@ -274,10 +353,10 @@ __global__ void __launch_bounds__(1024, 1) diff_schedule_kernel(const SchedulePa
   if (lane == 0) atomicMax(&top_s, top);
   __syncthreads();
   top = max(top_s, 1);
-  // ---- the range length: 32 candidates from what fills every pair kMostWaves times to no
+  // ---- the range length: 32 candidates from what makes all the units that there is room for to no
   // cut at all, each worked out by a warp: rounds x (range + a unit's fixed cost)
   const float units_per = 2.0f * p.H;
-  const int least = max(1, min(top, static_cast<int>(ceilf(units_per * total / (static_cast<float>(kMostWaves) * p.pairs)))));
+  const int least = max(1, min(top, static_cast<int>(ceilf(units_per * total / static_cast<float>(p.more)))));
   constexpr float kFixedTiles = 8.0f;
   auto candidate = [&](int k) {
     return max(least, min(top, static_cast<int>(ceilf(least * exp2f(log2f(static_cast<float>(top) / least) * k / 31.0f)))));
@@ -302,17 +381,30 @@ __global__ void __launch_bounds__(1024, 1) diff_schedule_kernel(const SchedulePa
   for (int i = i0; i < i1; ++i) mine += ((brief ? cells_s[i] : s.tiles[i].cell_tiles) + range - 1) / range * 2 * p.H;
   int u = scan_block(mine, red, &all);
   for (int i = i0; i < i1; ++i) {
-    const TokenTile t = s.tiles[i];
-    const int sp = (t.cell_tiles + range - 1) / range, len = sp ? (t.cell_tiles + sp - 1) / sp : 0;
+    const int ct = brief ? cells_s[i] : s.tiles[i].cell_tiles, sp = (ct + range - 1) / range;
     s.tiles[i].splits = sp;
     s.tiles[i].first = u;
-    for (int k = 0; k < 2 * p.H; ++k)
-      for (int c = 0; c < sp; ++c, ++u)
-        if (u < p.most) s.units[u] = Unit{t.seq, t.tok0, t.n, t.vis0, c * len, min(len, t.cell_tiles - c * len), t.most, k};
+    if (brief) ends_s[i] = u;                                  // (the sequences' ends are done with)
+    u += 2 * p.H * sp;
+  }
+  all = static_cast<int>(min(static_cast<int64_t>(all), p.most));
+  __syncthreads();
+  auto first_of = [&](int i) { return brief ? ends_s[i] : s.tiles[i].first; };
+  for (int v = tid; v < all; v += 1024) {
+    int lo = 0, hi = n_tiles - 1;                              // the last tile that begins at or ahead of v (tiles without
+    while (lo < hi) {                                          // units begin where the next one does)
+      const int mid = (lo + hi + 1) >> 1;
+      if (first_of(mid) <= v) lo = mid;
+      else hi = mid - 1;
+    }
+    const TokenTile t = s.tiles[lo];
+    const int len = (t.cell_tiles + t.splits - 1) / t.splits, k = (v - t.first) / t.splits, c = (v - t.first) - k * t.splits;
+    s.units[v] = Unit{t.seq, t.tok0, t.n, t.vis0, c * len, min(len, t.cell_tiles - c * len), t.most, k};
   }
   if (tid == 0) {
-    s.head[0] = static_cast<int>(min(static_cast<int64_t>(all), p.most));
+    s.head[0] = all;
     s.head[1] = n_tiles;
+    s.head[2] = static_cast<int>(min(static_cast<int64_t>(n_rows), p.most_rows));
   }
 }
 
@@ -1106,7 +1198,7 @@ int planned_pairs(int num_sms) { return std::max(1, std::min(num_sms / 2, kDiffM
 }  // namespace
 
 size_t diff_ws_bytes(const CacheView& C, int n_seqs, int n_tok, int max_seq_len, int num_sms) {
-  return place(nullptr, nullptr, n_seqs, n_tok, max_seq_len, C.H, planned_pairs(num_sms));
+  return place(nullptr, nullptr, n_seqs, n_tok, max_seq_len, C.H, planned_pairs(num_sms), num_sms);
 }
 
 int launch_diff(const Launch& L, const CacheView& C, const void* q, int q_dtype, const int32_t* offsets, int n_tok,
@@ -1115,7 +1207,7 @@ int launch_diff(const Launch& L, const CacheView& C, const void* q, int q_dtype,
   if (device_pairs() < 1) return K8V4_ECUDA;
   const int pairs = planned_pairs(L.num_sms);
   ScheduleParams sp;
-  place(&sp.s, static_cast<uint8_t*>(ws), n_seqs, n_tok, max_seq_len, C.H, pairs);
+  place(&sp.s, static_cast<uint8_t*>(ws), n_seqs, n_tok, max_seq_len, C.H, pairs, L.num_sms);
   sp.offsets = offsets;
   sp.lens = lens;
   sp.steps = steps;
@@ -1125,8 +1217,13 @@ int launch_diff(const Launch& L, const CacheView& C, const void* q, int q_dtype,
   sp.H = C.H;
   sp.pairs = pairs;
   sp.most = most_units(n_seqs, n_tok, max_seq_len, C.H, pairs);
+  sp.more = more_units(most_tiles(n_seqs, n_tok) * 2 * C.H, pairs);
+  sp.most_rows = most_rows(n_seqs, n_tok);
   sp.status = L.status;
   int rc = launch_behind(L, diff_schedule_kernel, dim3(1), dim3(1024), sp);
+  if (rc) return rc;
+  rc = launch_diff_split(L, C, q, q_dtype, pt, max_pages, sp.s.row_vis, DiffQueries{sp.s.row_seq, sp.s.row_tok, sp.s.head + 2}, 0,
+                         max_seq_len, sm_scale, sp.s.pieces);
   if (rc) return rc;
   PairParams p;
   p.C = C;
@@ -1162,8 +1259,8 @@ int launch_diff(const Launch& L, const CacheView& C, const void* q, int q_dtype,
   r.tok_tile = sp.s.tok_tile;
   r.tiles = reinterpret_cast<const int32_t*>(sp.s.tiles);
   // few token tiles: their rows have tens of ranges each, and a row gets four warps
-  const bool wide = most_tiles(n_seqs, n_tok) * 2 * C.H < pairs;
-  return launch_diff_combine_ragged(L, sp.s.rows, r, n_tok, C.H, wide, diff, out);
+  const bool few = most_tiles(n_seqs, n_tok) * 2 * C.H < pairs;
+  return launch_diff_combine_ragged(L, sp.s.rows, r, sp.s.pieces, sp.s.row_vis, n_tok, C.H, few, diff, out);
 }
 
 }  // namespace k8v4
