@@ -357,6 +357,8 @@ __global__ void __launch_bounds__(1024, 1) diff_schedule_kernel(const SchedulePa
   // cut at all, each worked out by a warp: rounds x (range + a unit's fixed cost)
   const float units_per = 2.0f * p.H;
   const int least = max(1, min(top, static_cast<int>(ceilf(units_per * total / static_cast<float>(p.more)))));
+  // (what a unit takes beside its tiles: launch, query, first products 4.7 us, O and its rows 4.3, hand-over 1, at
+  // 1.29 us a tile: 12 prompts of 900 tokens)
   constexpr float kFixedTiles = 8.0f;
   auto candidate = [&](int k) {
     return max(least, min(top, static_cast<int>(ceilf(least * exp2f(log2f(static_cast<float>(top) / least) * k / 31.0f)))));
@@ -663,12 +665,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     __syncwarp();
   };
-  // the first tiles, while the others set Q up: their barriers are the CTA's own, and the three warps
+  // the first tile, while the others set Q up: their barriers are the CTA's own, and the three warps
   // see them initialised
   if (warp >= kLoadWarp0) {
     asm volatile("barrier.cta.sync 3, %0;" ::"n"(32 * kLoadWarps) : "memory");
     page_next = lookup(0);
-    for (int i = 0; i < min(n_tiles, p.stages); ++i) load_tile(i, i);
+    load_tile(0, 0);                                       // (a tile's copies take a warp up to 800 clocks to issue: the others after the barrier)
   }
 
   // ---- visibility of this thread's row
@@ -678,31 +680,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     my_vis = p.steps ? max(0, min(__ldcg(p.steps + t), vis0)) : max(0, vis0 + t - tok0);
   }
   // ---- Q rows of this map -> fp16 with a power of two per row, swizzled K-major: half a warp
-  // takes a row at a time (8 elements a lane)
+  // takes a row at a time (8 elements a lane); every load goes out ahead of the first use (one row after
+  // the other took 3.2 us of a unit's 10.5 beside its tiles)
   if (warp < kIssueWarp) {
     constexpr int kPer = kRows / (2 * kIssueWarp);
     const int sub = lane >> 4, l16 = lane & 15;
+    uint4 qa[kPer], qb[kPer];
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
       const int r = 2 * (warp + kIssueWarp * j) + sub;
-      float x[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+      qa[j] = qb[j] = make_uint4(0, 0, 0, 0);
       if (r / kGqa < tok_n) {
         const int64_t e0 = (static_cast<int64_t>(tok_first + r / kGqa) * HQ + g * kGqa + r % kGqa) * kD + 128 * map + 8 * l16;
-        if (p.q_f32) {
-          const float4* src = reinterpret_cast<const float4*>(static_cast<const float*>(p.q) + e0);
-          const float4 a = __ldcg(src), b = __ldcg(src + 1);
-          x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-          x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-        } else {
-          const uint4 a = __ldcg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + e0));
-          const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            x[2 * u] = __uint_as_float(w[u] << 16);
-            x[2 * u + 1] = __uint_as_float(w[u] & 0xffff0000u);
-          }
-        }
+        const uint4* src = p.q_f32 ? reinterpret_cast<const uint4*>(static_cast<const float*>(p.q) + e0)
+                                   : reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + e0);
+        qa[j] = __ldcg(src);
+        if (p.q_f32) qb[j] = __ldcg(src + 1);
       }
+    }
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const int r = 2 * (warp + kIssueWarp * j) + sub;
+      const uint32_t w[8] = {qa[j].x, qa[j].y, qa[j].z, qa[j].w, qb[j].x, qb[j].y, qb[j].z, qb[j].w};
+      float x[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u)
+        x[u] = __uint_as_float(p.q_f32 ? w[u] : (u & 1) ? w[u >> 1] & 0xffff0000u : w[u >> 1] << 16);
       float amax = 0.0f;
 #pragma unroll
       for (int u = 0; u < 8; ++u) amax = fmaxf(amax, fabsf(x[u]));
@@ -1066,10 +1069,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
     } else {
       // ============================================================== copies
-      int i = min(n_tiles, p.stages), stage = i == p.stages ? 0 : i;
-      uint32_t phase = 0;                                  // of the stage's last use
+      int i = 1, stage = 1 % p.stages;
+      uint32_t phase = p.stages == 1 ? 0 : 1;              // of the stage's last use
       for (; i < n_tiles; ++i) {
-        if (!__all_sync(kFull, wait_soon(bars + 8 * (kBarRawEmpty + stage), phase, p.wait_ns))) { ctl[1] = 1; break; }
+        if (i >= p.stages && !__all_sync(kFull, wait_soon(bars + 8 * (kBarRawEmpty + stage), phase, p.wait_ns))) { ctl[1] = 1; break; }
         load_tile(i, stage);
         if (++stage == p.stages) {
           stage = 0;
@@ -1136,8 +1139,7 @@ int device_pairs() {
   }
   return g_pairs[dev] = pairs;
 }
-// The tensor maps of a cache's K and V rows as the decode's, with boxes of `box` cells; those of
-// the last caches are kept (encoding is host work)
+// A tensor map of a cache's K or V rows as the decode's, with boxes of `box` cells
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
   static std::once_flag once;
@@ -1160,36 +1162,6 @@ bool encode_rows(CUtensorMap* m, const CacheView& C, int64_t run_off, int row_by
   const cuuint32_t shape[4] = {128, 1, static_cast<cuuint32_t>(box), 1}, one[4] = {1, 1, 1, 1};
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, C.pages + run_off, dims, strides, shape, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-struct MapEntry {
-  const uint8_t* pages = nullptr;
-  int64_t n_pages = 0;
-  int P = 0, H = 0;
-  CUtensorMap k, v;
-};
-std::mutex g_map_mu;
-MapEntry g_maps[64];
-int g_map_next = 0;
-bool boxed_maps(const CacheView& C, int box, CUtensorMap* k, CUtensorMap* v) {
-  std::lock_guard<std::mutex> lock(g_map_mu);
-  for (const MapEntry& e : g_maps) {
-    if (e.pages == C.pages && e.n_pages == C.n_pages && e.P == C.P && e.H == C.H) {   // the box goes by P
-      *k = e.k;
-      *v = e.v;
-      return true;
-    }
-  }
-  MapEntry& e = g_maps[g_map_next];
-  e.pages = nullptr;
-  if (!encode_rows(&e.k, C, 0, 256, box) || !encode_rows(&e.v, C, C.v_off(), 128, box)) return false;
-  e.pages = C.pages;
-  e.n_pages = C.n_pages;
-  e.P = C.P;
-  e.H = C.H;
-  g_map_next = (g_map_next + 1) % 64;
-  *k = e.k;
-  *v = e.v;
-  return true;
 }
 // the pairs that a workspace and its schedule are sized for: of the device's SMs, the same whether or
 // not the set-up has worked yet
@@ -1241,7 +1213,7 @@ int launch_diff(const Launch& L, const CacheView& C, const void* q, int q_dtype,
   p.stage_bytes = raw_bytes(C.H);
   p.box_shift = C.P % 64 == 0 ? 6 : C.P % 32 == 0 ? 5 : 4;
   CUtensorMap mk, mv;
-  if (!boxed_maps(C, 1 << p.box_shift, &mk, &mv)) return K8V4_ECUDA;
+  if (!encode_rows(&mk, C, 0, 256, 1 << p.box_shift) || !encode_rows(&mv, C, C.v_off(), 128, 1 << p.box_shift)) return K8V4_ECUDA;
   if (2 * sp.most > INT32_MAX) return K8V4_EINVAL;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(2 * sp.most));
