@@ -11,8 +11,8 @@
 //   S_m^T = K_m q_m^T    8 + 8 products m16n8k16 (cells x 8 heads)
 //   O_m^T += V^T P_m^T   16 + 16 products (dims x 8 heads), V converted once
 // with K codes exact in fp16, q in fp16 (bf16 is exact after a power of two per row and
-// map), P and V rounded to fp16 once each: 2^-12 of each term, against the 2^-9 of the bf16
-// result, where the plain decode carries both in two terms (48 products of V, not 32, and
+// map), P and V rounded to fp16 once each: 2^-11 of each term at most, against the 2^-8 of the
+// bf16 result, where the plain decode carries both in two terms (48 products of V, not 32, and
 // for one map).
 //
 // The worker warps are the decode kernel's: they take a range's tiles in turn, each with a ring of
@@ -20,6 +20,13 @@
 // end to end, are cut into one equal piece for each SM, so that a ragged batch keeps every SM
 // busy to the end.  A piece covers one pair's cells or the end of one and the beginning of others;
 // each CTA finds its own from the lengths.
+//
+// What bounds it: the matrix instructions, about 6.8 clocks each on an SM (48 a tile: 32 us of one
+// sequence of 237,568 cells), beside the conversions of the codes (970 instructions a tile in
+// all); two warps a scheduler do not overlap them wholly.  That sequence, 2 KV heads: 56 us with the
+// joining, 3.4 TB/s of the cache's 194 MB; 32 sequences of up to 8,192 cells 37 us.  Two warps to a
+// worker, each with a map's scores and half of V's dims (16 warps of 128 registers, weights handed
+// over through shared memory): 63 us and 41.
 #include <algorithm>
 #include <climits>
 
@@ -711,7 +718,10 @@ __device__ __forceinline__ void finish_row(float v[8], const k8v4_diff& d, int l
 }
 
 // WARPS to a (row, query head): sixteen where a few rows have tens of ranges each (one sequence of
-// 237,568 cells: 16 rows of 76), one where there are thousands of rows of a few.
+// 237,568 cells: 16 rows of 76, 10 us cold), one where there are thousands of rows of a few (11,700 CTAs
+// of four rows: 33 us for 97 MB of partial rows and 24 MB of results, bound by its instructions), four
+// between.  Sixteen on more rows than SMs wait in line (78 registers: one row an SM): 256 rows of five
+// ranges 13 us, with four 8.8.
 template <int WARPS, bool RAGGED>
 __global__ void __launch_bounds__(WARPS > 4 ? 32 * WARPS : kCombineThreads, WARPS == 1 ? 10 : 1) diff_combine_kernel(const CombineParams p) {
   constexpr int kRowsCta = WARPS > 4 ? 1 : kCombineThreads / 32 / WARPS;

@@ -18,7 +18,7 @@
 //
 // Each CTA of the pair dequantises half of every tile (64 of the 128 cells of K, 128 of the
 // 256 dims of V); the pair reads both halves as one operand.  P and V are rounded to fp16
-// once (2^-12 of each term; the result is bf16), so a tile takes 8 products of 64 clocks for
+// once (2^-11 of each term at most; the result is bf16), so a tile takes 8 products of 64 clocks for
 // S and 8 of 128 for O where the exact kernels' two terms each would take three times the
 // latter.
 //
@@ -48,6 +48,10 @@
 // device are evenly loaded.  Sequences of few tokens would leave most of a tile's 256 rows empty;
 // where it is estimated to be faster their tokens go through the single queries' kernel
 // (k8v4_diff.cu) one by one.
+//
+// What bounds it: the products (1,536 of a tile's about 2,600 clocks) and what the row warps do
+// between them; 4,096 tokens on 32,768 cells 2.14 - 2.26 ms, 1.37 - 1.45 PFLOP/s.  Short units pay 10 us each
+// beside their tiles: 12 prompts of 900 tokens 195 us.
 //
 // Tensor memory (512 columns): S [0,128), P [128,192) and [192,256), O [256,512).
 //
