@@ -504,8 +504,14 @@ __global__ void __launch_bounds__(32 * kMaxWorkers, 1)
         for (int bp = 0; bp < 4; ++bp) {
           uint32_t R[4];
           ldmatrix_x4_t(R, st + vrow + 16 * ((2 * bp + (mi >> 1)) ^ vsw));
-          const uint32_t w0 = lds32(st + soff0 + 4 * bp), w1 = lds32(st + soff1 + 4 * bp);
-          const uint32_t w2 = lds32(st + soff0 + s8 + 4 * bp), w3 = lds32(st + soff1 + s8 + 4 * bp);
+          uint32_t w0 = lds32(st + soff0 + 4 * bp), w1 = lds32(st + soff1 + 4 * bp);
+          uint32_t w2 = lds32(st + soff0 + s8 + 4 * bp), w3 = lds32(st + soff1 + s8 + 4 * bp);
+          if (cell0 + 16 > c_end) {          // cells that nobody sees count with V = 0: their bytes are anything
+            if (cell0 + sigma(2 * c) >= c_end) w0 = 0;
+            if (cell0 + sigma(2 * c + 1) >= c_end) w1 = 0;
+            if (cell0 + 8 + sigma(2 * c) >= c_end) w2 = 0;
+            if (cell0 + 8 + sigma(2 * c + 1) >= c_end) w3 = 0;
+          }
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const uint32_t sel = h ? 0x7632u : 0x5410u;

@@ -1218,9 +1218,8 @@ int launch_diff(const Launch& L, const CacheView& C, const void* q, int q_dtype,
   p.box_shift = C.P % 64 == 0 ? 6 : C.P % 32 == 0 ? 5 : 4;
   CUtensorMap mk, mv;
   if (!encode_rows(&mk, C, 0, 256, 1 << p.box_shift) || !encode_rows(&mv, C, C.v_off(), 128, 1 << p.box_shift)) return K8V4_ECUDA;
-  if (2 * sp.most > INT32_MAX) return K8V4_EINVAL;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(2 * sp.most));
+  cfg.gridDim = dim3(static_cast<unsigned>(2 * sp.most));                // below 2^25 with n_tok < 2^24, n_seqs < 2^16
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = kRawOff + p.stages * p.stage_bytes;
   cfg.stream = L.stream;
