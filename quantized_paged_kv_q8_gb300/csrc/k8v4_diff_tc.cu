@@ -119,7 +119,9 @@ constexpr uint32_t kTmemCols = 512, kPCol = 128, kPBuf = 64, kOCol = 256;
 constexpr int kTileTok = 32;                  // tokens of a token tile
 // ranges: room for so many units more than token tiles, per pair of the device: four where there are
 // few tiles, two where the tiles alone are several rounds (every unit without work costs a launch of
-// two empty CTAs: 12 prompts of 900 tokens 208 us with four, 197 with two; 300 tokens behind 100,000 649 and 721)
+// two empty CTAs: 12 prompts of 900 tokens 208 us with four, 197 with two; 300 tokens behind 100,000 649 and 721),
+// one where few tokens a sequence leave the tiles without work most often (8 sequences of up to
+// 5 tokens 53.0 us with four, 51.4 with one)
 constexpr int kMostWaves = 4, kFewWaves = 2;
 struct TokenTile {
   int seq, tok0, n, splits, first, cell_tiles, vis0, most;   // vis0: cells that its first token sees (causal), or the steps' bound
@@ -145,12 +147,13 @@ struct Schedule {                             // places in the workspace
 constexpr int kMostFew = 8;                   // tokens of a sequence that may go one by one
 int64_t most_rows(int n_seqs, int n_tok) { return std::min<int64_t>(n_tok, static_cast<int64_t>(kMostFew) * n_seqs); }
 int64_t most_tiles(int n_seqs, int n_tok) { return n_tok / kTileTok + std::min(n_seqs, n_tok); }
-int64_t more_units(int64_t base, int pairs) {
+int64_t more_units(int64_t base, int pairs, int n_seqs, int n_tok) {
+  if (n_tok <= static_cast<int64_t>(kMostFew) * n_seqs) return pairs;
   return std::max(static_cast<int64_t>(kFewWaves) * pairs, static_cast<int64_t>(kMostWaves) * pairs - base);
 }
 int64_t most_units(int n_seqs, int n_tok, int max_seq_len, int H, int pairs) {
   const int64_t base = most_tiles(n_seqs, n_tok) * 2 * H;
-  return std::min(base * std::max(1, (max_seq_len + kTileN - 1) / kTileN), base + more_units(base, pairs));
+  return std::min(base * std::max(1, (max_seq_len + kTileN - 1) / kTileN), base + more_units(base, pairs, n_seqs, n_tok));
 }
 size_t place(Schedule* s, uint8_t* ws, int n_seqs, int n_tok, int max_seq_len, int H, int pairs, int num_sms) {
   size_t at = 0;
@@ -209,18 +212,20 @@ __device__ __forceinline__ int scan_block(int v, int* red, int* total) {   // 1,
 }
 
 // One CTA.  Token tiles of each sequence, the last first (it sees the most cells); the range
-// length that keeps the pairs of the device evenly loaded; the units in the tiles' order.  What
-// is searched and counted stays in shared memory while the lists are short (a search of a
-// list in global memory is a chain of reads of 300 ns each).
-constexpr int kShortList = 4096;
+// length that keeps the pairs of the device evenly loaded; the units.  What is searched and
+// counted stays in shared memory while the lists are short (a search of a list in global
+// memory is a chain of reads of 300 ns each).
+constexpr int kShortList = 4096, kBuckets = 256;
 __global__ void __launch_bounds__(1024, 1) diff_schedule_kernel(const ScheduleParams p) {
   __shared__ int red[32];
   __shared__ float cost_s[32];
   __shared__ int top_s, few_n;
   __shared__ int ends_s[kShortList], cells_s[kShortList];
   __shared__ unsigned long long few_s[kMostFew + 1];           // sixteens of cells of the sequences of so many tokens; [0] of the others' token tiles
+  __shared__ int bucket_s[kBuckets];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (threadIdx.x <= kMostFew) few_s[threadIdx.x] = 0;
+  if (threadIdx.x < kBuckets) bucket_s[threadIdx.x] = 0;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const Schedule& s = p.s;
@@ -380,32 +385,51 @@ __global__ void __launch_bounds__(1024, 1) diff_schedule_kernel(const SchedulePa
     for (int o = 16; o >= 1; o >>= 1) best = fminf(best, __shfl_xor_sync(kFull, best, o));
     range = candidate(31 - __clz(__ballot_sync(kFull, cost_s[lane] == best)));
   }
-  // ---- the units
-  const int tiles_per = (n_tiles + 1023) / 1024;
-  const int i0 = min(n_tiles, tid * tiles_per), i1 = min(n_tiles, i0 + tiles_per);
-  int mine = 0, all;
-  for (int i = i0; i < i1; ++i) mine += ((brief ? cells_s[i] : s.tiles[i].cell_tiles) + range - 1) / range * 2 * p.H;
-  int u = scan_block(mine, red, &all);
-  for (int i = i0; i < i1; ++i) {
-    const int ct = brief ? cells_s[i] : s.tiles[i].cell_tiles, sp = (ct + range - 1) / range;
-    s.tiles[i].splits = sp;
-    s.tiles[i].first = u;
-    if (brief) ends_s[i] = u;                                  // (the sequences' ends are done with)
-    u += 2 * p.H * sp;
+  // ---- the units, the longest first, so that the pairs finish together (40 sequences of up to 300 tokens: 154 us in the
+  // tiles' order, 144 so); a long list stays in the tiles' order
+  int all;
+  if (brief) {
+    auto splits_of = [&](int i) { return (cells_s[i] + range - 1) / range; };
+    auto bucket_of = [&](int i, int sp) {                      // by the tiles of a unit, at most `range`
+      return kBuckets - 1 - ((cells_s[i] + sp - 1) / sp) * (kBuckets - 1) / range;
+    };
+    for (int i = tid; i < n_tiles; i += 1024) {
+      const int sp = splits_of(i);
+      if (sp) atomicAdd(bucket_s + bucket_of(i, sp), sp * 2 * p.H);
+    }
+    __syncthreads();
+    const int mine = tid < kBuckets ? bucket_s[tid] : 0;
+    const int before = scan_block(mine, red, &all);
+    if (tid < kBuckets) bucket_s[tid] = before;
+    __syncthreads();
+    for (int i = tid; i < n_tiles; i += 1024) {                // (the order within a bucket moves where rows are kept, not what is in them)
+      const int sp = splits_of(i);
+      s.tiles[i].splits = sp;
+      s.tiles[i].first = sp ? atomicAdd(bucket_s + bucket_of(i, sp), sp * 2 * p.H) : 0;
+    }
+  } else {
+    const int tiles_per = (n_tiles + 1023) / 1024;
+    const int i0 = min(n_tiles, tid * tiles_per), i1 = min(n_tiles, i0 + tiles_per);
+    int mine = 0;
+    for (int i = i0; i < i1; ++i) mine += (s.tiles[i].cell_tiles + range - 1) / range * 2 * p.H;
+    int u = scan_block(mine, red, &all);
+    for (int i = i0; i < i1; ++i) {
+      const int sp = (s.tiles[i].cell_tiles + range - 1) / range;
+      s.tiles[i].splits = sp;
+      s.tiles[i].first = u;
+      u += 2 * p.H * sp;
+    }
   }
   all = static_cast<int>(min(static_cast<int64_t>(all), p.most));
   __syncthreads();
-  auto first_of = [&](int i) { return brief ? ends_s[i] : s.tiles[i].first; };
-  for (int v = tid; v < all; v += 1024) {
-    int lo = 0, hi = n_tiles - 1;                              // the last tile that begins at or ahead of v (tiles without
-    while (lo < hi) {                                          // units begin where the next one does)
-      const int mid = (lo + hi + 1) >> 1;
-      if (first_of(mid) <= v) lo = mid;
-      else hi = mid - 1;
+  for (int i = warp; i < n_tiles; i += 32) {                   // a warp writes a tile's units
+    const TokenTile t = s.tiles[i];
+    if (t.splits == 0) continue;
+    const int len = (t.cell_tiles + t.splits - 1) / t.splits, units = 2 * p.H * t.splits;
+    for (int v = lane; v < units && t.first + v < all; v += 32) {
+      const int k = v / t.splits, c = v - k * t.splits;
+      s.units[t.first + v] = Unit{t.seq, t.tok0, t.n, t.vis0, c * len, min(len, t.cell_tiles - c * len), t.most, k};
     }
-    const TokenTile t = s.tiles[lo];
-    const int len = (t.cell_tiles + t.splits - 1) / t.splits, k = (v - t.first) / t.splits, c = (v - t.first) - k * t.splits;
-    s.units[v] = Unit{t.seq, t.tok0, t.n, t.vis0, c * len, min(len, t.cell_tiles - c * len), t.most, k};
   }
   if (tid == 0) {
     s.head[0] = all;
@@ -1193,7 +1217,7 @@ int launch_diff(const Launch& L, const CacheView& C, const void* q, int q_dtype,
   sp.H = C.H;
   sp.pairs = pairs;
   sp.most = most_units(n_seqs, n_tok, max_seq_len, C.H, pairs);
-  sp.more = more_units(most_tiles(n_seqs, n_tok) * 2 * C.H, pairs);
+  sp.more = more_units(most_tiles(n_seqs, n_tok) * 2 * C.H, pairs, n_seqs, n_tok);
   sp.most_rows = most_rows(n_seqs, n_tok);
   sp.status = L.status;
   int rc = launch_behind(L, diff_schedule_kernel, dim3(1), dim3(1024), sp);
