@@ -662,18 +662,6 @@ struct CombineParams {
 };
 constexpr int kCombineThreads = 128;        // or 32 WARPS, where a row takes more
 
-// the first warps of a row: exp(q1 . k1) and exp(q2 . k2) of its head (0 without vectors)
-__device__ __forceinline__ float lambda_term(const k8v4_diff& d, int hq, int term, int lane) {
-  if (!d.lambda_q1) return 0.0f;
-  const int64_t at = (d.n_lambda > 1 ? hq * 128 : 0) + 4 * lane;
-  const float4 a = *reinterpret_cast<const float4*>((term ? d.lambda_q2 : d.lambda_q1) + at);
-  const float4 b = *reinterpret_cast<const float4*>((term ? d.lambda_k2 : d.lambda_k1) + at);
-  float dot = a.x * b.x + a.y * b.y + a.z * b.z + a.w * b.w;
-#pragma unroll
-  for (int o = 16; o >= 1; o >>= 1) dot += __shfl_xor_sync(kFull, dot, o);
-  return expf(dot);
-}
-
 // a warp: the difference in rotated space (lane: dims 4 lane + e and 128 + 4 lane + e) brought
 // back (linear, so once for both maps), normed, scaled, rounded and written
 __device__ __forceinline__ void finish_row(float v[8], const k8v4_diff& d, int lane, uint16_t* out) {
@@ -689,11 +677,10 @@ __device__ __forceinline__ void finish_row(float v[8], const k8v4_diff& d, int l
   }
 #pragma unroll
   for (int mm = 1; mm < 32; mm <<= 1) {
-    const bool upper = (lane & mm) != 0;
+    const float sign = (lane & mm) ? -1.0f : 1.0f;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const float tt = __shfl_xor_sync(kFull, v[e], mm);
-      v[e] = upper ? tt - v[e] : v[e] + tt;
+      v[e] = fmaf(sign, v[e], __shfl_xor_sync(kFull, v[e], mm));       // (exactly the difference or the sum)
     }
   }
   float s2 = 0.0f;
@@ -725,11 +712,11 @@ __device__ __forceinline__ void finish_row(float v[8], const k8v4_diff& d, int l
 
 // WARPS to a (row, query head): sixteen where a few rows have tens of ranges each (one sequence of
 // 237,568 cells: 16 rows of 76, 10 us cold), one where there are thousands of rows of a few (11,700 CTAs
-// of four rows: 33 us for 97 MB of partial rows and 24 MB of results, bound by its instructions), four
-// between.  Sixteen on more rows than SMs wait in line (78 registers: one row an SM): 256 rows of five
+// of four rows, 97 MB of partial rows and 24 MB of results, bound by its instructions: 40 registers for
+// twelve CTAs an SM, the lambdas worked out ahead), four between.  Sixteen on more rows than SMs wait in line (78 registers: one row an SM): 256 rows of five
 // ranges 13 us, with four 8.8.
 template <int WARPS, bool RAGGED>
-__global__ void __launch_bounds__(WARPS > 4 ? 32 * WARPS : kCombineThreads, WARPS == 1 ? 10 : 1) diff_combine_kernel(const CombineParams p) {
+__global__ void __launch_bounds__(WARPS > 4 ? 32 * WARPS : kCombineThreads, WARPS == 1 ? 12 : 1) diff_combine_kernel(const CombineParams p) {
   constexpr int kRowsCta = WARPS > 4 ? 1 : kCombineThreads / 32 / WARPS;
   constexpr int kMost = kDiffMostRanges;
   __shared__ float wt[kRowsCta][2][kMost];
@@ -780,8 +767,7 @@ __global__ void __launch_bounds__(WARPS > 4 ? 32 * WARPS : kCombineThreads, WARP
       x[m][1] = __ldcs(src + 32 + lane);
       l[m] = base[m * m_stride + 257];
     }
-    const float t0 = lambda_term(p.d, hq, 0, lane), t1 = lambda_term(p.d, hq, 1, lane);
-    const float lambda = p.d.lambda_q1 ? t0 - t1 + p.d.lambda_init : p.d.lambda_init;
+    const float lambda = p.r.lambdas[hq];               // (only ragged batches have a warp to a row)
     const float f0 = l[0] > 0.0f ? 1.0f / l[0] : 0.0f, f1 = l[1] > 0.0f ? -lambda / l[1] : 0.0f;
     // (what a range in which the row sees nothing left in o counts with 0)
     float v[8];
@@ -807,11 +793,8 @@ __global__ void __launch_bounds__(WARPS > 4 ? 32 * WARPS : kCombineThreads, WARP
     if (WARPS > 1 && lane == 0) red[slot][0][m][warp] = Mx[m];
   }
   float term[2] = {0.0f, 0.0f};
-  if (WARPS == 1) {
-    term[0] = lambda_term(p.d, hq, 0, lane);
-    term[1] = lambda_term(p.d, hq, 1, lane);
-  } else if (warp < 2) {
-    const float e = lambda_term(p.d, hq, warp, lane);
+  if (!RAGGED && warp < 2) {
+    const float e = diff_lambda_term(p.d, hq, warp, lane);
     if (lane == 0) lam_s[warp] = e;
   }
   sync();
@@ -836,7 +819,7 @@ __global__ void __launch_bounds__(WARPS > 4 ? 32 * WARPS : kCombineThreads, WARP
   for (int m = 0; m < 2; ++m) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) acc[m][e] = 0.0f;
-    constexpr int kUnroll = WARPS == 1 ? 2 : 4;
+    constexpr int kUnroll = WARPS == 1 ? 1 : 4;
     for (int s0 = warp; s0 < splits; s0 += WARPS * kUnroll) {
       float4 x[kUnroll][2];
       float w[kUnroll];
@@ -865,8 +848,10 @@ __global__ void __launch_bounds__(WARPS > 4 ? 32 * WARPS : kCombineThreads, WARP
   if (WARPS > 1) {
     __syncthreads();
     if (warp) return;
-    term[0] = lam_s[0];
-    term[1] = lam_s[1];
+    if (!RAGGED) {
+      term[0] = lam_s[0];
+      term[1] = lam_s[1];
+    }
 #pragma unroll
     for (int m = 0; m < 2; ++m) {
       L[m] = 0.0f;
@@ -880,7 +865,7 @@ __global__ void __launch_bounds__(WARPS > 4 ? 32 * WARPS : kCombineThreads, WARP
       }
     }
   }
-  const float lambda = p.d.lambda_q1 ? term[0] - term[1] + p.d.lambda_init : p.d.lambda_init;
+  const float lambda = RAGGED ? p.r.lambdas[hq] : p.d.lambda_q1 ? term[0] - term[1] + p.d.lambda_init : p.d.lambda_init;
   const float f0 = L[0] > 0.0f ? 1.0f / L[0] : 0.0f, f1 = L[1] > 0.0f ? -lambda / L[1] : 0.0f;
   float v[8];
 #pragma unroll
@@ -974,7 +959,7 @@ int launch_diff_decode(const Launch& L, const CacheView& C, const void* q, int q
   if (rc) return rc;
   CombineParams c;
   c.ws = nullptr;
-  c.r = DiffRagged{nullptr, nullptr};
+  c.r = DiffRagged{nullptr, nullptr, nullptr};
   c.pieces = pieces;
   c.lens = lens;
   c.H = C.H;

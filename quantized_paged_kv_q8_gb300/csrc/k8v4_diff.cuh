@@ -32,11 +32,24 @@ int launch_diff_split(const Launch& L, const CacheView& C, const void* q, int q_
                       const int32_t* lens, const DiffQueries& rows, int n_seqs, int max_seq_len, float sm_scale,
                       const DiffPieces& ws);
 
+// a warp: exp(q1 . k1) (term 0) or exp(q2 . k2) of a query head, 0 without vectors
+__device__ __forceinline__ float diff_lambda_term(const k8v4_diff& d, int hq, int term, int lane) {
+  if (!d.lambda_q1) return 0.0f;
+  const int64_t at = (d.n_lambda > 1 ? hq * 128 : 0) + 4 * lane;
+  const float4 a = *reinterpret_cast<const float4*>((term ? d.lambda_q2 : d.lambda_q1) + at);
+  const float4 b = *reinterpret_cast<const float4*>((term ? d.lambda_k2 : d.lambda_k1) + at);
+  float dot = a.x * b.x + a.y * b.y + a.z * b.z + a.w * b.w;
+#pragma unroll
+  for (int o = 16; o >= 1; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+  return expf(dot);
+}
+
 // A ragged batch's rows: each packed token's tile, or -1 (no sequence's), or -2 - query (one of the
 // single queries above); and the tiles of 8 words: [1] the first token, [3] ranges, [4] the first
 // block.  Range s of map m of query head h, KV head g, is in block first + (2 g + m) * ranges + s,
 // row (token - first token) * 8 + h, blocks of 256 rows.
 struct DiffRagged {
+  const float* lambdas;       // of each query head
   const int32_t* tok_tile;
   const int32_t* tiles;
 };

@@ -51,7 +51,7 @@
 //
 // What bounds it: the products (1,536 of a tile's about 2,600 clocks) and what the row warps do
 // between them; 4,096 tokens on 32,768 cells 2.14 - 2.26 ms, 1.37 - 1.45 PFLOP/s.  Short units pay 10 us each
-// beside their tiles: 12 prompts of 900 tokens 195 us.
+// beside their tiles: 12 prompts of 900 tokens 190 us.
 //
 // Tensor memory (512 columns): S [0,128), P [128,192) and [192,256), O [256,512).
 //
@@ -134,6 +134,7 @@ struct Unit {
 
 struct Schedule {                             // places in the workspace
   int32_t* head;                              // [0] units, [1] token tiles, [2] single queries
+  float* lambdas;                             // [8 H]
   int32_t* tile_end;                          // [n_seqs] token tiles up to each sequence
   TokenTile* tiles;
   int32_t* tok_tile;                          // [n_tok], -1: no sequence's, -2 - query: a single query
@@ -165,6 +166,7 @@ size_t place(Schedule* s, uint8_t* ws, int n_seqs, int n_tok, int max_seq_len, i
   const int64_t tiles = most_tiles(n_seqs, n_tok), units = most_units(n_seqs, n_tok, max_seq_len, H, pairs);
   Schedule t;
   t.head = reinterpret_cast<int32_t*>(take(12));
+  t.lambdas = reinterpret_cast<float*>(take(sizeof(float) * kGqa * H));
   t.tile_end = reinterpret_cast<int32_t*>(take(4 * static_cast<size_t>(n_seqs)));
   t.tiles = reinterpret_cast<TokenTile*>(take(sizeof(TokenTile) * tiles));
   t.tok_tile = reinterpret_cast<int32_t*>(take(4 * static_cast<size_t>(n_tok)));
@@ -181,6 +183,7 @@ size_t place(Schedule* s, uint8_t* ws, int n_seqs, int n_tok, int max_seq_len, i
 
 struct ScheduleParams {
   Schedule s;
+  k8v4_diff d;
   const int32_t* offsets;
   const int32_t* lens;
   const int32_t* steps;
@@ -230,6 +233,11 @@ __global__ void __launch_bounds__(1024, 1) diff_schedule_kernel(const SchedulePa
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const Schedule& s = p.s;
   for (int t = tid; t < p.n_tok; t += 1024) s.tok_tile[t] = -1;
+  // ---- lambda of each head, for the joining (a warp there that works it out for its row: 5 of 12 900-token prompts' 195 us)
+  for (int hq = warp; hq < kGqa * p.H; hq += 32) {
+    const float t0 = diff_lambda_term(p.d, hq, 0, lane), t1 = diff_lambda_term(p.d, hq, 1, lane);
+    if (lane == 0) s.lambdas[hq] = p.d.lambda_q1 ? t0 - t1 + p.d.lambda_init : p.d.lambda_init;
+  }
   __syncthreads();
   // ---- the sequences' tokens and cells
   int* const ends = p.n_seqs <= kShortList ? ends_s : s.tile_end;
@@ -1208,6 +1216,7 @@ int launch_diff(const Launch& L, const CacheView& C, const void* q, int q_dtype,
   const int pairs = planned_pairs(L.num_sms);
   ScheduleParams sp;
   place(&sp.s, static_cast<uint8_t*>(ws), n_seqs, n_tok, max_seq_len, C.H, pairs, L.num_sms);
+  sp.d = diff;
   sp.offsets = offsets;
   sp.lens = lens;
   sp.steps = steps;
@@ -1255,6 +1264,7 @@ int launch_diff(const Launch& L, const CacheView& C, const void* q, int q_dtype,
   if (cudaLaunchKernelEx(&cfg, diff_pair_kernel, mk, mv, p) != cudaSuccess) return K8V4_ECUDA;
   if (cudaGetLastError() != cudaSuccess) return K8V4_ECUDA;
   DiffRagged r;
+  r.lambdas = sp.s.lambdas;
   r.tok_tile = sp.s.tok_tile;
   r.tiles = reinterpret_cast<const int32_t*>(sp.s.tiles);
   // few token tiles: their rows have tens of ranges each, and a row gets four warps
