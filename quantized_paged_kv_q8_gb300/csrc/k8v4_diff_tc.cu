@@ -222,10 +222,12 @@ constexpr int kShortList = 4096, kBuckets = 256;
 __global__ void __launch_bounds__(1024, 1) diff_schedule_kernel(const ScheduleParams p) {
   __shared__ int red[32];
   __shared__ float cost_s[32];
+  __shared__ int cand_s[32];
   __shared__ int top_s, few_n;
   __shared__ int ends_s[kShortList], cells_s[kShortList];
   __shared__ unsigned long long few_s[kMostFew + 1];           // sixteens of cells of the sequences of so many tokens; [0] of the others' token tiles
   __shared__ int bucket_s[kBuckets];
+  __shared__ uint8_t bucket_of[kShortList];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (threadIdx.x <= kMostFew) few_s[threadIdx.x] = 0;
   if (threadIdx.x < kBuckets) bucket_s[threadIdx.x] = 0;
@@ -235,8 +237,10 @@ __global__ void __launch_bounds__(1024, 1) diff_schedule_kernel(const SchedulePa
   for (int t = tid; t < p.n_tok; t += 1024) s.tok_tile[t] = -1;
   // ---- lambda of each head, for the joining (a warp there that works it out for its row: 5 of 12 900-token prompts' 195 us)
   for (int hq = warp; hq < kGqa * p.H; hq += 32) {
-    const float t0 = diff_lambda_term(p.d, hq, 0, lane), t1 = diff_lambda_term(p.d, hq, 1, lane);
-    if (lane == 0) s.lambdas[hq] = p.d.lambda_q1 ? t0 - t1 + p.d.lambda_init : p.d.lambda_init;
+    float l = 0.0f;
+#pragma unroll 1
+    for (int term = 0; term < 2; ++term) l = diff_lambda_term(p.d, hq, term, lane) - l;     // -(first - second)
+    if (lane == 0) s.lambdas[hq] = p.d.lambda_init - l;
   }
   __syncthreads();
   // ---- the sequences' tokens and cells
@@ -264,7 +268,7 @@ __global__ void __launch_bounds__(1024, 1) diff_schedule_kernel(const SchedulePa
   if (warp == 0) {
     const float t = lane <= kMostFew ? static_cast<float>(few_s[lane]) : 0.f;
     float one = 0.f, tile = 0.f;
-#pragma unroll
+#pragma unroll 1
     for (int n = 0; n <= kMostFew; ++n) {
       const float tn = __shfl_sync(kFull, t, n);
       if (n >= 1 && n <= lane) one += 1.4f * n * tn;
@@ -377,33 +381,31 @@ __global__ void __launch_bounds__(1024, 1) diff_schedule_kernel(const SchedulePa
   // (what a unit takes beside its tiles: launch, query, first products 4.7 us, O and its rows 4.3, hand-over 1, at
   // 1.29 us a tile: 12 prompts of 900 tokens)
   constexpr float kFixedTiles = 8.0f;
-  auto candidate = [&](int k) {
-    return max(least, min(top, static_cast<int>(ceilf(least * exp2f(log2f(static_cast<float>(top) / least) * k / 31.0f)))));
-  };
   int range = top;
   if (brief) {                                                 // long lists are not cut
-    const int cand = candidate(warp);
+    const int cand = max(least, min(top, static_cast<int>(ceilf(least * exp2f(log2f(static_cast<float>(top) / least) * warp / 31.0f)))));
     int units = 0;
     for (int i = lane; i < n_tiles; i += 32) units += (cells_s[i] + cand - 1) / cand;
     units = __reduce_add_sync(kFull, units);
-    if (lane == 0) cost_s[warp] = ceilf(units * units_per / p.pairs) * (cand + kFixedTiles);
+    if (lane == 0) cand_s[warp] = cand, cost_s[warp] = ceilf(units * units_per / p.pairs) * (cand + kFixedTiles);
     __syncthreads();
     float best = cost_s[lane];
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) best = fminf(best, __shfl_xor_sync(kFull, best, o));
-    range = candidate(31 - __clz(__ballot_sync(kFull, cost_s[lane] == best)));
+    range = cand_s[31 - __clz(__ballot_sync(kFull, cost_s[lane] == best))];
   }
   // ---- the units, the longest first, so that the pairs finish together (40 sequences of up to 300 tokens: 154 us in the
   // tiles' order, 144 so); a long list stays in the tiles' order
   int all;
   if (brief) {
-    auto splits_of = [&](int i) { return (cells_s[i] + range - 1) / range; };
-    auto bucket_of = [&](int i, int sp) {                      // by the tiles of a unit, at most `range`
-      return kBuckets - 1 - ((cells_s[i] + sp - 1) / sp) * (kBuckets - 1) / range;
-    };
+    int* const splits_s = ends_s;                              // (the sequences' ends are done with)
     for (int i = tid; i < n_tiles; i += 1024) {
-      const int sp = splits_of(i);
-      if (sp) atomicAdd(bucket_s + bucket_of(i, sp), sp * 2 * p.H);
+      const int sp = splits_s[i] = (cells_s[i] + range - 1) / range;
+      if (sp == 0) continue;
+      const int len = (cells_s[i] + sp - 1) / sp;              // the tiles of a unit, at most `range`
+      const int b = kBuckets - 1 - static_cast<int>(static_cast<float>(len) * (kBuckets - 1) / range);
+      bucket_of[i] = static_cast<uint8_t>(max(b, 0));
+      atomicAdd(bucket_s + bucket_of[i], sp * 2 * p.H);
     }
     __syncthreads();
     const int mine = tid < kBuckets ? bucket_s[tid] : 0;
@@ -411,9 +413,9 @@ __global__ void __launch_bounds__(1024, 1) diff_schedule_kernel(const SchedulePa
     if (tid < kBuckets) bucket_s[tid] = before;
     __syncthreads();
     for (int i = tid; i < n_tiles; i += 1024) {                // (the order within a bucket moves where rows are kept, not what is in them)
-      const int sp = splits_of(i);
+      const int sp = splits_s[i];
       s.tiles[i].splits = sp;
-      s.tiles[i].first = sp ? atomicAdd(bucket_s + bucket_of(i, sp), sp * 2 * p.H) : 0;
+      s.tiles[i].first = sp ? atomicAdd(bucket_s + bucket_of[i], sp * 2 * p.H) : 0;
     }
   } else {
     const int tiles_per = (n_tiles + 1023) / 1024;
