@@ -103,7 +103,7 @@ constexpr int kSmemMax = 227 * 1024;
 // a raw tile: K codes of the CTA's 64 cells (4 boxes of 16 cells x 128 B), V nibbles of the 128 cells (8 boxes),
 // and the runs of K and V scales of all heads (8 groups x 128 H and 256 H bytes)
 constexpr int kRawV = 8192, kRawKs = 24576;
-constexpr int raw_bytes(int H) { return (kRawKs + 3072 * H + 1023) / 1024 * 1024; }
+constexpr int raw_bytes(int H) { return (kRawKs + 3 * 1024 * H + 1023) / 1024 * 1024; }
 constexpr int raw_stages(int H) { return (kSmemMax - kRawOff) / raw_bytes(H) < 3 ? (kSmemMax - kRawOff) / raw_bytes(H) : 3; }
 static_assert(raw_stages(2) == 3 && raw_stages(7) >= 2 && raw_stages(8) >= 1, "raw stages");
 // the epilogue reuses the operand tiles as a fp32 [128][256] row buffer
