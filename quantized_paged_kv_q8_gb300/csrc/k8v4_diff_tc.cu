@@ -94,10 +94,15 @@ constexpr int kKOff = kQOff + 32768;                  // K fp16, 2 buffers x [2 
 constexpr int kKBuf = 16384;
 constexpr int kVOff = kKOff + 2 * kKBuf;              // V fp16, 2 buffers x [2 atoms][128 cells][128 B]
 constexpr int kVBuf = 32768, kVAtom = 16384;
-constexpr int kKsOff = kVOff + 2 * kVBuf;             // K scales, 4 tiles x [128] f32
-constexpr int kRedOff = kKsOff + 4 * 512;             // [128] f32 each: score factors, references, sums of the two groups
+// K scales, kKsRing tiles x [128] f32, and as many words of bad groups.  A row frees S before it reads these, so
+// the conversion of tile i, which waits for S(i - 2) and with it for S(i - 3) to be read, knows that the rows are done
+// with tile i - 5 (a group is in its tile i - 3) and have taken tile i - 6's reference: five places would do.
+// Four (with three raw tiles in flight, nothing else holds the conversion back) would not
+constexpr int kKsRing = 8;
+constexpr int kKsOff = kVOff + 2 * kVBuf;
+constexpr int kRedOff = kKsOff + kKsRing * 512;             // [128] f32 each: score factors, references, sums of the two groups
 constexpr int kBarOff = kRedOff + 4 * 512;
-constexpr int kCtlOff = kBarOff + 256;                // tmem slot, failure word, bad groups of 4 tiles, valid groups of the stages
+constexpr int kCtlOff = kBarOff + 256;                // tmem slot, failure word, bad groups of the ring's tiles, valid groups of the stages
 constexpr int kRawOff = (kCtlOff + 64 + 1023) / 1024 * 1024;
 constexpr int kSmemMax = 227 * 1024;
 // a raw tile: K codes of the CTA's 64 cells (4 boxes of 16 cells x 128 B), V nibbles of the 128 cells (8 boxes),
@@ -105,7 +110,7 @@ constexpr int kSmemMax = 227 * 1024;
 constexpr int kRawV = 8192, kRawKs = 24576;
 constexpr int raw_bytes(int H) { return (kRawKs + 3 * 1024 * H + 1023) / 1024 * 1024; }
 constexpr int raw_stages(int H) { return (kSmemMax - kRawOff) / raw_bytes(H) < 3 ? (kSmemMax - kRawOff) / raw_bytes(H) : 3; }
-static_assert(raw_stages(2) == 3 && raw_stages(7) >= 2 && raw_stages(8) >= 1, "raw stages");
+static_assert(kKsRing >= 5 && kKsRing <= 8 && raw_stages(2) == 3 && raw_stages(7) >= 2 && raw_stages(8) >= 1, "raw stages");
 // the epilogue reuses the operand tiles as a fp32 [128][256] row buffer
 static_assert(kKsOff - kQOff >= kRows * 256 * 4, "row buffer");
 
@@ -618,7 +623,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const int HQ = C.H * kGqa;
   const int row = tid & (kRows - 1), group = tid >> 7;     // (row warps) tiles group, group + 2, ...
   const uint32_t bars = sb + kBarOff;
-  volatile int* ctl = reinterpret_cast<volatile int*>(smem + kCtlOff);   // [0] tmem, [1] failed, [4..7] bad groups of 4 tiles, [8..10] valid groups
+  volatile int* ctl = reinterpret_cast<volatile int*>(smem + kCtlOff);   // [0] tmem, [1] failed, [4..11] bad groups, [12..14] valid groups
   float* fsc = reinterpret_cast<float*>(smem + kRedOff);                 // [128] score factors
   float* ref = fsc + kRows;                                              // [128] reference maxima
   float* sums = fsc + 2 * kRows;                                         // [2][128]
@@ -682,7 +687,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (lane == 0) {
       if (which == 0) {
         if (bad) record_status(p.status, K8V4_ERANGE);
-        ctl[8 + stage] = static_cast<int>(good | (bad << 8));
+        ctl[12 + stage] = static_cast<int>(good | (bad << 8));
       }
       const uint32_t n = __popc(good), nk = __popc((good >> (4 * rank)) & 15u);
       mbar_expect_tx(bar, which == 0 ? n * 2048u : which == 1 ? n * 256u * H : n * 128u * H + nk * 2048u);
@@ -795,7 +800,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) arrive_cluster(s_free0);
       // scores, unscaled (my_f > 0, so the maximum commutes with it)
-      const float* ks = ksbuf + 128 * (i & 3);
+      const float* ks = ksbuf + 128 * (i % kKsRing);
 #pragma unroll
       for (int c = 0; c < kTileN; c += 4) {
         const float4 k4 = *reinterpret_cast<const float4*>(ks + c);
@@ -805,7 +810,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         sc[c + 2] = b.x; sc[c + 3] = b.y;
       }
       const int vis = my_vis - (tile0 + i) * kTileN;                   // cells [0, vis) of the tile
-      const int bad = ctl[4 + (i & 3)];                                // its groups of 16 cells on a page out of range
+      const int bad = ctl[4 + i % kKsRing];                               // its groups of 16 cells on a page out of range
       if (vis < kTileN || bad) {
 #pragma unroll
         for (int c = 0; c < kTileN; ++c)
@@ -972,7 +977,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const int buf = i & 1;
       const uint32_t raw = sb + kRawOff + stage * p.stage_bytes;
       if (!wait_soon(bars + 8 * (kBarRawFull + stage), raw_phase, p.wait_ns)) { ctl[1] = 1; break; }
-      const int valid = ctl[8 + stage];                    // the tile's 16-cell groups that were copied; bits 8..15: on a bad page
+      const int valid = ctl[12 + stage];                   // the tile's 16-cell groups that were copied; bits 8..15: on a bad page
       if (!is_v) {
         uint4 kw[4];
 #pragma unroll
@@ -994,8 +999,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           sts128(dst + swz(kcell, 2 * u), h[0], h[1], h[2], h[3]);
           sts128(dst + swz(kcell, 2 * u + 1), h[4], h[5], h[6], h[7]);
         }
-        ksbuf[128 * (i & 3) + t] = ksc;
-        if (t == 0) ctl[4 + (i & 3)] = valid >> 8;
+        ksbuf[128 * (i % kKsRing) + t] = ksc;
+        if (t == 0) ctl[4 + i % kKsRing] = valid >> 8;
         fence_async_smem();
         __syncwarp();
         if (lane == 0) {
