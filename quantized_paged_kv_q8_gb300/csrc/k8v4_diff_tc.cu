@@ -229,6 +229,7 @@ __global__ void __launch_bounds__(1024, 1) diff_schedule_kernel(const SchedulePa
   __shared__ float cost_s[32];
   __shared__ int cand_s[32];
   __shared__ int top_s, few_n;
+  __shared__ unsigned long long claimed_s, cells_sum_s;        // token tiles and their cell tiles: offsets that name tokens again and again pass 32 bits
   __shared__ int ends_s[kShortList], cells_s[kShortList];
   __shared__ unsigned long long few_s[kMostFew + 1];           // sixteens of cells of the sequences of so many tokens; [0] of the others' token tiles
   __shared__ int bucket_s[kBuckets];
@@ -236,6 +237,7 @@ __global__ void __launch_bounds__(1024, 1) diff_schedule_kernel(const SchedulePa
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (threadIdx.x <= kMostFew) few_s[threadIdx.x] = 0;
   if (threadIdx.x < kBuckets) bucket_s[threadIdx.x] = 0;
+  if (threadIdx.x == 0) claimed_s = cells_sum_s = 0;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const Schedule& s = p.s;
@@ -298,6 +300,7 @@ __global__ void __launch_bounds__(1024, 1) diff_schedule_kernel(const SchedulePa
     else rows += max(n, 0);
     ends[b] = sum;                                             // of this thread's sequences so far
   }
+  if (sum) atomicAdd(&claimed_s, static_cast<unsigned long long>(sum));
   const int at = scan_block(sum, red, &n_tiles);
   int row = scan_block(rows, red, &n_rows);
   for (int b = b0; b < b1; ++b) {
@@ -320,7 +323,7 @@ __global__ void __launch_bounds__(1024, 1) diff_schedule_kernel(const SchedulePa
     }
   }
   // offsets that do not follow one another can claim more tiles than there is room for
-  if (n_tiles > p.n_tok / kTileTok + min(p.n_seqs, p.n_tok)) {
+  if (claimed_s > static_cast<unsigned long long>(p.n_tok / kTileTok + min(p.n_seqs, p.n_tok))) {
     if (tid == 0) record_status(p.status, K8V4_ERANGE);
     n_tiles = 0;
   }
@@ -334,7 +337,8 @@ __global__ void __launch_bounds__(1024, 1) diff_schedule_kernel(const SchedulePa
   __syncthreads();
   // ---- each tile's tokens and cells
   const bool brief = n_tiles <= kShortList;
-  int cells = 0, top = 0;
+  unsigned long long cells = 0;
+  int top = 0;
   for (int i = tid; i < n_tiles; i += 1024) {
     int lo = 0, hi = p.n_seqs - 1;
     while (lo < hi) {
@@ -373,11 +377,11 @@ __global__ void __launch_bounds__(1024, 1) diff_schedule_kernel(const SchedulePa
     cells += t.cell_tiles;
     top = max(top, t.cell_tiles);
   }
-  int total;
-  (void)scan_block(cells, red, &total);
+  if (cells) atomicAdd(&cells_sum_s, cells);
   top = __reduce_max_sync(kFull, top);
   if (lane == 0) atomicMax(&top_s, top);
   __syncthreads();
+  const float total = static_cast<float>(cells_sum_s);
   top = max(top_s, 1);
   // ---- the range length: 32 candidates from what makes all the units that there is room for to no
   // cut at all, each worked out by a warp: rounds x (range + a unit's fixed cost)
