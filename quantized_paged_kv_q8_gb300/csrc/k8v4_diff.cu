@@ -655,8 +655,8 @@ struct CombineParams {
   const float* ws;
   DiffRagged r;               // a ragged batch's rows
   DiffPieces pieces;          // those of single queries
-  const int32_t* lens;        // and the cells that each sees
-  int H, n_rows;              // rows: (sequence or token, query head)
+  const int32_t* lens;        // and the cells that each sees, max_seq_len at most
+  int max_seq_len, H, n_rows;              // rows: (sequence or token, query head)
   k8v4_diff d;
   uint16_t* out;
 };
@@ -744,7 +744,7 @@ __global__ void __launch_bounds__(WARPS > 4 ? 32 * WARPS : kCombineThreads, WARP
     m_stride = s_stride * splits;
     base = p.ws + (static_cast<int64_t>(tile[4]) + 2 * g * splits) * s_stride + ((row - tile[1]) * kGqa + h) * kDiffRow;
   } else {
-    const int len = p.lens[-2 - i];
+    const int len = min(p.lens[-2 - i], p.max_seq_len);
     int2 at = p.pieces.pairs[static_cast<int64_t>(-2 - i) * p.H + g];      // not written where there is nothing to see
     if (len <= 0 || at.x < 0 || at.y < 0 || at.x > p.pieces.blocks - at.y) at = make_int2(0, 0);   // (nor behind a failed wait)
     splits = min(at.y, kMost);
@@ -900,6 +900,7 @@ int launch_diff_combine_ragged(const Launch& L, const float* ws, const DiffRagge
   p.r = r;
   p.pieces = pieces;
   p.lens = lens;
+  p.max_seq_len = INT_MAX;                              // (the schedule's are clipped)
   p.H = H;
   p.n_rows = n_tok * H * kGqa;                          // below 2^30
   p.d = diff;
@@ -962,6 +963,7 @@ int launch_diff_decode(const Launch& L, const CacheView& C, const void* q, int q
   c.r = DiffRagged{nullptr, nullptr, nullptr};
   c.pieces = pieces;
   c.lens = lens;
+  c.max_seq_len = max_seq_len;
   c.H = C.H;
   c.n_rows = n_seqs * C.H * kGqa;
   c.d = diff;
