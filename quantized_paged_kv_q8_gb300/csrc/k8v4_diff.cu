@@ -613,6 +613,7 @@ __global__ void __launch_bounds__(32 * kMaxWorkers, 1)
     // the next pair's copies overwrite what the workers wrote and the merge read; after a failure the CTA leaves (its
     // other pieces' rows would be older ones: their blocks are marked empty)
     fence_async_smem();
+    const bool stop = *abort_flag != 0;        // (the same in every warp: behind the barrier one may fail in the next pair already)
     __syncthreads();
     pos += n_tiles;
     if (++g == H) {
@@ -620,7 +621,7 @@ __global__ void __launch_bounds__(32 * kMaxWorkers, 1)
       begin_b += line_of(pair_tiles, H);
       ++b;
     }
-    if (*abort_flag) break;
+    if (stop) break;
   }
 #pragma unroll 1
   while (pos < end) {                        // (only after a failure)
