@@ -13,7 +13,9 @@
 // with K codes exact in fp16, q in fp16 (bf16 is exact after a power of two per row and
 // map), P and V rounded to fp16 once each: 2^-11 of each term at most, against the 2^-8 of the
 // bf16 result, where the plain decode carries both in two terms (48 products of V, not 32, and
-// for one map).
+// for one map).  V is (n - 8) d: a subnormal d is a multiple of fp16's least step, and so is
+// (n - 8) d.  Only from d = 2^13 on does fp16 not hold it; a tile that has such a block (big_blocks)
+// counts with V / 8 and 8 P, which is 3 added to its scores, and its values below 2^-11 to 2^-22.
 //
 // The worker warps are the decode kernel's: they take a range's tiles in turn, each with a ring of
 // its own filled by TMA.  The ranges are not: the tiles of all (sequence, KV head) pairs, laid
@@ -146,21 +148,20 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
 }
 // 2^e exactly for e >= -126, 0 below
 __device__ __forceinline__ float pow2i(int e) { return e < -126 ? 0.0f : __int_as_float((e + 127) << 23); }
-// one word of nibble bytes b0..b3 -> four fp16x2 of (n - 8) / 8, exact: {b0, b2} and {b1, b3}
+// one word of nibble bytes b0..b3 -> four fp16x2 of n - 8, exact: {b0, b2} and {b1, b3}
 // of the low nibbles, then of the high ones.  0x640n is 1024 + n and 0x64n0 is 1024 + 16 n in
-// fp16; (1024 + n) / 8 - 129 and (1024 + 16 n) / 128 - 9 are both (n - 8) / 8
-__device__ __forceinline__ void nibs_8th(uint32_t r, __half2 v[4]) {
+// fp16; 1024 + n - 1032 and (1024 + 16 n) / 16 - 72 are both n - 8
+__device__ __forceinline__ void nibs(uint32_t r, __half2 v[4]) {
   const uint32_t r8 = r >> 8;
-  const __half2 eighth = __halves2half2(__ushort_as_half(0x3000), __ushort_as_half(0x3000));    // 1/8
-  const __half2 m129 = __halves2half2(__ushort_as_half(0xd808), __ushort_as_half(0xd808));      // -129
-  const __half2 c128th = __halves2half2(__ushort_as_half(0x2000), __ushort_as_half(0x2000));    // 1/128
-  const __half2 m9 = __halves2half2(__ushort_as_half(0xc880), __ushort_as_half(0xc880));        // -9
+  const __half2 m1032 = __halves2half2(__ushort_as_half(0xe408), __ushort_as_half(0xe408));     // -1032
+  const __half2 c16th = __halves2half2(__ushort_as_half(0x2c00), __ushort_as_half(0x2c00));     // 1/16
+  const __half2 m72 = __halves2half2(__ushort_as_half(0xd480), __ushort_as_half(0xd480));       // -72
   uint32_t t0 = (r & 0x000f000fu) | 0x64006400u, t1 = (r8 & 0x000f000fu) | 0x64006400u;
   uint32_t t2 = (r & 0x00f000f0u) | 0x64006400u, t3 = (r8 & 0x00f000f0u) | 0x64006400u;
-  v[0] = __hfma2(*reinterpret_cast<__half2*>(&t0), eighth, m129);
-  v[1] = __hfma2(*reinterpret_cast<__half2*>(&t1), eighth, m129);
-  v[2] = __hfma2(*reinterpret_cast<__half2*>(&t2), c128th, m9);
-  v[3] = __hfma2(*reinterpret_cast<__half2*>(&t3), c128th, m9);
+  v[0] = __hadd2(*reinterpret_cast<__half2*>(&t0), m1032);
+  v[1] = __hadd2(*reinterpret_cast<__half2*>(&t1), m1032);
+  v[2] = __hfma2(*reinterpret_cast<__half2*>(&t2), c16th, m72);
+  v[3] = __hfma2(*reinterpret_cast<__half2*>(&t3), c16th, m72);
 }
 __device__ __forceinline__ uint32_t times(__half2 a, uint32_t d) {
   const __half2 r = __hmul2(a, *reinterpret_cast<const __half2*>(&d));
@@ -402,6 +403,7 @@ __global__ void __launch_bounds__(32 * kMaxWorkers, 1)
     // the V scales of the fragment's four cells k = 2c, 2c+1, 2c+8, 2c+9
     const uint32_t soff0 = LY.vsc_off + (sigma(2 * c) * H + g) * 16, soff1 = LY.vsc_off + (sigma(2 * c + 1) * H + g) * 16;
     const uint32_t s8 = 8 * H * 16;
+    const uint32_t half_row = LY.vsc_off + ((lane >> 1) * H + g) * 16 + 8 * (lane & 1);     // half of a cell's scales
     const uint32_t qf = sb + LY.q_off + 8 * lane;
 
     float o[2][16][4];                   // [map][16-dim m-tile][fragment]: heads 2c, 2c+1 of dims r0 (+8)
@@ -427,6 +429,10 @@ __global__ void __launch_bounds__(32 * kMaxWorkers, 1)
         const uint2 kAu = lds64(st + ksA), kBu = lds64(st + ksB);
         const int cell0 = c_begin + 16 * (w + W * u);
         const bool vA = cell0 + rowA < c_end, vB = cell0 + rowB < c_end;
+        const uint2 dd = lds64(st + half_row);
+        const bool big = __any_sync(kFull, big_blocks(dd.x, dd.y));       // a block that fp16 does not hold eight times over
+        const bool odd = big || cell0 + 16 > c_end;
+        const float more = big ? 3.0f : 0.0f, counts = big ? 0.125f : 1.0f;   // added to the scores, and what P counts in l
         uint32_t ph[2][2];
         // ---- S_m^T[cell][head] of both maps, two accumulators each
         float acc[2][2][4];
@@ -456,10 +462,10 @@ __global__ void __launch_bounds__(32 * kMaxWorkers, 1)
 #pragma unroll
         for (int m = 0; m < 2; ++m) {
           const float kA = __uint_as_float(m ? kAu.y : kAu.x), kB = __uint_as_float(m ? kBu.y : kBu.x);
-          sc[m][0] = vA ? kA * (acc[m][0][0] + acc[m][1][0]) * f[m][0] : -INFINITY;
-          sc[m][1] = vA ? kA * (acc[m][0][1] + acc[m][1][1]) * f[m][1] : -INFINITY;
-          sc[m][2] = vB ? kB * (acc[m][0][2] + acc[m][1][2]) * f[m][0] : -INFINITY;
-          sc[m][3] = vB ? kB * (acc[m][0][3] + acc[m][1][3]) * f[m][1] : -INFINITY;
+          sc[m][0] = vA ? fmaf(kA * (acc[m][0][0] + acc[m][1][0]), f[m][0], more) : -INFINITY;
+          sc[m][1] = vA ? fmaf(kA * (acc[m][0][1] + acc[m][1][1]), f[m][1], more) : -INFINITY;
+          sc[m][2] = vB ? fmaf(kB * (acc[m][0][2] + acc[m][1][2]), f[m][0], more) : -INFINITY;
+          sc[m][3] = vB ? fmaf(kB * (acc[m][0][3] + acc[m][1][3]), f[m][1], more) : -INFINITY;
           up = up || sc[m][0] > 8.0f * M[m][0] || sc[m][2] > 8.0f * M[m][0] || sc[m][1] > 8.0f * M[m][1] || sc[m][3] > 8.0f * M[m][1];
         }
         // ---- softmax against the running bucket of each head (the decode kernel's), both maps at a time
@@ -492,13 +498,13 @@ __global__ void __launch_bounds__(32 * kMaxWorkers, 1)
           const float rf0 = 8.0f * M[m][0] - 14.0f, rf1 = 8.0f * M[m][1] - 14.0f;
           const float p0 = ex2_ftz(sc[m][0] - rf0), p1 = ex2_ftz(sc[m][1] - rf1);      // p' = 2^(s - ref + 14) <= 2^14
           const float p2 = ex2_ftz(sc[m][2] - rf0), p3 = ex2_ftz(sc[m][3] - rf1);
-          l[m][0] += p0 + p2;
-          l[m][1] += p1 + p3;
+          l[m][0] = fmaf(p0 + p2, counts, l[m][0]);
+          l[m][1] = fmaf(p1 + p3, counts, l[m][1]);
           // to the B layout (head r0; cells 2c, 2c+1 | 2c+8, 2c+9)
           ph[m][0] = movmatrix_t(pack_f16(p0, p1));
           ph[m][1] = movmatrix_t(pack_f16(p2, p3));
         }
-        // ---- PV of both maps in rotated space: V = RN((n - 8) / 8 * d), m-tile 2 blk + hf = block
+        // ---- PV of both maps in rotated space: V = RN((n - 8) d), m-tile 2 blk + hf = block
         // blk, dims 16 hf .. 16 hf + 15
 #pragma unroll
         for (int bp = 0; bp < 4; ++bp) {
@@ -506,7 +512,9 @@ __global__ void __launch_bounds__(32 * kMaxWorkers, 1)
           ldmatrix_x4_t(R, st + vrow + 16 * ((2 * bp + (mi >> 1)) ^ vsw));
           uint32_t w0 = lds32(st + soff0 + 4 * bp), w1 = lds32(st + soff1 + 4 * bp);
           uint32_t w2 = lds32(st + soff0 + s8 + 4 * bp), w3 = lds32(st + soff1 + s8 + 4 * bp);
-          if (cell0 + 16 > c_end) {          // cells that nobody sees count with V = 0: their bytes are anything
+          if (odd) {
+            if (big) w0 = eighth_of(w0), w1 = eighth_of(w1), w2 = eighth_of(w2), w3 = eighth_of(w3);
+            // cells that nobody sees count with V = 0: their bytes are anything
             if (cell0 + sigma(2 * c) >= c_end) w0 = 0;
             if (cell0 + sigma(2 * c + 1) >= c_end) w1 = 0;
             if (cell0 + 8 + sigma(2 * c) >= c_end) w2 = 0;
@@ -517,8 +525,8 @@ __global__ void __launch_bounds__(32 * kMaxWorkers, 1)
             const uint32_t sel = h ? 0x7632u : 0x5410u;
             const uint32_t d01 = prmt(w0, w1, sel), d89 = prmt(w2, w3, sel);     // d of block 2bp+h, cell pairs
             __half2 xa[4], xb[4];
-            nibs_8th(R[2 * h], xa);
-            nibs_8th(R[2 * h + 1], xb);
+            nibs(R[2 * h], xa);
+            nibs(R[2 * h + 1], xb);
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf) {
               const uint32_t a[4] = {times(xa[2 * hf], d01), times(xa[2 * hf + 1], d01), times(xb[2 * hf], d89), times(xb[2 * hf + 1], d89)};
@@ -601,7 +609,7 @@ __global__ void __launch_bounds__(32 * kMaxWorkers, 1)
           Ls += lw * fw;
         }
       }
-      constexpr float kInv = 1.0f / 2048.0f;     // 2^-14 of p', 2^3 of (n - 8) / 8
+      constexpr float kInv = 1.0f / 16384.0f;    // 2^-14 of p'
       float* dst = rows + h * kDiffRow;
       reinterpret_cast<float4*>(dst)[lane] = make_float4(v[0] * kInv, v[1] * kInv, v[2] * kInv, v[3] * kInv);
       reinterpret_cast<float4*>(dst)[32 + lane] = make_float4(v[4] * kInv, v[5] * kInv, v[6] * kInv, v[7] * kInv);

@@ -32,6 +32,18 @@ int launch_diff_split(const Launch& L, const CacheView& C, const void* q, int q_
                       const int32_t* lens, const DiffQueries& rows, int n_seqs, int max_seq_len, float sm_scale,
                       const DiffPieces& ws);
 
+// four or eight fp16 block scales: nonzero where one is at least 2^13 in size, so that 8 d does not fit fp16
+__device__ __forceinline__ uint32_t larger_of(uint32_t a, uint32_t b) {                    // in size, of each half
+  const __half2 r = __hmax2(__habs2(*reinterpret_cast<const __half2*>(&a)), __habs2(*reinterpret_cast<const __half2*>(&b)));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ uint32_t big_blocks(uint32_t a, uint32_t b) { return (larger_of(a, b) + 0x10001000u) & 0x80008000u; }
+__device__ __forceinline__ uint32_t big_blocks(const uint4& d) { return big_blocks(larger_of(d.x, d.y), larger_of(d.z, d.w)); }
+__device__ __forceinline__ uint32_t eighth_of(uint32_t d) {
+  const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&d), __halves2half2(__ushort_as_half(0x3000), __ushort_as_half(0x3000)));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
 // a warp: exp(q1 . k1) (term 0) or exp(q2 . k2) of a query head, 0 without vectors
 __device__ __forceinline__ float diff_lambda_term(const k8v4_diff& d, int hq, int term, int lane) {
   if (!d.lambda_q1) return 0.0f;

@@ -11,14 +11,15 @@
 // in tiles of 128 cells
 //   S  = Q_m K_m^T        128 lanes, N = 128
 //   P  = 2^(s - ref) 2^2  online softmax in the log2 domain, fp16
-//   O += P V              N = 256, V = RN((n - 8) / 8 d) in fp16
+//   O += P V              N = 256, V = RN((n - 8) d) in fp16
 // and writes its partial rows (o, m, l); the combine joins ranges and maps.  The two maps'
 // units read and convert the same V; a pair that kept both maps of 16 tokens instead would
 // need both key halves too, and twice the conversions per product.
 //
 // Each CTA of the pair dequantises half of every tile (64 of the 128 cells of K, 128 of the
 // 256 dims of V); the pair reads both halves as one operand.  P and V are rounded to fp16
-// once (2^-11 of each term at most; the result is bf16), so a tile takes 8 products of 64 clocks for
+// once (2^-11 of each term at most; the result is bf16; 32 cells with a block that fp16 does not hold eight
+// times over count with V / 8 and 8 P, as a tile in k8v4_diff.cu), so a tile takes 8 products of 64 clocks for
 // S and 8 of 128 for O where the exact kernels' two terms each would take three times the
 // latter.
 //
@@ -94,15 +95,15 @@ constexpr int kKOff = kQOff + 32768;                  // K fp16, 2 buffers x [2 
 constexpr int kKBuf = 16384;
 constexpr int kVOff = kKOff + 2 * kKBuf;              // V fp16, 2 buffers x [2 atoms][128 cells][128 B]
 constexpr int kVBuf = 32768, kVAtom = 16384;
-// K scales, kKsRing tiles x [128] f32, and as many words of bad groups.  A row frees S before it reads these, so
-// the conversion of tile i, which waits for S(i - 2) and with it for S(i - 3) to be read, knows that the rows are done
-// with tile i - 5 (a group is in its tile i - 3) and have taken tile i - 6's reference: five places would do.
+// K scales, kKsRing tiles x [128] f32, and as many words of odd cells.  A row frees S before it reads these, so
+// the conversion of tile i, which waits for S(i - 2) and with it for S(i - 3) and S(i - 4) to be read, knows that the
+// groups are in their tiles i - 3 and i - 4 and done with those up to i - 5 and i - 6: six places would do.
 // Four (with three raw tiles in flight, nothing else holds the conversion back) would not
 constexpr int kKsRing = 8;
 constexpr int kKsOff = kVOff + 2 * kVBuf;
 constexpr int kRedOff = kKsOff + kKsRing * 512;             // [128] f32 each: score factors, references, sums of the two groups
 constexpr int kBarOff = kRedOff + 4 * 512;
-constexpr int kCtlOff = kBarOff + 256;                // tmem slot, failure word, bad groups of the ring's tiles, valid groups of the stages
+constexpr int kCtlOff = kBarOff + 256;                // tmem slot, failure word, odd cells of the ring's tiles, valid groups of the stages
 constexpr int kRawOff = (kCtlOff + 64 + 1023) / 1024 * 1024;
 constexpr int kSmemMax = 227 * 1024;
 // a raw tile: K codes of the CTA's 64 cells (4 boxes of 16 cells x 128 B), V nibbles of the 128 cells (8 boxes),
@@ -110,7 +111,7 @@ constexpr int kSmemMax = 227 * 1024;
 constexpr int kRawV = 8192, kRawKs = 24576;
 constexpr int raw_bytes(int H) { return (kRawKs + 3 * 1024 * H + 1023) / 1024 * 1024; }
 constexpr int raw_stages(int H) { return (kSmemMax - kRawOff) / raw_bytes(H) < 3 ? (kSmemMax - kRawOff) / raw_bytes(H) : 3; }
-static_assert(kKsRing >= 5 && kKsRing <= 8 && raw_stages(2) == 3 && raw_stages(7) >= 2 && raw_stages(8) >= 1, "raw stages");
+static_assert(kKsRing >= 6 && kKsRing <= 8 && raw_stages(2) == 3 && raw_stages(7) >= 2 && raw_stages(8) >= 1, "raw stages");
 // the epilogue reuses the operand tiles as a fp32 [128][256] row buffer
 static_assert(kKsOff - kQOff >= kRows * 256 * 4, "row buffer");
 
@@ -577,22 +578,21 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const float v[32]) {
       : "memory");
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-// A word of nibble bytes b0..b3 -> fp16 pairs of V = RN((n - 8) / 8 * d): lo {b0, b2}, {b1, b3} of the
+// A word of nibble bytes b0..b3 -> fp16 pairs of V = RN((n - 8) d): lo {b0, b2}, {b1, b3} of the
 // low nibbles, hi of the high ones.  0x640n is 1024 + n and 0x64n0 is 1024 + 16 n in fp16;
-// (1024 + n) / 8 - 129 and (1024 + 16 n) / 128 - 9 are both (n - 8) / 8, exactly.  (Elements 1 and
+// 1024 + n - 1032 and (1024 + 16 n) / 16 - 72 are both n - 8, exactly.  (Elements 1 and
 // 2 of each four come out swapped; the rows are put right as they are written.)
 __device__ __forceinline__ void nib_word(uint32_t r, __half2 d2, uint32_t lo[2], uint32_t hi[2]) {
   const uint32_t r8 = r >> 8;
-  const __half2 eighth = __halves2half2(__ushort_as_half(0x3000), __ushort_as_half(0x3000));    // 1/8
-  const __half2 m129 = __halves2half2(__ushort_as_half(0xd808), __ushort_as_half(0xd808));      // -129
-  const __half2 c128th = __halves2half2(__ushort_as_half(0x2000), __ushort_as_half(0x2000));    // 1/128
-  const __half2 m9 = __halves2half2(__ushort_as_half(0xc880), __ushort_as_half(0xc880));        // -9
+  const __half2 m1032 = __halves2half2(__ushort_as_half(0xe408), __ushort_as_half(0xe408));     // -1032
+  const __half2 c16th = __halves2half2(__ushort_as_half(0x2c00), __ushort_as_half(0x2c00));     // 1/16
+  const __half2 m72 = __halves2half2(__ushort_as_half(0xd480), __ushort_as_half(0xd480));       // -72
   const uint32_t t0 = (r & 0x000f000fu) | 0x64006400u, t1 = (r8 & 0x000f000fu) | 0x64006400u;
   const uint32_t t2 = (r & 0x00f000f0u) | 0x64006400u, t3 = (r8 & 0x00f000f0u) | 0x64006400u;
-  const __half2 v0 = __hmul2(__hfma2(*reinterpret_cast<const __half2*>(&t0), eighth, m129), d2);
-  const __half2 v1 = __hmul2(__hfma2(*reinterpret_cast<const __half2*>(&t1), eighth, m129), d2);
-  const __half2 v2 = __hmul2(__hfma2(*reinterpret_cast<const __half2*>(&t2), c128th, m9), d2);
-  const __half2 v3 = __hmul2(__hfma2(*reinterpret_cast<const __half2*>(&t3), c128th, m9), d2);
+  const __half2 v0 = __hmul2(__hadd2(*reinterpret_cast<const __half2*>(&t0), m1032), d2);
+  const __half2 v1 = __hmul2(__hadd2(*reinterpret_cast<const __half2*>(&t1), m1032), d2);
+  const __half2 v2 = __hmul2(__hfma2(*reinterpret_cast<const __half2*>(&t2), c16th, m72), d2);
+  const __half2 v3 = __hmul2(__hfma2(*reinterpret_cast<const __half2*>(&t3), c16th, m72), d2);
   lo[0] = *reinterpret_cast<const uint32_t*>(&v0);
   lo[1] = *reinterpret_cast<const uint32_t*>(&v1);
   hi[0] = *reinterpret_cast<const uint32_t*>(&v2);
@@ -627,7 +627,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const int HQ = C.H * kGqa;
   const int row = tid & (kRows - 1), group = tid >> 7;     // (row warps) tiles group, group + 2, ...
   const uint32_t bars = sb + kBarOff;
-  volatile int* ctl = reinterpret_cast<volatile int*>(smem + kCtlOff);   // [0] tmem, [1] failed, [4..11] bad groups, [12..14] valid groups
+  volatile int* ctl = reinterpret_cast<volatile int*>(smem + kCtlOff);   // [0] tmem, [1] failed, [4..11] odd cells (a byte for each 32: bad groups, 4: large blocks), [12..14] valid groups
   float* fsc = reinterpret_cast<float*>(smem + kRedOff);                 // [128] score factors
   float* ref = fsc + kRows;                                              // [128] reference maxima
   float* sums = fsc + 2 * kRows;                                         // [2][128]
@@ -814,11 +814,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         sc[c + 2] = b.x; sc[c + 3] = b.y;
       }
       const int vis = my_vis - (tile0 + i) * kTileN;                   // cells [0, vis) of the tile
-      const int bad = ctl[4 + i % kKsRing];                               // its groups of 16 cells on a page out of range
-      if (vis < kTileN || bad) {
+      const unsigned odd = ctl[4 + i % kKsRing];                       // 16-cell groups on a page out of range, cells of large blocks
+      if (vis < kTileN || odd) {
 #pragma unroll
         for (int c = 0; c < kTileN; ++c)
-          if (c >= vis || ((bad >> (c >> 4)) & 1)) sc[c] = -INFINITY;
+          if (c >= vis || ((odd >> (8 * (c >> 5) + ((c >> 4) & 1))) & 1)) sc[c] = -INFINITY;
       }
       float mx[4] = {sc[0], sc[1], sc[2], sc[3]};
 #pragma unroll
@@ -828,7 +828,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
 #pragma unroll
       for (int k = 0; k < 4; ++k) mx[k] = fmaxf(mx[k], sc[kTileN - 4 + k]);
-      const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * my_f;
+      const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * my_f + (odd & 0x04040404u ? 3.0f : 0.0f);
       // the row's reference, as the tile before left it
       float m_run = -INFINITY, alpha = 1.0f;
       if (i > 0) {
@@ -850,7 +850,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         l_ref = m_run;
       }
       const float mu = (m_run == -INFINITY ? 0.0f : m_run) - kLift;
-      const float2 f2 = make_float2(my_f, my_f), mu2 = make_float2(-mu, -mu);
+      const float2 f2 = make_float2(my_f, my_f);
       // P(i - 2) has been read
       if (i >= 2 && !wait_soon(bars + 8 * (kBarODone + group), ((i - 2) >> 1) & 1, p.wait_ns)) {
         failed = true;
@@ -862,13 +862,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const uint32_t pcol = tmem + lane_base + kPCol + kPBuf * group;
 #pragma unroll
       for (int h = 0; h < 4; ++h) {
+        const bool big = (odd >> (8 * h + 2)) & 1;                     // 8 P, which counts as P in the sum
+        const float off = big ? 3.0f - mu : -mu, one = big ? 0.125f : 1.0f;
+        const float2 mu2 = make_float2(off, off), counts = make_float2(one, one);
         uint32_t ph[16];
 #pragma unroll
         for (int c = 0; c < 16; ++c) {
           const float2 e = __ffma2_rn(make_float2(sc[32 * h + 2 * c], sc[32 * h + 2 * c + 1]), f2, mu2);
           const float2 q = make_float2(ex2_ftz(e.x), ex2_ftz(e.y));
           const __half2 hq = __floats2half2_rn(q.x, q.y);
-          psum[c & 3] = __fadd2_rn(psum[c & 3], q);
+          psum[c & 3] = __ffma2_rn(q, counts, psum[c & 3]);
           ph[c] = *reinterpret_cast<const uint32_t*>(&hq);
         }
         tmem_st16(pcol + 16 * h, ph);
@@ -942,7 +945,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             x.x += old.x; x.y += old.y; x.z += old.z; x.w += old.w;
           }
           *reinterpret_cast<float4*>(rowbuf + row * 256 + ((32 * h + 4 * c + 4 * row) & 255)) =
-              make_float4(8.0f * x.x, 8.0f * x.z, 8.0f * x.y, 8.0f * x.w);   // (dims 1 and 2 of each four are swapped)
+              make_float4(x.x, x.z, x.y, x.w);                 // (dims 1 and 2 of each four are swapped)
         }
       }
       tc_fence_before();
@@ -972,7 +975,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const uint32_t kraw = (kcell >> 4) * 2048 + (kcell & 15) * 128;
     const uint32_t vraw = kRawV + (t >> 4) * 2048 + (t & 15) * 128;
     const uint32_t ksraw = kRawKs + (t >> 4) * 128 * C.H + ((t & 15) * C.H + g) * 8 + 4 * map;
-    const uint32_t vsraw = kRawKs + 1024 * C.H + (t >> 4) * 256 * C.H + ((t & 15) * C.H + g) * 16 + 8 * rank;
+    const uint32_t vsraw = kRawKs + 1024 * C.H + (t >> 4) * 256 * C.H + ((t & 15) * C.H + g) * 16;     // a cell's eight V scales
     // a tile's buffers are free once the product of tile i - 2 has read them
     const uint32_t freed = bars + 8 * (is_v ? kBarODone : kBarSFull);
     int stage = 0;
@@ -988,6 +991,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         for (int u = 0; u < 4; ++u) kw[u] = lds128(raw + kraw + (((4 * kchunk + u) ^ (kcell & 7)) << 4));
         float ksc;
         asm volatile("ld.shared.f32 %0, [%1];" : "=f"(ksc) : "r"(raw + ksraw));
+        const uint4 vd = lds128(raw + vsraw);
+        const bool big = __any_sync(kFull, big_blocks(vd));
         if (i >= 2 && !wait_soon(freed + 8 * buf, ((i - 2) >> 1) & 1, p.wait_ns)) { ctl[1] = 1; break; }
         __syncwarp();
         if (lane == 0) arrive_local(bars + 8 * (kBarRawEmpty + stage));
@@ -1004,7 +1009,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           sts128(dst + swz(kcell, 2 * u + 1), h[4], h[5], h[6], h[7]);
         }
         ksbuf[128 * (i % kKsRing) + t] = ksc;
-        if (t == 0) ctl[4 + i % kKsRing] = valid >> 8;
+        if (lane == 0) {
+          reinterpret_cast<volatile uint8_t*>(ctl + 4 + i % kKsRing)[t >> 5] = static_cast<uint8_t>(((valid >> 8) >> (2 * (t >> 5)) & 3) | (big ? 4 : 0));
+        }
         fence_async_smem();
         __syncwarp();
         if (lane == 0) {
@@ -1014,8 +1021,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       } else {
         const uint32_t dst = sb + kVOff + buf * kVBuf;
         // a cell that was not copied, or that nobody sees, counts with V = 0 (its P is 0, its bytes are anything)
-        uint32_t vd[2];
-        asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(vd[0]), "=r"(vd[1]) : "r"(raw + vsraw));
+        const uint4 all = lds128(raw + vsraw);
+        uint32_t vd[2] = {rank ? all.z : all.x, rank ? all.w : all.y};
+        if (__any_sync(kFull, big_blocks(all))) vd[0] = eighth_of(vd[0]), vd[1] = eighth_of(vd[1]);
         uint4 vw[4];
 #pragma unroll
         for (int b = 0; b < 4; ++b) vw[b] = lds128(raw + vraw + (((4 * rank + b) ^ (t & 7)) << 4));

@@ -1,0 +1,90 @@
+"""What the differential attention's operands keep, where it shows: values far below and far above 1, and cells whose
+values differ by as much."""
+import numpy as np
+import pytest
+import torch
+
+import quantized_paged_kv_q8_gb300 as k8
+from diff_util import all_cells, check, expected, weights
+from test_gpu_diff import queries
+
+pytestmark = pytest.mark.gpu
+
+
+def cache_of(k, v, P=64):
+    """One sequence: k, v float32 numpy [n, H, 256]."""
+    n, H, _ = k.shape
+    pages = -(-n // P)
+    cache = k8.PagedCache(pages, P, H)
+    cache.pages.zero_()
+    pt = torch.arange(pages, dtype=torch.int32, device="cuda")[None]
+    k8.kv_append_k8v4(cache, pt, torch.zeros(1, dtype=torch.int64, device="cuda"), torch.from_numpy(k)[None].cuda(), torch.from_numpy(v)[None].cuda())
+    assert k8.k8v4_last_device_status() == 0
+    return cache, pt
+
+
+def attend(way, cache, pt, q, n, heads):
+    """The last cells' queries through either kernel: one by one ("one"), or as the first tokens of a prompt chunk
+    long enough for token tiles ("tile"), whose other tokens see as many cells."""
+    if way == "one":
+        out = torch.empty(q.shape, dtype=torch.bfloat16, device="cuda")
+        lens = torch.full((len(q),), n, dtype=torch.int32, device="cuda")
+        ws = k8.diff_decode_workspace(cache, len(q), n)
+        k8.attn_k8v4_diff_decode(cache, q, pt.expand(len(q), -1).contiguous(), lens, n, heads, out, ws)
+        return out
+    T = 40
+    packed = q.repeat(-(-T // len(q)), 1, 1)[:T].contiguous()
+    out = torch.empty(packed.shape, dtype=torch.bfloat16, device="cuda")
+    i32 = dict(dtype=torch.int32, device="cuda")
+    k8.attn_k8v4_diff(cache, packed, torch.tensor([0, T], **i32), pt, torch.tensor([n], **i32), n, heads, out,
+                      k8.diff_workspace(cache, 1, T, n), steps=torch.full((T,), n, **i32))
+    return out[:len(q)]
+
+
+WAYS = pytest.mark.parametrize("way", ["one", "tile"])
+
+
+@WAYS
+@pytest.mark.parametrize("gain", [1e-7, 1e-6, 1e-5, 3e-4, 1.0, 3e3, 3e4])
+@pytest.mark.parametrize("n", [1, 3, 200])
+def test_values_of_any_size(way, gain, n):
+    """V enters the products with half a step of fp16 at most, down to scales that are subnormal and up to those that
+    eight times over fp16 does not hold."""
+    rng = np.random.default_rng(n)
+    v = (gain * np.clip(rng.standard_normal((n, 2, 256)), -1, 1)).astype(np.float32)
+    if gain > 1e4:
+        v[::2] = gain * np.where(rng.random((len(v[::2]), 2, 1)) < 0.5, 1, -1)         # 16 times that in one rotated element
+    cache, pt = cache_of((rng.standard_normal((n, 2, 256))).astype(np.float32), v)
+    q = queries(rng, 2, 16, "bf16", 2.0)
+    cells = all_cells(cache)
+    heads, lam, w = weights(rng, 1, norm=False)
+    out = attend(way, cache, pt, q, n, heads)
+    assert k8.k8v4_last_device_status() == 0
+    want, bound = expected(cells, q.double(), torch.arange(n, device="cuda"), [n] * 2, lam, 0.6, w, 0.4)
+    check(out, want, bound)
+
+
+@WAYS
+def test_cells_of_all_sizes(way):
+    """Cells of small, ordinary, large and the largest values in one sequence, each kind far ahead in a row of its
+    own."""
+    rng = np.random.default_rng(5)
+    n = 700
+    kind = np.arange(n) // 64 % 4                          # (beside values of 2^16 those below 2^-11 keep 2^-22)
+    k = (0.1 * rng.standard_normal((n, 2, 256))).astype(np.float32)
+    k[:, :, :4] = 0
+    k[:, :, :128] += 0.5 * np.eye(128, dtype=np.float32)[kind][:, None]          # lane `kind` of the first map's keys
+    v = (np.array([1e-5, 1.0, 1e3, 1.0])[kind][:, None, None] * rng.standard_normal((n, 2, 256))).astype(np.float32)
+    big = kind == 3
+    v[big] += 3e4 * np.where(rng.random((big.sum(), 2, 1)) < 0.5, 1, -1).astype(np.float32)
+    cache, pt = cache_of(k, v)
+    cells = all_cells(cache)
+    q = torch.zeros(4, 16, 256, device="cuda")
+    for r in range(4):                                     # row r: its own kind far ahead of the others
+        q[r, :, r], q[r, :, 128:] = 2000.0, 0.3
+    q = q.bfloat16()
+    heads = k8.DifferentialHeads(lambda_init=0.0)
+    out = attend(way, cache, pt, q, n, heads)
+    assert k8.k8v4_last_device_status() == 0
+    want, bound = expected(cells, q.double(), torch.arange(n, device="cuda"), [n] * 4, None, 0.0, None, 1.0)
+    check(out, want, bound)
