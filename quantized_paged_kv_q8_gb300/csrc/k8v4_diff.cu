@@ -430,7 +430,8 @@ __global__ void __launch_bounds__(32 * kMaxWorkers, 1)
         const int cell0 = c_begin + 16 * (w + W * u);
         const bool vA = cell0 + rowA < c_end, vB = cell0 + rowB < c_end;
         const uint2 dd = lds64(st + half_row);
-        const bool big = __any_sync(kFull, big_blocks(dd.x, dd.y));       // a block that fp16 does not hold eight times over
+        // a block that fp16 does not hold eight times over, of a cell that is seen
+        const bool big = __any_sync(kFull, cell0 + (lane >> 1) < c_end && big_blocks(dd.x, dd.y));
         const bool odd = big || cell0 + 16 > c_end;
         const float more = big ? 3.0f : 0.0f, counts = big ? 0.125f : 1.0f;   // added to the scores, and what P counts in l
         uint32_t ph[2][2];

@@ -985,6 +985,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const uint32_t raw = sb + kRawOff + stage * p.stage_bytes;
       if (!wait_soon(bars + 8 * (kBarRawFull + stage), raw_phase, p.wait_ns)) { ctl[1] = 1; break; }
       const int valid = ctl[12 + stage];                   // the tile's 16-cell groups that were copied; bits 8..15: on a bad page
+      const bool seen = (valid >> (t >> 4)) & 1 && (tile0 + i) * kTileN + t < limit;   // cell t is copied and some row sees it
       if (!is_v) {
         uint4 kw[4];
 #pragma unroll
@@ -992,7 +993,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         float ksc;
         asm volatile("ld.shared.f32 %0, [%1];" : "=f"(ksc) : "r"(raw + ksraw));
         const uint4 vd = lds128(raw + vsraw);
-        const bool big = __any_sync(kFull, big_blocks(vd));
+        const bool big = __any_sync(kFull, seen && big_blocks(vd));
         if (i >= 2 && !wait_soon(freed + 8 * buf, ((i - 2) >> 1) & 1, p.wait_ns)) { ctl[1] = 1; break; }
         __syncwarp();
         if (lane == 0) arrive_local(bars + 8 * (kBarRawEmpty + stage));
@@ -1023,11 +1024,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // a cell that was not copied, or that nobody sees, counts with V = 0 (its P is 0, its bytes are anything)
         const uint4 all = lds128(raw + vsraw);
         uint32_t vd[2] = {rank ? all.z : all.x, rank ? all.w : all.y};
-        if (__any_sync(kFull, big_blocks(all))) vd[0] = eighth_of(vd[0]), vd[1] = eighth_of(vd[1]);
+        if (__any_sync(kFull, seen && big_blocks(all))) vd[0] = eighth_of(vd[0]), vd[1] = eighth_of(vd[1]);
         uint4 vw[4];
 #pragma unroll
         for (int b = 0; b < 4; ++b) vw[b] = lds128(raw + vraw + (((4 * rank + b) ^ (t & 7)) << 4));
-        if (!((valid >> (t >> 4)) & 1) || (tile0 + i) * kTileN + t >= limit) vd[0] = vd[1] = 0;
+        if (!seen) vd[0] = vd[1] = 0;
         if (i >= 2 && !wait_soon(freed + 8 * buf, ((i - 2) >> 1) & 1, p.wait_ns)) { ctl[1] = 1; break; }
         __syncwarp();
         if (lane == 0) arrive_local(bars + 8 * (kBarRawEmpty + stage));

@@ -88,3 +88,21 @@ def test_cells_of_all_sizes(way):
     assert k8.k8v4_last_device_status() == 0
     want, bound = expected(cells, q.double(), torch.arange(n, device="cuda"), [n] * 4, None, 0.0, None, 1.0)
     check(out, want, bound)
+
+
+@WAYS
+@pytest.mark.parametrize("n", [5, 130, 200])
+def test_cells_that_nobody_sees_change_no_bit(way, n):
+    """Small values in front of cells whose bytes are those of the largest scales, or 0."""
+    rng = np.random.default_rng(n)
+    k, v = (rng.standard_normal((n, 2, 256)).astype(np.float32) for _ in range(2))
+    cache, pt = cache_of(k, 1e-6 * v, P=256)
+    q = queries(rng, 2, 16, "bf16", 2.0)
+    heads = k8.DifferentialHeads(lambda_init=0.5)
+    a = attend(way, cache, pt, q, n, heads)
+    P, H = 256, 2
+    run = cache.pages.view(-1)[392 * H * P:].view(P, H * 16)
+    assert (run[n:] == 0).all()
+    run[n:] = 0x7b
+    b = attend(way, cache, pt, q, n, heads)
+    assert k8.k8v4_last_device_status() == 0 and torch.equal(a, b) and (a != 0).any()
