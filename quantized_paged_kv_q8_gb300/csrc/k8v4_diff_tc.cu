@@ -34,11 +34,11 @@
 // one waits for the other's reader: 4,096 tokens on 32,768 cells 2.53 ms against 2.03 without
 // any rescaling): a row's thread takes its 128 scores into registers at once and frees S, and P
 // has two buffers of its own.
-// The reference maximum of a row moves only when a tile exceeds it by 2^13, and then its O
+// The reference maximum of a row moves only when a tile exceeds it by 2^10, and then its O
 // is rescaled in tensor memory, which holds the pair up for about 1,100 clocks; the two groups
-// hand the reference on from tile to tile.  P is kept 2^2 above it: fp16 drops what is 2^-27 of
-// the reference and less.  (At 2^11 and 2^4 the peaked scores of that case took 2.51 ms, at
-// 2^13 2.34.)
+// hand the reference on from tile to tile.  P is kept 2^5 above it: what is less than 2^-19 of the
+// reference is subnormal, and off by 2^-30 of it at most.  (That case, and with queries 10 times as large:
+// 2.30 and 3.87 ms; at 2^13 and 2^2, where terms of 2^-27 are dropped, 2.26 and 3.65, at 2^8 and 2^7 2.36 and 4.04.)
 // Every kChain tiles O is added to a running sum in global memory (the unit's own partial
 // rows serve as its place), because the tensor core's accumulation is not rounded to
 // nearest: measured 2.9e-5 after 2,048 cells in three products each, so about 4e-5 after
@@ -81,7 +81,7 @@ constexpr int kLoadWarps = 3, kThreads = 32 * (kLoadWarp0 + kLoadWarps);
 // the register split waits for whole warpgroups: roles begin at multiples of four warps
 static_assert(kConvWarp0 % 4 == 0 && kIssueWarp % 4 == 0 && kThreads == 32 * (kIssueWarp + 4), "roles");
 constexpr int kChain = 64;                    // tiles accumulated in tensor memory (8,192 cells)
-constexpr float kSlack = 13.0f, kLift = 2.0f; // log2 headroom of P above its row's reference maximum, and what P is lifted by
+constexpr float kSlack = 10.0f, kLift = 5.0f; // log2 headroom of P above its row's reference maximum, and what P is lifted by
 static_assert(kSlack + kLift <= 15.0f, "P in fp16");
 constexpr uint32_t kWaitDefaultNs = 1000000000u;
 // registers per thread after the split (8 row, 8 conversion and 4 other warps), out of those of

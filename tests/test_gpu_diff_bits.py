@@ -1,5 +1,5 @@
-"""What the differential attention's operands keep, where it shows: values far below and far above 1, and cells whose
-values differ by as much."""
+"""What the differential attention's operands keep, where it shows: values far below and far above 1, cells whose values
+differ by as much, a large weight beside many small ones."""
 import numpy as np
 import pytest
 import torch
@@ -106,3 +106,28 @@ def test_cells_that_nobody_sees_change_no_bit(way, n):
     run[n:] = 0x7b
     b = attend(way, cache, pt, q, n, heads)
     assert k8.k8v4_last_device_status() == 0 and torch.equal(a, b) and (a != 0).any()
+
+
+@WAYS
+@pytest.mark.parametrize("n,gap", [(3000, 14.0), (30000, 20.0), (30000, 28.0)])
+def test_many_small_weights_beside_a_large_one(way, n, gap):
+    """A first cell that takes nearly all the weight and has no value, as the first token of a text often does: the
+    result is what the many others add, each 2^-`gap` of it or so.  Weights are fp16 with at least 2^5 as the largest:
+    a subnormal one is off by half of 2^-24, so by 2^-30 of the largest at most."""
+    rng = np.random.default_rng(n)
+    k = (0.3 * rng.standard_normal((n, 1, 256))).astype(np.float32)
+    v = (1.0 + 0.5 * rng.standard_normal((n, 1, 256))).astype(np.float32)
+    k[:, :, 0] = k[:, :, 128] = 0
+    v[0] = 0
+    q = 0.5 * rng.standard_normal((2, 8, 256)).astype(np.float32)
+    q[:, :, 0] = q[:, :, 128] = 4.0
+    k[0, :, 0] = k[0, :, 128] = gap * np.log(2) * 128 ** 0.5 / 4.0
+    cache, pt = cache_of(k, v)
+    q = torch.from_numpy(q).bfloat16().cuda()
+    heads = k8.DifferentialHeads(lambda_init=-0.5)
+    out = attend(way, cache, pt, q, n, heads)
+    cells = all_cells(cache)
+    want, bound = expected(cells, q.double(), torch.arange(n, device="cuda"), [n] * 2, None, -0.5, None, 1.0)
+    lost = 2.0 ** -30 * 1.5 * cells[1][1:, 0].abs().sum(0).norm().item()
+    assert lost < 0.4 * want.norm(dim=-1).min().item()   # (else it would be seen too late)
+    check(out, want, bound + lost)
