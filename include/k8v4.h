@@ -456,9 +456,9 @@ int kv_append_k8v4_slots(const k8v4_cache* cache, const int64_t* slots, int32_t 
  * probabilities and Vhat enter the products as fp16, every sum is fp32.  A value of Vhat (in
  * rotated space) is off by 2^-11 of it at most; within 32 cells of one of 2^16 or more, by 2^-22
  * where that is more.  A probability is off by 2^-11 of it, or by 2^-30 of its row's largest where
- * that is more.  q is bf16 or fp32 (rounded
- * to fp16 after a power of two per row and map; bf16 is exact).  Rows that see no cell
- * are 0.  The stored scales of visible cells are finite; the others' bytes are anything. */
+ * that is more.  q is bf16, or fp32 in two fp16 terms; scores are below 2^26 in size.  Rows that
+ * see no cell are 0.  The stored scales of visible cells are finite; the others' bytes are
+ * anything. */
 
 /* Workspace bytes of attn_k8v4_diff_decode; 0 for another format or a bad size. */
 size_t attn_k8v4_diff_decode_workspace_bytes(const k8v4_cache* cache, int32_t n_seqs, int32_t max_seq_len);

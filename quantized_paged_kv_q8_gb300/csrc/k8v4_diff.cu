@@ -11,7 +11,7 @@
 //   S_m^T = K_m q_m^T    8 + 8 products m16n8k16 (cells x 8 heads)
 //   O_m^T += V^T P_m^T   16 + 16 products (dims x 8 heads), V converted once
 // with K codes exact in fp16, q in fp16 (bf16 is exact after a power of two per row and
-// map), P and V rounded to fp16 once each: 2^-11 of each term at most, against the 2^-8 of the
+// map; fp32 takes two terms and twice the products of S, as in the decode kernel), P and V rounded to fp16 once each: 2^-11 of each term at most, against the 2^-8 of the
 // bf16 result, where the plain decode carries both in two terms (48 products of V, not 32, and
 // for one map).  V is (n - 8) d: a subnormal d is a multiple of fp16's least step, and so is
 // (n - 8) d.  Only from d = 2^13 on does fp16 not hold it; a tile that has such a block (big_blocks)
@@ -58,7 +58,8 @@ struct Layout {
   int stage_bytes, tx_bytes;
   int q_off, bar_off, ctl_off, total;
 };
-constexpr int kVOff = 4096, kQBytes = 16 * 32 * 8;  // q fragments [16 k-steps][32 lanes][2 words]
+constexpr int kQTerm = 16 * 32 * 8;
+constexpr int kVOff = 4096, kQBytes = 2 * kQTerm;  // q fragments [term][16 k-steps][32 lanes][2 words]
 
 inline Layout layout_of(int H) {
   Layout L;
@@ -99,7 +100,6 @@ int ctas_of(int num_sms) { return std::min(num_sms, kMostCtas); }
 struct DiffParams {
   CacheView C;
   const void* q;
-  int q_f32;
   const int32_t* pt;
   int64_t max_pages;
   const int32_t* lens;        // visible cells of each query
@@ -146,6 +146,8 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
   return d;
 }
+__device__ __forceinline__ float f16_lo(uint32_t h) { return __low2float(*reinterpret_cast<const __half2*>(&h)); }
+__device__ __forceinline__ float f16_hi(uint32_t h) { return __high2float(*reinterpret_cast<const __half2*>(&h)); }
 // 2^e exactly for e >= -126, 0 below
 __device__ __forceinline__ float pow2i(int e) { return e < -126 ? 0.0f : __int_as_float((e + 127) << 23); }
 // one word of nibble bytes b0..b3 -> four fp16x2 of n - 8, exact: {b0, b2} and {b1, b3}
@@ -186,6 +188,7 @@ __device__ __forceinline__ bool wait_or_abort(uint32_t bar, uint32_t parity, uin
 
 // ---------------------------------------------------------------- the split kernel
 // grid: one CTA per SM
+template <bool QF32>
 __global__ void __launch_bounds__(32 * kMaxWorkers, 1)
     diff_split_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const DiffParams p) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -341,7 +344,7 @@ __global__ void __launch_bounds__(32 * kMaxWorkers, 1)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const int64_t e0 = qrow + 128 * m + 64 * i + 16 * c;
-          if (p.q_f32) {
+          if (QF32) {
             const float4* src = reinterpret_cast<const float4*>(static_cast<const float*>(p.q) + e0);
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
@@ -369,7 +372,7 @@ __global__ void __launch_bounds__(32 * kMaxWorkers, 1)
         amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, 1));
         amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, 2));
         const int ex = amax > 0.0f ? static_cast<int>((__float_as_uint(amax) >> 23) & 0xffu) - 127 : 0;
-        const int sh = max(-100, min(100, 14 - ex));              // amax * 2^sh in [2^14, 2^15)
+        const int sh = max(-113, min(100, 14 - ex));              // amax * 2^sh in [2^14, 2^15)
         const float up = ldexpf(1.0f, sh);
         const float fscale = p.sm_scale_log2 * ldexpf(1.0f, -sh);
         if (w == 0) {
@@ -378,6 +381,11 @@ __global__ void __launch_bounds__(32 * kMaxWorkers, 1)
             const int o = 16 * (ks >> 2) + 4 * (ks & 3);
             const uint32_t h0 = pack_f16(qv[o] * up, qv[o + 1] * up), h1 = pack_f16(qv[o + 2] * up, qv[o + 3] * up);
             asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(sb + LY.q_off + ((8 * m + ks) * 32 + lane) * 8), "r"(h0), "r"(h1) : "memory");
+            if (QF32) {
+              const uint32_t l0 = pack_f16(qv[o] * up - f16_lo(h0), qv[o + 1] * up - f16_hi(h0));
+              const uint32_t l1 = pack_f16(qv[o + 2] * up - f16_lo(h1), qv[o + 3] * up - f16_hi(h1));
+              asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(sb + LY.q_off + kQTerm + ((8 * m + ks) * 32 + lane) * 8), "r"(l0), "r"(l1) : "memory");
+            }
           }
         }
         f[m][0] = __shfl_sync(kFull, fscale, 8 * c);
@@ -455,6 +463,10 @@ __global__ void __launch_bounds__(32 * kMaxWorkers, 1)
               i8x4_to_f16(wb[j], a[1], a[3]);
               const uint2 qb = lds64(qf + (8 * m + 4 * i + j) * 256);
               mma16(acc[m][j & 1], a, qb.x, qb.y);
+              if (QF32) {
+                const uint2 ql = lds64(qf + kQTerm + (8 * m + 4 * i + j) * 256);
+                mma16(acc[m][j & 1], a, ql.x, ql.y);
+              }
             }
           }
         }
@@ -927,7 +939,6 @@ int launch_diff_split(const Launch& L, const CacheView& C, const void* q, int q_
   DiffParams p;
   p.C = C;
   p.q = q;
-  p.q_f32 = q_dtype == K8V4_F32;
   p.pt = pt;
   p.max_pages = max_pages;
   p.lens = lens;
@@ -944,8 +955,9 @@ int launch_diff_split(const Launch& L, const CacheView& C, const void* q, int q_
   p.L = layout_of(C.H);
   CUtensorMap mk, mv;
   if (!tensor_maps_of(C, &mk, &mv)) return K8V4_ECUDA;
-  if (cudaFuncSetAttribute(diff_split_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, p.L.total) != cudaSuccess ||
-      cudaFuncSetAttribute(diff_split_kernel, cudaFuncAttributePreferredSharedMemoryCarveout, 100) != cudaSuccess)
+  const auto kernel = q_dtype == K8V4_F32 ? diff_split_kernel<true> : diff_split_kernel<false>;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, p.L.total) != cudaSuccess ||
+      cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, 100) != cudaSuccess)
     return K8V4_ECUDA;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(ctas_of(L.num_sms));
@@ -957,7 +969,7 @@ int launch_diff_split(const Launch& L, const CacheView& C, const void* q, int q_
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, diff_split_kernel, mk, mv, p) != cudaSuccess) return K8V4_ECUDA;
+  if (cudaLaunchKernelEx(&cfg, kernel, mk, mv, p) != cudaSuccess) return K8V4_ECUDA;
   return cudaGetLastError() == cudaSuccess ? K8V4_OK : K8V4_ECUDA;
 }
 

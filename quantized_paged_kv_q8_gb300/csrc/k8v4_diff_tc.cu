@@ -9,7 +9,7 @@
 // heads of a KV head = 256 rows) over a range of the cells: a CTA pair (tcgen05
 // cta_group::2, M = 256, 128 rows per SM) keeps its O in tensor memory and sweeps the range
 // in tiles of 128 cells
-//   S  = Q_m K_m^T        128 lanes, N = 128
+//   S  = Q_m K_m^T        128 lanes, N = 128 (fp32 queries in two fp16 terms: twice)
 //   P  = 2^(s - ref) 2^2  online softmax in the log2 domain, fp16
 //   O += P V              N = 256, V = RN((n - 8) d) in fp16
 // and writes its partial rows (o, m, l); the combine joins ranges and maps.  The two maps'
@@ -110,8 +110,14 @@ constexpr int kSmemMax = 227 * 1024;
 // and the runs of K and V scales of all heads (8 groups x 128 H and 256 H bytes)
 constexpr int kRawV = 8192, kRawKs = 24576;
 constexpr int raw_bytes(int H) { return (kRawKs + 3 * 1024 * H + 1023) / 1024 * 1024; }
-constexpr int raw_stages(int H) { return (kSmemMax - kRawOff) / raw_bytes(H) < 3 ? (kSmemMax - kRawOff) / raw_bytes(H) : 3; }
-static_assert(kKsRing >= 6 && kKsRing <= 8 && raw_stages(2) == 3 && raw_stages(7) >= 2 && raw_stages(8) >= 1, "raw stages");
+// fp32 queries: the second terms, laid out as the first, stand behind the raw tiles
+constexpr int kQBytes = 32768;
+constexpr int raw_stages(int H, bool q_f32) {
+  const int fit = (kSmemMax - kRawOff - (q_f32 ? kQBytes : 0)) / raw_bytes(H);
+  return fit < 3 ? fit : 3;
+}
+static_assert(kKsRing >= 6 && kKsRing <= 8 && raw_stages(2, false) == 3 && raw_stages(7, false) >= 2 && raw_stages(8, false) >= 1, "raw stages");
+static_assert(raw_stages(2, true) >= 2 && raw_stages(8, true) >= 1, "raw stages");
 // the epilogue reuses the operand tiles as a fp32 [128][256] row buffer
 static_assert(kKsOff - kQOff >= kRows * 256 * 4, "row buffer");
 
@@ -613,6 +619,7 @@ struct PairParams {
   uint32_t wait_ns;
   FastDiv page_div;
   int stages, stage_bytes;  // raw tiles in flight
+  int q_lo;                 // fp32 queries: where in shared memory the second terms stand
   int box_shift;            // log2 of the cells of a copy: 4, 5 or 6
 };
 
@@ -759,7 +766,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int o = 8; o >= 1; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, o));
       const int ex = amax > 0.0f ? static_cast<int>((__float_as_uint(amax) >> 23) & 0xffu) - 127 : 0;
-      const int sh = max(-100, min(100, 14 - ex));
+      const int sh = max(-113, min(100, 14 - ex));
       const float up = ldexpf(1.0f, sh);
       // above 0 also where the product underflows: a masked score is -inf times it
       if (l16 == 0) fsc[r] = fmaxf(p.sm_scale_log2 * ldexpf(1.0f, -sh), 1.2e-38f);
@@ -769,7 +776,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const __half2 h2 = __floats2half2_rn(__fmul_rn(x[2 * u], up), __fmul_rn(x[2 * u + 1], up));
         hv[u] = *reinterpret_cast<const uint32_t*>(&h2);
       }
-      sts128(sb + kQOff + (l16 >> 3) * 16384 + swz(r, l16 & 7), hv[0], hv[1], hv[2], hv[3]);
+      const uint32_t at = (l16 >> 3) * 16384 + swz(r, l16 & 7);
+      sts128(sb + kQOff + at, hv[0], hv[1], hv[2], hv[3]);
+      if (p.q_f32) {                                                   // what fp16 leaves of them
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&hv[u]));
+          const __half2 l2 = __floats2half2_rn(__fmul_rn(x[2 * u], up) - h.x, __fmul_rn(x[2 * u + 1], up) - h.y);
+          hv[u] = *reinterpret_cast<const uint32_t*>(&l2);
+        }
+        sts128(sb + p.q_lo + at, hv[0], hv[1], hv[2], hv[3]);
+      }
     }
   }
   asm volatile("fence.proxy.async;" ::: "memory");
@@ -1068,6 +1085,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         constexpr uint32_t idO = idesc_f16(256, 256, false, true);
         const uint32_t tm = __shfl_sync(kFull, tmem, 0);
         const uint64_t dq0 = smem_desc(sb + kQOff, 16, 1024);
+        const uint64_t dl0 = smem_desc(sb + p.q_lo, 16, 1024);
         const uint64_t dk0 = smem_desc(sb + kKOff, 16, 1024);
         const uint64_t dv0 = smem_desc(sb + kVOff, kVAtom, 1024);
         const bool leader = elect_one();
@@ -1076,6 +1094,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           for (int kk = 0; kk < 8; ++kk) {
             const uint32_t off = (kk & 3) * 32;
             mma_pair(tm, dq0 + (((kk >> 2) * 16384 + off) >> 4), dk0 + ((buf * kKBuf + (kk >> 2) * 8192 + off) >> 4), idS, kk ? 1u : 0u);
+          }
+          if (p.q_f32) {
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk) {
+              const uint32_t off = (kk & 3) * 32;
+              mma_pair(tm, dl0 + (((kk >> 2) * 16384 + off) >> 4), dk0 + ((buf * kKBuf + (kk >> 2) * 8192 + off) >> 4), idS, 1u);
+            }
           }
           commit_both(bars + 8 * (kBarSFull + buf));
         };
@@ -1266,15 +1291,16 @@ int launch_diff(const Launch& L, const CacheView& C, const void* q, int q_dtype,
   p.status = L.status;
   p.wait_ns = wait_limit_ns() ? wait_limit_ns() : kWaitDefaultNs;
   p.page_div = FastDiv(static_cast<uint32_t>(C.P));
-  p.stages = raw_stages(C.H);
+  p.stages = raw_stages(C.H, p.q_f32);
   p.stage_bytes = raw_bytes(C.H);
+  p.q_lo = p.q_f32 ? kRawOff + p.stages * p.stage_bytes : kQOff;
   p.box_shift = C.P % 64 == 0 ? 6 : C.P % 32 == 0 ? 5 : 4;
   CUtensorMap mk, mv;
   if (!encode_rows(&mk, C, 0, 256, 1 << p.box_shift) || !encode_rows(&mv, C, C.v_off(), 128, 1 << p.box_shift)) return K8V4_ECUDA;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(2 * sp.most));                // below 2^25 with n_tok < 2^24, n_seqs < 2^16
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = kRawOff + p.stages * p.stage_bytes;
+  cfg.dynamicSmemBytes = kRawOff + p.stages * p.stage_bytes + (p.q_f32 ? kQBytes : 0);
   cfg.stream = L.stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

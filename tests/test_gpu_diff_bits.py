@@ -1,11 +1,11 @@
 """What the differential attention's operands keep, where it shows: values far below and far above 1, cells whose values
-differ by as much, a large weight beside many small ones."""
+differ by as much, a large weight beside many small ones, fp32 queries that need more than fp16's bits."""
 import numpy as np
 import pytest
 import torch
 
 import quantized_paged_kv_q8_gb300 as k8
-from diff_util import all_cells, check, expected, weights
+from diff_util import BF16_HALF, F16_HALF, all_cells, check, expected, weights
 from test_gpu_diff import queries
 
 pytestmark = pytest.mark.gpu
@@ -131,3 +131,31 @@ def test_many_small_weights_beside_a_large_one(way, n, gap):
     lost = 2.0 ** -30 * 1.5 * cells[1][1:, 0].abs().sum(0).norm().item()
     assert lost < 0.4 * want.norm(dim=-1).min().item()   # (else it would be seen too late)
     check(out, want, bound + lost)
+
+
+@WAYS
+def test_fp32_queries_keep_their_bits(way):
+    """Two cells that a query's bits past fp16's set apart: lanes of 1 + 2^-12 meet the one's keys, lanes of 1 - 2^-13
+    the other's.  Rounded to fp16 both lanes are 1 and the cells weigh the same; their scores are 0.37 apart."""
+    rng = np.random.default_rng(6)
+    half = np.zeros((2, 128), np.float32)
+    half[0, ::2], half[1, 1::2] = 1.0, 1.0
+    k = np.tile(half[:, None], (1, 2, 2))
+    v = rng.standard_normal((2, 2, 256)).astype(np.float32)
+    cache, pt = cache_of(k, v)
+    lanes = np.where(np.arange(256) % 2 == 0, 1 + 2.0 ** -12, 1 - 2.0 ** -13).astype(np.float32)
+    size = 1000.0                                          # of a score
+    q = torch.from_numpy(np.tile(lanes * np.float32(size / 64 * 128 ** 0.5), (3, 16, 1))).cuda()
+    q[1, :, 128:] = 0
+    q[2] *= -1
+    cells = all_cells(cache)
+    assert np.allclose(cells[0][:2, 0, :128].cpu().numpy(), half, rtol=1e-6)
+    for lam0 in (0.0, 0.7):
+        heads = k8.DifferentialHeads(lambda_init=lam0)
+        out = attend(way, cache, pt, q, 2, heads)
+        want, _ = expected(cells, q.double(), torch.arange(2, device="cuda"), [2] * 3, None, lam0, None, 1.0)
+        # (a score is 64 equal products of each of the query's two parts in at most 32 steps, each off by a unit of 2^-23 of
+        # what it has reached; the cells' weights move by a quarter of what their scores move apart, in both maps)
+        apart = 2 * 32 * 2.0 ** -23 * size / 4 * (1 + lam0) * (cells[1][0] - cells[1][1]).norm(dim=-1).max().item()
+        off = apart + (2 * F16_HALF + 2.0 ** -16) * (1 + lam0) * cells[1].norm(dim=-1).max().item() + BF16_HALF * want.norm(dim=-1)
+        check(out, want, off)
