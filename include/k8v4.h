@@ -474,7 +474,8 @@ int attn_k8v4_diff_decode(const k8v4_cache* cache, const void* q, int32_t q_dtyp
                           float sm_scale, const k8v4_diff* diff, void* out, void* workspace, size_t workspace_bytes,
                           void* stream);
 
-/* Workspace bytes of attn_k8v4_diff; 0 for another format or a bad size. */
+/* Workspace bytes of attn_k8v4_diff; 0 for another format or a bad size.  No smaller batch (in each of the three
+ * sizes) needs more. */
 size_t attn_k8v4_diff_workspace_bytes(const k8v4_cache* cache, int32_t n_seqs, int32_t n_tok, int32_t max_seq_len);
 
 /* A ragged batch: the queries of sequence b are the packed tokens token_offsets[b] ..

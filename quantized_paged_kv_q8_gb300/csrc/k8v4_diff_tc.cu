@@ -168,6 +168,13 @@ int64_t most_units(int n_seqs, int n_tok, int max_seq_len, int H, int pairs) {
   const int64_t base = most_tiles(n_seqs, n_tok) * 2 * H;
   return std::min(base * std::max(1, (max_seq_len + kTileN - 1) / kTileN), base + more_units(base, pairs, n_seqs, n_tok));
 }
+// what a workspace has room for: the most that any batch within these sizes can have, so that one which was made for
+// the largest batch serves all (sequences of few tokens take fewer ranges than as many tokens of one)
+int64_t room_for(int n_seqs, int n_tok, int max_seq_len, int H, int pairs) {
+  const int64_t base = most_tiles(n_seqs, n_tok) * 2 * H;
+  return std::min(base * std::max(1, (max_seq_len + kTileN - 1) / kTileN),
+                  std::max(base + static_cast<int64_t>(kFewWaves) * pairs, static_cast<int64_t>(kMostWaves) * pairs));
+}
 size_t place(Schedule* s, uint8_t* ws, int n_seqs, int n_tok, int max_seq_len, int H, int pairs, int num_sms) {
   size_t at = 0;
   auto take = [&](size_t bytes) {
@@ -175,7 +182,7 @@ size_t place(Schedule* s, uint8_t* ws, int n_seqs, int n_tok, int max_seq_len, i
     at += (bytes + 255) / 256 * 256;
     return p;
   };
-  const int64_t tiles = most_tiles(n_seqs, n_tok), units = most_units(n_seqs, n_tok, max_seq_len, H, pairs);
+  const int64_t tiles = most_tiles(n_seqs, n_tok), units = room_for(n_seqs, n_tok, max_seq_len, H, pairs);
   Schedule t;
   t.head = reinterpret_cast<int32_t*>(take(12));
   t.lambdas = reinterpret_cast<float*>(take(sizeof(float) * kGqa * H));
