@@ -468,7 +468,8 @@ size_t attn_k8v4_diff_decode_workspace_bytes(const k8v4_cache* cache, int32_t n_
  *        16-byte aligned.
  *   sm_scale: (0, 1e30], 1 / sqrt(128) as published.
  * Lengths, table and workspace as in attn_k8v4_decode (a workspace for each call that
- * may run at the same time). */
+ * may run at the same time).  A length past 2^31 - 256 is clipped to it like one past
+ * max_seq_len, here and in attn_k8v4_diff. */
 int attn_k8v4_diff_decode(const k8v4_cache* cache, const void* q, int32_t q_dtype, const int32_t* page_table,
                           int64_t max_pages, const int32_t* seq_lens, int32_t n_seqs, int32_t max_seq_len,
                           float sm_scale, const k8v4_diff* diff, void* out, void* workspace, size_t workspace_bytes,

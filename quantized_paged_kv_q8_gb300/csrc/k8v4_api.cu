@@ -563,8 +563,8 @@ int attn_k8v4_diff_decode(const k8v4_cache* cache, const void* q, int32_t q_dtyp
   Launch L;
   if ((rc = make_launch(stream, &L))) return rc;
   if (workspace_bytes < diff_decode_ws_bytes(C, n_seqs, L.num_sms)) return K8V4_ENOSPACE;
-  return launch_diff_decode(L, C, q, q_dtype, page_table, max_pages, seq_lens, n_seqs, max_seq_len, sm_scale, *diff,
-                            out, workspace);
+  return launch_diff_decode(L, C, q, q_dtype, page_table, max_pages, seq_lens, n_seqs, std::min(max_seq_len, kDiffMostCells),
+                            sm_scale, *diff, out, workspace);
 }
 
 size_t attn_k8v4_diff_workspace_bytes(const k8v4_cache* cache, int32_t n_seqs, int32_t n_tok, int32_t max_seq_len) {
@@ -573,7 +573,7 @@ size_t attn_k8v4_diff_workspace_bytes(const k8v4_cache* cache, int32_t n_seqs, i
   if (n_seqs < 0 || n_seqs > 65535 || n_tok < 0 || n_tok >= (1 << 24) || max_seq_len < 0) return 0;
   DeviceState* s = nullptr;
   const int sms = device_state(&s) == K8V4_OK ? s->num_sms : 152;
-  return diff_ws_bytes(C, n_seqs, n_tok, max_seq_len, sms);
+  return diff_ws_bytes(C, n_seqs, n_tok, std::min(max_seq_len, kDiffMostCells), sms);
 }
 
 int attn_k8v4_diff(const k8v4_cache* cache, const void* q, int32_t q_dtype, const int32_t* token_offsets, int32_t n_tok,
@@ -595,6 +595,7 @@ int attn_k8v4_diff(const k8v4_cache* cache, const void* q, int32_t q_dtype, cons
     return K8V4_EALIGN;
   Launch L;
   if ((rc = make_launch(stream, &L))) return rc;
+  max_seq_len = std::min(max_seq_len, kDiffMostCells);
   if (workspace_bytes < diff_ws_bytes(C, n_seqs, n_tok, max_seq_len, L.num_sms)) return K8V4_ENOSPACE;
   return launch_diff(L, C, q, q_dtype, token_offsets, n_tok, page_table, max_pages, seq_lens, steps, n_seqs, max_seq_len,
                      sm_scale, *diff, out, workspace);

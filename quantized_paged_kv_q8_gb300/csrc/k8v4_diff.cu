@@ -300,8 +300,8 @@ __global__ void __launch_bounds__(32 * kMaxWorkers, 1)
     auto page_of = [&](int u) -> int {         // warp-uniform u; all lanes call
       if (u < win0 || u >= win0 + 32) {
         win0 = u;
-        const int cell = c_begin + 16 * (w + W * (u + lane));
-        const int64_t pidx = cell >= 0 ? static_cast<int64_t>(p.page_div.div(static_cast<uint32_t>(cell))) : 0;
+        const uint32_t cell = static_cast<uint32_t>(c_begin) + 16u * (w + W * (u + lane));     // (looked up only where it is one)
+        const int64_t pidx = p.page_div.div(cell);
         win_page = (u + lane < n_my && pidx < p.max_pages) ? pt_row[pidx] : -1;
       }
       const int page = __shfl_sync(kFull, win_page, u - win0);

@@ -687,9 +687,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const int which = warp - kLoadWarp0, per = p.box_shift - 4, copies = 8 >> per;   // 1 << per groups a copy
   int page_next = 0, page_mine = 0;
   auto lookup = [&](int i) -> int {
-    const int c = (tile0 + i + (lane >> 3)) * kTileN + 16 * ((lane & 7) >> per << per);
-    if (i + (lane >> 3) >= n_tiles || c >= limit) return INT32_MIN;        // behind the limit, or another range's
-    const int64_t pidx = p.page_div.div(static_cast<uint32_t>(c));
+    const uint32_t c = static_cast<uint32_t>(tile0 + i + (lane >> 3)) * kTileN + 16 * ((lane & 7) >> per << per);
+    if (i + (lane >> 3) >= n_tiles || c >= static_cast<uint32_t>(limit)) return INT32_MIN;        // behind the limit, or another range's
+    const int64_t pidx = p.page_div.div(c);
     return pidx < p.max_pages ? __ldcg(pt + pidx) : -1;
   };
   auto load_tile = [&](int i, int stage) {

@@ -2,6 +2,8 @@
 // appends through slots, differential attention and the norm between blocks.
 #pragma once
 
+#include <climits>
+
 #include "k8v4_common.cuh"
 
 namespace k8v4 {
@@ -32,6 +34,9 @@ int launch_append_slots(const Launch& L, const CacheView& C, const int64_t* slot
 
 // differential attention: one query per sequence, and a ragged batch
 bool diff_supported(const CacheView& C);
+// The longest length that the kernels take (a larger bound counts as this one): cell numbers, rounded up to a tile,
+// stay within 31 bits
+constexpr int kDiffMostCells = INT_MAX - 255;
 size_t diff_decode_ws_bytes(const CacheView& C, int n_seqs, int num_sms);
 int launch_diff_decode(const Launch& L, const CacheView& C, const void* q, int q_dtype, const int32_t* pt, int64_t max_pages,
                        const int32_t* lens, int n_seqs, int max_seq_len, float sm_scale, const k8v4_diff& diff, void* out,

@@ -14,7 +14,7 @@ def test_a_smaller_batch_needs_no_larger_workspace(L, H):  # noqa: F811
     d = _desc(n_pages=1 << 20, page_size=64, n_kv_heads=H)
     seqs = [0, 1, 2, 7, 8, 9, 60, 63, 64, 65, 600, 65535]
     toks = [0, 1, 8, 9, 31, 32, 33, 56, 63, 64, 65, 480, 504, 512, 513, 4096, 5000, 21429, (1 << 24) - 1]
-    cells = [0, 1, 127, 128, 129, 4000, 32768, 1 << 24]
+    cells = [0, 1, 127, 128, 129, 4000, 32768, 1 << 24, 2 ** 31 - 257, 2 ** 31 - 256, 2 ** 31 - 129, 2 ** 31 - 1]
     need = {a: L.attn_k8v4_diff_workspace_bytes(d, *a) for a in itertools.product(seqs, toks, cells)}
     for (s, t, c), n in need.items():
         assert n > 0
