@@ -182,7 +182,8 @@ __global__ void __launch_bounds__(1024, NV == 1 && !F32 ? 2 : 1) block_norm_kern
         const float z = g0.at(e);
         float f = z;
         if (p.gate_act != K8V4_GATE_NONE) {
-          const float u = 1.0f / (1.0f + __expf(-z));
+          // (the short exponential is off by |z| units or so of fp32, which bf16 results do not see)
+          const float u = 1.0f / (1.0f + (F32 ? expf(-z) : __expf(-z)));
           f = p.gate_act == K8V4_GATE_SILU ? z * u : u;
         }
         x[i][e] *= f;
