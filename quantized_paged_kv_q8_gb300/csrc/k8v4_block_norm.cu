@@ -220,7 +220,7 @@ int launch_types(const Launch& L, const NormParams& p, bool wide) {
   const int hold = wide ? (chunks <= (F32 ? 512 : 1024) ? 1 : chunks <= 2048 ? 2 : 4) : (chunks <= 4096 ? 4 : chunks <= 16384 ? 16 : 32);
   const int threads = std::max(32, ((chunks + hold - 1) / hold + 31) & ~31);
   const int rows = threads == 32 ? 4 : 1;
-  const dim3 block(threads, rows), grid(static_cast<unsigned>((p.n_tok + rows - 1) / rows));
+  const dim3 block(threads, rows), grid(static_cast<unsigned>((static_cast<int64_t>(p.n_tok) + rows - 1) / rows));
   if (wide && hold == 1) return launch_behind(L, block_norm_kernel<YF32, F32, 8, 1>, grid, block, p);
   if (wide && hold == 2) return launch_behind(L, block_norm_kernel<YF32, F32, 8, 2>, grid, block, p);
   if (wide) return launch_behind(L, block_norm_kernel<YF32, F32, 8, 4>, grid, block, p);

@@ -21,3 +21,16 @@ def test_fp32_gates_far_from_0(act, dim):
     u = torch.sigmoid(z.double())
     want = y.double() * (z.double() * u if act == "silu" else u)
     assert ((h.double() - want).abs() <= 10 * F32_HALF * want.abs() + 2.0 ** -149).all()
+
+
+def test_most_rows():
+    """2^31 - 1 rows of one element, four to a CTA."""
+    n = 2 ** 31 - 1
+    if torch.cuda.mem_get_info()[0] < 24 << 30:
+        pytest.skip("9 GB of rows")
+    y, h = (torch.empty(n, 1, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    y.fill_(3.0)
+    y[-1], h[-4:] = 5.0, 0.0
+    k8.block_norm_k8v4(y, None, h, residual_scale=2.0)
+    torch.cuda.synchronize()
+    assert h[-1].item() == 10.0 and h[0].item() == 6.0 and (h[-1000:-1] == 6.0).all()
