@@ -438,7 +438,7 @@ PyObject* block_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (a[4] != Py_None) {
       const at::Tensor& g = tensor(a[4], "gate");
       if (g.scalar_type() != type || device_of(g) != dev) bad("gate: the dtype and device of h expected");
-      if (g.numel() == dim && (g.dim() == 1 || n_tok != 1)) {   // one row for all tokens
+      if (g.numel() == dim && (g.dim() == 1 || (n_tok != 1 && g.dim() == 2 && g.size(1) == dim))) {   // one row for all tokens
         if (!g.is_contiguous()) bad("gate: [n_tok, dim] with contiguous rows, or [dim], expected");
       } else {
         g_stride = row_stride(g, n_tok, dim, "gate");
