@@ -412,10 +412,12 @@ int attn_k8v4_prefill(const k8v4_cache* cache, const void* q, int32_t q_dtype, c
  *   page_table: int32 [n_seqs][max_pages]; only the entries of pages handed out are
  *              written, behind those that the row has.
  * Given-back pages go on the stack first, in (sequence, entry) order; then each
- * sequence in order takes the pages it needs from the top.  A sequence whose pages
- * are no longer all there gets none of its tokens (a later one that needs no page
- * still does), nor does one that would pass max_pages pages or max_tokens packed
- * tokens; its length stays and its tokens keep their place in the packing.
+ * sequence in order takes the pages it needs from the top.  The first one whose pages
+ * are not all there gets none of its tokens, and neither does any later one that needs a
+ * page, also where its own would be there (one that needs none still does); nor does one
+ * that would pass max_pages pages or max_tokens packed tokens.  Its length stays and its
+ * tokens keep their place in the packing: the calls that go by token_offsets take them for
+ * tokens like others (attn_k8v4_diff says how their rows are left empty).
  *   token_offsets: int32 [n_seqs + 1], where each sequence's n_new tokens begin (at
  *              most max_tokens).
  *   positions: int64 [max_tokens], the cell index of each token in its sequence (0 for
@@ -428,7 +430,8 @@ int attn_k8v4_prefill(const k8v4_cache* cache, const void* q, int32_t q_dtype, c
  * Apart from those two no two arrays overlap; no page is in two places of the stack and the own
  * entries of the tables.  1 <= n_pages < 2^31, n_seqs <= 8192, n_seqs * max_pages < 2^31,
  * 0 <= max_tokens.  Device-side (K8V4_ERANGE): a length or count out of range refuses
- * the sequence, a page id outside [0, n_pages) in a finished row leaves the row as it is.
+ * the sequence, a page id outside [0, n_pages) in a finished row leaves the row as it is; one
+ * on the stack is handed out all the same, and the tokens in it have slot -1.
  * K8V4_ENOSPACE is recorded when a sequence was refused for want of pages or
  * max_tokens. */
 int kv_plan_k8v4(int32_t page_size, int64_t n_pages, int32_t* free_pages, const int32_t* n_free, int32_t* page_table,
@@ -489,6 +492,9 @@ size_t attn_k8v4_diff_workspace_bytes(const k8v4_cache* cache, int32_t n_seqs, i
  *   steps: int32 [n_tok] (device) or NULL; a count outside [0, seq_lens[b]] is clipped
  *        and recorded.  Without steps, tokens ahead of the sequence's first cell (n_b >
  *        seq_lens[b]) see none.
+ * Behind kv_plan_k8v4, steps of positions[t] + 1 where slots[t] >= 0, and 0 elsewhere, are the
+ * causal counts, and leave the rows of refused tokens 0 without reading a cell for them; without
+ * steps a refused sequence's tokens are taken for its last cells.
  * n_seqs <= 65535, n_tok < 2^24.  Device-side: offsets out of order or out of range leave
  * their sequence out (K8V4_ERANGE). */
 int attn_k8v4_diff(const k8v4_cache* cache, const void* q, int32_t q_dtype, const int32_t* token_offsets, int32_t n_tok,

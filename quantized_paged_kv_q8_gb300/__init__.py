@@ -298,7 +298,8 @@ def kv_plan_k8v4(page_size: int, free_pages: torch.Tensor, n_free: torch.Tensor,
     """Pages for the new tokens of a step, and back from finished sequences (n_new -1), on the device.  int32: free_pages
     [n_pages] (a stack), n_free [1], page_table [n_seqs, max_pages], seq_lens, n_new, granted, new_lens, n_borrowed
     [n_seqs], token_offsets [n_seqs + 1], n_free_out [1]; int64: positions, slots [max_tokens].  Without new_lens and
-    n_free_out, seq_lens and n_free are moved on in place."""
+    n_free_out, seq_lens and n_free are moved on in place.  The tokens of refused sequences (granted 0) keep their place in
+    the packing, with slot -1."""
     rc = (_binding or _native()).plan(page_size, free_pages, n_free, page_table, seq_lens, n_new, n_borrowed, token_offsets,
                                       positions, slots, granted, seq_lens if new_lens is None else new_lens,
                                       n_free if n_free_out is None else n_free_out,
@@ -380,7 +381,8 @@ def attn_k8v4_diff(cache: PagedCache, q: torch.Tensor, token_offsets: torch.Tens
                    steps: torch.Tensor | None = None, sm_scale: float = 128 ** -0.5, stream=None) -> torch.Tensor:
     """Differential attention of a ragged batch: q [n_tok, 8H, 256] (bf16 or f32), the tokens of sequence b at
     token_offsets[b] .. token_offsets[b + 1] - 1 (int32 [n_seqs + 1]), the last cells of its seq_lens[b] (int32, the new
-    ones included), causal or seeing steps int32 [n_tok] cells; page_table int32 [n_seqs, max_pages]; out bfloat16 like q."""
+    ones included), causal or seeing steps int32 [n_tok] cells; page_table int32 [n_seqs, max_pages]; out bfloat16 like q.
+    Where a plan may have refused sequences, steps = where(slots >= 0, positions + 1, 0) leaves their rows 0."""
     rc = (_binding or _native()).diff(cache.address, cache.pages, q, token_offsets, page_table, seq_lens, steps, max_seq_len,
                                       heads.address, heads.device, out, ws, sm_scale,
                                       stream if stream is None else _stream(stream))
