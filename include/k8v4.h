@@ -461,7 +461,13 @@ int kv_append_k8v4_slots(const k8v4_cache* cache, const int64_t* slots, int32_t 
  * where that is more.  A probability is off by 2^-11 of it, or by 2^-30 of its row's largest where
  * that is more.  q is bf16, or fp32 in two fp16 terms; scores are below 2^26 in size.  Rows that
  * see no cell are 0.  The stored scales of visible cells are finite; the others' bytes are
- * anything. */
+ * anything.
+ * Positions: qk_norm_rope_k8v4 and kv_append_k8v4_rope rotate each map as a head of 128 with
+ * interleaved pairs, rot_dim 256 and a table whose rows hold a map's 64 cosines twice, then its
+ * 64 sines twice (1 and 0 for pairs that pass through), and without a norm weight: their norm
+ * is over both maps.  With another rot_dim, or split pairs, lanes of the one map would turn by
+ * the other's; a projection made for split pairs within a map (i, i + 64) has its rows put in
+ * the order 0, 64, 1, 65, ... in queries and keys alike, which leaves the scores as they are. */
 
 /* Workspace bytes of attn_k8v4_diff_decode; 0 for another format or a bad size. */
 size_t attn_k8v4_diff_decode_workspace_bytes(const k8v4_cache* cache, int32_t n_seqs, int32_t max_seq_len);

@@ -320,7 +320,8 @@ def kv_append_k8v4_slots(cache: PagedCache, slots: torch.Tensor, k: torch.Tensor
 class DifferentialHeads:
     """The learned weights of a layer's differential heads: lambdas, the four vectors (q1, k1, q2, k2) as float32
     [128] or [1, 128] (one set for all heads) or [8H, 128], or None; norm_weight float32 [256] or None.  The tensors
-    are kept, not copied: a change of their values counts from the next call on."""
+    are kept, not copied: a change of their values counts from the next call on.  Their queries and keys are rotated by
+    qk_norm_rope_k8v4 with interleaved=True, no norm weights and rows cat(cos, cos, sin, sin) of a map's 64 angles."""
 
     def __init__(self, lambdas=None, lambda_init: float = 0.8, norm_weight: torch.Tensor | None = None, eps: float = 1e-6,
                  out_scale: float = 1.0):
