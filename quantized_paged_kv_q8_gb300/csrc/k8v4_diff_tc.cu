@@ -911,8 +911,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           break;
         }
         tc_fence_after();
-        // the running sum is relative to the reference too: both move
+        // the running sum is relative to the reference too: both move.  The other group's thread of this row wrote it
+        // last, and what came between (P's arrival, perhaps at the other CTA's barrier, and the product's completion)
+        // orders it for this CTA's threads only with a fence on either side
         const bool have = i > kChain;
+        if (have) asm volatile("fence.acq_rel.cluster;" ::: "memory");
         float4* const acc = reinterpret_cast<float4*>(block) + row;
 #pragma unroll 1
         for (int h = 0; h < 2; ++h) {
@@ -939,6 +942,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
           }
         }
+        if (folds || have) asm volatile("fence.acq_rel.cluster;" ::: "memory");
       }
       tmem_wait_st();
       tc_fence_before();
