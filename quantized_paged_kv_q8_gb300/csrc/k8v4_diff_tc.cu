@@ -145,7 +145,7 @@ struct Unit {
 };
 
 struct Schedule {                             // places in the workspace
-  int32_t* head;                              // [0] units, [1] token tiles, [2] single queries
+  int32_t* head;                              // [0] units, [1] single queries
   float* lambdas;                             // [8 H]
   int32_t* tile_end;                          // [n_seqs] token tiles up to each sequence
   TokenTile* tiles;
@@ -184,7 +184,7 @@ size_t place(Schedule* s, uint8_t* ws, int n_seqs, int n_tok, int max_seq_len, i
   };
   const int64_t tiles = most_tiles(n_seqs, n_tok), units = room_for(n_seqs, n_tok, max_seq_len, H, pairs);
   Schedule t;
-  t.head = reinterpret_cast<int32_t*>(take(12));
+  t.head = reinterpret_cast<int32_t*>(take(8));
   t.lambdas = reinterpret_cast<float*>(take(sizeof(float) * kGqa * H));
   t.tile_end = reinterpret_cast<int32_t*>(take(4 * static_cast<size_t>(n_seqs)));
   t.tiles = reinterpret_cast<TokenTile*>(take(sizeof(TokenTile) * tiles));
@@ -343,8 +343,8 @@ __global__ void __launch_bounds__(1024, 1) diff_schedule_kernel(const SchedulePa
   }
   if (n_tiles == 0) {
     if (tid == 0) {
-      s.head[0] = s.head[1] = 0;
-      s.head[2] = static_cast<int>(min(static_cast<int64_t>(n_rows), p.most_rows));
+      s.head[0] = 0;
+      s.head[1] = static_cast<int>(min(static_cast<int64_t>(n_rows), p.most_rows));
     }
     return;
   }
@@ -466,8 +466,7 @@ __global__ void __launch_bounds__(1024, 1) diff_schedule_kernel(const SchedulePa
   }
   if (tid == 0) {
     s.head[0] = all;
-    s.head[1] = n_tiles;
-    s.head[2] = static_cast<int>(min(static_cast<int64_t>(n_rows), p.most_rows));
+    s.head[1] = static_cast<int>(min(static_cast<int64_t>(n_rows), p.most_rows));
   }
 }
 
@@ -1287,7 +1286,7 @@ int launch_diff(const Launch& L, const CacheView& C, const void* q, int q_dtype,
   sp.status = L.status;
   int rc = launch_behind(L, diff_schedule_kernel, dim3(1), dim3(1024), sp);
   if (rc) return rc;
-  rc = launch_diff_split(L, C, q, q_dtype, pt, max_pages, sp.s.row_vis, DiffQueries{sp.s.row_seq, sp.s.row_tok, sp.s.head + 2}, 0,
+  rc = launch_diff_split(L, C, q, q_dtype, pt, max_pages, sp.s.row_vis, DiffQueries{sp.s.row_seq, sp.s.row_tok, sp.s.head + 1}, 0,
                          max_seq_len, sm_scale, sp.s.pieces);
   if (rc) return rc;
   PairParams p;
