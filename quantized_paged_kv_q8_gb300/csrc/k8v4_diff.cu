@@ -24,9 +24,10 @@
 // each CTA finds its own from the lengths.
 //
 // What bounds it: the matrix instructions, about 6.8 clocks each on an SM (48 a tile: 32 us of one
-// sequence of 237,568 cells), beside the conversions of the codes (970 instructions a tile in
-// all); two warps a scheduler do not overlap them wholly.  That sequence, 2 KV heads: 56 us with the
-// joining, 3.4 TB/s of the cache's 194 MB; 32 sequences of up to 8,192 cells 37 us.  Two warps to a
+// sequence of 237,568 cells), beside the conversions of the codes (about 980 instructions a tile in
+// all); two warps a scheduler do not overlap them wholly.  That sequence, 2 KV heads: 58 us with the
+// joining, 3.3 TB/s of the cache's 194 MB (fp32 queries, 64 products a tile: 62.5); 32 sequences of up to 8,192
+// cells 41 us (44).  Two warps to a
 // worker, each with a map's scores and half of V's dims (16 warps of 128 registers, weights handed
 // over through shared memory): 63 us and 41.
 #include <algorithm>

@@ -31,7 +31,7 @@
 //      warps 17-19  copy the raw tiles (TMA, boxes of 64, 32 or 16 cells as the page size allows; a
 //                   copy takes its warp about 100 clocks to issue, and 16-cell boxes need 28 a tile)
 // The issuing warp hands over whichever product is ready, S or O (in a fixed order of the two
-// one waits for the other's reader: 4,096 tokens on 32,768 cells 2.53 ms against 2.03 without
+// one waits for the other's reader: 4,096 tokens on 32,768 cells 2.53 ms against 2.03 then, without
 // any rescaling): a row's thread takes its 128 scores into registers at once and frees S, and P
 // has two buffers of its own.
 // The reference maximum of a row moves only when a tile exceeds it by 2^10, and then its O
@@ -50,9 +50,10 @@
 // where it is estimated to be faster their tokens go through the single queries' kernel
 // (k8v4_diff.cu) one by one.
 //
-// What bounds it: the products (1,536 of a tile's about 2,600 clocks) and what the row warps do
-// between them; 4,096 tokens on 32,768 cells 2.14 - 2.26 ms, 1.37 - 1.45 PFLOP/s.  Short units pay 10 us each
-// beside their tiles: 12 prompts of 900 tokens 190 us.
+// What bounds it: the products (1,536 of a tile's about 2,700 clocks) and what the row warps do
+// between them; 4,096 tokens on 32,768 cells 2.30 ms, 1.34 PFLOP/s (2.10 without the look at the blocks' sizes, the
+// fence and the small weights' bits).  Short units pay 10 us each
+// beside their tiles: 12 prompts of 900 tokens 229 us.
 //
 // Tensor memory (512 columns): S [0,128), P [128,192) and [192,256), O [256,512).
 //
@@ -97,7 +98,7 @@ constexpr int kVOff = kKOff + 2 * kKBuf;              // V fp16, 2 buffers x [2 
 constexpr int kVBuf = 32768, kVAtom = 16384;
 // K scales, kKsRing tiles x [128] f32, and as many words of odd cells.  A row frees S before it reads these, so
 // the conversion of tile i, which waits for S(i - 2) and with it for S(i - 3) and S(i - 4) to be read, knows that the
-// groups are in their tiles i - 3 and i - 4 and done with those up to i - 5 and i - 6: six places would do.
+// groups are in their tiles i - 3 and i - 4 and done with those up to i - 5 and i - 6: six places do.
 // Four (with three raw tiles in flight, nothing else holds the conversion back) would not
 constexpr int kKsRing = 8;
 constexpr int kKsOff = kVOff + 2 * kVBuf;

@@ -18,7 +18,7 @@
 // of the tokens, handed-out pages and given-back pages as flat lists, finding each one's
 // sequence by bisection.  The pages are handed out ahead of a barrier behind which the tokens read
 // them from the table: a token that worked its page out again took a second bisection.
-// 32 sequences with a token each 5.6 us; 600 sequences, 60 of them finished, 21,000
+// 32 sequences with a token each 5.3 us; 600 sequences, 60 of them finished, 21,000
 // tokens 16 us (19 with an item at a time; 59 in one CTA).
 #include <algorithm>
 #include <climits>

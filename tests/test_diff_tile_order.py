@@ -128,8 +128,6 @@ def kernel(tiles, stages, ring, moves=True):
                 g.arrive(who, ("reference", c, w, buf), i)
                 if i >= 2:
                     g.wait(who, ("O done", buf), i - 2)
-                for k in range(4):                          # (which cells have large blocks, once more)
-                    g.use(who, ("K scales", c, k, i % ring), i, False)
                 g.use(who, ("P", c, w, buf), i, True)
                 if i and moves:                             # a reference that moved, or a fold: any tile may, or none
                     g.wait(who, ("O done", buf ^ 1), i - 1)
