@@ -458,10 +458,10 @@ int kv_append_k8v4_slots(const k8v4_cache* cache, const int64_t* slots, int32_t 
  * K8V4 format.  The maps are scored exactly as in the attention above; their
  * probabilities and Vhat enter the products as fp16, every sum is fp32.  A value of Vhat (in
  * rotated space) is off by 2^-11 of it at most; within 32 cells of one of 2^16 or more, by 2^-22
- * where that is more.  A probability is off by 2^-11 of it, or by 2^-30 of its row's largest where
- * that is more.  q is bf16, or fp32 in two fp16 terms; scores are below 2^26 in size.  Rows that
- * see no cell are 0.  The stored scales of visible cells are finite; the others' bytes are
- * anything.
+ * where that is more.  A probability is off by 2^-11 of it, or by 2^-30 of its row's largest (2^-27
+ * where the row sees values of 2^16 or more) where that is more.  q is bf16, or fp32 in two fp16
+ * terms; scores are below 2^26 in size.  Rows that see no cell are 0.  The stored scales of
+ * visible cells are finite; the others' bytes are anything.
  * Positions: qk_norm_rope_k8v4 and kv_append_k8v4_rope rotate each map as a head of 128 with
  * interleaved pairs, rot_dim 256 and a table whose rows hold a map's 64 cosines twice, then its
  * 64 sines twice (1 and 0 for pairs that pass through), and without a norm weight: their norm
